@@ -53,6 +53,8 @@ extern "C" {
 #define WA_STATUS_BAD_HI 2    /* a prompt hi[i] was outside [p0+i, p0+n-1] (clamped) */
 #define WA_STATUS_TIMEOUT 4   /* a bounded device wait gave up; outputs are not valid */
 #define WA_STATUS_LAYOUT 8    /* a kernel found its shared memory misaligned and wrote nothing */
+#define WA_STATUS_BAD_TREE 16 /* a parent, node count, draft token, path or length was out of range (see the call) */
+#define WA_STATUS_NO_MASS 32  /* wa_tree_verify: a distribution without mass; that row's token is -1 */
 
 /* Token strides in elements for the prompt form (head stride is always d).
  * Zero means dense: hq*d for q and out, hkv*d for k and v. */
@@ -225,6 +227,150 @@ int wa_prep_append(const void* src, const int32_t* pos, int32_t n, int32_t hq, i
                    int32_t mode, const float* q_scale, const float* inv_freq, int32_t ring,
                    const wa_prep_layout* lay, void* q_out, void* k_ring, void* v_ring,
                    void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted tokens.  A serving step that drafts several tokens a sequence and
+ * keeps those that the target model accepts:
+ *
+ *   wa_prep_append   the nodes' q, and their k and v into a buffer [rows, nodes]
+ *                    of their own (one ring of length 1 a token)
+ *   wa_tree_decode   per layer: the nodes' attention over ring and buffer
+ *   wa_tree_verify   which nodes are kept, and the token after them
+ *   wa_tree_commit   the kept nodes' keys and values into the rings
+ *
+ * A row's drafts form a tree of up to WA_TREE_MAX_NODES nodes: parent[i] < i is
+ * the node before node i, -1 for a node that follows the cache directly.  The
+ * nodes stay out of the ring until they are kept, because an append to a ring
+ * of win slots overwrites keys that are needed again once a draft is dropped,
+ * and because siblings stand at the same position.
+ * ------------------------------------------------------------------------- */
+
+#define WA_TREE_MAX_NODES 128
+
+/* Layout of wa_tree_decode in elements (the head stride is always d): between
+ * the rows (sequences) and between a row's nodes.  Zero means dense: hq*d or
+ * hkv*d between nodes, nodes times that between rows. */
+typedef struct wa_tree_strides {
+    int64_t q_row, q_tok;
+    int64_t k_row, k_tok;      /* k_tree */
+    int64_t v_row, v_tok;      /* v_tree */
+    int64_t out_row, out_tok;
+} wa_tree_strides;
+
+/* Workspace bytes wa_tree_decode needs for these sizes; 0 for invalid ones. */
+size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t hkv, int32_t d, int32_t win,
+                               int32_t ring);
+
+/*
+ * Decode for a tree of drafted tokens.  Row r's cache holds the keys up to
+ * position pos[r]; node i of depth t (0 for a root) stands at position
+ * P = pos[r] + 1 + t and sees
+ *   the ring's keys j with max(0, P - win + 1) <= j <= pos[r]  (win = 0: all), and
+ *   itself and its ancestors, those less than win positions back (win = 0: all).
+ * out = softmax(scale * q . K^T) V over them, as a wa_decode call would give for
+ * a cache that holds the node's ancestors and itself at their positions.
+ *
+ *   q       [rows, nodes, hq, d]   bf16
+ *   k_ring  [rows, ring, hkv, d]   bf16, dense, as for wa_decode
+ *   v_ring  [rows, ring, hkv, d]   bf16, dense
+ *   k_tree  [rows, nodes, hkv, d]  bf16: the nodes' keys, not in the ring
+ *   v_tree  [rows, nodes, hkv, d]  bf16
+ *   pos     [rows]         int32, device; -1 for an empty cache.  Below -1, or
+ *                          >= ring with win = 0: clamped, WA_STATUS_BAD_POS
+ *   parent  [rows, nodes]  int32, device; a value outside [-1, i) counts as -1
+ *                          and is reported (WA_STATUS_BAD_TREE)
+ *   n       [rows]         int32, device, or NULL (all nodes): row r's nodes are
+ *                          0 .. n[r]-1.  Outside [0, nodes]: clamped, BAD_TREE
+ *   out     [rows, nodes, hq, d]   bf16; nodes >= n[r] are left as they were
+ *
+ * Probabilities enter P V as two bf16 parts whose sum is within 2^-17 of them,
+ * as in wa_decode's tensor-core form.  The softmax runs over 128-key tiles at
+ * absolute positions, in spans whose ends depend on the row's own position,
+ * the window and hkv alone: an output's bits do not depend on the batch, the
+ * row's place in it, nodes, n, or other branches of the tree.  1 <= nodes <=
+ * WA_TREE_MAX_NODES; other constraints as wa_decode, WA_EINVAL otherwise.
+ * Calls whose work can overlap need workspaces of their own; two captured
+ * graphs that replay at the same time do too.
+ */
+int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
+                   const int32_t* pos, const int32_t* parent, const int32_t* n, int32_t rows, int32_t nodes,
+                   int32_t hq, int32_t hkv, int32_t d, int32_t win, int32_t ring, float scale,
+                   const wa_tree_strides* strides, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Layout of wa_tree_verify in elements: between rows and between nodes of
+ * target and draft.  Zero means dense. */
+typedef struct wa_verify_strides {
+    int64_t t_row, t_node;
+    int64_t d_row, d_node;
+} wa_verify_strides;
+
+/* Workspace bytes wa_tree_verify and wa_tree_commit need: the 256-byte header. */
+#define WA_TREE_WS_BYTES 256u
+
+/*
+ * Verification of drafted tokens against the target's probabilities: speculative
+ * sampling over a tree, from given random numbers.  Node 0 is the last sampled
+ * token (kept already); the walk starts there.  At node v with target
+ * distribution p = target[r, v] and draft distribution q = draft[r, v]:
+ *
+ *   W = p, s = 1
+ *   for each child c of v, in index order, with token x = tokens[r, c]:
+ *       if u[r, c] * q(x) * s < W(x): keep c and go on from there
+ *       W' = max(W - s q, 0);  if its sum is positive: W = W', s = sum of W'
+ *   no child kept: the token after v is the first x with
+ *       W(0) + .. + W(x) > u[r, 0] * (sum of W)
+ *
+ * With u uniform in [0, 1) and children drawn from q, the kept tokens and the
+ * sampled one are distributed as if the target had sampled them one by one.
+ * draft = NULL stands for children that were not drawn (the draft's best
+ * tokens): q is then 1 at x and 0 elsewhere.
+ *
+ *   target  [rows, nodes, vocab]  fp32 probabilities
+ *   draft   [rows, nodes, vocab]  fp32 probabilities, or NULL
+ *   parent  [rows, nodes]  int32, as wa_tree_decode's; nodes that do not descend
+ *                          from node 0 are never reached
+ *   tokens  [rows, nodes]  int32: a node's token; one outside [0, vocab) takes its
+ *                          node out of the tree (WA_STATUS_BAD_TREE); tokens[r, 0] is not read
+ *   n       [rows]         int32, or NULL (all nodes), as wa_tree_decode's
+ *   u       [rows, nodes]  fp32: u[r, c] tests node c, u[r, 0] samples the last token
+ *   path    [rows, nodes]  int32, written: the kept nodes, node 0 first, then -1
+ *   length  [rows]         int32, written: how many were kept (0 where n[r] is 0)
+ *   token   [rows]         int32, written: the token after the last kept node; -1 where
+ *                          n[r] is 0 or the distribution has no mass (WA_STATUS_NO_MASS)
+ *
+ * Probabilities that are NaN or below 0 count as 0, those above 1 as 1.  Sums
+ * carry about 46 bits in a fixed order.  All pointers are device pointers;
+ * 1 <= nodes <= WA_TREE_MAX_NODES, 1 <= vocab <= 2^24.
+ */
+int wa_tree_verify(const float* target, const float* draft, const int32_t* parent, const int32_t* tokens,
+                   const int32_t* n, const float* u, int32_t rows, int32_t nodes, int32_t vocab,
+                   const wa_verify_strides* strides, int32_t* path, int32_t* length, int32_t* token,
+                   void* ws, size_t ws_bytes, void* stream);
+
+#define WA_COMMIT_MAX_LAYERS 64
+
+/*
+ * The kept nodes' keys and values into the rings of up to WA_COMMIT_MAX_LAYERS
+ * layers: for j < length[r], node path[r, j] goes to slot (pos[r] + 1 + j) mod
+ * ring of row r.  The row's new last position is pos[r] + length[r] (pos itself
+ * is left to the caller).
+ *
+ *   k_tree, v_tree  host arrays of `layers` device pointers, each [rows, nodes, hkv, d] bf16
+ *   k_ring, v_ring  host arrays of `layers` device pointers, each [rows, ring[l], hkv, d] bf16, dense
+ *   ring    host array of `layers` ring lengths
+ *   lay     strides of the trees in elements (wa_tree_strides' k_* and v_*), or NULL: dense
+ *   path    [rows, most]  int32, device: wa_tree_verify's, or any other choice of nodes.
+ *                         An entry outside [0, nodes) is not copied (WA_STATUS_BAD_TREE)
+ *   length  [rows]        int32, device; outside [0, most]: clamped, BAD_TREE
+ *   pos     [rows]        int32, device; below -1: the row is not copied (WA_STATUS_BAD_POS)
+ *
+ * Where length exceeds a ring, the last ring[l] nodes are what stays.  The rings
+ * must not overlap the trees.
+ */
+int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const* v_tree, void* const* k_ring,
+                   void* const* v_ring, const int32_t* ring, int32_t rows, int32_t nodes, int32_t hkv, int32_t d,
+                   const wa_tree_strides* lay, const int32_t* path, int32_t most, const int32_t* length,
+                   const int32_t* pos, void* ws, size_t ws_bytes, void* stream);
 
 /* Waits for `stream`, then returns the WA_STATUS_* bits the last call that
  * used `ws` left (0 when clean), or a negative WA_E* code if the read fails.

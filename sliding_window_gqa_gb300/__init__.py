@@ -18,9 +18,10 @@ import torch
 
 __all__ = [
     "WAError", "lib", "lib_path", "decode", "decode_static", "prompt", "prompt_sparse", "prep_append", "status",
-    "decode_ws_bytes", "prompt_ws_bytes",
+    "tree_decode", "tree_verify", "tree_commit", "decode_ws_bytes", "prompt_ws_bytes", "tree_decode_ws_bytes",
     "WA_OK", "WA_EINVAL", "WA_EWORKSPACE", "WA_ECUDA", "WA_EDEVICE",
     "WA_STATUS_BAD_POS", "WA_STATUS_BAD_HI", "WA_STATUS_TIMEOUT",
+    "WA_STATUS_BAD_TREE", "WA_STATUS_NO_MASS", "WA_TREE_MAX_NODES", "WA_COMMIT_MAX_LAYERS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +48,10 @@ WA_EDEVICE = _C["WA_EDEVICE"]
 WA_STATUS_BAD_POS = _C["WA_STATUS_BAD_POS"]
 WA_STATUS_BAD_HI = _C["WA_STATUS_BAD_HI"]
 WA_STATUS_TIMEOUT = _C["WA_STATUS_TIMEOUT"]
+WA_STATUS_BAD_TREE = _C["WA_STATUS_BAD_TREE"]
+WA_STATUS_NO_MASS = _C["WA_STATUS_NO_MASS"]
+WA_TREE_MAX_NODES = _C["WA_TREE_MAX_NODES"]
+WA_COMMIT_MAX_LAYERS = _C["WA_COMMIT_MAX_LAYERS"]
 
 
 class WAError(RuntimeError):
@@ -62,6 +67,14 @@ class _Strides(ctypes.Structure):
 class _PrepLayout(ctypes.Structure):
     _fields_ = [("src_tok", ctypes.c_int64), ("q_tok", ctypes.c_int64), ("ring_row", ctypes.c_int64),
                 ("slot", ctypes.c_int64)]
+
+
+class _TreeStrides(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("q_row", "q_tok", "k_row", "k_tok", "v_row", "v_tok", "out_row", "out_tok")]
+
+
+class _VerifyStrides(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("t_row", "t_node", "d_row", "d_node")]
 
 
 _lib = None
@@ -98,6 +111,17 @@ def lib() -> ctypes.CDLL:
         L.wa_prep_append.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _I, ctypes.POINTER(_PrepLayout),
                                      _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.wa_prep_append.restype = ctypes.c_int
+        L.wa_tree_decode_ws_bytes.argtypes = [_I] * 7
+        L.wa_tree_decode_ws_bytes.restype = ctypes.c_size_t
+        L.wa_tree_decode.argtypes = [_P] * 8 + [_I] * 7 + [ctypes.c_float, ctypes.POINTER(_TreeStrides), _P, _P,
+                                                          ctypes.c_size_t, _P]
+        L.wa_tree_decode.restype = ctypes.c_int
+        L.wa_tree_verify.argtypes = [_P] * 6 + [_I] * 3 + [ctypes.POINTER(_VerifyStrides), _P, _P, _P, _P,
+                                                          ctypes.c_size_t, _P]
+        L.wa_tree_verify.restype = ctypes.c_int
+        L.wa_tree_commit.argtypes = [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.POINTER(_TreeStrides), _P, _I, _P,
+                                     _P, _P, ctypes.c_size_t, _P]
+        L.wa_tree_commit.restype = ctypes.c_int
         L.wa_status.argtypes = [_P, _P]
         L.wa_status.restype = ctypes.c_int
         L.wa_strerror.argtypes = [ctypes.c_int]
@@ -353,6 +377,243 @@ def prep_append(src, pos, q_out, k_ring, v_ring=None, mode: str = "rmsnorm", q_s
                               ws.data_ptr(), _ws_bytes(ws), _stream_handle(stream))
     if rc != WA_OK:
         raise WAError(rc, "wa_prep_append")
+    return ws
+
+
+# Drafted tokens.  These calls run on their inputs' device, whichever is current, and on `stream`
+# or that device's current stream; what they allocate is kept for that stream.
+
+class _on_device:
+    """The inputs' device made current for a call, where it is not already."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _keep_for(stream, *made) -> None:
+    """Memory allocated on the current stream and used on another is not reused before that one is done."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _check_i32(name: str, t, shape) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda:
+        raise TypeError(f"{name} must be an int32 CUDA tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and of shape {tuple(shape)}")
+
+
+def _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out):
+    """(rows, nodes, hq, hkv, d, ring) of a tree decode call; ValueError if the tensors disagree."""
+    if q.dim() != 4 or k_ring.dim() != 4:
+        raise ValueError("q must be [rows, nodes, hq, d] and k_ring [rows, ring, hkv, d]")
+    rows, nodes, hq, d = q.shape
+    _, ring, hkv, _ = k_ring.shape
+    if k_ring.shape[0] != rows or k_ring.shape[3] != d:
+        raise ValueError(f"k_ring {tuple(k_ring.shape)} does not match q {tuple(q.shape)}")
+    if v_ring.shape != k_ring.shape:
+        raise ValueError(f"v_ring {tuple(v_ring.shape)} must have k_ring's shape {tuple(k_ring.shape)}")
+    if not k_ring.is_contiguous() or not v_ring.is_contiguous():
+        raise ValueError("k_ring and v_ring must be contiguous")
+    for name, t in (("k_tree", k_tree), ("v_tree", v_tree)):
+        if t.shape != (rows, nodes, hkv, d):
+            raise ValueError(f"{name} must have shape {(rows, nodes, hkv, d)}")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape):
+        raise ValueError(f"out must be a bf16 tensor of q's shape {tuple(q.shape)}")
+    return rows, nodes, hq, hkv, d, ring
+
+
+def _node_strides(name: str, t: torch.Tensor, d: int):
+    """(row, node) strides in elements of a [rows, nodes, heads, d] tensor."""
+    row, tok, head, one = t.stride()
+    rows, nodes, heads, _ = t.shape
+    if one != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name} must be [rows, nodes, heads, d] with head stride d and unit dim stride")
+    # a dimension of one element may carry any stride
+    tok = tok if nodes > 1 else heads * d
+    row = row if rows > 1 else tok * nodes
+    if tok < heads * d or row < heads * d:      # an expanded tensor: the library reads stride 0 as dense
+        raise ValueError(f"{name}'s rows and nodes must not share memory")
+    return row, tok
+
+
+def tree_decode_ws_bytes(rows: int, nodes: int, hq: int, hkv: int, d: int, win: int, ring: int) -> int:
+    return int(lib().wa_tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring))
+
+
+def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None, scale: float = 1.0,
+                out=None, ws=None, stream=None):
+    """Decode for a tree of drafted tokens a row.
+
+    q [rows, nodes, hq, d] and k_tree / v_tree [rows, nodes, hkv, d] hold the nodes (bf16, row- and
+    node-strided), k_ring / v_ring [rows, ring, hkv, d] (dense) the cache up to position pos (int32
+    [rows], -1 = empty).  parent int32 [rows, nodes]: the node before each (below its own index), -1
+    for one that follows the cache; n int32 [rows] or None: nodes in use.  A node sees the cache, its
+    ancestors and itself, as far as the window reaches back.  Returns out [rows, nodes, hq, d] bf16,
+    whose nodes past n are not written.  ``ws``: a reused uint8 CUDA buffer of tree_decode_ws_bytes(...)."""
+    for n_, t in (("q", q), ("k_ring", k_ring), ("v_ring", v_ring), ("k_tree", k_tree), ("v_tree", v_tree)):
+        _check_bf16(n_, t)
+    rows, nodes, hq, hkv, d, ring = _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out)
+    _check_i32("pos", pos, (rows,))
+    _check_i32("parent", parent, (rows, nodes))
+    if n is not None:
+        _check_i32("n", n, (rows,))
+    dev = q.device
+    _same_device(dev, k_ring=k_ring, v_ring=v_ring, k_tree=k_tree, v_tree=v_tree, pos=pos, parent=parent, n=n, out=out)
+    with _on_device(dev):
+        made = [None, None]
+        if out is None:
+            out = made[0] = torch.empty((rows, nodes, hq, d), dtype=torch.bfloat16, device=dev)
+        st = _TreeStrides(*_node_strides("q", q, d), *_node_strides("k_tree", k_tree, d),
+                          *_node_strides("v_tree", v_tree, d), *_node_strides("out", out, d))
+        if ws is None:
+            made[1] = ws = _workspace(tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring), dev, None)
+        else:
+            _workspace(0, dev, ws)
+        rc = lib().wa_tree_decode(q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(),
+                                  v_tree.data_ptr(), pos.data_ptr(), parent.data_ptr(),
+                                  None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring,
+                                  float(scale), ctypes.byref(st), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
+                                  _stream_handle(stream))
+        _keep_for(stream, *made)
+    if rc != WA_OK:
+        raise WAError(rc, "wa_tree_decode")
+    return out
+
+
+def _prob_strides(name: str, t: torch.Tensor, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be an fp32 CUDA tensor")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be [rows, nodes, vocab], the same for target and draft")
+    rows, nodes, vocab = t.shape
+    if vocab > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride over the vocabulary")
+    node = t.stride(1) if nodes > 1 else vocab
+    row = t.stride(0) if rows > 1 else node * nodes
+    if node < vocab or row < vocab:      # an expanded tensor: the library reads stride 0 as dense
+        raise ValueError(f"{name}'s rows and nodes must not share memory")
+    return row, node
+
+
+def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length=None, token=None, ws=None,
+                stream=None):
+    """Which drafted tokens the target keeps, and the token after them: speculative sampling over a tree.
+
+    target fp32 [rows, nodes, vocab]: the target's probabilities after each node; draft: those that the
+    node's children were drawn from, or None where they were not drawn.  parent, tokens int32
+    [rows, nodes]; node 0 is the last sampled token.  u fp32 [rows, nodes] in [0, 1): u[:, c] tests node
+    c, u[:, 0] samples the last token.  n int32 [rows] or None: nodes in use.  Returns (path int32
+    [rows, nodes], length int32 [rows], token int32 [rows]): the kept nodes in order, then -1; how many;
+    the token sampled after them (-1: no nodes, or a distribution without mass)."""
+    t_row, t_node = _prob_strides("target", target, None)
+    rows, nodes, vocab = target.shape
+    d_row, d_node = (0, 0) if draft is None else _prob_strides("draft", draft, target.shape)
+    _check_i32("parent", parent, (rows, nodes))
+    _check_i32("tokens", tokens, (rows, nodes))
+    if not isinstance(u, torch.Tensor) or u.dtype != torch.float32 or not u.is_cuda:
+        raise TypeError("u must be an fp32 CUDA tensor")
+    if u.shape != (rows, nodes) or not u.is_contiguous():
+        raise ValueError(f"u must be contiguous and of shape {(rows, nodes)}")
+    for n_, t, shape in (("n", n, (rows,)), ("path", path, (rows, nodes)), ("length", length, (rows,)),
+                         ("token", token, (rows,))):
+        if t is not None:
+            _check_i32(n_, t, shape)
+    dev = target.device
+    _same_device(dev, draft=draft, parent=parent, tokens=tokens, u=u, n=n, path=path, length=length, token=token)
+    with _on_device(dev):
+        made = []
+        if path is None or length is None or token is None:
+            # one allocation for the outputs that are not given
+            buf = torch.empty(rows * (nodes + 2), dtype=torch.int32, device=dev)
+            made.append(buf)
+            length = buf[:rows] if length is None else length
+            token = buf[rows:2 * rows] if token is None else token
+            path = buf[2 * rows:].view(rows, nodes) if path is None else path
+        if ws is None:
+            ws = _workspace(256, dev, None)
+            made.append(ws)
+        else:
+            _workspace(0, dev, ws)
+        st = _VerifyStrides(t_row, t_node, d_row, d_node)
+        rc = lib().wa_tree_verify(target.data_ptr(), None if draft is None else draft.data_ptr(), parent.data_ptr(),
+                                  tokens.data_ptr(), None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes,
+                                  vocab, ctypes.byref(st), path.data_ptr(), length.data_ptr(), token.data_ptr(),
+                                  ws.data_ptr(), _ws_bytes(ws), _stream_handle(stream))
+        _keep_for(stream, *made)
+    if rc != WA_OK:
+        raise WAError(rc, "wa_tree_verify")
+    return path, length, token
+
+
+def _layer_list(name: str, ts):
+    ts = [ts] if isinstance(ts, torch.Tensor) else list(ts)
+    for t in ts:
+        _check_bf16(name, t)
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [rows, nodes or ring, hkv, d]")
+    return ts
+
+
+def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stream=None):
+    """The kept nodes' keys and values into the rings: node path[r, j], j < length[r], goes to slot
+    (pos[r] + 1 + j) mod ring.
+
+    k_tree / v_tree [rows, nodes, hkv, d] and k_ring / v_ring [rows, ring, hkv, d] (bf16), or lists of
+    them, one a layer (at most WA_COMMIT_MAX_LAYERS; rings may differ in length, trees share their
+    strides).  path int32 [rows, most], length and pos int32 [rows], as tree_verify returned and
+    tree_decode took them; afterwards the row's last position is pos + length.  Returns the
+    workspace, whose status status() reads."""
+    kt, vt, kr, vr = (_layer_list(*x) for x in (("k_tree", k_tree), ("v_tree", v_tree), ("k_ring", k_ring),
+                                               ("v_ring", v_ring)))
+    L = len(kt)
+    if not (0 < L <= WA_COMMIT_MAX_LAYERS) or not len(vt) == len(kr) == len(vr) == L:
+        raise ValueError(f"between 1 and {WA_COMMIT_MAX_LAYERS} layers, the same number of each tensor")
+    shape = kt[0].shape
+    rows, nodes, hkv, d = shape
+    k_st, v_st = _node_strides("k_tree", kt[0], d), _node_strides("v_tree", vt[0], d)
+    dev = kt[0].device
+    for l in range(L):
+        if kt[l].shape != shape or vt[l].shape != shape:
+            raise ValueError(f"k_tree and v_tree must have one shape, {tuple(shape)}")
+        if l and (_node_strides("k_tree", kt[l], d) != k_st or _node_strides("v_tree", vt[l], d) != v_st):
+            raise ValueError("the layers' trees must have the same strides")
+        want = (rows, kr[l].shape[1], hkv, d)
+        if kr[l].shape != want or vr[l].shape != want or not kr[l].is_contiguous() or not vr[l].is_contiguous():
+            raise ValueError(f"k_ring and v_ring must be contiguous [rows, ring, hkv, d] = {want}")
+        _same_device(dev, k_tree=kt[l], v_tree=vt[l], k_ring=kr[l], v_ring=vr[l])
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be [rows, most]")
+    most = path.shape[1]
+    _check_i32("path", path, (rows, most))
+    _check_i32("length", length, (rows,))
+    _check_i32("pos", pos, (rows,))
+    _same_device(dev, path=path, length=length, pos=pos)
+    with _on_device(dev):
+        made = None
+        if ws is None:
+            made = ws = _workspace(256, dev, None)
+        else:
+            _workspace(0, dev, ws)
+        ptrs = [(_P * L)(*[t.data_ptr() for t in ts]) for ts in (kt, vt, kr, vr)]
+        rings = (_I * L)(*[t.shape[1] for t in kr])
+        st = _TreeStrides(0, 0, *k_st, *v_st, 0, 0)
+        rc = lib().wa_tree_commit(L, *ptrs, rings, rows, nodes, hkv, d, ctypes.byref(st), path.data_ptr(), most,
+                                  length.data_ptr(), pos.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
+                                  _stream_handle(stream))
+        _keep_for(stream, made)
+    if rc != WA_OK:
+        raise WAError(rc, "wa_tree_commit")
     return ws
 
 

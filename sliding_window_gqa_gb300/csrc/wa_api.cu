@@ -4,7 +4,8 @@
 // request #1123, section "What this changes": decode (bullet "Decode") and
 // prompt rows with an optional per-row last key (bullet "promptRows(...,
 // hi)"), a scale parameter and window 0 as a linear cache (bullet "Scale is
-// a parameter"), and the optional two-half P (bullet "Window.p32").
+// a parameter"), and the optional two-half P (bullet "Window.p32").  The calls
+// for drafted tokens (tree decode, verification, commit) build on the decode form.
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -225,6 +226,145 @@ int wa_prep_append(const void* src, const int32_t* pos, int32_t n, int32_t hq, i
     return WA_OK;
 }
 
+size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t hkv, int32_t d, int32_t win,
+                               int32_t ring) {
+    if (rows <= 0 || nodes <= 0 || nodes > WA_TREE_MAX_NODES || !heads_ok(hq, hkv) || (d != 128 && d != 256) ||
+        win < 0 || ring <= 0 || win > ring)
+        return 0;
+    const int64_t units = static_cast<int64_t>(rows) * nodes * hq;
+    if (units > INT32_MAX) return 0;
+    return wa::kHeaderBytes + flags_bytes(units);
+}
+
+int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
+                   const int32_t* pos, const int32_t* parent, const int32_t* n, int32_t rows, int32_t nodes,
+                   int32_t hq, int32_t hkv, int32_t d, int32_t win, int32_t ring, float scale,
+                   const wa_tree_strides* strides, void* out, void* ws, size_t ws_bytes, void* stream) {
+    if (!q || !k_ring || !v_ring || !k_tree || !v_tree || !pos || !parent || !out) return WA_EINVAL;
+    if (rows <= 0 || rows > 65535 || nodes <= 0 || nodes > WA_TREE_MAX_NODES || !heads_ok(hq, hkv) || hkv > 65535)
+        return WA_EINVAL;
+    if (d != 128 && d != 256) return WA_EINVAL;
+    if (win < 0 || ring <= 0 || win > ring) return WA_EINVAL;
+    if (!std::isfinite(scale)) return WA_EINVAL;
+    if (static_cast<int64_t>(rows) * nodes * hq > INT32_MAX) return WA_EINVAL;
+    const int64_t qw = static_cast<int64_t>(hq) * d, kw = static_cast<int64_t>(hkv) * d;
+    wa::TreeArgs a{};
+    a.q_tok = a.o_tok = qw;
+    a.kt_tok = a.vt_tok = kw;
+    if (strides) {
+        if (strides->q_tok) a.q_tok = strides->q_tok;
+        if (strides->k_tok) a.kt_tok = strides->k_tok;
+        if (strides->v_tok) a.vt_tok = strides->v_tok;
+        if (strides->out_tok) a.o_tok = strides->out_tok;
+    }
+    a.q_row = a.q_tok * nodes; a.kt_row = a.kt_tok * nodes; a.vt_row = a.vt_tok * nodes; a.o_row = a.o_tok * nodes;
+    if (strides) {
+        if (strides->q_row) a.q_row = strides->q_row;
+        if (strides->k_row) a.kt_row = strides->k_row;
+        if (strides->v_row) a.vt_row = strides->v_row;
+        if (strides->out_row) a.o_row = strides->out_row;
+    }
+    if (a.q_tok < qw || a.o_tok < qw || a.kt_tok < kw || a.vt_tok < kw) return WA_EINVAL;
+    if (a.q_row < qw || a.o_row < qw || a.kt_row < kw || a.vt_row < kw) return WA_EINVAL;
+    if ((a.q_tok | a.q_row | a.o_tok | a.o_row | a.kt_tok | a.kt_row | a.vt_tok | a.vt_row) & 7) return WA_EINVAL;
+    if (!aligned16(q) || !aligned16(k_ring) || !aligned16(v_ring) || !aligned16(k_tree) || !aligned16(v_tree) ||
+        !aligned16(out))
+        return WA_EINVAL;
+    const size_t need = wa_tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring);
+    if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    a.q = q; a.k = k_ring; a.v = v_ring; a.kt = k_tree; a.vt = v_tree;
+    a.pos = pos; a.parent = parent; a.n = n;
+    a.rows = rows; a.nodes = nodes; a.hq = hq; a.hkv = hkv; a.d = d; a.win = win; a.ring = ring; a.scale = scale;
+    a.out = out;
+    a.hdr = reinterpret_cast<wa::WsHeader*>(base);
+    a.flags = reinterpret_cast<int*>(base + wa::kHeaderBytes);
+    if (cudaMemsetAsync(base, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
+    if (wa::launch_tree(a, s) != cudaSuccess) return WA_ECUDA;
+
+    wa::RerunArgs r{};
+    r.mode = 3; r.q = q; r.k = k_ring; r.v = v_ring; r.kt = k_tree; r.vt = v_tree; r.idx = pos; r.parent = parent;
+    r.n = n; r.nodes = nodes;
+    r.rows = rows * nodes; r.hq = hq; r.hkv = hkv; r.d = d; r.win = win; r.ring = ring; r.scale = scale;
+    r.q_row = a.q_row; r.q_tok = a.q_tok; r.kt_row = a.kt_row; r.kt_tok = a.kt_tok; r.vt_row = a.vt_row;
+    r.vt_tok = a.vt_tok; r.o_row = a.o_row; r.o_tok = a.o_tok;
+    r.out = out; r.hdr = a.hdr; r.flags = a.flags;
+    if (wa::launch_rerun(r, s) != cudaSuccess) return WA_ECUDA;
+    return WA_OK;
+}
+
+int wa_tree_verify(const float* target, const float* draft, const int32_t* parent, const int32_t* tokens,
+                   const int32_t* n, const float* u, int32_t rows, int32_t nodes, int32_t vocab,
+                   const wa_verify_strides* strides, int32_t* path, int32_t* length, int32_t* token,
+                   void* ws, size_t ws_bytes, void* stream) {
+    if (!target || !parent || !tokens || !u || !path || !length || !token) return WA_EINVAL;
+    if (rows <= 0 || rows > 65535 || nodes <= 0 || nodes > WA_TREE_MAX_NODES || vocab <= 0 || vocab > (1 << 24))
+        return WA_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & 3u) return WA_EINVAL;
+    wa::VerifyArgs a{};
+    a.t_node = a.d_node = vocab;
+    if (strides && strides->t_node) a.t_node = strides->t_node;
+    if (strides && strides->d_node) a.d_node = strides->d_node;
+    a.t_row = a.t_node * nodes;
+    a.d_row = a.d_node * nodes;
+    if (strides && strides->t_row) a.t_row = strides->t_row;
+    if (strides && strides->d_row) a.d_row = strides->d_row;
+    if (a.t_node < vocab || a.t_row < vocab || (draft && (a.d_node < vocab || a.d_row < vocab))) return WA_EINVAL;
+    if (!ws || ws_bytes < WA_TREE_WS_BYTES || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.target = target; a.draft = draft; a.parent = parent; a.tokens = tokens; a.n = n; a.u = u;
+    a.rows = rows; a.nodes = nodes; a.vocab = vocab;
+    a.path = path; a.length = length; a.token = token;
+    a.hdr = static_cast<wa::WsHeader*>(ws);
+    if (cudaMemsetAsync(ws, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
+    if (wa::launch_verify(a, s) != cudaSuccess) return WA_ECUDA;
+    return WA_OK;
+}
+
+int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const* v_tree, void* const* k_ring,
+                   void* const* v_ring, const int32_t* ring, int32_t rows, int32_t nodes, int32_t hkv, int32_t d,
+                   const wa_tree_strides* lay, const int32_t* path, int32_t most, const int32_t* length,
+                   const int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
+    if (!k_tree || !v_tree || !k_ring || !v_ring || !ring || !path || !length || !pos) return WA_EINVAL;
+    if (layers <= 0 || layers > WA_COMMIT_MAX_LAYERS || rows <= 0 || rows > 65535) return WA_EINVAL;
+    if (nodes <= 0 || nodes > WA_TREE_MAX_NODES || most <= 0 || most > WA_TREE_MAX_NODES) return WA_EINVAL;
+    if (hkv <= 0 || hkv > 65535 || (d != 128 && d != 256)) return WA_EINVAL;
+    const int64_t kw = static_cast<int64_t>(hkv) * d;
+    wa::CommitArgs a{};
+    a.tok[0] = lay && lay->k_tok ? lay->k_tok : kw;
+    a.tok[1] = lay && lay->v_tok ? lay->v_tok : kw;
+    a.row[0] = lay && lay->k_row ? lay->k_row : a.tok[0] * nodes;
+    a.row[1] = lay && lay->v_row ? lay->v_row : a.tok[1] * nodes;
+    for (int kv = 0; kv < 2; ++kv)
+        if (a.tok[kv] < kw || a.row[kv] < kw || ((a.tok[kv] | a.row[kv]) & 7)) return WA_EINVAL;
+    for (int l = 0; l < layers; ++l) {
+        if (!k_tree[l] || !v_tree[l] || !k_ring[l] || !v_ring[l] || ring[l] <= 0) return WA_EINVAL;
+        if (!aligned16(k_tree[l]) || !aligned16(v_tree[l]) || !aligned16(k_ring[l]) || !aligned16(v_ring[l]))
+            return WA_EINVAL;
+        a.src[0][l] = k_tree[l]; a.src[1][l] = v_tree[l];
+        a.dst[0][l] = k_ring[l]; a.dst[1][l] = v_ring[l];
+        a.ring[l] = ring[l];
+    }
+    if (!ws || ws_bytes < WA_TREE_WS_BYTES || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.layers = layers; a.rows = rows; a.nodes = nodes; a.hkv = hkv; a.d = d; a.most = most;
+    a.path = path; a.length = length; a.pos = pos;
+    a.hdr = static_cast<wa::WsHeader*>(ws);
+    if (cudaMemsetAsync(ws, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
+    if (wa::launch_commit(a, s) != cudaSuccess) return WA_ECUDA;
+    return WA_OK;
+}
+
 int wa_status(const void* ws, void* stream) {
     if (!ws) {   // the header of wa_decode_static's scratch on the current device
         void* sws = nullptr;
@@ -250,6 +390,8 @@ const char* wa_strerror(int code) {
         case WA_STATUS_BAD_POS: return "status: a decode or append position was out of range (clamped or skipped)";
         case WA_STATUS_BAD_HI: return "status: a prompt hi[i] was out of range (clamped)";
         case WA_STATUS_TIMEOUT: return "status: a device wait ran out; outputs are not valid";
+        case WA_STATUS_BAD_TREE: return "status: a tree's parent, node count, token, path or length was out of range (clamped or skipped)";
+        case WA_STATUS_NO_MASS: return "status: a distribution without mass; its row has no token";
         case WA_STATUS_LAYOUT: return "status: shared memory misaligned; outputs were not written";
         default:
             if (code > 0) return "status: several WA_STATUS bits";
@@ -257,6 +399,6 @@ const char* wa_strerror(int code) {
     }
 }
 
-int wa_version(void) { return 100; }
+int wa_version(void) { return 200; }
 
 }  // extern "C"

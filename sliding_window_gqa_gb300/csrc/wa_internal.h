@@ -7,6 +7,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "wa.h"
+
 namespace wa {
 
 constexpr int kChunk = 256;     // decode: keys per chunk, at absolute positions [256c, 256c+255]
@@ -54,9 +56,67 @@ struct PromptArgs {
     int nsel;
 };
 
-// Float64 re-run of every flagged (row, head); mode 0 = decode, 1 = prompt, 2 = block-sparse prompt.
+// Attention of trees of drafted tokens over ring caches.
+struct TreeArgs {
+    const void* q;
+    const void* k;           // ring
+    const void* v;
+    const void* kt;          // the nodes' keys and values
+    const void* vt;
+    const int32_t* pos;
+    const int32_t* parent;   // [rows, nodes]
+    const int32_t* n;        // may be null
+    int rows, nodes, hq, hkv, d, win, ring;
+    float scale;
+    int64_t q_row, q_tok, kt_row, kt_tok, vt_row, vt_tok, o_row, o_tok;   // elements
+    void* out;
+    WsHeader* hdr;
+    int* flags;              // [rows * nodes * hq]
+};
+
+// Verification of drafted tokens.
+struct VerifyArgs {
+    const float* target;
+    const float* draft;      // may be null
+    const int32_t* parent;
+    const int32_t* tokens;
+    const int32_t* n;        // may be null
+    const float* u;
+    int rows, nodes, vocab;
+    int64_t t_row, t_node, d_row, d_node;
+    int32_t* path;
+    int32_t* length;
+    int32_t* token;
+    WsHeader* hdr;
+};
+
+// Kept nodes' keys and values into the rings of several layers.
+struct CommitArgs {
+    const void* src[2][WA_COMMIT_MAX_LAYERS];   // [k, v]
+    void* dst[2][WA_COMMIT_MAX_LAYERS];
+    int ring[WA_COMMIT_MAX_LAYERS];
+    int64_t row[2], tok[2];                     // strides of the trees, elements
+    int layers, rows, nodes, hkv, d, most;
+    const int32_t* path;
+    const int32_t* length;
+    const int32_t* pos;
+    WsHeader* hdr;
+};
+
+// A node's parent as every kernel uses it: a value outside [-1, i) counts as -1.
+__host__ __device__ inline int tree_parent(int raw, int i) { return raw >= -1 && raw < i ? raw : -1; }
+
+// Float64 re-run of every flagged (row, head); mode 0 = decode, 1 = prompt, 2 = block-sparse prompt,
+// 3 = tree decode (a row there is a node: row * nodes + node).
 struct RerunArgs {
     int mode;
+    // mode 3 only
+    const void* kt;
+    const void* vt;
+    const int32_t* parent;
+    const int32_t* n;
+    int nodes;
+    int64_t q_row, kt_row, kt_tok, vt_row, vt_tok, o_row;
     const int32_t* sel;   // mode 2: [rows, hkv, nsel] selected 64-key blocks
     int nsel;
     const void* q;
@@ -94,6 +154,9 @@ cudaError_t launch_prompt_sparse(const PromptArgs& a, cudaStream_t s);
 cudaError_t prompt_sparse_prepare_device(int dev);
 cudaError_t launch_rerun(const RerunArgs& a, cudaStream_t s);
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t s);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t prompt_prepare_device(int dev);
 cudaError_t decode_prepare_device(int dev);
 // Decode partials on the tensor cores (query-head groups of kTcMinGroup and more); the merge is shared.

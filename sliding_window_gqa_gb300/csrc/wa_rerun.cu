@@ -9,6 +9,10 @@
 // in its selected 64-key blocks (TensorFold pull request #1622); a row with none
 // gets 0 / 0 = NaN, as the formula's empty sums give.
 //
+// The tree decode (mode 3) numbers a node's keys lo .. pos (the ring) and then
+// pos + 1 + t for node t of its tree, of which its ancestors and itself count,
+// those less than win positions back.
+//
 // A grid of a few CTAs per SM (at most one per (row, head)) walks the flagged
 // list; with nothing flagged every CTA exits at once.  Per flagged head:
 //   pass 0  fp32 scores (each bf16 x bf16 product is exact in fp32), keys in
@@ -116,6 +120,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
     __shared__ double wb[kRerunThreads];
     __shared__ double red[kRerunThreads / 32];
     __shared__ int sel_row[64];
+    __shared__ unsigned char anc[WA_TREE_MAX_NODES];   // mode 3: node t is visible
     __shared__ unsigned char vis[kRerunThreads];
     const int nflag = *reinterpret_cast<volatile int*>(&a.hdr->nflag);
     const int t = threadIdx.x;
@@ -133,7 +138,35 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
         const uint16_t *qrow, *kb, *vb;
         int64_t kst, vst;
         uint16_t* orow;
-        if (a.mode == 0) {
+        // mode 3: keys past `ring_last` are tree nodes
+        int ring_last = 0x7FFFFFFF;
+        const uint16_t *ktb = nullptr, *vtb = nullptr;
+        if (a.mode == 3) {
+            const int seq = row / a.nodes, node = row % a.nodes;
+            const int32_t* par = a.parent + static_cast<int64_t>(seq) * a.nodes;
+            int p = a.idx[seq];
+            if (p < -1) p = -1;
+            if (a.win == 0 && p >= a.ring) p = a.ring - 1;
+            int depth = 0;
+            for (int x = node; (x = tree_parent(par[x], x)) >= 0;) ++depth;
+            for (int x = t; x < a.nodes; x += kRerunThreads) anc[x] = 0;
+            __syncthreads();
+            if (t == 0) {
+                int back = 0;
+                for (int x = node; x >= 0 && (a.win == 0 || back < a.win); x = tree_parent(par[x], x), ++back) anc[x] = 1;
+            }
+            lo = a.win > 0 ? max(0, p + 1 + depth - a.win + 1) : 0;
+            ring_last = p;
+            lo = min(lo, p + 1);
+            last = p + 1 + node;      // an ancestor has a smaller index
+            qrow = q + seq * a.q_row + node * a.q_tok + static_cast<int64_t>(h) * d;
+            kb = k + static_cast<int64_t>(seq) * a.ring * a.hkv * d + static_cast<int64_t>(g) * d;
+            vb = v + static_cast<int64_t>(seq) * a.ring * a.hkv * d + static_cast<int64_t>(g) * d;
+            kst = vst = static_cast<int64_t>(a.hkv) * d;
+            ktb = static_cast<const uint16_t*>(a.kt) + seq * a.kt_row + static_cast<int64_t>(g) * d;
+            vtb = static_cast<const uint16_t*>(a.vt) + seq * a.vt_row + static_cast<int64_t>(g) * d;
+            orow = out + seq * a.o_row + node * a.o_tok + static_cast<int64_t>(h) * d;
+        } else if (a.mode == 0) {
             int p = a.idx[row];
             if (p < 0) p = 0;
             if (a.win == 0 && p >= a.ring) p = a.ring - 1;
@@ -165,14 +198,22 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
         if (t < nsel) sel_row[t] = a.sel[(static_cast<int64_t>(row) * a.hkv + g) * a.nsel + t];
         __syncthreads();
         // mode 2: key j counts only if its block j / 64 is selected
+        // mode 3: a tree node counts only if it is the node itself or an ancestor in the window
         auto selected = [&](int j) {
+            if (j > ring_last) return anc[j - ring_last - 1] != 0;
             if (a.mode != 2) return true;
             bool hit = false;
             for (int e = 0; e < nsel; ++e) hit |= sel_row[e] == (j >> 6);
             return hit;
         };
+        auto key = [&](int j) {
+            return j > ring_last ? ktb + (j - ring_last - 1) * a.kt_tok : kb + static_cast<int64_t>(j % a.ring) * kst;
+        };
+        auto val = [&](int j) {
+            return j > ring_last ? vtb + (j - ring_last - 1) * a.vt_tok : vb + static_cast<int64_t>(j % a.ring) * vst;
+        };
         auto score = [&](int j) {
-            const uint16_t* kr = kb + static_cast<int64_t>(j % a.ring) * kst;
+            const uint16_t* kr = key(j);
             return dot_f64(qd, kr, d) * static_cast<double>(a.scale);
         };
 
@@ -182,7 +223,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
             const int j = base + t;
             bool hit = false;
             if (j <= last && selected(j)) {
-                const float sf = dot_f32(qf, kb + static_cast<int64_t>(j % a.ring) * kst, d);
+                const float sf = dot_f32(qf, key(j), d);
                 if (!isfinite(sf)) {
                     const double s = score(j);
                     hit = isnan(s) || (isinf(s) && s > 0.0);
@@ -222,7 +263,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
                 const int cnt = min(kRerunThreads, last - base + 1);
                 for (int jj = 0; jj < cnt; ++jj)
                     if (vis[jj])
-                        acc = acc + wb[jj] * bf16_bits_to_f64(vb[static_cast<int64_t>((base + jj) % a.ring) * vst + t]);
+                        acc = acc + wb[jj] * bf16_bits_to_f64(val(base + jj)[t]);
             }
             __syncthreads();
         }

@@ -1,0 +1,160 @@
+"""Refusals of the calls for drafted tokens: the C ABI's argument errors and the binding's (CPU, before any CUDA call)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import sliding_window_gqa_gb300 as wa
+from _util import ensure_built
+
+FAKE = ctypes.c_void_p(1 << 20)    # never dereferenced: validation fails first
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _decode(**kw):
+    L = ensure_built().lib()
+    a = dict(q=FAKE, k=FAKE, v=FAKE, kt=FAKE, vt=FAKE, pos=FAKE, parent=FAKE, n=None, rows=3, nodes=8, hq=16, hkv=8,
+             d=256, win=1024, ring=1536, scale=1.0, st=None, out=FAKE, ws=FAKE, ws_bytes=1 << 40)
+    a.update(kw)
+    st = None if a["st"] is None else ctypes.byref(wa._TreeStrides(**a["st"]))
+    return L.wa_tree_decode(a["q"], a["k"], a["v"], a["kt"], a["vt"], a["pos"], a["parent"], a["n"], a["rows"],
+                            a["nodes"], a["hq"], a["hkv"], a["d"], a["win"], a["ring"], a["scale"], st, a["out"],
+                            a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=None), dict(kt=None), dict(pos=None), dict(parent=None), dict(out=None), dict(rows=0), dict(rows=65536),
+    dict(nodes=0), dict(nodes=129), dict(hq=12), dict(hq=136), dict(d=192), dict(d=64), dict(win=-1), dict(win=1537),
+    dict(ring=0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=ODD), dict(kt=ODD), dict(out=ODD),
+    dict(st=dict(q_tok=100)), dict(st=dict(q_tok=16 * 256 + 4)), dict(st=dict(k_row=8)), dict(st=dict(v_tok=-2048)),
+    dict(st=dict(out_row=-8)), dict(rows=60000, nodes=128, hq=512, hkv=512, d=128),
+], ids=str)
+def test_tree_decode_argument_errors(bad):
+    assert _decode(**bad) == wa.WA_EINVAL
+
+
+def test_tree_decode_workspace_errors():
+    need = ensure_built().lib().wa_tree_decode_ws_bytes(3, 8, 16, 8, 256, 1024, 1536)
+    assert need > 0
+    assert _decode(ws=None) == wa.WA_EWORKSPACE
+    assert _decode(ws_bytes=need - 1) == wa.WA_EWORKSPACE
+    assert _decode(ws=ctypes.c_void_p((1 << 20) + 128)) == wa.WA_EWORKSPACE
+
+
+@pytest.mark.parametrize("size", [(0, 8, 16, 8, 256, 0, 64), (1, 0, 16, 8, 256, 0, 64), (1, 129, 16, 8, 256, 0, 64),
+                                  (1, 8, 17, 8, 256, 0, 64), (1, 8, 16, 8, 192, 0, 64), (1, 8, 16, 8, 256, 65, 64),
+                                  (1, 8, 16, 8, 256, 0, 0)])
+def test_tree_decode_ws_bytes_of_invalid_sizes(size):
+    assert ensure_built().lib().wa_tree_decode_ws_bytes(*size) == 0
+
+
+def _verify(**kw):
+    L = ensure_built().lib()
+    a = dict(target=FAKE, draft=FAKE, parent=FAKE, tokens=FAKE, n=None, u=FAKE, rows=3, nodes=8, vocab=1000, st=None,
+             path=FAKE, length=FAKE, token=FAKE, ws=FAKE, ws_bytes=256)
+    a.update(kw)
+    st = None if a["st"] is None else ctypes.byref(wa._VerifyStrides(**a["st"]))
+    return L.wa_tree_verify(a["target"], a["draft"], a["parent"], a["tokens"], a["n"], a["u"], a["rows"], a["nodes"],
+                            a["vocab"], st, a["path"], a["length"], a["token"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(target=None), dict(parent=None), dict(tokens=None), dict(u=None), dict(path=None), dict(length=None),
+    dict(token=None), dict(rows=0), dict(rows=65536), dict(nodes=0), dict(nodes=129), dict(vocab=0),
+    dict(vocab=(1 << 24) + 1), dict(target=ODD), dict(draft=ODD), dict(st=dict(t_node=999)), dict(st=dict(t_row=8)),
+    dict(st=dict(d_node=-1000)),
+], ids=str)
+def test_tree_verify_argument_errors(bad):
+    assert _verify(**bad) == wa.WA_EINVAL
+
+
+def test_tree_verify_workspace_errors():
+    assert _verify(ws=None) == wa.WA_EWORKSPACE
+    assert _verify(ws_bytes=255) == wa.WA_EWORKSPACE
+    assert _verify(ws=ctypes.c_void_p((1 << 20) + 8)) == wa.WA_EWORKSPACE
+
+
+def _commit(**kw):
+    L = ensure_built().lib()
+    a = dict(layers=2, ptr=1 << 20, ring=64, rows=3, nodes=8, hkv=8, d=256, st=None, path=FAKE, most=8, length=FAKE,
+             pos=FAKE, ws=FAKE, ws_bytes=256, lists=True)
+    a.update(kw)
+    st = None if a["st"] is None else ctypes.byref(wa._TreeStrides(**a["st"]))
+    arr = (ctypes.c_void_p * 64)(*[a["ptr"]] * 64) if a["lists"] else None
+    return L.wa_tree_commit(a["layers"], arr, arr, arr, arr, (ctypes.c_int32 * 64)(*[a["ring"]] * 64), a["rows"],
+                            a["nodes"], a["hkv"], a["d"], st, a["path"], a["most"], a["length"], a["pos"], a["ws"],
+                            a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(layers=0), dict(layers=65), dict(ptr=0), dict(ptr=(1 << 20) + 8), dict(ring=0), dict(rows=0), dict(nodes=0),
+    dict(nodes=129), dict(hkv=0), dict(d=64), dict(path=None), dict(most=0), dict(most=129), dict(length=None),
+    dict(pos=None), dict(lists=False), dict(st=dict(k_tok=8)), dict(st=dict(v_tok=8 * 256 + 4)),
+], ids=str)
+def test_tree_commit_argument_errors(bad):
+    assert _commit(**bad) == wa.WA_EINVAL
+
+
+def test_tree_commit_workspace_errors():
+    assert _commit(ws=None) == wa.WA_EWORKSPACE
+    assert _commit(ws_bytes=128) == wa.WA_EWORKSPACE
+
+
+def test_status_names():
+    L = ensure_built().lib()
+    assert b"tree" in L.wa_strerror(wa.WA_STATUS_BAD_TREE)
+    assert b"mass" in L.wa_strerror(wa.WA_STATUS_NO_MASS)
+
+
+# ---- the binding: tensors that disagree never reach the library
+
+def _shapes(**kw):
+    a = dict(q=bf16(3, 8, 16, 256), k_ring=bf16(3, 64, 8, 256), v_ring=bf16(3, 64, 8, 256), k_tree=bf16(3, 8, 8, 256),
+             v_tree=bf16(3, 8, 8, 256), out=None)
+    a.update(kw)
+    return wa._tree_shapes(**a)
+
+
+def test_tree_shapes_accept_a_consistent_call():
+    assert _shapes() == (3, 8, 16, 8, 256, 64)
+    assert _shapes(out=bf16(3, 8, 16, 256)) == (3, 8, 16, 8, 256, 64)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=bf16(8, 16, 256)), dict(k_ring=bf16(2, 64, 8, 256)), dict(k_ring=bf16(3, 64, 8, 128)),
+    dict(v_ring=bf16(3, 63, 8, 256)), dict(k_tree=bf16(3, 7, 8, 256)), dict(v_tree=bf16(3, 8, 4, 256)),
+    dict(out=bf16(3, 8, 8, 256)), dict(out=torch.zeros(3, 8, 16, 256)),
+    dict(k_ring=bf16(64, 3, 8, 256).transpose(0, 1)),
+], ids=range(9))
+def test_tree_shapes_refuse_disagreeing_tensors(bad):
+    with pytest.raises(ValueError):
+        _shapes(**bad)
+
+
+def test_node_strides():
+    assert wa._node_strides("q", bf16(3, 8, 16, 256), 256) == (8 * 4096, 4096)
+    assert wa._node_strides("q", bf16(8, 3, 16, 256).transpose(0, 1), 256) == (4096, 3 * 4096)
+    fused = bf16(3, 8, 24 * 128)
+    assert wa._node_strides("v", fused[:, :, 20 * 128:].unflatten(2, (4, 128)), 128) == (8 * 24 * 128, 24 * 128)
+    assert wa._node_strides("q", bf16(1, 1, 4, 128), 128) == (512, 512)
+    for t in (bf16(1, 8, 4, 128).expand(3, 8, 4, 128), bf16(3, 1, 4, 128).expand(3, 8, 4, 128),
+              bf16(3, 8, 4, 256)[..., ::2], bf16(3, 8, 8, 128)[:, :, ::2]):
+        with pytest.raises(ValueError):
+            wa._node_strides("q", t, 128)
+
+
+def test_calls_refuse_host_tensors_and_types():
+    q, ring, tr = bf16(1, 2, 4, 128), bf16(1, 8, 4, 128), bf16(1, 2, 4, 128)
+    i = torch.zeros((1, 2), dtype=torch.int32)
+    with pytest.raises(TypeError):
+        wa.tree_decode(q, ring, ring, tr, tr, i[:, 0], i, 0)
+    with pytest.raises(TypeError):
+        wa.tree_verify(torch.zeros(1, 2, 9), i, i, torch.zeros(1, 2))
+    with pytest.raises(TypeError):
+        wa.tree_commit(tr, tr, ring, ring, i, i[:, 0], i[:, 0])

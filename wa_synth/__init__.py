@@ -33,6 +33,8 @@ __all__ = [
     "prompt_case",
     "dense_qkv_case",
     "sparse_selection",
+    "draft_tree",
+    "tree_case",
     "window_lo",
 ]
 
@@ -230,3 +232,48 @@ def sparse_selection(n, p0, hkv, nsel, seed, win=0, slice_rows=64, block=64, dev
                         blocks.append(b)
             sel[i, g, :len(blocks)] = torch.tensor(blocks[:nsel], dtype=torch.int32)
     return sel.to(device)
+
+
+def draft_tree(kind, nodes, seed):
+    """Parents of a tree over `nodes` nodes (parents before children, node 0 a root): "chain", "bushy" (three
+    children a node, level by level), "flat" (all nodes roots) or "random"."""
+    gen = torch.Generator().manual_seed(int(seed) * 104_729 + 5)
+    if kind == "chain":
+        return [i - 1 for i in range(nodes)]
+    if kind == "flat":
+        return [-1] * nodes
+    if kind == "bushy":
+        return [-1] + [(i - 1) // 3 for i in range(1, nodes)]
+    return [-1] + [int(torch.randint(max(0, i - 6), i, (1,), generator=gen)) for i in range(1, nodes)]
+
+
+def tree_case(rows, nodes, hq, hkv, d, win, ring, pos, seed, kind="random", n=None, device="cpu", outside="nan"):
+    """Tree-decode inputs: decode_case's rings up to position pos (-1: an empty cache), and per row a tree of
+    `nodes` nodes with q [rows,nodes,hq,d], k_tree / v_tree [rows,nodes,hkv,d] (bf16), parent int32
+    [rows,nodes].  With ``outside == "nan"`` the rings' slots without a visible key and the nodes past n[r]
+    hold NaN."""
+    device = torch.device(device)
+    c = decode_case(rows, hq, hkv, d, win, ring, [max(0, p) for p in pos], seed, device=device, outside=outside)
+    q, _ = _draw_rows((rows, nodes, hq, d), 0.95, 1.05, _gen(seed + 1, "q", device), _gen(seed + 1, "qr", device),
+                      device)
+    kt, kr = _draw_rows((rows, nodes, hkv, d), 0.06, 0.13, _gen(seed + 1, "k", device), _gen(seed + 1, "kr", device),
+                        device)
+    vt = torch.randn((rows, nodes, hkv, d), generator=_gen(seed + 1, "v", device), device=device)
+    q, kt, vt = q.to(torch.bfloat16), kt.to(torch.bfloat16), vt.to(torch.bfloat16)
+    G = hq // hkv
+    for i in range(0, nodes, 3):      # every third node peaks on itself or, for its children, on their parent
+        qh = q[:, i, i % G::G].float()
+        kt[:, i] = (qh * (kr[:, i] / torch.sqrt((qh * qh).mean(-1, keepdim=True)))).to(torch.bfloat16)
+    for r in range(rows):
+        if pos[r] < 0 and outside == "nan":
+            c["k"][r] = float("nan")
+            c["v"][r] = float("nan")
+        if n is not None and outside == "nan":
+            q[r, n[r]:] = float("nan")
+            kt[r, n[r]:] = float("nan")
+            vt[r, n[r]:] = float("nan")
+    c.update(q=q, k_tree=kt, v_tree=vt, nodes=nodes, pos=torch.tensor(pos, dtype=torch.int32, device=device),
+             parent=torch.tensor([draft_tree(kind, nodes, seed + r) for r in range(rows)], dtype=torch.int32,
+                                 device=device),
+             n=None if n is None else torch.tensor(n, dtype=torch.int32, device=device))
+    return c
