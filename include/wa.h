@@ -275,8 +275,9 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
  *   v_ring  [rows, ring, hkv, d]   bf16, dense
  *   k_tree  [rows, nodes, hkv, d]  bf16: the nodes' keys, not in the ring
  *   v_tree  [rows, nodes, hkv, d]  bf16
- *   pos     [rows]         int32, device; -1 for an empty cache.  Below -1, or
- *                          >= ring with win = 0: clamped, WA_STATUS_BAD_POS
+ *   pos     [rows]         int32, device; -1 for an empty cache.  Below -1,
+ *                          above 2^31 - 4097, or >= ring with win = 0: clamped,
+ *                          WA_STATUS_BAD_POS
  *   parent  [rows, nodes]  int32, device; a value outside [-1, i) counts as -1
  *                          and is reported (WA_STATUS_BAD_TREE)
  *   n       [rows]         int32, device, or NULL (all nodes): row r's nodes are
@@ -287,7 +288,9 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
  * as in wa_decode's tensor-core form.  The softmax runs over 128-key tiles at
  * absolute positions, in spans whose ends depend on the row's own position,
  * the window and hkv alone: an output's bits do not depend on the batch, the
- * row's place in it, nodes, n, or other branches of the tree.  1 <= nodes <=
+ * row's place in it, nodes, n, or other branches of the tree.  (A NaN or
+ * infinite value in v that some of a row's nodes do not see makes theirs
+ * non-finite ones to compute again: float64's values, rounded.)  1 <= nodes <=
  * WA_TREE_MAX_NODES; other constraints as wa_decode, WA_EINVAL otherwise.
  * Calls whose work can overlap need workspaces of their own; two captured
  * graphs that replay at the same time do too.

@@ -45,7 +45,7 @@ int ensure_device() {
         return WA_EDEVICE;
     }
     if (wa::decode_prepare_device(dev) != cudaSuccess || wa::prompt_prepare_device(dev) != cudaSuccess ||
-        wa::prompt_sparse_prepare_device(dev) != cudaSuccess)
+        wa::prompt_sparse_prepare_device(dev) != cudaSuccess || wa::tree_prepare_device(dev) != cudaSuccess)
         return WA_ECUDA;
     g_ready[dev] = 1;
     return WA_OK;
@@ -232,8 +232,10 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
         win < 0 || ring <= 0 || win > ring)
         return 0;
     const int64_t units = static_cast<int64_t>(rows) * nodes * hq;
-    if (units > INT32_MAX) return 0;
-    return wa::kHeaderBytes + flags_bytes(units);
+    const wa::TreePlan pl = wa::tree_plan(rows, nodes, hq, hkv, win, ring);
+    if (units > INT32_MAX || pl.units > INT32_MAX / 2) return 0;
+    return wa::kHeaderBytes + flags_bytes(units) +
+           static_cast<size_t>(pl.units) * pl.lanes * (static_cast<size_t>(d) + 4) * sizeof(float);
 }
 
 int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
@@ -271,6 +273,7 @@ int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const 
         !aligned16(out))
         return WA_EINVAL;
     const size_t need = wa_tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring);
+    if (need == 0) return WA_EINVAL;
     if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
     const int rc = ensure_device();
     if (rc != WA_OK) return rc;
@@ -283,6 +286,7 @@ int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const 
     a.out = out;
     a.hdr = reinterpret_cast<wa::WsHeader*>(base);
     a.flags = reinterpret_cast<int*>(base + wa::kHeaderBytes);
+    a.part = base + wa::kHeaderBytes + flags_bytes(static_cast<int64_t>(rows) * nodes * hq);
     if (cudaMemsetAsync(base, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
     if (wa::launch_tree(a, s) != cudaSuccess) return WA_ECUDA;
 

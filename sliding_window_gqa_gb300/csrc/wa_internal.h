@@ -72,7 +72,16 @@ struct TreeArgs {
     void* out;
     WsHeader* hdr;
     int* flags;              // [rows * nodes * hq]
+    void* part;              // partial results: float4[units * lanes], then float[units * lanes * d]
 };
+
+// How a tree decode call is cut: nodes a query tile, query tiles a key head, spans a row at most, query rows
+// kept of a tile, units = rows * hkv * mtiles * spans.
+struct TreePlan {
+    int npt, mtiles, spans, lanes;
+    int64_t units;
+};
+TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring);
 
 // Verification of drafted tokens.
 struct VerifyArgs {
@@ -105,6 +114,13 @@ struct CommitArgs {
 
 // A node's parent as every kernel uses it: a value outside [-1, i) counts as -1.
 __host__ __device__ inline int tree_parent(int raw, int i) { return raw >= -1 && raw < i ? raw : -1; }
+
+// A row's last position as every tree kernel uses it: key indices up to a span past it stay in 32 bits.
+constexpr int kTreeMaxPos = INT32_MAX - 4096;
+__host__ __device__ inline int tree_pos(int raw, int win, int ring) {
+    const int most = win == 0 && ring - 1 < kTreeMaxPos ? ring - 1 : kTreeMaxPos;
+    return raw < -1 ? -1 : raw > most ? most : raw;
+}
 
 // Float64 re-run of every flagged (row, head); mode 0 = decode, 1 = prompt, 2 = block-sparse prompt,
 // 3 = tree decode (a row there is a node: row * nodes + node).
@@ -157,6 +173,7 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t s);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
+cudaError_t tree_prepare_device(int dev);
 cudaError_t prompt_prepare_device(int dev);
 cudaError_t decode_prepare_device(int dev);
 // Decode partials on the tensor cores (query-head groups of kTcMinGroup and more); the merge is shared.

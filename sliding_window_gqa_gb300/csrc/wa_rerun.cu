@@ -144,9 +144,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
         if (a.mode == 3) {
             const int seq = row / a.nodes, node = row % a.nodes;
             const int32_t* par = a.parent + static_cast<int64_t>(seq) * a.nodes;
-            int p = a.idx[seq];
-            if (p < -1) p = -1;
-            if (a.win == 0 && p >= a.ring) p = a.ring - 1;
+            const int p = tree_pos(a.idx[seq], a.win, a.ring);
             int depth = 0;
             for (int x = node; (x = tree_parent(par[x], x)) >= 0;) ++depth;
             for (int x = t; x < a.nodes; x += kRerunThreads) anc[x] = 0;
