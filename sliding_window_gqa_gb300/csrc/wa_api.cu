@@ -234,8 +234,7 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
     const int64_t units = static_cast<int64_t>(rows) * nodes * hq;
     const wa::TreePlan pl = wa::tree_plan(rows, nodes, hq, hkv, win, ring);
     if (units > INT32_MAX || pl.units > INT32_MAX / 2) return 0;
-    return wa::kHeaderBytes + flags_bytes(units) +
-           static_cast<size_t>(pl.units) * pl.lanes * (static_cast<size_t>(d) + 4) * sizeof(float);
+    return wa::kHeaderBytes + static_cast<size_t>(pl.units) * pl.lanes * (static_cast<size_t>(d) + 4) * sizeof(float);
 }
 
 int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
@@ -285,19 +284,9 @@ int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const 
     a.rows = rows; a.nodes = nodes; a.hq = hq; a.hkv = hkv; a.d = d; a.win = win; a.ring = ring; a.scale = scale;
     a.out = out;
     a.hdr = reinterpret_cast<wa::WsHeader*>(base);
-    a.flags = reinterpret_cast<int*>(base + wa::kHeaderBytes);
-    a.part = base + wa::kHeaderBytes + flags_bytes(static_cast<int64_t>(rows) * nodes * hq);
+    a.part = base + wa::kHeaderBytes;
     if (cudaMemsetAsync(base, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
     if (wa::launch_tree(a, s) != cudaSuccess) return WA_ECUDA;
-
-    wa::RerunArgs r{};
-    r.mode = 3; r.q = q; r.k = k_ring; r.v = v_ring; r.kt = k_tree; r.vt = v_tree; r.idx = pos; r.parent = parent;
-    r.n = n; r.nodes = nodes;
-    r.rows = rows * nodes; r.hq = hq; r.hkv = hkv; r.d = d; r.win = win; r.ring = ring; r.scale = scale;
-    r.q_row = a.q_row; r.q_tok = a.q_tok; r.kt_row = a.kt_row; r.kt_tok = a.kt_tok; r.vt_row = a.vt_row;
-    r.vt_tok = a.vt_tok; r.o_row = a.o_row; r.o_tok = a.o_tok;
-    r.out = out; r.hdr = a.hdr; r.flags = a.flags;
-    if (wa::launch_rerun(r, s) != cudaSuccess) return WA_ECUDA;
     return WA_OK;
 }
 

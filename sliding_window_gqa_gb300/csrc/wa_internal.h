@@ -71,7 +71,6 @@ struct TreeArgs {
     int64_t q_row, q_tok, kt_row, kt_tok, vt_row, vt_tok, o_row, o_tok;   // elements
     void* out;
     WsHeader* hdr;
-    int* flags;              // [rows * nodes * hq]
     void* part;              // partial results: float4[units * lanes], then float[units * lanes * d]
 };
 
@@ -122,17 +121,9 @@ __host__ __device__ inline int tree_pos(int raw, int win, int ring) {
     return raw < -1 ? -1 : raw > most ? most : raw;
 }
 
-// Float64 re-run of every flagged (row, head); mode 0 = decode, 1 = prompt, 2 = block-sparse prompt,
-// 3 = tree decode (a row there is a node: row * nodes + node).
+// Float64 re-run of every flagged (row, head); mode 0 = decode, 1 = prompt, 2 = block-sparse prompt.
 struct RerunArgs {
     int mode;
-    // mode 3 only
-    const void* kt;
-    const void* vt;
-    const int32_t* parent;
-    const int32_t* n;
-    int nodes;
-    int64_t q_row, kt_row, kt_tok, vt_row, vt_tok, o_row;
     const int32_t* sel;   // mode 2: [rows, hkv, nsel] selected 64-key blocks
     int nsel;
     const void* q;

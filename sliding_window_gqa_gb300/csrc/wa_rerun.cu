@@ -9,10 +9,6 @@
 // in its selected 64-key blocks (TensorFold pull request #1622); a row with none
 // gets 0 / 0 = NaN, as the formula's empty sums give.
 //
-// The tree decode (mode 3) numbers a node's keys lo .. pos (the ring) and then
-// pos + 1 + t for node t of its tree, of which its ancestors and itself count,
-// those less than win positions back.
-//
 // A grid of a few CTAs per SM (at most one per (row, head)) walks the flagged
 // list; with nothing flagged every CTA exits at once.  Per flagged head:
 //   pass 0  fp32 scores (each bf16 x bf16 product is exact in fp32), keys in
@@ -30,6 +26,7 @@
 // trees, so the bits depend only on the row's own inputs.
 #include <cuda_bf16.h>
 
+#include "wa_f64.cuh"
 #include "wa_internal.h"
 #include "wa_ptx.cuh"
 
@@ -37,90 +34,12 @@ namespace wa {
 
 namespace {
 
-constexpr int kRerunThreads = 256;
-
-__device__ __forceinline__ double bf16_bits_to_f64(uint16_t b) {
-    return static_cast<double>(__uint_as_float(static_cast<uint32_t>(b) << 16));
-}
-
-// Round a float64 value to bf16, nearest-even, in one step; an underflow keeps its sign.
-__device__ uint16_t f64_to_bf16_rn(double x) {
-    const uint16_t sign = (__double_as_longlong(x) < 0) ? 0x8000u : 0u;
-    if (isnan(x)) return sign | 0x7FC0u;
-    const double ax = fabs(x);
-    if (isinf(ax)) return sign | 0x7F80u;
-    if (ax < 0x1p-126) {   // subnormal range: quantum 2^-133
-        return sign | static_cast<uint16_t>(rint(ax * 0x1p133));
-    }
-    int e;
-    const double m = frexp(ax, &e);      // ax = m * 2^e, m in [0.5, 1)
-    double sig = rint(ldexp(m, 8));      // 8 significant bits
-    if (sig >= 256.0) {
-        sig = 128.0;
-        e += 1;
-    }
-    const int biased = e - 1 + 127;
-    if (biased >= 255) return sign | 0x7F80u;
-    return sign | static_cast<uint16_t>((biased << 7) | (static_cast<int>(sig) - 128));
-}
-
-__device__ __forceinline__ double block_reduce(double x, bool is_max, double* red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        const double y = __shfl_xor_sync(0xFFFFFFFFu, x, off);
-        x = is_max ? ((isnan(x) || isnan(y)) ? (x + y) : fmax(x, y)) : (x + y);
-    }
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    double r = red[0];
-    for (int w = 1; w < kRerunThreads / 32; ++w) {
-        const double y = red[w];
-        r = is_max ? ((isnan(r) || isnan(y)) ? (r + y) : fmax(r, y)) : (r + y);
-    }
-    __syncthreads();
-    return r;
-}
-
-// d bf16 values of a row as float64 (16-byte loads; the row is 16-byte aligned).
-__device__ __forceinline__ double dot_f64(const double* qd, const uint16_t* kr, int d) {
-    double s = 0.0;
-    for (int e = 0; e < d; e += 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kr + e);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s = s + qd[e + 2 * i] * static_cast<double>(__uint_as_float(w[i] << 16));
-            s = s + qd[e + 2 * i + 1] * static_cast<double>(__uint_as_float(w[i] & 0xFFFF0000u));
-        }
-    }
-    return s;
-}
-
-// The same dot product in fp32: every product of two bf16 values is exact in fp32 unless it
-// overflows or underflows, so a finite float64 score can only come out non-finite here through
-// overflow, and a float64 NaN or infinity always shows as non-finite.
-__device__ __forceinline__ float dot_f32(const float* qf, const uint16_t* kr, int d) {
-    float s = 0.f;
-    for (int e = 0; e < d; e += 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kr + e);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s = fmaf(qf[e + 2 * i], __uint_as_float(w[i] << 16), s);
-            s = fmaf(qf[e + 2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u), s);
-        }
-    }
-    return s;
-}
-
 __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
     __shared__ double qd[256];
     __shared__ float qf[256];
     __shared__ double wb[kRerunThreads];
     __shared__ double red[kRerunThreads / 32];
     __shared__ int sel_row[64];
-    __shared__ unsigned char anc[WA_TREE_MAX_NODES];   // mode 3: node t is visible
     __shared__ unsigned char vis[kRerunThreads];
     const int nflag = *reinterpret_cast<volatile int*>(&a.hdr->nflag);
     const int t = threadIdx.x;
@@ -138,33 +57,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
         const uint16_t *qrow, *kb, *vb;
         int64_t kst, vst;
         uint16_t* orow;
-        // mode 3: keys past `ring_last` are tree nodes
-        int ring_last = 0x7FFFFFFF;
-        const uint16_t *ktb = nullptr, *vtb = nullptr;
-        if (a.mode == 3) {
-            const int seq = row / a.nodes, node = row % a.nodes;
-            const int32_t* par = a.parent + static_cast<int64_t>(seq) * a.nodes;
-            const int p = tree_pos(a.idx[seq], a.win, a.ring);
-            int depth = 0;
-            for (int x = node; (x = tree_parent(par[x], x)) >= 0;) ++depth;
-            for (int x = t; x < a.nodes; x += kRerunThreads) anc[x] = 0;
-            __syncthreads();
-            if (t == 0) {
-                int back = 0;
-                for (int x = node; x >= 0 && (a.win == 0 || back < a.win); x = tree_parent(par[x], x), ++back) anc[x] = 1;
-            }
-            lo = a.win > 0 ? max(0, p + 1 + depth - a.win + 1) : 0;
-            ring_last = p;
-            lo = min(lo, p + 1);
-            last = p + 1 + node;      // an ancestor has a smaller index
-            qrow = q + seq * a.q_row + node * a.q_tok + static_cast<int64_t>(h) * d;
-            kb = k + static_cast<int64_t>(seq) * a.ring * a.hkv * d + static_cast<int64_t>(g) * d;
-            vb = v + static_cast<int64_t>(seq) * a.ring * a.hkv * d + static_cast<int64_t>(g) * d;
-            kst = vst = static_cast<int64_t>(a.hkv) * d;
-            ktb = static_cast<const uint16_t*>(a.kt) + seq * a.kt_row + static_cast<int64_t>(g) * d;
-            vtb = static_cast<const uint16_t*>(a.vt) + seq * a.vt_row + static_cast<int64_t>(g) * d;
-            orow = out + seq * a.o_row + node * a.o_tok + static_cast<int64_t>(h) * d;
-        } else if (a.mode == 0) {
+        if (a.mode == 0) {
             int p = a.idx[row];
             if (p < 0) p = 0;
             if (a.win == 0 && p >= a.ring) p = a.ring - 1;
@@ -196,22 +89,14 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
         if (t < nsel) sel_row[t] = a.sel[(static_cast<int64_t>(row) * a.hkv + g) * a.nsel + t];
         __syncthreads();
         // mode 2: key j counts only if its block j / 64 is selected
-        // mode 3: a tree node counts only if it is the node itself or an ancestor in the window
         auto selected = [&](int j) {
-            if (j > ring_last) return anc[j - ring_last - 1] != 0;
             if (a.mode != 2) return true;
             bool hit = false;
             for (int e = 0; e < nsel; ++e) hit |= sel_row[e] == (j >> 6);
             return hit;
         };
-        auto key = [&](int j) {
-            return j > ring_last ? ktb + (j - ring_last - 1) * a.kt_tok : kb + static_cast<int64_t>(j % a.ring) * kst;
-        };
-        auto val = [&](int j) {
-            return j > ring_last ? vtb + (j - ring_last - 1) * a.vt_tok : vb + static_cast<int64_t>(j % a.ring) * vst;
-        };
         auto score = [&](int j) {
-            const uint16_t* kr = key(j);
+            const uint16_t* kr = kb + static_cast<int64_t>(j % a.ring) * kst;
             return dot_f64(qd, kr, d) * static_cast<double>(a.scale);
         };
 
@@ -221,7 +106,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
             const int j = base + t;
             bool hit = false;
             if (j <= last && selected(j)) {
-                const float sf = dot_f32(qf, key(j), d);
+                const float sf = dot_f32(qf, kb + static_cast<int64_t>(j % a.ring) * kst, d);
                 if (!isfinite(sf)) {
                     const double s = score(j);
                     hit = isnan(s) || (isinf(s) && s > 0.0);
@@ -261,7 +146,7 @@ __global__ void __launch_bounds__(kRerunThreads) rerun_f64_kernel(RerunArgs a) {
                 const int cnt = min(kRerunThreads, last - base + 1);
                 for (int jj = 0; jj < cnt; ++jj)
                     if (vis[jj])
-                        acc = acc + wb[jj] * bf16_bits_to_f64(val(base + jj)[t]);
+                        acc = acc + wb[jj] * bf16_bits_to_f64(vb[static_cast<int64_t>((base + jj) % a.ring) * vst + t]);
             }
             __syncthreads();
         }

@@ -35,6 +35,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "wa_f64.cuh"
 #include "wa_prompt_kernel.cuh"
 
 namespace wa {
@@ -64,16 +65,19 @@ __host__ __device__ inline int tree_spans(int p, int win, int hkv) {
 }
 
 struct TreeParams {
-    CUtensorMap tq;            // [rows][nodes][hq][d], box 64 dims x G heads x 128 / G nodes
-    CUtensorMap tk, tv;        // rings [rows][ring][hkv][d], boxes of 128 keys (K) and 64 keys (V)
-    CUtensorMap tk8, tv8;      // the same in boxes of 8 keys
-    CUtensorMap tkt, tvt;      // nodes' keys and values [rows][nodes][hkv][d], boxes of 128 and 64
+    // five dimensions (64 dims, tokens, blocks of 64 dims, heads, rows) put a whole half-operand, in the
+    // [block][token][64] order that the tensor core reads, into one copy
+    CUtensorMap tq;            // q: 64 x G heads x 128 / G nodes x D / 64 blocks
+    CUtensorMap tk, tv;        // rings: 128 keys x half the blocks (K), 64 keys x all blocks (V)
+    CUtensorMap tk8;           // K ring in pieces of 8 keys x one block
+    CUtensorMap tv8;
+    CUtensorMap tkt, tvt;      // nodes' keys and values, boxes as tk's and tv's
     const uint16_t* k;
     const uint16_t* v;
     const int32_t* pos;
     const int32_t* parent;
     const int32_t* n;
-    float* part_o;             // [unit][lanes][d]
+    float4* part_o;            // [unit][lanes / 32][d / 4][32]: a store of 32 lanes is 512 bytes in a row
     float4* part_ml;           // [unit][lanes]: m (log2 units), l of each column half
     int* status;
     int* next_unit;
@@ -130,6 +134,12 @@ struct TreeCfg {
 // and V(t) in it (two half-loads each).
 __device__ __forceinline__ int op_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int op_v(int t, bool last_of_all) { return last_of_all ? 2 * t + 1 : 2 * t + 2; }
+
+// Its inverse: operand o is K or V of tile t, where K loads have begun for `tiles` tiles.
+__device__ __forceinline__ void load_at(int o, int tiles, int& t, bool& is_v) {
+    is_v = o > 0 && ((o & 1) == 0 || o == 2 * tiles - 1);
+    t = o == 0 ? 0 : is_v ? (o == 2 * tiles - 1 ? tiles - 1 : o / 2 - 1) : (o + 1) / 2;
+}
 
 // A published unit.  nt = 0 marks the end.
 struct TreeUnit {
@@ -202,93 +212,119 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         const uint64_t pol = p.shared_kv ? policy_evict_last() : policy_evict_first();
         const int64_t tok = static_cast<int64_t>(p.hkv) * D;
         int u = 0;                                // half-loads issued
-        uint32_t lastbar[C::NSLOT], lastph[C::NSLOT];   // barrier and phase of the load in each slot
-        // one half-operand: keys [key0, key0 + nkeys) of a ring or node buffer, dims from dim0
-        auto load_half = [&](const TreeUnit& x, int idx, int t, bool is_v, int half) -> bool {
+        int tk = 0;                               // tiles whose K loads have begun
+        // one half-operand: K of 128 keys and half the dims, or V of 64 keys and all dims; slot0: the ring
+        // slot of the tile's first key, -1 for the nodes' own keys
+        auto load_half = [&](const TreeUnit& x, int slot0, int t, bool is_v, int half) -> bool {
             const int s = u % C::NSLOT, use = u / C::NSLOT;
             if (use > 0 && !warp_wait(BAR(C::B_FREE + s), (use - 1) & 1, p.status)) return false;
             const uint32_t full = LOADBAR(is_v ? C::B_VFULL : C::B_KFULL, half, t);
             const uint32_t dst = SLOT(s);
-            const int nblk = is_v ? C::KB : C::KB / 2, dim0 = is_v ? 0 : half * (D / 2);
-            const int nkeys = is_v ? 64 : kTile, blk = nkeys * 128;
-            if (idx >= x.nring) {                 // the nodes' own keys
+            const int blk0 = is_v ? 0 : half * (C::KB / 2), key = is_v ? half * 64 : 0, nkeys = is_v ? 64 : kTile;
+            int sl0 = slot0 + key;
+            if (p.win > 0) {
+                if (sl0 >= p.ring) sl0 -= p.ring;
+                if (sl0 >= p.ring) sl0 %= p.ring;          // rings shorter than a tile
+            }
+            if (slot0 < 0 || p.win == 0 || sl0 + nkeys <= p.ring) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, C::SLOT);
-                    for (int b = 0; b < nblk; ++b)
-                        tma_load_4d(dst + b * blk, is_v ? &p.tvt : &p.tkt, dim0 + b * 64, x.g, is_v ? half * 64 : 0, x.r, full,
-                                    pol);
+                    if (slot0 < 0) tma_load_5d(dst, is_v ? &p.tvt : &p.tkt, 0, key, blk0, x.g, x.r, full, pol);
+                    else tma_load_5d(dst, is_v ? &p.tv : &p.tk, 0, sl0, blk0, x.g, x.r, full, pol);
                 }
             } else {
-                const int key0 = (x.t0 + idx) * kTile + (is_v ? half * 64 : 0);
-                const int slot0 = p.win > 0 ? key0 % p.ring : key0;
-                if (p.win == 0 || slot0 + nkeys <= p.ring) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(full, C::SLOT);
+                // pieces of 8 keys: by TMA, or by the warp where the piece itself wraps
+                const int nblk = is_v ? C::KB : C::KB / 2, blk = nkeys * 128;
+                const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(x.r) * p.ring * tok +
+                                       static_cast<int64_t>(x.g) * D + blk0 * 64;
+                int whole = 0;
+                for (int a = 0; a < nkeys / 8; ++a) {
+                    const int sl = (sl0 + 8 * a) % p.ring;
+                    if (sl + 8 <= p.ring) {
+                        ++whole;
+                        continue;
+                    }
+                    for (int e = lane; e < 64 * nblk; e += 32) {
+                        const int k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
+                        const uint4 val = ld_global_nc_v4(base + (sl + k) % p.ring * tok + b * 64 + cc * 8);
+                        st_shared_v4(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), val.x, val.y, val.z, val.w);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(full, whole * nblk * 1024);
+                __syncwarp();
+                // one lane a piece (nkeys / 8 is at most 16)
+                if (lane < nkeys / 8) {
+                    const int sl = (sl0 + 8 * lane) % p.ring;
+                    if (sl + 8 <= p.ring)
                         for (int b = 0; b < nblk; ++b)
-                            tma_load_4d(dst + b * blk, is_v ? &p.tv : &p.tk, dim0 + b * 64, x.g, slot0, x.r, full, pol);
-                    }
-                } else {
-                    // pieces of 8 keys: by TMA, or by the warp where the piece itself wraps
-                    const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(x.r) * p.ring * tok + static_cast<int64_t>(x.g) * D + dim0;
-                    int whole = 0;
-                    for (int a = 0; a < nkeys / 8; ++a) {
-                        const int sl = (slot0 + 8 * a) % p.ring;
-                        if (sl + 8 <= p.ring) {
-                            ++whole;
-                            continue;
-                        }
-                        for (int e = lane; e < 64 * nblk; e += 32) {
-                            const int k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
-                            const uint4 val = ld_global_nc_v4(base + (sl + k) % p.ring * tok + b * 64 + cc * 8);
-                            st_shared_v4(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), val.x, val.y, val.z, val.w);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(full, whole * nblk * 1024);
-                        for (int a = 0; a < nkeys / 8; ++a) {
-                            const int sl = (slot0 + 8 * a) % p.ring;
-                            if (sl + 8 > p.ring) continue;
-                            for (int b = 0; b < nblk; ++b)
-                                tma_load_4d(dst + b * blk + a * 1024, is_v ? &p.tv8 : &p.tk8, dim0 + b * 64, x.g, sl, x.r, full,
-                                            pol);
-                        }
-                    }
+                            tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, sl, blk0 + b, x.g, x.r, full, pol);
                 }
             }
             __syncwarp();
-            lastbar[s] = full;
-            lastph[s] = LOADPH(t);
             ++u;
             return true;
         };
+        auto load_k = [&](const TreeUnit& x, int slot0, int t) -> bool {
+            tk = t + 1;
+            return load_half(x, slot0, t, false, 0) && load_half(x, slot0, t, false, 1);
+        };
+        // the ring slot of a unit's first tile, and of the tile after one
+        auto first_slot = [&](const TreeUnit& x) { return x.nring == 0 ? -1 : p.win > 0 ? x.t0 * kTile % p.ring : x.t0 * kTile; };
+        auto next_slot = [&](const TreeUnit& x, int idx, int slot0) {
+            if (idx + 1 >= x.nring) return -1;
+            int sl = slot0 + kTile;
+            if (p.win > 0 && sl >= p.ring) {
+                sl -= p.ring;
+                if (sl >= p.ring) sl %= p.ring;
+            }
+            return sl;
+        };
         TreeUnit cur, nxt;
-        int U = 0, t = 0, idx = 0;
+        int U = 0, t = 0, idx = 0, sc = -1;
         bool ok = take_unit(U++, cur, true);
         bool more = ok && cur.nt > 0;
-        if (more) ok = load_half(cur, 0, 0, false, 0) && load_half(cur, 0, 0, false, 1);
+        if (more) {
+            sc = first_slot(cur);
+            ok = load_k(cur, sc, 0);
+        }
         while (ok && more) {
-            // the tile after (cur, idx)
+            // the tile after (cur, idx): its K goes first
             const bool same = idx + 1 < cur.nt;
-            if (!same) {
+            int sn = -1;
+            if (same) {
+                sn = next_slot(cur, idx, sc);
+                ok = load_k(cur, sn, t + 1);
+            } else {
                 if (!(ok = take_unit(U++, nxt, true))) break;
                 more = nxt.nt > 0;
+                if (more) {
+                    sn = first_slot(nxt);
+                    ok = load_k(nxt, sn, t + 1);
+                }
             }
-            if (same) ok = load_half(cur, idx + 1, t + 1, false, 0) && load_half(cur, idx + 1, t + 1, false, 1);
-            else if (more) ok = load_half(nxt, 0, t + 1, false, 0) && load_half(nxt, 0, t + 1, false, 1);
-            ok = ok && load_half(cur, idx, t, true, 0) && load_half(cur, idx, t, true, 1);
+            if (!ok) break;
+            ok = load_half(cur, sc, t, true, 0) && load_half(cur, sc, t, true, 1);
             if (same) {
                 ++idx;
             } else {
                 cur = nxt;
                 idx = 0;
             }
+            sc = sn;
             ++t;
         }
-        // the copies in flight land before the block exits, whichever role stopped early
-        if (lane == 0)
-            for (int i = max(0, u - C::NSLOT); i < u; ++i) mbar_wait(lastbar[i % C::NSLOT], lastph[i % C::NSLOT], p.status);
+        // the copies in flight land before the block exits, whichever role stopped early (after a whole
+        // run every one was consumed, and the waits return at once); u half-loads were issued
+        if (lane == 0) {
+            for (int i = max(0, u - C::NSLOT); i < u; ++i) {
+                int tt, half = i & 1;
+                bool v;
+                load_at(i >> 1, tk, tt, v);
+                mbar_wait(LOADBAR(v ? C::B_VFULL : C::B_KFULL, half, tt), LOADPH(tt), p.status);
+            }
+        }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (one thread)
         if (lane == 0) {
@@ -403,18 +439,17 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         }
     } else if (warp == 3) {
         // ------------------------------------------------ units; Q
-        if (lane == 0) prefetch_tensormap(&p.tq);
         int k_cur = blockIdx.x, k_ans = 0, pub = 0, loaded = 0;
         bool asked = false, ended = false, ok = true;
-        // the next unit with any work (nt = 0: none left); its number is asked for one unit ahead
+        int par[4];               // the unit's parents, four a lane
+        // the next unit with any work (nt = 0: none left).  Its number was asked for one unit ahead, and
+        // everything a unit needs is loaded at once: one trip to memory a unit.
         auto next_unit = [&](TreeUnit& x) {
             for (;;) {
                 if (asked) k_cur = __shfl_sync(0xFFFFFFFFu, k_ans, 0) + static_cast<int>(gridDim.x);
                 x.nt = 0;
                 x.nring = 0;
                 if (k_cur >= p.units) return;
-                if (lane == 0) k_ans = atomicAdd(p.next_unit, 1);
-                asked = true;
                 int k = k_cur;
                 const int mt = k % p.mtiles;
                 k /= p.mtiles;
@@ -422,20 +457,23 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 k /= p.spans;
                 x.g = k % p.hkv;
                 x.r = k / p.hkv;
+                const int raw_p = __ldg(p.pos + x.r), raw_n = p.n ? __ldg(p.n + x.r) : p.nodes;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    par[e] = lane + 32 * e < p.nodes ? __ldg(p.parent + static_cast<int64_t>(x.r) * p.nodes + lane + 32 * e) : -1;
+                if (lane == 0) k_ans = atomicAdd(p.next_unit, 1);
+                asked = true;
                 x.node0 = mt * p.npt;
-                const int raw_p = p.pos[x.r], raw_n = p.n ? p.n[x.r] : p.nodes;
                 x.n = min(max(raw_n, 0), p.nodes);
                 x.p = tree_pos(raw_p, p.win, p.ring);
-                if (x.g == 0 && mt == 0 && x.span == 0) {     // reported once a row
-                    int bad = 0;
-                    if (raw_n != x.n) bad |= WA_STATUS_BAD_TREE;
-                    if (raw_p != x.p) bad |= WA_STATUS_BAD_POS;
-                    for (int i = lane; i < x.n; i += 32) {
-                        const int a = p.parent[static_cast<int64_t>(x.r) * p.nodes + i];
-                        if (tree_parent(a, i) != a) bad |= WA_STATUS_BAD_TREE;
-                    }
-                    if (bad) atomicOr(p.status, bad);
+                int bad = (raw_n != x.n ? WA_STATUS_BAD_TREE : 0) | (raw_p != x.p ? WA_STATUS_BAD_POS : 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = lane + 32 * e, a = tree_parent(par[e], i);
+                    if (i < x.n && a != par[e]) bad |= WA_STATUS_BAD_TREE;
+                    par[e] = a;
                 }
+                if (bad && x.g == 0 && mt == 0 && x.span == 0) atomicOr(p.status, bad);   // reported once a row
                 if (x.node0 >= x.n) continue;
                 x.lo = tree_first(x.p, p.win);
                 if (x.lo > x.p) {                             // no key of the ring: the tree alone
@@ -454,8 +492,8 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 return;
             }
         };
-        TreeUnit ahead[kAhead + 1];
         auto publish_next = [&](TreeUnit& x) -> bool {
+            x.nt = 0;
             if (ended) return true;
             next_unit(x);
             ended = x.nt <= 0;
@@ -463,9 +501,9 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 return false;
             volatile int* e = unit_ints(pub);
             if (!ended) {
-                volatile uint8_t* par = reinterpret_cast<volatile uint8_t*>(e + 8);
-                for (int i = lane; i < p.nodes; i += 32)
-                    par[i] = static_cast<uint8_t>(tree_parent(p.parent[static_cast<int64_t>(x.r) * p.nodes + i], i));
+                volatile uint8_t* out = reinterpret_cast<volatile uint8_t*>(e + 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[lane + 32 * i] = static_cast<uint8_t>(par[i]);
             }
             if (lane == 0) {
                 e[0] = x.r; e[1] = x.g | (x.node0 << 16); e[2] = x.span; e[3] = x.t0;
@@ -476,27 +514,33 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             ++pub;
             return true;
         };
-        for (int i = 0; ok && i <= kAhead; ++i) {
-            ahead[i].nt = 0;
-            ok = publish_next(ahead[i]);
-        }
-        for (int U = 0; ok; ++U) {
-            const TreeUnit x = ahead[0];
-            if (x.nt <= 0) break;
-            // Q of unit U, once the last S of unit U - 1 has read the buffer
-            if (U > 0 && !(ok = warp_wait(BAR(C::B_QFREE), (U - 1) & 1, p.status))) break;
+        auto load_q = [&](const TreeUnit& x) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(BAR(C::B_QFULL), C::KB * p.gsz * p.npt * 128);
-                for (int b = 0; b < C::KB; ++b)
-                    tma_load_4d(sbase + C::OFF_Q + b * C::Q_BLOCK, &p.tq, b * 64, x.g * p.gsz, x.node0, x.r, BAR(C::B_QFULL),
-                                policy_evict_last());
+                if (p.gsz * p.npt == 128) {
+                    tma_load_5d(sbase + C::OFF_Q, &p.tq, 0, x.g * p.gsz, x.node0, 0, x.r, BAR(C::B_QFULL), policy_evict_last());
+                } else {        // a tile of fewer than 128 rows: block by block
+                    for (int b = 0; b < C::KB; ++b)
+                        tma_load_5d(sbase + C::OFF_Q + b * C::Q_BLOCK, &p.tq, 0, x.g * p.gsz, x.node0, b, x.r, BAR(C::B_QFULL),
+                                    policy_evict_last());
+                }
             }
-            loaded = U + 1;
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) ahead[i] = ahead[i + 1];
-            ahead[kAhead].nt = 0;
-            ok = publish_next(ahead[kAhead]);
+            ++loaded;
+        };
+        TreeUnit u0, u1, u2;      // the unit whose Q is next, and kAhead = 2 more
+        static_assert(kAhead == 2, "units held here");
+        ok = publish_next(u0);
+        if (ok && u0.nt > 0) load_q(u0);
+        u1.nt = u2.nt = 0;
+        ok = ok && publish_next(u1) && publish_next(u2);
+        for (int U = 1; ok; ++U) {
+            u0 = u1;
+            u1 = u2;
+            if (u0.nt <= 0 || !(ok = publish_next(u2))) break;
+            // Q of unit U, once the last S of unit U - 1 has read the buffer
+            if (!(ok = warp_wait(BAR(C::B_QFREE), (U - 1) & 1, p.status))) break;
+            load_q(u0);
         }
         if (lane == 0 && loaded > 0) mbar_wait(BAR(C::B_QFULL), (loaded - 1) & 1, p.status);
     } else {
@@ -563,58 +607,49 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                     w1 = static_cast<uint32_t>(bits >> 32);
                 }
                 const bool masked = !__all_sync(0xFFFFFFFFu, (w0 & w1) == 0xFFFFFFFFu);
-                float mx8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
-                if (masked) {
+                if (masked) {   // a masked score is -inf, whatever it was: weight 0
 #pragma unroll
                     for (int k = 0; k < 64; ++k)
-                        mx8[k & 7] = fmaxf(mx8[k & 7], ((k < 32 ? w0 : w1) >> (k & 31)) & 1u ? sv[k] : -INFINITY);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2) mx8[(k >> 1) & 7] = max3(mx8[(k >> 1) & 7], sv[k], sv[k + 1]);
+                        if (!(((k < 32 ? w0 : w1) >> (k & 31)) & 1u)) sv[k] = -INFINITY;
                 }
-                const float mh = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                float mx8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = max3(sv[e], sv[e + 8], sv[e + 16]);
+#pragma unroll
+                for (int k = 24; k < 56; k += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx8[e] = max3(mx8[e], sv[k + e], sv[k + e + 8]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(mx8[e], sv[56 + e]);
+                const float mh = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
                 float* xs = xbuf + b * 256;
                 xs[wg * 128 + r] = mh;
                 __syncwarp();   // the warp's stores precede lane 0's (cumulative) release
                 if (lane == 0) mbar_arrive(BAR(C::B_XCHG + b));
-                float ls8[8];
-                auto exponents = [&](float m_sub) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ls8[e] = 0.f;
-                    if (masked) {   // a masked column is 0 whatever its score
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) {
-                            const float pk = ((k < 32 ? w0 : w1) >> (k & 31)) & 1u ? ex2(fmaf(sv[k], c, -m_sub)) : 0.f;
-                            sv[k] = pk;
-                            ls8[2 * ((k >> 1) & 3) + (k & 1)] += pk;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 64; k += 2) {
-                            float x0, x1;
-                            fma_x2(x0, x1, sv[k], sv[k + 1], c, c, -m_sub, -m_sub);
-                            sv[k] = ex2(x0);
-                            sv[k + 1] = ex2(x1);
-                            add_x2(ls8[2 * ((k >> 1) & 3)], ls8[2 * ((k >> 1) & 3) + 1], sv[k], sv[k + 1]);
-                        }
-                    }
-                };
-                // The running max usually stays (lazy rule), so the exponentials start with it while
-                // the other half's maximum is on its way, and are redone from S if it moved.
-                const bool spec = __all_sync(0xFFFFFFFFu, !live || (m_run != -INFINITY && mh * c <= m_run + kLazy));
-                if (spec) exponents(m_run);
                 if (!(ok = warp_wait(BAR(C::B_XCHG + b), ph, p.status))) break;
                 const float mt = fmaxf(xs[r], xs[128 + r]) * c;
+                // lazy rule: keep the running max unless the tile's exceeds it by more than kLazy
                 const float m_new = (mt > m_run + kLazy) ? mt : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : ex2(m_run - m_new);
                 const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
-                if (!spec || __any_sync(0xFFFFFFFFu, live && m_new != m_run)) {
-                    if (spec) load_s<64>(t_s, sv);
-                    exponents(m_sub);
+                float ls8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ls8[e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    float x0, x1;
+                    fma_x2(x0, x1, sv[k], sv[k + 1], c, c, -m_sub, -m_sub);
+                    sv[k] = ex2(x0);
+                    sv[k + 1] = ex2(x1);
                 }
+                if (c == 0.f && masked) {   // scale 0: -inf * 0 is no weight
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (!(((k < 32 ? w0 : w1) >> (k & 31)) & 1u)) sv[k] = 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 64; k += 2)
+                    add_x2(ls8[2 * ((k >> 1) & 3)], ls8[2 * ((k >> 1) & 3) + 1], sv[k], sv[k + 1]);
                 // O's rescale, once the previous P V is done; a unit's first P V starts O afresh
                 if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f)) {
                     if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status)))
@@ -664,24 +699,19 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status))) break;
             tc_fence_after();
             const int64_t unit = ((static_cast<int64_t>(x.r) * p.hkv + x.g) * p.mtiles + x.node0 / p.npt) * p.spans + x.span;
-            const int64_t rec = unit * p.lanes + r;
+            float4* po = p.part_o + ((unit * (p.lanes >> 5) + (warp & 3)) * (D / 4) + wg * (D / 8)) * 32 + lane;
 #pragma unroll 1
             for (int cc = 0; cc < D / 64; ++cc) {
                 uint32_t o[32];
                 tmem_ld32_wait(tbase + lane_addr + wg * (D / 2) + cc * 32, o);
-                if (live) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + rec * D + wg * (D / 2) + cc * 32);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                }
+                for (int e = 0; e < 8; ++e)
+                    po[(cc * 8 + e) * 32] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
             }
-            if (live) {
-                float* ml = reinterpret_cast<float*>(p.part_ml + rec);
-                if (wg == 0) *reinterpret_cast<float2*>(ml) = make_float2(m_run, l_run);
-                else ml[2] = l_run;
-            }
+            float* ml = reinterpret_cast<float*>(p.part_ml + unit * p.lanes + r);
+            if (wg == 0) *reinterpret_cast<float2*>(ml) = make_float2(m_run, l_run);
+            else ml[2] = l_run;
         }
     }
 
@@ -691,66 +721,184 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
     if (warp == 1) tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
-// o = sum_s a_s O_s / sum_s a_s l_s over a row's spans in order, a_s = 2^(m_s - M); one warp a (node, query head).
-template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part_o, const float4* __restrict__ part_ml,
-                                                         const TreeArgs a, int npt, int mtiles, int spans, int lanes) {
-    constexpr int V4 = D / 128;      // float4 a lane
-    const int lane = threadIdx.x & 31;
-    const int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (unit >= a.rows * a.nodes * a.hq) return;
-    const int h = unit % a.hq, node = unit / a.hq % a.nodes, r = unit / a.hq / a.nodes;
-    if (node >= min(a.n ? a.n[r] : a.nodes, a.nodes)) return;
+// The float64 value of 64 of an output's dims (from col0), by the whole block: a node's keys are numbered
+// lo .. p (the ring) and then p + 1 + t for node t of its tree, of which those in `anc` count.
+struct TreeRerun {
+    double qd[256];
+    float qf[256];
+    double wb[kRerunThreads], red[kRerunThreads / 32];
+    unsigned char anc[WA_TREE_MAX_NODES], use[kRerunThreads];
+};
+
+__device__ void tree_rerun(const TreeArgs& a, TreeRerun& sm, int r, int node, int h, int col0) {
+    const int t = threadIdx.x, d = a.d, g = h / (a.hq / a.hkv);
+    const int32_t* par = a.parent + static_cast<int64_t>(r) * a.nodes;
     const int p = tree_pos(a.pos[r], a.win, a.ring);
-    const int G = a.hq / a.hkv, g = h / G;
-    const int count = tree_spans(p, a.win, a.hkv);
-    const int64_t rec0 = ((static_cast<int64_t>(r) * a.hkv + g) * mtiles + node / npt) * spans * lanes + (node % npt) * G + h % G;
-    float M = -INFINITY;
-    for (int s = 0; s < count; ++s) M = fmaxf(M, part_ml[rec0 + static_cast<int64_t>(s) * lanes].x);
-    float4 num[V4];
-#pragma unroll
-    for (int e = 0; e < V4; ++e) num[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-    for (int s = 0; s < count; ++s) {
-        const int64_t rec = rec0 + static_cast<int64_t>(s) * lanes;
-        const float4 ml = part_ml[rec];
-        const float w = exp2f(ml.x - M);
-        den = fmaf(w, ml.y + ml.z, den);
-        const float4* o = reinterpret_cast<const float4*>(part_o + rec * D);
-#pragma unroll
-        for (int e = 0; e < V4; ++e) {
-            const float4 x = o[e * 32 + lane];
-            num[e].x = fmaf(w, x.x, num[e].x);
-            num[e].y = fmaf(w, x.y, num[e].y);
-            num[e].z = fmaf(w, x.z, num[e].z);
-            num[e].w = fmaf(w, x.w, num[e].w);
+    int depth = 0;
+    for (int x = node; (x = tree_parent(par[x], x)) >= 0;) ++depth;
+    for (int x = t; x < a.nodes; x += kRerunThreads) sm.anc[x] = 0;
+    __syncthreads();
+    if (t == 0)
+        for (int x = node, back = 0; x >= 0 && (a.win == 0 || back < a.win); x = tree_parent(par[x], x), ++back) sm.anc[x] = 1;
+    const int lo = min(a.win > 0 ? max(0, p + 1 + depth - a.win + 1) : 0, p + 1);
+    const int last = p + 1 + node;           // an ancestor has a smaller index
+    const uint16_t* qrow = static_cast<const uint16_t*>(a.q) + r * a.q_row + node * a.q_tok + static_cast<int64_t>(h) * d;
+    const int64_t kst = static_cast<int64_t>(a.hkv) * d, base = r * a.ring * kst + static_cast<int64_t>(g) * d;
+    const uint16_t* kb = static_cast<const uint16_t*>(a.k) + base;
+    const uint16_t* vb = static_cast<const uint16_t*>(a.v) + base;
+    const uint16_t* ktb = static_cast<const uint16_t*>(a.kt) + r * a.kt_row + static_cast<int64_t>(g) * d;
+    const uint16_t* vtb = static_cast<const uint16_t*>(a.vt) + r * a.vt_row + static_cast<int64_t>(g) * d;
+    uint16_t* orow = static_cast<uint16_t*>(a.out) + r * a.o_row + node * a.o_tok + static_cast<int64_t>(h) * d + col0;
+    if (t < d) {
+        const float x = __uint_as_float(static_cast<uint32_t>(qrow[t]) << 16);
+        sm.qf[t] = x * a.scale;   // only the class of the fp32 score matters
+        sm.qd[t] = static_cast<double>(x);
+    }
+    __syncthreads();
+    auto visible = [&](int j) { return j <= last && (j <= p || sm.anc[j - p - 1] != 0); };
+    auto key = [&](int j) { return j > p ? ktb + (j - p - 1) * a.kt_tok : kb + static_cast<int64_t>(j % a.ring) * kst; };
+    auto val = [&](int j) { return j > p ? vtb + (j - p - 1) * a.vt_tok : vb + static_cast<int64_t>(j % a.ring) * kst; };
+    auto score = [&](int j) { return dot_f64(sm.qd, key(j), d) * static_cast<double>(a.scale); };
+    // a float64 score that is NaN or +inf makes the output NaN: settled without the passes below
+    for (int b = lo; b <= last; b += kRerunThreads) {
+        const int j = b + t;
+        bool hit = false;
+        if (visible(j) && !isfinite(dot_f32(sm.qf, key(j), d))) {
+            const double s = score(j);
+            hit = isnan(s) || (isinf(s) && s > 0.0);
+        }
+        if (__syncthreads_or(hit)) {
+            if (t < 64) orow[t] = 0x7FC0u;
+            return;
         }
     }
-    uint2* orow = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * a.o_row + node * a.o_tok + static_cast<int64_t>(h) * D);
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < V4; ++e) {
-        const float x = __fdiv_rn(num[e].x, den), y = __fdiv_rn(num[e].y, den);
-        const float z = __fdiv_rn(num[e].z, den), w = __fdiv_rn(num[e].w, den);
-        bad |= !(isfinite(x) && isfinite(y) && isfinite(z) && isfinite(w));
-        orow[e * 32 + lane] = make_uint2(pack_bf16(x, y), pack_bf16(z, w));
+    double mloc = -INFINITY;
+    for (int j = lo + t; j <= last; j += kRerunThreads) {
+        if (!visible(j)) continue;
+        const double s = score(j);
+        mloc = (isnan(s) || isnan(mloc)) ? (s + mloc) : fmax(mloc, s);
     }
-    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) a.flags[atomicAdd(&a.hdr->nflag, 1)] = unit;
+    const double M = block_reduce(mloc, true, sm.red);
+    double lloc = 0.0, acc = 0.0;
+    for (int b = lo; b <= last; b += kRerunThreads) {
+        const int j = b + t;
+        const bool use = visible(j);
+        double w = 0.0;
+        if (use) {
+            w = exp(score(j) - M);
+            lloc += w;
+        }
+        sm.wb[t] = w;
+        sm.use[t] = use ? 1 : 0;
+        __syncthreads();
+        if (t < 64) {
+            const int cnt = min(kRerunThreads, last - b + 1);
+            for (int jj = 0; jj < cnt; ++jj)
+                if (sm.use[jj]) acc = acc + sm.wb[jj] * bf16_bits_to_f64(val(b + jj)[col0 + t]);
+        }
+        __syncthreads();
+    }
+    const double l = block_reduce(lloc, false, sm.red);
+    if (t < 64) orow[t] = f64_to_bf16_rn(acc / l);
 }
 
-// A [rows][toks][heads][d] bf16 tensor in boxes of 64 dims x box_heads x box_toks, 128-byte swizzle.
-bool encode_4d(CUtensorMap* m, const void* base, int d, int heads, int toks, int rows, int64_t tok, int64_t row, int box_heads,
-               int box_toks) {
+// o = sum_s a_s O_s / sum_s a_s l_s over a row's spans in order, a_s = 2^(m_s - M).  A block takes 32 query
+// rows (lanes) and 64 dims (8 a warp) of a tile, reads the partial results in the order they were stored
+// (512 bytes a warp and load, four spans in flight), and turns them round in shared memory for the output.
+// A row with a value that is not finite is computed again in float64.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_ml,
+                                                         const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans, int lanes) {
+    __shared__ __align__(16) uint8_t tile[32 * 144];
+    __shared__ int bad[32];
+    __shared__ TreeRerun again;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int quarters = lanes >> 5;
+    int k = blockIdx.x;
+    const int qd = k % quarters;
+    k /= quarters;
+    const int64_t unit0 = static_cast<int64_t>(k) * spans;
+    const int mt = k % mtiles;
+    k /= mtiles;
+    const int g = k % a.hkv, r = k / a.hkv;
+    const int G = a.hq / a.hkv, node0 = mt * npt;
+    const int n = min(a.n ? __ldg(a.n + r) : a.nodes, a.nodes);
+    const int count = tree_spans(tree_pos(__ldg(a.pos + r), a.win, a.ring), a.win, a.hkv);
+    const int first = qd * 32 / G;                        // the block's first node
+    if (first >= npt || node0 + first >= n) return;
+    if (t < 32) bad[t] = 0;
+    __syncthreads();
+    const float4* ml = part_ml + unit0 * lanes + qd * 32 + lane;
+    const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + blockIdx.y * 16 + warp * 2) * 32 + lane;
+    const int64_t ostep = static_cast<int64_t>(quarters) * (D / 4) * 32;
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int s = 0; s < count; ++s) M = fmaxf(M, ml[static_cast<int64_t>(s) * lanes].x);
+    float num[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) num[e] = 0.f;
+    float den = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < count; ++s) {
+        const float4 x = ml[static_cast<int64_t>(s) * lanes];
+        const float4 o0 = po[s * ostep], o1 = po[s * ostep + 32];
+        const float w = exp2f(x.x - M);
+        den = fmaf(w, x.y + x.z, den);
+        num[0] = fmaf(w, o0.x, num[0]);
+        num[1] = fmaf(w, o0.y, num[1]);
+        num[2] = fmaf(w, o0.z, num[2]);
+        num[3] = fmaf(w, o0.w, num[3]);
+        num[4] = fmaf(w, o1.x, num[4]);
+        num[5] = fmaf(w, o1.y, num[5]);
+        num[6] = fmaf(w, o1.z, num[6]);
+        num[7] = fmaf(w, o1.w, num[7]);
+    }
+    const int row = qd * 32 + lane;
+    const bool live = row / G < npt && node0 + row / G < n;
+    bool nonfinite = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        num[e] = __fdiv_rn(num[e], den);
+        nonfinite |= !isfinite(num[e]);
+    }
+    if (live && nonfinite) bad[lane] = 1;
+    *reinterpret_cast<uint4*>(tile + lane * 144 + warp * 16) =
+        make_uint4(pack_bf16(num[0], num[1]), pack_bf16(num[2], num[3]), pack_bf16(num[4], num[5]), pack_bf16(num[6], num[7]));
+    const int any = __syncthreads_or(live && nonfinite);
+    {   // eight threads a row
+        const int m = qd * 32 + t / 8, rn = m / G;
+        if (rn < npt && node0 + rn < n && !bad[t / 8]) {
+            uint16_t* orow = static_cast<uint16_t*>(a.out) + r * a.o_row + (node0 + rn) * a.o_tok +
+                             static_cast<int64_t>(g * G + m % G) * D + blockIdx.y * 64;
+            reinterpret_cast<uint4*>(orow)[t % 8] = *reinterpret_cast<const uint4*>(tile + t / 8 * 144 + t % 8 * 16);
+        }
+    }
+    if (!any) return;
+    for (int i = 0; i < 32; ++i) {
+        if (!bad[i]) continue;
+        const int m = qd * 32 + i;
+        tree_rerun(a, again, r, node0 + m / G, g * G + m % G, blockIdx.y * 64);
+        __syncthreads();
+    }
+}
+
+// A [rows][toks][heads][d] bf16 tensor as (64 dims, tokens or heads x tokens, blocks of 64 dims, ...), 128-byte
+// swizzle.  `heads_first`: q, whose boxes take heads and tokens (64, heads, tokens, blocks, rows); otherwise
+// k and v (64, tokens, blocks, heads, rows).
+bool encode_5d(CUtensorMap* m, const void* base, int d, int heads, int toks, int rows, int64_t tok, int64_t row, bool heads_first,
+               int box1, int box2, int box3) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(toks),
-                          static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(tok) * 2, static_cast<cuuint64_t>(row) * 2};
-    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_toks), 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t nd = static_cast<cuuint64_t>(d) / 64, nh = heads, nt = toks, nr = rows;
+    const cuuint64_t sh = static_cast<cuuint64_t>(d) * 2, st = static_cast<cuuint64_t>(tok) * 2, sb = 128,
+                     sr = static_cast<cuuint64_t>(row) * 2;
+    cuuint64_t dims_q[5] = {64, nh, nt, nd, nr}, strides_q[4] = {sh, st, sb, sr};
+    cuuint64_t dims_k[5] = {64, nt, nd, nh, nr}, strides_k[4] = {st, sb, sh, sr};
+    cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), static_cast<cuuint32_t>(box3), 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), heads_first ? dims_q : dims_k,
+               heads_first ? strides_q : strides_k, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -760,19 +908,21 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     TreeParams t{};
     const int G = a.hq / a.hkv;
     const int64_t ktok = static_cast<int64_t>(a.hkv) * D, krow = ktok * a.ring;
-    if (!encode_4d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, G, pl.npt) ||
-        !encode_4d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, 1, kTile) ||
-        !encode_4d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, 1, kTile / 2) ||
-        !encode_4d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, 1, 8) ||
-        !encode_4d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, 1, 8) ||
-        !encode_4d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, 1, kTile) ||
-        !encode_4d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, 1, kTile / 2))
+    constexpr int KB = C::KB;
+    const bool whole = G * pl.npt == 128;    // a tile's rows fill a block of the Q buffer: one copy for all blocks
+    if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, pl.npt, whole ? KB : 1) ||
+        !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, KB / 2, 1) ||
+        !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile / 2, KB, 1) ||
+        !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
+        !encode_5d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
+        !encode_5d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, false, kTile, KB / 2, 1) ||
+        !encode_5d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, false, kTile / 2, KB, 1))
         return cudaErrorInvalidValue;
     t.k = static_cast<const uint16_t*>(a.k);
     t.v = static_cast<const uint16_t*>(a.v);
     t.pos = a.pos; t.parent = a.parent; t.n = a.n;
     t.part_ml = static_cast<float4*>(a.part);
-    t.part_o = reinterpret_cast<float*>(t.part_ml + pl.units * pl.lanes);
+    t.part_o = t.part_ml + pl.units * pl.lanes;
     t.status = &a.hdr->status;
     t.next_unit = &a.hdr->next_unit;
     t.rows = a.rows; t.nodes = a.nodes; t.hq = a.hq; t.hkv = a.hkv; t.gsz = G; t.npt = pl.npt; t.mtiles = pl.mtiles;
@@ -787,8 +937,8 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     tree_kernel<D><<<grid, 384, C::SMEM, s>>>(t);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int outs = a.rows * a.nodes * a.hq;
-    tree_merge_kernel<D><<<(outs + 7) / 8, 256, 0, s>>>(t.part_o, t.part_ml, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
+    const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
+    tree_merge_kernel<D><<<mgrid, 256, 0, s>>>(t.part_o, t.part_ml, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
     return cudaGetLastError();
 }
 
@@ -799,7 +949,7 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
     const int G = hq / hkv;
     pl.npt = 128 / G;
     pl.mtiles = (nodes + pl.npt - 1) / pl.npt;
-    pl.lanes = (nodes < pl.npt ? nodes : pl.npt) * G;
+    pl.lanes = ((nodes < pl.npt ? nodes : pl.npt) * G + 31) / 32 * 32;
     pl.spans = 1;
     if (win > 0) {
         // win - 1 keys from any position touch at most this many spans
