@@ -71,7 +71,7 @@ struct TreeArgs {
     int64_t q_row, q_tok, kt_row, kt_tok, vt_row, vt_tok, o_row, o_tok;   // elements
     void* out;
     WsHeader* hdr;
-    void* part;              // partial results: float4[units * lanes], then float[units * lanes * d]
+    void* part;              // partial results: l float4[units * lanes], O float[units * lanes * d], m float[units * lanes]
 };
 
 // How a tree decode call is cut: nodes a query tile, query tiles a key head, spans a row at most, query rows

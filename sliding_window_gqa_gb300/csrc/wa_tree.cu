@@ -14,22 +14,24 @@
 // joins a row's spans in order.  Nothing in a unit depends on the other rows, so
 // neither do the bits.
 //
-// tree_kernel<D>: a persistent grid, one CTA an SM, 384 threads, that streams the
+// tree_kernel<D>: a persistent grid, one CTA an SM, 640 threads, that streams the
 // keys of its units without a break between units:
-//   warp 0      TMA producer: K and V in half-tiles through a ring of slots, in the
-//               order the tensor core reads them (K0, K1, V0, K2, V1, ...), on across
-//               unit ends.  A tile that wraps around the end of a ring is loaded in
-//               8-row boxes; the one 8-row piece that holds the wrap itself is
-//               copied by the warp.
+//   warp 0      TMA producer: K and V through a ring of 32 KiB slots (head dim 256: half a
+//               tile's K or V each), in the order the tensor core reads them (K0, K1, V0,
+//               K2, V1, ...), on across unit ends.  A tile that wraps around the end of a
+//               ring is loaded in 8-row boxes; the one 8-row piece that holds the wrap
+//               itself is copied by the warp.
 //   warp 1      allocates tensor memory; lane 0 issues S(t + 1) = Q K^T and
 //               O += P(t) V (two bf16 parts of P), commits free the slots.
 //   warp 2      zeroes V rows that no node of the row sees (stale ring slots, nodes
 //               past n), so that they never meet a zero probability as 0 * inf.
 //   warp 3      takes units from a counter, publishes them through a ring of unit
 //               slots, and loads each unit's Q once the previous unit's last S is done.
-//   warps 4..11 softmax, one query row a thread in two column halves: mask,
-//               exponentials, P over S in tensor memory, a lazy rescale of O, and
-//               the unit's partial result.
+//   warps 4..19 softmax, one query row a thread in four column quarters: mask,
+//               exponentials, P over S in tensor memory, a lazy rescale of O, and the
+//               unit's partial result.  Four warps share a row group, so that the chain
+//               S -> P of a tile is 32 columns long (with two warps of 64 columns it took
+//               about 3,000 cycles at 16 query rows, more than the tile's reads).
 // Every wait is bounded (a status bit after kWaitLimitNs) and warp-uniform where a
 // warp waits.
 #include <cuda_bf16.h>
@@ -43,8 +45,13 @@ namespace wa {
 namespace {
 
 constexpr int kTile = 128;         // keys a tile
+constexpr int kTreeThreads = 640;
 constexpr int kUnits = 4;          // unit slots
 constexpr int kAhead = 2;          // units published beyond the one whose Q is loaded next
+
+// log2 units the running max may trail before O is rescaled.  P, l and O are floating point, so a stale
+// maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
+constexpr float kTreeLazy = 32.0f;
 
 // Keys a span: enough spans that hkv key heads of one row occupy the card, in powers of two.
 __host__ __device__ inline int tree_span(int64_t keys, int hkv) {
@@ -68,7 +75,7 @@ struct TreeParams {
     // five dimensions (64 dims, tokens, blocks of 64 dims, heads, rows) put a whole half-operand, in the
     // [block][token][64] order that the tensor core reads, into one copy
     CUtensorMap tq;            // q: 64 x G heads x 128 / G nodes x D / 64 blocks
-    CUtensorMap tk, tv;        // rings: 128 keys x half the blocks (K), 64 keys x all blocks (V)
+    CUtensorMap tk, tv;        // rings: 128 keys x 2 blocks (K), VKEYS keys x all blocks (V)
     CUtensorMap tk8;           // K ring in pieces of 8 keys x one block
     CUtensorMap tv8;
     CUtensorMap tkt, tvt;      // nodes' keys and values, boxes as tk's and tv's
@@ -78,7 +85,8 @@ struct TreeParams {
     const int32_t* parent;
     const int32_t* n;
     float4* part_o;            // [unit][lanes / 32][d / 4][32]: a store of 32 lanes is 512 bytes in a row
-    float4* part_ml;           // [unit][lanes]: m (log2 units), l of each column half
+    float4* part_l;            // [unit][lanes]: l of each column quarter
+    float* part_m;             // [unit][lanes]: m (log2 units)
     int* status;
     int* next_unit;
     int rows, nodes, hq, hkv, gsz, npt, mtiles, spans, lanes, win, ring, units, shared_kv;
@@ -91,34 +99,36 @@ struct TreeCfg {
     static constexpr int KB = D / 64;
     static constexpr int Q_BLOCK = 128 * 128;                 // 64 dims of 128 rows
     static constexpr int Q_BYTES = KB * Q_BLOCK;
-    static constexpr int SLOT = D * 128;                      // K: 128 keys x d / 2; V: 64 keys x d
-    static constexpr int NSLOT = D == 256 ? 5 : 10;
-    // Load barriers are per operand half and tile, tile mod NB: a parity wait is sound while the
+    static constexpr int HV = D / 128;                        // loads an operand and tile
+    static constexpr int SLOT = 32768;                        // K: 128 keys x 128 dims; V: 128 / HV keys x D dims
+    static constexpr int NSLOT = D == 256 ? 5 : 6;
+    // Load barriers are per operand part and tile, tile mod NB: a parity wait is sound while the
     // load of tile t + NB cannot land before the one of tile t was waited for, which the slot
-    // ring gives for 4 NB > NSLOT (four half-loads a tile).
+    // ring gives for 2 HV NB > NSLOT + HV - 1 (2 HV loads a tile).
     static constexpr int NB = D == 256 ? 2 : 4;
-    static_assert(4 * NB > NSLOT, "load barrier phases");
+    static_assert(2 * HV * NB > NSLOT + HV - 1, "load barrier phases");
+    static constexpr int VKEYS = kTile / HV;                  // keys of a V load
     static constexpr int K_BLOCK = kTile * 128;
-    static constexpr int V_BLOCK = (kTile / 2) * 128;
+    static constexpr int V_BLOCK = VKEYS * 128;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + Q_BYTES;
-    static constexpr int OFF_X = OFF_RING + NSLOT * SLOT;     // row maxima [2 tiles][2 halves][128]
-    static constexpr int B_KFULL = 0;                         // [half][NB]
-    static constexpr int B_VFULL = B_KFULL + 2 * NB;
-    static constexpr int B_VREADY = B_VFULL + 2 * NB;
-    static constexpr int B_FREE = B_VREADY + 2 * NB;          // [NSLOT]
+    static constexpr int OFF_X = OFF_RING + NSLOT * SLOT;     // row maxima [3 tiles][128]
+    static constexpr int B_KFULL = 0;                         // [HV][NB]
+    static constexpr int B_VFULL = B_KFULL + HV * NB;
+    static constexpr int B_VREADY = B_VFULL + HV * NB;
+    static constexpr int B_FREE = B_VREADY + HV * NB;         // [NSLOT]
     static constexpr int B_SFULL = B_FREE + NSLOT;            // [tile & 1] from here
     static constexpr int B_PVDONE = B_SFULL + 2;
-    static constexpr int B_XCHG = B_PVDONE + 2;
-    static constexpr int B_PHALF = B_XCHG + 2;
+    static constexpr int B_PHALF = B_PVDONE + 2;
     static constexpr int B_PFULL = B_PHALF + 2;
-    static constexpr int B_QFULL = B_PFULL + 2;
+    static constexpr int B_XCHG = B_PFULL + 2;                // [lane quarter][tile & 1]
+    static constexpr int B_QFULL = B_XCHG + 8;
     static constexpr int B_QFREE = B_QFULL + 1;
     static constexpr int B_UFULL = B_QFREE + 1;               // [kUnits]
     static constexpr int B_UFREE = B_UFULL + kUnits;
     static constexpr int B_DRAIN = B_UFREE + kUnits;
     static constexpr int NBAR = B_DRAIN + 1;
-    static constexpr int OFF_BAR = OFF_X + 2 * 2 * 128 * 4;
+    static constexpr int OFF_BAR = OFF_X + 3 * 128 * 4;
     static constexpr int OFF_UNIT = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;   // 8 ints and 128 parents a slot
     static constexpr int UNIT_BYTES = 32 + WA_TREE_MAX_NODES;
     static constexpr int OFF_MISC = OFF_UNIT + kUnits * UNIT_BYTES;
@@ -131,7 +141,7 @@ struct TreeCfg {
 };
 
 // The load order is K(0), then for each tile t: K(t + 1) if there is one, V(t).  Operand index of K(t)
-// and V(t) in it (two half-loads each).
+// and V(t) in it (HV loads each).
 __device__ __forceinline__ int op_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int op_v(int t, bool last_of_all) { return last_of_all ? 2 * t + 1 : 2 * t + 2; }
 
@@ -141,13 +151,21 @@ __device__ __forceinline__ void load_at(int o, int tiles, int& t, bool& is_v) {
     t = o == 0 ? 0 : is_v ? (o == 2 * tiles - 1 ? tiles - 1 : o / 2 - 1) : (o + 1) / 2;
 }
 
+// fp32 values as integers of the same order (NaN aside), and -inf in that order.
+__device__ __forceinline__ int ordered(float x) {
+    const int b = __float_as_int(x);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
+constexpr int kNoMax = static_cast<int>(0xFF800000u) ^ 0x7FFFFFFF;
+
 // A published unit.  nt = 0 marks the end.
 struct TreeUnit {
     int r, g, node0, span, t0, nring, nt, p, n, lo;
 };
 
 template <int D>
-__global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     using C = TreeCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -161,19 +179,21 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
     auto LOADBAR = [&](int base, int half, int t) { return BAR(base + half * C::NB + t % C::NB); };
     auto LOADPH = [&](int t) { return static_cast<uint32_t>(t / C::NB) & 1u; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-    float* xbuf = reinterpret_cast<float*>(smem + C::OFF_X);
+    int* xbuf = reinterpret_cast<int*>(smem + C::OFF_X);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
             int count = 1;
-            if (i >= C::B_XCHG && i < C::B_PFULL) count = 8;               // XCHG, PHALF: the softmax warps
-            else if (i >= C::B_PFULL && i < C::B_QFULL) count = 4;         // PFULL: those of the second half
-            else if (i >= C::B_UFREE && i < C::B_DRAIN) count = 11;        // producer, MMA, V, softmax warps
+            if (i >= C::B_PHALF && i < C::B_PFULL) count = 16;             // the softmax warps
+            else if (i >= C::B_PFULL && i < C::B_XCHG) count = 8;          // those of keys 64 and up
+            else if (i >= C::B_XCHG && i < C::B_QFULL) count = 4;          // those of a lane quarter
+            else if (i >= C::B_UFREE && i < C::B_DRAIN) count = 19;        // producer, MMA, V, softmax warps
             mbar_init(BAR(i), count);
         }
         fence_mbar_init();
     }
+    if (threadIdx.x >= 128 && threadIdx.x < 256) xbuf[threadIdx.x - 128] = kNoMax;    // the first tile's maxima
     if (warp == 1) {
         tmem_alloc(smem_u32(misc), C::TMEM_COLS);
         tmem_relinquish();
@@ -211,16 +231,16 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         // K and V are read once, unless several query tiles of a row share them
         const uint64_t pol = p.shared_kv ? policy_evict_last() : policy_evict_first();
         const int64_t tok = static_cast<int64_t>(p.hkv) * D;
-        int u = 0;                                // half-loads issued
+        int u = 0;                                // loads issued
         int tk = 0;                               // tiles whose K loads have begun
-        // one half-operand: K of 128 keys and half the dims, or V of 64 keys and all dims; slot0: the ring
-        // slot of the tile's first key, -1 for the nodes' own keys
+        // one load: K of 128 keys and 128 dims, or V of VKEYS keys and all dims; slot0: the ring slot of the
+        // tile's first key, -1 for the nodes' own keys
         auto load_half = [&](const TreeUnit& x, int slot0, int t, bool is_v, int half) -> bool {
             const int s = u % C::NSLOT, use = u / C::NSLOT;
             if (use > 0 && !warp_wait(BAR(C::B_FREE + s), (use - 1) & 1, p.status)) return false;
             const uint32_t full = LOADBAR(is_v ? C::B_VFULL : C::B_KFULL, half, t);
             const uint32_t dst = SLOT(s);
-            const int blk0 = is_v ? 0 : half * (C::KB / 2), key = is_v ? half * 64 : 0, nkeys = is_v ? 64 : kTile;
+            const int blk0 = is_v ? 0 : half * 2, key = is_v ? half * C::VKEYS : 0, nkeys = is_v ? C::VKEYS : kTile;
             int sl0 = slot0 + key;
             if (p.win > 0) {
                 if (sl0 >= p.ring) sl0 -= p.ring;
@@ -234,7 +254,7 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 }
             } else {
                 // pieces of 8 keys: by TMA, or by the warp where the piece itself wraps
-                const int nblk = is_v ? C::KB : C::KB / 2, blk = nkeys * 128;
+                const int nblk = is_v ? C::KB : 2, blk = nkeys * 128;
                 const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(x.r) * p.ring * tok +
                                        static_cast<int64_t>(x.g) * D + blk0 * 64;
                 int whole = 0;
@@ -268,7 +288,10 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         };
         auto load_k = [&](const TreeUnit& x, int slot0, int t) -> bool {
             tk = t + 1;
-            return load_half(x, slot0, t, false, 0) && load_half(x, slot0, t, false, 1);
+            bool ok = true;
+#pragma unroll
+            for (int h = 0; h < C::HV; ++h) ok = ok && load_half(x, slot0, t, false, h);
+            return ok;
         };
         // the ring slot of a unit's first tile, and of the tile after one
         auto first_slot = [&](const TreeUnit& x) { return x.nring == 0 ? -1 : p.win > 0 ? x.t0 * kTile % p.ring : x.t0 * kTile; };
@@ -305,7 +328,8 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 }
             }
             if (!ok) break;
-            ok = load_half(cur, sc, t, true, 0) && load_half(cur, sc, t, true, 1);
+#pragma unroll
+            for (int h = 0; h < C::HV; ++h) ok = ok && load_half(cur, sc, t, true, h);
             if (same) {
                 ++idx;
             } else {
@@ -316,12 +340,13 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             ++t;
         }
         // the copies in flight land before the block exits, whichever role stopped early (after a whole
-        // run every one was consumed, and the waits return at once); u half-loads were issued
+        // run every one was consumed, and the waits return at once)
         if (lane == 0) {
             for (int i = max(0, u - C::NSLOT); i < u; ++i) {
-                int tt, half = i & 1;
+                int tt;
+                const int half = i % C::HV;
                 bool v;
-                load_at(i >> 1, tk, tt, v);
+                load_at(i / C::HV, tk, tt, v);
                 mbar_wait(LOADBAR(v ? C::B_VFULL : C::B_KFULL, half, tt), LOADPH(tt), p.status);
             }
         }
@@ -334,14 +359,14 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             // slots in load order: K of tile t, then V of tile t - 1; V of the last tile has no K before it
             auto issue_s = [&](int t) -> bool {
 #pragma unroll
-                for (int kh = 0; kh < 2; ++kh) {
-                    const int s = (2 * op_k(t) + kh) % C::NSLOT;
+                for (int kh = 0; kh < C::HV; ++kh) {
+                    const int s = (C::HV * op_k(t) + kh) % C::NSLOT;
                     if (!mbar_wait(LOADBAR(C::B_KFULL, kh, t), LOADPH(t), p.status)) return false;
                     tc_fence_after();
                     const uint64_t bk = sdesc_sw128(SLOT(s), 16, 1024);
 #pragma unroll
-                    for (int k8 = 0; k8 < D / 32; ++k8) {
-                        const int kk = (D / 32) * kh + k8;
+                    for (int k8 = 0; k8 < 8; ++k8) {
+                        const int kk = 8 * kh + k8;
                         mma_bf16_ss(tbase + C::s_col(t & 1), aq + (((kk >> 2) * C::Q_BLOCK + (kk & 3) * 32) >> 4),
                                     bk + (((k8 >> 2) * C::K_BLOCK + (k8 & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
                     }
@@ -350,22 +375,24 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 mma_commit(BAR(C::B_SFULL + (t & 1)));
                 return true;
             };
+            // keys 0..63 of the tile, then 64..127, as their P arrives
             auto issue_pv = [&](int t, bool first, bool last_of_all) -> bool {
                 const int b = t & 1;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const int s = (2 * op_v(t, last_of_all) + hh) % C::NSLOT;
-                    if (!mbar_wait(LOADBAR(C::B_VREADY, hh, t), LOADPH(t), p.status)) return false;
+                    const int part_v = hh * 64 / C::VKEYS;
+                    const int s = (C::HV * op_v(t, last_of_all) + part_v) % C::NSLOT;
+                    if (hh * 64 % C::VKEYS == 0 && !mbar_wait(LOADBAR(C::B_VREADY, part_v, t), LOADPH(t), p.status)) return false;
                     if (!mbar_wait(BAR((hh ? C::B_PFULL : C::B_PHALF) + b), (t >> 1) & 1, p.status)) return false;
                     tc_fence_after();
-                    const uint64_t v0 = sdesc_sw128(SLOT(s), C::V_BLOCK, 1024);
+                    const uint64_t v0 = sdesc_sw128(SLOT(s) + (hh * 64 % C::VKEYS) * 128, C::V_BLOCK, 1024);
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4)
                             mma_bf16_ts(tbase, tbase + C::s_col(b) + hh * 64 + part * 32 + k4 * 8, v0 + ((k4 * 16 * 128) >> 4),
                                         idO, (!first || hh > 0 || part > 0 || k4 > 0) ? 1u : 0u);
-                    mma_commit(BAR(C::B_FREE + s));
+                    if ((hh + 1) * 64 % C::VKEYS == 0) mma_commit(BAR(C::B_FREE + s));
                 }
                 mma_commit(BAR(C::B_PVDONE + b));
                 return true;
@@ -407,18 +434,18 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                     have_next = true;
                 }
                 const bool last_of_all = have_next && nxt.nt <= 0;
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int s = (2 * op_v(t, last_of_all) + hh) % C::NSLOT;
+                for (int hh = 0; hh < C::HV; ++hh) {
+                    const int s = (C::HV * op_v(t, last_of_all) + hh) % C::NSLOT;
                     if (!(ok = warp_wait(LOADBAR(C::B_VFULL, hh, t), LOADPH(t), p.status))) break;
-                    int z_lo, z_hi, z_end = 64;       // rows [0, z_lo) and [z_hi, z_end) are cleared
+                    int z_lo, z_hi, z_end = C::VKEYS;       // rows [0, z_lo) and [z_hi, z_end) are cleared
                     if (idx < x.nring) {
-                        const int key0 = (x.t0 + idx) * kTile + hh * 64;
-                        z_lo = min(64, max(0, x.lo - key0));
-                        z_hi = max(0, min(64, x.p - key0 + 1));
+                        const int key0 = (x.t0 + idx) * kTile + hh * C::VKEYS;
+                        z_lo = min(C::VKEYS, max(0, x.lo - key0));
+                        z_hi = max(0, min(C::VKEYS, x.p - key0 + 1));
                     } else {
                         z_lo = 0;
-                        z_hi = max(0, min(64, x.n - hh * 64));
-                        z_end = max(0, min(64, p.nodes - hh * 64));   // past the buffer's nodes TMA has filled zeros
+                        z_hi = max(0, min(C::VKEYS, x.n - hh * C::VKEYS));
+                        z_end = max(0, min(C::VKEYS, p.nodes - hh * C::VKEYS));   // past the buffer's nodes TMA has filled zeros
                     }
                     z_hi = max(z_hi, z_lo);
                     const int nz = z_lo + max(0, z_end - z_hi);
@@ -544,12 +571,14 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         }
         if (lane == 0 && loaded > 0) mbar_wait(BAR(C::B_QFULL), (loaded - 1) & 1, p.status);
     } else {
-        // ------------------------------------------------ softmax: query row r, column half wg
-        const int wg = (warp - 4) >> 2;
-        const int r = (warp & 3) * 32 + lane;
+        // ------------------------------------------------ softmax: query row r, column quarter cq
+        const int cq = (warp - 4) >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;
         const int rn = r / p.gsz;                             // the row's node within the tile
-        const int col0 = wg * 64;
-        const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int col0 = cq * 32;
+        const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        // P of this quarter's keys: parts at column 64 h + 32 part + 16 (cq & 1), h = cq / 2
+        const uint32_t p_col = (cq >> 1) * 64 + (cq & 1) * 16;
         const float c = p.c;
         int t = 0;
         bool ok = true;
@@ -560,18 +589,15 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             const int node = x.node0 + rn;
             const bool live = x.nt > 0 && rn < p.npt && node < x.n;
             // the node's depth, and which of its ancestors (and itself) are in its window
-            int row_lo = INT_MIN / 2;                         // rows without a node: nothing masked, nothing stored
-            uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;      // tree columns [64 wg, 64 wg + 64)
+            int row_lo = 0;
+            uint32_t seen = 0xFFFFFFFFu;                      // tree columns [col0, col0 + 32); rows without a node: all
             if (live) {
                 const volatile uint8_t* par = reinterpret_cast<const volatile uint8_t*>(unit_ints(U) + 8);
                 int back = 0;
-                m0 = m1 = 0u;
+                seen = 0u;
                 for (int a = node; a != 255; a = par[a], ++back) {
                     const int col = a - col0;
-                    if (p.win == 0 || back < p.win) {
-                        if (col >= 0 && col < 32) m0 |= 1u << col;
-                        if (col >= 32 && col < 64) m1 |= 1u << (col - 32);
-                    }
+                    if (col >= 0 && col < 32 && (p.win == 0 || back < p.win)) seen |= 1u << col;
                 }
                 row_lo = p.win > 0 ? max(0, x.p + back - p.win + 1) : 0;   // back = depth + 1
             }
@@ -584,59 +610,56 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 const int b = t & 1;
                 const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
                 if (!(ok = warp_wait(BAR(C::B_SFULL + b), ph, p.status))) break;
+                const int xb = t % 3 * 128, xnext = (t + 1) % 3 * 128;
+                if (cq == 0) xbuf[xnext + r] = kNoMax;        // free since every warp read tile t - 2's maxima
                 if (idle) {
+                    __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(BAR(C::B_XCHG + b));
+                        mbar_arrive(BAR(C::B_XCHG + 2 * quarter + b));
                         mbar_arrive(BAR(C::B_PHALF + b));
-                        if (wg == 1) mbar_arrive(BAR(C::B_PFULL + b));
+                        if (cq >= 2) mbar_arrive(BAR(C::B_PFULL + b));
                     }
                     __syncwarp();
+                    // the quarter's warps stay within a tile of each other, as the maxima's buffers need
+                    if (!(ok = warp_wait(BAR(C::B_XCHG + 2 * quarter + b), ph, p.status))) break;
                     continue;
                 }
                 tc_fence_after();
-                const uint32_t t_s = tbase + lane_addr + C::s_col(b) + col0;
-                float sv[64];
-                load_s<64>(t_s, sv);
-                // visible columns of this half as bits
-                uint32_t w0 = m0, w1 = m1;
+                float sv[32];
+                load_s<32>(tbase + lane_addr + C::s_col(b) + col0, sv);
+                // visible columns of this quarter as bits
+                uint32_t vis = seen;
                 if (idx < x.nring) {
                     const int kbase = (x.t0 + idx) * kTile + col0;
-                    const int vlo = live ? max(0, row_lo - kbase) : 0, vhi = live ? min(63, x.p - kbase) : 63;
-                    const unsigned long long bits = vlo > vhi ? 0ull : (~0ull >> (63 - (vhi - vlo))) << vlo;
-                    w0 = static_cast<uint32_t>(bits);
-                    w1 = static_cast<uint32_t>(bits >> 32);
+                    const int vlo = live ? max(0, row_lo - kbase) : 0, vhi = live ? min(31, x.p - kbase) : 31;
+                    vis = vlo > vhi ? 0u : (0xFFFFFFFFu >> (31 - (vhi - vlo))) << vlo;
                 }
-                const bool masked = !__all_sync(0xFFFFFFFFu, (w0 & w1) == 0xFFFFFFFFu);
+                const bool masked = !__all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu);
                 if (masked) {   // a masked score is -inf, whatever it was: weight 0
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!(((k < 32 ? w0 : w1) >> (k & 31)) & 1u)) sv[k] = -INFINITY;
+                    for (int k = 0; k < 32; ++k)
+                        if (!((vis >> k) & 1u)) sv[k] = -INFINITY;
                 }
-                float mx8[8];
+                float mx4[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx8[e] = max3(sv[e], sv[e + 8], sv[e + 16]);
-#pragma unroll
-                for (int k = 24; k < 56; k += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mx8[e] = max3(mx8[e], sv[k + e], sv[k + e + 8]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(mx8[e], sv[56 + e]);
-                const float mh = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-                float* xs = xbuf + b * 256;
-                xs[wg * 128 + r] = mh;
+                for (int e = 0; e < 4; ++e)
+                    mx4[e] = max3(max3(sv[e], sv[e + 4], sv[e + 8]), max3(sv[e + 12], sv[e + 16], sv[e + 20]),
+                                  fmaxf(sv[e + 24], sv[e + 28]));
+                const float mh = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
+                if (mh > -INFINITY) atomicMax(&xbuf[xb + r], ordered(mh));   // (not for a NaN)
+                tc_fence_before();                            // this warp's S has been read: others may write P there
                 __syncwarp();   // the warp's stores precede lane 0's (cumulative) release
-                if (lane == 0) mbar_arrive(BAR(C::B_XCHG + b));
-                if (!(ok = warp_wait(BAR(C::B_XCHG + b), ph, p.status))) break;
-                const float mt = fmaxf(xs[r], xs[128 + r]) * c;
-                // lazy rule: keep the running max unless the tile's exceeds it by more than kLazy
-                const float m_new = (mt > m_run + kLazy) ? mt : m_run;
+                if (lane == 0) mbar_arrive(BAR(C::B_XCHG + 2 * quarter + b));
+                if (!(ok = warp_wait(BAR(C::B_XCHG + 2 * quarter + b), ph, p.status))) break;
+                tc_fence_after();
+                const float mt = unordered(xbuf[xb + r]) * c;
+                // lazy rule: keep the running max unless the tile's exceeds it by more than kTreeLazy
+                const float m_new = (mt > m_run + kTreeLazy) ? mt : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : ex2(m_run - m_new);
                 const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
-                float ls8[8];
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ls8[e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < 64; k += 2) {
+                for (int k = 0; k < 32; k += 2) {
                     float x0, x1;
                     fma_x2(x0, x1, sv[k], sv[k + 1], c, c, -m_sub, -m_sub);
                     sv[k] = ex2(x0);
@@ -644,21 +667,19 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                 }
                 if (c == 0.f && masked) {   // scale 0: -inf * 0 is no weight
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!(((k < 32 ? w0 : w1) >> (k & 31)) & 1u)) sv[k] = 0.f;
+                    for (int k = 0; k < 32; ++k)
+                        if (!((vis >> k) & 1u)) sv[k] = 0.f;
                 }
-#pragma unroll
-                for (int k = 0; k < 64; k += 2)
-                    add_x2(ls8[2 * ((k >> 1) & 3)], ls8[2 * ((k >> 1) & 3) + 1], sv[k], sv[k + 1]);
-                // O's rescale, once the previous P V is done; a unit's first P V starts O afresh
-                if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f)) {
+                // O's rescale, once the previous P V is done; a unit's first P V starts O afresh, and a row
+                // that has seen nothing yet has an O of zeros
+                if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f && m_run != -INFINITY)) {
                     if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status)))
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 64; ++cc) {
+                    for (int cc = 0; cc < D / 128; ++cc) {
                         uint32_t o[32];
-                        const uint32_t ta = tbase + lane_addr + wg * (D / 2) + cc * 32;
+                        const uint32_t ta = tbase + lane_addr + cq * (D / 4) + cc * 32;
                         tmem_ld32_wait(ta, o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
@@ -666,32 +687,38 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
                     }
                     tmem_wait_st();
                 }
-                if (wg == 1) {   // the second half's O columns are ready for this tile's first P V half
+                if (cq >= 2) {   // this quarter's O columns are ready for the tile's first P V half
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_PHALF + b));
                 }
-                // P = bf16(p) + bf16(p - bf16(p)) over this half's own S columns: within 2^-17 of p, which
-                // keeps the output to the decode form's accuracy (one bf16 part alone: 2^-9)
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
+                // P = hi + lo, two bf16: hi is p cut to 8 bits (its upper half), lo the rest rounded, so the sum
+                // is within 2^-16 of p, which keeps the output to the decode form's accuracy (one part: 2^-9)
+                {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = sv[cc * 32 + 2 * e], bb = sv[cc * 32 + 2 * e + 1];
-                        hi[e] = pack_bf16(a, bb);
-                        lo[e] = pack_bf16(a - __uint_as_float(hi[e] << 16), bb - __uint_as_float(hi[e] & 0xFFFF0000u));
+                        const float a = sv[2 * e], bb = sv[2 * e + 1];
+                        hi[e] = __byte_perm(__float_as_uint(a), __float_as_uint(bb), 0x7632);
+                        lo[e] = pack_bf16(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                                          bb - __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u));
                     }
-                    tmem_st16(t_s + cc * 16, hi);
-                    tmem_st16(t_s + 32 + cc * 16, lo);
+                    const uint32_t ta = tbase + lane_addr + C::s_col(b) + p_col;
+                    tmem_st16(ta, hi);
+                    tmem_st16(ta + 32, lo);
                 }
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    add_x2(ls[0], ls[1], sv[k], sv[k + 1]);
+                    add_x2(ls[2], ls[3], sv[k + 2], sv[k + 3]);
+                }
+                const float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                l_run = (alpha == 1.f) ? (l_run + lsum) : fmaf(l_run, alpha, lsum);
+                m_run = m_new;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR((wg == 0 ? C::B_PHALF : C::B_PFULL) + b));
-                const float lsum = ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
-                l_run = (alpha == 1.f) ? (l_run + lsum) : fmaf(l_run, alpha, lsum);
-                m_run = m_new;
+                if (lane == 0) mbar_arrive(BAR((cq < 2 ? C::B_PHALF : C::B_PFULL) + b));
             }
             if (!ok) break;
             if (idle) continue;
@@ -699,19 +726,18 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status))) break;
             tc_fence_after();
             const int64_t unit = ((static_cast<int64_t>(x.r) * p.hkv + x.g) * p.mtiles + x.node0 / p.npt) * p.spans + x.span;
-            float4* po = p.part_o + ((unit * (p.lanes >> 5) + (warp & 3)) * (D / 4) + wg * (D / 8)) * 32 + lane;
+            float4* po = p.part_o + ((unit * (p.lanes >> 5) + quarter) * (D / 4) + cq * (D / 16)) * 32 + lane;
 #pragma unroll 1
-            for (int cc = 0; cc < D / 64; ++cc) {
+            for (int cc = 0; cc < D / 128; ++cc) {
                 uint32_t o[32];
-                tmem_ld32_wait(tbase + lane_addr + wg * (D / 2) + cc * 32, o);
+                tmem_ld32_wait(tbase + lane_addr + cq * (D / 4) + cc * 32, o);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     po[(cc * 8 + e) * 32] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
             }
-            float* ml = reinterpret_cast<float*>(p.part_ml + unit * p.lanes + r);
-            if (wg == 0) *reinterpret_cast<float2*>(ml) = make_float2(m_run, l_run);
-            else ml[2] = l_run;
+            reinterpret_cast<float*>(p.part_l + unit * p.lanes + r)[cq] = l_run;
+            if (cq == 0) p.part_m[unit * p.lanes + r] = m_run;
         }
     }
 
@@ -807,7 +833,8 @@ __device__ void tree_rerun(const TreeArgs& a, TreeRerun& sm, int r, int node, in
 // (512 bytes a warp and load, four spans in flight), and turns them round in shared memory for the output.
 // A row with a value that is not finite is computed again in float64.
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_ml,
+__global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_l,
+                                                         const float* __restrict__ part_m,
                                                          const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans, int lanes) {
     __shared__ __align__(16) uint8_t tile[32 * 144];
     __shared__ int bad[32];
@@ -828,22 +855,22 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restric
     if (first >= npt || node0 + first >= n) return;
     if (t < 32) bad[t] = 0;
     __syncthreads();
-    const float4* ml = part_ml + unit0 * lanes + qd * 32 + lane;
+    const int64_t rec = unit0 * lanes + qd * 32 + lane;
     const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + blockIdx.y * 16 + warp * 2) * 32 + lane;
     const int64_t ostep = static_cast<int64_t>(quarters) * (D / 4) * 32;
     float M = -INFINITY;
 #pragma unroll 4
-    for (int s = 0; s < count; ++s) M = fmaxf(M, ml[static_cast<int64_t>(s) * lanes].x);
+    for (int s = 0; s < count; ++s) M = fmaxf(M, part_m[rec + static_cast<int64_t>(s) * lanes]);
     float num[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) num[e] = 0.f;
     float den = 0.f;
 #pragma unroll 4
     for (int s = 0; s < count; ++s) {
-        const float4 x = ml[static_cast<int64_t>(s) * lanes];
+        const float4 l4 = part_l[rec + static_cast<int64_t>(s) * lanes];
         const float4 o0 = po[s * ostep], o1 = po[s * ostep + 32];
-        const float w = exp2f(x.x - M);
-        den = fmaf(w, x.y + x.z, den);
+        const float w = exp2f(part_m[rec + static_cast<int64_t>(s) * lanes] - M);
+        den = fmaf(w, (l4.x + l4.y) + (l4.z + l4.w), den);
         num[0] = fmaf(w, o0.x, num[0]);
         num[1] = fmaf(w, o0.y, num[1]);
         num[2] = fmaf(w, o0.z, num[2]);
@@ -911,18 +938,19 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     constexpr int KB = C::KB;
     const bool whole = G * pl.npt == 128;    // a tile's rows fill a block of the Q buffer: one copy for all blocks
     if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, pl.npt, whole ? KB : 1) ||
-        !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, KB / 2, 1) ||
-        !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile / 2, KB, 1) ||
+        !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, 2, 1) ||
+        !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, C::VKEYS, KB, 1) ||
         !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
         !encode_5d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
-        !encode_5d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, false, kTile, KB / 2, 1) ||
-        !encode_5d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, false, kTile / 2, KB, 1))
+        !encode_5d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, false, kTile, 2, 1) ||
+        !encode_5d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, false, C::VKEYS, KB, 1))
         return cudaErrorInvalidValue;
     t.k = static_cast<const uint16_t*>(a.k);
     t.v = static_cast<const uint16_t*>(a.v);
     t.pos = a.pos; t.parent = a.parent; t.n = a.n;
-    t.part_ml = static_cast<float4*>(a.part);
-    t.part_o = t.part_ml + pl.units * pl.lanes;
+    t.part_l = static_cast<float4*>(a.part);
+    t.part_o = t.part_l + pl.units * pl.lanes;
+    t.part_m = reinterpret_cast<float*>(t.part_o + pl.units * pl.lanes * (D / 4));
     t.status = &a.hdr->status;
     t.next_unit = &a.hdr->next_unit;
     t.rows = a.rows; t.nodes = a.nodes; t.hq = a.hq; t.hkv = a.hkv; t.gsz = G; t.npt = pl.npt; t.mtiles = pl.mtiles;
@@ -934,11 +962,11 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
     const int grid = static_cast<int>(pl.units < sms ? pl.units : sms);
-    tree_kernel<D><<<grid, 384, C::SMEM, s>>>(t);
+    tree_kernel<D><<<grid, kTreeThreads, C::SMEM, s>>>(t);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
-    tree_merge_kernel<D><<<mgrid, 256, 0, s>>>(t.part_o, t.part_ml, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
+    tree_merge_kernel<D><<<mgrid, 256, 0, s>>>(t.part_o, t.part_l, t.part_m, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
     return cudaGetLastError();
 }
 
