@@ -74,7 +74,7 @@ __host__ __device__ inline int tree_spans(int p, int win, int hkv) {
 struct TreeParams {
     // five dimensions (64 dims, tokens, blocks of 64 dims, heads, rows) put a whole half-operand, in the
     // [block][token][64] order that the tensor core reads, into one copy
-    CUtensorMap tq;            // q: 64 x G heads x 128 / G nodes x D / 64 blocks
+    CUtensorMap tq;            // q: 64 x G heads x qn nodes x D / 64 blocks or one
     CUtensorMap tk, tv;        // rings: 128 keys x 2 blocks (K), VKEYS keys x all blocks (V)
     CUtensorMap tk8;           // K ring in pieces of 8 keys x one block
     CUtensorMap tv8;
@@ -89,19 +89,21 @@ struct TreeParams {
     float* part_m;             // [unit][lanes]: m (log2 units)
     int* status;
     int* next_unit;
-    int rows, nodes, hq, hkv, gsz, npt, mtiles, spans, lanes, win, ring, units, shared_kv;
+    int rows, nodes, hq, hkv, gsz, npt, qn, mtiles, spans, lanes, win, ring, units, shared_kv;
     float c;                   // |scale| * log2(e)
     int neg;
 };
 
-template <int D>
+// QR: query rows that the Q buffer holds.  A tile of up to 64 rows leaves room for one more slot at head
+// dim 256; the tensor core then reads rows past the buffer, which no output uses.
+template <int D, int QR>
 struct TreeCfg {
     static constexpr int KB = D / 64;
-    static constexpr int Q_BLOCK = 128 * 128;                 // 64 dims of 128 rows
+    static constexpr int Q_BLOCK = QR * 128;                  // 64 dims of QR rows
     static constexpr int Q_BYTES = KB * Q_BLOCK;
     static constexpr int HV = D / 128;                        // loads an operand and tile
     static constexpr int SLOT = 32768;                        // K: 128 keys x 128 dims; V: 128 / HV keys x D dims
-    static constexpr int NSLOT = D == 256 ? 5 : 6;
+    static constexpr int NSLOT = D == 256 && QR == 128 ? 5 : 6;
     // Load barriers are per operand part and tile, tile mod NB: a parity wait is sound while the
     // load of tile t + NB cannot land before the one of tile t was waited for, which the slot
     // ring gives for 2 HV NB > NSLOT + HV - 1 (2 HV loads a tile).
@@ -164,9 +166,9 @@ struct TreeUnit {
     int r, g, node0, span, t0, nring, nt, p, n, lo;
 };
 
-template <int D>
+template <int D, int QR>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-    using C = TreeCfg<D>;
+    using C = TreeCfg<D, QR>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {
@@ -390,8 +392,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4)
-                            mma_bf16_ts(tbase, tbase + C::s_col(b) + hh * 64 + part * 32 + k4 * 8, v0 + ((k4 * 16 * 128) >> 4),
-                                        idO, (!first || hh > 0 || part > 0 || k4 > 0) ? 1u : 0u);
+                            mma_bf16_ts(tbase, tbase + C::s_col(b) + hh * 64 + (k4 >> 1) * 32 + part * 16 + (k4 & 1) * 8,
+                                        v0 + ((k4 * 16 * 128) >> 4), idO, (!first || hh > 0 || part > 0 || k4 > 0) ? 1u : 0u);
                     if ((hh + 1) * 64 % C::VKEYS == 0) mma_commit(BAR(C::B_FREE + s));
                 }
                 mma_commit(BAR(C::B_PVDONE + b));
@@ -543,10 +545,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         };
         auto load_q = [&](const TreeUnit& x) {
             if (lane == 0) {
-                mbar_arrive_expect_tx(BAR(C::B_QFULL), C::KB * p.gsz * p.npt * 128);
-                if (p.gsz * p.npt == 128) {
+                mbar_arrive_expect_tx(BAR(C::B_QFULL), C::KB * p.gsz * p.qn * 128);
+                if (p.gsz * p.qn == QR) {
                     tma_load_5d(sbase + C::OFF_Q, &p.tq, 0, x.g * p.gsz, x.node0, 0, x.r, BAR(C::B_QFULL), policy_evict_last());
-                } else {        // a tile of fewer than 128 rows: block by block
+                } else {        // a tile that does not fill a block: block by block
                     for (int b = 0; b < C::KB; ++b)
                         tma_load_5d(sbase + C::OFF_Q + b * C::Q_BLOCK, &p.tq, 0, x.g * p.gsz, x.node0, b, x.r, BAR(C::B_QFULL),
                                     policy_evict_last());
@@ -577,69 +579,86 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int rn = r / p.gsz;                             // the row's node within the tile
         const int col0 = cq * 32;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        // P of this quarter's keys: parts at column 64 h + 32 part + 16 (cq & 1), h = cq / 2
-        const uint32_t p_col = (cq >> 1) * 64 + (cq & 1) * 16;
         const float c = p.c;
-        int t = 0;
-        bool ok = true;
-        for (int U = 0; ok; ++U) {
+        // a unit as this thread sees it
+        int t0 = 0, nring = 0, nt = 0, row_lo = 0, row_hi = 0;
+        uint32_t seen = 0;                                    // tree columns [col0, col0 + 32) that the row sees
+        bool live = false, idle = true;
+        int64_t unit = 0;
+        auto fetch = [&](int U) -> bool {
+            if (!warp_wait(BAR(C::B_UFULL + U % kUnits), static_cast<uint32_t>(U / kUnits) & 1u, p.status)) return false;
             TreeUnit x;
-            if (!(ok = warp_wait(BAR(C::B_UFULL + U % kUnits), static_cast<uint32_t>(U / kUnits) & 1u, p.status))) break;
             read_unit(U, x);
+            t0 = x.t0;
+            nring = x.nring;
+            nt = x.nt;
+            row_hi = x.p;
             const int node = x.node0 + rn;
-            const bool live = x.nt > 0 && rn < p.npt && node < x.n;
-            // the node's depth, and which of its ancestors (and itself) are in its window
-            int row_lo = 0;
-            uint32_t seen = 0xFFFFFFFFu;                      // tree columns [col0, col0 + 32); rows without a node: all
+            live = x.nt > 0 && rn < p.npt && node < x.n;
+            row_lo = 0;
+            seen = 0xFFFFFFFFu;                               // rows without a node: nothing masked
             if (live) {
-                const volatile uint8_t* par = reinterpret_cast<const volatile uint8_t*>(unit_ints(U) + 8);
+                const uint32_t par = sbase + C::OFF_UNIT + (U % kUnits) * C::UNIT_BYTES + 32;
+                uint32_t a = node;
                 int back = 0;
                 seen = 0u;
-                for (int a = node; a != 255; a = par[a], ++back) {
-                    const int col = a - col0;
-                    if (col >= 0 && col < 32 && (p.win == 0 || back < p.win)) seen |= 1u << col;
-                }
+                do {
+                    const uint32_t col = a - col0;
+                    if (col < 32u && (p.win == 0 || back < p.win)) seen |= 1u << col;
+                    ++back;
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(a) : "r"(par + a) : "memory");
+                } while (a != 255u);
                 row_lo = p.win > 0 ? max(0, x.p + back - p.win + 1) : 0;   // back = depth + 1
             }
+            idle = !__any_sync(0xFFFFFFFFu, live);            // a warp without rows only keeps the barriers going
+            unit = ((static_cast<int64_t>(x.r) * p.hkv + x.g) * p.mtiles + x.node0 / p.npt) * p.spans + x.span;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kUnits));
-            if (x.nt <= 0) break;
-            const bool idle = !__any_sync(0xFFFFFFFFu, live);     // a warp without rows only keeps the barriers going
+            return true;
+        };
+        int t = 0;
+        bool ok = fetch(0);
+        for (int U = 0; ok && nt > 0; ++U) {
             float m_run = -INFINITY, l_run = 0.f;
-            for (int idx = 0; idx < x.nt; ++idx, ++t) {
+            for (int idx = 0; idx < nt; ++idx, ++t) {
                 const int b = t & 1;
                 const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
+                const uint32_t xbar = BAR(C::B_XCHG + 2 * quarter + b);
                 if (!(ok = warp_wait(BAR(C::B_SFULL + b), ph, p.status))) break;
                 const int xb = t % 3 * 128, xnext = (t + 1) % 3 * 128;
                 if (cq == 0) xbuf[xnext + r] = kNoMax;        // free since every warp read tile t - 2's maxima
                 if (idle) {
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(BAR(C::B_XCHG + 2 * quarter + b));
+                        mbar_arrive(xbar);
                         mbar_arrive(BAR(C::B_PHALF + b));
                         if (cq >= 2) mbar_arrive(BAR(C::B_PFULL + b));
                     }
                     __syncwarp();
                     // the quarter's warps stay within a tile of each other, as the maxima's buffers need
-                    if (!(ok = warp_wait(BAR(C::B_XCHG + 2 * quarter + b), ph, p.status))) break;
+                    if (!(ok = warp_wait(xbar, ph, p.status))) break;
                     continue;
                 }
                 tc_fence_after();
-                float sv[32];
-                load_s<32>(tbase + lane_addr + C::s_col(b) + col0, sv);
+                const uint32_t t_s = tbase + lane_addr + C::s_col(b) + col0;
                 // visible columns of this quarter as bits
                 uint32_t vis = seen;
-                if (idx < x.nring) {
-                    const int kbase = (x.t0 + idx) * kTile + col0;
-                    const int vlo = live ? max(0, row_lo - kbase) : 0, vhi = live ? min(31, x.p - kbase) : 31;
+                if (idx < nring) {
+                    const int kbase = (t0 + idx) * kTile + col0;
+                    const int vlo = live ? max(0, row_lo - kbase) : 0, vhi = live ? min(31, row_hi - kbase) : 31;
                     vis = vlo > vhi ? 0u : (0xFFFFFFFFu >> (31 - (vhi - vlo))) << vlo;
                 }
                 const bool masked = !__all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu);
-                if (masked) {   // a masked score is -inf, whatever it was: weight 0
+                float sv[32];
+                auto load = [&]() {
+                    load_s<32>(t_s, sv);
+                    if (masked) {   // a masked score is -inf, whatever it was: weight 0
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((vis >> k) & 1u)) sv[k] = -INFINITY;
-                }
+                        for (int k = 0; k < 32; ++k)
+                            if (!((vis >> k) & 1u)) sv[k] = -INFINITY;
+                    }
+                };
+                load();
                 float mx4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -647,43 +666,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                                   fmaxf(sv[e + 24], sv[e + 28]));
                 const float mh = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
                 if (mh > -INFINITY) atomicMax(&xbuf[xb + r], ordered(mh));   // (not for a NaN)
-                tc_fence_before();                            // this warp's S has been read: others may write P there
                 __syncwarp();   // the warp's stores precede lane 0's (cumulative) release
-                if (lane == 0) mbar_arrive(BAR(C::B_XCHG + 2 * quarter + b));
-                if (!(ok = warp_wait(BAR(C::B_XCHG + 2 * quarter + b), ph, p.status))) break;
-                tc_fence_after();
-                const float mt = unordered(xbuf[xb + r]) * c;
-                // lazy rule: keep the running max unless the tile's exceeds it by more than kTreeLazy
-                const float m_new = (mt > m_run + kTreeLazy) ? mt : m_run;
-                const float alpha = (m_new == m_run) ? 1.f : ex2(m_run - m_new);
-                const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                if (lane == 0) mbar_arrive(xbar);
+                // The row's maximum over the four quarters; lazy rule: the running one stays unless the tile's
+                // exceeds it by more than kTreeLazy.  So the exponentials below start with the running one while
+                // the other quarters' maxima are on their way, and are done again, from S, where it moved.
+                float m_old = m_run, alpha = 1.f;
+                bool spec = __all_sync(0xFFFFFFFFu, !live || m_run != -INFINITY);
+                float lsum;
+                for (;;) {
+                    if (!spec) {
+                        if (!(ok = warp_wait(xbar, ph, p.status))) break;
+                        const float mt = unordered(xbuf[xb + r]) * c;
+                        m_run = (mt > m_old + kTreeLazy) ? mt : m_old;
+                        alpha = (m_run == m_old) ? 1.f : ex2(m_old - m_run);
+                    }
+                    const float m_sub = (m_run == -INFINITY) ? 0.f : m_run;
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float x0, x1;
-                    fma_x2(x0, x1, sv[k], sv[k + 1], c, c, -m_sub, -m_sub);
-                    sv[k] = ex2(x0);
-                    sv[k + 1] = ex2(x1);
-                }
-                if (c == 0.f && masked) {   // scale 0: -inf * 0 is no weight
+                    for (int k = 0; k < 32; k += 2) {
+                        float x0, x1;
+                        fma_x2(x0, x1, sv[k], sv[k + 1], c, c, -m_sub, -m_sub);
+                        sv[k] = ex2(x0);
+                        sv[k + 1] = ex2(x1);
+                    }
+                    if (c == 0.f && masked) {   // scale 0: -inf * 0 is no weight
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((vis >> k) & 1u)) sv[k] = 0.f;
+                        for (int k = 0; k < 32; ++k)
+                            if (!((vis >> k) & 1u)) sv[k] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        add_x2(ls[0], ls[1], sv[k], sv[k + 1]);
+                        add_x2(ls[2], ls[3], sv[k + 2], sv[k + 3]);
+                    }
+                    lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    if (!spec) break;
+                    if (!(ok = warp_wait(xbar, ph, p.status))) break;
+                    const float mt = unordered(xbuf[xb + r]) * c;
+                    if (!__any_sync(0xFFFFFFFFu, live && mt > m_old + kTreeLazy)) break;
+                    spec = false;
+                    load();
                 }
+                if (!ok) break;
                 // O's rescale, once the previous P V is done; a unit's first P V starts O afresh, and a row
                 // that has seen nothing yet has an O of zeros
-                if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f && m_run != -INFINITY)) {
+                if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f && m_old != -INFINITY)) {
                     if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status)))
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 128; ++cc) {
-                        uint32_t o[32];
-                        const uint32_t ta = tbase + lane_addr + cq * (D / 4) + cc * 32;
-                        tmem_ld32_wait(ta, o);
+                    for (int cc = 0; cc < D / 64; ++cc) {
+                        uint32_t o[16];
+                        const uint32_t ta = tbase + lane_addr + cq * (D / 4) + cc * 16;
+                        tmem_ld16_wait(ta, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(ta, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(ta, o);
                     }
                     tmem_wait_st();
                 }
@@ -692,41 +731,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_PHALF + b));
                 }
-                // P = hi + lo, two bf16: hi is p cut to 8 bits (its upper half), lo the rest rounded, so the sum
-                // is within 2^-16 of p, which keeps the output to the decode form's accuracy (one part: 2^-9)
+                // P over this quarter's own columns of S: hi in the first 16, lo in the others.  hi is p cut to 8
+                // bits (its upper half), lo the rest rounded to bf16, so their sum is within 2^-16 of p, which
+                // keeps the output to the decode form's accuracy (one part alone: 2^-9).
                 {
-                    uint32_t hi[16], lo[16];
+                    uint32_t w[32];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float a = sv[2 * e], bb = sv[2 * e + 1];
-                        hi[e] = __byte_perm(__float_as_uint(a), __float_as_uint(bb), 0x7632);
-                        lo[e] = pack_bf16(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
-                                          bb - __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u));
+                        w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(bb), 0x7632);
+                        w[16 + e] = pack_bf16(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                                              bb - __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u));
                     }
-                    const uint32_t ta = tbase + lane_addr + C::s_col(b) + p_col;
-                    tmem_st16(ta, hi);
-                    tmem_st16(ta + 32, lo);
+                    tmem_st32(t_s, w);
                 }
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    add_x2(ls[0], ls[1], sv[k], sv[k + 1]);
-                    add_x2(ls[2], ls[3], sv[k + 2], sv[k + 3]);
-                }
-                const float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 l_run = (alpha == 1.f) ? (l_run + lsum) : fmaf(l_run, alpha, lsum);
-                m_run = m_new;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR((cq < 2 ? C::B_PHALF : C::B_PFULL) + b));
             }
             if (!ok) break;
-            if (idle) continue;
+            // the next unit's rows are looked up while the last P V runs
+            const bool was_idle = idle;
+            const int64_t done = unit;
+            if (!(ok = fetch(U + 1))) break;
+            if (was_idle) continue;
             // the unit's partial result; the next unit's first P V waits for this warp's next PHALF
             if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status))) break;
             tc_fence_after();
-            const int64_t unit = ((static_cast<int64_t>(x.r) * p.hkv + x.g) * p.mtiles + x.node0 / p.npt) * p.spans + x.span;
-            float4* po = p.part_o + ((unit * (p.lanes >> 5) + quarter) * (D / 4) + cq * (D / 16)) * 32 + lane;
+            float4* po = p.part_o + ((done * (p.lanes >> 5) + quarter) * (D / 4) + cq * (D / 16)) * 32 + lane;
 #pragma unroll 1
             for (int cc = 0; cc < D / 128; ++cc) {
                 uint32_t o[32];
@@ -736,8 +770,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     po[(cc * 8 + e) * 32] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
             }
-            reinterpret_cast<float*>(p.part_l + unit * p.lanes + r)[cq] = l_run;
-            if (cq == 0) p.part_m[unit * p.lanes + r] = m_run;
+            reinterpret_cast<float*>(p.part_l + done * p.lanes + r)[cq] = l_run;
+            if (cq == 0) p.part_m[done * p.lanes + r] = m_run;
         }
     }
 
@@ -928,16 +962,17 @@ bool encode_5d(CUtensorMap* m, const void* base, int d, int heads, int toks, int
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int QR>
 cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
-    using C = TreeCfg<D>;
+    using C = TreeCfg<D, QR>;
     const TreePlan pl = tree_plan(a.rows, a.nodes, a.hq, a.hkv, a.win, a.ring);
     TreeParams t{};
     const int G = a.hq / a.hkv;
     const int64_t ktok = static_cast<int64_t>(a.hkv) * D, krow = ktok * a.ring;
     constexpr int KB = C::KB;
-    const bool whole = G * pl.npt == 128;    // a tile's rows fill a block of the Q buffer: one copy for all blocks
-    if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, pl.npt, whole ? KB : 1) ||
+    t.qn = a.nodes < pl.npt ? a.nodes : pl.npt;
+    const bool whole = G * t.qn == QR;       // a tile's rows fill a block of the Q buffer: one copy for all blocks
+    if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, t.qn, whole ? KB : 1) ||
         !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, 2, 1) ||
         !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, C::VKEYS, KB, 1) ||
         !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
@@ -962,12 +997,17 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
     const int grid = static_cast<int>(pl.units < sms ? pl.units : sms);
-    tree_kernel<D><<<grid, kTreeThreads, C::SMEM, s>>>(t);
+    tree_kernel<D, QR><<<grid, kTreeThreads, C::SMEM, s>>>(t);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
     tree_merge_kernel<D><<<mgrid, 256, 0, s>>>(t.part_o, t.part_l, t.part_m, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
     return cudaGetLastError();
+}
+
+template <int D, int QR>
+cudaError_t tree_attr() {
+    return cudaFuncSetAttribute(tree_kernel<D, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<D, QR>::SMEM);
 }
 
 }  // namespace
@@ -997,13 +1037,16 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
 }
 
 cudaError_t tree_prepare_device(int) {
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<128>::SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(tree_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<256>::SMEM);
+    cudaError_t e;
+    if ((e = tree_attr<128, 128>()) != cudaSuccess) return e;
+    if ((e = tree_attr<256, 64>()) != cudaSuccess) return e;
+    return tree_attr<256, 128>();
 }
 
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
-    return a.d == 256 ? launch_tree_d<256>(a, s) : launch_tree_d<128>(a, s);
+    if (a.d == 128) return launch_tree_d<128, 128>(a, s);
+    return tree_plan(a.rows, a.nodes, a.hq, a.hkv, a.win, a.ring).lanes <= 64 ? launch_tree_d<256, 64>(a, s)
+                                                                              : launch_tree_d<256, 128>(a, s);
 }
 
 }  // namespace wa
