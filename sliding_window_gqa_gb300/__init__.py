@@ -11,6 +11,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -380,30 +381,26 @@ def prep_append(src, pos, q_out, k_ring, v_ring=None, mode: str = "rmsnorm", q_s
     return ws
 
 
-# Drafted tokens.  These calls run on their inputs' device, whichever is current, and on `stream`
-# or that device's current stream; what they allocate is kept for that stream.
+# Drafted tokens.  These calls run on their inputs' device, whichever is current, and on `stream` or
+# that device's current stream; what they allocate is kept for that stream.  A drafted step makes one
+# call a layer, of a few microseconds on the GPU for a single sequence, so each call asks everything
+# that has to hold of its tensors in one expression, and a call that does not pass goes through checks
+# that say what is wrong (or accept what the short form does not cover, as strided nodes).
 
-class _on_device:
-    """The inputs' device made current for a call, where it is not already."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _keep_for(stream, *made) -> None:
+def _keep_for(stream, made) -> None:
     """Memory allocated on the current stream and used on another is not reused before that one is done."""
-    if stream is not None and stream != torch.cuda.current_stream():
+    if stream != torch.cuda.current_stream():
         for t in made:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_ws_bytes(*sizes) -> int:
+    return max(256, int(lib().wa_tree_decode_ws_bytes(*sizes)))
 
 
 def _check_i32(name: str, t, shape) -> None:
@@ -447,6 +444,23 @@ def _node_strides(name: str, t: torch.Tensor, d: int):
     return row, tok
 
 
+def _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out):
+    """((rows, nodes, hq, hkv, d, ring), strides) of a tree decode call; raises where its tensors disagree."""
+    for n_, t in (("q", q), ("k_ring", k_ring), ("v_ring", v_ring), ("k_tree", k_tree), ("v_tree", v_tree)):
+        _check_bf16(n_, t)
+    sizes = rows, nodes, hq, hkv, d, ring = _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out)
+    _check_i32("pos", pos, (rows,))
+    _check_i32("parent", parent, (rows, nodes))
+    if n is not None:
+        _check_i32("n", n, (rows,))
+    _same_device(q.device, k_ring=k_ring, v_ring=v_ring, k_tree=k_tree, v_tree=v_tree, pos=pos, parent=parent, n=n,
+                 out=out)
+    dense = (0, 0)      # as the library takes them
+    return sizes, _TreeStrides(*_node_strides("q", q, d), *_node_strides("k_tree", k_tree, d),
+                               *_node_strides("v_tree", v_tree, d),
+                               *(dense if out is None else _node_strides("out", out, d)))
+
+
 def tree_decode_ws_bytes(rows: int, nodes: int, hq: int, hkv: int, d: int, win: int, ring: int) -> int:
     return int(lib().wa_tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring))
 
@@ -461,31 +475,47 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
     for one that follows the cache; n int32 [rows] or None: nodes in use.  A node sees the cache, its
     ancestors and itself, as far as the window reaches back.  Returns out [rows, nodes, hq, d] bf16,
     whose nodes past n are not written.  ``ws``: a reused uint8 CUDA buffer of tree_decode_ws_bytes(...)."""
-    for n_, t in (("q", q), ("k_ring", k_ring), ("v_ring", v_ring), ("k_tree", k_tree), ("v_tree", v_tree)):
-        _check_bf16(n_, t)
-    rows, nodes, hq, hkv, d, ring = _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out)
-    _check_i32("pos", pos, (rows,))
-    _check_i32("parent", parent, (rows, nodes))
-    if n is not None:
-        _check_i32("n", n, (rows,))
-    dev = q.device
-    _same_device(dev, k_ring=k_ring, v_ring=v_ring, k_tree=k_tree, v_tree=v_tree, pos=pos, parent=parent, n=n, out=out)
-    with _on_device(dev):
-        made = [None, None]
-        if out is None:
-            out = made[0] = torch.empty((rows, nodes, hq, d), dtype=torch.bfloat16, device=dev)
-        st = _TreeStrides(*_node_strides("q", q, d), *_node_strides("k_tree", k_tree, d),
-                          *_node_strides("v_tree", v_tree, d), *_node_strides("out", out, d))
-        if ws is None:
-            made[1] = ws = _workspace(tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring), dev, None)
-        else:
-            _workspace(0, dev, ws)
-        rc = lib().wa_tree_decode(q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(),
-                                  v_tree.data_ptr(), pos.data_ptr(), parent.data_ptr(),
-                                  None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring,
-                                  float(scale), ctypes.byref(st), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
-                                  _stream_handle(stream))
-        _keep_for(stream, *made)
+    try:
+        rows, nodes, hq, d = q.shape
+        _, ring, hkv, _ = cache = k_ring.shape
+        tree, dev = (rows, nodes, hkv, d), q.get_device()
+        plain = (q.dtype is _BF16 and k_ring.dtype is _BF16 and v_ring.dtype is _BF16 and k_tree.dtype is _BF16
+                 and v_tree.dtype is _BF16 and cache[0] == rows and cache[3] == d and v_ring.shape == cache
+                 and k_tree.shape == tree and v_tree.shape == tree and pos.dtype is _I32 and parent.dtype is _I32
+                 and pos.shape == (rows,) and parent.shape == (rows, nodes) and k_ring.get_device() == dev
+                 and v_ring.get_device() == dev and k_tree.get_device() == dev and v_tree.get_device() == dev
+                 and pos.get_device() == dev and parent.get_device() == dev and dev >= 0 and q.is_contiguous()
+                 and k_ring.is_contiguous() and v_ring.is_contiguous() and k_tree.is_contiguous()
+                 and v_tree.is_contiguous() and pos.is_contiguous() and parent.is_contiguous()
+                 and (n is None or (n.dtype is _I32 and n.shape == (rows,) and n.get_device() == dev
+                                    and n.is_contiguous()))
+                 and (out is None or (out.dtype is _BF16 and out.shape == q.shape and out.get_device() == dev
+                                      and out.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    st = None
+    if not plain:
+        (rows, nodes, hq, hkv, d, ring), st = _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out)
+        dev = q.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws, stream)
+    made = []
+    if out is None:
+        out = torch.empty((rows, nodes, hq, d), dtype=_BF16, device=q.device)
+        made.append(out)
+    if ws is None:
+        nbytes = _tree_ws_bytes(rows, nodes, hq, hkv, d, win, ring)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        made.append(ws)
+    else:
+        nbytes = _ws_bytes(_workspace(0, q.device, ws))
+    rc = lib().wa_tree_decode(
+        q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), pos.data_ptr(),
+        parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring, scale, st,
+        out.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if stream is not None:
+        _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_decode")
     return out
@@ -506,19 +536,11 @@ def _prob_strides(name: str, t: torch.Tensor, shape):
     return row, node
 
 
-def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length=None, token=None, ws=None,
-                stream=None):
-    """Which drafted tokens the target keeps, and the token after them: speculative sampling over a tree.
-
-    target fp32 [rows, nodes, vocab]: the target's probabilities after each node; draft: those that the
-    node's children were drawn from, or None where they were not drawn.  parent, tokens int32
-    [rows, nodes]; node 0 is the last sampled token.  u fp32 [rows, nodes] in [0, 1): u[:, c] tests node
-    c, u[:, 0] samples the last token.  n int32 [rows] or None: nodes in use.  Returns (path int32
-    [rows, nodes], length int32 [rows], token int32 [rows]): the kept nodes in order, then -1; how many;
-    the token sampled after them (-1: no nodes, or a distribution without mass)."""
-    t_row, t_node = _prob_strides("target", target, None)
+def _verify_check(target, parent, tokens, u, draft, n, path, length, token):
+    """Strides of a verification call; raises where its tensors disagree."""
+    t_st = _prob_strides("target", target, None)
     rows, nodes, vocab = target.shape
-    d_row, d_node = (0, 0) if draft is None else _prob_strides("draft", draft, target.shape)
+    d_st = (0, 0) if draft is None else _prob_strides("draft", draft, target.shape)
     _check_i32("parent", parent, (rows, nodes))
     _check_i32("tokens", tokens, (rows, nodes))
     if not isinstance(u, torch.Tensor) or u.dtype != torch.float32 or not u.is_cuda:
@@ -529,40 +551,92 @@ def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length
                          ("token", token, (rows,))):
         if t is not None:
             _check_i32(n_, t, shape)
-    dev = target.device
-    _same_device(dev, draft=draft, parent=parent, tokens=tokens, u=u, n=n, path=path, length=length, token=token)
-    with _on_device(dev):
-        made = []
-        if path is None or length is None or token is None:
-            # one allocation for the outputs that are not given
-            buf = torch.empty(rows * (nodes + 2), dtype=torch.int32, device=dev)
-            made.append(buf)
-            length = buf[:rows] if length is None else length
-            token = buf[rows:2 * rows] if token is None else token
-            path = buf[2 * rows:].view(rows, nodes) if path is None else path
-        if ws is None:
-            ws = _workspace(256, dev, None)
-            made.append(ws)
-        else:
-            _workspace(0, dev, ws)
-        st = _VerifyStrides(t_row, t_node, d_row, d_node)
-        rc = lib().wa_tree_verify(target.data_ptr(), None if draft is None else draft.data_ptr(), parent.data_ptr(),
-                                  tokens.data_ptr(), None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes,
-                                  vocab, ctypes.byref(st), path.data_ptr(), length.data_ptr(), token.data_ptr(),
-                                  ws.data_ptr(), _ws_bytes(ws), _stream_handle(stream))
-        _keep_for(stream, *made)
+    _same_device(target.device, draft=draft, parent=parent, tokens=tokens, u=u, n=n, path=path, length=length,
+                 token=token)
+    return _VerifyStrides(*t_st, *d_st)
+
+
+def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length=None, token=None, ws=None,
+                stream=None):
+    """Which drafted tokens the target keeps, and the token after them: speculative sampling over a tree.
+
+    target fp32 [rows, nodes, vocab]: the target's probabilities after each node; draft: those that the
+    node's children were drawn from, or None where they were not drawn.  parent, tokens int32
+    [rows, nodes]; node 0 is the last sampled token.  u fp32 [rows, nodes] in [0, 1): u[:, c] tests node
+    c, u[:, 0] samples the last token.  n int32 [rows] or None: nodes in use.  Returns (path int32
+    [rows, nodes], length int32 [rows], token int32 [rows]): the kept nodes in order, then -1; how many;
+    the token sampled after them (-1: no nodes, or a distribution without mass)."""
+    try:
+        rows, nodes, vocab = shape = target.shape
+        per, dev = (rows, nodes), target.get_device()
+        plain = (target.dtype is _F32 and dev >= 0 and target.is_contiguous() and parent.dtype is _I32
+                 and tokens.dtype is _I32 and u.dtype is _F32 and parent.shape == per and tokens.shape == per
+                 and u.shape == per and parent.get_device() == dev and tokens.get_device() == dev
+                 and u.get_device() == dev and parent.is_contiguous() and tokens.is_contiguous()
+                 and u.is_contiguous() and path is None and length is None and token is None
+                 and (draft is None or (draft.dtype is _F32 and draft.shape == shape and draft.get_device() == dev
+                                        and draft.is_contiguous()))
+                 and (n is None or (n.dtype is _I32 and n.shape == (rows,) and n.get_device() == dev
+                                    and n.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    st = None
+    if not plain:
+        st = _verify_check(target, parent, tokens, u, draft, n, path, length, token)
+        rows, nodes, vocab = target.shape
+        dev = target.get_device()
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return tree_verify(target, parent, tokens, u, draft, n, path, length, token, ws, stream)
+    made, device = [], target.device
+    if path is None:
+        path = torch.empty((rows, nodes), dtype=_I32, device=device)
+        made.append(path)
+    if length is None:
+        length = torch.empty(rows, dtype=_I32, device=device)
+        made.append(length)
+    if token is None:
+        token = torch.empty(rows, dtype=_I32, device=device)
+        made.append(token)
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=device)
+        made.append(ws)
+    else:
+        _workspace(0, device, ws)
+    rc = lib().wa_tree_verify(
+        target.data_ptr(), None if draft is None else draft.data_ptr(), parent.data_ptr(), tokens.data_ptr(),
+        None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes, vocab, st, path.data_ptr(), length.data_ptr(),
+        token.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if stream is not None:
+        _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_verify")
     return path, length, token
 
 
-def _layer_list(name: str, ts):
-    ts = [ts] if isinstance(ts, torch.Tensor) else list(ts)
-    for t in ts:
-        _check_bf16(name, t)
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [rows, nodes or ring, hkv, d]")
-    return ts
+def _commit_layers(kt, vt, kr, vr):
+    """(rows, nodes, hkv, d, k strides, v strides) of the layers' tensors; raises where they disagree."""
+    L = len(kt)
+    if not (0 < L <= WA_COMMIT_MAX_LAYERS) or not len(vt) == len(kr) == len(vr) == L:
+        raise ValueError(f"between 1 and {WA_COMMIT_MAX_LAYERS} layers, the same number of each tensor")
+    for name, ts in (("k_tree", kt), ("v_tree", vt), ("k_ring", kr), ("v_ring", vr)):
+        for t in ts:
+            _check_bf16(name, t)
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [rows, nodes or ring, hkv, d]")
+    shape = kt[0].shape
+    rows, nodes, hkv, d = shape
+    k_st, v_st = _node_strides("k_tree", kt[0], d), _node_strides("v_tree", vt[0], d)
+    for l in range(L):
+        if kt[l].shape != shape or vt[l].shape != shape:
+            raise ValueError(f"k_tree and v_tree must have one shape, {tuple(shape)}")
+        if l and (_node_strides("k_tree", kt[l], d) != k_st or _node_strides("v_tree", vt[l], d) != v_st):
+            raise ValueError("the layers' trees must have the same strides")
+        want = (rows, kr[l].shape[1], hkv, d)
+        if kr[l].shape != want or vr[l].shape != want or not kr[l].is_contiguous() or not vr[l].is_contiguous():
+            raise ValueError(f"k_ring and v_ring must be contiguous [rows, ring, hkv, d] = {want}")
+        _same_device(kt[0].device, k_tree=kt[l], v_tree=vt[l], k_ring=kr[l], v_ring=vr[l])
+    return rows, nodes, hkv, d, k_st, v_st
 
 
 def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stream=None):
@@ -574,43 +648,59 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     strides).  path int32 [rows, most], length and pos int32 [rows], as tree_verify returned and
     tree_decode took them; afterwards the row's last position is pos + length.  Returns the
     workspace, whose status status() reads."""
-    kt, vt, kr, vr = (_layer_list(*x) for x in (("k_tree", k_tree), ("v_tree", v_tree), ("k_ring", k_ring),
-                                               ("v_ring", v_ring)))
-    L = len(kt)
-    if not (0 < L <= WA_COMMIT_MAX_LAYERS) or not len(vt) == len(kr) == len(vr) == L:
-        raise ValueError(f"between 1 and {WA_COMMIT_MAX_LAYERS} layers, the same number of each tensor")
-    shape = kt[0].shape
-    rows, nodes, hkv, d = shape
-    k_st, v_st = _node_strides("k_tree", kt[0], d), _node_strides("v_tree", vt[0], d)
-    dev = kt[0].device
-    for l in range(L):
-        if kt[l].shape != shape or vt[l].shape != shape:
-            raise ValueError(f"k_tree and v_tree must have one shape, {tuple(shape)}")
-        if l and (_node_strides("k_tree", kt[l], d) != k_st or _node_strides("v_tree", vt[l], d) != v_st):
-            raise ValueError("the layers' trees must have the same strides")
-        want = (rows, kr[l].shape[1], hkv, d)
-        if kr[l].shape != want or vr[l].shape != want or not kr[l].is_contiguous() or not vr[l].is_contiguous():
-            raise ValueError(f"k_ring and v_ring must be contiguous [rows, ring, hkv, d] = {want}")
-        _same_device(dev, k_tree=kt[l], v_tree=vt[l], k_ring=kr[l], v_ring=vr[l])
-    if not isinstance(path, torch.Tensor) or path.dim() != 2:
-        raise ValueError("path must be [rows, most]")
-    most = path.shape[1]
-    _check_i32("path", path, (rows, most))
-    _check_i32("length", length, (rows,))
-    _check_i32("pos", pos, (rows,))
-    _same_device(dev, path=path, length=length, pos=pos)
-    with _on_device(dev):
-        made = None
-        if ws is None:
-            made = ws = _workspace(256, dev, None)
-        else:
-            _workspace(0, dev, ws)
-        ptrs = [(_P * L)(*[t.data_ptr() for t in ts]) for ts in (kt, vt, kr, vr)]
-        rings = (_I * L)(*[t.shape[1] for t in kr])
+    kt, vt, kr, vr = [[x] if isinstance(x, torch.Tensor) else list(x) for x in (k_tree, v_tree, k_ring, v_ring)]
+    L, st, ptrs, rings = len(kt), None, [], []
+    try:
+        shape, dev = kt[0].shape, kt[0].get_device()
+        rows, nodes, hkv, d = shape
+        most = path.shape[1]
+        plain = (0 < L <= WA_COMMIT_MAX_LAYERS and len(vt) == len(kr) == len(vr) == L and dev >= 0
+                 and path.dtype is _I32 and length.dtype is _I32 and pos.dtype is _I32 and path.shape == (rows, most)
+                 and length.shape == (rows,) and pos.shape == (rows,) and path.get_device() == dev
+                 and length.get_device() == dev and pos.get_device() == dev and path.is_contiguous()
+                 and length.is_contiguous() and pos.is_contiguous())
+        for t in kt + vt:
+            plain = plain and (t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous())
+            ptrs.append(t.data_ptr())
+        for k, v in zip(kr, vr):
+            size = k.shape
+            plain = plain and (k.dtype is _BF16 and v.dtype is _BF16 and v.shape == size and size[0] == rows
+                               and size[2] == hkv and size[3] == d and k.get_device() == dev
+                               and v.get_device() == dev and k.is_contiguous() and v.is_contiguous())
+            rings.append(size[1])
+    except (AttributeError, IndexError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        rows, nodes, hkv, d, k_st, v_st = _commit_layers(kt, vt, kr, vr)
         st = _TreeStrides(0, 0, *k_st, *v_st, 0, 0)
-        rc = lib().wa_tree_commit(L, *ptrs, rings, rows, nodes, hkv, d, ctypes.byref(st), path.data_ptr(), most,
-                                  length.data_ptr(), pos.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
-                                  _stream_handle(stream))
+        if not isinstance(path, torch.Tensor) or path.dim() != 2:
+            raise ValueError("path must be [rows, most]")
+        most = path.shape[1]
+        _check_i32("path", path, (rows, most))
+        _check_i32("length", length, (rows,))
+        _check_i32("pos", pos, (rows,))
+        dev = kt[0].get_device()
+        _same_device(kt[0].device, path=path, length=length, pos=pos)
+        ptrs = [t.data_ptr() for t in kt + vt]
+        rings = [t.shape[1] for t in kr]
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws, stream)
+    made = []
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=kt[0].device)
+        made.append(ws)
+    else:
+        _workspace(0, kt[0].device, ws)
+    # the host arrays of pointers, one after the other
+    ptrs += [t.data_ptr() for t in kr + vr]
+    table = (ctypes.c_uint64 * (4 * L))(*ptrs)
+    at = ctypes.addressof(table)
+    rc = lib().wa_tree_commit(
+        L, at, at + 8 * L, at + 16 * L, at + 24 * L, (_I * L)(*rings), rows, nodes, hkv, d, st, path.data_ptr(), most,
+        length.data_ptr(), pos.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if stream is not None:
         _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_commit")

@@ -53,11 +53,12 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 // maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
 constexpr float kTreeLazy = 32.0f;
 
-// Keys a span: enough spans that hkv key heads of one row occupy the card, in powers of two.
+// Keys a span: enough spans that hkv key heads of one row make about kSpanUnits units, in powers of two.
+constexpr int kSpanMin = 2048, kSpanMax = 4096, kSpanUnits = 128;
 __host__ __device__ inline int tree_span(int64_t keys, int hkv) {
-    const int64_t want = keys * hkv / 128;
-    int len = 512;
-    while (len < 2048 && 2 * len <= want) len *= 2;
+    const int64_t want = keys * hkv / kSpanUnits;
+    int len = kSpanMin;
+    while (len < kSpanMax && 2 * len <= want) len *= 2;
     return len;
 }
 
@@ -1024,9 +1025,9 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
         const int len = tree_span(win, hkv);
         pl.spans = win > 1 ? (win - 2 + len - 1) / len + 1 : 1;
     } else {
-        for (int len = 512; len <= 2048; len *= 2) {
+        for (int len = kSpanMin; len <= kSpanMax; len *= 2) {
             // the most keys with this span
-            int64_t keys = len == 2048 ? ring : (256LL * len + hkv - 1) / hkv - 1;
+            int64_t keys = len == kSpanMax ? ring : (2LL * kSpanUnits * len + hkv - 1) / hkv - 1;
             keys = keys < ring ? keys : ring;
             const int spans = static_cast<int>((keys + len - 1) / len);
             pl.spans = spans > pl.spans ? spans : pl.spans;
