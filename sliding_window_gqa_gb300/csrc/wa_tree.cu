@@ -54,7 +54,7 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 constexpr float kTreeLazy = 32.0f;
 
 // Keys a span: enough spans that hkv key heads of one row make about kSpanUnits units, in powers of two.
-constexpr int kSpanMin = 2048, kSpanMax = 4096, kSpanUnits = 128;
+constexpr int kSpanMin = 512, kSpanMax = 4096, kSpanUnits = 32;
 __host__ __device__ inline int tree_span(int64_t keys, int hkv) {
     const int64_t want = keys * hkv / kSpanUnits;
     int len = kSpanMin;
@@ -776,6 +776,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
     }
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -863,9 +864,11 @@ __device__ void tree_rerun(const TreeArgs& a, TreeRerun& sm, int r, int node, in
     if (t < 64) orow[t] = f64_to_bf16_rn(acc / l);
 }
 
+constexpr int kMergeSpans = 4;
+
 // o = sum_s a_s O_s / sum_s a_s l_s over a row's spans in order, a_s = 2^(m_s - M).  A block takes 32 query
 // rows (lanes) and 64 dims (8 a warp) of a tile, reads the partial results in the order they were stored
-// (512 bytes a warp and load, four spans in flight), and turns them round in shared memory for the output.
+// (512 bytes a warp and load, kMergeSpans spans in flight), and turns them round in shared memory for the output.
 // A row with a value that is not finite is computed again in float64.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_l,
@@ -889,31 +892,50 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restric
     const int first = qd * 32 / G;                        // the block's first node
     if (first >= npt || node0 + first >= n) return;
     if (t < 32) bad[t] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");    // the partial results
     __syncthreads();
     const int64_t rec = unit0 * lanes + qd * 32 + lane;
     const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + blockIdx.y * 16 + warp * 2) * 32 + lane;
     const int64_t ostep = static_cast<int64_t>(quarters) * (D / 4) * 32;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int s = 0; s < count; ++s) M = fmaxf(M, part_m[rec + static_cast<int64_t>(s) * lanes]);
-    float num[8];
+    float M = -INFINITY, den = 0.f, num[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) num[e] = 0.f;
-    float den = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < count; ++s) {
-        const float4 l4 = part_l[rec + static_cast<int64_t>(s) * lanes];
-        const float4 o0 = po[s * ostep], o1 = po[s * ostep + 32];
-        const float w = exp2f(part_m[rec + static_cast<int64_t>(s) * lanes] - M);
-        den = fmaf(w, (l4.x + l4.y) + (l4.z + l4.w), den);
-        num[0] = fmaf(w, o0.x, num[0]);
-        num[1] = fmaf(w, o0.y, num[1]);
-        num[2] = fmaf(w, o0.z, num[2]);
-        num[3] = fmaf(w, o0.w, num[3]);
-        num[4] = fmaf(w, o1.x, num[4]);
-        num[5] = fmaf(w, o1.y, num[5]);
-        num[6] = fmaf(w, o1.z, num[6]);
-        num[7] = fmaf(w, o1.w, num[7]);
+    // kMergeSpans at a time, all their loads in flight together, folded in order
+    for (int s0 = 0; s0 < count; s0 += kMergeSpans) {
+        float m[kMergeSpans];
+        float4 l[kMergeSpans], o[kMergeSpans][2];
+#pragma unroll
+        for (int i = 0; i < kMergeSpans; ++i) {
+            if (s0 + i >= count) break;
+            const int64_t at = rec + static_cast<int64_t>(s0 + i) * lanes;
+            m[i] = part_m[at];
+            l[i] = part_l[at];
+            o[i][0] = po[(s0 + i) * ostep];
+            o[i][1] = po[(s0 + i) * ostep + 32];
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kMergeSpans; ++i)
+            if (s0 + i < count) top = fmaxf(top, m[i]);
+        const float keep = (M == -INFINITY) ? 0.f : exp2f(M - top);
+        M = top;
+        den *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) num[e] *= keep;
+#pragma unroll
+        for (int i = 0; i < kMergeSpans; ++i) {
+            if (s0 + i >= count) break;
+            const float w = exp2f(m[i] - M);
+            den = fmaf(w, (l[i].x + l[i].y) + (l[i].z + l[i].w), den);
+            num[0] = fmaf(w, o[i][0].x, num[0]);
+            num[1] = fmaf(w, o[i][0].y, num[1]);
+            num[2] = fmaf(w, o[i][0].z, num[2]);
+            num[3] = fmaf(w, o[i][0].w, num[3]);
+            num[4] = fmaf(w, o[i][1].x, num[4]);
+            num[5] = fmaf(w, o[i][1].y, num[5]);
+            num[6] = fmaf(w, o[i][1].z, num[6]);
+            num[7] = fmaf(w, o[i][1].w, num[7]);
+        }
     }
     const int row = qd * 32 + lane;
     const bool live = row / G < npt && node0 + row / G < n;
@@ -1002,7 +1024,19 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
-    tree_merge_kernel<D><<<mgrid, 256, 0, s>>>(t.part_o, t.part_l, t.part_m, a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
+    // launched while the units still run: its blocks wait for them on the GPU
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = mgrid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, const_cast<const float4*>(t.part_o), const_cast<const float4*>(t.part_l),
+                           const_cast<const float*>(t.part_m), a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 

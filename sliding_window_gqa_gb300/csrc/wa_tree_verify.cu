@@ -9,34 +9,39 @@
 // The vocabulary's rows are read only where a child was dropped (for the sum of W) and
 // where the walk ends (for the token's place in the running sum of W).
 //
-// What bounds it: a chain of dependent passes over one node's rows, each of vocab / 8
-// tokens a CTA, and at many rows the reads of those rows.  So
-//   - a cluster of 8 CTAs serves a row, each a slice of the vocabulary, each warp a
-//     stretch of the slice; totals meet in the cluster's shared memory;
+// What bounds it: a chain of dependent passes over one node's rows, each a trip to memory
+// and a meeting of the CTAs, and at many rows the reads of those rows.  So
+//   - the vocabulary is cut into 8 slices of 16 stretches; a cluster of 8, 4, 2 or 1 CTAs
+//     serves a row (as many as leave all rows' CTAs on the card at once), each with its share
+//     of the slices, each warp one stretch of a slice; the slices' sums meet in the cluster's
+//     shared memory;
 //   - the tests' probabilities of all nodes are fetched at once at the start;
 //   - a pass leaves the sums of every stretch, so the search for the token reads one
-//     stretch again and not the rows.
+//     stretch again and not the rows, and a token taken out (no draft probabilities) only
+//     changes its own stretch.
 //
-// Sums carry hi + lo fp32 pairs (about 46 bits: the fp64 pipe of this GPU would take ten
-// times as long), so that a border of the running sum that 64 bits would place on one
+// All arithmetic is in hi + lo fp32 pairs (about 46 bits), two tokens an instruction where it
+// counts: the fp64 pipe of this GPU has a fiftieth of the fp32 rate.  So a border of the running sum that 64 bits would place on one
 // side of a random number stays on that side but for numbers within about 2^-40 of it.
-// Their order is fixed by vocab alone.
+// Their order is fixed by vocab alone, whatever the cluster.
 #include <cuda_runtime.h>
 
 #include "wa_internal.h"
+#include "wa_ptx.cuh"
 
 namespace wa {
 
 namespace {
 
-constexpr int kCluster = 8;
+constexpr int kSlices = 8;
 constexpr int kVerWarps = 16;
 constexpr int kVerThreads = kVerWarps * 32;
 
-__device__ __forceinline__ float prob(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+// x in [0, 1]; NaN is 0.
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
 // An unevaluated sum hi + lo of two fp32 values.
-struct Pair {
+struct __align__(8) Pair {
     float hi, lo;
 };
 
@@ -55,10 +60,64 @@ __device__ __forceinline__ Pair weight_pair(float p, float q, float sh, float sl
     const float d = __fsub_rn(p, m);
     const float b = __fsub_rn(d, p);
     const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(m, b)), me);
-    return __fadd_rn(d, e) > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
+    const float h = __fadd_rn(d, e);
+    return h > 0.f ? Pair{h, __fsub_rn(e, __fsub_rn(h, d))} : Pair{0.f, 0.f};
 }
 
-__device__ __forceinline__ double pair_f64(const Pair& s) { return static_cast<double>(s.hi) + static_cast<double>(s.lo); }
+// Two tokens at a time: packed fp32 operations (one instruction each, rounded as the plain ones).
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two mul2(const Two& x, const Two& y) {
+    Two r;
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 r, p, q;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.a), "=f"(r.b) : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+    return r;
+}
+__device__ __forceinline__ Two add2(const Two& x, const Two& y) {
+    Two r;
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 r, p, q;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.a), "=f"(r.b) : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+    return r;
+}
+__device__ __forceinline__ Two fma2(const Two& x, const Two& y, const Two& z) {
+    Two r;
+    asm("{\n\t.reg .b64 p, q, c, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, p, q, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.a), "=f"(r.b) : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b), "f"(z.a), "f"(z.b));
+    return r;
+}
+__device__ __forceinline__ Two sub2(const Two& x, const Two& y) { return fma2(y, Two{-1.f, -1.f}, x); }
+
+// pair_add of two sums side by side.
+__device__ __forceinline__ void pair_add2(Two& hi, Two& lo, const Two& d, const Two& e) {
+    const Two t = add2(hi, d), b = sub2(t, hi);
+    lo = add2(lo, add2(add2(sub2(hi, sub2(t, b)), sub2(d, b)), e));
+    hi = t;
+}
+
+// weight_pair of two tokens, not brought to the form |e| << |d|; ns* = -S.
+__device__ __forceinline__ void weight_pair2(const Two& p, const Two& q, const Two& sh, const Two& nsh, const Two& nsl, Two& d, Two& e) {
+    const Two m = mul2(sh, q);
+    const Two nme = fma2(nsl, q, fma2(nsh, q, m));                 // m - S q
+    d = sub2(p, m);
+    const Two b = sub2(d, p);
+    e = add2(sub2(sub2(p, sub2(d, b)), add2(m, b)), nme);
+    const Two h = add2(d, e);
+    if (!(h.a > 0.f)) d.a = e.a = 0.f;
+    if (!(h.b > 0.f)) d.b = e.b = 0.f;
+}
+
+// Whether a < b: equal hi parts are told apart by lo.
+__device__ __forceinline__ bool pair_less(const Pair& a, const Pair& b) {
+    return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) < 0.f;
+}
+
+// x * s
+__device__ __forceinline__ Pair pair_scale(float x, const Pair& s) {
+    const float h = __fmul_rn(x, s.hi);
+    return Pair{h, __fmaf_rn(x, s.lo, __fmaf_rn(x, s.hi, -h))};
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -66,75 +125,90 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// Store to the same shared-memory variable of CTA `rank` of the cluster, counted on that CTA's mbarrier.
+__device__ __forceinline__ void st_cluster_pair(Pair* p, uint64_t* bar, uint32_t rank, const Pair& x) {
+    uint32_t a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    const uint64_t v = static_cast<uint64_t>(__float_as_uint(x.hi)) | static_cast<uint64_t>(__float_as_uint(x.lo)) << 32;
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" :: "r"(a), "l"(v), "r"(b) : "memory");
 }
 
-// Store to the same shared-memory variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void st_cluster_f64(double* p, uint32_t rank, double x) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(a), "d"(x) : "memory");
-}
-
-__device__ __forceinline__ double warp_scan_f64(double x, int lane) {
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
+        const float hi = __shfl_up_sync(0xFFFFFFFFu, x.hi, o), lo = __shfl_up_sync(0xFFFFFFFFu, x.lo, o);
+        if (lane >= o) pair_add(x, hi, lo);
     }
     return x;
+}
+
+__device__ __forceinline__ Pair warp_get(const Pair& x, int lane) {
+    return Pair{__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
 // The first of the warp's parts whose running sum (`before` + the inclusive scan) passes `want`, else the
 // last part with any weight (rounding can leave the sum just below); -1 if there is none.  `before`
 // becomes the sum before that part.
-__device__ __forceinline__ int pick(double part, double want, double& before, int lane) {
-    const double run = before + warp_scan_f64(part, lane);
-    const uint32_t some = __ballot_sync(0xFFFFFFFFu, part > 0.0);
-    const uint32_t hit = some & __ballot_sync(0xFFFFFFFFu, run > want);
+__device__ __forceinline__ int pick(const Pair& part, const Pair& want, Pair& before, int lane) {
+    Pair run = warp_scan(part, lane);
+    pair_add(run, before.hi, before.lo);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, part.hi > 0.f);
+    const uint32_t hit = some & __ballot_sync(0xFFFFFFFFu, pair_less(want, run));
     if (some == 0u) return -1;
     const int at = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-    const double prev = __shfl_sync(0xFFFFFFFFu, run, max(at - 1, 0));
+    const Pair prev = warp_get(run, max(at - 1, 0));
     if (at > 0) before = prev;
     return at;
 }
 
 struct VerifyShared {
-    double seg[kVerWarps];              // sums of this CTA's stretches
-    double tot[2][kCluster];            // the CTAs' sums, by pass parity
-    double sub[kVerWarps];
-    double mass, want, before;
+    uint64_t bar[2];                    // the slices' sums of a pass have arrived, by pass parity
+    Pair seg[kSlices][kVerWarps];       // sums of the stretches of this CTA's slices
+    Pair tot[2][kSlices];               // the slices' sums, by pass parity
+    Pair sub[kVerWarps];
+    Pair mass, want, before;
     float pp[WA_TREE_MAX_NODES], qq[WA_TREE_MAX_NODES];   // a node's token at its parent: target, draft
     float u[WA_TREE_MAX_NODES];
     int par[WA_TREE_MAX_NODES], tok[WA_TREE_MAX_NODES];
-    uint32_t kids[WA_TREE_MAX_NODES][4];
+    uint2 kids[WA_TREE_MAX_NODES][2];   // a node's children as bits
     int gone[WA_TREE_MAX_NODES];        // tokens out of W (no draft probabilities)
-    int ngone, node, len, cmd, stretch;
-    float sh, sl;                       // S
+    // the walk, as warp 0 left it
+    Pair s, S_prev;
+    unsigned long long kids_lo, kids_hi;      // the current node's children that are still to test
+    int summed;                               // the stretches' sums are those of the current W
+    int asked;                                // a child was dropped and the sum is awaited
+    int ngone, node, len, cmd, slice, stretch;
+    int changed;                        // no draft: the one token that left W since the sums, or -1
+    Pair S;
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs a) {
+template <int CL, bool DRAFT>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    constexpr int PER = kSlices / CL;           // slices of a CTA
     __shared__ VerifyShared sm;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int rank = static_cast<int>(cluster_rank());
-    const int r = blockIdx.x / kCluster;
+    const int r = blockIdx.x / CL;
     const int raw_n = a.n ? a.n[r] : a.nodes;
     const int n = min(max(raw_n, 0), a.nodes);
-    const bool draft = a.draft != nullptr;
-    // shared memory of another CTA may be written once that CTA runs: the wait is before the walk
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const float* trow = a.target + r * a.t_row;
-    const float* drow = draft ? a.draft + r * a.d_row : nullptr;
+    const float* drow = DRAFT ? a.draft + r * a.d_row : nullptr;
     int32_t* path = a.path + static_cast<int64_t>(r) * a.nodes;
 
     // the tree, and every test's probabilities
     if (t < WA_TREE_MAX_NODES) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sm.kids[t][w] = 0u;
+        sm.kids[t][0] = sm.kids[t][1] = make_uint2(0u, 0u);
     }
-    if (t == 0) sm.ngone = 0;
+    if (t == 0) {
+        sm.ngone = 0;
+        mbar_init(smem_u32(&sm.bar[0]), 1);
+        mbar_init(smem_u32(&sm.bar[1]), 1);
+        fence_mbar_init();
+    }
     __syncthreads();
+    // another CTA's shared memory may be written once that CTA has come here: the wait is before the walk
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (t < n) {
         const int64_t at = static_cast<int64_t>(r) * a.nodes + t;
         const int raw = a.parent[at], par = tree_parent(raw, t);
@@ -146,184 +220,226 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerThreads, 
         sm.u[t] = a.u[at];
         if (par >= 0 && in) {
             sm.pp[t] = prob(trow[par * a.t_node + tok]);
-            sm.qq[t] = draft ? prob(drow[par * a.d_node + tok]) : 1.f;
-            atomicOr(&sm.kids[par][t >> 5], 1u << (t & 31));
+            sm.qq[t] = DRAFT ? prob(drow[par * a.d_node + tok]) : 1.f;
+            atomicOr(reinterpret_cast<uint32_t*>(&sm.kids[par][0]) + (t >> 5), 1u << (t & 31));
         }
     }
     if (t == 0 && rank == 0 && raw_n != n) atomicOr(&a.hdr->status, WA_STATUS_BAD_TREE);
     __syncthreads();
 
-    // this warp's stretch of the vocabulary
-    const int slice = (a.vocab + kCluster - 1) / kCluster;
-    const int len_w = ((slice + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;
-    const int c0 = min(a.vocab, rank * slice), c1 = min(a.vocab, c0 + slice);
-    const int x0 = min(c1, c0 + warp * len_w), x1 = min(c1, x0 + len_w);
+    // stretch `st` of slice `sl` is [stretch_at(sl, st), stretch_at(sl, st + 1))
+    const int slice = ((a.vocab + kSlices - 1) / kSlices + 3) / 4 * 4;
+    const int len_w = ((slice + kVerWarps - 1) / kVerWarps + 127) / 128 * 128;
+    auto stretch_at = [&](int sl, int st) { return min(a.vocab, min((sl + 1) * slice, sl * slice + st * len_w)); };   // multiples of 4, or vocab
 
-    // the weight of token x at the current node
-    auto weight_at = [&](const float* p, const float* q, int x, float sh, float sl, int ngone) -> Pair {
-        if (draft) return weight_pair(prob(p[x]), prob(q[x]), sh, sl);
+    // a token's weight at the current node, given its probabilities
+    auto weight = [&](float px, float qx, int x, const Pair& S, int ngone) -> Pair {
+        if (DRAFT) return weight_pair(prob(px), prob(qx), S.hi, S.lo);
         for (int k = 0; k < ngone; ++k)
             if (sm.gone[k] == x) return Pair{0.f, 0.f};
-        return Pair{prob(p[x]), 0.f};
+        return Pair{prob(px), 0.f};
     };
-    // The sum of W over [b0, b1) by one warp, in lane 0.
-    auto stretch_sum = [&](const float* p, const float* q, int b0, int b1, float sh, float sl) -> double {
+    // The sum of W over [b0, b1), b0 a multiple of 4, by one warp, the same in every lane.  A lane takes four
+    // tokens in a row, 16 bytes where the rows lie on such borders (the order of the sum is the same where
+    // they do not), and kLoads such groups at a time.
+    constexpr int kLoads = DRAFT ? 4 : 8;
+    auto stretch_sum = [&](const float* p, const float* q, int b0, int b1, const Pair& S) -> Pair {
         int ngone = 0;
-        if (!draft) {       // only the stretches that hold a token taken out look for it
+        if (!DRAFT) {       // only the stretches that hold a token taken out look for it
             bool here = false;
             for (int k = lane; k < sm.ngone; k += 32) here |= sm.gone[k] >= b0 && sm.gone[k] < b1;
             ngone = __any_sync(0xFFFFFFFFu, here) ? sm.ngone : 0;
         }
-        Pair s{0.f, 0.f};
-        int x = b0 + lane;
-        if (draft) {
-            for (; x + 7 * 32 < b1; x += 8 * 32) {
-                float pv[8], qv[8];
+        const bool vec_p = (reinterpret_cast<uintptr_t>(p) & 15u) == 0, vec_q = (reinterpret_cast<uintptr_t>(q) & 15u) == 0;
+        auto load = [&](const float* row, int x, bool vec) -> float4 {
+            if (vec && x + 4 <= b1) return __ldg(reinterpret_cast<const float4*>(row + x));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < b1) v.x = __ldg(row + x);
+            if (x + 1 < b1) v.y = __ldg(row + x + 1);
+            if (x + 2 < b1) v.z = __ldg(row + x + 2);
+            if (x + 3 < b1) v.w = __ldg(row + x + 3);
+            return v;
+        };
+        Two hi{0.f, 0.f}, lo{0.f, 0.f};
+        const Two sh{S.hi, S.hi}, nsh{-S.hi, -S.hi}, nsl{-S.lo, -S.lo};
+        for (int x = b0 + 4 * lane; x - 4 * lane < b1; x += kLoads * 128) {
+            float4 pv[kLoads], qv[kLoads];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    pv[e] = __ldg(p + x + e * 32);
-                    qv[e] = __ldg(q + x + e * 32);
-                }
+            for (int e = 0; e < kLoads; ++e) {
+                pv[e] = load(p, x + e * 128, vec_p);
+                if (DRAFT) qv[e] = load(q, x + e * 128, vec_q);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const Pair w = weight_pair(prob(pv[e]), prob(qv[e]), sh, sl);
-                    pair_add(s, w.hi, w.lo);
+            for (int e = 0; e < kLoads; ++e) {
+                Two p0{prob(pv[e].x), prob(pv[e].y)}, p1{prob(pv[e].z), prob(pv[e].w)};
+                if (DRAFT) {
+                    const Two q0{prob(qv[e].x), prob(qv[e].y)}, q1{prob(qv[e].z), prob(qv[e].w)};
+                    Two d, err;
+                    weight_pair2(p0, q0, sh, nsh, nsl, d, err);
+                    pair_add2(hi, lo, d, err);
+                    weight_pair2(p1, q1, sh, nsh, nsl, d, err);
+                    pair_add2(hi, lo, d, err);
+                } else {
+                    for (int k = 0; k < ngone; ++k) {
+                        const int at = sm.gone[k] - (x + e * 128);
+                        if (at == 0) p0.a = 0.f;
+                        if (at == 1) p0.b = 0.f;
+                        if (at == 2) p1.a = 0.f;
+                        if (at == 3) p1.b = 0.f;
+                    }
+                    pair_add2(hi, lo, p0, Two{0.f, 0.f});
+                    pair_add2(hi, lo, p1, Two{0.f, 0.f});
                 }
             }
-        } else if (ngone == 0) {
-            for (; x + 7 * 32 < b1; x += 8 * 32) {
-                float pv[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pv[e] = __ldg(p + x + e * 32);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pair_add(s, prob(pv[e]), 0.f);
-            }
         }
-        for (; x < b1; x += 32) {
-            const Pair w = weight_at(p, q, x, sh, sl, ngone);
-            pair_add(s, w.hi, w.lo);
-        }
+        Pair s{hi.a, lo.a};
+        pair_add(s, hi.b, lo.b);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
             const float hi = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o), lo = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
             pair_add(s, hi, lo);
         }
-        return pair_f64(s);
+        return s;
     };
 
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    // Warp 0 of every CTA walks alike; the whole cluster sums W when it asks for it.
+    // Warp 0 of every CTA walks alike; the whole cluster sums W when it asks for it.  Between two passes the
+    // walk's state lies in shared memory (as registers it was spilled).
     int pass = 0;
-    int len = 0, node = 0;
-    double S = 0.0, s = 1.0;
-    uint32_t kids[4] = {0u, 0u, 0u, 0u};
-    bool summed = false;      // the stretches' sums are those of the current W
-    double S_prev = 0.0;
-    bool asked = false;       // a child was dropped and the sum is awaited
-    if (warp == 0 && n > 0) {
-        len = 1;
-        if (rank == 0 && lane == 0) path[0] = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) kids[w] = sm.kids[0][w];
+    if (t == 0) {
+        sm.kids_lo = sm.kids[0][0].x | static_cast<unsigned long long>(sm.kids[0][0].y) << 32;
+        sm.kids_hi = sm.kids[0][1].x | static_cast<unsigned long long>(sm.kids[0][1].y) << 32;
+        sm.S = sm.S_prev = Pair{0.f, 0.f};
+        sm.s = Pair{1.f, 0.f};
+        sm.summed = sm.asked = 0;
+        sm.node = 0;
+        sm.len = n > 0;
+        if (rank == 0 && n > 0) path[0] = 0;
     }
     while (n > 0) {
         if (warp == 0) {
-            bool pass_wanted = false;
-            if (asked) {
-                asked = false;
-                const double left = sm.mass;
-                if (left > 0.0) {
+            __syncwarp();
+            Pair S = sm.S, s = sm.s, S_prev = sm.S_prev;
+            unsigned long long kids_lo = sm.kids_lo, kids_hi = sm.kids_hi;
+            int node = sm.node, len = sm.len, ngone = sm.ngone;
+            bool summed = sm.summed != 0, asked = false;
+            int changed = -1;         // the only token whose weight has changed since the last sums, or -1
+            if (sm.asked) {
+                const Pair left = sm.mass;
+                summed = left.hi > 0.f;
+                if (summed) {
                     s = left;
-                    summed = true;
                 } else {               // nothing left: W stays as it was
                     S = S_prev;
-                    if (!draft && lane == 0) --sm.ngone;
-                    summed = false;
+                    if (!DRAFT) --ngone;
                 }
-                __syncwarp();
             }
-            for (;;) {
-                int c = -1;
-#pragma unroll
-                for (int w = 3; w >= 0; --w)
-                    if (kids[w]) c = 32 * w + __ffs(kids[w]) - 1;
-                if (c < 0) break;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (w == (c >> 5)) kids[w] &= kids[w] - 1u;
-                const double pp = sm.pp[c], qq = sm.qq[c];
-                double W = pp - S * qq;
-                if (!draft) {
-                    W = pp;
-                    for (int k = 0; k < sm.ngone; ++k)
-                        if (sm.gone[k] == sm.tok[c]) W = 0.0;
+            while (kids_lo | kids_hi) {
+                int c;
+                if (kids_lo) {
+                    c = __ffsll(kids_lo) - 1;
+                    kids_lo &= kids_lo - 1;
+                } else {
+                    c = 63 + __ffsll(kids_hi);
+                    kids_hi &= kids_hi - 1;
                 }
-                if (static_cast<double>(sm.u[c]) * qq * s < fmax(W, 0.0)) {
+                const float pp = sm.pp[c], qq = sm.qq[c], uc = sm.u[c], uq = __fmul_rn(uc, qq);
+                const int x = sm.tok[c];
+                Pair W{pp, 0.f};
+                if (DRAFT) {
+                    W = weight_pair(pp, qq, S.hi, S.lo);
+                } else {
+                    for (int k = 0; k < ngone; ++k)
+                        if (sm.gone[k] == x) W.hi = 0.f;
+                }
+                Pair bar = pair_scale(uq, s);                 // u q s, with u q's own rounding error
+                bar.lo = __fmaf_rn(__fmaf_rn(uc, qq, -uq), s.hi, bar.lo);
+                if (pair_less(bar, W)) {
                     node = c;
                     if (rank == 0 && lane == 0) path[len] = c;
                     ++len;
-                    S = 0.0;
-                    s = 1.0;
+                    S = Pair{0.f, 0.f};
+                    s = Pair{1.f, 0.f};
                     summed = false;
-                    __syncwarp();
-                    if (lane == 0) sm.ngone = 0;
-                    __syncwarp();
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) kids[w] = sm.kids[c][w];
+                    ngone = 0;
+                    kids_lo = sm.kids[c][0].x | static_cast<unsigned long long>(sm.kids[c][0].y) << 32;
+                    kids_hi = sm.kids[c][1].x | static_cast<unsigned long long>(sm.kids[c][1].y) << 32;
                     continue;
                 }
                 S_prev = S;
-                if (draft) S += s;
-                __syncwarp();
-                if (!draft && lane == 0) sm.gone[sm.ngone++] = sm.tok[c];
-                __syncwarp();
-                asked = pass_wanted = true;
+                if (DRAFT) {
+                    pair_add(S, s.hi, s.lo);
+                } else {
+                    changed = summed ? x : -1;
+                    if (lane == 0) sm.gone[ngone] = x;
+                    ++ngone;
+                }
+                asked = true;
                 break;
             }
             if (lane == 0) {
-                sm.cmd = pass_wanted ? 1 : summed ? 0 : 2;     // 0: sample; 1: sum and go on; 2: sum, then sample
+                sm.S = S;
+                sm.s = s;
+                sm.S_prev = S_prev;
+                sm.kids_lo = kids_lo;
+                sm.kids_hi = kids_hi;
                 sm.node = node;
-                sm.sh = static_cast<float>(S);
-                sm.sl = static_cast<float>(S - static_cast<double>(static_cast<float>(S)));
+                sm.len = len;
+                sm.ngone = ngone;
+                sm.summed = summed;
+                sm.asked = asked;
+                sm.changed = asked ? changed : -1;
+                sm.cmd = asked ? 1 : summed ? 0 : 2;     // 0: sample; 1: sum and go on; 2: sum, then sample
             }
         }
         __syncthreads();
         const int cmd = sm.cmd;
-        const float sh = sm.sh, sl = sm.sl;
+        const Pair Sn = sm.S;
         const float* p = trow + sm.node * a.t_node;
-        const float* q = draft ? drow + sm.node * a.d_node : nullptr;
+        const float* q = DRAFT ? drow + sm.node * a.d_node : nullptr;
         if (cmd != 0) {
-            const double x = stretch_sum(p, q, x0, x1, sh, sl);
-            if (lane == 0) sm.seg[warp] = x;
-            __syncthreads();
-            double* tot = sm.tot[pass & 1];
-            if (warp == 0) {
-                const double run = warp_scan_f64(lane < kVerWarps ? sm.seg[lane] : 0.0, lane);
-                const double all = __shfl_sync(0xFFFFFFFFu, run, 31);
-                if (lane < kCluster) st_cluster_f64(&tot[rank], lane, all);
+            const int only = sm.changed;
+#pragma unroll 1
+            for (int k = 0; k < PER; ++k) {
+                const int sl_ = rank * PER + k, b0 = stretch_at(sl_, warp), b1 = stretch_at(sl_, warp + 1);
+                if (only >= 0 && (only < b0 || only >= b1)) continue;
+                const Pair x = stretch_sum(p, q, b0, b1, Sn);
+                if (lane == 0) sm.seg[k][warp] = x;
             }
-            cluster_sync_all();
+            __syncthreads();
+            Pair* tot = sm.tot[pass & 1];
+            uint64_t* bar = &sm.bar[pass & 1];
+            if (warp < PER) {
+                const Pair all = warp_get(warp_scan(lane < kVerWarps ? sm.seg[warp][lane] : Pair{0.f, 0.f}, lane), 31);
+                if (lane < CL) st_cluster_pair(&tot[rank * PER + warp], bar, lane, all);
+            }
+            // Only warp 0 waits for the other CTAs' sums (a cluster barrier of all warps lets the last one go
+            // 4,000 cycles after the first).  A pass's barrier and buffer are used again two passes on, when
+            // every CTA has sent, and so has read this pass's.
             if (warp == 0) {
-                const double run = warp_scan_f64(lane < kCluster ? tot[lane] : 0.0, lane);
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(bar), kSlices * sizeof(Pair));
+                const bool ok = warp_wait(smem_u32(bar), (pass >> 1) & 1, &a.hdr->status);
+                const Pair run = warp_scan(ok && lane < kSlices ? tot[lane] : Pair{0.f, 0.f}, lane);
                 if (lane == 31) sm.mass = run;
+                __syncwarp();
             }
             ++pass;
-            __syncthreads();
         }
         if (cmd == 1) continue;
 
         // the token: the CTA, its stretch, a sixteenth of the stretch, the place
         if (warp == 0) {
-            const double want = static_cast<double>(sm.u[0]) * sm.mass;
-            double before = 0.0;
-            const int at = pick(lane < kCluster ? sm.tot[(pass - 1) & 1][lane] : 0.0, want, before, lane);
+            const Pair want = pair_scale(sm.u[0], sm.mass);
+            Pair before{0.f, 0.f};
+            const int at = pick(lane < kSlices ? sm.tot[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, want, before, lane);
             int st = -1;
-            if (at == rank) st = pick(lane < kVerWarps ? sm.seg[lane] : 0.0, want, before, lane);
+            if (at >= 0 && at / PER == rank) st = pick(lane < kVerWarps ? sm.seg[at % PER][lane] : Pair{0.f, 0.f}, want, before, lane);
             if (at < 0 && rank == 0 && lane == 0) {
                 a.token[r] = -1;
                 atomicOr(&a.hdr->status, WA_STATUS_NO_MASS);
             }
             if (lane == 0) {
+                sm.slice = at;
                 sm.stretch = st;
                 sm.want = want;
                 sm.before = before;
@@ -331,46 +447,62 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kVerThreads, 
         }
         __syncthreads();
         if (sm.stretch < 0) break;
-        const int b0 = min(c1, c0 + sm.stretch * len_w), b1 = min(c1, b0 + len_w);
-        const int part = ((b1 - b0 + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;
+        const int b0 = stretch_at(sm.slice, sm.stretch), b1 = stretch_at(sm.slice, sm.stretch + 1);
+        const int part = ((b1 - b0 + kVerWarps - 1) / kVerWarps + 31) / 32 * 32;   // a multiple of 4
         const int y0 = min(b1, b0 + warp * part), y1 = min(b1, y0 + part);
-        const double x = stretch_sum(p, q, y0, y1, sh, sl);
+        const Pair x = stretch_sum(p, q, y0, y1, Sn);
         if (lane == 0) sm.sub[warp] = x;
         __syncthreads();
         if (warp == 0) {
-            const double want = sm.want;
-            double before = sm.before;
-            const int k = max(pick(lane < kVerWarps ? sm.sub[lane] : 0.0, want, before, lane), 0);
+            const Pair want = sm.want;
+            Pair before = sm.before;
+            const int k = max(pick(lane < kVerWarps ? sm.sub[lane] : Pair{0.f, 0.f}, want, before, lane), 0);
             const int z0 = min(b1, b0 + k * part), z1 = min(b1, z0 + part);
             int found = -1, last = -1;
             for (int z = z0; z < z1 && found < 0; z += 32) {
-                const double w = z + lane < z1 ? pair_f64(weight_at(p, q, z + lane, sh, sl, sm.ngone)) : 0.0;
-                const double run = before + warp_scan_f64(w, lane);
-                const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.0);
-                const uint32_t hit = some & __ballot_sync(0xFFFFFFFFu, run > want);
+                const bool in = z + lane < z1;
+                const Pair w = in ? weight(p[z + lane], DRAFT ? q[z + lane] : 0.f, z + lane, Sn, sm.ngone) : Pair{0.f, 0.f};
+                Pair run = warp_scan(w, lane);
+                pair_add(run, before.hi, before.lo);
+                const uint32_t some = __ballot_sync(0xFFFFFFFFu, w.hi > 0.f);
+                const uint32_t hit = some & __ballot_sync(0xFFFFFFFFu, pair_less(want, run));
                 if (hit) found = z + __ffs(hit) - 1;
                 if (some) last = z + 31 - __clz(some);
-                before = __shfl_sync(0xFFFFFFFFu, run, 31);
+                before = warp_get(run, 31);
             }
             if (lane == 0) a.token[r] = found >= 0 ? found : last;
         }
         break;
     }
     if (warp == 0 && rank == 0) {
-        for (int i = len + lane; i < a.nodes; i += 32) path[i] = -1;
+        __syncwarp();
+        for (int i = sm.len + lane; i < a.nodes; i += 32) path[i] = -1;
         if (lane == 0) {
-            a.length[r] = len;
+            a.length[r] = sm.len;
             if (n == 0) a.token[r] = -1;
         }
     }
-    // no CTA leaves while another one may still write to its shared memory: every such write is
-    // followed by a cluster barrier that both pass
+    // No CTA leaves while another one may still write to its shared memory: it has waited for all the
+    // writes of every pass.
+}
+
+template <int CL>
+void launch_cl(const VerifyArgs& a, cudaStream_t s) {
+    if (a.draft) verify_kernel<CL, true><<<a.rows * CL, kVerThreads, 0, s>>>(a);
+    else verify_kernel<CL, false><<<a.rows * CL, kVerThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
-    verify_kernel<<<a.rows * kCluster, kVerThreads, 0, s>>>(a);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    const int most = 2 * sms / a.rows;      // two CTAs an SM
+    if (most >= 8) launch_cl<8>(a, s);
+    else if (most >= 4) launch_cl<4>(a, s);
+    else if (most >= 2) launch_cl<2>(a, s);
+    else launch_cl<1>(a, s);
     return cudaGetLastError();
 }
 

@@ -199,3 +199,18 @@ def test_kept_tokens_are_distributed_as_the_target(wa):
     after = torch.where(length > 1, kept, token)
     share = torch.bincount(after, minlength=V).double() / rows
     assert (share - p.double()).abs().max() < 4 * np.sqrt(0.25 / rows)
+
+
+def test_result_does_not_depend_on_the_rows_around_it(wa):
+    """The same row alone, among 40, 80 and 400: clusters of 8, 4, 2 and 1 CTAs sum in one order."""
+    c = make(8, 12, 30011, seed=21, kind="bushy", noise=1.5)
+    for draft in (c["draft"], None):
+        want = [t.tolist() for t in wa.tree_verify(c["target"], c["parent"], c["tokens"], c["u"], draft=draft)]
+        for times in (5, 10, 50):
+            rep = lambda t: t.repeat(times, *[1] * (t.dim() - 1))   # noqa: E731
+            got = wa.tree_verify(rep(c["target"]), rep(c["parent"]), rep(c["tokens"]), rep(c["u"]),
+                                 draft=None if draft is None else rep(draft))
+            assert [t.tolist() for t in got] == [w * times for w in want]
+        one = wa.tree_verify(*[c[x][3:4].contiguous() for x in ("target", "parent", "tokens", "u")],
+                             draft=None if draft is None else draft[3:4].contiguous())
+        assert [t.tolist() for t in one] == [w[3:4] for w in want]
