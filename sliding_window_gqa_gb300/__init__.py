@@ -11,7 +11,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 import re
 
@@ -27,6 +27,7 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libwa.so")
+_BIND_PATH = os.path.join(_HERE, "_build", "wa_bind.so")
 _HEADER = os.path.join(os.path.dirname(_HERE), "include", "wa.h")
 
 
@@ -79,6 +80,7 @@ class _VerifyStrides(ctypes.Structure):
 
 
 _lib = None
+_bind = None      # the short way to the drafted-token calls (csrc/wa_bind.cpp)
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 
@@ -89,9 +91,9 @@ def lib_path() -> str:
 
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
-    global _lib
+    global _lib, _bind
     if _lib is None:
-        if not os.path.exists(_LIB_PATH):
+        if not os.path.exists(_LIB_PATH) or not os.path.exists(_BIND_PATH):
             raise RuntimeError(
                 f"{_LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(_LIB_PATH)
@@ -129,6 +131,9 @@ def lib() -> ctypes.CDLL:
         L.wa_strerror.restype = ctypes.c_char_p
         L.wa_version.argtypes = []
         L.wa_version.restype = ctypes.c_int
+        spec = importlib.util.spec_from_file_location("wa_bind", _BIND_PATH)
+        _bind = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_bind)
         _lib = L
     return _lib
 
@@ -383,13 +388,9 @@ def prep_append(src, pos, q_out, k_ring, v_ring=None, mode: str = "rmsnorm", q_s
 
 # Drafted tokens.  These calls run on their inputs' device, whichever is current, and on `stream` or
 # that device's current stream; what they allocate is kept for that stream.  A drafted step makes one
-# call a layer, of a few microseconds on the GPU for a single sequence, so each call asks everything
-# that has to hold of its tensors in one expression, and a call that does not pass goes through checks
-# that say what is wrong (or accept what the short form does not cover, as strided nodes).
-
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
+# call a layer, of a few microseconds on the GPU for a single sequence, so the ordinary call (contiguous
+# tensors on the current device and stream) is checked and made by the extension module; it returns None
+# for any other one, which goes through the checks here.
 
 def _keep_for(stream, made) -> None:
     """Memory allocated on the current stream and used on another is not reused before that one is done."""
@@ -398,9 +399,15 @@ def _keep_for(stream, made) -> None:
             t.record_stream(stream)
 
 
-@functools.lru_cache(maxsize=256)
-def _tree_ws_bytes(*sizes) -> int:
-    return max(256, int(lib().wa_tree_decode_ws_bytes(*sizes)))
+def _stream_on(index: int, stream) -> int:
+    return int((torch.cuda.current_stream(index) if stream is None else stream).cuda_stream)
+
+
+def _result(got, what: str):
+    """What the extension module returned: tensors, or a code that is raised."""
+    if isinstance(got, int):
+        raise WAError(got, what)
+    return got
 
 
 def _check_i32(name: str, t, shape) -> None:
@@ -475,45 +482,29 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
     for one that follows the cache; n int32 [rows] or None: nodes in use.  A node sees the cache, its
     ancestors and itself, as far as the window reaches back.  Returns out [rows, nodes, hq, d] bf16,
     whose nodes past n are not written.  ``ws``: a reused uint8 CUDA buffer of tree_decode_ws_bytes(...)."""
-    try:
-        rows, nodes, hq, d = q.shape
-        _, ring, hkv, _ = cache = k_ring.shape
-        tree, dev = (rows, nodes, hkv, d), q.get_device()
-        plain = (q.dtype is _BF16 and k_ring.dtype is _BF16 and v_ring.dtype is _BF16 and k_tree.dtype is _BF16
-                 and v_tree.dtype is _BF16 and cache[0] == rows and cache[3] == d and v_ring.shape == cache
-                 and k_tree.shape == tree and v_tree.shape == tree and pos.dtype is _I32 and parent.dtype is _I32
-                 and pos.shape == (rows,) and parent.shape == (rows, nodes) and k_ring.get_device() == dev
-                 and v_ring.get_device() == dev and k_tree.get_device() == dev and v_tree.get_device() == dev
-                 and pos.get_device() == dev and parent.get_device() == dev and dev >= 0 and q.is_contiguous()
-                 and k_ring.is_contiguous() and v_ring.is_contiguous() and k_tree.is_contiguous()
-                 and v_tree.is_contiguous() and pos.is_contiguous() and parent.is_contiguous()
-                 and (n is None or (n.dtype is _I32 and n.shape == (rows,) and n.get_device() == dev
-                                    and n.is_contiguous()))
-                 and (out is None or (out.dtype is _BF16 and out.shape == q.shape and out.get_device() == dev
-                                      and out.is_contiguous())))
-    except (AttributeError, TypeError, ValueError):
-        plain = False
-    st = None
-    if not plain:
-        (rows, nodes, hq, hkv, d, ring), st = _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out)
-        dev = q.get_device()
-    if dev != torch.cuda.current_device():
+    if stream is None:
+        lib()
+        got = _bind.tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws)
+        if got is not None:
+            return _result(got, "wa_tree_decode")
+    (rows, nodes, hq, hkv, d, ring), st = _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out)
+    dev = q.device
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws, stream)
     made = []
     if out is None:
-        out = torch.empty((rows, nodes, hq, d), dtype=_BF16, device=q.device)
+        out = torch.empty((rows, nodes, hq, d), dtype=torch.bfloat16, device=dev)
         made.append(out)
     if ws is None:
-        nbytes = _tree_ws_bytes(rows, nodes, hq, hkv, d, win, ring)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = _workspace(tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring), dev, None)
         made.append(ws)
     else:
-        nbytes = _ws_bytes(_workspace(0, q.device, ws))
+        _workspace(0, dev, ws)
     rc = lib().wa_tree_decode(
         q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), pos.data_ptr(),
-        parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring, scale, st,
-        out.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, int(win), ring, float(scale),
+        ctypes.byref(st), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
     if stream is not None:
         _keep_for(stream, made)
     if rc != WA_OK:
@@ -566,47 +557,35 @@ def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length
     c, u[:, 0] samples the last token.  n int32 [rows] or None: nodes in use.  Returns (path int32
     [rows, nodes], length int32 [rows], token int32 [rows]): the kept nodes in order, then -1; how many;
     the token sampled after them (-1: no nodes, or a distribution without mass)."""
-    try:
-        rows, nodes, vocab = shape = target.shape
-        per, dev = (rows, nodes), target.get_device()
-        plain = (target.dtype is _F32 and dev >= 0 and target.is_contiguous() and parent.dtype is _I32
-                 and tokens.dtype is _I32 and u.dtype is _F32 and parent.shape == per and tokens.shape == per
-                 and u.shape == per and parent.get_device() == dev and tokens.get_device() == dev
-                 and u.get_device() == dev and parent.is_contiguous() and tokens.is_contiguous()
-                 and u.is_contiguous() and path is None and length is None and token is None
-                 and (draft is None or (draft.dtype is _F32 and draft.shape == shape and draft.get_device() == dev
-                                        and draft.is_contiguous()))
-                 and (n is None or (n.dtype is _I32 and n.shape == (rows,) and n.get_device() == dev
-                                    and n.is_contiguous())))
-    except (AttributeError, TypeError, ValueError):
-        plain = False
-    st = None
-    if not plain:
-        st = _verify_check(target, parent, tokens, u, draft, n, path, length, token)
-        rows, nodes, vocab = target.shape
-        dev = target.get_device()
-    if dev != torch.cuda.current_device():
+    if stream is None and path is None and length is None and token is None:
+        lib()
+        got = _bind.tree_verify(target, parent, tokens, u, draft, n, ws)
+        if got is not None:
+            return _result(got, "wa_tree_verify")
+    st = _verify_check(target, parent, tokens, u, draft, n, path, length, token)
+    rows, nodes, vocab = target.shape
+    dev = target.device
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return tree_verify(target, parent, tokens, u, draft, n, path, length, token, ws, stream)
-    made, device = [], target.device
-    if path is None:
-        path = torch.empty((rows, nodes), dtype=_I32, device=device)
-        made.append(path)
-    if length is None:
-        length = torch.empty(rows, dtype=_I32, device=device)
-        made.append(length)
-    if token is None:
-        token = torch.empty(rows, dtype=_I32, device=device)
-        made.append(token)
+    made = []
+
+    def ints(t, *shape):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=dev)
+            made.append(t)
+        return t
+
+    path, length, token = ints(path, rows, nodes), ints(length, rows), ints(token, rows)
     if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=device)
+        ws = _workspace(256, dev, None)
         made.append(ws)
     else:
-        _workspace(0, device, ws)
+        _workspace(0, dev, ws)
     rc = lib().wa_tree_verify(
         target.data_ptr(), None if draft is None else draft.data_ptr(), parent.data_ptr(), tokens.data_ptr(),
-        None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes, vocab, st, path.data_ptr(), length.data_ptr(),
-        token.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes, vocab, ctypes.byref(st), path.data_ptr(),
+        length.data_ptr(), token.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
     if stream is not None:
         _keep_for(stream, made)
     if rc != WA_OK:
@@ -648,58 +627,36 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     strides).  path int32 [rows, most], length and pos int32 [rows], as tree_verify returned and
     tree_decode took them; afterwards the row's last position is pos + length.  Returns the
     workspace, whose status status() reads."""
-    kt, vt, kr, vr = [[x] if isinstance(x, torch.Tensor) else list(x) for x in (k_tree, v_tree, k_ring, v_ring)]
-    L, st, ptrs, rings = len(kt), None, [], []
-    try:
-        shape, dev = kt[0].shape, kt[0].get_device()
-        rows, nodes, hkv, d = shape
-        most = path.shape[1]
-        plain = (0 < L <= WA_COMMIT_MAX_LAYERS and len(vt) == len(kr) == len(vr) == L and dev >= 0
-                 and path.dtype is _I32 and length.dtype is _I32 and pos.dtype is _I32 and path.shape == (rows, most)
-                 and length.shape == (rows,) and pos.shape == (rows,) and path.get_device() == dev
-                 and length.get_device() == dev and pos.get_device() == dev and path.is_contiguous()
-                 and length.is_contiguous() and pos.is_contiguous())
-        for t in kt + vt:
-            plain = plain and (t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous())
-            ptrs.append(t.data_ptr())
-        for k, v in zip(kr, vr):
-            size = k.shape
-            plain = plain and (k.dtype is _BF16 and v.dtype is _BF16 and v.shape == size and size[0] == rows
-                               and size[2] == hkv and size[3] == d and k.get_device() == dev
-                               and v.get_device() == dev and k.is_contiguous() and v.is_contiguous())
-            rings.append(size[1])
-    except (AttributeError, IndexError, TypeError, ValueError):
-        plain = False
-    if not plain:
-        rows, nodes, hkv, d, k_st, v_st = _commit_layers(kt, vt, kr, vr)
-        st = _TreeStrides(0, 0, *k_st, *v_st, 0, 0)
-        if not isinstance(path, torch.Tensor) or path.dim() != 2:
-            raise ValueError("path must be [rows, most]")
-        most = path.shape[1]
-        _check_i32("path", path, (rows, most))
-        _check_i32("length", length, (rows,))
-        _check_i32("pos", pos, (rows,))
-        dev = kt[0].get_device()
-        _same_device(kt[0].device, path=path, length=length, pos=pos)
-        ptrs = [t.data_ptr() for t in kt + vt]
-        rings = [t.shape[1] for t in kr]
-    if dev != torch.cuda.current_device():
+    if stream is None:
+        lib()
+        got = _bind.tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws)
+        if got is not None:
+            return _result(got, "wa_tree_commit")
+    kt, vt, kr, vr = ([x] if isinstance(x, torch.Tensor) else list(x) for x in (k_tree, v_tree, k_ring, v_ring))
+    rows, nodes, hkv, d, k_st, v_st = _commit_layers(kt, vt, kr, vr)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be [rows, most]")
+    most = path.shape[1]
+    _check_i32("path", path, (rows, most))
+    _check_i32("length", length, (rows,))
+    _check_i32("pos", pos, (rows,))
+    dev = kt[0].device
+    _same_device(dev, path=path, length=length, pos=pos)
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws, stream)
+            return tree_commit(kt, vt, kr, vr, path, length, pos, ws, stream)
     made = []
     if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=kt[0].device)
+        ws = _workspace(256, dev, None)
         made.append(ws)
     else:
-        _workspace(0, kt[0].device, ws)
-    # the host arrays of pointers, one after the other
-    ptrs += [t.data_ptr() for t in kr + vr]
-    table = (ctypes.c_uint64 * (4 * L))(*ptrs)
-    at = ctypes.addressof(table)
+        _workspace(0, dev, ws)
+    L = len(kt)
+    ptrs = [(_P * L)(*[t.data_ptr() for t in ts]) for ts in (kt, vt, kr, vr)]
     rc = lib().wa_tree_commit(
-        L, at, at + 8 * L, at + 16 * L, at + 24 * L, (_I * L)(*rings), rows, nodes, hkv, d, st, path.data_ptr(), most,
-        length.data_ptr(), pos.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        L, *ptrs, (_I * L)(*[t.shape[1] for t in kr]), rows, nodes, hkv, d,
+        ctypes.byref(_TreeStrides(0, 0, *k_st, *v_st, 0, 0)), path.data_ptr(), most, length.data_ptr(), pos.data_ptr(),
+        ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
     if stream is not None:
         _keep_for(stream, made)
     if rc != WA_OK:

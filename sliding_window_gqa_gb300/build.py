@@ -1,4 +1,5 @@
-"""Builds libwa.so in-tree with nvcc for sm_103a (one translation unit per job, in parallel)."""
+"""Builds libwa.so in-tree with nvcc for sm_103a (one translation unit per job, in parallel), and the binding's
+wa_bind.so, a Python extension against the installed PyTorch's headers, with g++ at the same time."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,12 +7,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libwa.so")
+BIND = os.path.join(OUT, "wa_bind.so")
 SOURCES = ["wa_api.cu", "wa_decode.cu", "wa_prompt.cu", "wa_rerun.cu", "wa_static.cu", "wa_decode_tc.cu", "wa_prep.cu", "wa_prompt_sparse.cu",
            "wa_tree.cu", "wa_tree_verify.cu", "wa_tree_commit.cu"]
 
@@ -36,18 +39,44 @@ def _compile(nvcc: str, src: str, extra) -> str:
     return obj
 
 
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_bind(nvcc: str, torch_dir: str) -> str:
+    import torch
+    obj = os.path.join(OUT, "wa_bind.o")
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+           os.path.join(ROOT, "include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{p}" for p in inc], "-c",
+          os.path.join(CSRC, "wa_bind.cpp"), "-o", obj], "g++ on wa_bind.cpp")
+    return obj
+
+
 def build(verbose: bool = False, extra=()) -> str:
-    """Compile every source and link libwa.so; returns the library path."""
+    """Compile every source and link libwa.so and wa_bind.so; returns libwa.so's path."""
+    import torch
     os.makedirs(OUT, exist_ok=True)
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = os.path.dirname(torch.__file__)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(_compile_bind, nvcc, torch_dir)
         objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra)), SOURCES))
+        bind_obj = bind.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BIND + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT, "-l:libwa.so", "-L" + os.path.join(torch_dir, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of wa_bind.so")
+    os.replace(tmp, BIND)
     if verbose:
         print("built", LIB)
     return LIB

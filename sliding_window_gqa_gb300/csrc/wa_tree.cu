@@ -8,7 +8,7 @@
 // Split.  A key head's G query heads of 128 / G nodes make a tile of up to 128
 // query rows (tensor-memory lane m = node m / G, head m % G), so K and V are read
 // once for all of them.  A row's keys are cut into spans at multiples of
-// tree_span() keys, which depends on the row's own key count and hkv; the tree's
+// tree_span() keys, which depends on the row's own key count and hq; the tree's
 // own keys are one more 128-key tile of the last span.  A unit of work is (row,
 // key head, query tile, span); it leaves (m, l, O) in fp32 and tree_merge_kernel
 // joins a row's spans in order.  Nothing in a unit depends on the other rows, so
@@ -53,10 +53,13 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 // maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
 constexpr float kTreeLazy = 32.0f;
 
-// Keys a span: enough spans that hkv key heads of one row make about kSpanUnits units, in powers of two.
-constexpr int kSpanMin = 512, kSpanMax = 4096, kSpanUnits = 32;
-__host__ __device__ inline int tree_span(int64_t keys, int hkv) {
-    const int64_t want = keys * hkv / kSpanUnits;
+// Keys a span, a power of two: keys * hq / 128.  Short spans put a single row's keys on more SMs, long ones
+// leave fewer partial results and fewer ends of the pipeline: one row of 32,000 keys, 16/8 heads, runs 75, 56
+// and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads, 795, 617 and 549 us with 512,
+// 1,024 and 2,048; one row of a 1,024-key window 25 us with 512 and 33 with 1,024, 64 of them 332 and 309.
+constexpr int kSpanMin = 512, kSpanMax = 4096, kSpanUnits = 128;
+__host__ __device__ inline int tree_span(int64_t keys, int hq) {
+    const int64_t want = keys * hq / kSpanUnits;
     int len = kSpanMin;
     while (len < kSpanMax && 2 * len <= want) len *= 2;
     return len;
@@ -65,10 +68,10 @@ __host__ __device__ inline int tree_span(int64_t keys, int hkv) {
 // Spans of a row at (clamped) position p, given its first visible key: at least one, for the tree.
 __host__ __device__ inline int tree_first(int p, int win) { return win > 0 && p + 2 - win > 0 ? p + 2 - win : 0; }
 __host__ __device__ inline int64_t tree_keys(int p, int win) { return win > 0 ? win : static_cast<int64_t>(p) + 1; }
-__host__ __device__ inline int tree_spans(int p, int win, int hkv) {
+__host__ __device__ inline int tree_spans(int p, int win, int hq) {
     const int lo = tree_first(p, win);
     if (lo > p) return 1;
-    const int len = tree_span(tree_keys(p, win), hkv);
+    const int len = tree_span(tree_keys(p, win), hq);
     return p / len - lo / len + 1;
 }
 
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     x.nt = 1;
                     return;
                 }
-                const int len = tree_span(tree_keys(x.p, p.win), p.hkv);
+                const int len = tree_span(tree_keys(x.p, p.win), p.hq);
                 const int sp = x.lo / len + x.span;
                 if (sp > x.p / len) continue;
                 const int kb = max(x.lo, sp * len), ke = min(x.p, sp * len + (len - 1));
@@ -888,7 +891,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restric
     const int g = k % a.hkv, r = k / a.hkv;
     const int G = a.hq / a.hkv, node0 = mt * npt;
     const int n = min(a.n ? __ldg(a.n + r) : a.nodes, a.nodes);
-    const int count = tree_spans(tree_pos(__ldg(a.pos + r), a.win, a.ring), a.win, a.hkv);
+    const int count = tree_spans(tree_pos(__ldg(a.pos + r), a.win, a.ring), a.win, a.hq);
     const int first = qd * 32 / G;                        // the block's first node
     if (first >= npt || node0 + first >= n) return;
     if (t < 32) bad[t] = 0;
@@ -1056,12 +1059,12 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
     pl.spans = 1;
     if (win > 0) {
         // win - 1 keys from any position touch at most this many spans
-        const int len = tree_span(win, hkv);
+        const int len = tree_span(win, hq);
         pl.spans = win > 1 ? (win - 2 + len - 1) / len + 1 : 1;
     } else {
         for (int len = kSpanMin; len <= kSpanMax; len *= 2) {
             // the most keys with this span
-            int64_t keys = len == kSpanMax ? ring : (2LL * kSpanUnits * len + hkv - 1) / hkv - 1;
+            int64_t keys = len == kSpanMax ? ring : (2LL * kSpanUnits * len + hq - 1) / hq - 1;
             keys = keys < ring ? keys : ring;
             const int spans = static_cast<int>((keys + len - 1) / len);
             pl.spans = spans > pl.spans ? spans : pl.spans;

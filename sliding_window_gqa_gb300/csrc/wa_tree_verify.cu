@@ -12,7 +12,7 @@
 // What bounds it: a chain of dependent passes over one node's rows, each a trip to memory
 // and a meeting of the CTAs, and at many rows the reads of those rows.  So
 //   - the vocabulary is cut into 8 slices of 16 stretches; a cluster of 8, 4, 2 or 1 CTAs
-//     serves a row (as many as leave all rows' CTAs on the card at once), each with its share
+//     serves a row (fewer for many rows), each with its share
 //     of the slices, each warp one stretch of a slice; the slices' sums meet in the cluster's
 //     shared memory;
 //   - the tests' probabilities of all nodes are fetched at once at the start;
@@ -498,7 +498,7 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    const int most = 2 * sms / a.rows;      // two CTAs an SM
+    const int most = 4 * sms / a.rows;      // up to two waves of two CTAs an SM: rows end after one to five passes
     if (most >= 8) launch_cl<8>(a, s);
     else if (most >= 4) launch_cl<4>(a, s);
     else if (most >= 2) launch_cl<2>(a, s);
