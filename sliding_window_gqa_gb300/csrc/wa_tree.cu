@@ -21,7 +21,7 @@
 //               K2, V1, ...), on across unit ends.  A tile that wraps around the end of a
 //               ring is loaded in 8-row boxes; the one 8-row piece that holds the wrap
 //               itself is copied by the warp.
-//   warp 1      allocates tensor memory; lane 0 issues S(t + 1) = Q K^T and
+//   warp 1      allocates tensor memory; one lane issues S(t + 1) = Q K^T and
 //               O += P(t) V (two bf16 parts of P), commits free the slots.
 //   warp 2      zeroes V rows that no node of the row sees (stale ring slots, nodes
 //               past n), so that they never meet a zero probability as 0 * inf.
@@ -146,15 +146,39 @@ struct TreeCfg {
     static_assert(s_col(1) + kTile <= TMEM_COLS, "tensor memory budget");
 };
 
-// The load order is K(0), then for each tile t: K(t + 1) if there is one, V(t).  Operand index of K(t)
-// and V(t) in it (HV loads each).
-__device__ __forceinline__ int op_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
+// The load order is K(0), then for each tile t: K(t + 1) if there is one, V(t).  Operand index of V(t) in
+// it (HV loads each).
 __device__ __forceinline__ int op_v(int t, bool last_of_all) { return last_of_all ? 2 * t + 1 : 2 * t + 2; }
 
 // Its inverse: operand o is K or V of tile t, where K loads have begun for `tiles` tiles.
 __device__ __forceinline__ void load_at(int o, int tiles, int& t, bool& is_v) {
     is_v = o > 0 && ((o & 1) == 0 || o == 2 * tiles - 1);
     t = o == 0 ? 0 : is_v ? (o == 2 * tiles - 1 ? tiles - 1 : o / 2 - 1) : (o + 1) / 2;
+}
+
+// One tcgen05.mma with its operands in the form the issue needs: descriptors as two 32-bit halves of which
+// only the low one (the address) changes, and the accumulate flag as an immediate.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);      // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+        :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(kDescHi));
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(kDescHi));
+}
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // fp32 values as integers of the same order (NaN aside), and -inf in that order.
@@ -189,6 +213,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < C::NBAR; ++i) {
             int count = 1;
             if (i >= C::B_PHALF && i < C::B_PFULL) count = 16;             // the softmax warps
@@ -216,13 +241,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         x.r = e[0]; x.g = e[1] & 0xFFFF; x.node0 = e[1] >> 16; x.span = e[2]; x.t0 = e[3];
         x.nring = e[4] & 0xFFFFFF; x.nt = x.nring + (e[4] >> 24); x.p = e[5]; x.n = e[6]; x.lo = e[7];
     };
-    auto take_unit = [&](int U, TreeUnit& x, bool whole) -> bool {
-        const uint32_t ph = static_cast<uint32_t>(U / kUnits) & 1u;
-        const uint32_t full = BAR(C::B_UFULL + U % kUnits);
-        if (!(whole ? warp_wait(full, ph, p.status) : mbar_wait(full, ph, p.status))) return false;
+    auto take_unit = [&](int U, TreeUnit& x) -> bool {
+        if (!warp_wait(BAR(C::B_UFULL + U % kUnits), static_cast<uint32_t>(U / kUnits) & 1u, p.status)) return false;
         read_unit(U, x);
-        if (whole) __syncwarp();
-        if (!whole || lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kUnits));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kUnits));
         return true;
     };
 
@@ -312,7 +335,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         };
         TreeUnit cur, nxt;
         int U = 0, t = 0, idx = 0, sc = -1;
-        bool ok = take_unit(U++, cur, true);
+        bool ok = take_unit(U++, cur);
         bool more = ok && cur.nt > 0;
         if (more) {
             sc = first_slot(cur);
@@ -326,7 +349,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 sn = next_slot(cur, idx, sc);
                 ok = load_k(cur, sn, t + 1);
             } else {
-                if (!(ok = take_unit(U++, nxt, true))) break;
+                if (!(ok = take_unit(U++, nxt))) break;
                 more = nxt.nt > 0;
                 if (more) {
                     sn = first_slot(nxt);
@@ -357,71 +380,94 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (one thread)
-        if (lane == 0) {
-            const uint32_t idS = idesc_bf16_f32(128, kTile, 0, 0, p.neg ? 1u : 0u);
-            constexpr uint32_t idO = idesc_bf16_f32(128, D, 0, 1);
-            const uint64_t aq = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
-            // slots in load order: K of tile t, then V of tile t - 1; V of the last tile has no K before it
-            auto issue_s = [&](int t) -> bool {
+        // ------------------------------------------------ MMA issuer: the warp together, one lane's instructions
+        // The warp walks converged over values that the compiler can see to be the same in every lane, so that
+        // addresses and descriptors live in uniform registers.  As one thread's code over 64-bit descriptors an
+        // instruction took about 130 cycles to issue beside the softmax warps, twice its time on the tensor core.
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+        const bool leader = elect_one();
+        const uint32_t idS = idesc_bf16_f32(128, kTile, 0, 0, p.neg ? 1u : 0u);
+        constexpr uint32_t idO = idesc_bf16_f32(128, D, 0, 1);
+        const uint32_t aq = desc_lo(sbase + C::OFF_Q, 16);
+        // the slots of K(t) and V(t): K0, K1, V0, K2, V1, ... with HV loads each; the last tile's V has no K before it
+        int ks = 0, vs = 2 * C::HV % C::NSLOT;
+        auto wrap = [](int x) { return x >= C::NSLOT ? x - C::NSLOT : x; };
+        auto issue_s = [&](int t) -> bool {
+            const uint32_t d = tb + C::s_col(t & 1);
 #pragma unroll
-                for (int kh = 0; kh < C::HV; ++kh) {
-                    const int s = (C::HV * op_k(t) + kh) % C::NSLOT;
-                    if (!mbar_wait(LOADBAR(C::B_KFULL, kh, t), LOADPH(t), p.status)) return false;
-                    tc_fence_after();
-                    const uint64_t bk = sdesc_sw128(SLOT(s), 16, 1024);
+            for (int kh = 0; kh < C::HV; ++kh) {
+                const int s = wrap(ks + kh);
+                if (!warp_wait(LOADBAR(C::B_KFULL, kh, t), LOADPH(t), p.status)) return false;
+                tc_fence_after();
+                const uint32_t bk = desc_lo(SLOT(s), 16);
+                if (leader) {
 #pragma unroll
                     for (int k8 = 0; k8 < 8; ++k8) {
                         const int kk = 8 * kh + k8;
-                        mma_bf16_ss(tbase + C::s_col(t & 1), aq + (((kk >> 2) * C::Q_BLOCK + (kk & 3) * 32) >> 4),
-                                    bk + (((k8 >> 2) * C::K_BLOCK + (k8 & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                        const uint32_t a = aq + (((kk >> 2) * C::Q_BLOCK + (kk & 3) * 32) >> 4);
+                        const uint32_t b = bk + (((k8 >> 2) * C::K_BLOCK + (k8 & 3) * 32) >> 4);
+                        if (kk == 0) mma_ss<false>(d, a, b, idS);
+                        else mma_ss<true>(d, a, b, idS);
                     }
                     mma_commit(BAR(C::B_FREE + s));
+                    if (kh == C::HV - 1) mma_commit(BAR(C::B_SFULL + (t & 1)));
                 }
-                mma_commit(BAR(C::B_SFULL + (t & 1)));
-                return true;
-            };
-            // keys 0..63 of the tile, then 64..127, as their P arrives
-            auto issue_pv = [&](int t, bool first, bool last_of_all) -> bool {
-                const int b = t & 1;
+                __syncwarp();
+            }
+            ks = wrap(ks + (t == 0 ? C::HV : 2 * C::HV));
+            return true;
+        };
+        // keys 0..63 of the tile, then 64..127, as their P arrives
+        auto issue_pv = [&](int t, bool first, bool last_of_all) -> bool {
+            const uint32_t pb = tb + C::s_col(t & 1);
+            const int v = last_of_all ? wrap(vs + C::NSLOT - C::HV) : vs;
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int part_v = hh * 64 / C::VKEYS;
-                    const int s = (C::HV * op_v(t, last_of_all) + part_v) % C::NSLOT;
-                    if (hh * 64 % C::VKEYS == 0 && !mbar_wait(LOADBAR(C::B_VREADY, part_v, t), LOADPH(t), p.status)) return false;
-                    if (!mbar_wait(BAR((hh ? C::B_PFULL : C::B_PHALF) + b), (t >> 1) & 1, p.status)) return false;
-                    tc_fence_after();
-                    const uint64_t v0 = sdesc_sw128(SLOT(s) + (hh * 64 % C::VKEYS) * 128, C::V_BLOCK, 1024);
+            for (int hh = 0; hh < 2; ++hh) {
+                const int part_v = hh * 64 / C::VKEYS;
+                const int s = wrap(v + part_v);
+                if (hh * 64 % C::VKEYS == 0 && !warp_wait(LOADBAR(C::B_VREADY, part_v, t), LOADPH(t), p.status)) return false;
+                if (!warp_wait(BAR((hh ? C::B_PFULL : C::B_PHALF) + (t & 1)), (t >> 1) & 1, p.status)) return false;
+                tc_fence_after();
+                const uint32_t v0 = desc_lo(SLOT(s) + (hh * 64 % C::VKEYS) * 128, C::V_BLOCK);
+                if (leader) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4)
-                            mma_bf16_ts(tbase, tbase + C::s_col(b) + hh * 64 + (k4 >> 1) * 32 + part * 16 + (k4 & 1) * 8,
-                                        v0 + ((k4 * 16 * 128) >> 4), idO, (!first || hh > 0 || part > 0 || k4 > 0) ? 1u : 0u);
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const uint32_t a = pb + hh * 64 + (k4 >> 1) * 32 + part * 16 + (k4 & 1) * 8;
+                            const uint32_t b = v0 + ((k4 * 16 * 128) >> 4);
+                            if (hh == 0 && part == 0 && k4 == 0 && first) mma_ts<false>(tb, a, b, idO);
+                            else mma_ts<true>(tb, a, b, idO);
+                        }
                     if ((hh + 1) * 64 % C::VKEYS == 0) mma_commit(BAR(C::B_FREE + s));
+                    if (hh == 1) mma_commit(BAR(C::B_PVDONE + (t & 1)));
                 }
-                mma_commit(BAR(C::B_PVDONE + b));
-                return true;
-            };
-            int t = 0;
-            bool ok = true, pending = false, pending_first = false;
-            for (int U = 0; ok; ++U) {
-                TreeUnit x;
-                if (!(ok = take_unit(U, x, false))) break;
-                // a unit's last P V goes before the next unit's S, which may still wait for its Q
-                if (pending) ok = issue_pv(t - 1, pending_first, x.nt <= 0);
-                pending = false;
-                if (!ok || x.nt <= 0) break;
-                ok = mbar_wait(BAR(C::B_QFULL), U & 1, p.status);
-                for (int idx = 0; ok && idx < x.nt; ++idx, ++t) {
-                    ok = issue_s(t);
-                    if (ok && idx == x.nt - 1) mma_commit(BAR(C::B_QFREE));
-                    if (ok && pending) ok = issue_pv(t - 1, pending_first, false);
-                    pending = true;
-                    pending_first = idx == 0;
-                }
+                __syncwarp();
             }
-            // every product issued has finished before tensor memory can be released
+            vs = wrap(vs + 2 * C::HV);
+            return true;
+        };
+        int t = 0;
+        bool ok = true, pending = false, pending_first = false;
+        for (int U = 0; ok; ++U) {
+            TreeUnit x;
+            if (!(ok = take_unit(U, x))) break;
+            const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
+            // a unit's last P V goes before the next unit's S, which may still wait for its Q
+            if (pending) ok = issue_pv(t - 1, pending_first, nt <= 0);
+            pending = false;
+            if (!ok || nt <= 0) break;
+            ok = warp_wait(BAR(C::B_QFULL), U & 1, p.status);
+            for (int idx = 0; ok && idx < nt; ++idx, ++t) {
+                ok = issue_s(t);
+                if (ok && idx == nt - 1 && leader) mma_commit(BAR(C::B_QFREE));
+                if (ok && pending) ok = issue_pv(t - 1, pending_first, false);
+                pending = true;
+                pending_first = idx == 0;
+            }
+        }
+        // every product issued has finished before tensor memory can be released
+        if (leader) {
             mma_commit(BAR(C::B_DRAIN));
             mbar_wait(BAR(C::B_DRAIN), 0, p.status);
         }
@@ -430,13 +476,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         // ------------------------------------------------ V rows that no node sees -> 0
         int t = 0;
         TreeUnit x, nxt;
-        bool ok = take_unit(0, x, true);
+        bool ok = take_unit(0, x);
         for (int U = 1; ok && x.nt > 0; ++U) {
             bool have_next = false;
             for (int idx = 0; ok && idx < x.nt; ++idx, ++t) {
                 // whether this is the very last tile decides where its V sits in the load order
                 if (idx == x.nt - 1) {
-                    if (!(ok = take_unit(U, nxt, true))) break;
+                    if (!(ok = take_unit(U, nxt))) break;
                     have_next = true;
                 }
                 const bool last_of_all = have_next && nxt.nt <= 0;
