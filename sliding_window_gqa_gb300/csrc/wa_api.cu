@@ -353,7 +353,6 @@ int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const*
     a.layers = layers; a.rows = rows; a.nodes = nodes; a.hkv = hkv; a.d = d; a.most = most;
     a.path = path; a.length = length; a.pos = pos;
     a.hdr = static_cast<wa::WsHeader*>(ws);
-    if (cudaMemsetAsync(ws, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
     if (wa::launch_commit(a, s) != cudaSuccess) return WA_ECUDA;
     return WA_OK;
 }

@@ -21,8 +21,8 @@
 //               K2, V1, ...), on across unit ends.  A tile that wraps around the end of a
 //               ring is loaded in 8-row boxes; the one 8-row piece that holds the wrap
 //               itself is copied by the warp.
-//   warp 1      allocates tensor memory; one lane issues S(t + 1) = Q K^T and
-//               O += P(t) V (two bf16 parts of P), commits free the slots.
+//   warp 1      allocates tensor memory; one lane issues S(t) = Q K^T and
+//               O += P(t - NS + 1) V (two bf16 parts of P), commits free the slots.
 //   warp 2      zeroes V rows that no node of the row sees (stale ring slots, nodes
 //               past n), so that they never meet a zero probability as 0 * inf.
 //   warp 3      takes units from a counter, publishes them through a ring of unit
@@ -123,11 +123,14 @@ struct TreeCfg {
     static constexpr int B_VFULL = B_KFULL + HV * NB;
     static constexpr int B_VREADY = B_VFULL + HV * NB;
     static constexpr int B_FREE = B_VREADY + HV * NB;         // [NSLOT]
-    static constexpr int B_SFULL = B_FREE + NSLOT;            // [tile & 1] from here
-    static constexpr int B_PVDONE = B_SFULL + 2;
-    static constexpr int B_PHALF = B_PVDONE + 2;
-    static constexpr int B_PFULL = B_PHALF + 2;
-    static constexpr int B_XCHG = B_PFULL + 2;                // [lane quarter][tile & 1]
+    // S buffers: S runs NS - 1 tiles ahead of P V, so with three (head dim 128 has the columns) the softmax
+    // finds its next tile done while the tensor core works on P V of the last two.
+    static constexpr int NS = D == 128 ? 3 : 2;
+    static constexpr int B_SFULL = B_FREE + NSLOT;            // [tile mod NS] from here
+    static constexpr int B_PVDONE = B_SFULL + NS;
+    static constexpr int B_PHALF = B_PVDONE + NS;
+    static constexpr int B_PFULL = B_PHALF + NS;
+    static constexpr int B_XCHG = B_PFULL + NS;                // [lane quarter][tile & 1]
     static constexpr int B_QFULL = B_XCHG + 8;
     static constexpr int B_QFREE = B_QFULL + 1;
     static constexpr int B_UFULL = B_QFREE + 1;               // [kUnits]
@@ -140,10 +143,10 @@ struct TreeCfg {
     static constexpr int OFF_MISC = OFF_UNIT + kUnits * UNIT_BYTES;
     static constexpr int SMEM = OFF_MISC + 16;
     static_assert(SMEM <= 232448, "shared memory budget");
-    // tensor memory: O (D columns), two S buffers; P's two parts over S
+    // tensor memory: O (D columns), NS buffers of S; P's two parts over S
     static constexpr int TMEM_COLS = 512;
     __host__ __device__ static constexpr int s_col(int b) { return D + b * kTile; }
-    static_assert(s_col(1) + kTile <= TMEM_COLS, "tensor memory budget");
+    static_assert(s_col(NS - 1) + kTile <= TMEM_COLS, "tensor memory budget");
 };
 
 // The load order is K(0), then for each tile t: K(t + 1) if there is one, V(t).  Operand index of V(t) in
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         int ks = 0, vs = 2 * C::HV % C::NSLOT;
         auto wrap = [](int x) { return x >= C::NSLOT ? x - C::NSLOT : x; };
         auto issue_s = [&](int t) -> bool {
-            const uint32_t d = tb + C::s_col(t & 1);
+            const uint32_t d = tb + C::s_col(t % C::NS);
 #pragma unroll
             for (int kh = 0; kh < C::HV; ++kh) {
                 const int s = wrap(ks + kh);
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         else mma_ss<true>(d, a, b, idS);
                     }
                     mma_commit(BAR(C::B_FREE + s));
-                    if (kh == C::HV - 1) mma_commit(BAR(C::B_SFULL + (t & 1)));
+                    if (kh == C::HV - 1) mma_commit(BAR(C::B_SFULL + t % C::NS));
                 }
                 __syncwarp();
             }
@@ -419,14 +422,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         };
         // keys 0..63 of the tile, then 64..127, as their P arrives
         auto issue_pv = [&](int t, bool first, bool last_of_all) -> bool {
-            const uint32_t pb = tb + C::s_col(t & 1);
+            const uint32_t pb = tb + C::s_col(t % C::NS);
             const int v = last_of_all ? wrap(vs + C::NSLOT - C::HV) : vs;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const int part_v = hh * 64 / C::VKEYS;
                 const int s = wrap(v + part_v);
                 if (hh * 64 % C::VKEYS == 0 && !warp_wait(LOADBAR(C::B_VREADY, part_v, t), LOADPH(t), p.status)) return false;
-                if (!warp_wait(BAR((hh ? C::B_PFULL : C::B_PHALF) + (t & 1)), (t >> 1) & 1, p.status)) return false;
+                if (!warp_wait(BAR((hh ? C::B_PFULL : C::B_PHALF) + t % C::NS), (t / C::NS) & 1, p.status)) return false;
                 tc_fence_after();
                 const uint32_t v0 = desc_lo(SLOT(s) + (hh * 64 % C::VKEYS) * 128, C::V_BLOCK);
                 if (leader) {
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                             else mma_ts<true>(tb, a, b, idO);
                         }
                     if ((hh + 1) * 64 % C::VKEYS == 0) mma_commit(BAR(C::B_FREE + s));
-                    if (hh == 1) mma_commit(BAR(C::B_PVDONE + (t & 1)));
+                    if (hh == 1) mma_commit(BAR(C::B_PVDONE + t % C::NS));
                 }
                 __syncwarp();
             }
@@ -448,23 +451,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             return true;
         };
         int t = 0;
-        bool ok = true, pending = false, pending_first = false;
+        bool ok = true;
+        int ntl = 0;                              // the last unit's tiles: P V of its last NS - 1 is still to issue
         for (int U = 0; ok; ++U) {
             TreeUnit x;
             if (!(ok = take_unit(U, x))) break;
             const int nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
-            // a unit's last P V goes before the next unit's S, which may still wait for its Q
-            if (pending) ok = issue_pv(t - 1, pending_first, nt <= 0);
-            pending = false;
+            // a unit's last P V go before the next unit's S, which may still wait for its Q
+            for (int i = min(ntl, C::NS - 1); ok && i > 0; --i) ok = issue_pv(t - i, ntl == i, nt <= 0 && i == 1);
             if (!ok || nt <= 0) break;
             ok = warp_wait(BAR(C::B_QFULL), U & 1, p.status);
             for (int idx = 0; ok && idx < nt; ++idx, ++t) {
                 ok = issue_s(t);
                 if (ok && idx == nt - 1 && leader) mma_commit(BAR(C::B_QFREE));
-                if (ok && pending) ok = issue_pv(t - 1, pending_first, false);
-                pending = true;
-                pending_first = idx == 0;
+                if (ok && idx >= C::NS - 1) ok = issue_pv(t - (C::NS - 1), idx == C::NS - 1, false);
             }
+            ntl = nt;
         }
         // every product issued has finished before tensor memory can be released
         if (leader) {
@@ -633,6 +635,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         // a unit as this thread sees it
         int t0 = 0, nring = 0, nt = 0, row_lo = 0, row_hi = 0;
         uint32_t seen = 0;                                    // tree columns [col0, col0 + 32) that the row sees
+        int first_full = 0, last_full = 0;                    // keys that every row of the warp sees
         bool live = false, idle = true;
         int64_t unit = 0;
         auto fetch = [&](int U) -> bool {
@@ -661,6 +664,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 row_lo = p.win > 0 ? max(0, x.p + back - p.win + 1) : 0;   // back = depth + 1
             }
             idle = !__any_sync(0xFFFFFFFFu, live);            // a warp without rows only keeps the barriers going
+            first_full = __reduce_max_sync(0xFFFFFFFFu, row_lo);
+            last_full = x.p;
             unit = ((static_cast<int64_t>(x.r) * p.hkv + x.g) * p.mtiles + x.node0 / p.npt) * p.spans + x.span;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kUnits));
@@ -671,10 +676,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         for (int U = 0; ok && nt > 0; ++U) {
             float m_run = -INFINITY, l_run = 0.f;
             for (int idx = 0; idx < nt; ++idx, ++t) {
-                const int b = t & 1;
+                const int b = t % C::NS;
                 const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
-                const uint32_t xbar = BAR(C::B_XCHG + 2 * quarter + b);
-                if (!(ok = warp_wait(BAR(C::B_SFULL + b), ph, p.status))) break;
+                const uint32_t xbar = BAR(C::B_XCHG + 2 * quarter + (t & 1));
+                if (!(ok = warp_wait(BAR(C::B_SFULL + b), static_cast<uint32_t>(t / C::NS) & 1u, p.status))) break;
                 const int xb = t % 3 * 128, xnext = (t + 1) % 3 * 128;
                 if (cq == 0) xbuf[xnext + r] = kNoMax;        // free since every warp read tile t - 2's maxima
                 if (idle) {
@@ -691,14 +696,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 }
                 tc_fence_after();
                 const uint32_t t_s = tbase + lane_addr + C::s_col(b) + col0;
-                // visible columns of this quarter as bits
+                // visible columns of this quarter as bits, unless every row sees them all
+                const int kbase = (t0 + idx) * kTile + col0;
+                const bool masked = idx >= nring || kbase < first_full || kbase + 31 > last_full;
                 uint32_t vis = seen;
-                if (idx < nring) {
-                    const int kbase = (t0 + idx) * kTile + col0;
+                if (masked && idx < nring) {
                     const int vlo = live ? max(0, row_lo - kbase) : 0, vhi = live ? min(31, row_hi - kbase) : 31;
                     vis = vlo > vhi ? 0u : (0xFFFFFFFFu >> (31 - (vhi - vlo))) << vlo;
                 }
-                const bool masked = !__all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu);
                 float sv[32];
                 auto load = [&]() {
                     load_s<32>(t_s, sv);
@@ -762,7 +767,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 // O's rescale, once the previous P V is done; a unit's first P V starts O afresh, and a row
                 // that has seen nothing yet has an O of zeros
                 if (idx > 0 && __any_sync(0xFFFFFFFFu, live && alpha != 1.f && m_old != -INFINITY)) {
-                    if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status)))
+                    if (!(ok = warp_wait(BAR(C::B_PVDONE + (t - 1) % C::NS), static_cast<uint32_t>((t - 1) / C::NS) & 1u, p.status)))
                         break;
                     tc_fence_after();
 #pragma unroll 1
@@ -789,9 +794,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float a = sv[2 * e], bb = sv[2 * e + 1];
+                        float ra, rb;                       // exact
                         w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(bb), 0x7632);
-                        w[16 + e] = pack_bf16(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
-                                              bb - __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u));
+                        fma_x2(ra, rb, __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
+                               __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u), -1.f, -1.f, a, bb);
+                        w[16 + e] = pack_bf16(ra, rb);
                     }
                     tmem_st32(t_s, w);
                 }
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (!(ok = fetch(U + 1))) break;
             if (was_idle) continue;
             // the unit's partial result; the next unit's first P V waits for this warp's next PHALF
-            if (!(ok = warp_wait(BAR(C::B_PVDONE + ((t - 1) & 1)), static_cast<uint32_t>((t - 1) >> 1) & 1u, p.status))) break;
+            if (!(ok = warp_wait(BAR(C::B_PVDONE + (t - 1) % C::NS), static_cast<uint32_t>((t - 1) / C::NS) & 1u, p.status))) break;
             tc_fence_after();
             float4* po = p.part_o + ((done * (p.lanes >> 5) + quarter) * (D / 4) + cq * (D / 16)) * 32 + lane;
 #pragma unroll 1

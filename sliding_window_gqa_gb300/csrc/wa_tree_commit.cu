@@ -1,9 +1,14 @@
 // wa_tree_commit.cu — the kept nodes' keys and values into the rings of several layers.
 //
-// Node path[r, j] of row r goes to slot (pos[r] + 1 + j) mod ring, j < length[r].
-// A copy of hkv * d bf16 values a (layer, K or V, row, j): one block each, 16 bytes
-// a thread and pass.  Where length exceeds the ring, the nodes that a later one
-// would overwrite are left out, so no two blocks write one slot.
+// Node path[r, j] of row r goes to slot (pos[r] + 1 + j) mod ring, j < length[r]: a copy of hkv * d bf16 values a
+// (layer, K or V, row, j), bound by latency for one sequence (the row's numbers, then its path, then the data) and
+// by HBM for many.  A block takes kNodes nodes of one (layer, K or V, row), so the numbers are fetched once for
+// them and all of a node's 16-byte pieces are in flight together (a block a node left 7 waves of blocks to launch
+// for 12 layers of 48 rows: 13 us against 5).  Where length exceeds the ring, the nodes that a later one would
+// overwrite are left out, so no two blocks write one slot.
+//
+// The status word is written by block 0 alone, which looks through every row's numbers, so that a call is one
+// launch; for calls of more than kOneBlockEntries entries it is cleared before, and each block reports its own.
 #include <cuda_runtime.h>
 
 #include "wa_internal.h"
@@ -12,34 +17,80 @@ namespace wa {
 
 namespace {
 
-__global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ CommitArgs a) {
-    const int r = blockIdx.x / a.most, j = blockIdx.x % a.most;
-    const int l = blockIdx.y, kv = blockIdx.z;
-    const int p = a.pos[r], raw = a.length[r];
-    const int len = min(max(raw, 0), a.most);
-    const bool first = l == 0 && kv == 0 && threadIdx.x == 0;
-    if (first && j == 0) {
-        if (raw != len) atomicOr(&a.hdr->status, WA_STATUS_BAD_TREE);
-        if (p < -1) atomicOr(&a.hdr->status, WA_STATUS_BAD_POS);
+constexpr int kNodes = 8;
+constexpr int kCommitThreads = 256;
+constexpr int64_t kOneBlockEntries = 32768;
+
+// What is wrong with row r's length and position.
+__device__ __forceinline__ int row_faults(const CommitArgs& a, int r) {
+    const int raw = a.length[r];
+    return (raw < 0 || raw > a.most ? WA_STATUS_BAD_TREE : 0) | (a.pos[r] < -1 ? WA_STATUS_BAD_POS : 0);
+}
+
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_constant__ CommitArgs a, int groups, int one_block) {
+    const int r = blockIdx.x / groups, j0 = blockIdx.x % groups * kNodes;
+    const int l = blockIdx.y, kv = blockIdx.z, t = threadIdx.x;
+    const bool first = blockIdx.x == 0 && l == 0 && kv == 0;
+    const int p = a.pos[r], len = min(max(a.length[r], 0), a.most);
+    const int j1 = min(j0 + kNodes, len);
+    if (p >= -1 && j0 < j1) {
+        const int ring = a.ring[l];
+        const int pieces = a.hkv * a.d / 8;        // 16 bytes each
+        const uint16_t* src = static_cast<const uint16_t*>(a.src[kv][l]) + r * a.row[kv];
+        uint4* dst = reinterpret_cast<uint4*>(a.dst[kv][l]) + static_cast<int64_t>(r) * ring * pieces;
+        const int32_t* path = a.path + static_cast<int64_t>(r) * a.most;
+        // pieces of all the block's nodes in a row, four at a time loaded before they are stored
+        const int total = (j1 - j0) * pieces;
+        for (int e0 = t; e0 < total; e0 += 4 * kCommitThreads) {
+            uint4 v[4];
+            int64_t to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + i * kCommitThreads, j = j0 + e / pieces, c = e % pieces;
+                const int node = e < total ? path[j] : -1;
+                to[i] = -1;
+                if (node >= 0 && node < a.nodes && j >= len - ring) {
+                    to[i] = (static_cast<int64_t>(p) + 1 + j) % ring * pieces + c;
+                    v[i] = *reinterpret_cast<const uint4*>(src + node * a.tok[kv] + static_cast<int64_t>(c) * 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (to[i] >= 0) dst[to[i]] = v[i];
+        }
     }
-    if (p < -1 || j >= len || j < len - a.ring[l]) return;
-    const int node = a.path[static_cast<int64_t>(r) * a.most + j];
-    if (node < 0 || node >= a.nodes) {
-        if (first) atomicOr(&a.hdr->status, WA_STATUS_BAD_TREE);
-        return;
+    if (one_block ? !first : l != 0 || kv != 0) return;
+    // the status: of every entry, or of this block's
+    int bad = 0;
+    if (one_block) {
+        for (int i = t; i < a.rows; i += kCommitThreads) bad |= row_faults(a, i);
+        for (int64_t i = t; i < static_cast<int64_t>(a.rows) * a.most; i += kCommitThreads) {
+            const int row = static_cast<int>(i / a.most), j = static_cast<int>(i % a.most), node = a.path[i];
+            if (a.pos[row] >= -1 && j < a.length[row] && (node < 0 || node >= a.nodes)) bad |= WA_STATUS_BAD_TREE;
+        }
+        const int tree = __syncthreads_or(bad & WA_STATUS_BAD_TREE), pos = __syncthreads_or(bad & WA_STATUS_BAD_POS);
+        if (t == 0) a.hdr->status = (tree ? WA_STATUS_BAD_TREE : 0) | (pos ? WA_STATUS_BAD_POS : 0);
+    } else {
+        if (t == 0 && j0 == 0) bad = row_faults(a, r);
+        if (p >= -1 && t < j1 - j0) {
+            const int node = a.path[static_cast<int64_t>(r) * a.most + j0 + t];
+            if (node < 0 || node >= a.nodes) bad |= WA_STATUS_BAD_TREE;
+        }
+        if (bad) atomicOr(&a.hdr->status, bad);
     }
-    const int64_t slot = (static_cast<int64_t>(p) + 1 + j) % a.ring[l];
-    const int64_t width = static_cast<int64_t>(a.hkv) * a.d;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[kv][l]) + r * a.row[kv] + node * a.tok[kv]);
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dst[kv][l]) + (static_cast<int64_t>(r) * a.ring[l] + slot) * width);
-    for (int e = threadIdx.x; e < width / 8; e += blockDim.x) dst[e] = src[e];
 }
 
 }  // namespace
 
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.rows) * a.most, a.layers, 2);
-    commit_kernel<<<grid, 128, 0, s>>>(a);
+    const int groups = (a.most + kNodes - 1) / kNodes;
+    const bool one_block = static_cast<int64_t>(a.rows) * a.most <= kOneBlockEntries;
+    if (!one_block) {
+        const cudaError_t e = cudaMemsetAsync(a.hdr, 0, kHeaderBytes, s);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(static_cast<unsigned>(a.rows) * groups, a.layers, 2);
+    commit_kernel<<<grid, kCommitThreads, 0, s>>>(a, groups, one_block ? 1 : 0);
     return cudaGetLastError();
 }
 

@@ -118,3 +118,22 @@ def test_in_a_graph(wa):
         g.replay()
         torch.cuda.synchronize()
         assert (bits(kr) == k).all() and (bits(vr) == v).all() and pos.tolist() == at and wa.status(ws) == 0
+
+
+def test_many_rows_report_their_own_faults(wa):
+    """More entries than the one block looks through: the status is cleared and gathered instead."""
+    rows, nodes, most = 700, 64, 64
+    kt, vt, kr, vr = (rnd(rows, m, 1, 128) for m in (nodes, nodes, 80, 80))
+    gen = torch.Generator().manual_seed(3)
+    path = torch.randint(0, nodes, (rows, most), generator=gen).tolist()
+    length = torch.randint(0, most + 1, (rows,), generator=gen).tolist()
+    pos = torch.randint(-1, 10 ** 6, (rows,), generator=gen).tolist()
+    args = dict(kt=[kt], vt=[vt], kr=[kr], vr=[vr])
+    assert both(wa, **args, path=path, length=length, pos=pos) == 0
+    length[-1] = 5
+    path[-1][3] = nodes
+    assert both(wa, **args, path=path, length=length, pos=pos) == wa.WA_STATUS_BAD_TREE
+    path[-1][3], pos[0] = 0, -9
+    assert both(wa, **args, path=path, length=length, pos=pos) == wa.WA_STATUS_BAD_POS
+    pos[0], length[350] = 0, most + 1
+    assert both(wa, **args, path=path, length=length, pos=pos) == wa.WA_STATUS_BAD_TREE
