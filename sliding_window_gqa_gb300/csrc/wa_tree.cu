@@ -215,16 +215,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     int* xbuf = reinterpret_cast<int*>(smem + C::OFF_X);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < C::NBAR; ++i) {
-            int count = 1;
-            if (i >= C::B_PHALF && i < C::B_PFULL) count = 16;             // the softmax warps
-            else if (i >= C::B_PFULL && i < C::B_XCHG) count = 8;          // those of keys 64 and up
-            else if (i >= C::B_XCHG && i < C::B_QFULL) count = 4;          // those of a lane quarter
-            else if (i >= C::B_UFREE && i < C::B_DRAIN) count = 19;        // producer, MMA, V, softmax warps
-            mbar_init(BAR(i), count);
-        }
+    // a barrier a thread: one thread takes 100 cycles each, 6,000 for all
+    static_assert(C::NBAR <= 128, "warps 4..7 set up the barriers");
+    if (threadIdx.x >= 128 && threadIdx.x < 128 + C::NBAR) {
+        const int i = threadIdx.x - 128;
+        int count = 1;
+        if (i >= C::B_PHALF && i < C::B_PFULL) count = 16;             // the softmax warps
+        else if (i >= C::B_PFULL && i < C::B_XCHG) count = 8;          // those of keys 64 and up
+        else if (i >= C::B_XCHG && i < C::B_QFULL) count = 4;          // those of a lane quarter
+        else if (i >= C::B_UFREE && i < C::B_DRAIN) count = 19;        // producer, MMA, V, softmax warps
+        mbar_init(BAR(i), count);
         fence_mbar_init();
     }
     if (threadIdx.x >= 128 && threadIdx.x < 256) xbuf[threadIdx.x - 128] = kNoMax;    // the first tile's maxima
@@ -920,14 +920,14 @@ __device__ void tree_rerun(const TreeArgs& a, TreeRerun& sm, int r, int node, in
     if (t < 64) orow[t] = f64_to_bf16_rn(acc / l);
 }
 
-constexpr int kMergeSpans = 4;
+constexpr int kMergeSpans = 2;
 
 // o = sum_s a_s O_s / sum_s a_s l_s over a row's spans in order, a_s = 2^(m_s - M).  A block takes 32 query
 // rows (lanes) and 64 dims (8 a warp) of a tile, reads the partial results in the order they were stored
 // (512 bytes a warp and load, kMergeSpans spans in flight), and turns them round in shared memory for the output.
 // A row with a value that is not finite is computed again in float64.
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_l,
+__global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_l,
                                                          const float* __restrict__ part_m,
                                                          const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans, int lanes) {
     __shared__ __align__(16) uint8_t tile[32 * 144];
