@@ -53,13 +53,14 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 // maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
 constexpr float kTreeLazy = 32.0f;
 
-// Keys a span, a power of two: keys * hq / 128.  Short spans put a single row's keys on more SMs, long ones
-// leave fewer partial results and fewer ends of the pipeline: one row of 32,000 keys, 16/8 heads, runs 75, 56
-// and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads, 795, 617 and 549 us with 512,
-// 1,024 and 2,048; one row of a 1,024-key window 25 us with 512 and 33 with 1,024, 64 of them 332 and 309.
-constexpr int kSpanMin = 512, kSpanMax = 4096, kSpanUnits = 128;
-__host__ __device__ inline int tree_span(int64_t keys, int hq) {
-    const int64_t want = keys * hq / kSpanUnits;
+// Keys a span, a power of two: keys * hq / 128 on a linear cache, win * hq / 32 on a window.  Short spans put a
+// single row's keys on more SMs, long ones leave fewer partial results and fewer ends of the pipeline.  One row of
+// 32,000 keys, 16/8 heads: 75, 56 and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads,
+// 10,000 keys: 795, 617 and 549 us with 512, 1,024 and 2,048 (an earlier state of the kernel); a 1,024-key window:
+// one row of 16/8 heads 25 us with 512 and 33 with 1,024, 64 rows of 32/16 heads 316 and 295.
+constexpr int kSpanMin = 512, kSpanMax = 2048, kSpanLinear = 128, kSpanWindow = 32;
+__host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
+    const int64_t want = keys * hq / (window ? kSpanWindow : kSpanLinear);
     int len = kSpanMin;
     while (len < kSpanMax && 2 * len <= want) len *= 2;
     return len;
@@ -71,7 +72,7 @@ __host__ __device__ inline int64_t tree_keys(int p, int win) { return win > 0 ? 
 __host__ __device__ inline int tree_spans(int p, int win, int hq) {
     const int lo = tree_first(p, win);
     if (lo > p) return 1;
-    const int len = tree_span(tree_keys(p, win), hq);
+    const int len = tree_span(tree_keys(p, win), win > 0, hq);
     return p / len - lo / len + 1;
 }
 
@@ -197,6 +198,48 @@ struct TreeUnit {
     int r, g, node0, span, t0, nring, nt, p, n, lo;
 };
 
+// Keys at ring slots sl0, sl0 + 1, ... that pass the ring's end, into a slot of the shared-memory ring, by one
+// warp: pieces of 8 keys by TMA, and by the warp where the piece itself wraps.  Out of line: few tiles come here,
+// and its code among the producer's cost the other roles 14 % at 128 query rows.
+template <int D, bool is_v>
+__device__ __noinline__ void load_wrapped(const TreeParams& p, int r, int g, int blk0, int sl0, uint32_t dst, uint32_t full,
+                                          uint64_t pol, int lane) {
+    constexpr int KB = D / 64, nkeys = is_v ? kTile * 128 / D : kTile, nblk = is_v ? KB : 2, blk = nkeys * 128;
+    const int64_t tok = static_cast<int64_t>(p.hkv) * D;
+    const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(r) * p.ring * tok + static_cast<int64_t>(g) * D + blk0 * 64;
+    int whole = 0;
+    for (int a = 0; a < nkeys / 8; ++a) {
+        const int sl = (sl0 + 8 * a) % p.ring;
+        if (sl + 8 <= p.ring) {
+            ++whole;
+            continue;
+        }
+        // every load before the first store: one trip to memory
+        uint4 val[2 * nblk];
+#pragma unroll
+        for (int i = 0; i < 2 * nblk; ++i) {
+            const int e = lane + 32 * i, k = e / (8 * nblk), rem = e % (8 * nblk);
+            val[i] = ld_global_nc_v4(base + (sl + k) % p.ring * tok + rem * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * nblk; ++i) {
+            const int e = lane + 32 * i, k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
+            st_shared_v4(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), val[i].x, val[i].y, val[i].z, val[i].w);
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(full, whole * nblk * 1024);
+    __syncwarp();
+    // one lane a piece (nkeys / 8 is at most 16)
+    if (lane < nkeys / 8) {
+        const int sl = (sl0 + 8 * lane) % p.ring;
+        if (sl + 8 <= p.ring)
+            for (int b = 0; b < nblk; ++b)
+                tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, sl, blk0 + b, g, r, full, pol);
+    }
+}
+
 template <int D, int QR>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     using C = TreeCfg<D, QR>;
@@ -262,7 +305,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
         // K and V are read once, unless several query tiles of a row share them
         const uint64_t pol = p.shared_kv ? policy_evict_last() : policy_evict_first();
-        const int64_t tok = static_cast<int64_t>(p.hkv) * D;
         int u = 0;                                // loads issued
         int tk = 0;                               // tiles whose K loads have begun
         // one load: K of 128 keys and 128 dims, or V of VKEYS keys and all dims; slot0: the ring slot of the
@@ -284,35 +326,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     if (slot0 < 0) tma_load_5d(dst, is_v ? &p.tvt : &p.tkt, 0, key, blk0, x.g, x.r, full, pol);
                     else tma_load_5d(dst, is_v ? &p.tv : &p.tk, 0, sl0, blk0, x.g, x.r, full, pol);
                 }
+            } else if (is_v) {
+                load_wrapped<D, true>(p, x.r, x.g, blk0, sl0, dst, full, pol, lane);
             } else {
-                // pieces of 8 keys: by TMA, or by the warp where the piece itself wraps
-                const int nblk = is_v ? C::KB : 2, blk = nkeys * 128;
-                const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(x.r) * p.ring * tok +
-                                       static_cast<int64_t>(x.g) * D + blk0 * 64;
-                int whole = 0;
-                for (int a = 0; a < nkeys / 8; ++a) {
-                    const int sl = (sl0 + 8 * a) % p.ring;
-                    if (sl + 8 <= p.ring) {
-                        ++whole;
-                        continue;
-                    }
-                    for (int e = lane; e < 64 * nblk; e += 32) {
-                        const int k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
-                        const uint4 val = ld_global_nc_v4(base + (sl + k) % p.ring * tok + b * 64 + cc * 8);
-                        st_shared_v4(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), val.x, val.y, val.z, val.w);
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(full, whole * nblk * 1024);
-                __syncwarp();
-                // one lane a piece (nkeys / 8 is at most 16)
-                if (lane < nkeys / 8) {
-                    const int sl = (sl0 + 8 * lane) % p.ring;
-                    if (sl + 8 <= p.ring)
-                        for (int b = 0; b < nblk; ++b)
-                            tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, sl, blk0 + b, x.g, x.r, full, pol);
-                }
+                load_wrapped<D, false>(p, x.r, x.g, blk0, sl0, dst, full, pol, lane);
             }
             __syncwarp();
             ++u;
@@ -563,7 +580,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     x.nt = 1;
                     return;
                 }
-                const int len = tree_span(tree_keys(x.p, p.win), p.hq);
+                const int len = tree_span(tree_keys(x.p, p.win), p.win > 0, p.hq);
                 const int sp = x.lo / len + x.span;
                 if (sp > x.p / len) continue;
                 const int kb = max(x.lo, sp * len), ke = min(x.p, sp * len + (len - 1));
@@ -1112,12 +1129,12 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
     pl.spans = 1;
     if (win > 0) {
         // win - 1 keys from any position touch at most this many spans
-        const int len = tree_span(win, hq);
+        const int len = tree_span(win, true, hq);
         pl.spans = win > 1 ? (win - 2 + len - 1) / len + 1 : 1;
     } else {
         for (int len = kSpanMin; len <= kSpanMax; len *= 2) {
             // the most keys with this span
-            int64_t keys = len == kSpanMax ? ring : (2LL * kSpanUnits * len + hq - 1) / hq - 1;
+            int64_t keys = len == kSpanMax ? ring : (2LL * kSpanLinear * len + hq - 1) / hq - 1;
             keys = keys < ring ? keys : ring;
             const int spans = static_cast<int>((keys + len - 1) / len);
             pl.spans = spans > pl.spans ? spans : pl.spans;

@@ -158,3 +158,28 @@ def test_calls_refuse_host_tensors_and_types():
         wa.tree_verify(torch.zeros(1, 2, 9), i, i, torch.zeros(1, 2))
     with pytest.raises(TypeError):
         wa.tree_commit(tr, tr, ring, ring, i, i[:, 0], i[:, 0])
+
+
+def _spans(p, win, hq):
+    """Spans that a row at position p is cut into, from the documented rule: its own key count, window and hq."""
+    lo = max(0, p + 2 - win) if win else 0
+    if lo > p:
+        return 1
+    want = win * hq // 32 if win else (p + 1) * hq // 128
+    length = 512
+    while length < 2048 and 2 * length <= want:
+        length *= 2
+    return p // length - lo // length + 1
+
+
+@pytest.mark.parametrize("win", [0, 1, 2, 300, 512, 513, 1000, 1024, 2049, 9000])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (16, 8), (12, 4), (16, 1), (64, 4)])
+def test_the_workspace_holds_every_rows_spans(win, hq, hkv):
+    """The workspace's size counts the most spans any position can have, whatever the ring."""
+    L = ensure_built().lib()
+    for ring in (win, win + 7, win + 5000) if win else (1, 511, 512, 513, 4095, 4096, 20000, 60001):
+        lanes = (hq // hkv + 31) // 32 * 32
+        held = (L.wa_tree_decode_ws_bytes(1, 1, hq, hkv, 128, win, ring) - 256) // (hkv * lanes * (128 + 5) * 4)
+        at = range(-1, 30000, 13) if win else [*range(-1, ring, 29), ring - 1]
+        most = max(_spans(p, win, hq) for p in at)
+        assert most <= held <= most + 1, (ring, most, held)
