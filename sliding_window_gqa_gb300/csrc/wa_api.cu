@@ -234,7 +234,8 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
     const int64_t units = static_cast<int64_t>(rows) * nodes * hq;
     const wa::TreePlan pl = wa::tree_plan(rows, nodes, hq, hkv, win, ring);
     if (units > INT32_MAX || pl.units > INT32_MAX / 2) return 0;
-    return wa::kHeaderBytes + static_cast<size_t>(pl.units) * pl.lanes * (static_cast<size_t>(d) + 5) * sizeof(float);
+    return wa::kHeaderBytes + static_cast<size_t>(pl.units) * pl.lanes * (static_cast<size_t>(d) + 5) * sizeof(float) +
+           static_cast<size_t>(rows) * pl.spans * wa::kTreePairBytes;
 }
 
 int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
@@ -285,7 +286,6 @@ int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const 
     a.out = out;
     a.hdr = reinterpret_cast<wa::WsHeader*>(base);
     a.part = base + wa::kHeaderBytes;
-    if (cudaMemsetAsync(base, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
     if (wa::launch_tree(a, s) != cudaSuccess) return WA_ECUDA;
     return WA_OK;
 }

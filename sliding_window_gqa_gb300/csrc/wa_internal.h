@@ -18,8 +18,9 @@ constexpr int kHeaderBytes = 256;
 struct WsHeader {
     int status;   // WA_STATUS_* bits
     int nflag;    // (row, head) pairs queued for the float64 re-run
-    int next_unit;   // tensor-core decode: units taken so far past the first one of each CTA
-    int pad[61];
+    int next_unit;   // tensor-core decode, tree decode: units taken so far past the first one of each CTA
+    int pairs;       // tree decode: listed (row, span) pairs
+    int pad[60];
 };
 
 inline int decode_chunks_max(int win, int ring) {
@@ -71,8 +72,11 @@ struct TreeArgs {
     int64_t q_row, q_tok, kt_row, kt_tok, vt_row, vt_tok, o_row, o_tok;   // elements
     void* out;
     WsHeader* hdr;
-    void* part;              // partial results: l float4[units * lanes], O float[units * lanes * d], m float[units * lanes]
+    void* part;              // partial results: l float4[units * lanes], O float[units * lanes * d], m float[units * lanes],
+                             // the list of (row, span) pairs: kTreePairBytes each, rows * spans at most
 };
+
+constexpr int kTreePairBytes = 32 + WA_TREE_MAX_NODES;
 
 // How a tree decode call is cut: nodes a query tile, query tiles a key head, spans a row at most, query rows
 // kept of a tile, units = rows * hkv * mtiles * spans.

@@ -14,6 +14,8 @@
 // joins a row's spans in order.  Nothing in a unit depends on the other rows, so
 // neither do the bits.
 //
+// tree_plan_kernel: one block lists the (row, span) pairs with any key, longest first, with all that a unit needs
+// of its row (position, nodes, parents), checks the rows' numbers for the status word, and clears the header.
 // tree_kernel<D>: a persistent grid, one CTA an SM, 640 threads, that streams the
 // keys of its units without a break between units:
 //   warp 0      TMA producer: K and V through a ring of 32 KiB slots (head dim 256: half a
@@ -25,8 +27,8 @@
 //               O += P(t - NS + 1) V (two bf16 parts of P), commits free the slots.
 //   warp 2      zeroes V rows that no node of the row sees (stale ring slots, nodes
 //               past n), so that they never meet a zero probability as 0 * inf.
-//   warp 3      takes units from a counter, publishes them through a ring of unit
-//               slots, and loads each unit's Q once the previous unit's last S is done.
+//   warp 3      takes units from the list by a counter (long ones first: taken as they came, the
+//               last ones ended 10 % after the mean), publishes them through a ring of unit slots, and loads each unit's Q once the previous unit's last S is done.
 //   warps 4..19 softmax, one query row a thread in four column quarters: mask,
 //               exponentials, P over S in tensor memory, a lazy rescale of O, and the
 //               unit's partial result.  Four warps share a row group, so that the chain
@@ -76,6 +78,11 @@ __host__ __device__ inline int tree_spans(int p, int win, int hq) {
     return p / len - lo / len + 1;
 }
 
+// A listed pair: row, span, first tile, ring tiles, tiles, position, nodes, first key, then the row's 128 parents
+// as bytes (255: a root).
+constexpr int kPair = 8 + WA_TREE_MAX_NODES / 4;
+static_assert(kPair * 4 == kTreePairBytes, "workspace");
+
 struct TreeParams {
     // five dimensions (64 dims, tokens, blocks of 64 dims, heads, rows) put a whole half-operand, in the
     // [block][token][64] order that the tensor core reads, into one copy
@@ -86,15 +93,14 @@ struct TreeParams {
     CUtensorMap tkt, tvt;      // nodes' keys and values, boxes as tk's and tv's
     const uint16_t* k;
     const uint16_t* v;
-    const int32_t* pos;
-    const int32_t* parent;
-    const int32_t* n;
     float4* part_o;            // [unit][lanes / 32][d / 4][32]: a store of 32 lanes is 512 bytes in a row
     float4* part_l;            // [unit][lanes]: l of each column quarter
     float* part_m;             // [unit][lanes]: m (log2 units)
     int* status;
     int* next_unit;
-    int rows, nodes, hq, hkv, gsz, npt, qn, mtiles, spans, lanes, win, ring, units, shared_kv;
+    const int* list;           // kPair ints a (row, span) pair
+    const int* pairs;          // how many
+    int rows, nodes, hq, hkv, gsz, npt, qn, mtiles, spans, lanes, win, ring, shared_kv;
     float c;                   // |scale| * log2(e)
     int neg;
 };
@@ -198,6 +204,99 @@ struct TreeUnit {
     int r, g, node0, span, t0, nring, nt, p, n, lo;
 };
 
+__global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restrict__ pos, const int32_t* __restrict__ parent,
+                                                         const int32_t* __restrict__ n, int rows, int nodes, int hq, int win,
+                                                         int ring, WsHeader* hdr, int* __restrict__ list) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ int count[32], at[32];          // pairs of so many tiles (at most 16 of a span and the tree's)
+    static_assert(kSpanMax / kTile + 1 < 32, "tiles of a pair");
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    struct Row {
+        int p, n, lo, len, spans;
+    };
+    auto row_at = [&](int r, int& bad) {
+        Row x;
+        const int raw_p = __ldg(pos + r), raw_n = n ? __ldg(n + r) : nodes;
+        x.n = min(max(raw_n, 0), nodes);
+        x.p = tree_pos(raw_p, win, ring);
+        x.lo = tree_first(x.p, win);
+        x.len = tree_span(tree_keys(x.p, win), win > 0, hq);
+        x.spans = x.n > 0 ? tree_spans(x.p, win, hq) : 0;
+        bad |= (raw_n != x.n ? WA_STATUS_BAD_TREE : 0) | (raw_p != x.p ? WA_STATUS_BAD_POS : 0);
+        return x;
+    };
+    // a span's first tile, ring tiles and all its tiles; the tree's own keys go with the row's last span
+    auto tiles = [&](const Row& x, int s, int& t0, int& nring) {
+        t0 = nring = 0;
+        if (x.lo <= x.p) {
+            const int64_t b = static_cast<int64_t>(x.lo / x.len + s) * x.len;
+            t0 = static_cast<int>(max(static_cast<int64_t>(x.lo), b)) / kTile;
+            nring = static_cast<int>(min(static_cast<int64_t>(x.p), b + x.len - 1)) / kTile - t0 + 1;
+        }
+        return nring + (s == x.spans - 1 ? 1 : 0);
+    };
+    // four parents a lane, as bytes
+    auto parents = [&](int r) {
+        int4 v;
+        const int32_t* row = parent + static_cast<int64_t>(r) * nodes + 4 * lane;
+        v.x = 4 * lane < nodes ? __ldg(row) : -1;
+        v.y = 4 * lane + 1 < nodes ? __ldg(row + 1) : -1;
+        v.z = 4 * lane + 2 < nodes ? __ldg(row + 2) : -1;
+        v.w = 4 * lane + 3 < nodes ? __ldg(row + 3) : -1;
+        return v;
+    };
+    int4 raw = warp < rows ? parents(warp) : make_int4(-1, -1, -1, -1);
+    if (t < 32) count[t] = 0;
+    __syncthreads();
+    int bad = 0, t0, nring;
+    for (int r = t; r < rows; r += 1024) {
+        const Row x = row_at(r, bad);
+        for (int s = 0; s < x.spans; ++s) atomicAdd(&count[tiles(x, s, t0, nring)], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {       // longest first: a pair goes after all longer ones
+        const int mine = count[31 - lane];
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        at[31 - lane] = sum - mine;
+        if (lane == 31) {
+            hdr->nflag = 0;
+            hdr->next_unit = 0;
+            hdr->pairs = sum;
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += 32) {
+        const Row x = row_at(r, bad);
+        if (r != warp) raw = parents(r);
+        const int v[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 4 * lane + e, a = tree_parent(v[e], i);
+            if (i < x.n && a != v[e]) bad |= WA_STATUS_BAD_TREE;
+            bytes |= (static_cast<uint32_t>(a) & 255u) << (8 * e);
+        }
+        for (int s = 0; s < x.spans; ++s) {
+            const int nt = tiles(x, s, t0, nring);
+            int slot = lane == 0 ? atomicAdd(&at[nt], 1) : 0;
+            slot = __shfl_sync(0xFFFFFFFFu, slot, 0);
+            int* rec = list + static_cast<int64_t>(slot) * kPair;
+            if (lane == 0) {
+                reinterpret_cast<int4*>(rec)[0] = make_int4(r, s, t0, nring);
+                reinterpret_cast<int4*>(rec)[1] = make_int4(nt, x.p, x.n, x.lo);
+            }
+            rec[8 + lane] = static_cast<int>(bytes);
+        }
+    }
+    const int tree = __syncthreads_or(bad & WA_STATUS_BAD_TREE), where = __syncthreads_or(bad & WA_STATUS_BAD_POS);
+    if (t == 0) hdr->status = (tree ? WA_STATUS_BAD_TREE : 0) | (where ? WA_STATUS_BAD_POS : 0);
+}
+
 // Keys at ring slots sl0, sl0 + 1, ... that pass the ring's end, into a slot of the shared-memory ring, by one
 // warp: pieces of 8 keys by TMA, and by the warp where the piece itself wraps.  Out of line: few tiles come here,
 // and its code among the producer's cost the other roles 14 % at 128 query rows.
@@ -246,6 +345,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");     // the plan writes the status word
         if (threadIdx.x == 0) atomicOr(p.status, WA_STATUS_LAYOUT);
         return;
     }
@@ -537,57 +637,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
     } else if (warp == 3) {
         // ------------------------------------------------ units; Q
+        // this kernel starts while the plan still runs (and so does all that follows its first published unit)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int per = p.hkv * p.mtiles, units = *p.pairs * per;
         int k_cur = blockIdx.x, k_ans = 0, pub = 0, loaded = 0;
         bool asked = false, ended = false, ok = true;
-        int par[4];               // the unit's parents, four a lane
-        // the next unit with any work (nt = 0: none left).  Its number was asked for one unit ahead, and
-        // everything a unit needs is loaded at once: one trip to memory a unit.
+        int par = 0;              // four of the unit's parents a lane
+        // the next unit with any work (nt = 0: none left); its number was asked for one unit ahead
         auto next_unit = [&](TreeUnit& x) {
             for (;;) {
                 if (asked) k_cur = __shfl_sync(0xFFFFFFFFu, k_ans, 0) + static_cast<int>(gridDim.x);
                 x.nt = 0;
                 x.nring = 0;
-                if (k_cur >= p.units) return;
-                int k = k_cur;
-                const int mt = k % p.mtiles;
-                k /= p.mtiles;
-                x.span = k % p.spans;
-                k /= p.spans;
-                x.g = k % p.hkv;
-                x.r = k / p.hkv;
-                const int raw_p = __ldg(p.pos + x.r), raw_n = p.n ? __ldg(p.n + x.r) : p.nodes;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    par[e] = lane + 32 * e < p.nodes ? __ldg(p.parent + static_cast<int64_t>(x.r) * p.nodes + lane + 32 * e) : -1;
+                if (k_cur >= units) return;
+                const int pair = k_cur / per, rem = k_cur % per;
+                const int* rec = p.list + static_cast<int64_t>(pair) * kPair;
+                const int field = rec[lane & 7];
+                par = rec[8 + lane];
                 if (lane == 0) k_ans = atomicAdd(p.next_unit, 1);
                 asked = true;
-                x.node0 = mt * p.npt;
-                x.n = min(max(raw_n, 0), p.nodes);
-                x.p = tree_pos(raw_p, p.win, p.ring);
-                int bad = (raw_n != x.n ? WA_STATUS_BAD_TREE : 0) | (raw_p != x.p ? WA_STATUS_BAD_POS : 0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = lane + 32 * e, a = tree_parent(par[e], i);
-                    if (i < x.n && a != par[e]) bad |= WA_STATUS_BAD_TREE;
-                    par[e] = a;
-                }
-                if (bad && x.g == 0 && mt == 0 && x.span == 0) atomicOr(p.status, bad);   // reported once a row
-                if (x.node0 >= x.n) continue;
-                x.lo = tree_first(x.p, p.win);
-                if (x.lo > x.p) {                             // no key of the ring: the tree alone
-                    if (x.span > 0) continue;
-                    x.t0 = 0;
-                    x.nt = 1;
-                    return;
-                }
-                const int len = tree_span(tree_keys(x.p, p.win), p.win > 0, p.hq);
-                const int sp = x.lo / len + x.span;
-                if (sp > x.p / len) continue;
-                const int kb = max(x.lo, sp * len), ke = min(x.p, sp * len + (len - 1));
-                x.t0 = kb / kTile;
-                x.nring = ke / kTile - x.t0 + 1;
-                x.nt = x.nring + (sp == x.p / len ? 1 : 0);
-                return;
+                x.g = rem / p.mtiles;
+                x.node0 = rem % p.mtiles * p.npt;
+                x.r = __shfl_sync(0xFFFFFFFFu, field, 0);
+                x.span = __shfl_sync(0xFFFFFFFFu, field, 1);
+                x.t0 = __shfl_sync(0xFFFFFFFFu, field, 2);
+                x.nring = __shfl_sync(0xFFFFFFFFu, field, 3);
+                x.nt = __shfl_sync(0xFFFFFFFFu, field, 4);
+                x.p = __shfl_sync(0xFFFFFFFFu, field, 5);
+                x.n = __shfl_sync(0xFFFFFFFFu, field, 6);
+                x.lo = __shfl_sync(0xFFFFFFFFu, field, 7);
+                if (x.node0 < x.n) return;
             }
         };
         auto publish_next = [&](TreeUnit& x) -> bool {
@@ -598,11 +677,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (pub >= kUnits && !warp_wait(BAR(C::B_UFREE + pub % kUnits), static_cast<uint32_t>(pub / kUnits - 1) & 1u, p.status))
                 return false;
             volatile int* e = unit_ints(pub);
-            if (!ended) {
-                volatile uint8_t* out = reinterpret_cast<volatile uint8_t*>(e + 8);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[lane + 32 * i] = static_cast<uint8_t>(par[i]);
-            }
+            if (!ended) e[8 + lane] = par;
             if (lane == 0) {
                 e[0] = x.r; e[1] = x.g | (x.node0 << 16); e[2] = x.span; e[3] = x.t0;
                 e[4] = x.nring | ((x.nt - x.nring) << 24); e[5] = x.p; e[6] = x.n; e[7] = x.lo;
@@ -1078,14 +1153,16 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     t.k = static_cast<const uint16_t*>(a.k);
     t.v = static_cast<const uint16_t*>(a.v);
-    t.pos = a.pos; t.parent = a.parent; t.n = a.n;
     t.part_l = static_cast<float4*>(a.part);
     t.part_o = t.part_l + pl.units * pl.lanes;
     t.part_m = reinterpret_cast<float*>(t.part_o + pl.units * pl.lanes * (D / 4));
     t.status = &a.hdr->status;
     t.next_unit = &a.hdr->next_unit;
+    t.pairs = &a.hdr->pairs;
+    int* list = reinterpret_cast<int*>(t.part_m + pl.units * pl.lanes);
+    t.list = list;
     t.rows = a.rows; t.nodes = a.nodes; t.hq = a.hq; t.hkv = a.hkv; t.gsz = G; t.npt = pl.npt; t.mtiles = pl.mtiles;
-    t.spans = pl.spans; t.lanes = pl.lanes; t.win = a.win; t.ring = a.ring; t.units = static_cast<int>(pl.units);
+    t.spans = pl.spans; t.lanes = pl.lanes; t.win = a.win; t.ring = a.ring;
     t.shared_kv = pl.mtiles > 1;
     t.neg = a.scale < 0.f ? 1 : 0;
     t.c = (a.scale < 0.f ? -a.scale : a.scale) * 1.4426950408889634f;
@@ -1093,20 +1170,26 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
     const int grid = static_cast<int>(pl.units < sms ? pl.units : sms);
-    tree_kernel<D, QR><<<grid, kTreeThreads, C::SMEM, s>>>(t);
+    tree_plan_kernel<<<1, 1024, 0, s>>>(a.pos, a.parent, a.n, a.rows, a.nodes, a.hq, a.win, a.ring, a.hdr, list);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
-    // launched while the units still run: its blocks wait for them on the GPU
+    // each kernel is launched while the one before it runs, sets itself up and waits for it on the GPU
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = mgrid;
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<D, QR>, t);
+    if (e != cudaSuccess) return e;
+    const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
+    cfg.gridDim = mgrid;
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, const_cast<const float4*>(t.part_o), const_cast<const float4*>(t.part_l),
                            const_cast<const float*>(t.part_m), a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
     if (e != cudaSuccess) return e;
