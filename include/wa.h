@@ -292,8 +292,8 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
  * infinite value in v that some of a row's nodes do not see makes theirs
  * non-finite ones to compute again: float64's values, rounded.)  1 <= nodes <=
  * WA_TREE_MAX_NODES; other constraints as wa_decode, WA_EINVAL otherwise.
- * Calls whose work can overlap need workspaces of their own; two captured
- * graphs that replay at the same time do too.
+ * `out` must not overlap the inputs.  Calls whose work can overlap need
+ * workspaces of their own; two captured graphs that replay at the same time do too.
  */
 int wa_tree_decode(const void* q, const void* k_ring, const void* v_ring, const void* k_tree, const void* v_tree,
                    const int32_t* pos, const int32_t* parent, const int32_t* n, int32_t rows, int32_t nodes,

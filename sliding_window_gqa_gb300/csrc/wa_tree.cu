@@ -1019,9 +1019,9 @@ constexpr int kMergeSpans = 2;
 // (512 bytes a warp and load, kMergeSpans spans in flight), and turns them round in shared memory for the output.
 // A row with a value that is not finite is computed again in float64.
 template <int D>
-__global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* __restrict__ part_o, const float4* __restrict__ part_l,
-                                                         const float* __restrict__ part_m,
-                                                         const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans, int lanes) {
+__global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* part_o, const float4* part_l, const float* part_m,
+                                                            const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans,
+                                                            int lanes) {
     __shared__ __align__(16) uint8_t tile[32 * 144];
     __shared__ int bad[32];
     __shared__ TreeRerun again;
@@ -1038,9 +1038,11 @@ __global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* __rest
     const int n = min(a.n ? __ldg(a.n + r) : a.nodes, a.nodes);
     const int count = tree_spans(tree_pos(__ldg(a.pos + r), a.win, a.ring), a.win, a.hq);
     const int first = qd * 32 / G;                        // the block's first node
-    if (first >= npt || node0 + first >= n) return;
     if (t < 32) bad[t] = 0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");    // the partial results
+    // The partial results (plain pointers: they are written while this kernel is there already, so no load may go
+    // the read-only way or before this line).  Blocks without work wait too: nothing behind the call starts early.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (first >= npt || node0 + first >= n) return;
     __syncthreads();
     const int64_t rec = unit0 * lanes + qd * 32 + lane;
     const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + blockIdx.y * 16 + warp * 2) * 32 + lane;

@@ -273,3 +273,86 @@ def test_offsets_past_32_bits(wa):
                       parent[:1].cpu().numpy(), 0, 0.088)
     assert_parity(got[0], ref[0], check.TOL_FP32_P)
     assert np.isfinite(ref).all()
+
+
+def test_rows_without_nodes(wa):
+    """No row has a node: nothing is written, and a call behind it on the same workspace is not disturbed."""
+    c = _case(5, 7, 4, 2, 128, 0, 1000, [-1, 0, 500, 999, 12], seed=6, outside="keep")
+    ws = torch.empty(wa.tree_decode_ws_bytes(5, 7, 4, 2, 128, 0, 1000), dtype=torch.uint8, device="cuda")
+    want = _run(wa, c)
+    out = torch.full_like(c["q"], 7.0)
+    none = torch.zeros(5, dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        _run(wa, c, n=none, out=out, ws=ws)
+        got = _run(wa, c, ws=ws)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and _eq(got, want) and wa.status(ws) == 0
+
+
+def test_more_rows_than_the_plan_has_threads(wa):
+    """1,100 rows of their own lengths, each as it would be alone (checked for some) and by the definition."""
+    rows = 1100
+    pos = [(37 * r) % 1301 - 1 for r in range(rows)]
+    n = [r % 4 for r in range(rows)]
+    c = _case(rows, 3, 2, 1, 128, 0, 1300, pos, seed=12, n=n, outside="keep")
+    ws = torch.empty(wa.tree_decode_ws_bytes(rows, 3, 2, 1, 128, 0, 1300), dtype=torch.uint8, device="cuda")
+    got = _run(wa, c, out=torch.zeros_like(c["q"]), ws=ws)
+    assert wa.status(ws) == 0
+    pick = [0, 1, 31, 32, 1023, 1025, 1026, 1099]
+    sub = dict(c, rows=len(pick))
+    for x in ("q", "k", "v", "k_tree", "v_tree", "pos", "parent", "n"):
+        sub[x] = c[x][pick].contiguous()
+    ref = _ref(sub)
+    _check(got[pick], ref, sub)
+    alone = _run(wa, sub, out=torch.zeros_like(sub["q"]))
+    assert _eq(got[pick], alone)
+    c["parent"][1090, 1], c["pos"][1091] = 1, 1300          # found by threads that take a second row
+    c["n"][1090] = 2
+    _run(wa, c, ws=ws)
+    assert wa.status(ws) == wa.WA_STATUS_BAD_TREE | wa.WA_STATUS_BAD_POS
+
+
+def test_two_captured_calls_replayed_at_once(wa):
+    """Two graphs of several calls each, with workspaces of their own, on two streams: as the calls one by one."""
+    cs = [_case(3, 20, 8, 2, 256, 0, 3000, [2999, 100, -1], seed=31, outside="keep"),
+          _case(6, 33, 8, 8, 128, 700, 720, [5, 719, 720, 100000, 699, 40], seed=32, outside="keep")]
+    want = [_run(wa, c) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[torch.zeros_like(c["q"]) for _ in range(3)] for c in cs]
+    graphs = []
+    torch.cuda.synchronize()
+    for c, s, out in zip(cs, streams, outs):
+        ws = torch.empty(wa.tree_decode_ws_bytes(c["rows"], c["nodes"], c["q"].shape[2], c["k"].shape[2], c["q"].shape[3],
+                                                 c["win"], c["k"].shape[1]), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for o in out:                    # one behind another on one workspace
+                _run(wa, c, out=o, ws=ws, stream=s)
+        graphs.append((g, s, ws))
+    for _ in range(10):
+        for g, s, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, out, (_, _, ws) in zip(want, outs, graphs):
+        assert all(_eq(o, w) for o in out) and wa.status(ws) == 0
+
+
+def test_beside_the_other_tensor_core_kernels(wa):
+    """A tree decode, a decode and a prompt at the same time on three streams."""
+    c = _case(8, 16, 16, 2, 256, 0, 4000, [3999 - 300 * r for r in range(8)], seed=41, outside="keep")
+    dc = wa_synth.decode_case(8, 16, 2, 256, 1024, 1024, [3000 + r for r in range(8)], seed=42, device="cuda")
+    pc = wa_synth.prompt_case(500, 100, 8, 4, 128, 0, 600, seed=43, device="cuda")
+    s = [torch.cuda.Stream() for _ in range(3)]
+    calls = [lambda s: _run(wa, c, stream=s),
+             lambda s: wa.decode(dc["q"], dc["k"], dc["v"], dc["pos"], 1024, 1.0, stream=s),
+             lambda s: wa.prompt(pc["q"], pc["k"], pc["v"], 100, None, 0, 0.088, stream=s)]
+    want = [f(torch.cuda.current_stream()) for f in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [f(x) for f, x in zip(calls, s)]
+    torch.cuda.synchronize()
+    assert all(_eq(a, b) for a, b in zip(got, want))
+    again = _run(wa, c)                  # the ordinary call's way gives the same bits as the one with a stream
+    assert _eq(again, want[0])
