@@ -179,6 +179,7 @@ struct VerifyShared {
     int summed;                               // the stretches' sums are those of the current W
     int asked;                                // a child was dropped and the sum is awaited
     int ngone, node, len, cmd, slice, stretch;
+    int late;                           // a sum of another CTA did not arrive in time
     int changed;                        // no draft: the one token that left W since the sums, or -1
     Pair S;
 };
@@ -311,7 +312,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) ver
         sm.kids_hi = sm.kids[0][1].x | static_cast<unsigned long long>(sm.kids[0][1].y) << 32;
         sm.S = sm.S_prev = Pair{0.f, 0.f};
         sm.s = Pair{1.f, 0.f};
-        sm.summed = sm.asked = 0;
+        sm.summed = sm.asked = sm.late = 0;
         sm.node = 0;
         sm.len = n > 0;
         if (rank == 0 && n > 0) path[0] = 0;
@@ -389,11 +390,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) ver
                 sm.summed = summed;
                 sm.asked = asked;
                 sm.changed = asked ? changed : -1;
-                sm.cmd = asked ? 1 : summed ? 0 : 2;     // 0: sample; 1: sum and go on; 2: sum, then sample
+                // 0: sample; 1: sum and go on; 2: sum, then sample; 3: stop, nothing more is sent
+                sm.cmd = sm.late ? 3 : asked ? 1 : summed ? 0 : 2;
             }
         }
         __syncthreads();
         const int cmd = sm.cmd;
+        if (cmd == 3) break;
         const Pair Sn = sm.S;
         const float* p = trow + sm.node * a.t_node;
         const float* q = DRAFT ? drow + sm.node * a.d_node : nullptr;
@@ -420,7 +423,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) ver
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(bar), kSlices * sizeof(Pair));
                 const bool ok = warp_wait(smem_u32(bar), (pass >> 1) & 1, &a.hdr->status);
                 const Pair run = warp_scan(ok && lane < kSlices ? tot[lane] : Pair{0.f, 0.f}, lane);
-                if (lane == 31) sm.mass = run;
+                if (lane == 31) {
+                    sm.mass = run;
+                    sm.late = !ok;
+                }
                 __syncwarp();
             }
             ++pass;
@@ -431,7 +437,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) ver
         if (warp == 0) {
             const Pair want = pair_scale(sm.u[0], sm.mass);
             Pair before{0.f, 0.f};
-            const int at = pick(lane < kSlices ? sm.tot[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, want, before, lane);
+            const bool sums = lane < kSlices && !sm.late;
+            const int at = pick(sums ? sm.tot[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, want, before, lane);
             int st = -1;
             if (at >= 0 && at / PER == rank) st = pick(lane < kVerWarps ? sm.seg[at % PER][lane] : Pair{0.f, 0.f}, want, before, lane);
             if (at < 0 && rank == 0 && lane == 0) {
@@ -482,8 +489,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kVerThreads, 2) ver
             if (n == 0) a.token[r] = -1;
         }
     }
-    // No CTA leaves while another one may still write to its shared memory: it has waited for all the
-    // writes of every pass.
+    // No CTA leaves while another one may still write to its shared memory: it has waited for all the writes of
+    // every pass, and one that gave up on a pass waits once more (it has sent nothing since, so CTAs that leave
+    // get nothing from it).
+    if (warp == 0 && n > 0 && sm.late) warp_wait(smem_u32(&sm.bar[(pass - 1) & 1]), ((pass - 1) >> 1) & 1, &a.hdr->status);
 }
 
 template <int CL>
