@@ -251,7 +251,11 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
     int bad = 0, t0, nring;
     for (int r = t; r < rows; r += 1024) {
         const Row x = row_at(r, bad);
-        for (int s = 0; s < x.spans; ++s) atomicAdd(&count[tiles(x, s, t0, nring)], 1);
+        if (x.spans == 0) continue;
+        // the first span, the last one, and those between, which are full
+        atomicAdd(&count[tiles(x, 0, t0, nring)], 1);
+        if (x.spans > 1) atomicAdd(&count[tiles(x, x.spans - 1, t0, nring)], 1);
+        if (x.spans > 2) atomicAdd(&count[x.len / kTile], x.spans - 2);
     }
     __syncthreads();
     if (warp == 0) {       // longest first: a pair goes after all longer ones
@@ -281,62 +285,70 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
             if (i < x.n && a != v[e]) bad |= WA_STATUS_BAD_TREE;
             bytes |= (static_cast<uint32_t>(a) & 255u) << (8 * e);
         }
-        for (int s = 0; s < x.spans; ++s) {
-            const int nt = tiles(x, s, t0, nring);
-            int slot = lane == 0 ? atomicAdd(&at[nt], 1) : 0;
-            slot = __shfl_sync(0xFFFFFFFFu, slot, 0);
-            int* rec = list + static_cast<int64_t>(slot) * kPair;
-            if (lane == 0) {
-                reinterpret_cast<int4*>(rec)[0] = make_int4(r, s, t0, nring);
-                reinterpret_cast<int4*>(rec)[1] = make_int4(nt, x.p, x.n, x.lo);
+        for (int s0 = 0; s0 < x.spans; s0 += 32) {       // a span a lane
+            const int s = s0 + lane, left = min(32, x.spans - s0);
+            int slot = 0;
+            if (lane < left) {
+                const int nt = tiles(x, s, t0, nring);
+                slot = atomicAdd(&at[nt], 1);
+                int4* rec = reinterpret_cast<int4*>(list + static_cast<int64_t>(slot) * kPair);
+                rec[0] = make_int4(r, s, t0, nring);
+                rec[1] = make_int4(nt, x.p, x.n, x.lo);
             }
-            rec[8 + lane] = static_cast<int>(bytes);
+            for (int i = 0; i < left; ++i)
+                list[static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, slot, i)) * kPair + 8 + lane] = static_cast<int>(bytes);
         }
     }
     const int tree = __syncthreads_or(bad & WA_STATUS_BAD_TREE), where = __syncthreads_or(bad & WA_STATUS_BAD_POS);
     if (t == 0) hdr->status = (tree ? WA_STATUS_BAD_TREE : 0) | (where ? WA_STATUS_BAD_POS : 0);
 }
 
-// Keys at ring slots sl0, sl0 + 1, ... that pass the ring's end, into a slot of the shared-memory ring, by one
-// warp: pieces of 8 keys by TMA, and by the warp where the piece itself wraps.  Out of line: few tiles come here,
-// and its code among the producer's cost the other roles 14 % at 128 query rows.
+// 16 bytes to shared memory, without a register in between; over with cp.async.wait_all.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+
+// Keys at ring slots sl0, sl0 + 1, ... (sl0 < ring) that pass the ring's end, into a slot of the shared-memory ring,
+// by one warp: pieces of 8 keys by TMA, a lane each, and the piece that itself wraps by the warp.  Everything is
+// asked for before anything is waited for: about 3,000 cycles, where one part after another took 8,000 (a ragged
+// batch over an odd ring 40.5 us, now 31.5).  Out of line: few tiles come here, and its code among the producer's
+// cost the other roles 14 % at 128 query rows.
 template <int D, bool is_v>
 __device__ __noinline__ void load_wrapped(const TreeParams& p, int r, int g, int blk0, int sl0, uint32_t dst, uint32_t full,
                                           uint64_t pol, int lane) {
     constexpr int KB = D / 64, nkeys = is_v ? kTile * 128 / D : kTile, nblk = is_v ? KB : 2, blk = nkeys * 128;
     const int64_t tok = static_cast<int64_t>(p.hkv) * D;
     const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(r) * p.ring * tok + static_cast<int64_t>(g) * D + blk0 * 64;
-    int whole = 0;
-    for (int a = 0; a < nkeys / 8; ++a) {
-        const int sl = (sl0 + 8 * a) % p.ring;
-        if (sl + 8 <= p.ring) {
-            ++whole;
-            continue;
-        }
-        // every load before the first store: one trip to memory
-        uint4 val[2 * nblk];
-#pragma unroll
-        for (int i = 0; i < 2 * nblk; ++i) {
-            const int e = lane + 32 * i, k = e / (8 * nblk), rem = e % (8 * nblk);
-            val[i] = ld_global_nc_v4(base + (sl + k) % p.ring * tok + rem * 8);
-        }
+    // piece `lane`: its ring slot, and whether it wraps
+    int mine = sl0 + 8 * lane;
+    if (mine >= p.ring) mine -= p.ring;
+    if (mine >= p.ring) mine %= p.ring;                  // rings shorter than a tile
+    const bool in = lane < nkeys / 8, whole = in && mine + 8 <= p.ring;
+    const uint32_t wholes = __ballot_sync(0xFFFFFFFFu, whole);
+    uint32_t split = __ballot_sync(0xFFFFFFFFu, in && !whole);
+    // the pieces that wrap, by asynchronous copies that take no registers, while the others are asked for
+    while (split != 0u) {
+        const int a = __ffs(split) - 1, sl = __shfl_sync(0xFFFFFFFFu, mine, a);
+        split &= split - 1;
 #pragma unroll
         for (int i = 0; i < 2 * nblk; ++i) {
             const int e = lane + 32 * i, k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
-            st_shared_v4(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), val[i].x, val[i].y, val[i].z, val[i].w);
+            int slot = sl + k;
+            if (slot >= p.ring) slot -= p.ring;
+            if (slot >= p.ring) slot %= p.ring;
+            cp_async_16(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), base + slot * tok + rem * 8);
         }
     }
+    // (the copies may land before the barrier is told how much to expect: its one arrival is still to come)
+    if (whole)
+        for (int b = 0; b < nblk; ++b)
+            tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, mine, blk0 + b, g, r, full, pol);
+    __syncwarp();
+    asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(full, whole * nblk * 1024);
+    if (lane == 0) mbar_arrive_expect_tx(full, __popc(wholes) * nblk * 1024);
     __syncwarp();
-    // one lane a piece (nkeys / 8 is at most 16)
-    if (lane < nkeys / 8) {
-        const int sl = (sl0 + 8 * lane) % p.ring;
-        if (sl + 8 <= p.ring)
-            for (int b = 0; b < nblk; ++b)
-                tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, sl, blk0 + b, g, r, full, pol);
-    }
 }
 
 template <int D, int QR>
