@@ -60,23 +60,24 @@ constexpr float kTreeLazy = 32.0f;
 // 32,000 keys, 16/8 heads: 75, 56 and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads,
 // 10,000 keys: 795, 617 and 549 us with 512, 1,024 and 2,048 (an earlier state of the kernel); a 1,024-key window:
 // one row of 16/8 heads 25 us with 512 and 33 with 1,024, 64 rows of 32/16 heads 316 and 295.
-constexpr int kSpanMin = 512, kSpanMax = 2048, kSpanLinear = 128, kSpanWindow = 32;
+constexpr int kSpanMinWindow = 256, kSpanMinLinear = 512, kSpanMax = 2048, kSpanLinear = 128, kSpanWindow = 64;
 __host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
     const int64_t want = keys * hq / (window ? kSpanWindow : kSpanLinear);
-    int len = kSpanMin;
+    int len = window ? kSpanMinWindow : kSpanMinLinear;
     while (len < kSpanMax && 2 * len <= want) len *= 2;
     return len;
 }
 
-// Spans of a row at (clamped) position p, given its first visible key: at least one, for the tree.
+// A row at (clamped) position p has tiles of 128 keys from its first visible one, and one of its tree's; they are
+// cut evenly into spans of at most a tile more than tree_span()'s keys: span s is tiles s * tiles / spans and up.
 __host__ __device__ inline int tree_first(int p, int win) { return win > 0 && p + 2 - win > 0 ? p + 2 - win : 0; }
 __host__ __device__ inline int64_t tree_keys(int p, int win) { return win > 0 ? win : static_cast<int64_t>(p) + 1; }
-__host__ __device__ inline int tree_spans(int p, int win, int hq) {
-    const int lo = tree_first(p, win);
-    if (lo > p) return 1;
-    const int len = tree_span(tree_keys(p, win), win > 0, hq);
-    return p / len - lo / len + 1;
+__host__ __device__ inline int tree_tiles(int p, int win) { return (max(p - tree_first(p, win) + 1, 0) + kTile - 1) / kTile + 1; }
+__host__ __device__ inline int tree_cut(int tiles, int64_t keys, int win, int hq) {
+    const int most = tree_span(keys, win > 0, hq) / kTile + 1;
+    return (tiles + most - 1) / most;
 }
+__host__ __device__ inline int tree_spans(int p, int win, int hq) { return tree_cut(tree_tiles(p, win), tree_keys(p, win), win, hq); }
 
 // A listed pair: row, span, first tile, ring tiles, tiles, position, nodes, first key, then the row's 128 parents
 // as bytes (255: a root).
@@ -201,7 +202,7 @@ constexpr int kNoMax = static_cast<int>(0xFF800000u) ^ 0x7FFFFFFF;
 
 // A published unit.  nt = 0 marks the end.
 struct TreeUnit {
-    int r, g, node0, span, t0, nring, nt, p, n, lo;
+    int r, g, node0, span, k0, nring, nt, p, n, lo;
 };
 
 __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restrict__ pos, const int32_t* __restrict__ parent,
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
     static_assert(kSpanMax / kTile + 1 < 32, "tiles of a pair");
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     struct Row {
-        int p, n, lo, len, spans;
+        int p, n, lo, tiles, spans;
     };
     auto row_at = [&](int r, int& bad) {
         Row x;
@@ -220,20 +221,10 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
         x.n = min(max(raw_n, 0), nodes);
         x.p = tree_pos(raw_p, win, ring);
         x.lo = tree_first(x.p, win);
-        x.len = tree_span(tree_keys(x.p, win), win > 0, hq);
+        x.tiles = tree_tiles(x.p, win);
         x.spans = x.n > 0 ? tree_spans(x.p, win, hq) : 0;
         bad |= (raw_n != x.n ? WA_STATUS_BAD_TREE : 0) | (raw_p != x.p ? WA_STATUS_BAD_POS : 0);
         return x;
-    };
-    // a span's first tile, ring tiles and all its tiles; the tree's own keys go with the row's last span
-    auto tiles = [&](const Row& x, int s, int& t0, int& nring) {
-        t0 = nring = 0;
-        if (x.lo <= x.p) {
-            const int64_t b = static_cast<int64_t>(x.lo / x.len + s) * x.len;
-            t0 = static_cast<int>(max(static_cast<int64_t>(x.lo), b)) / kTile;
-            nring = static_cast<int>(min(static_cast<int64_t>(x.p), b + x.len - 1)) / kTile - t0 + 1;
-        }
-        return nring + (s == x.spans - 1 ? 1 : 0);
     };
     // four parents a lane, as bytes
     auto parents = [&](int r) {
@@ -248,14 +239,13 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
     int4 raw = warp < rows ? parents(warp) : make_int4(-1, -1, -1, -1);
     if (t < 32) count[t] = 0;
     __syncthreads();
-    int bad = 0, t0, nring;
+    int bad = 0;
     for (int r = t; r < rows; r += 1024) {
         const Row x = row_at(r, bad);
         if (x.spans == 0) continue;
-        // the first span, the last one, and those between, which are full
-        atomicAdd(&count[tiles(x, 0, t0, nring)], 1);
-        if (x.spans > 1) atomicAdd(&count[tiles(x, x.spans - 1, t0, nring)], 1);
-        if (x.spans > 2) atomicAdd(&count[x.len / kTile], x.spans - 2);
+        const int more = x.tiles % x.spans;
+        atomicAdd(&count[x.tiles / x.spans], x.spans - more);
+        if (more > 0) atomicAdd(&count[x.tiles / x.spans + 1], more);
     }
     __syncthreads();
     if (warp == 0) {       // longest first: a pair goes after all longer ones
@@ -289,10 +279,11 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
             const int s = s0 + lane, left = min(32, x.spans - s0);
             int slot = 0;
             if (lane < left) {
-                const int nt = tiles(x, s, t0, nring);
+                const int t0 = static_cast<int>(static_cast<int64_t>(s) * x.tiles / x.spans);
+                const int nt = static_cast<int>(static_cast<int64_t>(s + 1) * x.tiles / x.spans) - t0;
                 slot = atomicAdd(&at[nt], 1);
                 int4* rec = reinterpret_cast<int4*>(list + static_cast<int64_t>(slot) * kPair);
-                rec[0] = make_int4(r, s, t0, nring);
+                rec[0] = make_int4(r, s, x.lo + t0 * kTile, nt - (s == x.spans - 1 ? 1 : 0));
                 rec[1] = make_int4(nt, x.p, x.n, x.lo);
             }
             for (int i = 0; i < left; ++i)
@@ -313,41 +304,42 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
 // asked for before anything is waited for: about 3,000 cycles, where one part after another took 8,000 (a ragged
 // batch over an odd ring 40.5 us, now 31.5).  Out of line: few tiles come here, and its code among the producer's
 // cost the other roles 14 % at 128 query rows.
-template <int D, bool is_v>
-__device__ __noinline__ void load_wrapped(const TreeParams& p, int r, int g, int blk0, int sl0, uint32_t dst, uint32_t full,
-                                          uint64_t pol, int lane) {
-    constexpr int KB = D / 64, nkeys = is_v ? kTile * 128 / D : kTile, nblk = is_v ? KB : 2, blk = nkeys * 128;
-    const int64_t tok = static_cast<int64_t>(p.hkv) * D;
-    const uint16_t* base = (is_v ? p.v : p.k) + static_cast<int64_t>(r) * p.ring * tok + static_cast<int64_t>(g) * D + blk0 * 64;
+constexpr int kPiece = 16;
+// `lg`: log2 of a key's 16-byte parts of the load; `base`: the first of them of key slot 0; `map`: boxes of kPiece
+// keys and 64 dims.  Loops are not unrolled: the code runs once or twice a call, from a cold instruction cache.
+__device__ __noinline__ void load_wrapped(const CUtensorMap* map, const uint16_t* base, int64_t tok, int ring, int nkeys, int lg,
+                                          int blk0, int g, int r, int sl0, uint32_t dst, uint32_t full, uint64_t pol) {
+    const int lane = static_cast<int>(threadIdx.x) & 31, blk = nkeys * 128;
     // piece `lane`: its ring slot, and whether it wraps
-    int mine = sl0 + 8 * lane;
-    if (mine >= p.ring) mine -= p.ring;
-    if (mine >= p.ring) mine %= p.ring;                  // rings shorter than a tile
-    const bool in = lane < nkeys / 8, whole = in && mine + 8 <= p.ring;
+    int mine = sl0 + kPiece * lane;
+    if (mine >= ring) mine -= ring;
+    if (mine >= ring) mine %= ring;                  // rings shorter than a tile
+    const bool in = lane * kPiece < nkeys, whole = in && mine + kPiece <= ring;
     const uint32_t wholes = __ballot_sync(0xFFFFFFFFu, whole);
     uint32_t split = __ballot_sync(0xFFFFFFFFu, in && !whole);
-    // the pieces that wrap, by asynchronous copies that take no registers, while the others are asked for
+    // the pieces that wrap, by asynchronous copies
     while (split != 0u) {
         const int a = __ffs(split) - 1, sl = __shfl_sync(0xFFFFFFFFu, mine, a);
         split &= split - 1;
-#pragma unroll
-        for (int i = 0; i < 2 * nblk; ++i) {
-            const int e = lane + 32 * i, k = e / (8 * nblk), rem = e % (8 * nblk), b = rem / 8, cc = rem % 8;
+#pragma unroll 1
+        for (int e = lane; e < kPiece << lg; e += 32) {
+            const int k = e >> lg, part = e & ((1 << lg) - 1);
             int slot = sl + k;
-            if (slot >= p.ring) slot -= p.ring;
-            if (slot >= p.ring) slot %= p.ring;
-            cp_async_16(dst + b * blk + (8 * a + k) * 128 + ((cc ^ k) * 16), base + slot * tok + rem * 8);
+            if (slot >= ring) slot -= ring;
+            if (slot >= ring) slot %= ring;
+            cp_async_16(dst + (part >> 3) * blk + (kPiece * a + k) * 128 + (((part & 7) ^ (k & 7)) * 16), base + slot * tok + part * 8);
         }
     }
-    // (the copies may land before the barrier is told how much to expect: its one arrival is still to come)
-    if (whole)
-        for (int b = 0; b < nblk; ++b)
-            tma_load_5d(dst + b * blk + lane * 1024, is_v ? &p.tv8 : &p.tk8, 0, mine, blk0 + b, g, r, full, pol);
+    // the others by TMA (which may land before the barrier is told how much to expect: its one arrival is still to
+    // come, and one more for each lane, once its own copies have landed)
+    if (whole) {
+#pragma unroll 1
+        for (int b = 0; b < 1 << (lg - 3); ++b)
+            tma_load_5d(dst + b * blk + lane * kPiece * 128, map, 0, mine, blk0 + b, g, r, full, pol);
+    }
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" :: "r"(full) : "memory");
     __syncwarp();
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(full, __popc(wholes) * nblk * 1024);
+    if (lane == 0) mbar_arrive_expect_tx(full, (__popc(wholes) * kPiece * 16) << lg);
     __syncwarp();
 }
 
@@ -396,7 +388,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     // Unit U as published; the caller arrives on its UFREE barrier when it has read what it needs.
     auto read_unit = [&](int U, TreeUnit& x) {
         volatile int* e = unit_ints(U);
-        x.r = e[0]; x.g = e[1] & 0xFFFF; x.node0 = e[1] >> 16; x.span = e[2]; x.t0 = e[3];
+        x.r = e[0]; x.g = e[1] & 0xFFFF; x.node0 = e[1] >> 16; x.span = e[2]; x.k0 = e[3];
         x.nring = e[4] & 0xFFFFFF; x.nt = x.nring + (e[4] >> 24); x.p = e[5]; x.n = e[6]; x.lo = e[7];
     };
     auto take_unit = [&](int U, TreeUnit& x) -> bool {
@@ -438,10 +430,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     if (slot0 < 0) tma_load_5d(dst, is_v ? &p.tvt : &p.tkt, 0, key, blk0, x.g, x.r, full, pol);
                     else tma_load_5d(dst, is_v ? &p.tv : &p.tk, 0, sl0, blk0, x.g, x.r, full, pol);
                 }
-            } else if (is_v) {
-                load_wrapped<D, true>(p, x.r, x.g, blk0, sl0, dst, full, pol, lane);
             } else {
-                load_wrapped<D, false>(p, x.r, x.g, blk0, sl0, dst, full, pol, lane);
+                const int64_t tok = static_cast<int64_t>(p.hkv) * D;
+                load_wrapped(is_v ? &p.tv8 : &p.tk8, (is_v ? p.v : p.k) + (static_cast<int64_t>(x.r) * p.ring * p.hkv + x.g) * D + blk0 * 64, tok, p.ring, nkeys,
+                             is_v && D == 256 ? 5 : 4, blk0, x.g, x.r, sl0, dst, full, pol);
             }
             __syncwarp();
             ++u;
@@ -455,7 +447,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             return ok;
         };
         // the ring slot of a unit's first tile, and of the tile after one
-        auto first_slot = [&](const TreeUnit& x) { return x.nring == 0 ? -1 : p.win > 0 ? x.t0 * kTile % p.ring : x.t0 * kTile; };
+        auto first_slot = [&](const TreeUnit& x) { return x.nring == 0 ? -1 : p.win > 0 ? x.k0 % p.ring : x.k0; };
         auto next_slot = [&](const TreeUnit& x, int idx, int slot0) {
             if (idx + 1 >= x.nring) return -1;
             int sl = slot0 + kTile;
@@ -530,6 +522,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             for (int kh = 0; kh < C::HV; ++kh) {
                 const int s = wrap(ks + kh);
                 if (!warp_wait(LOADBAR(C::B_KFULL, kh, t), LOADPH(t), p.status)) return false;
+                fence_proxy_async_smem();        // for load_wrapped's copies
                 tc_fence_after();
                 const uint32_t bk = desc_lo(SLOT(s), 16);
                 if (leader) {
@@ -622,7 +615,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     if (!(ok = warp_wait(LOADBAR(C::B_VFULL, hh, t), LOADPH(t), p.status))) break;
                     int z_lo, z_hi, z_end = C::VKEYS;       // rows [0, z_lo) and [z_hi, z_end) are cleared
                     if (idx < x.nring) {
-                        const int key0 = (x.t0 + idx) * kTile + hh * C::VKEYS;
+                        const int key0 = x.k0 + idx * kTile + hh * C::VKEYS;
                         z_lo = min(C::VKEYS, max(0, x.lo - key0));
                         z_hi = max(0, min(C::VKEYS, x.p - key0 + 1));
                     } else {
@@ -639,8 +632,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                             const int row = zr < z_lo ? zr : z_hi + (zr - z_lo);
                             st_shared_v4(vst + (rem / 8) * C::V_BLOCK + row * 128 + (rem % 8) * 16, 0u, 0u, 0u, 0u);
                         }
-                        fence_proxy_async_smem();
                     }
+                    fence_proxy_async_smem();        // for these, and for load_wrapped's copies
                     __syncwarp();
                     if (lane == 0) mbar_arrive(LOADBAR(C::B_VREADY, hh, t));
                 }
@@ -672,7 +665,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 x.node0 = rem % p.mtiles * p.npt;
                 x.r = __shfl_sync(0xFFFFFFFFu, field, 0);
                 x.span = __shfl_sync(0xFFFFFFFFu, field, 1);
-                x.t0 = __shfl_sync(0xFFFFFFFFu, field, 2);
+                x.k0 = __shfl_sync(0xFFFFFFFFu, field, 2);
                 x.nring = __shfl_sync(0xFFFFFFFFu, field, 3);
                 x.nt = __shfl_sync(0xFFFFFFFFu, field, 4);
                 x.p = __shfl_sync(0xFFFFFFFFu, field, 5);
@@ -691,7 +684,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             volatile int* e = unit_ints(pub);
             if (!ended) e[8 + lane] = par;
             if (lane == 0) {
-                e[0] = x.r; e[1] = x.g | (x.node0 << 16); e[2] = x.span; e[3] = x.t0;
+                e[0] = x.r; e[1] = x.g | (x.node0 << 16); e[2] = x.span; e[3] = x.k0;
                 e[4] = x.nring | ((x.nt - x.nring) << 24); e[5] = x.p; e[6] = x.n; e[7] = x.lo;
             }
             __syncwarp();
@@ -737,7 +730,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const float c = p.c;
         // a unit as this thread sees it
-        int t0 = 0, nring = 0, nt = 0, row_lo = 0, row_hi = 0;
+        int k0 = 0, nring = 0, nt = 0, row_lo = 0, row_hi = 0;
         uint32_t seen = 0;                                    // tree columns [col0, col0 + 32) that the row sees
         int first_full = 0, last_full = 0;                    // keys that every row of the warp sees
         bool live = false, idle = true;
@@ -746,7 +739,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (!warp_wait(BAR(C::B_UFULL + U % kUnits), static_cast<uint32_t>(U / kUnits) & 1u, p.status)) return false;
             TreeUnit x;
             read_unit(U, x);
-            t0 = x.t0;
+            k0 = x.k0;
             nring = x.nring;
             nt = x.nt;
             row_hi = x.p;
@@ -801,7 +794,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 tc_fence_after();
                 const uint32_t t_s = tbase + lane_addr + C::s_col(b) + col0;
                 // visible columns of this quarter as bits, unless every row sees them all
-                const int kbase = (t0 + idx) * kTile + col0;
+                const int kbase = k0 + idx * kTile + col0;
                 const bool masked = idx >= nring || kbase < first_full || kbase + 31 > last_full;
                 uint32_t vis = seen;
                 if (masked && idx < nring) {
@@ -1160,8 +1153,8 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, t.qn, whole ? KB : 1) ||
         !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, 2, 1) ||
         !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, C::VKEYS, KB, 1) ||
-        !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
-        !encode_5d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, 8, 1, 1) ||
+        !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
+        !encode_5d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
         !encode_5d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, false, kTile, 2, 1) ||
         !encode_5d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, false, C::VKEYS, KB, 1))
         return cudaErrorInvalidValue;
@@ -1225,15 +1218,13 @@ TreePlan tree_plan(int rows, int nodes, int hq, int hkv, int win, int ring) {
     pl.lanes = ((nodes < pl.npt ? nodes : pl.npt) * G + 31) / 32 * 32;
     pl.spans = 1;
     if (win > 0) {
-        // win - 1 keys from any position touch at most this many spans
-        const int len = tree_span(win, true, hq);
-        pl.spans = win > 1 ? (win - 2 + len - 1) / len + 1 : 1;
+        pl.spans = tree_spans(kTreeMaxPos, win, hq);       // any position with the whole window
     } else {
-        for (int len = kSpanMin; len <= kSpanMax; len *= 2) {
+        for (int len = kSpanMinLinear; len <= kSpanMax; len *= 2) {
             // the most keys with this span
             int64_t keys = len == kSpanMax ? ring : (2LL * kSpanLinear * len + hq - 1) / hq - 1;
             keys = keys < ring ? keys : ring;
-            const int spans = static_cast<int>((keys + len - 1) / len);
+            const int spans = tree_cut(static_cast<int>((keys + kTile - 1) / kTile) + 1, keys, win, hq);
             pl.spans = spans > pl.spans ? spans : pl.spans;
         }
     }

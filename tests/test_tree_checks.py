@@ -163,13 +163,12 @@ def test_calls_refuse_host_tensors_and_types():
 def _spans(p, win, hq):
     """Spans that a row at position p is cut into, from the documented rule: its own key count, window and hq."""
     lo = max(0, p + 2 - win) if win else 0
-    if lo > p:
-        return 1
-    want = win * hq // 32 if win else (p + 1) * hq // 128
-    length = 512
+    tiles = -(-max(p - lo + 1, 0) // 128) + 1
+    want = win * hq // 64 if win else (p + 1) * hq // 128
+    length = 256 if win else 512
     while length < 2048 and 2 * length <= want:
         length *= 2
-    return p // length - lo // length + 1
+    return -(-tiles // (length // 128 + 1))
 
 
 @pytest.mark.parametrize("win", [0, 1, 2, 300, 512, 513, 1000, 1024, 2049, 9000])
