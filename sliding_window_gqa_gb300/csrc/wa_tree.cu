@@ -312,8 +312,7 @@ __device__ __noinline__ void load_wrapped(const CUtensorMap* map, const uint16_t
     const int lane = static_cast<int>(threadIdx.x) & 31, blk = nkeys * 128;
     // piece `lane`: its ring slot, and whether it wraps
     int mine = sl0 + kPiece * lane;
-    if (mine >= ring) mine -= ring;
-    if (mine >= ring) mine %= ring;                  // rings shorter than a tile
+    while (mine >= ring) mine -= ring;               // more than once only where a ring is shorter than a tile
     const bool in = lane * kPiece < nkeys, whole = in && mine + kPiece <= ring;
     const uint32_t wholes = __ballot_sync(0xFFFFFFFFu, whole);
     uint32_t split = __ballot_sync(0xFFFFFFFFu, in && !whole);
@@ -325,8 +324,7 @@ __device__ __noinline__ void load_wrapped(const CUtensorMap* map, const uint16_t
         for (int e = lane; e < kPiece << lg; e += 32) {
             const int k = e >> lg, part = e & ((1 << lg) - 1);
             int slot = sl + k;
-            if (slot >= ring) slot -= ring;
-            if (slot >= ring) slot %= ring;
+            while (slot >= ring) slot -= ring;
             cp_async_16(dst + (part >> 3) * blk + (kPiece * a + k) * 128 + (((part & 7) ^ (k & 7)) * 16), base + slot * tok + part * 8);
         }
     }
@@ -420,10 +418,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const uint32_t dst = SLOT(s);
             const int blk0 = is_v ? 0 : half * 2, key = is_v ? half * C::VKEYS : 0, nkeys = is_v ? C::VKEYS : kTile;
             int sl0 = slot0 + key;
-            if (p.win > 0) {
-                if (sl0 >= p.ring) sl0 -= p.ring;
-                if (sl0 >= p.ring) sl0 %= p.ring;          // rings shorter than a tile
-            }
+            if (p.win > 0)
+                while (sl0 >= p.ring) sl0 -= p.ring;       // more than once only where a ring is shorter than a tile
             if (slot0 < 0 || p.win == 0 || sl0 + nkeys <= p.ring) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, C::SLOT);
@@ -451,10 +447,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         auto next_slot = [&](const TreeUnit& x, int idx, int slot0) {
             if (idx + 1 >= x.nring) return -1;
             int sl = slot0 + kTile;
-            if (p.win > 0 && sl >= p.ring) {
-                sl -= p.ring;
-                if (sl >= p.ring) sl %= p.ring;
-            }
+            if (p.win > 0)
+                while (sl >= p.ring) sl -= p.ring;
             return sl;
         };
         TreeUnit cur, nxt;
