@@ -7,28 +7,40 @@
 //
 // Split.  A key head's G query heads of 128 / G nodes make a tile of up to 128
 // query rows (tensor-memory lane m = node m / G, head m % G), so K and V are read
-// once for all of them.  A row's keys are cut into spans at multiples of
-// tree_span() keys, which depends on the row's own key count and hq; the tree's
-// own keys are one more 128-key tile of the last span.  A unit of work is (row,
-// key head, query tile, span); it leaves (m, l, O) in fp32 and tree_merge_kernel
-// joins a row's spans in order.  Nothing in a unit depends on the other rows, so
-// neither do the bits.
+// once for all of them.  A row's keys are taken in tiles of 128 from its first
+// visible one (a window of 1,024 keys from anywhere is then 8 tiles; cut at absolute
+// multiples it was 9 mostly, and a batch over a window 7 % slower), its tree's own
+// keys are one tile more, and the tiles are cut evenly into spans, whose number
+// depends on the row's own position, the window and hq.  A unit of work is (row, key
+// head, query tile, span); it leaves (m, l, O) in fp32 and tree_merge_kernel joins a
+// row's spans in order.  Nothing in a unit depends on the other rows, so neither do
+// the bits.
 //
-// tree_plan_kernel: one block lists the (row, span) pairs with any key, longest first, with all that a unit needs
-// of its row (position, nodes, parents), checks the rows' numbers for the status word, and clears the header.
+// What bounds it.  Up to 64 query rows a tile: the reads of K and V (a linear batch of
+// 16 rows, 16/8 heads of 256, 9,000 to 32,700 keys: 445 us, 91 % of the measured copy
+// rate over the whole call; 64 rows over a window of 1,024, 32/16 heads: 222 us, 73 %,
+// of which 25 us join the spans).  128 query rows at head dim 128: the softmax warps, whose
+// chain S -> P of a tile takes 2,500 cycles where its products take 1,536 (32 rows of
+// 64 nodes, 32/4 heads: 449 us; 268 us of products at the measured rate).  One
+// sequence over a window (20 us): start of three kernels, loads of one CTA (36 bytes a
+// cycle) and that chain.
+//
+// tree_plan_kernel: one block lists the (row, span) pairs, longest first, with all that a
+// unit needs of its row (position, nodes, parents), checks the rows' numbers for the status
+// word, and clears the header.
 // tree_kernel<D>: a persistent grid, one CTA an SM, 640 threads, that streams the
 // keys of its units without a break between units:
 //   warp 0      TMA producer: K and V through a ring of 32 KiB slots (head dim 256: half a
 //               tile's K or V each), in the order the tensor core reads them (K0, K1, V0,
 //               K2, V1, ...), on across unit ends.  A tile that wraps around the end of a
-//               ring is loaded in 8-row boxes; the one 8-row piece that holds the wrap
-//               itself is copied by the warp.
+//               ring goes through load_wrapped.
 //   warp 1      allocates tensor memory; one lane issues S(t) = Q K^T and
 //               O += P(t - NS + 1) V (two bf16 parts of P), commits free the slots.
 //   warp 2      zeroes V rows that no node of the row sees (stale ring slots, nodes
 //               past n), so that they never meet a zero probability as 0 * inf.
 //   warp 3      takes units from the list by a counter (long ones first: taken as they came, the
-//               last ones ended 10 % after the mean), publishes them through a ring of unit slots, and loads each unit's Q once the previous unit's last S is done.
+//               last ones ended 10 % after the mean), publishes them through a ring of unit
+//               slots, and loads each unit's Q once the previous unit's last S is done.
 //   warps 4..19 softmax, one query row a thread in four column quarters: mask,
 //               exponentials, P over S in tensor memory, a lazy rescale of O, and the
 //               unit's partial result.  Four warps share a row group, so that the chain
@@ -55,11 +67,12 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 // maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
 constexpr float kTreeLazy = 32.0f;
 
-// Keys a span, a power of two: keys * hq / 128 on a linear cache, win * hq / 32 on a window.  Short spans put a
+// Keys a span, a power of two: keys * hq / 128 on a linear cache, win * hq / 64 on a window.  Short spans put a
 // single row's keys on more SMs, long ones leave fewer partial results and fewer ends of the pipeline.  One row of
 // 32,000 keys, 16/8 heads: 75, 56 and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads,
-// 10,000 keys: 795, 617 and 549 us with 512, 1,024 and 2,048 (an earlier state of the kernel); a 1,024-key window:
-// one row of 16/8 heads 25 us with 512 and 33 with 1,024, 64 rows of 32/16 heads 316 and 295.
+// 10,000 keys: 795, 617 and 549 us with 512, 1,024 and 2,048 (an earlier state of the kernel).  A window of 1,024
+// with win * hq / 64 and / 32: one row of 16/8 heads 21 and 25 us, 64 rows of 32/16 heads 232 and 222; 13 ragged
+// rows of 24/8 heads, a window of 1,000: 27 and 28.5.  The rule sees no number of rows, so that a row's bits do not either.
 constexpr int kSpanMinWindow = 256, kSpanMinLinear = 512, kSpanMax = 2048, kSpanLinear = 128, kSpanWindow = 64;
 __host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
     const int64_t want = keys * hq / (window ? kSpanWindow : kSpanLinear);
@@ -79,7 +92,7 @@ __host__ __device__ inline int tree_cut(int tiles, int64_t keys, int win, int hq
 }
 __host__ __device__ inline int tree_spans(int p, int win, int hq) { return tree_cut(tree_tiles(p, win), tree_keys(p, win), win, hq); }
 
-// A listed pair: row, span, first tile, ring tiles, tiles, position, nodes, first key, then the row's 128 parents
+// A listed pair: row, span, first key, ring tiles, tiles, position, nodes, first key, then the row's 128 parents
 // as bytes (255: a root).
 constexpr int kPair = 8 + WA_TREE_MAX_NODES / 4;
 static_assert(kPair * 4 == kTreePairBytes, "workspace");
@@ -89,8 +102,7 @@ struct TreeParams {
     // [block][token][64] order that the tensor core reads, into one copy
     CUtensorMap tq;            // q: 64 x G heads x qn nodes x D / 64 blocks or one
     CUtensorMap tk, tv;        // rings: 128 keys x 2 blocks (K), VKEYS keys x all blocks (V)
-    CUtensorMap tk8;           // K ring in pieces of 8 keys x one block
-    CUtensorMap tv8;
+    CUtensorMap tkp, tvp;      // rings in pieces of kPiece keys x one block
     CUtensorMap tkt, tvt;      // nodes' keys and values, boxes as tk's and tv's
     const uint16_t* k;
     const uint16_t* v;
@@ -300,13 +312,15 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
 }
 
 // Keys at ring slots sl0, sl0 + 1, ... (sl0 < ring) that pass the ring's end, into a slot of the shared-memory ring,
-// by one warp: pieces of 8 keys by TMA, a lane each, and the piece that itself wraps by the warp.  Everything is
-// asked for before anything is waited for: about 3,000 cycles, where one part after another took 8,000 (a ragged
-// batch over an odd ring 40.5 us, now 31.5).  Out of line: few tiles come here, and its code among the producer's
-// cost the other roles 14 % at 128 query rows.
+// by one warp: pieces of kPiece keys by TMA, a lane each, and the piece that itself wraps by asynchronous copies;
+// nothing is waited for.  It takes the producer about 2,400 cycles: 150 for a copy of the warp, 70 for a box. The
+// slots come into range by subtraction: `x %= ring` under an `if` was run always, division and all (a batch over a
+// window 232 us, now 222).  Pieces of 8, 16 and 32 keys: 223.6, 221.5 and 226 us.  Out of line and not unrolled: few
+// tiles come here, once or twice a call, from a cold instruction cache, and among the producer's code it cost the
+// other roles 14 % at 128 query rows.
+// `lg`: log2 of a key's 16-byte parts of the load; `base`: the first of them of ring slot 0; `map`: boxes of kPiece
+// keys and 64 dims.
 constexpr int kPiece = 16;
-// `lg`: log2 of a key's 16-byte parts of the load; `base`: the first of them of key slot 0; `map`: boxes of kPiece
-// keys and 64 dims.  Loops are not unrolled: the code runs once or twice a call, from a cold instruction cache.
 __device__ __noinline__ void load_wrapped(const CUtensorMap* map, const uint16_t* base, int64_t tok, int ring, int nkeys, int lg,
                                           int blk0, int g, int r, int sl0, uint32_t dst, uint32_t full, uint64_t pol) {
     const int lane = static_cast<int>(threadIdx.x) & 31, blk = nkeys * 128;
@@ -428,7 +442,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 }
             } else {
                 const int64_t tok = static_cast<int64_t>(p.hkv) * D;
-                load_wrapped(is_v ? &p.tv8 : &p.tk8, (is_v ? p.v : p.k) + (static_cast<int64_t>(x.r) * p.ring * p.hkv + x.g) * D + blk0 * 64, tok, p.ring, nkeys,
+                load_wrapped(is_v ? &p.tvp : &p.tkp, (is_v ? p.v : p.k) + (static_cast<int64_t>(x.r) * p.ring * p.hkv + x.g) * D + blk0 * 64, tok, p.ring, nkeys,
                              is_v && D == 256 ? 5 : 4, blk0, x.g, x.r, sl0, dst, full, pol);
             }
             __syncwarp();
@@ -1147,8 +1161,8 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     if (!encode_5d(&t.tq, a.q, D, a.hq, a.nodes, a.rows, a.q_tok, a.q_row, true, G, t.qn, whole ? KB : 1) ||
         !encode_5d(&t.tk, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kTile, 2, 1) ||
         !encode_5d(&t.tv, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, C::VKEYS, KB, 1) ||
-        !encode_5d(&t.tk8, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
-        !encode_5d(&t.tv8, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
+        !encode_5d(&t.tkp, a.k, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
+        !encode_5d(&t.tvp, a.v, D, a.hkv, a.ring, a.rows, ktok, krow, false, kPiece, 1, 1) ||
         !encode_5d(&t.tkt, a.kt, D, a.hkv, a.nodes, a.rows, a.kt_tok, a.kt_row, false, kTile, 2, 1) ||
         !encode_5d(&t.tvt, a.vt, D, a.hkv, a.nodes, a.rows, a.vt_tok, a.vt_row, false, C::VKEYS, KB, 1))
         return cudaErrorInvalidValue;
