@@ -316,7 +316,6 @@ int wa_tree_verify(const float* target, const float* draft, const int32_t* paren
     a.rows = rows; a.nodes = nodes; a.vocab = vocab;
     a.path = path; a.length = length; a.token = token;
     a.hdr = static_cast<wa::WsHeader*>(ws);
-    if (cudaMemsetAsync(ws, 0, wa::kHeaderBytes, s) != cudaSuccess) return WA_ECUDA;
     if (wa::launch_verify(a, s) != cudaSuccess) return WA_ECUDA;
     return WA_OK;
 }

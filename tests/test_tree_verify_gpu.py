@@ -214,3 +214,17 @@ def test_result_does_not_depend_on_the_rows_around_it(wa):
         one = wa.tree_verify(*[c[x][3:4].contiguous() for x in ("target", "parent", "tokens", "u")],
                              draft=None if draft is None else draft[3:4].contiguous())
         assert [t.tolist() for t in one] == [w[3:4] for w in want]
+
+
+def test_a_single_rows_status(wa):
+    """One row clears the workspace's status itself: whatever a call before left, or fresh memory holds."""
+    good = make(1, 6, 3001, seed=8)
+    bad = dict(good, tokens=good["tokens"].clone(), target=torch.zeros_like(good["target"]))
+    bad["tokens"][0, 3] = -5
+    ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+    for c, want in ((good, 0), (bad, wa.WA_STATUS_BAD_TREE | wa.WA_STATUS_NO_MASS), (good, 0)):
+        path, length, token = wa.tree_verify(c["target"], c["parent"], c["tokens"], c["u"], draft=c["draft"], ws=ws)
+        assert wa.status(ws) == want
+        ref = tree.verify(c["target"].cpu().numpy(), c["draft"].cpu().numpy(), c["parent"].tolist(), c["tokens"].tolist(),
+                          c["u"].cpu().numpy())
+        assert (path.tolist(), length.tolist(), token.tolist()) == ref
