@@ -1030,27 +1030,25 @@ constexpr int kMergeSpans = 2;
 // o = sum_s a_s O_s / sum_s a_s l_s over a row's spans in order, a_s = 2^(m_s - M).  A block takes 32 query
 // rows (lanes) and 64 dims (8 a warp) of a tile, reads the partial results in the order they were stored
 // (512 bytes a warp and load, kMergeSpans spans in flight), and turns them round in shared memory for the output.
-// A row with a value that is not finite is computed again in float64.
+// A row with a value that is not finite is computed again in float64.  Issue bound it when each block worked out its
+// place and each output its quotient by divisions: 64 rows over a window, 32/16 heads, 222 us a call, now 217; five
+// blocks an SM 217.3, six (spills) 218.5, four 216.9.
 template <int D>
-__global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* part_o, const float4* part_l, const float* part_m,
+__global__ void __launch_bounds__(256, 5) tree_merge_kernel(const float4* part_o, const float4* part_l, const float* part_m,
                                                             const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans,
-                                                            int lanes) {
+                                                            int lanes, int G, int by_quarters, int by_group) {
     __shared__ __align__(16) uint8_t tile[32 * 144];
     __shared__ int bad[32];
     __shared__ TreeRerun again;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int quarters = lanes >> 5;
-    int k = blockIdx.x;
-    const int qd = k % quarters;
-    k /= quarters;
-    const int64_t unit0 = static_cast<int64_t>(k) * spans;
-    const int mt = k % mtiles;
-    k /= mtiles;
-    const int g = k % a.hkv, r = k / a.hkv;
-    const int G = a.hq / a.hkv, node0 = mt * npt;
+    // x / quarters and x / G by a factor, for x below 2^7 (a runtime division takes 30 instructions or more)
+    const int quarters = lanes >> 5, r = blockIdx.x, g = blockIdx.y, z = blockIdx.z / (D / 64), db = blockIdx.z % (D / 64);
+    const int mt = z * by_quarters >> 16, qd = z - mt * quarters, node0 = mt * npt;
+    auto node_of = [&](int row) { return row * by_group >> 16; };
+    const int64_t unit0 = ((static_cast<int64_t>(r) * a.hkv + g) * mtiles + mt) * spans;
     const int n = min(a.n ? __ldg(a.n + r) : a.nodes, a.nodes);
     const int count = tree_spans(tree_pos(__ldg(a.pos + r), a.win, a.ring), a.win, a.hq);
-    const int first = qd * 32 / G;                        // the block's first node
+    const int first = node_of(qd * 32);                        // the block's first node
     if (t < 32) bad[t] = 0;
     // The partial results (plain pointers: they are written while this kernel is there already, so no load may go
     // the read-only way or before this line).  Blocks without work wait too: nothing behind the call starts early.
@@ -1058,7 +1056,7 @@ __global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* part_o
     if (first >= npt || node0 + first >= n) return;
     __syncthreads();
     const int64_t rec = unit0 * lanes + qd * 32 + lane;
-    const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + blockIdx.y * 16 + warp * 2) * 32 + lane;
+    const float4* po = part_o + ((unit0 * quarters + qd) * (D / 4) + db * 16 + warp * 2) * 32 + lane;
     const int64_t ostep = static_cast<int64_t>(quarters) * (D / 4) * 32;
     float M = -INFINITY, den = 0.f, num[8];
 #pragma unroll
@@ -1101,11 +1099,12 @@ __global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* part_o
         }
     }
     const int row = qd * 32 + lane;
-    const bool live = row / G < npt && node0 + row / G < n;
+    const bool live = node_of(row) < npt && node0 + node_of(row) < n;
     bool nonfinite = false;
+    const float inv = __frcp_rn(den);        // two roundings of 2^-24 each, beside the output's 2^-9
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        num[e] = __fdiv_rn(num[e], den);
+        num[e] *= inv;
         nonfinite |= !isfinite(num[e]);
     }
     if (live && nonfinite) bad[lane] = 1;
@@ -1113,18 +1112,18 @@ __global__ void __launch_bounds__(256, 6) tree_merge_kernel(const float4* part_o
         make_uint4(pack_bf16(num[0], num[1]), pack_bf16(num[2], num[3]), pack_bf16(num[4], num[5]), pack_bf16(num[6], num[7]));
     const int any = __syncthreads_or(live && nonfinite);
     {   // eight threads a row
-        const int m = qd * 32 + t / 8, rn = m / G;
+        const int m = qd * 32 + t / 8, rn = node_of(m);
         if (rn < npt && node0 + rn < n && !bad[t / 8]) {
             uint16_t* orow = static_cast<uint16_t*>(a.out) + r * a.o_row + (node0 + rn) * a.o_tok +
-                             static_cast<int64_t>(g * G + m % G) * D + blockIdx.y * 64;
+                             static_cast<int64_t>(g * G + m - rn * G) * D + db * 64;
             reinterpret_cast<uint4*>(orow)[t % 8] = *reinterpret_cast<const uint4*>(tile + t / 8 * 144 + t % 8 * 16);
         }
     }
     if (!any) return;
     for (int i = 0; i < 32; ++i) {
         if (!bad[i]) continue;
-        const int m = qd * 32 + i;
-        tree_rerun(a, again, r, node0 + m / G, g * G + m % G, blockIdx.y * 64);
+        const int m = qd * 32 + i, rn = node_of(m);
+        tree_rerun(a, again, r, node0 + rn, g * G + m - rn * G, db * 64);
         __syncthreads();
     }
 }
@@ -1201,12 +1200,13 @@ cudaError_t launch_tree_d(const TreeArgs& a, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, tree_kernel<D, QR>, t);
     if (e != cudaSuccess) return e;
-    const dim3 mgrid(static_cast<unsigned>(a.rows) * a.hkv * pl.mtiles * (pl.lanes / 32), D / 64);
-    cfg.gridDim = mgrid;
+    const int quarters = pl.lanes / 32;
+    cfg.gridDim = dim3(a.rows, a.hkv, pl.mtiles * quarters * (D / 64));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, const_cast<const float4*>(t.part_o), const_cast<const float4*>(t.part_l),
-                           const_cast<const float*>(t.part_m), a, pl.npt, pl.mtiles, pl.spans, pl.lanes);
+                           const_cast<const float*>(t.part_m), a, pl.npt, pl.mtiles, pl.spans, pl.lanes, G,
+                           (65536 + quarters - 1) / quarters, (65536 + G - 1) / G);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

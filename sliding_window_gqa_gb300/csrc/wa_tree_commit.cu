@@ -3,8 +3,9 @@
 // Node path[r, j] of row r goes to slot (pos[r] + 1 + j) mod ring, j < length[r]: a copy of hkv * d bf16 values a
 // (layer, K or V, row, j), bound by latency for one sequence (the row's numbers, then its path, then the data) and
 // by HBM for many.  A block takes kNodes nodes of one (layer, K or V, row), so the numbers are fetched once for
-// them and all of a node's 16-byte pieces are in flight together (a block a node left 7 waves of blocks to launch
-// for 12 layers of 48 rows: 16.5 us against 14.7).  Where length exceeds the ring, the nodes that a later one would
+// them; its warps divide among the nodes, so that slots and addresses are computed once a warp and not for every 16
+// bytes, which bound it before (12 layers of 48 rows, 8 heads of 256: 11.7 us, 15.1 with a division a piece, 16.5
+// with a block a node; one row and layer 3.1 us).  Where length exceeds the ring, the nodes that a later one would
 // overwrite are left out, so no two blocks write one slot.
 //
 // The status word is written by block 0 alone, which looks through every row's numbers, so that a call is one
@@ -29,34 +30,30 @@ __device__ __forceinline__ int row_faults(const CommitArgs& a, int r) {
 
 __global__ void __launch_bounds__(kCommitThreads, 4) commit_kernel(const __grid_constant__ CommitArgs a, int groups, int one_block) {
     const int r = blockIdx.x / groups, j0 = blockIdx.x % groups * kNodes;
-    const int l = blockIdx.y, kv = blockIdx.z, t = threadIdx.x;
+    const int l = blockIdx.y, kv = blockIdx.z, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const bool first = blockIdx.x == 0 && l == 0 && kv == 0;
+    const int32_t* path = a.path + static_cast<int64_t>(r) * a.most + j0;
+    const int entry = lane < kNodes && j0 + lane < a.most ? path[lane] : -1;
     const int p = a.pos[r], len = min(max(a.length[r], 0), a.most);
-    const int j1 = min(j0 + kNodes, len);
-    if (p >= -1 && j0 < j1) {
-        const int ring = a.ring[l];
-        const int pieces = a.hkv * a.d / 8;        // 16 bytes each
-        const uint16_t* src = static_cast<const uint16_t*>(a.src[kv][l]) + r * a.row[kv];
-        uint4* dst = reinterpret_cast<uint4*>(a.dst[kv][l]) + static_cast<int64_t>(r) * ring * pieces;
-        const int32_t* path = a.path + static_cast<int64_t>(r) * a.most;
-        // pieces of all the block's nodes in a row, two at a time loaded before they are stored
-        const int total = (j1 - j0) * pieces;
-        for (int e0 = t; e0 < total; e0 += 2 * kCommitThreads) {
-            uint4 v[2];
-            int64_t to[2];
+    const int count = min(kNodes, len - j0);
+    if (p >= -1 && count > 0) {
+        // 16 warps: 16, 8, 4, 2 or 1 a node
+        const int sh = count > 8 ? 0 : count > 4 ? 1 : count > 2 ? 2 : count > 1 ? 3 : 4;
+        const int i = warp >> sh, j = j0 + i, node = __shfl_sync(0xFFFFFFFFu, entry, i), ring = a.ring[l];
+        if (i < count && node >= 0 && node < a.nodes && j >= len - ring) {
+            const int pieces = a.hkv * a.d / 8, step = 32 << sh;        // of 16 bytes
+            const uint32_t slot = (static_cast<uint32_t>(p) + 1u + static_cast<uint32_t>(j)) % static_cast<uint32_t>(ring);
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.src[kv][l]) + r * a.row[kv] + node * a.tok[kv]);
+            uint4* dst = reinterpret_cast<uint4*>(a.dst[kv][l]) + (static_cast<int64_t>(r) * ring + slot) * pieces;
+            for (int c = (warp & ((1 << sh) - 1)) * 32 + lane; c < pieces; c += 4 * step) {
+                uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = e0 + i * kCommitThreads, j = j0 + e / pieces, c = e % pieces;
-                const int node = e < total ? path[j] : -1;
-                to[i] = -1;
-                if (node >= 0 && node < a.nodes && j >= len - ring) {
-                    to[i] = (static_cast<int64_t>(p) + 1 + j) % ring * pieces + c;
-                    v[i] = *reinterpret_cast<const uint4*>(src + node * a.tok[kv] + static_cast<int64_t>(c) * 8);
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (c + e * step < pieces) v[e] = src[c + e * step];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e * step < pieces) dst[c + e * step] = v[e];
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (to[i] >= 0) dst[to[i]] = v[i];
         }
     }
     if (one_block ? !first : l != 0 || kv != 0) return;
@@ -72,10 +69,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) commit_kernel(const __grid_
         if (t == 0) a.hdr->status = (tree ? WA_STATUS_BAD_TREE : 0) | (pos ? WA_STATUS_BAD_POS : 0);
     } else {
         if (t == 0 && j0 == 0) bad = row_faults(a, r);
-        if (p >= -1 && t < j1 - j0) {
-            const int node = a.path[static_cast<int64_t>(r) * a.most + j0 + t];
-            if (node < 0 || node >= a.nodes) bad |= WA_STATUS_BAD_TREE;
-        }
+        if (p >= -1 && t < count && (entry < 0 || entry >= a.nodes)) bad |= WA_STATUS_BAD_TREE;
         if (bad) atomicOr(&a.hdr->status, bad);
     }
 }
