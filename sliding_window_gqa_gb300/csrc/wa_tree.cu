@@ -17,13 +17,13 @@
 // the bits.
 //
 // What bounds it.  Up to 64 query rows a tile: the reads of K and V (a linear batch of
-// 8 rows, 32/16 heads of 256, 9,000 to 32,700 keys: 445 us, 91 % of the measured copy
-// rate over the whole call; 64 rows over a window of 1,024, 32/16 heads: 222 us, 73 %,
-// of which 25 us join the spans).  128 query rows at head dim 128: the softmax warps, whose
-// chain S -> P of a tile takes 2,500 cycles where its products take 1,536 (32 rows of
-// 64 nodes, 32/4 heads: 449 us; 268 us of products at the measured rate).  One
-// sequence over a window (20 us): start of three kernels, loads of one CTA (36 bytes a
-// cycle) and that chain.
+// 8 rows, 32/16 heads of 256, 9,000 to 32,700 keys: 440 us, 92 % of the measured copy
+// rate over the whole call; 64 rows over a window of 1,024, 32/16 heads: 217 us, 75 %,
+// the rest being the start and the join of the spans).  128 query rows at head dim 128:
+// the softmax warps, whose chain S -> P of a tile takes 2,500 cycles where its products
+// take 1,536 (32 rows of 64 nodes, 32/4 heads: 447 us; 268 us of products at the measured
+// rate).  One sequence over a window (19 us): the start of three kernels, one CTA's loads
+// (36 bytes a cycle) and that chain.
 //
 // tree_plan_kernel: one block lists the (row, span) pairs, longest first, with all that a
 // unit needs of its row (position, nodes, parents), checks the rows' numbers for the status
