@@ -82,7 +82,8 @@ __host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
 }
 
 // A row at (clamped) position p has tiles of 128 keys from its first visible one, and one of its tree's; they are
-// cut evenly into spans of at most a tile more than tree_span()'s keys: span s is tiles s * tiles / spans and up.
+// cut evenly into spans of at most a tile more than tree_span()'s keys, the longer ones last (the tree's tile is little
+// to read: with the longer ones first a batch over a window took 226 us instead of 217).
 __host__ __device__ inline int tree_first(int p, int win) { return win > 0 && p + 2 - win > 0 ? p + 2 - win : 0; }
 __host__ __device__ inline int64_t tree_keys(int p, int win) { return win > 0 ? win : static_cast<int64_t>(p) + 1; }
 __host__ __device__ inline int tree_tiles(int p, int win) { return (max(p - tree_first(p, win) + 1, 0) + kTile - 1) / kTile + 1; }
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
     static_assert(kSpanMax / kTile + 1 < 32, "tiles of a pair");
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     struct Row {
-        int p, n, lo, tiles, spans;
+        int p, n, lo, spans, each, more;       // the last `more` spans have each + 1 tiles, the others each
     };
     auto row_at = [&](int r, int& bad) {
         Row x;
@@ -233,8 +234,10 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
         x.n = min(max(raw_n, 0), nodes);
         x.p = tree_pos(raw_p, win, ring);
         x.lo = tree_first(x.p, win);
-        x.tiles = tree_tiles(x.p, win);
-        x.spans = x.n > 0 ? tree_spans(x.p, win, hq) : 0;
+        const int tiles = tree_tiles(x.p, win), spans = tree_cut(tiles, tree_keys(x.p, win), win, hq);
+        x.spans = x.n > 0 ? spans : 0;
+        x.each = tiles / spans;
+        x.more = tiles - x.each * spans;
         bad |= (raw_n != x.n ? WA_STATUS_BAD_TREE : 0) | (raw_p != x.p ? WA_STATUS_BAD_POS : 0);
         return x;
     };
@@ -255,9 +258,8 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
     for (int r = t; r < rows; r += 1024) {
         const Row x = row_at(r, bad);
         if (x.spans == 0) continue;
-        const int more = x.tiles % x.spans;
-        atomicAdd(&count[x.tiles / x.spans], x.spans - more);
-        if (more > 0) atomicAdd(&count[x.tiles / x.spans + 1], more);
+        atomicAdd(&count[x.each], x.spans - x.more);
+        if (x.more > 0) atomicAdd(&count[x.each + 1], x.more);
     }
     __syncthreads();
     if (warp == 0) {       // longest first: a pair goes after all longer ones
@@ -291,8 +293,7 @@ __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restri
             const int s = s0 + lane, left = min(32, x.spans - s0);
             int slot = 0;
             if (lane < left) {
-                const int t0 = static_cast<int>(static_cast<int64_t>(s) * x.tiles / x.spans);
-                const int nt = static_cast<int>(static_cast<int64_t>(s + 1) * x.tiles / x.spans) - t0;
+                const int extra = s - (x.spans - x.more), t0 = s * x.each + max(extra, 0), nt = x.each + (extra >= 0 ? 1 : 0);
                 slot = atomicAdd(&at[nt], 1);
                 int4* rec = reinterpret_cast<int4*>(list + static_cast<int64_t>(slot) * kPair);
                 rec[0] = make_int4(r, s, x.lo + t0 * kTile, nt - (s == x.spans - 1 ? 1 : 0));
