@@ -284,7 +284,7 @@ size_t wa_tree_decode_ws_bytes(int32_t rows, int32_t nodes, int32_t hq, int32_t 
  *                          0 .. n[r]-1.  Outside [0, nodes]: clamped, BAD_TREE
  *   out     [rows, nodes, hq, d]   bf16; nodes >= n[r] are left as they were
  *
- * Probabilities enter P V as two bf16 parts whose sum is within 2^-16 of them,
+ * Probabilities enter P V as two bf16 parts whose sum is within 2^-17 of them,
  * as in wa_decode's tensor-core form.  The softmax runs over 128-key tiles from
  * the row's first visible key, in spans that depend on the row's own position,
  * the window and hq alone: an output's bits do not depend on the batch, the

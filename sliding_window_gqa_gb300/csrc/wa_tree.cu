@@ -892,18 +892,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_PHALF + b));
                 }
-                // P over this quarter's own columns of S: hi in the first 16, lo in the others.  hi is p cut to 8
-                // bits (its upper half), lo the rest rounded to bf16, so their sum is within 2^-16 of p, which
-                // keeps the output to the decode form's accuracy (one part alone: 2^-9).
+                // P over this quarter's own columns of S: hi = bf16(p) in the first 16, lo = bf16(p - hi) in the others,
+                // so their sum is within 2^-17 of p, as in the one-token decode (one part alone: 2^-8).  hi as p's upper
+                // half, cut and not rounded, would leave twice the error.
                 {
                     uint32_t w[32];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float a = sv[2 * e], bb = sv[2 * e + 1];
                         float ra, rb;                       // exact
-                        w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(bb), 0x7632);
-                        fma_x2(ra, rb, __uint_as_float(__float_as_uint(a) & 0xFFFF0000u),
-                               __uint_as_float(__float_as_uint(bb) & 0xFFFF0000u), -1.f, -1.f, a, bb);
+                        w[e] = pack_bf16(a, bb);
+                        fma_x2(ra, rb, __uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u), -1.f, -1.f, a, bb);
                         w[16 + e] = pack_bf16(ra, rb);
                     }
                     tmem_st32(t_s, w);

@@ -356,3 +356,36 @@ def test_beside_the_other_tensor_core_kernels(wa):
     assert all(_eq(a, b) for a, b in zip(got, want))
     again = _run(wa, c)                  # the ordinary call's way gives the same bits as the one with a stream
     assert _eq(again, want[0])
+
+
+def test_weights_enter_the_products_within_half_a_step_of_two_parts(wa):
+    """A root sees one ring key of weight 1 and itself with weight p = e^s in (1/2, 1), s a bf16 number, so scores
+    are exact; the ring's value is a, the node's -b, with b near a / p, so that what is left of a - p b shows p's error.
+
+    Tolerance, before the first run: p in two bf16 parts is off by at most 2^-18 here (the first part by half of its
+    step 2^-8, so the rest is at most 2^-9 and its step 2^-17); the exponential by 2^-22 and its argument's roundings by
+    less; products are exact, and each of the few fp32 sums of terms up to 2 is off by at most 2^-23 (one that cuts, at
+    |terms| up to 2), 2^-21 in all.  Over l = 1 + p >= 1.5 and with b <= 4: (4 (2^-18 + 2^-21) + 2^-21) / l, the l's own
+    2^-23 of a result below 2^-6, and the output's rounding: 2^-8 of its value at most."""
+    rows, nodes, heads, d = 4, 128, 2, 128
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    s = (-0.69 * torch.rand((rows, nodes, heads), generator=gen, device="cuda")).to(torch.bfloat16)
+    p = s.double().exp()
+    assert p.min() > 0.5
+    q = torch.zeros((rows, nodes, heads, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    kt = torch.zeros_like(q)
+    kt[..., 0] = s
+    a = (1.0 + torch.arange(d, device="cuda") / 128.0).to(torch.bfloat16)
+    b = (a.double() / p[..., None]).to(torch.bfloat16)
+    k = torch.zeros((rows, 1, heads, d), dtype=torch.bfloat16, device="cuda")
+    v = a.expand(rows, 1, heads, d).contiguous()
+    pos = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    parent = torch.full((rows, nodes), -1, dtype=torch.int32, device="cuda")
+    got = wa.tree_decode(q, k, v, kt, -b, pos, parent, 0).double()
+    l = 1.0 + p[..., None]
+    want = (a.double() - p[..., None] * b.double()) / l
+    assert want.abs().max() < 2 ** -6
+    tol = (b.double() * (2 ** -18 + 2 ** -21) + 2 ** -21) / l + want.abs() * (2 ** -8 + 2 ** -17)
+    off = (got - want).abs() / tol
+    assert off.max() <= 1.0, (off.max().item(), (off > 1).double().mean().item())
