@@ -341,8 +341,10 @@ typedef struct wa_verify_strides {
  *   token   [rows]         int32, written: the token after the last kept node; -1 where
  *                          n[r] is 0 or the distribution has no mass (WA_STATUS_NO_MASS)
  *
- * Probabilities that are NaN or below 0 count as 0, those above 1 as 1.  Sums
- * carry about 46 bits in a fixed order.  All pointers are device pointers;
+ * Probabilities that are NaN or below 0 count as 0, those above 1 as 1.  A
+ * weight W(x) is within 2^-45 p(x) of its value, sums carry about 46 bits in a
+ * fixed order: a random number whose place is within about 2^-42 (of probability
+ * 1) of a border may fall on its other side.  All pointers are device pointers;
  * 1 <= nodes <= WA_TREE_MAX_NODES, 1 <= vocab <= 2^24.
  */
 int wa_tree_verify(const float* target, const float* draft, const int32_t* parent, const int32_t* tokens,

@@ -24,9 +24,12 @@
 //     changes its own stretch.
 //
 // All arithmetic is in hi + lo fp32 pairs (about 46 bits), two tokens an instruction where it
-// counts: the fp64 pipe of this GPU has a fiftieth of the fp32 rate.  So a border of the running sum that 64 bits would place on one
-// side of a random number stays on that side but for numbers within about 2^-40 of it.
-// Their order is fixed by vocab alone, whatever the cluster.
+// counts: the fp64 pipe of this GPU has a fiftieth of the fp32 rate.  A weight is off by at most 2^-45 p(x) and by q(x)
+// times S's error, 2^-47 a dropped child; a weight that is not 0 enters the sums as hi > 0 with |lo| <= 2^-24 hi, so that
+// hi alone says whether a sum, however small, has any weight.  So the token differs from the one that 64 bits would
+// choose only where a random number's place in the running sum is within about 2^-42 of a border: that is of
+// probability 1, not of what the drafts have left of it.  The order of the sums is fixed by vocab alone, whatever the
+// cluster.
 #include <cuda_runtime.h>
 
 #include "wa_internal.h"
@@ -99,7 +102,7 @@ __device__ __forceinline__ void pair_add2(Two& hi, Two& lo, const Two& d, const 
     hi = t;
 }
 
-// weight_pair of two tokens, not brought to the form |e| << |d|; ns* = -S.
+// weight_pair of two tokens; ns* = -S.
 __device__ __forceinline__ void weight_pair2(const Two& p, const Two& q, const Two& sh, const Two& nsh, const Two& nsl, Two& d, Two& e) {
     const Two m = mul2(sh, q);
     const Two nme = fma2(nsl, q, fma2(nsh, q, m));                 // m - S q
@@ -107,6 +110,8 @@ __device__ __forceinline__ void weight_pair2(const Two& p, const Two& q, const T
     const Two b = sub2(d, p);
     e = add2(sub2(sub2(p, sub2(d, b)), add2(m, b)), nme);
     const Two h = add2(d, e);
+    e = sub2(e, sub2(h, d));
+    d = h;
     if (!(h.a > 0.f)) d.a = e.a = 0.f;
     if (!(h.b > 0.f)) d.b = e.b = 0.f;
 }

@@ -228,3 +228,68 @@ def test_a_single_rows_status(wa):
         ref = tree.verify(c["target"].cpu().numpy(), c["draft"].cpu().numpy(), c["parent"].tolist(), c["tokens"].tolist(),
                           c["u"].cpu().numpy())
         assert (path.tolist(), length.tolist(), token.tolist()) == ref
+
+
+def near(rows, V, k, seed, device="cuda"):
+    """A target and a draft within 1e-8 to 1e-5 of it (relative to each token's own probability), and k siblings below
+    node 0 that hold tokens of which the draft has more: all are dropped, and what is left of the target is small."""
+    gen = torch.Generator().manual_seed(seed)
+    p = torch.softmax(2.0 * torch.randn((rows, V), generator=gen, dtype=torch.float64), -1).float()
+    size = 10.0 ** (-8.0 + 3.0 * torch.rand((rows, 1), generator=gen, dtype=torch.float64))
+    q = (p.double() * (1.0 + size * torch.randn((rows, V), generator=gen, dtype=torch.float64))).float()
+    over = (q > p).double() + 1e-30
+    tokens = torch.cat([torch.zeros((rows, 1), dtype=torch.int64), torch.multinomial(over, k, True, generator=gen)], 1)
+    u = torch.full((rows, k + 1), 1.0 - 2.0 ** -24)
+    u[:, 0] = torch.rand(rows, generator=gen)
+    parent = torch.zeros((rows, k + 1), dtype=torch.int32)
+    parent[:, 0] = -1
+    c = dict(target=p[:, None].expand(rows, k + 1, V), draft=q[:, None].expand(rows, k + 1, V), parent=parent,
+             tokens=tokens.int(), u=u)
+    return {n: t.contiguous().to(device) for n, t in c.items()}
+
+
+def dropped(c, tol):
+    """The definition in float64 for rows of near(): what is left of the target once every child is dropped, and the
+    rows of which it is sure, if weights, sums and S q may be off by tol, that all of them are."""
+    p, q = c["target"][:, 0].double(), c["draft"][:, 0].double()
+    rows, k = p.shape[0], c["u"].shape[1] - 1
+    row = torch.arange(rows, device=p.device)
+    w, S = p, torch.zeros(rows, 1, dtype=torch.float64, device=p.device)
+    s = torch.ones_like(S)
+    sure = torch.ones(rows, dtype=torch.bool, device=p.device)
+    for i in range(1, k + 1):
+        x = c["tokens"][:, i].long()
+        test = c["u"][:, i].double() * q[row, x] * s[:, 0] - w[row, x]
+        sure &= (test > tol) | ((test >= 0) & ((p - S * q)[row, x] < -tol * p[row, x]))
+        left = (p - (S + s) * q).clamp_min(0)
+        mass = left.sum(1, keepdim=True)
+        near_0 = ((p - (S + s) * q).abs() <= tol * p).any(1) & (S + s != 1)[:, 0]
+        sure &= (mass[:, 0] > tol) | ((mass[:, 0] == 0) & ~near_0)
+        on = mass > 0
+        w, S, s = torch.where(on, left, w), torch.where(on, S + s, S), torch.where(on, mass, s)
+    return w, sure
+
+
+@pytest.mark.parametrize("V,k,rows", [(5, 2, 3000), (5, 5, 3000), (31, 3, 3000), (130, 2, 2000), (1003, 4, 1500),
+                                      (20011, 3, 150)])
+def test_little_is_left_of_the_target(wa, V, k, rows):
+    """Draft probabilities next to the target's: the residual that the last token is drawn from is 1e-8 to 1e-5.
+
+    A weight W(x) = p(x) - S q(x) of the kernel is off by at most 2^-45 p(x) (its low part, at most 2^-23 p(x), takes six
+    fp32 roundings) and by q(x) times S's error, 2^-47 a drop (S's low part the same way); the sums of what is left add
+    2^-38 of sums below 2^-16 at most.  Running sums are off by less than 2^-45 + k 2^-47 + 2^-54 < 2^-43, the random
+    number's place the same, so the kernel's token is one whose stretch of the definition's running sum comes within
+    2^-41 of the place, and has weight there."""
+    tol = 2.0 ** -41
+    c = near(rows, V, k, seed=V + k)
+    path, length, token = wa.tree_verify(c["target"], c["parent"], c["tokens"], c["u"], draft=c["draft"])
+    w, sure = dropped(c, tol)
+    assert sure.double().mean() > 0.5
+    assert (length[sure] == 1).all()
+    run = w.cumsum(1)
+    place = c["u"][:, :1].double() * run[:, -1:]
+    assert (token[sure] >= 0).all()
+    at = token.long().clamp_min(0)[:, None]
+    end, own = run.gather(1, at), w.gather(1, at)
+    good = ((end - own <= place + tol) & (end > place - tol) & (own > 0))[:, 0]
+    assert good[sure].all(), f"{(~good[sure]).sum().item()} of {sure.sum().item()}"
