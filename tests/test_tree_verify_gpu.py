@@ -293,3 +293,25 @@ def test_little_is_left_of_the_target(wa, V, k, rows):
     end, own = run.gather(1, at), w.gather(1, at)
     good = ((end - own <= place + tol) & (end > place - tol) & (own > 0))[:, 0]
     assert good[sure].all(), f"{(~good[sure]).sum().item()} of {sure.sum().item()}"
+
+
+def cluster(rows, sms):
+    """CTAs a row: the most of 8, 4, 2, 1 with which the rows have at most 4 CTAs an SM."""
+    return next(cl for cl in (8, 4, 2, 1) if cl == 1 or 4 * sms // rows >= cl)
+
+
+def test_every_cluster_size(wa):
+    """The same eight rows among as many as bring clusters of 8, 4, 2 and 1 CTAs, on both sides of each border."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = make(8, 10, 4099, seed=23, kind="bushy", noise=1.5)
+    seen = set()
+    for draft in (True, False):
+        _, want = both(wa, c if draft else dict(c, draft=None))
+        for rows in (sms // 2, sms // 2 + 1, sms, sms + 1, 2 * sms - 3, 2 * sms, 2 * sms + 1, 4 * sms):
+            seen.add(cluster(rows, sms))
+            at = torch.arange(rows, device="cuda") % 8
+            got = wa.tree_verify(*[c[x][at] for x in ("target", "parent", "tokens", "u")],
+                                 draft=c["draft"][at] if draft else None)
+            for g, w in zip(got, want):
+                assert g.tolist() == [w[i] for i in at.tolist()], rows
+    assert seen == {8, 4, 2, 1}
