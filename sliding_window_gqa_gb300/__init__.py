@@ -417,6 +417,23 @@ def _check_i32(name: str, t, shape) -> None:
         raise ValueError(f"{name} must be contiguous and of shape {tuple(shape)}")
 
 
+def _number(name: str, x):
+    if not hasattr(x, "__index__") and not hasattr(x, "__float__"):
+        raise TypeError(f"{name} must be a number, not {type(x).__name__}")
+    return x
+
+
+def _window(win) -> int:
+    """A window of any numeric type as an int."""
+    try:
+        w = int(_number("win", win))
+    except (ValueError, OverflowError):      # not a finite number
+        w = None
+    if w is None or w != win:
+        raise ValueError(f"win must be a whole number of keys, not {win}")
+    return w
+
+
 def _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out):
     """(rows, nodes, hq, hkv, d, ring) of a tree decode call; ValueError if the tensors disagree."""
     if q.dim() != 4 or k_ring.dim() != 4:
@@ -488,6 +505,7 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
         if got is not None:
             return _result(got, "wa_tree_decode")
     (rows, nodes, hq, hkv, d, ring), st = _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out)
+    win, scale = _window(win), float(_number("scale", scale))
     dev = q.device
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -503,7 +521,7 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
         _workspace(0, dev, ws)
     rc = lib().wa_tree_decode(
         q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), pos.data_ptr(),
-        parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, int(win), ring, float(scale),
+        parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring, scale,
         ctypes.byref(st), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
     if stream is not None:
         _keep_for(stream, made)

@@ -32,7 +32,8 @@ bool sized(const Tensor* t, std::initializer_list<int64_t> want) { return t->siz
 
 PyObject* none() { Py_RETURN_NONE; }
 
-// Runs `f` (which returns a new reference) with any C++ or Python error turned into None.
+// Runs `f` (which returns a new reference) with any C++ or Python error turned into None, and none left set: a
+// conversion that failed (win = 1024.0) leaves one behind although f has returned.
 template <class F>
 PyObject* guarded(F&& f) {
     PyObject* r = nullptr;
@@ -41,7 +42,8 @@ PyObject* guarded(F&& f) {
     } catch (...) {
         r = nullptr;
     }
-    if (!r) {
+    if (!r || PyErr_Occurred()) {
+        Py_XDECREF(r);
         PyErr_Clear();
         return none();
     }

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -182,3 +183,14 @@ def test_the_workspace_holds_every_rows_spans(win, hq, hkv):
         at = range(-1, 30000, 13) if win else [*range(-1, ring, 29), ring - 1]
         most = max(_spans(p, win, hq) for p in at)
         assert most <= held <= most + 1, (ring, most, held)
+
+
+def test_windows_of_any_numeric_type():
+    for win in (64, 64.0, np.int64(64), np.float32(64.0), torch.tensor(64)):
+        assert wa._window(win) == 64 and type(wa._window(win)) is int
+    for win in (None, "64", [64]):
+        with pytest.raises(TypeError, match="win"):
+            wa._window(win)
+    for win in (64.5, float("nan"), float("inf")):
+        with pytest.raises(ValueError, match="win"):
+            wa._window(win)

@@ -389,3 +389,24 @@ def test_weights_enter_the_products_within_half_a_step_of_two_parts(wa):
     tol = (b.double() * (2 ** -18 + 2 ** -21) + 2 ** -21) / l + want.abs() * (2 ** -8 + 2 ** -17)
     off = (got - want).abs() / tol
     assert off.max() <= 1.0, (off.max().item(), (off > 1).double().mean().item())
+
+
+def test_windows_and_scales_of_other_types(wa):
+    """A window or a scale that is no plain number of its kind is taken for what it is or refused by its name."""
+    c = _case(2, 5, 4, 2, 128, 64, 90, [200, 30], seed=14)
+    want = _run(wa, c)
+    args = [c[x] for x in ("q", "k", "v", "k_tree", "v_tree", "pos", "parent")]
+    ws = torch.empty(wa.tree_decode_ws_bytes(2, 5, 4, 2, 128, 64, 90), dtype=torch.uint8, device="cuda")
+    for _ in range(20):       # an error left behind shows at once or once the interpreter has specialised the call
+        for win in (64.0, np.int64(64), np.float32(64.0)):
+            assert _eq(wa.tree_decode(*args, win), want)
+            assert _eq(wa.tree_decode(*args, win, ws=ws, scale=np.float64(1.0)), want)
+        for win in (None, "64", [64]):
+            with pytest.raises(TypeError, match="win"):
+                wa.tree_decode(*args, win)
+        for scale in (None, "x"):
+            with pytest.raises(TypeError, match="scale"):
+                wa.tree_decode(*args, 64, scale=scale)
+        with pytest.raises(ValueError, match="win"):
+            wa.tree_decode(*args, 64.5)
+    assert _eq(_run(wa, c), want)
