@@ -423,6 +423,16 @@ def _number(name: str, x):
     return x
 
 
+def _fit_32_bits(*sizes) -> bool:
+    """Whether the library can be told these numbers: ctypes would take larger ones modulo 2^32."""
+    return all(-2 ** 31 <= x < 2 ** 31 for x in sizes)
+
+
+def _check_sizes(sizes) -> None:
+    if not _fit_32_bits(*sizes):
+        raise ValueError(f"sizes {tuple(sizes)} must be below 2^31")
+
+
 def _window(win) -> int:
     """A window of any numeric type as an int."""
     try:
@@ -431,6 +441,8 @@ def _window(win) -> int:
         w = None
     if w is None or w != win:
         raise ValueError(f"win must be a whole number of keys, not {win}")
+    if not _fit_32_bits(w):
+        raise ValueError(f"win {w} must be below 2^31")
     return w
 
 
@@ -473,6 +485,7 @@ def _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out):
     for n_, t in (("q", q), ("k_ring", k_ring), ("v_ring", v_ring), ("k_tree", k_tree), ("v_tree", v_tree)):
         _check_bf16(n_, t)
     sizes = rows, nodes, hq, hkv, d, ring = _tree_shapes(q, k_ring, v_ring, k_tree, v_tree, out)
+    _check_sizes(sizes)
     _check_i32("pos", pos, (rows,))
     _check_i32("parent", parent, (rows, nodes))
     if n is not None:
@@ -486,7 +499,8 @@ def _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out):
 
 
 def tree_decode_ws_bytes(rows: int, nodes: int, hq: int, hkv: int, d: int, win: int, ring: int) -> int:
-    return int(lib().wa_tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring))
+    sizes = rows, nodes, hq, hkv, d, win, ring
+    return int(lib().wa_tree_decode_ws_bytes(*sizes)) if _fit_32_bits(*sizes) else 0
 
 
 def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None, scale: float = 1.0,
@@ -549,6 +563,7 @@ def _verify_check(target, parent, tokens, u, draft, n, path, length, token):
     """Strides of a verification call; raises where its tensors disagree."""
     t_st = _prob_strides("target", target, None)
     rows, nodes, vocab = target.shape
+    _check_sizes(target.shape)
     d_st = (0, 0) if draft is None else _prob_strides("draft", draft, target.shape)
     _check_i32("parent", parent, (rows, nodes))
     _check_i32("tokens", tokens, (rows, nodes))
@@ -623,6 +638,7 @@ def _commit_layers(kt, vt, kr, vr):
                 raise ValueError(f"{name} must be [rows, nodes or ring, hkv, d]")
     shape = kt[0].shape
     rows, nodes, hkv, d = shape
+    _check_sizes((*shape, *[t.shape[1] for t in kr]))
     k_st, v_st = _node_strides("k_tree", kt[0], d), _node_strides("v_tree", vt[0], d)
     for l in range(L):
         if kt[l].shape != shape or vt[l].shape != shape:
@@ -655,6 +671,7 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
         raise ValueError("path must be [rows, most]")
     most = path.shape[1]
+    _check_sizes(path.shape)
     _check_i32("path", path, (rows, most))
     _check_i32("length", length, (rows,))
     _check_i32("pos", pos, (rows,))

@@ -194,3 +194,18 @@ def test_windows_of_any_numeric_type():
     for win in (64.5, float("nan"), float("inf")):
         with pytest.raises(ValueError, match="win"):
             wa._window(win)
+
+
+def test_numbers_past_32_bits():
+    """What ctypes would take modulo 2^32 is refused (or no valid size, for a workspace) instead."""
+    for win in (2 ** 31, 2 ** 32, 2 ** 32 + 64, -2 ** 32 + 64, 2 ** 70, 2.0 ** 40):
+        with pytest.raises(ValueError, match="win"):
+            wa._window(win)
+    for sizes in ((2 ** 32 + 1, 8), (1, 2 ** 31), (-2 ** 32 + 1,)):
+        with pytest.raises(ValueError):
+            wa._check_sizes(sizes)
+    wa._check_sizes((1, 2 ** 31 - 1))
+    good = (1, 8, 16, 8, 256, 64, 64)
+    assert wa.tree_decode_ws_bytes(*good) > 0
+    for i in range(7):
+        assert wa.tree_decode_ws_bytes(*good[:i], good[i] + 2 ** 32, *good[i + 1:]) == 0

@@ -410,3 +410,13 @@ def test_windows_and_scales_of_other_types(wa):
         with pytest.raises(ValueError, match="win"):
             wa.tree_decode(*args, 64.5)
     assert _eq(_run(wa, c), want)
+
+
+@pytest.mark.parametrize("win", [2 ** 31, 2 ** 32, 2 ** 32 + 64, -2 ** 32 + 64, 2 ** 70])
+def test_windows_past_32_bits_are_refused(wa, win):
+    """Not taken modulo 2^32."""
+    c = _case(2, 5, 4, 2, 128, 64, 90, [80, 30], seed=14)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    for kw in ({}, dict(ws=ws)):
+        with pytest.raises(ValueError, match="win"):
+            wa.tree_decode(*[c[x] for x in ("q", "k", "v", "k_tree", "v_tree", "pos", "parent")], win, **kw)

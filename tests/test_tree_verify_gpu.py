@@ -315,3 +315,13 @@ def test_every_cluster_size(wa):
             for g, w in zip(got, want):
                 assert g.tolist() == [w[i] for i in at.tolist()], rows
     assert seen == {8, 4, 2, 1}
+
+
+def test_vocabularies_past_32_bits_are_refused(wa):
+    """Not taken modulo 2^32.  (17 GB that nothing reads.)"""
+    target = torch.empty((1, 1, 2 ** 32 + 8), device="cuda")
+    one = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        wa.tree_verify(target, one, one, one.float())
+    with pytest.raises(wa.WAError):
+        wa.tree_verify(target[:, :, :2 ** 24 + 1].contiguous(), one, one, one.float())
