@@ -387,16 +387,27 @@ def prep_append(src, pos, q_out, k_ring, v_ring=None, mode: str = "rmsnorm", q_s
 
 
 # Drafted tokens.  These calls run on their inputs' device, whichever is current, and on `stream` or
-# that device's current stream; what they allocate is kept for that stream.  A drafted step makes one
+# that device's current stream; what they allocate is that stream's.  A drafted step makes one
 # call a layer, of a few microseconds on the GPU for a single sequence, so the ordinary call (contiguous
 # tensors on the current device and stream) is checked and made by the extension module; it returns None
 # for any other one, which goes through the checks here.
 
-def _keep_for(stream, made) -> None:
-    """Memory allocated on the current stream and used on another is not reused before that one is done."""
-    if stream != torch.cuda.current_stream():
-        for t in made:
-            t.record_stream(stream)
+def _empty(shape, dtype, device, stream, handed_back=True):
+    """Memory for a call on ``stream``, from that stream's own: what was freed on the current stream may yet be written
+    by what is queued there.  The caller uses what is handed back on the current stream, so it is kept for that one too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if handed_back and stream != torch.cuda.current_stream():
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _workspace_on(stream, nbytes: int, device, ws, handed_back=False):
+    if ws is None:
+        return _empty(max(nbytes, 256), torch.uint8, device, stream, handed_back)
+    return _workspace(0, device, ws)
 
 
 def _stream_on(index: int, stream) -> int:
@@ -524,21 +535,13 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws, stream)
-    made = []
     if out is None:
-        out = torch.empty((rows, nodes, hq, d), dtype=torch.bfloat16, device=dev)
-        made.append(out)
-    if ws is None:
-        ws = _workspace(tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring), dev, None)
-        made.append(ws)
-    else:
-        _workspace(0, dev, ws)
+        out = _empty((rows, nodes, hq, d), torch.bfloat16, dev, stream)
+    ws = _workspace_on(stream, tree_decode_ws_bytes(rows, nodes, hq, hkv, d, win, ring), dev, ws)
     rc = lib().wa_tree_decode(
         q.data_ptr(), k_ring.data_ptr(), v_ring.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), pos.data_ptr(),
         parent.data_ptr(), None if n is None else n.data_ptr(), rows, nodes, hq, hkv, d, win, ring, scale,
         ctypes.byref(st), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
-    if stream is not None:
-        _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_decode")
     return out
@@ -601,26 +604,13 @@ def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return tree_verify(target, parent, tokens, u, draft, n, path, length, token, ws, stream)
-    made = []
-
-    def ints(t, *shape):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=dev)
-            made.append(t)
-        return t
-
-    path, length, token = ints(path, rows, nodes), ints(length, rows), ints(token, rows)
-    if ws is None:
-        ws = _workspace(256, dev, None)
-        made.append(ws)
-    else:
-        _workspace(0, dev, ws)
+    path, length, token = [_empty(shape, torch.int32, dev, stream) if t is None else t
+                           for t, shape in ((path, (rows, nodes)), (length, (rows,)), (token, (rows,)))]
+    ws = _workspace_on(stream, 256, dev, ws)
     rc = lib().wa_tree_verify(
         target.data_ptr(), None if draft is None else draft.data_ptr(), parent.data_ptr(), tokens.data_ptr(),
         None if n is None else n.data_ptr(), u.data_ptr(), rows, nodes, vocab, ctypes.byref(st), path.data_ptr(),
         length.data_ptr(), token.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
-    if stream is not None:
-        _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_verify")
     return path, length, token
@@ -680,20 +670,13 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return tree_commit(kt, vt, kr, vr, path, length, pos, ws, stream)
-    made = []
-    if ws is None:
-        ws = _workspace(256, dev, None)
-        made.append(ws)
-    else:
-        _workspace(0, dev, ws)
+    ws = _workspace_on(stream, 256, dev, ws, handed_back=True)
     L = len(kt)
     ptrs = [(_P * L)(*[t.data_ptr() for t in ts]) for ts in (kt, vt, kr, vr)]
     rc = lib().wa_tree_commit(
         L, *ptrs, (_I * L)(*[t.shape[1] for t in kr]), rows, nodes, hkv, d,
         ctypes.byref(_TreeStrides(0, 0, *k_st, *v_st, 0, 0)), path.data_ptr(), most, length.data_ptr(), pos.data_ptr(),
         ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
-    if stream is not None:
-        _keep_for(stream, made)
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_commit")
     return ws
