@@ -14,6 +14,8 @@ import ctypes
 import importlib.util
 import os
 import re
+import sys
+import warnings
 
 import torch
 
@@ -28,6 +30,7 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libwa.so")
 _BIND_PATH = os.path.join(_HERE, "_build", "wa_bind.so")
+_BIND_FOR = f"PyTorch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"   # as build.py has it
 _HEADER = os.path.join(os.path.dirname(_HERE), "include", "wa.h")
 
 
@@ -80,7 +83,7 @@ class _VerifyStrides(ctypes.Structure):
 
 
 _lib = None
-_bind = None      # the short way to the drafted-token calls (csrc/wa_bind.cpp)
+_bind = False     # the short way to the drafted-token calls (csrc/wa_bind.cpp); None: there is none, False: not looked for
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 
@@ -91,9 +94,9 @@ def lib_path() -> str:
 
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
-    global _lib, _bind
+    global _lib
     if _lib is None:
-        if not os.path.exists(_LIB_PATH) or not os.path.exists(_BIND_PATH):
+        if not os.path.exists(_LIB_PATH):
             raise RuntimeError(
                 f"{_LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(_LIB_PATH)
@@ -131,11 +134,29 @@ def lib() -> ctypes.CDLL:
         L.wa_strerror.restype = ctypes.c_char_p
         L.wa_version.argtypes = []
         L.wa_version.restype = ctypes.c_int
-        spec = importlib.util.spec_from_file_location("wa_bind", _BIND_PATH)
-        _bind = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_bind)
         _lib = L
     return _lib
+
+
+def _short_way():
+    """The extension module, or None where it is missing or was built for another PyTorch or Python: every call goes
+    through ctypes then, with the same results and some microseconds more on the host, which is warned of once."""
+    global _bind
+    if _bind is False:
+        lib()
+        try:
+            spec = importlib.util.spec_from_file_location("wa_bind", _BIND_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            built_for = getattr(module, "built_for", "something else")
+            if built_for != _BIND_FOR:
+                raise ImportError(f"built for {built_for}, this is {_BIND_FOR}")
+            _bind = module
+        except (ImportError, OSError) as e:
+            _bind = None
+            warnings.warn(f"{_BIND_PATH} cannot be used ({e}): the drafted-token calls take some microseconds longer",
+                          RuntimeWarning, stacklevel=3)
+    return _bind
 
 
 def _stream_handle(stream) -> int:
@@ -524,9 +545,9 @@ def tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win: int, n=None
     for one that follows the cache; n int32 [rows] or None: nodes in use.  A node sees the cache, its
     ancestors and itself, as far as the window reaches back.  Returns out [rows, nodes, hq, d] bf16,
     whose nodes past n are not written.  ``ws``: a reused uint8 CUDA buffer of tree_decode_ws_bytes(...)."""
-    if stream is None:
-        lib()
-        got = _bind.tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws)
+    bind = _short_way() if stream is None else None
+    if bind is not None:
+        got = bind.tree_decode(q, k_ring, v_ring, k_tree, v_tree, pos, parent, win, n, scale, out, ws)
         if got is not None:
             return _result(got, "wa_tree_decode")
     (rows, nodes, hq, hkv, d, ring), st = _tree_check(q, k_ring, v_ring, k_tree, v_tree, pos, parent, n, out)
@@ -593,9 +614,9 @@ def tree_verify(target, parent, tokens, u, draft=None, n=None, path=None, length
     c, u[:, 0] samples the last token.  n int32 [rows] or None: nodes in use.  Returns (path int32
     [rows, nodes], length int32 [rows], token int32 [rows]): the kept nodes in order, then -1; how many;
     the token sampled after them (-1: no nodes, or a distribution without mass)."""
-    if stream is None and path is None and length is None and token is None:
-        lib()
-        got = _bind.tree_verify(target, parent, tokens, u, draft, n, ws)
+    bind = _short_way() if stream is None and path is None and length is None and token is None else None
+    if bind is not None:
+        got = bind.tree_verify(target, parent, tokens, u, draft, n, ws)
         if got is not None:
             return _result(got, "wa_tree_verify")
     st = _verify_check(target, parent, tokens, u, draft, n, path, length, token)
@@ -651,9 +672,9 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     strides).  path int32 [rows, most], length and pos int32 [rows], as tree_verify returned and
     tree_decode took them; afterwards the row's last position is pos + length.  Returns the
     workspace, whose status status() reads."""
-    if stream is None:
-        lib()
-        got = _bind.tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws)
+    bind = _short_way() if stream is None else None
+    if bind is not None:
+        got = bind.tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws)
         if got is not None:
             return _result(got, "wa_tree_commit")
     kt, vt, kr, vr = ([x] if isinstance(x, torch.Tensor) else list(x) for x in (k_tree, v_tree, k_ring, v_ring))

@@ -1,5 +1,6 @@
 """Builds libwa.so in-tree with nvcc for sm_103a (one translation unit per job, in parallel), and the binding's
-wa_bind.so, a Python extension against the installed PyTorch's headers, with g++ at the same time."""
+wa_bind.so, a Python extension against the installed PyTorch's headers, with g++ at the same time.  Without wa_bind.so
+every call still works, so where it cannot be built that is said and the build goes on."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -52,8 +53,9 @@ def _compile_bind(nvcc: str, torch_dir: str) -> str:
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
            os.path.join(ROOT, "include")]
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{p}" for p in inc], "-c",
-          os.path.join(CSRC, "wa_bind.cpp"), "-o", obj], "g++ on wa_bind.cpp")
+    built_for = f"PyTorch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", f'-DWA_BIND_FOR="{built_for}"',
+          *[f"-I{p}" for p in inc], "-c", os.path.join(CSRC, "wa_bind.cpp"), "-o", obj], "g++ on wa_bind.cpp")
     return obj
 
 
@@ -66,17 +68,27 @@ def build(verbose: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         bind = ex.submit(_compile_bind, nvcc, torch_dir)
         objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra)), SOURCES))
-        bind_obj = bind.result()
+        try:
+            bind_obj, bind_error = bind.result(), None
+        except Exception as e:
+            bind_obj, bind_error = None, e
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = BIND + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT, "-l:libwa.so", "-L" + os.path.join(torch_dir, "lib"),
-          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of wa_bind.so")
-    os.replace(tmp, BIND)
+    try:
+        if bind_error:
+            raise bind_error
+        tmp = BIND + ".tmp"
+        _run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT, "-l:libwa.so", "-L" + os.path.join(torch_dir, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of wa_bind.so")
+        os.replace(tmp, BIND)
+    except Exception as e:
+        if os.path.exists(BIND):        # an earlier build's, of other sources
+            os.remove(BIND)
+        print(f"wa_bind.so was not built, the drafted-token calls go through ctypes: {e}", file=sys.stderr)
     if verbose:
         print("built", LIB)
     return LIB

@@ -228,4 +228,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "wa_bind", nullptr, -1, methods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_wa_bind() { return PyModule_Create(&module); }
+// `built_for`: the PyTorch and Python whose headers this was compiled against; the package uses it with no others.
+PyMODINIT_FUNC PyInit_wa_bind() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", WA_BIND_FOR) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

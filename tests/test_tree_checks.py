@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import numpy as np
 import pytest
@@ -209,3 +210,64 @@ def test_numbers_past_32_bits():
     assert wa.tree_decode_ws_bytes(*good) > 0
     for i in range(7):
         assert wa.tree_decode_ws_bytes(*good[:i], good[i] + 2 ** 32, *good[i + 1:]) == 0
+
+
+# ---- the extension module is a shorter way to the same calls, not a condition for any
+
+def test_the_extension_module_is_built_and_used():
+    ensure_built()
+    assert wa._short_way() is not None and wa._short_way().built_for == wa._BIND_FOR
+
+
+@pytest.fixture
+def not_loaded(monkeypatch):
+    ensure_built()
+    monkeypatch.setattr(wa, "_lib", None)
+    monkeypatch.setattr(wa, "_bind", False)
+    return monkeypatch
+
+
+@pytest.mark.parametrize("what", ["missing", "no module", "built for another"])
+def test_without_the_extension_module(not_loaded, tmp_path, what):
+    if what == "built for another":
+        not_loaded.setattr(wa, "_BIND_FOR", "PyTorch 1.0, Python 2.7")
+    else:
+        path = tmp_path / "wa_bind.so"
+        if what == "no module":
+            path.write_bytes(b"nothing")
+        not_loaded.setattr(wa, "_BIND_PATH", str(path))
+    assert wa.lib().wa_version() > 0              # the library, and with it every other call, does without
+    assert wa.decode_ws_bytes(1, 16, 256, 1024, 1536) > 0
+    q, ring, tr, i = bf16(1, 2, 4, 128), bf16(1, 8, 4, 128), bf16(1, 2, 4, 128), torch.zeros((1, 2), dtype=torch.int32)
+    with pytest.warns(RuntimeWarning, match="wa_bind.so"), pytest.raises(TypeError, match="CUDA"):
+        wa.tree_decode(q, ring, ring, tr, tr, i[:, 0], i, 0)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")            # said once
+        with pytest.raises(TypeError, match="CUDA"):
+            wa.tree_verify(torch.zeros(1, 2, 9), i, i, torch.zeros(1, 2))
+        with pytest.raises(TypeError, match="CUDA"):
+            wa.tree_commit(tr, tr, ring, ring, i, i[:, 0], i[:, 0])
+
+
+def test_a_missing_library_is_named(not_loaded, tmp_path):
+    not_loaded.setattr(wa, "_LIB_PATH", str(tmp_path / "libwa.so"))
+    with pytest.raises(RuntimeError, match="libwa.so is missing"):
+        wa.lib()
+
+
+def test_the_build_goes_on_without_the_extension_module(monkeypatch, tmp_path, capsys):
+    """A compiler that refuses wa_bind.cpp: libwa.so is built, an older wa_bind.so is taken away, and it is said."""
+    from sliding_window_gqa_gb300 import build
+    monkeypatch.setattr(build, "OUT", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libwa.so"))
+    monkeypatch.setattr(build, "BIND", str(tmp_path / "wa_bind.so"))
+    monkeypatch.setattr(build, "SOURCES", ["wa_tree_commit.cu"])
+
+    def refuse(*a):
+        raise RuntimeError("g++ on wa_bind.cpp failed")
+
+    monkeypatch.setattr(build, "_compile_bind", refuse)
+    (tmp_path / "wa_bind.so").write_bytes(b"old")
+    assert build.build() == str(tmp_path / "libwa.so")
+    assert (tmp_path / "libwa.so").exists() and not (tmp_path / "wa_bind.so").exists()
+    assert "wa_bind.so was not built" in capsys.readouterr().err

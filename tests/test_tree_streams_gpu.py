@@ -82,3 +82,12 @@ def test_captured_calls_that_allocate(wa):
         torch.cuda.synchronize()
         for n in want:
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got[n], want[n])), n
+
+
+def test_without_the_extension_module(wa, monkeypatch):
+    """The same bits by way of ctypes alone."""
+    calls = _calls(wa)
+    want = {n: calls[n](None) for n in ("decode", "verify")}
+    monkeypatch.setattr(wa, "_bind", None)
+    for n, ts in want.items():
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(calls[n](None), ts)), n
