@@ -370,7 +370,9 @@ int wa_tree_verify(const float* target, const float* draft, const int32_t* paren
  *   pos     [rows]        int32, device; below -1: the row is not copied (WA_STATUS_BAD_POS)
  *
  * Where length exceeds a ring, the last ring[l] nodes are what stays.  The rings
- * must not overlap the trees.
+ * must overlap neither the trees nor one another, but that one ring may stand for
+ * two where its tree does too (keys that are the values, a cache that layers
+ * share); one ring with two trees is WA_EINVAL.
  */
 int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const* v_tree, void* const* k_ring,
                    void* const* v_ring, const int32_t* ring, int32_t rows, int32_t nodes, int32_t hkv, int32_t d,

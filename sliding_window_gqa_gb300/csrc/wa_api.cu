@@ -6,6 +6,7 @@
 // hi)"), a scale parameter and window 0 as a linear cache (bullet "Scale is
 // a parameter"), and the optional two-half P (bullet "Window.p32").  The calls
 // for drafted tokens (tree decode, verification, commit) build on the decode form.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -52,6 +53,22 @@ int ensure_device() {
 }
 
 size_t flags_bytes(int64_t units) { return round_up(static_cast<size_t>(units) * sizeof(int), 256); }
+
+// Whether a ring is given twice with other nodes: one slot would get two values.
+bool rings_contradict(const wa::CommitArgs& a, int layers) {
+    const void* all[2 * WA_COMMIT_MAX_LAYERS];
+    for (int i = 0; i < 2 * layers; ++i) all[i] = a.dst[i / layers][i % layers];
+    std::sort(all, all + 2 * layers);
+    if (std::adjacent_find(all, all + 2 * layers) == all + 2 * layers) return false;
+    for (int i = 1; i < 2 * layers; ++i)
+        for (int j = 0; j < i; ++j) {
+            const int ki = i / layers, li = i % layers, kj = j / layers, lj = j % layers;
+            if (a.dst[ki][li] == a.dst[kj][lj] &&
+                (a.src[ki][li] != a.src[kj][lj] || a.ring[li] != a.ring[lj] || a.tok[ki] != a.tok[kj] || a.row[ki] != a.row[kj]))
+                return true;
+        }
+    return false;
+}
 
 }  // namespace
 
@@ -344,6 +361,7 @@ int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const*
         a.dst[0][l] = k_ring[l]; a.dst[1][l] = v_ring[l];
         a.ring[l] = ring[l];
     }
+    if (rings_contradict(a, layers)) return WA_EINVAL;
     if (!ws || ws_bytes < WA_TREE_WS_BYTES || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
     const int rc = ensure_device();
     if (rc != WA_OK) return rc;

@@ -108,6 +108,31 @@ def test_tree_commit_workspace_errors():
     assert _commit(ws_bytes=128) == wa.WA_EWORKSPACE
 
 
+@pytest.mark.parametrize("kt,vt,kr,vr,ok", [
+    ([1, 2], [3, 4], [5, 6], [7, 8], True),
+    ([1, 2], [3, 4], [5, 5], [7, 8], False),          # two layers' nodes into one ring
+    ([1, 2], [3, 4], [5, 6], [7, 6], False),          # keys and values into one ring
+    ([1, 2], [3, 1], [5, 6], [7, 5], True),           # one layer's values are another's keys
+    ([1, 1], [3, 3], [5, 5], [7, 7], True),           # a cache that layers share
+    ([1, 2], [1, 2], [5, 6], [5, 6], True),           # keys that are the values
+    ([1, 1], [3, 3], [5, 5], [7, 8], True),
+])
+def test_tree_commit_of_one_ring_twice(kt, vt, kr, vr, ok):
+    L = ensure_built().lib()
+    arr = lambda xs: (ctypes.c_void_p * 2)(*[x << 20 for x in xs])     # noqa: E731
+
+    def call(rings, st=None):
+        # without a workspace, which is looked at last: nothing is launched
+        return L.wa_tree_commit(2, arr(kt), arr(vt), arr(kr), arr(vr), (ctypes.c_int32 * 2)(*rings), 3, 8, 8, 256,
+                                None if st is None else ctypes.byref(st), FAKE, 8, FAKE, FAKE, None, 0, None)
+
+    assert call([64, 64]) == (wa.WA_EWORKSPACE if ok else wa.WA_EINVAL)
+    if ok and len({*kr, *vr}) < 4 and kr[0] == kr[1]:
+        assert call([64, 65]) == wa.WA_EINVAL          # one ring of two lengths
+    if ok and kr == vr:                                # one tree read two ways
+        assert call([64, 64], wa._TreeStrides(k_tok=2048, v_tok=4096)) == wa.WA_EINVAL
+
+
 def test_status_names():
     L = ensure_built().lib()
     assert b"tree" in L.wa_strerror(wa.WA_STATUS_BAD_TREE)

@@ -137,3 +137,16 @@ def test_many_rows_report_their_own_faults(wa):
     assert both(wa, **args, path=path, length=length, pos=pos) == wa.WA_STATUS_BAD_POS
     pos[0], length[350] = 0, most + 1
     assert both(wa, **args, path=path, length=length, pos=pos) == wa.WA_STATUS_BAD_TREE
+
+
+def test_one_ring_that_layers_share(wa):
+    """A cache of two layers, and keys that are the values: the same tree into the same ring; other trees are refused."""
+    t, other, r = rnd(2, 6, 2, 128), rnd(2, 6, 2, 128), rnd(2, 9, 2, 128)
+    path, length, pos = [[0, 2, 5], [1, 3, -1]], [3, 2], [7, 3]
+    want = tree.commit(bits(t), bits(r), path, length, pos)
+    wa.tree_commit([t, t], [t, t], [r, r], [r, r], i32(path), i32(length), i32(pos))
+    assert (bits(r) == want).all()
+    for kt, vt in (([t, other], [t, t]), ([t, t], [other, other])):
+        with pytest.raises(wa.WAError):
+            wa.tree_commit(kt, vt, [r, r], [r, r], i32(path), i32(length), i32(pos))
+    assert (bits(r) == want).all()
