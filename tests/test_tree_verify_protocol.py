@@ -14,9 +14,9 @@ SEND, WAIT, MEET, LEAVE, GONE = range(5)
 
 
 def lost_stores(ctas: int, passes: int, meet: bool) -> int:
-    """States in which a store finds its CTA gone.  meet: as the kernel does, every CTA announces that it sends nothing
-    more and stays until all have; else each leaves by itself.  Either way a late one waits once more for the pass that it
-    gave up on."""
+    """States in which a store finds its CTA gone.  meet: as the kernel does, a CTA that is through all passes announces it
+    and leaves, and a late one stays until all have announced that they are through or late; else a late one goes on by
+    itself.  Either way it then waits once more for the pass that it gave up on."""
     # a CTA: (what it does next, pass, late); a store under way: (from, to, pass); what has arrived: (to, pass) -> from
     start = (tuple((SEND, 0, False) for _ in range(ctas)), frozenset(), frozenset())
     todo, known, lost = [start], {start}, 0
@@ -38,14 +38,13 @@ def lost_stores(ctas: int, passes: int, meet: bool) -> int:
             if do == SEND:
                 step(i, (WAIT, k, False), flying=flying | {(i, j, k) for j in range(ctas)})
             elif do == WAIT:
-                done = MEET if meet else GONE
                 if through:
-                    step(i, (SEND, k + 1, False) if k + 1 < passes else (done, k, False))
+                    step(i, (SEND, k + 1, False) if k + 1 < passes else (GONE, k, False))
                 elif not any(m[0] == i for m in flying):
                     step(i, (MEET if meet else LEAVE, k, True))
             elif do == MEET:
                 if all(s[0] in (MEET, LEAVE, GONE) for s in state):
-                    step(i, (LEAVE if late else GONE, k, late))
+                    step(i, (LEAVE, k, late))
             elif do == LEAVE and (through or not meet or not flying):
                 step(i, (GONE, k, late))
     return lost
