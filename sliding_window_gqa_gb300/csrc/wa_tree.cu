@@ -17,13 +17,14 @@
 // the bits.
 //
 // What bounds it.  Up to 64 query rows a tile: the reads of K and V (a linear batch of
-// 8 rows, 32/16 heads of 256, 9,000 to 32,700 keys: 440 us, 92 % of the measured copy
-// rate over the whole call; 64 rows over a window of 1,024, 32/16 heads: 217 us, 75 %,
+// 8 rows, 32/16 heads of 256, 9,000 to 32,700 keys: 441 us, 92 % of the measured copy
+// rate over the whole call; 64 rows over a window of 1,024, 32/16 heads: 216 us, 75 %,
 // the rest being the start and the join of the spans).  128 query rows at head dim 128:
 // the softmax warps, whose chain S -> P of a tile takes 2,500 cycles where its products
-// take 1,536 (32 rows of 64 nodes, 32/4 heads: 447 us; 268 us of products at the measured
+// take 1,536 (32 rows of 64 nodes, 32/4 heads: 442 us; 268 us of products at the measured
 // rate).  One sequence over a window (19 us): the start of three kernels, one CTA's loads
-// (36 bytes a cycle) and that chain.
+// (36 bytes a cycle) and that chain.  Times in this file are of calls replayed as CUDA
+// graphs; called from Python one after another the four take 457, 218, 470 and 22 us.
 //
 // tree_plan_kernel: one block lists the (row, span) pairs, longest first, with all that a
 // unit needs of its row (position, nodes, parents), checks the rows' numbers for the status
@@ -67,12 +68,13 @@ constexpr int kAhead = 2;          // units published beyond the one whose Q is 
 // maximum costs no accuracy; 2^32 leaves them 2^90 below overflow, and what does overflow is computed again.
 constexpr float kTreeLazy = 32.0f;
 
-// Keys a span, a power of two: keys * hq / 128 on a linear cache, win * hq / 64 on a window.  Short spans put a
-// single row's keys on more SMs, long ones leave fewer partial results and fewer ends of the pipeline.  One row of
-// 32,000 keys, 16/8 heads: 75, 56 and 77 us with spans of 1,024, 2,048 and 4,096; 32 rows of 64 nodes, 32/4 heads,
-// 10,000 keys: 795, 617 and 549 us with 512, 1,024 and 2,048 (an earlier state of the kernel).  A window of 1,024
-// with win * hq / 64 and / 32: one row of 16/8 heads 21 and 25 us, 64 rows of 32/16 heads 232 and 222; 13 ragged
-// rows of 24/8 heads, a window of 1,000: 27 and 28.5.  The rule sees no number of rows, so that a row's bits do not either.
+// Keys a span, a power of two: keys * hq / 128 on a linear cache, win * hq / 64 on a window, 2,048 at most.  Short
+// spans put a single row's keys on more SMs, long ones leave fewer partial results and fewer ends of the pipeline.
+// Linear, with / 64, / 128 and / 256: one row of 32,000 keys, 16/8 heads, 52, 52 and 68 us; 32 rows of 64 nodes, 32/4
+// heads, 431, 442 and 508; 8 rows of 32/16 heads 440, 441 and 448; at most 1,024 with / 128: 68, 490 and 471.  A window
+// of 1,024 with / 32, / 64 and / 128: one row of 16/8 heads 23, 18.7 and 18.5; 64 rows of 32/16 heads 208, 216 and 238;
+// 13 ragged rows of 24/8 heads, a window of 1,000: 26.4, 25 and 24.  The rule sees no number of rows, so that a row's
+// bits do not either.
 constexpr int kSpanMinWindow = 256, kSpanMinLinear = 512, kSpanMax = 2048, kSpanLinear = 128, kSpanWindow = 64;
 __host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
     const int64_t want = keys * hq / (window ? kSpanWindow : kSpanLinear);
@@ -83,7 +85,7 @@ __host__ __device__ inline int tree_span(int64_t keys, bool window, int hq) {
 
 // A row at (clamped) position p has tiles of 128 keys from its first visible one, and one of its tree's; they are
 // cut evenly into spans of at most a tile more than tree_span()'s keys, the longer ones last (the tree's tile is little
-// to read: with the longer ones first a batch over a window took 226 us instead of 217).
+// to read: with the longer ones first a batch over a window took 226 us instead of 216).
 __host__ __device__ inline int tree_first(int p, int win) { return win > 0 && p + 2 - win > 0 ? p + 2 - win : 0; }
 __host__ __device__ inline int64_t tree_keys(int p, int win) { return win > 0 ? win : static_cast<int64_t>(p) + 1; }
 __host__ __device__ inline int tree_tiles(int p, int win) { return (max(p - tree_first(p, win) + 1, 0) + kTile - 1) / kTile + 1; }
@@ -218,6 +220,9 @@ struct TreeUnit {
     int r, g, node0, span, k0, nring, nt, p, n, lo;
 };
 
+// One block, a warp a row at a time, and nothing reads keys before it is done: 5 to 8 us up to 64 rows, then 50 ns a row.
+// Calls of many short rows feel it (4 nodes, 4/2 heads of 128, a window of 256): 13 of 50 us at 256 rows, 46 of 157 at
+// 1,024, 201 of 625 at 4,096, 795 of 2,490 at 16,384.
 __global__ void __launch_bounds__(1024) tree_plan_kernel(const int32_t* __restrict__ pos, const int32_t* __restrict__ parent,
                                                          const int32_t* __restrict__ n, int rows, int nodes, int hq, int win,
                                                          int ring, WsHeader* hdr, int* __restrict__ list) {
@@ -316,9 +321,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
 // by one warp: pieces of kPiece keys by TMA, a lane each, and the piece that itself wraps by asynchronous copies;
 // nothing is waited for.  It takes the producer about 2,400 cycles: 150 for a copy of the warp, 70 for a box. The
 // slots come into range by subtraction: `x %= ring` under an `if` was run always, division and all (a batch over a
-// window 232 us, now 222).  Pieces of 8, 16 and 32 keys: 223.6, 221.5 and 226 us.  Out of line and not unrolled: few
-// tiles come here, once or twice a call, from a cold instruction cache, and among the producer's code it cost the
-// other roles 14 % at 128 query rows.
+// window 232 us, then 222).  Pieces of 8, 16 and 32 keys: 217.6, 216.5 and 220.8 us; one sequence over a window 19.1, 18.7
+// and 19.9.  Out of line and not unrolled: few tiles come here, once or twice a call, from a cold instruction cache, and
+// among the producer's code it cost the other roles 14 % at 128 query rows.
 // `lg`: log2 of a key's 16-byte parts of the load; `base`: the first of them of ring slot 0; `map`: boxes of kPiece
 // keys and 64 dims.
 constexpr int kPiece = 16;
@@ -1031,8 +1036,9 @@ constexpr int kMergeSpans = 2;
 // rows (lanes) and 64 dims (8 a warp) of a tile, reads the partial results in the order they were stored
 // (512 bytes a warp and load, kMergeSpans spans in flight), and turns them round in shared memory for the output.
 // A row with a value that is not finite is computed again in float64.  Issue bound it when each block worked out its
-// place and each output its quotient by divisions: 64 rows over a window, 32/16 heads, 222 us a call, now 217; five
-// blocks an SM 217.3, six (spills) 218.5, four 216.9.
+// place and each output its quotient by divisions (64 rows over a window, 32/16 heads, 222 us a call, then 217).  Four,
+// five and six blocks an SM: that batch 216.9, 216.5 and 218.5 us, 32 rows of 64 nodes, 32/4 heads, 441, 442 and 450 (six
+// spill); four is within the noise of five.
 template <int D>
 __global__ void __launch_bounds__(256, 5) tree_merge_kernel(const float4* part_o, const float4* part_l, const float* part_m,
                                                             const __grid_constant__ TreeArgs a, int npt, int mtiles, int spans,

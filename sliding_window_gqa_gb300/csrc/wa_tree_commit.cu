@@ -4,9 +4,9 @@
 // (layer, K or V, row, j), bound by latency for one sequence (the row's numbers, then its path, then the data) and
 // by HBM for many.  A block takes kNodes nodes of one (layer, K or V, row), so the numbers are fetched once for
 // them; its warps divide among the nodes, so that slots and addresses are computed once a warp and not for every 16
-// bytes, which bound it before (12 layers of 48 rows, 8 heads of 256: 11.7 us, 15.1 with a division a piece, 16.5
-// with a block a node; one row and layer 3.1 us).  Where length exceeds the ring, the nodes that a later one would
-// overwrite are left out, so no two blocks write one slot.
+// bytes, which bound it before (12 layers of 48 rows, 8 heads of 256: 12.1 us, 15.1 with a division a piece, 16.5
+// with a block a node; one row and layer 3.2 us; graph replays, 13.7 and 5.2 us called from Python).  Where length
+// exceeds the ring, the nodes that a later one would overwrite are left out, so no two blocks write one slot.
 //
 // The status word is written by block 0 alone, which looks through every row's numbers, so that a call is one
 // launch; for calls of more than kOneBlockEntries entries it is cleared before, and each block reports its own.

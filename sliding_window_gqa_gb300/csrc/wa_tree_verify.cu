@@ -11,9 +11,10 @@
 //
 // What bounds it: a chain of dependent passes over one node's rows, each a trip to memory
 // and a meeting of the CTAs, and at many rows the reads of those rows (one row of 8 nodes,
-// 32,768 tokens: 7.5 us; 64 rows of 16 nodes, 131,072 tokens: 43.5 us, where the rows that the
+// 32,768 tokens: 7.6 us; 64 rows of 16 nodes, 131,072 tokens: 44.9 us, where the rows that the
 // walks need take 10 us at the copy rate; 24 rows of 26 nodes without draft probabilities,
-// 100,003 tokens: 19.8 us).  So
+// 100,003 tokens: 19.9 us; as graph replays, and 8.7, 46.7 and 21.7 us called from Python one
+// after another).  So
 //   - the vocabulary is cut into 8 slices of 16 stretches; a cluster of 8, 4, 2 or 1 CTAs
 //     serves a row (fewer for many rows), each with its share
 //     of the slices, each warp one stretch of a slice; the slices' sums meet in the cluster's
@@ -543,13 +544,16 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    // a single row's cluster clears the status itself: 7.5 us, 10.5 with a memset before it
+    // a single row's cluster clears the status itself: 7.6 us a graph replay, 10.5 with a memset before it
     if (a.rows > 1) {
         clear_kernel<<<1, 1, 0, s>>>(a.hdr);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const int most = 4 * sms / a.rows;      // up to two waves of two CTAs an SM: rows end after one to five passes
+    // As many CTAs a row as are up to two waves of two an SM, since rows end after one to five passes.  16 nodes, 131,072
+    // tokens, with draft probabilities, clusters of 8, 4, 2 and 1: 32 rows 29, 30, 49 and 86 us; 64 rows 45, 52, 64 and
+    // 113; 128 rows 77, 75, 83 and 130 (the rule's 4); 256 rows 125, 107, 115 and 144 (its 2).
+    const int most = 4 * sms / a.rows;
     const cudaError_t e = most >= 8 ? launch_cl<8>(a, s) : most >= 4 ? launch_cl<4>(a, s) : most >= 2 ? launch_cl<2>(a, s) : launch_cl<1>(a, s);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
