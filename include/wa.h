@@ -55,6 +55,7 @@ extern "C" {
 #define WA_STATUS_LAYOUT 8    /* a kernel found its shared memory misaligned and wrote nothing */
 #define WA_STATUS_BAD_TREE 16 /* a parent, node count, draft token, path or length was out of range (see the call) */
 #define WA_STATUS_NO_MASS 32  /* wa_tree_verify: a distribution without mass; that row's token is -1 */
+#define WA_STATUS_BAD_PAGE 64 /* a table entry that was needed named no page, or a token no row of the table (see the call) */
 
 /* Token strides in elements for the prompt form (head stride is always d).
  * Zero means dense: hq*d for q and out, hkv*d for k and v. */
@@ -378,6 +379,130 @@ int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const*
                    void* const* v_ring, const int32_t* ring, int32_t rows, int32_t nodes, int32_t hkv, int32_t d,
                    const wa_tree_strides* lay, const int32_t* path, int32_t most, const int32_t* length,
                    const int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and a cache in pages.
+ *
+ *   wa_rope          the rotation by itself, forward or inverse
+ *   wa_paged_append  the tokens' q rotated, their k rotated and v into pages
+ *   wa_paged_decode  one new token a sequence attends to its pages
+ * ------------------------------------------------------------------------- */
+
+#define WA_ROTARY_HALF 0          /* pair j is dims (j, j + dims / 2) */
+#define WA_ROTARY_INTERLEAVED 1   /* pair j is dims (2 j, 2 j + 1) */
+
+/* A rotation of the first `dims` dims of a head by the angles pos * inv_freq[j],
+ * j < dims / 2; the other dims stay.  dims is a multiple of 16, 0 .. d (0: nothing
+ * rotates, and inv_freq and factor are not used). */
+typedef struct wa_rotary {
+    const float* inv_freq;        /* [dims / 2] fp32, device, |inv_freq| < 16 (a larger one, or one that is not finite, gives NaN) */
+    int32_t dims;
+    int32_t layout;               /* WA_ROTARY_* */
+    float factor;                 /* multiplies the rotated dims (1: a plain rotation) */
+} wa_rotary;
+
+/*
+ * Rotary positions.  For pair (a, b) of token t with c, s the cosine and sine of
+ * pos[t] * inv_freq[j]:
+ *   out[a] = factor (x[a] c - x[b] s),   out[b] = factor (x[b] c + x[a] s),
+ * one rounding to bf16.  inverse = 1 turns the other way (s -> -s): the gradient
+ * of x given that of out.  Angles are exact to 2^-32 of a turn for every position,
+ * so far positions lose nothing.
+ *
+ *   x    [n, heads, d]  bf16, token stride x_tok, head stride d
+ *   pos  [n]            int32, device, any value
+ *   out  [n, heads, d]  bf16, token stride out_tok, head stride d; x itself (with the
+ *                       same stride) or memory that does not overlap it
+ *
+ * d is 128 or 256; pointers 16-byte aligned, token strides multiples of 8
+ * elements and at least heads * d.  Returns WA_EINVAL otherwise.  No workspace.
+ */
+int wa_rope(const void* x, const int32_t* pos, int32_t n, int32_t heads, int32_t d, const wa_rotary* rot,
+            int32_t inverse, int64_t x_tok, int64_t out_tok, void* out, void* stream);
+
+#define WA_PAGE_BF16 0
+#define WA_PAGE_E4M3 1            /* 8 bits: a value is the stored one times its head's scale */
+
+/* A cache in pages of page_size positions: position p of sequence (row) r is slot
+ * p mod page_size of page table[r, p / page_size].  Sequences may share pages.
+ * Strides are in elements; either layout of a page (positions of heads, heads of
+ * positions), and k and v in one tensor, are a matter of them. */
+typedef struct wa_pages {
+    void* k;                      /* [pages][page_size][hkv][d] by the strides below */
+    void* v;
+    const float* k_scale;         /* [hkv] fp32, device: WA_PAGE_E4M3 only, NULL = 1 */
+    const float* v_scale;
+    const int32_t* table;         /* [rows][most], device */
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+    int64_t table_row;            /* between the table's rows; at least most */
+    int32_t pages, page_size, rows, most;
+    int32_t hkv, d, type;         /* d is 128 or 256; type WA_PAGE_* */
+} wa_pages;
+
+#define WA_PAGED_APPEND_WS_BYTES 256u
+
+/*
+ * Append to a paged cache, with the rotation on the way.  For each of n tokens
+ * src holds hq query heads, hkv key heads and hkv value heads, d bf16 values
+ * each.  The query heads are rotated into q_out, the key heads rotated and the
+ * value heads as they are into position pos[t] of sequence row[t].  A rounding
+ * each: to bf16, or of x / scale to e4m3, where what exceeds 448 becomes 448.
+ *
+ *   src    [n] rows of (hq + 2 hkv) d bf16, token stride src_tok
+ *   pos    [n] int32, device; -1: a token that is left out (a padded batch).
+ *          Below -1, or most * page_size and more: left out, WA_STATUS_BAD_POS
+ *   row    [n] int32, device, or NULL: token t belongs to sequence t (n <= rows).
+ *          Outside [0, rows): k and v are left out, WA_STATUS_BAD_PAGE
+ *   cache  a table entry outside [0, pages): k and v are left out, WA_STATUS_BAD_PAGE
+ *   rot    the rotation, or NULL: none
+ *   q_out  [n, hq, d] bf16, token stride q_tok; may be the query heads of src
+ *          themselves (q_tok = src_tok), else must not overlap src
+ *   ws     WA_PAGED_APPEND_WS_BYTES of device memory, 256-byte aligned (status)
+ *
+ * A token that is left out has nothing written, q_out included.  Two tokens of
+ * one call must not share a place of the cache (one sequence and position, or
+ * sequences whose tables name one page there).  page_size is a power of two from
+ * 16 to 256; hq % hkv == 0, hq / hkv <= 16; no two elements of the k pages, and of
+ * the v pages, may share memory; pointers 16-byte aligned, strides of the pages
+ * multiples of 16 bytes, others of 8 elements.  Returns WA_EINVAL otherwise.
+ */
+int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int32_t n, int32_t hq,
+                    const wa_pages* cache, const wa_rotary* rot, int64_t src_tok, int64_t q_tok, void* q_out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes wa_paged_decode needs for `cache` (sizes and type are read, no
+ * pointers); 0 for invalid sizes. */
+size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
+
+/*
+ * Decode over a paged cache: one new token a sequence.  Sequence r's last key is
+ * at position pos[r] (its own, appended before); with ks, vs the scales of key
+ * head g = h / G,
+ *   out[r, h] = vs sum_j w_j v_j / sum_j w_j,  w_j = exp(scale ks q[r, h] . k_j - max),
+ * over the keys j with max(0, pos[r] - win + 1) <= j <= pos[r] (win = 0: all).
+ *
+ *   q    [rows, hq, d]  bf16, row stride q_row, head stride d
+ *   pos  [rows]         int32, device; -1: an empty sequence, whose out is zeros.
+ *                       Below -1: the same, WA_STATUS_BAD_POS; most * page_size and
+ *                       more: clamped to the last position, WA_STATUS_BAD_POS
+ *   cache               only entries of pages with a visible key are read; one of them
+ *                       outside [0, pages) stands for a page of zeros, WA_STATUS_BAD_PAGE
+ *   out  [rows, hq, d]  bf16, row stride out_row; must not overlap the inputs
+ *
+ * Probabilities are fp32 in the sums and enter P V as two bf16 parts, whose sum is
+ * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-12).  A (row,
+ * head) whose result is NaN or infinite is computed again in float64.  A row's
+ * bits depend on its own inputs alone: not on the batch, the row's place in it,
+ * which pages hold its keys, or `most`.  Slots past pos and before the window may
+ * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /
+ * hkv <= 16; strides of the pages multiples of 16 bytes, and the page stride a
+ * multiple of 8 slot strides or of the head stride; rows * hq < 2^31.  Returns WA_EINVAL otherwise.  Calls
+ * whose work can overlap need workspaces of their own; two captured graphs that
+ * replay at the same time do too.
+ */
+int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_pages* cache, int32_t win, float scale,
+                    int64_t q_row, int64_t out_row, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Waits for `stream`, then returns the WA_STATUS_* bits the last call that
  * used `ws` left (0 when clean), or a negative WA_E* code if the read fails.

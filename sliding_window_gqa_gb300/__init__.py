@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 import re
 import sys
@@ -22,9 +23,10 @@ import torch
 __all__ = [
     "WAError", "lib", "lib_path", "decode", "decode_static", "prompt", "prompt_sparse", "prep_append", "status",
     "tree_decode", "tree_verify", "tree_commit", "decode_ws_bytes", "prompt_ws_bytes", "tree_decode_ws_bytes",
+    "rope", "rope_frequencies", "paged_append", "paged_decode", "paged_decode_ws_bytes",
     "WA_OK", "WA_EINVAL", "WA_EWORKSPACE", "WA_ECUDA", "WA_EDEVICE",
     "WA_STATUS_BAD_POS", "WA_STATUS_BAD_HI", "WA_STATUS_TIMEOUT",
-    "WA_STATUS_BAD_TREE", "WA_STATUS_NO_MASS", "WA_TREE_MAX_NODES", "WA_COMMIT_MAX_LAYERS",
+    "WA_STATUS_BAD_TREE", "WA_STATUS_NO_MASS", "WA_STATUS_BAD_PAGE", "WA_TREE_MAX_NODES", "WA_COMMIT_MAX_LAYERS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +57,7 @@ WA_STATUS_BAD_HI = _C["WA_STATUS_BAD_HI"]
 WA_STATUS_TIMEOUT = _C["WA_STATUS_TIMEOUT"]
 WA_STATUS_BAD_TREE = _C["WA_STATUS_BAD_TREE"]
 WA_STATUS_NO_MASS = _C["WA_STATUS_NO_MASS"]
+WA_STATUS_BAD_PAGE = _C["WA_STATUS_BAD_PAGE"]
 WA_TREE_MAX_NODES = _C["WA_TREE_MAX_NODES"]
 WA_COMMIT_MAX_LAYERS = _C["WA_COMMIT_MAX_LAYERS"]
 
@@ -80,6 +83,17 @@ class _TreeStrides(ctypes.Structure):
 
 class _VerifyStrides(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in ("t_row", "t_node", "d_row", "d_node")]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("dims", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale", "table")] \
+        + [(f, ctypes.c_int64) for f in ("k_page", "k_slot", "k_head", "v_page", "v_slot", "v_head", "table_row")] \
+        + [(f, ctypes.c_int32) for f in ("pages", "page_size", "rows", "most", "hkv", "d", "type")]
 
 
 _lib = None
@@ -128,6 +142,16 @@ def lib() -> ctypes.CDLL:
         L.wa_tree_commit.argtypes = [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.POINTER(_TreeStrides), _P, _I, _P,
                                      _P, _P, ctypes.c_size_t, _P]
         L.wa_tree_commit.restype = ctypes.c_int
+        L.wa_rope.argtypes = [_P, _P, _I, _I, _I, ctypes.POINTER(_Rotary), _I, ctypes.c_int64, ctypes.c_int64, _P, _P]
+        L.wa_rope.restype = ctypes.c_int
+        L.wa_paged_append.argtypes = [_P, _P, _P, _I, _I, ctypes.POINTER(_Pages), ctypes.POINTER(_Rotary),
+                                      ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_size_t, _P]
+        L.wa_paged_append.restype = ctypes.c_int
+        L.wa_paged_decode_ws_bytes.argtypes = [ctypes.POINTER(_Pages), _I, _I]
+        L.wa_paged_decode_ws_bytes.restype = ctypes.c_size_t
+        L.wa_paged_decode.argtypes = [_P, _P, _I, ctypes.POINTER(_Pages), _I, ctypes.c_float, ctypes.c_int64,
+                                      ctypes.c_int64, _P, _P, ctypes.c_size_t, _P]
+        L.wa_paged_decode.restype = ctypes.c_int
         L.wa_status.argtypes = [_P, _P]
         L.wa_status.restype = ctypes.c_int
         L.wa_strerror.argtypes = [ctypes.c_int]
@@ -701,6 +725,290 @@ def tree_commit(k_tree, v_tree, k_ring, v_ring, path, length, pos, ws=None, stre
     if rc != WA_OK:
         raise WAError(rc, "wa_tree_commit")
     return ws
+
+
+# Rotary positions and a cache in pages.  As the drafted-token calls, these run on their inputs' device and on `stream`
+# or that device's current stream.
+
+_ROTARY_LAYOUTS = {"half": _C["WA_ROTARY_HALF"], "interleaved": _C["WA_ROTARY_INTERLEAVED"]}
+_PAGE_TYPES = {torch.bfloat16: _C["WA_PAGE_BF16"], torch.float8_e4m3fn: _C["WA_PAGE_E4M3"]}
+
+
+def rope_frequencies(dims: int, base: float = 10000.0, scaling=None, device=None):
+    """(inv_freq fp32 [dims / 2], factor) for rope() and paged_append(): base ** (-2 j / dims), and 1.0.
+
+    ``scaling`` stretches them for positions beyond the ``original`` length of training; s = its "factor":
+      {"kind": "linear", "factor"}: every frequency divided by s;
+      {"kind": "base", "factor"}: base times s ** (dims / (dims - 2)), which leaves the fastest pair as it is and
+          divides the slowest by s;
+      {"kind": "wavelength", "factor", "original", "low": 1, "high": 4}: pairs with fewer than `low` turns over the
+          original length divided by s, those with more than `high` as they are, in between a blend linear in the turns;
+      {"kind": "ramp", "factor", "original", "slow": 1, "fast": 32, "attention": None}: the pairs between the one of
+          `fast` turns over the original length and the one of `slow` blended linearly in the pair's index, and both
+          sides of the scores grow by `attention` (None: 0.1 ln s + 1), which is the factor returned.
+    Worked out in float64 and rounded once."""
+    dims = int(dims)
+    if dims <= 0 or dims % 2:
+        raise ValueError(f"dims must be even and positive, not {dims}")
+    if not (math.isfinite(base) and base > 1.0):
+        raise ValueError(f"base must be a number above 1, not {base}")
+    if scaling is not None and not isinstance(scaling, dict):
+        raise TypeError('scaling must be None or a dict with a "kind"')
+    opt = dict(scaling or {"kind": None})
+    kind, factor = opt.pop("kind", None), 1.0
+    inv = [base ** (-2.0 * j / dims) for j in range(dims // 2)]
+
+    def take(name, *default):
+        if name not in opt and not default:
+            raise ValueError(f'scaling "{kind}" needs "{name}"')
+        x = opt.pop(name, *default)
+        if x is not None and not (math.isfinite(x) and x > 0):
+            raise ValueError(f'"{name}" must be a positive number, not {x}')
+        return x
+
+    if kind is not None:
+        s = take("factor")
+    if kind == "linear":
+        inv = [w / s for w in inv]
+    elif kind == "base":
+        if dims < 4:
+            raise ValueError('scaling "base" needs at least 4 dims')
+        stretched = base * s ** (dims / (dims - 2))
+        inv = [stretched ** (-2.0 * j / dims) for j in range(dims // 2)]
+    elif kind == "wavelength":
+        original, lo, hi = take("original"), take("low", 1.0), take("high", 4.0)
+        if lo >= hi:
+            raise ValueError('"low" must be below "high"')
+        keep = [min(1.0, max(0.0, (original * w / (2 * math.pi) - lo) / (hi - lo))) for w in inv]
+        inv = [w * (k + (1 - k) / s) for w, k in zip(inv, keep)]
+    elif kind == "ramp":
+        original, slow, fast, attention = take("original"), take("slow", 1.0), take("fast", 32.0), take("attention", None)
+        if slow >= fast:
+            raise ValueError('"slow" must be below "fast"')
+
+        def pair(turns):      # the index of the pair with so many turns over the original length
+            return dims * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        first, last = max(0, math.floor(pair(fast))), min(dims - 1, math.ceil(pair(slow)))
+        cut = [min(1.0, max(0.0, (j - first) / max(last - first, 1e-3))) for j in range(dims // 2)]
+        inv = [w * (1 - c + c / s) for w, c in zip(inv, cut)]
+        factor = (0.1 * math.log(s) + 1.0 if s > 1 else 1.0) if attention is None else attention
+    elif kind is not None:
+        raise ValueError(f'scaling kind must be "linear", "base", "wavelength" or "ramp", not {kind!r}')
+    if opt:
+        raise ValueError(f"scaling has entries that {kind!r} does not take: {sorted(opt)}")
+    return torch.tensor(inv, dtype=torch.float64).float().to(device=device), float(factor)
+
+
+def _rotary(inv_freq, layout, factor, d: int):
+    """The library's description of a rotation (None: none); raises where it is not one of head dim d."""
+    if layout not in _ROTARY_LAYOUTS:
+        raise ValueError(f'layout must be "half" or "interleaved", not {layout!r}')
+    factor = float(_number("factor", factor))
+    if inv_freq is None:
+        return None
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 or not inv_freq.is_cuda:
+        raise TypeError("inv_freq must be an fp32 CUDA tensor")
+    dims = 2 * inv_freq.numel()
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or dims == 0 or dims % 16 or dims > d:
+        raise ValueError(f"inv_freq must be a contiguous vector of a multiple of 8 frequencies, at most {d // 2}")
+    if not math.isfinite(factor):
+        raise ValueError(f"factor must be finite, not {factor}")
+    return _Rotary(inv_freq.data_ptr(), dims, _ROTARY_LAYOUTS[layout], factor)
+
+
+def _token_rows(name: str, t: torch.Tensor):
+    """(token stride, heads, d) of a bf16 [tokens, heads, d] tensor whose tokens do not share memory."""
+    _check_bf16(name, t)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    n, heads, d = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be [tokens, heads, d] with head stride d and unit dim stride")
+    tok = int(t.stride(0)) if n > 1 else heads * d
+    if tok < heads * d:
+        raise ValueError(f"{name}'s tokens must not share memory")
+    return tok, heads, d
+
+
+def rope(x, pos, inv_freq, layout: str = "half", factor: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """Rotary positions: x [n, heads, d] bf16 (token-strided), pos int32 [n], inv_freq fp32 [dims / 2] on the GPU.
+
+    Pair (j, j + dims / 2) ("half") or (2 j, 2 j + 1) ("interleaved") of the first dims dims turns by pos * inv_freq[j]
+    and grows by ``factor``; the other dims stay.  ``inverse`` turns back: the gradient of x, given that of the
+    result.  Angles are exact for every position.  ``out`` may be x itself.  Returns out, [n, heads, d] bf16."""
+    bind = _short_way() if stream is None else None
+    if bind is not None:
+        got = bind.rope(x, pos, inv_freq, layout, factor, inverse, out)
+        if got is not None:
+            return _result(got, "wa_rope")
+    x_tok, heads, d = _token_rows("x", x)
+    n = x.shape[0]
+    _check_sizes(x.shape)
+    _check_i32("pos", pos, (n,))
+    if inv_freq is None:
+        raise TypeError("inv_freq must be an fp32 CUDA tensor")
+    rot = _rotary(inv_freq, layout, factor, d)
+    if out is not None:
+        out_tok = _token_rows("out", out)[0]
+        if out.shape != x.shape:
+            raise ValueError(f"out must have x's shape {tuple(x.shape)}")
+    _same_device(x.device, pos=pos, inv_freq=inv_freq, out=out)
+    dev = x.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope(x, pos, inv_freq, layout, factor, inverse, out, stream)
+    if out is None:
+        out, out_tok = _empty((n, heads, d), torch.bfloat16, dev, stream), heads * d
+    rc = lib().wa_rope(x.data_ptr(), pos.data_ptr(), n, heads, d, ctypes.byref(rot), int(bool(inverse)), x_tok, out_tok,
+                       out.data_ptr(), _stream_on(dev.index, stream))
+    if rc != WA_OK:
+        raise WAError(rc, "wa_rope")
+    return out
+
+
+def _pages(k_pages, v_pages, table, k_scale, v_scale):
+    """The library's description of a paged cache; raises where its tensors disagree."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _PAGE_TYPES or not t.is_cuda:
+            raise TypeError(f"{name} must be a bf16 or float8_e4m3fn CUDA tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [pages, page, hkv, d]")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must have unit dim stride")
+    if v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one type and one shape")
+    pages, page, hkv, d = k_pages.shape
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or not table.is_cuda:
+        raise TypeError("table must be an int32 CUDA tensor")
+    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be [rows, most] with unit inner stride")
+    rows, most = table.shape
+    _check_sizes((*k_pages.shape, rows, most))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None:
+            continue
+        if k_pages.dtype == torch.bfloat16:
+            raise ValueError(f"{name} belongs to pages of 8 bits")
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
+            raise TypeError(f"{name} must be an fp32 CUDA tensor")
+        if t.shape != (hkv,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and of shape {(hkv,)}")
+    _same_device(k_pages.device, v_pages=v_pages, table=table, k_scale=k_scale, v_scale=v_scale)
+
+    def strides(t):       # a dimension of one element may carry any stride
+        slot, head = t.stride(1), t.stride(2)
+        head = head if hkv > 1 else d
+        return (t.stride(0) if pages > 1 else max(slot * page, head * hkv)), slot, head
+
+    def at(t):
+        return None if t is None else t.data_ptr()
+
+    return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), at(k_scale), at(v_scale), table.data_ptr(), *strides(k_pages),
+                  *strides(v_pages), table.stride(0) if rows > 1 else most, pages, page, rows, most, hkv, d,
+                  _PAGE_TYPES[k_pages.dtype])
+
+
+def paged_append(src, pos, q_out, k_pages, v_pages, table, row=None, inv_freq=None, layout: str = "half",
+                 factor: float = 1.0, k_scale=None, v_scale=None, ws=None, stream=None):
+    """Append to a paged cache, with the rotation on the way.
+
+    src [n, (hq + 2 hkv) d] bf16 (token-strided): the tokens' query, key and value heads.  The query heads are rotated
+    into q_out [n, hq, d] (which may be their place in src), the key heads rotated and the value heads as they are into
+    position pos[t] (int32 [n]; -1: a token to leave out) of sequence row[t] (int32 [n], None: sequence t): slot
+    pos mod page of page table[row, pos / page] of k_pages / v_pages [pages, page, hkv, d], bf16 or float8_e4m3fn
+    (a value is stored as x / scale of its head, k_scale / v_scale fp32 [hkv]).  inv_freq, layout, factor as in rope();
+    None: no rotation.  Returns the workspace, whose status status() reads."""
+    bind = _short_way() if stream is None else None
+    if bind is not None:
+        got = bind.paged_append(src, pos, q_out, k_pages, v_pages, table, row, inv_freq, layout, factor, k_scale, v_scale, ws)
+        if got is not None:
+            return _result(got, "wa_paged_append")
+    _check_bf16("src", src)
+    if src.dim() != 2 or (src.shape[1] > 1 and src.stride(1) != 1):
+        raise ValueError("src must be [n, row] with unit inner stride")
+    cache = _pages(k_pages, v_pages, table, k_scale, v_scale)
+    q_tok, hq, d = _token_rows("q_out", q_out)
+    n, width = src.shape
+    _check_sizes((n, hq))
+    if q_out.shape[0] != n or d != cache.d:
+        raise ValueError(f"q_out {tuple(q_out.shape)} does not match {n} tokens of head dim {cache.d}")
+    if width < (hq + 2 * cache.hkv) * d:
+        raise ValueError(f"src rows hold {width} values, fewer than (hq + 2 hkv) d = {(hq + 2 * cache.hkv) * d}")
+    src_tok = int(src.stride(0)) if n > 1 else width
+    if src_tok < width:
+        raise ValueError("src's tokens must not share memory")
+    src_tok, q_tok = (src_tok, q_tok) if n > 1 else ((hq + 2 * cache.hkv) * d,) * 2
+    _check_i32("pos", pos, (n,))
+    if row is not None:
+        _check_i32("row", row, (n,))
+    elif n > cache.rows:
+        raise ValueError(f"{n} tokens of {cache.rows} sequences need `row`")
+    rot = _rotary(inv_freq, layout, factor, d)
+    _same_device(src.device, pos=pos, q_out=q_out, k_pages=k_pages, row=row, inv_freq=inv_freq)
+    dev = src.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_append(src, pos, q_out, k_pages, v_pages, table, row, inv_freq, layout, factor, k_scale, v_scale, ws,
+                                stream)
+    ws = _workspace_on(stream, 256, dev, ws, handed_back=True)
+    rc = lib().wa_paged_append(
+        src.data_ptr(), pos.data_ptr(), None if row is None else row.data_ptr(), n, hq, ctypes.byref(cache),
+        None if rot is None else ctypes.byref(rot), src_tok, q_tok, q_out.data_ptr(), ws.data_ptr(), _ws_bytes(ws),
+        _stream_on(dev.index, stream))
+    if rc != WA_OK:
+        raise WAError(rc, "wa_paged_append")
+    return ws
+
+
+def paged_decode_ws_bytes(rows: int, hq: int, hkv: int, d: int, page: int, most: int, win: int = 0,
+                          dtype=torch.bfloat16) -> int:
+    """Workspace bytes of paged_decode for these sizes (most: the table's columns); 0 for invalid ones."""
+    if not _fit_32_bits(rows, hq, hkv, d, page, most, win) or dtype not in _PAGE_TYPES:
+        return 0
+    sizes = _Pages(pages=1, page_size=page, rows=rows, most=most, hkv=hkv, d=d, type=_PAGE_TYPES[dtype])
+    return int(lib().wa_paged_decode_ws_bytes(ctypes.byref(sizes), hq, win))
+
+
+def paged_decode(q, k_pages, v_pages, table, pos, win: int = 0, scale: float = 1.0, k_scale=None, v_scale=None, out=None,
+                 ws=None, stream=None):
+    """Decode over a paged cache, one new token a sequence.
+
+    q [rows, hq, d] bf16 (row-strided); k_pages / v_pages [pages, page, hkv, d], bf16 or float8_e4m3fn with k_scale /
+    v_scale fp32 [hkv], in any layout of unit dim stride (heads of positions as a transposed view, keys and values in
+    one tensor); table int32 [rows, most]: the page of each `page` positions of a sequence, only those with a visible
+    key are read; pos int32 [rows]: the last key's position, -1 for an empty sequence, whose output is zeros.
+    Sequence r sees the last ``win`` keys (0: all).  Returns out [rows, hq, d] bf16.  ``ws``: a reused uint8 CUDA buffer
+    of paged_decode_ws_bytes(...)."""
+    bind = _short_way() if stream is None else None
+    if bind is not None:
+        got = bind.paged_decode(q, k_pages, v_pages, table, pos, win, scale, k_scale, v_scale, out, ws)
+        if got is not None:
+            return _result(got, "wa_paged_decode")
+    q_row, hq, d = _token_rows("q", q)
+    cache = _pages(k_pages, v_pages, table, k_scale, v_scale)
+    _check_sizes(q.shape)
+    if q.shape[0] != cache.rows or d != cache.d:
+        raise ValueError(f"q {tuple(q.shape)} does not match {cache.rows} sequences of head dim {cache.d}")
+    _check_i32("pos", pos, (cache.rows,))
+    if out is not None:
+        out_row = _token_rows("out", out)[0]
+        if out.shape != q.shape:
+            raise ValueError(f"out must have q's shape {tuple(q.shape)}")
+    win, scale = _window(win), float(_number("scale", scale))
+    _same_device(q.device, k_pages=k_pages, pos=pos, out=out)
+    dev = q.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_decode(q, k_pages, v_pages, table, pos, win, scale, k_scale, v_scale, out, ws, stream)
+    if out is None:
+        out, out_row = _empty(q.shape, torch.bfloat16, dev, stream), hq * d
+    ws = _workspace_on(stream, int(lib().wa_paged_decode_ws_bytes(ctypes.byref(cache), hq, win)), dev, ws)
+    rc = lib().wa_paged_decode(q.data_ptr(), pos.data_ptr(), hq, ctypes.byref(cache), win, scale, q_row, out_row,
+                               out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream_on(dev.index, stream))
+    if rc != WA_OK:
+        raise WAError(rc, "wa_paged_decode")
+    return out
 
 
 def status(ws, stream=None) -> int:

@@ -17,7 +17,8 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libwa.so")
 BIND = os.path.join(OUT, "wa_bind.so")
 SOURCES = ["wa_api.cu", "wa_decode.cu", "wa_prompt.cu", "wa_rerun.cu", "wa_static.cu", "wa_decode_tc.cu", "wa_prep.cu", "wa_prompt_sparse.cu",
-           "wa_tree.cu", "wa_tree_verify.cu", "wa_tree_commit.cu"]
+           "wa_tree.cu", "wa_tree_verify.cu", "wa_tree_commit.cu", "wa_paged_append.cu",
+           "wa_paged.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -70,6 +70,65 @@ bool rings_contradict(const wa::CommitArgs& a, int layers) {
     return false;
 }
 
+int log2_of(int32_t x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+// Whether no two elements of [pages][page_size][hkv][d] under these strides share memory, and all 16-byte pieces of a
+// head are aligned.
+bool pages_apart(const wa_pages& c, int64_t page, int64_t slot, int64_t head, int64_t align) {
+    if ((page | slot | head) & (align - 1)) return false;
+    struct { int64_t stride, size; } dim[3] = {{page, c.pages}, {slot, c.page_size}, {head, c.hkv}};
+    std::sort(dim, dim + 3, [](auto& x, auto& y) { return x.stride < y.stride; });
+    int64_t extent = c.d;        // elements that the dims so far span
+    for (auto& x : dim) {
+        if (x.size == 1) continue;
+        if (x.stride < extent || x.stride > (int64_t{1} << 38)) return false;
+        extent += x.stride * (x.size - 1);
+        if (extent > (int64_t{1} << 44)) return false;
+    }
+    return true;
+}
+
+bool page_sizes_ok(const wa_pages& c, int32_t hq, int32_t win) {
+    if (c.pages <= 0 || c.rows <= 0 || c.rows > 65535 || c.most <= 0 || !heads_ok(hq, c.hkv) || c.hkv > 65535) return false;
+    if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1)) || (c.d != 128 && c.d != 256)) return false;
+    if (c.type != WA_PAGE_BF16 && c.type != WA_PAGE_E4M3) return false;
+    if (static_cast<int64_t>(c.rows) * hq > INT32_MAX) return false;
+    // positions, and those of a tile past the last, stay in 32 bits
+    return win >= 0 && static_cast<int64_t>(c.most) * c.page_size <= INT32_MAX - 4096;
+}
+
+bool pages_ok(const wa_pages* c, int32_t hq, int32_t win) {
+    if (!c || !c->k || !c->v || !c->table || !page_sizes_ok(*c, hq, win)) return false;
+    if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->table) & 3u)) return false;
+    if (c->type == WA_PAGE_BF16 && (c->k_scale || c->v_scale)) return false;
+    if (c->table_row < c->most) return false;
+    const int64_t align = c->type == WA_PAGE_E4M3 ? 16 : 8;
+    return pages_apart(*c, c->k_page, c->k_slot, c->k_head, align) && pages_apart(*c, c->v_page, c->v_slot, c->v_head, align);
+}
+
+// Whether the decode's copies can name a page's keys by one index: pages apart by a whole number of 8 positions, or of heads.
+bool pages_in_steps(const wa_pages& c, int64_t page, int64_t slot, int64_t head) {
+    return c.pages == 1 || page % (8 * slot) == 0 || page % head == 0;
+}
+
+bool rotary_ok(const wa_rotary* r, int32_t d) {
+    if (!r || r->dims == 0) return true;
+    return r->inv_freq && r->dims > 0 && r->dims <= d && r->dims % 16 == 0 && std::isfinite(r->factor) &&
+           (r->layout == WA_ROTARY_HALF || r->layout == WA_ROTARY_INTERLEAVED);
+}
+
+void set_rotary(wa::PagedAppendArgs& a, const wa_rotary* r) {
+    if (!r || r->dims == 0) return;
+    a.inv_freq = r->inv_freq;
+    a.dims = r->dims;
+    a.layout = r->layout;
+    a.factor = r->factor;
+}
+
 }  // namespace
 
 extern "C" {
@@ -374,6 +433,82 @@ int wa_tree_commit(int32_t layers, const void* const* k_tree, const void* const*
     return WA_OK;
 }
 
+int wa_rope(const void* x, const int32_t* pos, int32_t n, int32_t heads, int32_t d, const wa_rotary* rot,
+            int32_t inverse, int64_t x_tok, int64_t out_tok, void* out, void* stream) {
+    if (!x || !pos || !out || !rot || !rotary_ok(rot, d)) return WA_EINVAL;
+    if (n <= 0 || heads <= 0 || heads > 65535 || (d != 128 && d != 256) || (inverse != 0 && inverse != 1)) return WA_EINVAL;
+    if (!aligned16(x) || !aligned16(out) || ((x_tok | out_tok) & 7)) return WA_EINVAL;
+    const int64_t width = static_cast<int64_t>(heads) * d;
+    if ((n > 1 && (x_tok < width || out_tok < width)) || (x == out && x_tok != out_tok)) return WA_EINVAL;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+    wa::PagedAppendArgs a{};
+    a.src = x; a.pos = pos; a.q_out = out;
+    a.n = n; a.hq = heads; a.d = d; a.inverse = inverse;
+    a.src_tok = x_tok; a.q_tok = out_tok;
+    set_rotary(a, rot);
+    return wa::launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WA_OK : WA_ECUDA;
+}
+
+int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int32_t n, int32_t hq,
+                    const wa_pages* cache, const wa_rotary* rot, int64_t src_tok, int64_t q_tok, void* q_out,
+                    void* ws, size_t ws_bytes, void* stream) {
+    if (!src || !pos || !q_out || n <= 0 || !pages_ok(cache, hq, 0) || !rotary_ok(rot, cache->d)) return WA_EINVAL;
+    if ((!row && n > cache->rows) || cache->k == cache->v) return WA_EINVAL;
+    if (!aligned16(src) || !aligned16(q_out) || ((src_tok | q_tok) & 7)) return WA_EINVAL;
+    const int64_t width = static_cast<int64_t>(hq + 2 * cache->hkv) * cache->d;
+    if (n > 1 && (src_tok < width || q_tok < static_cast<int64_t>(hq) * cache->d)) return WA_EINVAL;
+    if (src == q_out && n > 1 && src_tok != q_tok) return WA_EINVAL;
+    if (!ws || ws_bytes < WA_PAGED_APPEND_WS_BYTES || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+    wa::PagedAppendArgs a{};
+    a.src = src; a.pos = pos; a.row = row; a.q_out = q_out;
+    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, cache->k_head};
+    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, cache->v_head};
+    a.table = cache->table; a.table_row = cache->table_row;
+    a.src_tok = src_tok; a.q_tok = q_tok;
+    a.hdr = static_cast<wa::WsHeader*>(ws);
+    a.n = n; a.hq = hq; a.hkv = cache->hkv; a.d = cache->d;
+    a.pages = cache->pages; a.page_log = log2_of(cache->page_size); a.rows = cache->rows; a.most = cache->most;
+    a.e4m3 = cache->type == WA_PAGE_E4M3;
+    set_rotary(a, rot);
+    return wa::launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WA_OK : WA_ECUDA;
+}
+
+size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win) {
+    if (!cache || !page_sizes_ok(*cache, hq, win)) return 0;
+    return wa::kHeaderBytes + flags_bytes(static_cast<int64_t>(cache->rows) * hq);
+}
+
+int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_pages* cache, int32_t win, float scale,
+                    int64_t q_row, int64_t out_row, void* out, void* ws, size_t ws_bytes, void* stream) {
+    if (!q || !pos || !out || !pages_ok(cache, hq, win) || !std::isfinite(scale)) return WA_EINVAL;
+    if (!pages_in_steps(*cache, cache->k_page, cache->k_slot, cache->k_head) ||
+        !pages_in_steps(*cache, cache->v_page, cache->v_slot, cache->v_head))
+        return WA_EINVAL;
+    if (!aligned16(q) || !aligned16(out) || ((q_row | out_row) & 7)) return WA_EINVAL;
+    const int64_t width = static_cast<int64_t>(hq) * cache->d;
+    if (cache->rows > 1 && (q_row < width || out_row < width)) return WA_EINVAL;
+    const size_t need = wa_paged_decode_ws_bytes(cache, hq, win);
+    if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
+    const int rc = ensure_device();
+    if (rc != WA_OK) return rc;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    wa::PagedArgs a{};
+    a.q = q; a.pos = pos; a.out = out;
+    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, cache->k_head};
+    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, cache->v_head};
+    a.table = cache->table; a.table_row = cache->table_row; a.q_row = q_row; a.o_row = out_row;
+    a.hdr = reinterpret_cast<wa::WsHeader*>(base);
+    a.flags = reinterpret_cast<int*>(base + wa::kHeaderBytes);
+    a.rows = cache->rows; a.hq = hq; a.hkv = cache->hkv; a.d = cache->d;
+    a.pages = cache->pages; a.page_log = log2_of(cache->page_size); a.most = cache->most;
+    a.e4m3 = cache->type == WA_PAGE_E4M3;
+    a.win = win; a.scale = scale;
+    return wa::launch_paged_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WA_OK : WA_ECUDA;
+}
+
 int wa_status(const void* ws, void* stream) {
     if (!ws) {   // the header of wa_decode_static's scratch on the current device
         void* sws = nullptr;
@@ -401,6 +536,7 @@ const char* wa_strerror(int code) {
         case WA_STATUS_TIMEOUT: return "status: a device wait ran out; outputs are not valid";
         case WA_STATUS_BAD_TREE: return "status: a tree's parent, node count, token, path or length was out of range (clamped or skipped)";
         case WA_STATUS_NO_MASS: return "status: a distribution without mass; its row has no token";
+        case WA_STATUS_BAD_PAGE: return "status: a page table entry or a token's row was out of range (skipped, or read as zeros)";
         case WA_STATUS_LAYOUT: return "status: shared memory misaligned; outputs were not written";
         default:
             if (code > 0) return "status: several WA_STATUS bits";

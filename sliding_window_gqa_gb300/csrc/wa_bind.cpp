@@ -1,9 +1,9 @@
-// wa_bind.cpp — the drafted-token calls' short way from Python to the C ABI.
+// wa_bind.cpp — the short way from Python to the C ABI of the drafted-token and paged-cache calls.
 //
 // A call for one sequence runs for five to twenty microseconds on the GPU, and the checks of its tensors as
 // Python expressions took as long again.  This module does them on the tensors themselves (under a
-// microsecond) for the ordinary call: contiguous tensors of the right types on the current device, its current
-// stream.  For any other call, valid or not, each function returns None and the package's own checks, which name
+// microsecond) for the ordinary call: tensors of the right types (contiguous, or in the paged-cache calls laid out as
+// the library takes them) on the current device, its current stream.  For any other call, valid or not, each function returns None and the package's own checks, which name
 // what is wrong, take it from there.  On success a function returns the call's tensors, and a WA_E* code as an
 // int where the library refused it.
 #define PY_SSIZE_T_CLEAN
@@ -217,7 +217,199 @@ PyObject* tree_commit(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
     });
 }
 
+// ---- rotary positions and the paged cache
+
+bool on(const Tensor* t, at::ScalarType type, int64_t dev) {
+    return t && t->defined() && t->is_cuda() && t->scalar_type() == type && t->get_device() == dev;
+}
+
+// A bf16 [tokens, heads, d] tensor with head stride d; its token stride.
+bool token_rows(const Tensor* t, int64_t dev, int64_t& tok) {
+    if (!on(t, at::kBFloat16, dev) || t->dim() != 3) return false;
+    const int64_t n = t->size(0), heads = t->size(1), d = t->size(2);
+    if (n > INT32_MAX || heads > INT32_MAX || d > INT32_MAX || t->stride(2) != 1 || (heads > 1 && t->stride(1) != d)) return false;
+    tok = n > 1 ? t->stride(0) : heads * d;
+    return tok >= heads * d;
+}
+
+// inv_freq, layout, factor as the library takes them; dims 0 for no rotation.
+bool rotary(PyObject* freq, PyObject* layout, PyObject* factor, int64_t d, int64_t dev, wa_rotary& r) {
+    if (!PyUnicode_Check(layout)) return false;
+    if (PyUnicode_CompareWithASCIIString(layout, "half") == 0) r.layout = WA_ROTARY_HALF;
+    else if (PyUnicode_CompareWithASCIIString(layout, "interleaved") == 0) r.layout = WA_ROTARY_INTERLEAVED;
+    else return false;
+    const double f = PyFloat_AsDouble(factor);
+    if (PyErr_Occurred()) return false;
+    r.factor = static_cast<float>(f);
+    if (freq == Py_None) return true;
+    const Tensor* t = tensor(freq);
+    if (!plain(t, at::kFloat, dev) || t->dim() != 1 || t->numel() == 0 || 2 * t->numel() > d || t->numel() % 8) return false;
+    r.inv_freq = static_cast<const float*>(t->data_ptr());
+    r.dims = static_cast<int32_t>(2 * t->numel());
+    return true;
+}
+
+// The paged cache as the library takes it.
+bool paged(PyObject* ko, PyObject* vo, PyObject* table_o, PyObject* ks, PyObject* vs, int64_t dev, wa_pages& c) {
+    const Tensor *k = tensor(ko), *v = tensor(vo), *table = tensor(table_o);
+    if (!k || !k->defined() || k->dim() != 4) return false;
+    const at::ScalarType type = k->scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat8_e4m3fn) return false;
+    if (!on(k, type, dev) || !on(v, type, dev) || v->sizes() != k->sizes() || k->stride(3) != 1 || v->stride(3) != 1) return false;
+    if (!on(table, at::kInt, dev) || table->dim() != 2 || (table->size(1) > 1 && table->stride(1) != 1)) return false;
+    for (int64_t x : {k->size(0), k->size(1), k->size(2), k->size(3), table->size(0), table->size(1)})
+        if (x > INT32_MAX || x == 0) return false;
+    const int64_t pages = k->size(0), page = k->size(1), hkv = k->size(2), d = k->size(3);
+    const float* scale[2] = {nullptr, nullptr};
+    PyObject* so[2] = {ks, vs};
+    for (int i = 0; i < 2; ++i) {
+        if (so[i] == Py_None) continue;
+        const Tensor* t = tensor(so[i]);
+        if (type == at::kBFloat16 || !plain(t, at::kFloat, dev) || !sized(t, {hkv})) return false;
+        scale[i] = static_cast<const float*>(t->data_ptr());
+    }
+    auto strides = [&](const Tensor* t, int64_t& ps, int64_t& slot, int64_t& head) {
+        slot = t->stride(1);
+        head = hkv > 1 ? t->stride(2) : d;
+        ps = pages > 1 ? t->stride(0) : (slot * page > head * hkv ? slot * page : head * hkv);
+    };
+    c.k = k->data_ptr();
+    c.v = v->data_ptr();
+    c.k_scale = scale[0];
+    c.v_scale = scale[1];
+    c.table = static_cast<const int32_t*>(table->data_ptr());
+    strides(k, c.k_page, c.k_slot, c.k_head);
+    strides(v, c.v_page, c.v_slot, c.v_head);
+    c.rows = static_cast<int32_t>(table->size(0));
+    c.most = static_cast<int32_t>(table->size(1));
+    c.table_row = c.rows > 1 ? table->stride(0) : c.most;
+    c.pages = static_cast<int32_t>(pages);
+    c.page_size = static_cast<int32_t>(page);
+    c.hkv = static_cast<int32_t>(hkv);
+    c.d = static_cast<int32_t>(d);
+    c.type = type == at::kBFloat16 ? WA_PAGE_BF16 : WA_PAGE_E4M3;
+    return true;
+}
+
+// rope(x, pos, inv_freq, layout, factor, inverse, out) -> out
+PyObject* rope(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject* {
+        if (nargs != 7) return none();
+        const Tensor *x = tensor(arg[0]), *pos = tensor(arg[1]);
+        if (!x || !x->defined() || !x->is_cuda()) return none();
+        const int64_t dev = x->get_device();
+        int64_t x_tok, out_tok;
+        if (!token_rows(x, dev, x_tok) || !plain(pos, at::kInt, dev) || !sized(pos, {x->size(0)})) return none();
+        wa_rotary r{};
+        if (!rotary(arg[2], arg[3], arg[4], x->size(2), dev, r) || r.dims == 0) return none();
+        if ((arg[5] != Py_True && arg[5] != Py_False) || dev != c10::cuda::current_device()) return none();
+        Tensor out;
+        if (arg[6] == Py_None) {
+            out = make(x->sizes(), at::kBFloat16, *x);
+            out_tok = x->size(1) * x->size(2);
+        } else {
+            const Tensor* o = tensor(arg[6]);
+            if (!token_rows(o, dev, out_tok) || o->sizes() != x->sizes()) return none();
+            out = *o;
+        }
+        int rc;
+        cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
+        const int32_t inverse = arg[5] == Py_True;
+        Py_BEGIN_ALLOW_THREADS
+        rc = wa_rope(x->data_ptr(), static_cast<const int32_t*>(pos->data_ptr()), x->size(0), x->size(1), x->size(2), &r, inverse,
+                     x_tok, out_tok, out.data_ptr(), s);
+        Py_END_ALLOW_THREADS
+        if (rc != WA_OK) return PyLong_FromLong(rc);
+        if (arg[6] != Py_None) {
+            Py_INCREF(arg[6]);
+            return arg[6];
+        }
+        return THPVariable_Wrap(std::move(out));
+    });
+}
+
+// paged_append(src, pos, q_out, k_pages, v_pages, table, row, inv_freq, layout, factor, k_scale, v_scale, ws) -> ws
+PyObject* paged_append(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject* {
+        if (nargs != 13) return none();
+        const Tensor *src = tensor(arg[0]), *pos = tensor(arg[1]), *q = tensor(arg[2]);
+        if (!src || !src->defined() || !src->is_cuda() || src->dim() != 2 || src->stride(1) != 1) return none();
+        const int64_t dev = src->get_device(), n = src->size(0), width = src->size(1);
+        wa_pages c{};
+        wa_rotary r{};
+        int64_t q_tok;
+        if (!on(src, at::kBFloat16, dev) || !token_rows(q, dev, q_tok) || !paged(arg[3], arg[4], arg[5], arg[10], arg[11], dev, c)) return none();
+        const int64_t hq = q->size(1), need = (hq + 2 * static_cast<int64_t>(c.hkv)) * c.d;
+        if (n < 1 || n > INT32_MAX || q->size(0) != n || q->size(2) != c.d || width < need) return none();
+        int64_t src_tok = src->stride(0);
+        if (n == 1) src_tok = q_tok = need;
+        if (src_tok < (n > 1 ? width : need) || !plain(pos, at::kInt, dev) || !sized(pos, {n})) return none();
+        const Tensor* row = arg[6] == Py_None ? nullptr : tensor(arg[6]);
+        if (arg[6] != Py_None ? !plain(row, at::kInt, dev) || !sized(row, {n}) : n > c.rows) return none();
+        if (!rotary(arg[7], arg[8], arg[9], c.d, dev, r) || dev != c10::cuda::current_device()) return none();
+        Tensor ws;
+        if (!workspace(arg[12], WA_PAGED_APPEND_WS_BYTES, *src, ws)) return none();
+        int rc;
+        cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
+        Py_BEGIN_ALLOW_THREADS
+        rc = wa_paged_append(src->data_ptr(), static_cast<const int32_t*>(pos->data_ptr()),
+                             row ? static_cast<const int32_t*>(row->data_ptr()) : nullptr, n, hq, &c, &r, src_tok, q_tok,
+                             q->data_ptr(), ws.data_ptr(), ws.numel(), s);
+        Py_END_ALLOW_THREADS
+        if (rc != WA_OK) return PyLong_FromLong(rc);
+        if (arg[12] != Py_None) {
+            Py_INCREF(arg[12]);
+            return arg[12];
+        }
+        return THPVariable_Wrap(std::move(ws));
+    });
+}
+
+// paged_decode(q, k_pages, v_pages, table, pos, win, scale, k_scale, v_scale, out, ws) -> out
+PyObject* paged_decode(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject* {
+        if (nargs != 11) return none();
+        const Tensor *q = tensor(arg[0]), *pos = tensor(arg[4]);
+        if (!q || !q->defined() || !q->is_cuda()) return none();
+        const int64_t dev = q->get_device();
+        int64_t q_row, out_row;
+        wa_pages c{};
+        if (!token_rows(q, dev, q_row) || !paged(arg[1], arg[2], arg[3], arg[7], arg[8], dev, c)) return none();
+        const int64_t rows = q->size(0), hq = q->size(1), d = q->size(2);
+        if (rows != c.rows || d != c.d || !plain(pos, at::kInt, dev) || !sized(pos, {rows})) return none();
+        const long win = PyLong_AsLong(arg[5]);
+        const double scale = PyFloat_AsDouble(arg[6]);
+        if (PyErr_Occurred() || win < INT32_MIN || win > INT32_MAX) return none();
+        if (dev != c10::cuda::current_device()) return none();
+        Tensor out, ws;
+        if (arg[9] == Py_None) {
+            out = make(q->sizes(), at::kBFloat16, *q);
+            out_row = hq * d;
+        } else {
+            const Tensor* o = tensor(arg[9]);
+            if (!token_rows(o, dev, out_row) || o->sizes() != q->sizes()) return none();
+            out = *o;
+        }
+        if (!workspace(arg[10], wa_paged_decode_ws_bytes(&c, hq, win), *q, ws)) return none();
+        int rc;
+        cudaStream_t s = c10::cuda::getCurrentCUDAStream(dev).stream();
+        Py_BEGIN_ALLOW_THREADS
+        rc = wa_paged_decode(q->data_ptr(), static_cast<const int32_t*>(pos->data_ptr()), hq, &c, win, static_cast<float>(scale), q_row,
+                             out_row, out.data_ptr(), ws.data_ptr(), ws.numel(), s);
+        Py_END_ALLOW_THREADS
+        if (rc != WA_OK) return PyLong_FromLong(rc);
+        if (arg[9] != Py_None) {
+            Py_INCREF(arg[9]);
+            return arg[9];
+        }
+        return THPVariable_Wrap(std::move(out));
+    });
+}
+
 PyMethodDef methods[] = {
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope)), METH_FASTCALL, nullptr},
+    {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_append)), METH_FASTCALL, nullptr},
+    {"paged_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_decode)), METH_FASTCALL, nullptr},
     {"tree_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_decode)), METH_FASTCALL, nullptr},
     {"tree_verify", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_verify)), METH_FASTCALL, nullptr},
     {"tree_commit", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree_commit)), METH_FASTCALL, nullptr},

@@ -102,6 +102,42 @@ struct VerifyArgs {
     WsHeader* hdr;
 };
 
+// Keys or values of a paged cache: strides in elements.
+struct PageSide {
+    void* base;
+    const float* scale;      // may be null
+    int64_t page, slot, head;
+};
+
+// Rotary positions (hkv = 0, no cache) and append to a paged cache.
+struct PagedAppendArgs {
+    const void* src;
+    const int32_t* pos;
+    const int32_t* row;      // may be null
+    const float* inv_freq;
+    PageSide kv[2];
+    const int32_t* table;
+    int64_t src_tok, q_tok, table_row;
+    void* q_out;
+    WsHeader* hdr;           // null: nothing to report (wa_rope)
+    int n, hq, hkv, d, dims, layout, inverse, pages, page_log, rows, most, e4m3;
+    float factor;
+};
+
+// Decode over a paged cache.
+struct PagedArgs {
+    const void* q;
+    const int32_t* pos;
+    PageSide kv[2];
+    const int32_t* table;
+    int64_t table_row, q_row, o_row;
+    void* out;
+    WsHeader* hdr;
+    int* flags;              // [rows * hq]
+    int rows, hq, hkv, d, pages, page_log, most, e4m3, win;
+    float scale;
+};
+
 // Kept nodes' keys and values into the rings of several layers.
 struct CommitArgs {
     const void* src[2][WA_COMMIT_MAX_LAYERS];   // [k, v]
@@ -167,6 +203,8 @@ cudaError_t launch_rerun(const RerunArgs& a, cudaStream_t s);
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t s);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t tree_prepare_device(int dev);
 cudaError_t prompt_prepare_device(int dev);

@@ -1,0 +1,220 @@
+// wa_paged_append.cu — rotary positions, alone or on the way into a cache in pages.
+//
+// Pair (a, b) of token t turns by pos[t] * inv_freq[j]:
+//   y_a = f (x_a cos - x_b sin),  y_b = f (x_b cos + x_a sin).
+// One kernel serves both calls: wa_rope is an append of query heads alone.
+//
+// Angles.  fl32(pos * inv_freq) is off by up to 2^-24 of the angle, 0.06 rad at
+// position 10^6, and a float64 product runs at a fiftieth of the fp32 rate here.
+// So inv_freq / (2 pi) becomes a 64-bit fixed-point fraction of a turn, by a 24 x
+// 96-bit integer product, and times pos, modulo 2^64, that is the angle's
+// fraction of a turn to 2^-33 for every int32 position; sincospif takes it from there.
+//
+// HBM-bound: a head is served by L = d / 16 lanes of two 16-byte pieces each, so
+// that both halves of a pair sit in one lane for either layout, a warp takes P =
+// 32 / L heads a pass and kAppendPasses passes of one token, all loads issued
+// before the angles are worked out (once a warp, whatever its heads).
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "wa.h"
+#include "wa_internal.h"
+
+namespace wa {
+
+namespace {
+
+constexpr int kAppendWarps = 8;
+constexpr int kAppendPasses = 4;
+// Up to this many tokens one more block checks them all and writes the status word; beyond, the word is cleared
+// before the launch and a warp a token reports.
+constexpr int kStatusBlockTokens = 2048;
+
+struct AppendParams {
+    PagedAppendArgs a;
+    int warps_per_token, status_block;
+};
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void unpack(const uint4& u, float* x) {
+    x[0] = low(u.x); x[1] = high(u.x); x[2] = low(u.y); x[3] = high(u.y);
+    x[4] = low(u.z); x[5] = high(u.z); x[6] = low(u.w); x[7] = high(u.w);
+}
+
+__device__ __forceinline__ uint32_t pair_bf16(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 pack(const float* x) {
+    return make_uint4(pair_bf16(x[0], x[1]), pair_bf16(x[2], x[3]), pair_bf16(x[4], x[5]), pair_bf16(x[6], x[7]));
+}
+
+__device__ __forceinline__ uint32_t quad_e4m3(const float* x, float scale) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0] / scale, x[1] / scale), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2] / scale, x[3] / scale), __NV_SATFINITE, __NV_E4M3);
+    return a | (b << 16);
+}
+
+// |w| / (2 pi) modulo 1 as a 64-bit fraction, for |w| < 16: w = m 2^(e - 150), times 2^96 / (2 pi) to the nearest
+// integer, shifted down to units of 2^-64.  Cut off, so off by less than 2^-64 + 2^-73.
+__device__ __forceinline__ uint64_t turn_fraction(float w) {
+    const uint32_t b = __float_as_uint(w), e = (b >> 23) & 255u, exp = e ? e : 1u;
+    const uint64_t m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    const uint64_t p0 = m * 0x7F09D5F4u, p1 = m * 0x9391054Au + (p0 >> 32), p2 = m * 0x28BE60DBu + (p1 >> 32);
+    const uint64_t lo = (p1 << 32) | (p0 & 0xFFFFFFFFu), hi = p2;
+    const uint32_t s = 182u - exp;
+    const uint64_t f = s < 64u ? (hi << (64u - s)) | (lo >> s) : s < 128u ? hi >> (s - 64u) : 0ull;
+    return (b >> 31) ? 0ull - f : f;
+}
+
+// The bad bits of token t's place, and where it is: page < 0 for none.
+__device__ __forceinline__ int place(const PagedAppendArgs& a, int t, int pos, int& page) {
+    page = -1;
+    if (pos < 0) return pos < -1 ? WA_STATUS_BAD_POS : 0;
+    if ((pos >> a.page_log) >= a.most) return WA_STATUS_BAD_POS;
+    const int row = a.row ? a.row[t] : t;
+    if (row < 0 || row >= a.rows) return WA_STATUS_BAD_PAGE;
+    page = a.table[row * a.table_row + (pos >> a.page_log)];
+    if (page >= 0 && page < a.pages) return 0;
+    page = -1;
+    return WA_STATUS_BAD_PAGE;
+}
+
+template <int D, bool CACHE, bool FP8>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendParams p) {
+    const PagedAppendArgs& a = p.a;
+    constexpr int L = D / 16;              // lanes a head
+    constexpr int P = 32 / L;              // heads a pass
+    constexpr int HPW = P * kAppendPasses; // heads a warp
+    if constexpr (CACHE) {
+        if (p.status_block && blockIdx.x == gridDim.x - 1) {
+            int bad = 0, page;
+            for (int t = threadIdx.x; t < a.n; t += kAppendWarps * 32) bad |= place(a, t, a.pos[t], page);
+            const int where = __syncthreads_or(bad & WA_STATUS_BAD_POS), which = __syncthreads_or(bad & WA_STATUS_BAD_PAGE);
+            if (threadIdx.x == 0) a.hdr->status = (where ? WA_STATUS_BAD_POS : 0) | (which ? WA_STATUS_BAD_PAGE : 0);
+            return;
+        }
+    }
+    const int64_t wid = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+    if (wid >= static_cast<int64_t>(a.n) * p.warps_per_token) return;     // warp-uniform
+    const int lane = threadIdx.x & 31, li = lane % L, hp = lane / L;
+    const int t = static_cast<int>(wid / p.warps_per_token), first = static_cast<int>(wid % p.warps_per_token) * HPW;
+    const int nqk = a.hq + a.hkv, heads = nqk + a.hkv;
+    const int pos = a.pos[t];
+    const bool turns = li < a.dims / 16;
+    // a lane's two pieces of a head that turns: of dims (j, j + dims / 2), or 16 neighbours; of any other, 16 neighbours
+    const int one = turns && a.layout == WA_ROTARY_HALF ? 8 * li : 16 * li;
+    const int two = turns && a.layout == WA_ROTARY_HALF ? a.dims / 2 + 8 * li : 16 * li + 8;
+    const uint16_t* src = static_cast<const uint16_t*>(a.src) + t * a.src_tok;
+    uint4 raw[kAppendPasses][2];
+#pragma unroll
+    for (int u = 0; u < kAppendPasses; ++u) {
+        const int h = first + u * P + hp;
+        if (h < heads) {
+            const uint16_t* x = src + static_cast<int64_t>(h) * D;
+            raw[u][0] = *reinterpret_cast<const uint4*>(x + (h < nqk ? one : 16 * li));
+            raw[u][1] = *reinterpret_cast<const uint4*>(x + (h < nqk ? two : 16 * li + 8));
+        }
+    }
+    int page = -1;
+    if constexpr (CACHE) {
+        if (first + HPW > a.hq || (first == 0 && !p.status_block)) {       // a warp with keys or values, or one that reports
+            const int bad = place(a, t, pos, page);
+            if (bad && first == 0 && !p.status_block && lane == 0) atomicOr(&a.hdr->status, bad);
+        }
+        if (pos < 0 || (pos >> a.page_log) >= a.most) return;
+    }
+    float c[8], s[8];
+    if (turns && first < nqk) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float w = a.inv_freq[8 * li + e];
+            const uint64_t turn = turn_fraction(w) * static_cast<uint64_t>(static_cast<int64_t>(pos));
+            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s[e], &c[e]);
+            const float f = fabsf(w) < 16.f ? a.factor : NAN;
+            c[e] *= f;
+            s[e] *= a.inverse ? -f : f;
+        }
+    }
+    const int64_t slot = CACHE ? pos & ((1 << a.page_log) - 1) : 0;
+#pragma unroll
+    for (int u = 0; u < kAppendPasses; ++u) {
+        const int h = first + u * P + hp;
+        if (h >= heads) continue;
+        float x[16];
+        unpack(raw[u][0], x);
+        unpack(raw[u][1], x + 8);
+        if (turns && h < nqk) {
+            if (a.layout == WA_ROTARY_HALF) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xa = x[e], xb = x[8 + e];
+                    x[e] = fmaf(xa, c[e], -xb * s[e]);
+                    x[8 + e] = fmaf(xb, c[e], xa * s[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xa = x[2 * e], xb = x[2 * e + 1];
+                    x[2 * e] = fmaf(xa, c[e], -xb * s[e]);
+                    x[2 * e + 1] = fmaf(xb, c[e], xa * s[e]);
+                }
+            }
+        }
+        const int o1 = h < nqk ? one : 16 * li, o2 = h < nqk ? two : 16 * li + 8;
+        if (!CACHE || h < a.hq) {
+            uint16_t* out = static_cast<uint16_t*>(a.q_out) + t * a.q_tok + static_cast<int64_t>(h) * D;
+            *reinterpret_cast<uint4*>(out + o1) = pack(x);
+            *reinterpret_cast<uint4*>(out + o2) = pack(x + 8);
+        } else if (page >= 0) {
+            const PageSide& side = a.kv[h < nqk ? 0 : 1];
+            const int g = h - (h < nqk ? a.hq : nqk);
+            const int64_t at = page * side.page + slot * side.slot + g * side.head;
+            if constexpr (FP8) {
+                const float scale = side.scale ? side.scale[g] : 1.f;
+                uint8_t* out = static_cast<uint8_t*>(side.base) + at;
+                *reinterpret_cast<uint2*>(out + o1) = make_uint2(quad_e4m3(x, scale), quad_e4m3(x + 4, scale));
+                *reinterpret_cast<uint2*>(out + o2) = make_uint2(quad_e4m3(x + 8, scale), quad_e4m3(x + 12, scale));
+            } else {
+                uint16_t* out = static_cast<uint16_t*>(side.base) + at;
+                *reinterpret_cast<uint4*>(out + o1) = pack(x);
+                *reinterpret_cast<uint4*>(out + o2) = pack(x + 8);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
+    AppendParams p{};
+    p.a = a;
+    const int hpw = 32 / (a.d / 16) * kAppendPasses;
+    p.warps_per_token = (a.hq + 2 * a.hkv + hpw - 1) / hpw;
+    const bool cache = a.hkv > 0;
+    p.status_block = cache && a.n <= kStatusBlockTokens;
+    if (cache && !p.status_block) {
+        const cudaError_t e = cudaMemsetAsync(a.hdr, 0, sizeof(int), s);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t blocks = (static_cast<int64_t>(a.n) * p.warps_per_token + kAppendWarps - 1) / kAppendWarps + p.status_block;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    constexpr int threads = kAppendWarps * 32;
+    if (a.d == 256) {
+        if (!cache) append_kernel<256, false, false><<<grid, threads, 0, s>>>(p);
+        else if (a.e4m3) append_kernel<256, true, true><<<grid, threads, 0, s>>>(p);
+        else append_kernel<256, true, false><<<grid, threads, 0, s>>>(p);
+    } else {
+        if (!cache) append_kernel<128, false, false><<<grid, threads, 0, s>>>(p);
+        else if (a.e4m3) append_kernel<128, true, true><<<grid, threads, 0, s>>>(p);
+        else append_kernel<128, true, false><<<grid, threads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace wa

@@ -35,6 +35,7 @@ __all__ = [
     "sparse_selection",
     "draft_tree",
     "tree_case",
+    "paged_case",
     "window_lo",
 ]
 
@@ -277,3 +278,56 @@ def tree_case(rows, nodes, hq, hkv, d, win, ring, pos, seed, kind="random", n=No
                                  device=device),
              n=None if n is None else torch.tensor(n, dtype=torch.int32, device=device))
     return c
+
+
+def paged_case(lengths, hq, hkv, d, page, seed, win=0, bits=16, heads_first=False, joint=False, spare=2, most=None,
+               device="cpu", outside="nan", peaked=True):
+    """Paged-cache decode inputs: sequences of ``lengths`` keys (0: an empty one) out of one shuffled pool of pages.
+
+    Returns q [rows, hq, d] bf16, k / v [pages, page, hkv, d] (bf16, or float8_e4m3fn with k_scale / v_scale fp32
+    [hkv] for ``bits`` 8), table int32 [rows, most], pos int32 [rows].  ``heads_first``: a page holds heads of positions;
+    ``joint``: keys and values are halves of one tensor's pages.  Slots without a visible key, and pages that no table
+    names, hold NaN for ``outside == "nan"``; table entries of pages without a visible key are -1."""
+    device = torch.device(device)
+    rows, G = len(lengths), hq // hkv
+    q, _ = _draw_rows((rows, hq, d), 0.95, 1.05, _gen(seed, "q", device), _gen(seed, "qr", device), device)
+    q16 = q.to(torch.bfloat16)
+    first = [window_lo(n - 1, win) // page for n in lengths]
+    live = [(r, j) for r, n in enumerate(lengths) for j in range(first[r], (n - 1) // page + 1)]
+    count = len(live) + spare
+    order = torch.randperm(count, generator=_gen(seed, "pos", "cpu")).tolist()
+    most = most or max(1, max((n - 1) // page + 1 for n in lengths))
+    table = torch.full((rows, most), -1, dtype=torch.int32)
+    for (r, j), i in zip(live, order):
+        table[r, j] = i
+    k, kr = _draw_rows((count, page, hkv, d), 0.06, 0.13, _gen(seed, "k", device), _gen(seed, "kr", device), device)
+    v = torch.randn((count, page, hkv, d), generator=_gen(seed, "v", device), device=device)
+    held = torch.zeros((count, page), dtype=torch.bool)
+    gp = _gen(seed, "peak", "cpu")
+    for r, n in enumerate(lengths):
+        for at in range(window_lo(n - 1, win), n):
+            held[table[r, at // page], at % page] = True
+        for g in range(hkv if peaked and n > 0 else 0):
+            lo = window_lo(n - 1, win)
+            at, h = lo + int(torch.randint(n - lo, (1,), generator=gp)), g * G + int(torch.randint(G, (1,), generator=gp))
+            i, slot = int(table[r, at // page]), at % page
+            qh = q16[r, h].float()
+            k[i, slot, g] = qh * (kr[i, slot, g] / torch.sqrt((qh * qh).mean()))
+    scales = (None, None)
+    if bits == 8:      # four and a half deviations of a value, and the peaked keys, fit the type's range
+        scales = tuple(amax / 448 * torch.linspace(0.8, 1.25, hkv, device=device) for amax in (0.6, 4.5))
+        k, v = ((x / s[:, None]).clamp(-448, 448) for x, s in zip((k, v), scales))
+    if outside == "nan":
+        k[~held.to(device)] = float("nan")
+        v[~held.to(device)] = float("nan")
+    kind = torch.float8_e4m3fn if bits == 8 else torch.bfloat16
+    shape = (count, hkv, page, d) if heads_first else (count, page, hkv, d)
+    pool = torch.empty((shape[0], 2, *shape[1:]), dtype=kind, device=device) if joint else None
+    stored = []
+    for i, x in enumerate((k, v)):
+        t = pool[:, i] if joint else torch.empty(shape, dtype=kind, device=device)
+        t = t.transpose(1, 2) if heads_first else t
+        t.copy_(x.to(kind))
+        stored.append(t)
+    return {"q": q16, "k": stored[0], "v": stored[1], "k_scale": scales[0], "v_scale": scales[1], "table": table.to(device),
+            "pos": torch.tensor([n - 1 for n in lengths], dtype=torch.int32, device=device), "win": win}
