@@ -46,7 +46,8 @@ int ensure_device() {
         return WA_EDEVICE;
     }
     if (wa::decode_prepare_device(dev) != cudaSuccess || wa::prompt_prepare_device(dev) != cudaSuccess ||
-        wa::prompt_sparse_prepare_device(dev) != cudaSuccess || wa::tree_prepare_device(dev) != cudaSuccess)
+        wa::prompt_sparse_prepare_device(dev) != cudaSuccess || wa::tree_prepare_device(dev) != cudaSuccess ||
+        wa::paged_prepare_device(dev) != cudaSuccess)
         return WA_ECUDA;
     g_ready[dev] = 1;
     return WA_OK;
@@ -112,7 +113,8 @@ bool pages_ok(const wa_pages* c, int32_t hq, int32_t win) {
 
 // Whether the decode's copies can name a page's keys by one index: pages apart by a whole number of 8 positions, or of heads.
 bool pages_in_steps(const wa_pages& c, int64_t page, int64_t slot, int64_t head) {
-    return c.pages == 1 || page % (8 * slot) == 0 || page % head == 0;
+    const int64_t step = page % (8 * slot) == 0 ? 8 * slot : head;
+    return c.pages == 1 || (page % step == 0 && (c.pages - 1) * (page / step) + c.hkv + c.page_size < INT32_MAX);
 }
 
 bool rotary_ok(const wa_rotary* r, int32_t d) {
@@ -478,7 +480,8 @@ int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int
 
 size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win) {
     if (!cache || !page_sizes_ok(*cache, hq, win)) return 0;
-    return wa::kHeaderBytes + flags_bytes(static_cast<int64_t>(cache->rows) * hq);
+    return wa::paged_plan(cache->rows, hq, cache->hkv, cache->d, log2_of(cache->page_size), cache->most,
+                          cache->type == WA_PAGE_E4M3, win).bytes;
 }
 
 int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_pages* cache, int32_t win, float scale,
@@ -494,14 +497,12 @@ int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_page
     if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return WA_EWORKSPACE;
     const int rc = ensure_device();
     if (rc != WA_OK) return rc;
-    uint8_t* base = static_cast<uint8_t*>(ws);
     wa::PagedArgs a{};
     a.q = q; a.pos = pos; a.out = out;
     a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, cache->k_head};
     a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, cache->v_head};
     a.table = cache->table; a.table_row = cache->table_row; a.q_row = q_row; a.o_row = out_row;
-    a.hdr = reinterpret_cast<wa::WsHeader*>(base);
-    a.flags = reinterpret_cast<int*>(base + wa::kHeaderBytes);
+    a.hdr = static_cast<wa::WsHeader*>(ws);
     a.rows = cache->rows; a.hq = hq; a.hkv = cache->hkv; a.d = cache->d;
     a.pages = cache->pages; a.page_log = log2_of(cache->page_size); a.most = cache->most;
     a.e4m3 = cache->type == WA_PAGE_E4M3;

@@ -133,10 +133,22 @@ struct PagedArgs {
     int64_t table_row, q_row, o_row;
     void* out;
     WsHeader* hdr;
-    int* flags;              // [rows * hq]
     int rows, hq, hkv, d, pages, page_log, most, e4m3, win;
     float scale;
 };
+
+// The workspace of a paged decode call in bytes from its start, and the most spans of a (row, key head).
+struct PagedPlan {
+    int spans;
+    size_t flags;    // int[4 * rows * hq]: (row, head) to compute again, at most once a warp
+    size_t counts;   // int[rows * hkv] spans that are done, then int[rows / kPagedRows + 1] units that are taken
+    size_t clear;    // ints from `counts` that a call clears
+    size_t ml;       // float2[rows * hkv * spans * G]
+    size_t part;     // float[rows * hkv * spans * G * d]
+    size_t bytes;
+};
+constexpr int kPagedRows = 512;      // rows a launch
+PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win);
 
 // Kept nodes' keys and values into the rings of several layers.
 struct CommitArgs {
@@ -207,6 +219,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t tree_prepare_device(int dev);
+cudaError_t paged_prepare_device(int dev);
 cudaError_t prompt_prepare_device(int dev);
 cudaError_t decode_prepare_device(int dev);
 // Decode partials on the tensor cores (query-head groups of kTcMinGroup and more); the merge is shared.

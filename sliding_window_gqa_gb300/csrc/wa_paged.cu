@@ -1,14 +1,86 @@
-// wa_paged.cu — decode over a cache in pages: one new token a sequence.
+// wa_paged.cu — decode over a cache in pages: one new token a sequence, on the tensor cores.
+//
+//   o = vs sum_j w_j v_j / sum_j w_j,  w_j = 2^(c q.k_j - m),  c = scale ks log2(e)
+//
+// over the row's visible keys, for the G query heads of a key head together, so K and V
+// are read once.
+//
+// Turned round.  With one token a row there are at most 16 query heads a key head, and a
+// product with the queries as the 128 rows of the tensor core would be 7/8 padding.  So the
+// keys are the rows: S^T = K Q^T (128 keys x 16) and O^T = V^T P^T (128 dims x the parts of P).
+// Both A operands are then the cache's own tiles as the copies leave them, both B operands
+// small; P's parts are columns of one product, so V is read from shared memory once for all
+// of them.  A key is a lane of tensor memory, so a mask is one bit a thread, and the maximum
+// of a head is only worked out where some score exceeds the running one (a vote of 128 threads).
+//
+// 8-bit pages.  e4m3 has 4 significant bits, so a query, of 8, is two e4m3 numbers: 2^k q = hi +
+// lo / 16 to 2^-22 of the head's largest value, and S comes from exact products as with bf16.
+// P is three: 256 p = p1 + p2 / 16 + p3 / 256 to 2^-12 of p (one part alone: 2^-4; two: 2^-8, about
+// what the output's own rounding loses), or to 2^-26 of the largest where that is more.
+//
+// Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's
+// keys), are cut into even spans, as many as fill the GPU once (kFill) with this row
+// alone, of at most kSpanTiles.  A unit of work is (row, key head, span); it leaves (m, l, O) in
+// fp32, and the CTA that finishes a (row, key head)'s last unit joins its spans, in order.
+// Nothing in a unit depends on the other rows, so neither do the bits.
+//
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 256 threads, that streams the keys
+// of its units without a break between units:
+//   warp 0      TMA producer: K and V tiles through a ring of slots, in the order the tensor core
+//               reads them (K0, K1, V0, K2, V1, ...), a copy a page (or piece of one)
+//   warp 1      allocates tensor memory, issues the products; before O += V^T P^T of a row's first
+//               and last tile it zeroes V's slots without a visible key, so that what they hold
+//               never meets a zero probability as 0 * inf
+//   warp 2      takes units by a counter, looks up their pages, publishes them
+//   warp 3      Q to shared memory, split in two for 8-bit pages
+//   warps 4..7  softmax, a key a thread: exponentials, P to shared memory, a lazy rescale of O, the
+//               unit's result, the join
+// Every wait is bounded (a status bit after kWaitLimitNs).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "wa_f64.cuh"
-#include "wa_internal.h"
+#include "wa_prompt_kernel.cuh"
 
 namespace wa {
 
 namespace {
+
+constexpr int kPTile = 128;          // keys a tile
+constexpr int kPThreads = 256;
+constexpr int kPUnits = 4;           // unit slots
+constexpr int kFill = 152;           // units that a row is cut into, over its key heads
+constexpr int kSpanTiles = 16;       // at most
+
+// How a row is cut.  `align`: keys of a copy.
+struct RowCut {
+    int lo, k0, tiles, spans;        // first visible key, first key of the first tile
+};
+__host__ __device__ inline int span_tiles(int64_t tiles, int hkv) {
+    const int64_t want = (tiles * hkv + kFill - 1) / kFill;
+    return want < kSpanTiles ? static_cast<int>(want) : kSpanTiles;
+}
+__device__ __forceinline__ RowCut row_cut(int p, int win, int align, int hkv) {
+    RowCut c;
+    c.lo = win > 0 ? max(0, p - win + 1) : 0;
+    c.k0 = c.lo & ~(align - 1);
+    c.tiles = p < 0 ? 0 : (p - c.k0) / kPTile + 1;
+    const int each = span_tiles(c.tiles, hkv);
+    c.spans = c.tiles == 0 ? 0 : (c.tiles + each - 1) / each;
+    return c;
+}
+
+// Keys of one copy: a page, of at most 32 KiB and one tile.
+__host__ __device__ inline int copy_keys(int d, int e4m3, int page_log) {
+    const int most = d == 256 && !e4m3 ? 64 : 128;
+    return page_log >= 7 || (1 << page_log) > most ? most : 1 << page_log;
+}
+
+// A row's last position as every kernel uses it.
+__device__ __forceinline__ int paged_pos(int raw, int most, int page_log) {
+    return raw < -1 ? -1 : (raw >> page_log) >= most ? (most << page_log) - 1 : raw;
+}
 
 __device__ __forceinline__ float e4m3_to_f32(uint8_t b) {
     const __half_raw h = __nv_cvt_fp8_to_halfraw(b, __NV_E4M3);
@@ -21,38 +93,851 @@ __device__ __forceinline__ float stored(const void* base, int64_t at, int e4m3) 
                 : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at]) << 16);
 }
 
-// A row's last position as every kernel uses it.
-__device__ __forceinline__ int paged_pos(int raw, int most, int page_log) {
-    return raw < -1 ? -1 : (raw >> page_log) >= most ? (most << page_log) - 1 : raw;
+// How a copy names the keys of a page: dimensions (128 bytes, 8 keys, blocks of 128 bytes, key groups, heads) where pages
+// are apart by a whole number of 8 positions (`by_slots`), and otherwise (.., key groups of a page, heads of all pages).
+struct PageCoord {
+    int ratio, none, by_slots;     // none: a key group that is past the end (read as zeros)
+};
+
+struct PagedParams {
+    CUtensorMap map[2];
+    PageCoord at[2];
+    PagedArgs a;
+    int* flags;
+    int* counts;                   // [rows * hkv]
+    int* next_unit;
+    float2* ml;
+    float* part;
+    int row0, rows;                // the launch's rows
+    int spans;                     // most spans of a (row, key head)
+    int align;                     // keys of a copy
+    float c;                       // |scale| log2(e) (bf16 pages)
+};
+
+template <int D_, bool F8_, int GP_>
+struct PagedCfg {
+    static constexpr int D = D_, GP = GP_;               // GP: query heads a key head, rounded up to 4, 8 or 16
+    static constexpr bool F8 = F8_;
+    static constexpr int ESZ = F8 ? 1 : 2;
+    static constexpr int KB = D * ESZ / 128;             // blocks of 128 bytes a key
+    static constexpr int SLOT = kPTile * D * ESZ;        // a tile of K or V: [16 groups of 8 keys][KB][8][128 bytes]
+    static constexpr int NSLOT = 196608 / SLOT;
+    static constexpr int QN = F8 && GP == 16 ? 32 : 16;  // columns of S: the heads (8-bit: hi of GP heads, lo of them)
+    static constexpr int Q_BYTES = QN * D * ESZ;         // [KB][QN / 8][8][128 bytes]
+    static constexpr int PARTS = F8 ? 3 : 2;
+    static constexpr int PN = (PARTS * GP + 15) / 16 * 16;
+    static constexpr int P_CHUNK = PN * 128;             // 128 bytes of keys: [PN / 8][8][128 bytes]
+    static constexpr int P_BYTES = ESZ * P_CHUNK;
+    static constexpr int NP = D == 256 && !F8 && GP == 16 ? 1 : 2;   // P buffers that fit
+    static constexpr int KSTEP = 32 / ESZ;               // keys or dims a product
+    static constexpr int MB = D / 128;
+    static constexpr int S_COL = 0, O_COL = 64;          // tensor memory: two buffers of S, O of MB blocks
+    static constexpr int TMEM_COLS = 256;
+    static_assert(O_COL + MB * PN <= TMEM_COLS, "tensor memory budget");
+    static constexpr int PAGES = kSpanTiles * kPTile / 16;   // copies of a unit at most
+    static constexpr int OFF_RING = 0;
+    static constexpr int OFF_Q = OFF_RING + NSLOT * SLOT;
+    static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+    static constexpr int OFF_UNIT = OFF_P + NP * P_BYTES;    // 8 ints a slot
+    static constexpr int OFF_PAGES = OFF_UNIT + kPUnits * 32;
+    static constexpr int OFF_PRE = OFF_PAGES + kPUnits * PAGES * 4;   // units of the rows before
+    static constexpr int OFF_X = OFF_PRE + (kPagedRows + 4) * 4;      // [4 warps][16] maxima, then sums
+    static constexpr int OFF_C = OFF_X + 256;                // [kPUnits][16] c of each head (8-bit)
+    static constexpr int OFF_BAR = OFF_C + kPUnits * 64;
+    static constexpr int B_FULL = 0;                         // [NSLOT]
+    static constexpr int B_FREE = B_FULL + NSLOT;
+    static constexpr int B_SFULL = B_FREE + NSLOT;           // [tile & 1] from here
+    static constexpr int B_PFULL = B_SFULL + 2;
+    static constexpr int B_PVDONE = B_PFULL + 2;
+    static constexpr int B_QFULL = B_PVDONE + 2;             // [unit & 1]
+    static constexpr int B_QFREE = B_QFULL + 2;
+    static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod kPUnits] from here
+    static constexpr int B_UFREE = B_UFULL + kPUnits;
+    static constexpr int B_UTOOK = B_UFREE + kPUnits;        // the producer has begun the unit
+    static constexpr int B_UC = B_UTOOK + kPUnits;           // the unit's c are there (8-bit)
+    static constexpr int B_DRAIN = B_UC + kPUnits;
+    static constexpr int NBAR = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base, flag words
+    static constexpr int SMEM = OFF_MISC + 32;
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(NBAR <= 128, "warps 4..7 set up the barriers");
+};
+
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }   // version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+
+// One tcgen05.mma, descriptors as two halves of which only the low one (the address) changes.
+template <bool F8, uint32_t A_HI, uint32_t B_HI, bool ACC>
+__device__ __forceinline__ void paged_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+            "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}"
+            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(A_HI), "n"(B_HI));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+            "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(A_HI), "n"(B_HI));
 }
 
-// The float64 value of one (row, head) a block: the maximum score, then weights and their sums in key order, 256 keys at
-// a time; a NaN or +inf score settles the output before that.
-__global__ void __launch_bounds__(kRerunThreads) paged_f64_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
-    __shared__ int64_t vat[kRerunThreads];
-    const int t = threadIdx.x, d = a.d, G = a.hq / a.hkv;
-    const int units = a.rows * a.hq;
-    for (int f = blockIdx.x; f < units; f += gridDim.x) {
-        const int row = f / a.hq, h = f % a.hq, g = h / G;
-        const int raw = a.pos[row], p = paged_pos(raw, a.most, a.page_log);
-        uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d;
-        if (raw != p && t == 0) atomicOr(&a.hdr->status, WA_STATUS_BAD_POS);
-        if (p < 0) {
-            if (t < d) orow[t] = 0;
-            continue;
+// Instruction descriptor: fp32 accumulator, bf16 or e4m3 operands, B K-major.
+constexpr uint32_t paged_idesc(bool f8, uint32_t n, uint32_t a_mn) {
+    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (a_mn << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ bool paged_elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// N consecutive columns of the thread's own lane.
+template <int N>
+__device__ __forceinline__ void tm_load(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(taddr));
+    else
+        tmem_ld32(taddr, r);
+}
+// The wait, with the registers passed through it, so that no use of them is scheduled before the data has arrived.
+template <int N>
+__device__ __forceinline__ void tm_wait(uint32_t (&r)[N]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
+}
+template <int N>
+__device__ __forceinline__ void tm_store(uint32_t taddr, const uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16, "columns");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                     :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else
+        tmem_st16(taddr, r);
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+    asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" :: "r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
+
+// The softmax warps' barrier, alone and as a vote.
+__device__ __forceinline__ void group_sync() { named_bar_sync(1, 128); }
+__device__ __forceinline__ bool group_any(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ int p_ordered(float x) {     // integers of the same order as fp32 values
+    const int b = __float_as_int(x);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float p_unordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+// Clears what a call counts and reports; the next kernel sets itself up meanwhile.
+__global__ void __launch_bounds__(1024) paged_clear_kernel(WsHeader* hdr, int* counts, int n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = blockIdx.x * 1024 + threadIdx.x;
+    if (t == 0) {
+        hdr->status = 0;
+        hdr->nflag = 0;
+    }
+    for (int i = t; i < n; i += gridDim.x * 1024) counts[i] = 0;
+}
+
+// A published unit.  nt = 0 marks the end.
+struct PUnit {
+    int row, g, span, spans, k0, nt, lo, p;
+};
+
+template <int D, bool F8, int GP>
+__global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_constant__ PagedParams p) {
+    using C = PagedCfg<D, F8, GP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    int* const status = &p.a.hdr->status;
+    if (sbase & 1023u) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (threadIdx.x == 0) atomicOr(status, WA_STATUS_LAYOUT);
+        return;
+    }
+    const uint32_t bar0 = sbase + C::OFF_BAR;
+    auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    auto SLOT = [&](int s) { return sbase + C::OFF_RING + static_cast<uint32_t>(s) * C::SLOT; };
+    int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int G = p.a.hq / p.a.hkv;
+
+    // ---- set-up: barriers, tensor memory, zeros of Q and P, the units of each row
+    if (tid >= 128 && tid < 128 + C::NBAR) {
+        const int i = tid - 128;
+        int count = 1;
+        if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // the softmax warps
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 7;                // producer, MMA, Q, softmax warps
+        mbar_init(BAR(i), count);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(smem + C::OFF_MISC), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    for (int e = tid; e < (2 * C::Q_BYTES + C::NP * C::P_BYTES) / 16; e += kPThreads)
+        st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    int mine[2], bad = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = 2 * tid + e;
+        mine[e] = 0;
+        if (r < p.rows) {
+            const int raw = p.a.pos[p.row0 + r], at = paged_pos(raw, p.a.most, p.a.page_log);
+            if (raw != at) bad = 1;
+            mine[e] = row_cut(at, p.a.win, p.align, p.a.hkv).spans;
         }
+    }
+    {
+        int sum = mine[0] + mine[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        int* tot = reinterpret_cast<int*>(smem + C::OFF_X);
+        if (lane == 31) tot[warp] = sum;
+        bad = __syncthreads_or(bad);
+        int before = sum - mine[0] - mine[1];
+        for (int w = 0; w < warp; ++w) before += tot[w];
+        pre[2 * tid + 1] = before + mine[0];
+        pre[2 * tid + 2] = before + mine[0] + mine[1];
+        if (tid == 0) pre[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = misc[0];
+    static_assert(kPagedRows == 2 * kPThreads, "rows a thread");
+
+    auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % kPUnits) * 32); };
+    auto unit_pages = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_PAGES + (U % kPUnits) * C::PAGES * 4); };
+    auto uph = [](int U) { return static_cast<uint32_t>(U / kPUnits) & 1u; };
+    auto read_unit = [&](int U, PUnit& x) {
+        volatile int* e = unit_ints(U);
+        x.row = e[0]; x.g = e[1]; x.span = e[2]; x.spans = e[3]; x.k0 = e[4]; x.nt = e[5]; x.lo = e[6]; x.p = e[7];
+    };
+    const int pieces = kPTile / p.align;          // copies a tile
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            prefetch_tensormap(&p.map[0]);
+            prefetch_tensormap(&p.map[1]);
+        }
+        const uint64_t pol = policy_evict_first();
+        int u = 0;                                // loads issued
+        const int in_page = (1 << p.a.page_log) - 1;
+        // a tile of K (side 0) or V: lane j copies its j-th piece
+        auto load = [&](int U, const PUnit& x, int idx, int side) -> bool {
+            const int s = u % C::NSLOT, use = u / C::NSLOT;
+            if (use > 0 && !warp_wait(BAR(C::B_FREE + s), (use - 1) & 1, status)) return false;
+            const uint32_t full = BAR(C::B_FULL + s);
+            int id = -2;
+            if (lane < pieces) id = unit_pages(U)[idx * pieces + lane];
+            const int wanted = __popc(__ballot_sync(0xFFFFFFFFu, id != -2));
+            if (lane == 0) mbar_arrive_expect_tx(full, wanted * p.align * D * C::ESZ);
+            __syncwarp();
+            if (id != -2) {
+                const PageCoord& at = p.at[side];
+                const int group = ((x.k0 + idx * kPTile + lane * p.align) & in_page) >> 3;
+                const int c3 = id < 0 ? at.none : at.by_slots ? id * at.ratio + group : group;
+                const int c4 = id < 0 || at.by_slots ? x.g : id * at.ratio + x.g;
+                tma_load_5d(SLOT(s) + lane * p.align * D * C::ESZ, &p.map[side], 0, 0, 0, c3, c4, full, pol);
+            }
+            __syncwarp();
+            ++u;
+            return true;
+        };
+        auto take = [&](int U, PUnit& x) -> bool {
+            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
+            read_unit(U, x);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UTOOK + U % kPUnits));
+            return true;
+        };
+        auto done = [&](int U) {                  // the unit's pages are read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+        };
+        PUnit cur, nxt;
+        int U = 0, idx = 0;
+        bool ok = take(0, cur), more = ok && cur.nt > 0;
+        if (more) ok = load(0, cur, 0, 0);
+        while (ok && more) {
+            const bool same = idx + 1 < cur.nt;
+            if (same) {
+                if (!(ok = load(U, cur, idx + 1, 0))) break;
+            } else {
+                if (!(ok = take(U + 1, nxt))) break;
+                more = nxt.nt > 0;
+                if (more && !(ok = load(U + 1, nxt, 0, 0))) break;
+            }
+            if (!(ok = load(U, cur, idx, 1))) break;
+            if (same) {
+                ++idx;
+            } else {
+                done(U++);
+                cur = nxt;
+                idx = 0;
+            }
+        }
+        // the copies in flight land before the block exits, whichever role stopped early
+        for (int i = max(0, u - C::NSLOT); i < u; ++i)
+            if (!mbar_wait(BAR(C::B_FULL + i % C::NSLOT), static_cast<uint32_t>(i / C::NSLOT) & 1u, status)) break;
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer: the warp together, one lane's instructions
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+        const bool leader = paged_elect();
+        constexpr uint32_t idS = paged_idesc(F8, C::QN, 0), idO = paged_idesc(F8, C::PN, 1);
+        constexpr uint32_t kTileHi = desc_hi(C::KB * 1024), kSmallHi = desc_hi(1024);
+        int s = 0, use = 0;                       // the next load's slot
+        auto next_slot = [&]() {
+            if (++s == C::NSLOT) {
+                s = 0;
+                ++use;
+            }
+        };
+        // S^T(t) = K Q^T
+        auto issue_s = [&](int t, int U, bool last) -> bool {
+            if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t d = tb + C::S_COL + (t & 1) * 32, k = desc_lo(SLOT(s), 16),
+                               q = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES, 16);
+#pragma unroll
+                for (int i = 0; i < D / C::KSTEP; ++i) {
+                    const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4), b = q + (((i / 4) * C::QN * 128 + (i % 4) * 32) >> 4);
+                    if (i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
+                    else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                }
+                mma_commit(BAR(C::B_FREE + s));
+                mma_commit(BAR(C::B_SFULL + (t & 1)));
+                if (last) mma_commit(BAR(C::B_QFREE + (U & 1)));
+            }
+            __syncwarp();
+            next_slot();
+            return true;
+        };
+        // O^T += V^T P^T of a tile whose keys `from` .. `to` - 1 are visible
+        auto issue_pv = [&](int t, bool first, int from, int to) -> bool {
+            if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
+            if (from > 0 || to < kPTile) {
+                const int nz = from + kPTile - to;
+                for (int e = lane; e < nz * C::KB * 8; e += 32) {
+                    const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
+                    st_shared_v4(SLOT(s) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (!warp_wait(BAR(C::B_PFULL + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, status)) return false;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t v = desc_lo(SLOT(s), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + (t % C::NP) * C::P_BYTES, 16);
+#pragma unroll
+                for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+                    for (int i = 0; i < kPTile / C::KSTEP; ++i) {
+                        const uint32_t d = tb + C::O_COL + mb * C::PN;
+                        const uint32_t a = v + ((mb * (C::KB / C::MB) * 1024 + i * (C::KSTEP / 8) * C::KB * 1024) >> 4);
+                        const uint32_t b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
+                        if (i == 0 && first) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
+                        else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
+                    }
+                mma_commit(BAR(C::B_FREE + s));
+                mma_commit(BAR(C::B_PVDONE + (t & 1)));
+            }
+            __syncwarp();
+            next_slot();
+            return true;
+        };
+        PUnit x;
+        auto take = [&](int U) -> bool {
+            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
+            read_unit(U, x);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+            x.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
+            return true;
+        };
+        int t = 0, from = 0, to = 0;              // of tile t - 1, whose P V is to come
+        bool ok = true, first = false;
+        for (int U = 0; ok; ++U) {
+            if (!(ok = take(U)) || x.nt <= 0) break;
+            if (!(ok = warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status))) break;
+            for (int idx = 0; ok && idx < x.nt; ++idx, ++t) {
+                ok = issue_s(t, U, idx == x.nt - 1);
+                if (ok && t > 0) ok = issue_pv(t - 1, first, from, to);
+                const int key0 = x.k0 + idx * kPTile;
+                from = max(0, x.lo - key0);
+                to = min(kPTile, x.p - key0 + 1);
+                first = idx == 0;
+            }
+        }
+        if (ok && t > 0) issue_pv(t - 1, first, from, to);
+        // every product issued has finished before tensor memory can be released
+        if (leader) {
+            mma_commit(BAR(C::B_DRAIN));
+            mbar_wait(BAR(C::B_DRAIN), 0, status);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ units
+        // nothing before this line reads what the clear kernel writes
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (bad && blockIdx.x == 0 && lane == 0) atomicOr(status, WA_STATUS_BAD_POS);
+        const int units = pre[p.rows] * p.a.hkv;
+        int k = static_cast<int>(blockIdx.x);
+        for (int U = 0;; ++U) {
+            int nt = 0;
+            // the slot's last unit has been read by everyone
+            if (U >= kPUnits && !warp_wait(BAR(C::B_UFREE + U % kPUnits), uph(U - kPUnits), status)) break;
+            if (k < units) {
+                const int s = k / p.a.hkv, g = k - s * p.a.hkv;
+                int a = 0, b = p.rows;            // pre[a] <= s < pre[b]
+                while (b - a > 1) {
+                    const int m = (a + b) >> 1;
+                    if (pre[m] <= s) a = m; else b = m;
+                }
+                const int row = p.row0 + a, last = paged_pos(p.a.pos[row], p.a.most, p.a.page_log);
+                const RowCut cut = row_cut(last, p.a.win, p.align, p.a.hkv);
+                const int span = s - pre[a], each = cut.tiles / cut.spans, more = cut.tiles - each * cut.spans;
+                nt = each + (span < more ? 1 : 0);
+                const int k0 = cut.k0 + (span * each + min(span, more)) * kPTile;
+                volatile int* ids = unit_pages(U);
+                for (int e = lane; e < nt * pieces; e += 32) {
+                    const int key = k0 + e * p.align;
+                    int id = -2;                  // without a visible key: nothing is copied
+                    if (key <= last && key + p.align > cut.lo) {
+                        id = p.a.table[row * p.a.table_row + (key >> p.a.page_log)];
+                        if (id < 0 || id >= p.a.pages) {
+                            id = -1;
+                            atomicOr(status, WA_STATUS_BAD_PAGE);
+                        }
+                    }
+                    ids[e] = id;
+                }
+                if (lane == 0) {
+                    volatile int* x = unit_ints(U);
+                    x[0] = row; x[1] = g; x[2] = span; x[3] = cut.spans; x[4] = k0; x[5] = nt; x[6] = cut.lo; x[7] = last;
+                }
+            } else if (lane == 0) {
+                unit_ints(U)[5] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UFULL + U % kPUnits));
+            if (nt == 0) break;
+            // A unit is taken no earlier than needed, so that the last ones go to whoever is free: when the producer has
+            // begun this one or, where units are short, the one before it.
+            const int begun = nt >= 3 ? U : U - 1;
+            if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % kPUnits), uph(begun), status)) break;
+            int nk = 0;
+            if (lane == 0) nk = atomicAdd(p.next_unit, 1);
+            k = __shfl_sync(0xFFFFFFFFu, nk, 0) + static_cast<int>(gridDim.x);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------ Q
+        constexpr int EL = D / 32;                // values a lane and head
+        PUnit x;
+        for (int U = 0;; ++U) {
+            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
+            read_unit(U, x);
+            if (x.nt <= 0) break;
+            const uint16_t* q = static_cast<const uint16_t*>(p.a.q) + x.row * p.a.q_row + static_cast<int64_t>(x.g) * G * D + lane * EL;
+            uint32_t raw[GP][EL / 2];
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+#pragma unroll
+                for (int e = 0; e < EL / 2; ++e) raw[h][e] = 0u;
+                if (h < G) {
+                    if constexpr (EL == 4) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(q + h * D);
+                        raw[h][0] = v.x; raw[h][1] = v.y;
+                    } else {
+                        const uint4 v = *reinterpret_cast<const uint4*>(q + h * D);
+                        raw[h][0] = v.x; raw[h][1] = v.y; raw[h][2] = v.z; raw[h][3] = v.w;
+                    }
+                }
+            }
+            float c = p.a.scale * 1.4426950408889634f;
+            if constexpr (F8) c *= p.a.kv[0].scale ? p.a.kv[0].scale[x.g] : 1.f;
+            const bool neg = c < 0.f;             // the sign goes into Q, exactly
+            // the buffer's last unit's S have been worked out
+            if (U >= 2 && !warp_wait(BAR(C::B_QFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
+            const uint32_t dst = sbase + C::OFF_Q + (U & 1) * C::Q_BYTES;
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                if (h >= G) break;
+                if constexpr (!F8) {
+                    // dims lane * EL ..: block of 64 dims, 16-byte chunk, swizzled by the row
+                    const int el = lane * EL, chunk = (el & 63) * 2;
+                    const uint32_t at = dst + (el >> 6) * (C::QN * 128) + (h >> 3) * 1024 + (h & 7) * 128 + (chunk ^ ((h & 7) << 4));
+                    const uint32_t flip = neg ? 0x80008000u : 0u;
+#pragma unroll
+                    for (int e = 0; e < EL / 2; ++e) st_shared_u32(at + 4 * e, raw[h][e] ^ flip);
+                } else {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < EL / 2; ++e) {
+                        top = max(top, (raw[h][e] << 16) & 0x7FFFFFFFu);
+                        top = max(top, raw[h][e] & 0x7FFF0000u);
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    // 2^k brings the largest value to [128, 256) (k at most 120: what is smaller than 2^-113 loses bits)
+                    const int k = min(134 - static_cast<int>(top >> 23), 120);
+                    const float f = __int_as_float((k + 127) << 23) * (neg ? -1.f : 1.f);
+                    const bool fine = top < 0x7F800000u;
+                    uint32_t hi[EL / 4], lo[EL / 4];
+#pragma unroll
+                    for (int w = 0; w < EL / 4; ++w) {
+                        float v[4], r[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            v[2 * e] = __uint_as_float(raw[h][2 * w + e] << 16) * f;
+                            v[2 * e + 1] = __uint_as_float(raw[h][2 * w + e] & 0xFFFF0000u) * f;
+                        }
+                        const uint32_t a = e4m3_pair(v[0], v[1]), b = e4m3_pair(v[2], v[3]);
+                        const float2 fa = e4m3_pair_f32(a), fb = e4m3_pair_f32(b);
+                        r[0] = (v[0] - fa.x) * 16.f; r[1] = (v[1] - fa.y) * 16.f;
+                        r[2] = (v[2] - fb.x) * 16.f; r[3] = (v[3] - fb.y) * 16.f;
+                        hi[w] = fine ? a | (b << 16) : 0x7F7F7F7Fu;          // NaN: the head is computed again
+                        lo[w] = e4m3_pair(r[0], r[1]) | (e4m3_pair(r[2], r[3]) << 16);
+                    }
+                    const int el = lane * EL, low = h + GP;
+                    const uint32_t block = dst + (el >> 7) * (C::QN * 128);
+                    const uint32_t ah = block + (h >> 3) * 1024 + (h & 7) * 128 + ((el & 127) ^ ((h & 7) << 4));
+                    const uint32_t al = block + (low >> 3) * 1024 + (low & 7) * 128 + ((el & 127) ^ ((low & 7) << 4));
+#pragma unroll
+                    for (int w = 0; w < EL / 4; ++w) {
+                        st_shared_u32(ah + 4 * w, hi[w]);
+                        st_shared_u32(al + 4 * w, fine ? lo[w] : 0u);
+                    }
+                    if (lane == 0)
+                        reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % kPUnits) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(BAR(C::B_QFULL + (U & 1)));
+                if constexpr (F8) mbar_arrive(BAR(C::B_UC + U % kPUnits));
+                mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------ softmax: key `quarter` * 32 + lane of a tile
+        const int quarter = warp & 3, gt = tid - 128;
+        const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        volatile int* xbuf = reinterpret_cast<volatile int*>(smem + C::OFF_X);
+        constexpr float kLazyP = F8 ? 0.75f : 32.0f;     // log2 units m may trail: P fits its type (8-bit: 2^8.75 is below 448)
+        constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
+        // rows without a key: zeros
+        for (int r = static_cast<int>(blockIdx.x); r < p.rows; r += gridDim.x) {
+            if (pre[r + 1] != pre[r]) continue;
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + (p.row0 + r) * p.a.o_row);
+            for (int e = gt; e < p.a.hq * (D / 8); e += 128) o[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
+        // next vote, at which the four warps leave together.
+        bool dead = false;
+        auto wait = [&](int bar, uint32_t ph) {
+            if (!dead && !warp_wait(BAR(bar), ph, status)) dead = true;
+        };
+        const uint32_t pk = quarter * 32 + lane;         // this thread's key: its column of P
+        int t = 0;
+        for (int U = 0;; ++U) {
+            PUnit x;
+            wait(C::B_UFULL + U % kPUnits, uph(U));
+            read_unit(U, x);
+            float c[GP];
+#pragma unroll
+            for (int h = 0; h < GP; ++h) c[h] = p.c;
+            if (F8 && !dead && x.nt > 0) {
+                wait(C::B_UC + U % kPUnits, uph(U));
+#pragma unroll
+                for (int h = 0; h < GP; ++h)
+                    c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % kPUnits) * 16 + h] : 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+            if (group_any(dead) || x.nt <= 0) break;
+            float m[GP], l[GP];
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                m[h] = -INFINITY;
+                l[h] = 0.f;
+            }
+            bool left = false;
+            for (int idx = 0; idx < x.nt; ++idx, ++t) {
+                wait(C::B_SFULL + (t & 1), static_cast<uint32_t>(t >> 1) & 1u);
+                tc_fence_after();
+                const int key = x.k0 + idx * kPTile + static_cast<int>(pk);
+                const bool vis = key >= x.lo && key <= x.p;
+                float s[GP];
+                if constexpr (F8) {
+                    uint32_t r[2 * GP];
+                    tm_load(tbase + lane_addr + C::S_COL + (t & 1) * 32, r);
+                    tm_wait(r);
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) s[h] = fmaf(__uint_as_float(r[GP + h]), 0.0625f, __uint_as_float(r[h]));
+                } else {
+                    uint32_t r[GP];
+                    tm_load(tbase + lane_addr + C::S_COL + (t & 1) * 32, r);
+                    tm_wait(r);
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) s[h] = __uint_as_float(r[h]);
+                }
+                bool over = dead;
+#pragma unroll
+                for (int h = 0; h < GP; ++h) over |= vis && fmaf(s[h], c[h], -m[h]) > kLazyP;
+                if (group_any(over)) {
+                    // some head's maximum moves: the maxima over the tile's visible keys
+                    int best = 0;
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) {
+                        const float y = vis ? fmaxf(s[h] * c[h], -INFINITY) : -INFINITY;     // NaN: no maximum
+                        const int b = __reduce_max_sync(0xFFFFFFFFu, p_ordered(y));
+                        if (lane == h) best = b;
+                    }
+                    if (lane < GP) xbuf[quarter * 16 + lane] = best;
+                    if (lane == 0) misc[2 + quarter] = dead ? 1u : 0u;
+                    group_sync();
+                    left = (misc[2] | misc[3] | misc[4] | misc[5]) != 0u;
+                    if (left) break;
+                    float alpha[GP];
+                    bool moved = false;
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) {
+                        const float top = p_unordered(max(max(xbuf[h], xbuf[16 + h]), max(xbuf[32 + h], xbuf[48 + h])));
+                        const float now = top - m[h] > kLazyP ? top : m[h];
+                        alpha[h] = now == m[h] ? 1.f : ex2(m[h] - now);
+                        moved |= now != m[h];
+                        l[h] *= alpha[h];
+                        m[h] = now;
+                    }
+                    if (idx > 0 && moved) {       // a unit's first product starts O afresh
+                        wait(C::B_PVDONE + ((t - 1) & 1), static_cast<uint32_t>((t - 1) >> 1) & 1u);
+                        tc_fence_after();
+#pragma unroll
+                        for (int part = 0; part < C::MB * C::PARTS; ++part) {
+                            uint32_t o[GP];
+                            const uint32_t ta = tbase + lane_addr + C::O_COL + part / C::PARTS * C::PN + part % C::PARTS * GP;
+                            tm_load(ta, o);
+                            tm_wait(o);
+#pragma unroll
+                            for (int h = 0; h < GP; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+                            tm_store(ta, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    s[h] = vis ? ex2(fmaf(s[h], c[h], kShift - m[h])) : 0.f;
+                    l[h] += s[h];
+                }
+                // the buffer's last product is done
+                if (t >= C::NP) wait(C::B_PVDONE + ((t - C::NP) & 1), static_cast<uint32_t>((t - C::NP) >> 1) & 1u);
+                const uint32_t pb = sbase + C::OFF_P + (t % C::NP) * C::P_BYTES;
+                // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row
+                if constexpr (F8) {
+                    auto at = [&](int n) { return pb + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4)); };
+#pragma unroll
+                    for (int h = 0; h < GP; h += 2) {
+                        float a = s[h], b = s[h + 1];
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            const uint32_t e = e4m3_pair(a, b);
+                            st_shared_u8(at(part * GP + h), e);
+                            st_shared_u8(at(part * GP + h + 1), e >> 8);
+                            if (part < 2) {
+                                const float2 f = e4m3_pair_f32(e);
+                                a = (a - f.x) * 16.f;
+                                b = (b - f.y) * 16.f;
+                            }
+                        }
+                    }
+                } else {
+                    auto at = [&](int n) { return pb + (pk >> 6) * C::P_CHUNK + (n >> 3) * 1024 + (n & 7) * 128 + (((pk & 63) * 2) ^ ((n & 7) << 4)); };
+#pragma unroll
+                    for (int h = 0; h < GP; h += 2) {
+                        const uint32_t hi = pack_bf16(s[h], s[h + 1]);
+                        const uint32_t lo = pack_bf16(s[h] - __uint_as_float(hi << 16), s[h + 1] - __uint_as_float(hi & 0xFFFF0000u));
+                        st_shared_u16(at(h), hi);
+                        st_shared_u16(at(h + 1), hi >> 16);
+                        st_shared_u16(at(GP + h), lo);
+                        st_shared_u16(at(GP + h + 1), lo >> 16);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(C::B_PFULL + (t & 1)));
+            }
+            if (left) break;
+            // ---- the unit's result: l over the 128 keys of a tile in a fixed order, O from tensor memory
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
+            }
+            group_sync();                         // the maxima in this buffer have been read
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < GP; ++h) xbuf[quarter * 16 + h] = __float_as_int(l[h]);
+            }
+            group_sync();
+#pragma unroll
+            for (int h = 0; h < GP; ++h)
+                l[h] = (__int_as_float(xbuf[h]) + __int_as_float(xbuf[16 + h])) + (__int_as_float(xbuf[32 + h]) + __int_as_float(xbuf[48 + h]));
+            wait(C::B_PVDONE + ((t - 1) & 1), static_cast<uint32_t>((t - 1) >> 1) & 1u);
+            tc_fence_after();
+            const int64_t rg = static_cast<int64_t>(x.row) * p.a.hkv + x.g, unit = rg * p.spans + x.span;
+            const float vs = F8 && p.a.kv[1].scale ? p.a.kv[1].scale[x.g] : 1.f;
+            auto write_out = [&](int h, int dim, float val) {     // and whether it has to be computed again
+                static_cast<uint16_t*>(p.a.out)[x.row * p.a.o_row + static_cast<int64_t>(x.g * G + h) * D + dim] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(val));
+            };
+            uint32_t again = 0;                   // heads with a value that is not finite
+#pragma unroll
+            for (int mb = 0; mb < C::MB; ++mb) {
+                float o[GP];
+#pragma unroll
+                for (int part = C::PARTS - 1; part >= 0; --part) {
+                    uint32_t r[GP];
+                    tm_load(tbase + lane_addr + C::O_COL + mb * C::PN + part * GP, r);
+                    tm_wait(r);
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) {
+                        if (part == C::PARTS - 1) o[h] = __uint_as_float(r[h]);
+                        else o[h] = fmaf(o[h], F8 ? 0.0625f : 1.f, __uint_as_float(r[h]));
+                    }
+                }
+                const int dim = mb * 128 + quarter * 32 + lane;
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    if (h >= G) break;
+                    if (x.spans == 1) {
+                        const float val = o[h] / l[h] * vs;
+                        if (!isfinite(val)) again |= 1u << h;
+                        write_out(h, dim, val);
+                    } else {
+                        p.part[(unit * G + h) * D + dim] = o[h];
+                    }
+                }
+            }
+            if (x.spans > 1) {
+                if (gt == 0) {
+#pragma unroll
+                    for (int h = 0; h < GP; ++h)
+                        if (h < G) p.ml[unit * G + h] = make_float2(m[h] - kShift, l[h]);
+                }
+                // the last of a (row, key head)'s units joins them: o = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M)
+                __threadfence();
+                group_sync();
+                if (gt == 0) misc[1] = atomicAdd(p.counts + rg, 1) == x.spans - 1 ? 1u : 0u;
+                group_sync();
+                if (misc[1]) {
+                    __threadfence();
+                    const float2* ml = p.ml + rg * p.spans * G;
+                    const float* po = p.part + rg * p.spans * G * D;
+                    for (int h = 0; h < G; ++h) {
+                        float M = -INFINITY, den = 0.f, num[C::MB];
+                        for (int s = 0; s < x.spans; ++s) M = fmaxf(M, __ldcg(&ml[s * G + h].x));
+#pragma unroll
+                        for (int mb = 0; mb < C::MB; ++mb) num[mb] = 0.f;
+                        for (int s = 0; s < x.spans; ++s) {
+                            const float2 e = __ldcg(ml + s * G + h);
+                            const float w = exp2f(e.x - M);
+                            den = fmaf(w, e.y, den);
+#pragma unroll
+                            for (int mb = 0; mb < C::MB; ++mb)
+                                num[mb] = fmaf(w, __ldcg(po + (static_cast<int64_t>(s) * G + h) * D + mb * 128 + gt), num[mb]);
+                        }
+#pragma unroll
+                        for (int mb = 0; mb < C::MB; ++mb) {
+                            const float val = num[mb] / den * vs;
+                            if (!isfinite(val)) again |= 1u << h;
+                            write_out(h, mb * 128 + gt, val);
+                        }
+                    }
+                }
+            }
+            again = __reduce_or_sync(0xFFFFFFFFu, again);
+            if (lane == 0)
+                for (; again != 0u; again &= again - 1)
+                    p.flags[atomicAdd(&p.a.hdr->nflag, 1)] = x.row * p.a.hq + x.g * G + __ffs(again) - 1;
+        }
+    }
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, C::TMEM_COLS);
+}
+
+// The float64 value of each listed (row, head): the maximum score, then weights and their sums in key order, 256 keys at
+// a time; a NaN or +inf score settles the output before that.
+__global__ void __launch_bounds__(kRerunThreads) paged_f64_kernel(const __grid_constant__ PagedArgs a, const int* flags) {
+    __shared__ double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
+    __shared__ float qf[256];
+    __shared__ int64_t vat[kRerunThreads];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int t = threadIdx.x, d = a.d, G = a.hq / a.hkv;
+    const int count = *reinterpret_cast<volatile int*>(&a.hdr->nflag);
+    for (int f = blockIdx.x; f < count; f += gridDim.x) {
+        const int item = *reinterpret_cast<const volatile int*>(flags + f), row = item / a.hq, h = item % a.hq, g = h / G;
+        const int p = paged_pos(a.pos[row], a.most, a.page_log);
+        uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d;
         const int lo = a.win > 0 ? max(0, p - a.win + 1) : 0;
-        if (t < d) qd[t] = bf16_bits_to_f64(static_cast<const uint16_t*>(a.q)[row * a.q_row + static_cast<int64_t>(h) * d + t]);
-        __syncthreads();
         const double scale = static_cast<double>(a.scale) * (a.kv[0].scale ? static_cast<double>(a.kv[0].scale[g]) : 1.0);
+        if (t < d) {
+            qd[t] = bf16_bits_to_f64(static_cast<const uint16_t*>(a.q)[row * a.q_row + static_cast<int64_t>(h) * d + t]);
+            qf[t] = static_cast<float>(qd[t]) * static_cast<float>(scale);     // only the score's class matters
+        }
+        __syncthreads();
         // where key j's head starts in k or v; -1 in a page that is none
         auto at = [&](const PageSide& side, int j) -> int64_t {
             const int page = a.table[row * a.table_row + (j >> a.page_log)];
-            if (page < 0 || page >= a.pages) {
-                atomicOr(&a.hdr->status, WA_STATUS_BAD_PAGE);
-                return -1;
-            }
+            if (page < 0 || page >= a.pages) return -1;
             return page * side.page + (j & ((1 << a.page_log) - 1)) * side.slot + g * side.head;
         };
         auto score = [&](int j) {
@@ -61,6 +946,27 @@ __global__ void __launch_bounds__(kRerunThreads) paged_f64_kernel(const __grid_c
             for (int e = 0; e < d; ++e) s = s + qd[e] * (k < 0 ? 0.0 : static_cast<double>(stored(a.kv[0].base, k + e, a.e4m3)));
             return s * scale;
         };
+        // a float64 score that is NaN or +inf makes the output NaN; an fp32 one that is finite is neither
+        bool settled = false;
+        for (int base = lo; base <= p && !settled; base += kRerunThreads) {
+            const int j = base + t;
+            bool hit = false;
+            if (j <= p) {
+                const int64_t k = at(a.kv[0], j);
+                float s = 0.f;
+                for (int e = 0; e < d; ++e) s = fmaf(qf[e], k < 0 ? 0.f : stored(a.kv[0].base, k + e, a.e4m3), s);
+                if (!isfinite(s)) {
+                    const double s64 = score(j);
+                    hit = isnan(s64) || (isinf(s64) && s64 > 0.0);
+                }
+            }
+            settled = __syncthreads_or(hit) != 0;
+        }
+        if (settled) {
+            if (t < d) orow[t] = 0x7FC0u;
+            __syncthreads();
+            continue;
+        }
         double mloc = -INFINITY;
         for (int j = lo + t; j <= p; j += kRerunThreads) {
             const double s = score(j);
@@ -91,17 +997,119 @@ __global__ void __launch_bounds__(kRerunThreads) paged_f64_kernel(const __grid_c
     }
 }
 
+bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int esz = a.e4m3 ? 1 : 2, page = 1 << a.page_log;
+    const int64_t one = a.pages == 1 ? 1 : 0;          // a lone page's stride means nothing
+    at->by_slots = one || side.page % (8 * side.slot) == 0;
+    at->ratio = static_cast<int>(one ? 0 : at->by_slots ? side.page / (8 * side.slot) : side.page / side.head);
+    const int64_t reach = static_cast<int64_t>(a.pages - 1) * at->ratio;
+    const int64_t groups = page / 8 + (at->by_slots ? reach : 0), heads = a.hkv + (at->by_slots ? 0 : reach);
+    at->none = static_cast<int>(groups);
+    cuuint64_t dims[5] = {static_cast<cuuint64_t>(128 / esz), 8, static_cast<cuuint64_t>(a.d * esz / 128),
+                          static_cast<cuuint64_t>(groups), static_cast<cuuint64_t>(heads)};
+    cuuint64_t strides[4] = {static_cast<cuuint64_t>(side.slot * esz), 128, static_cast<cuuint64_t>(8 * side.slot * esz),
+                             static_cast<cuuint64_t>(side.head * esz)};
+    cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / esz), 8, static_cast<cuuint32_t>(a.d * esz / 128),
+                         static_cast<cuuint32_t>(align / 8), 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, side.base, dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               a.d * esz >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class F>
+cudaError_t for_each_paged(F&& f) {
+    cudaError_t e;
+#define WA_PAGED(D, F8, GP) \
+    if ((e = f(paged_kernel<D, F8, GP>, D, F8, GP, PagedCfg<D, F8, GP>::SMEM)) != cudaSuccess) return e
+    WA_PAGED(128, false, 4); WA_PAGED(128, false, 8); WA_PAGED(128, false, 16);
+    WA_PAGED(256, false, 4); WA_PAGED(256, false, 8); WA_PAGED(256, false, 16);
+    WA_PAGED(128, true, 4); WA_PAGED(128, true, 8); WA_PAGED(128, true, 16);
+    WA_PAGED(256, true, 4); WA_PAGED(256, true, 8); WA_PAGED(256, true, 16);
+#undef WA_PAGED
+    return cudaSuccess;
+}
+
 }  // namespace
 
+PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win) {
+    PagedPlan pl{};
+    const int align = copy_keys(d, e4m3, page_log);
+    const int64_t keys = static_cast<int64_t>(most) << page_log;
+    int64_t tiles = (keys + kPTile - 1) / kPTile;
+    if (win > 0 && (win + align - 2) / kPTile + 1 < tiles) tiles = (static_cast<int64_t>(win) + align - 2) / kPTile + 1;
+    // spans(t) = ceil(t / ceil(t hkv / kFill)) is at most kFill / hkv (rounded up) where that bounds a span, and t / kSpanTiles beyond
+    const int64_t fill = (kFill + hkv - 1) / hkv, least = fill < tiles ? fill : tiles, most_spans = (tiles + kSpanTiles - 1) / kSpanTiles;
+    pl.spans = static_cast<int>(least > most_spans ? least : most_spans);
+    const int64_t pairs = static_cast<int64_t>(rows) * hkv, heads = static_cast<int64_t>(rows) * hq;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    pl.flags = kHeaderBytes;
+    pl.counts = pl.flags + up(4 * heads * sizeof(int));
+    pl.clear = pairs + rows / kPagedRows + 1;
+    pl.ml = pl.counts + up(pl.clear * sizeof(int));
+    pl.part = pl.ml + up(heads * pl.spans * sizeof(float2));
+    pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
+    return pl;
+}
+
+cudaError_t paged_prepare_device(int) {
+    return for_each_paged([](auto kernel, int, bool, int, int smem) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+}
+
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaMemsetAsync(a.hdr, 0, kHeaderBytes, s);
-    if (e != cudaSuccess) return e;
+    const PagedPlan pl = paged_plan(a.rows, a.hq, a.hkv, a.d, a.page_log, a.most, a.e4m3, a.win);
+    const int G = a.hq / a.hkv, gp = G <= 4 ? 4 : G <= 8 ? 8 : 16;
+    PagedParams p{};
+    p.a = a;
+    p.align = copy_keys(a.d, a.e4m3, a.page_log);
+    for (int i = 0; i < 2; ++i)
+        if (!encode_pages(&p.map[i], &p.at[i], a.kv[i], a, p.align)) return cudaErrorInvalidValue;
+    uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
+    p.flags = reinterpret_cast<int*>(base + pl.flags);
+    p.counts = reinterpret_cast<int*>(base + pl.counts);
+    p.ml = reinterpret_cast<float2*>(base + pl.ml);
+    p.part = reinterpret_cast<float*>(base + pl.part);
+    p.spans = pl.spans;
+    p.c = fabsf(a.scale) * 1.4426950408889634f;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    const int64_t units = static_cast<int64_t>(a.rows) * a.hq;
-    paged_f64_kernel<<<static_cast<int>(units < 4LL * sms ? units : 4LL * sms), kRerunThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const int clear = static_cast<int>(pl.clear);
+    paged_clear_kernel<<<clear <= 4096 ? 1 : 16, 1024, 0, s>>>(a.hdr, p.counts, clear);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // each kernel is launched while the one before runs, sets itself up and waits for it on the GPU
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    for (int r0 = 0; r0 < a.rows; r0 += kPagedRows) {
+        p.row0 = r0;
+        p.rows = a.rows - r0 < kPagedRows ? a.rows - r0 : kPagedRows;
+        p.next_unit = p.counts + static_cast<int64_t>(a.rows) * a.hkv + r0 / kPagedRows;
+        const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
+        cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+        cfg.blockDim = dim3(kPThreads);
+        e = for_each_paged([&](auto kernel, int d, bool f8, int g, int smem) {
+            if (d != a.d || f8 != (a.e4m3 != 0) || g != gp) return cudaSuccess;
+            cfg.dynamicSmemBytes = smem;
+            return cudaLaunchKernelEx(&cfg, kernel, p);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.rows) * a.hq < 4LL * sms ? a.rows * a.hq : 4 * sms));
+    cfg.blockDim = dim3(kRerunThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, paged_f64_kernel, a, const_cast<const int*>(p.flags));
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace wa
