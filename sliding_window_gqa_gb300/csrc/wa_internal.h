@@ -140,9 +140,7 @@ struct PagedArgs {
 // The workspace of a paged decode call in bytes from its start, and the most spans of a (row, key head).
 struct PagedPlan {
     int spans;
-    size_t flags;    // int[4 * rows * hq]: (row, head) to compute again, at most once a warp
-    size_t counts;   // int[rows * hkv] spans that are done, then int[rows / kPagedRows + 1] units that are taken
-    size_t clear;    // ints from `counts` that a call clears
+    size_t taken;    // int[launches] units that are taken
     size_t ml;       // float2[rows * hkv * spans * G]
     size_t part;     // float[rows * hkv * spans * G * d]
     size_t bytes;

@@ -21,7 +21,8 @@
 // Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's
 // keys), are cut into even spans, as many as fill the GPU once (kFill) with this row
 // alone, of at most kSpanTiles.  A unit of work is (row, key head, span); it leaves (m, l, O) in
-// fp32, and the CTA that finishes a (row, key head)'s last unit joins its spans, in order.
+// fp32, and paged_merge_kernel joins a row's spans.  (Joined by the CTA that finished a row's last
+// unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
 //
 // paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 256 threads, that streams the keys
@@ -34,7 +35,7 @@
 //   warp 2      takes units by a counter, looks up their pages, publishes them
 //   warp 3      Q to shared memory, split in two for 8-bit pages
 //   warps 4..7  softmax, a key a thread: exponentials, P to shared memory, a lazy rescale of O, the
-//               unit's result, the join
+//               unit's result
 // Every wait is bounded (a status bit after kWaitLimitNs).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -103,8 +104,6 @@ struct PagedParams {
     CUtensorMap map[2];
     PageCoord at[2];
     PagedArgs a;
-    int* flags;
-    int* counts;                   // [rows * hkv]
     int* next_unit;
     float2* ml;
     float* part;
@@ -262,15 +261,12 @@ __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
 }
 
 // Clears what a call counts and reports; the next kernel sets itself up meanwhile.
-__global__ void __launch_bounds__(1024) paged_clear_kernel(WsHeader* hdr, int* counts, int n) {
+__global__ void __launch_bounds__(128) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int t = blockIdx.x * 1024 + threadIdx.x;
-    if (t == 0) {
-        hdr->status = 0;
-        hdr->nflag = 0;
-    }
-    for (int i = t; i < n; i += gridDim.x * 1024) counts[i] = 0;
+    if (threadIdx.x == 0) hdr->status = 0;
+    if (static_cast<int>(threadIdx.x) < n) taken[threadIdx.x] = 0;
 }
+static_assert(65535 / kPagedRows < 128, "a counter a thread");
 
 // A published unit.  nt = 0 marks the end.
 struct PUnit {
@@ -343,6 +339,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = misc[0];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the join waits for this kernel's end by itself
     static_assert(kPagedRows == 2 * kPThreads, "rows a thread");
 
     auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % kPUnits) * 32); };
@@ -668,12 +665,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         volatile int* xbuf = reinterpret_cast<volatile int*>(smem + C::OFF_X);
         constexpr float kLazyP = F8 ? 0.75f : 32.0f;     // log2 units m may trail: P fits its type (8-bit: 2^8.75 is below 448)
         constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
-        // rows without a key: zeros
-        for (int r = static_cast<int>(blockIdx.x); r < p.rows; r += gridDim.x) {
-            if (pre[r + 1] != pre[r]) continue;
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + (p.row0 + r) * p.a.o_row);
-            for (int e = gt; e < p.a.hq * (D / 8); e += 128) o[e] = make_uint4(0u, 0u, 0u, 0u);
-        }
         // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
         // next vote, at which the four warps leave together.
         bool dead = false;
@@ -829,13 +820,17 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 l[h] = (__int_as_float(xbuf[h]) + __int_as_float(xbuf[16 + h])) + (__int_as_float(xbuf[32 + h]) + __int_as_float(xbuf[48 + h]));
             wait(C::B_PVDONE + ((t - 1) & 1), static_cast<uint32_t>((t - 1) >> 1) & 1u);
             tc_fence_after();
-            const int64_t rg = static_cast<int64_t>(x.row) * p.a.hkv + x.g, unit = rg * p.spans + x.span;
-            const float vs = F8 && p.a.kv[1].scale ? p.a.kv[1].scale[x.g] : 1.f;
-            auto write_out = [&](int h, int dim, float val) {     // and whether it has to be computed again
-                static_cast<uint16_t*>(p.a.out)[x.row * p.a.o_row + static_cast<int64_t>(x.g * G + h) * D + dim] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(val));
-            };
-            uint32_t again = 0;                   // heads with a value that is not finite
+            const int64_t unit = (static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span;
+            if (gt < GP) {
+                float mine = 0.f, sum = 0.f;
+#pragma unroll
+                for (int h = 0; h < GP; ++h)
+                    if (gt == h) {
+                        mine = m[h];
+                        sum = l[h];
+                    }
+                if (gt < G) p.ml[unit * G + gt] = make_float2(mine - kShift, sum);
+            }
 #pragma unroll
             for (int mb = 0; mb < C::MB; ++mb) {
                 float o[GP];
@@ -854,147 +849,164 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
                     if (h >= G) break;
-                    if (x.spans == 1) {
-                        const float val = o[h] / l[h] * vs;
-                        if (!isfinite(val)) again |= 1u << h;
-                        write_out(h, dim, val);
-                    } else {
-                        p.part[(unit * G + h) * D + dim] = o[h];
-                    }
+                    p.part[(unit * G + h) * D + dim] = o[h];
                 }
             }
-            if (x.spans > 1) {
-                if (gt == 0) {
-#pragma unroll
-                    for (int h = 0; h < GP; ++h)
-                        if (h < G) p.ml[unit * G + h] = make_float2(m[h] - kShift, l[h]);
-                }
-                // the last of a (row, key head)'s units joins them: o = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M)
-                __threadfence();
-                group_sync();
-                if (gt == 0) misc[1] = atomicAdd(p.counts + rg, 1) == x.spans - 1 ? 1u : 0u;
-                group_sync();
-                if (misc[1]) {
-                    __threadfence();
-                    const float2* ml = p.ml + rg * p.spans * G;
-                    const float* po = p.part + rg * p.spans * G * D;
-                    for (int h = 0; h < G; ++h) {
-                        float M = -INFINITY, den = 0.f, num[C::MB];
-                        for (int s = 0; s < x.spans; ++s) M = fmaxf(M, __ldcg(&ml[s * G + h].x));
-#pragma unroll
-                        for (int mb = 0; mb < C::MB; ++mb) num[mb] = 0.f;
-                        for (int s = 0; s < x.spans; ++s) {
-                            const float2 e = __ldcg(ml + s * G + h);
-                            const float w = exp2f(e.x - M);
-                            den = fmaf(w, e.y, den);
-#pragma unroll
-                            for (int mb = 0; mb < C::MB; ++mb)
-                                num[mb] = fmaf(w, __ldcg(po + (static_cast<int64_t>(s) * G + h) * D + mb * 128 + gt), num[mb]);
-                        }
-#pragma unroll
-                        for (int mb = 0; mb < C::MB; ++mb) {
-                            const float val = num[mb] / den * vs;
-                            if (!isfinite(val)) again |= 1u << h;
-                            write_out(h, mb * 128 + gt, val);
-                        }
-                    }
-                }
-            }
-            again = __reduce_or_sync(0xFFFFFFFFu, again);
-            if (lane == 0)
-                for (; again != 0u; again &= again - 1)
-                    p.flags[atomicAdd(&p.a.hdr->nflag, 1)] = x.row * p.a.hq + x.g * G + __ffs(again) - 1;
         }
     }
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
-// The float64 value of each listed (row, head): the maximum score, then weights and their sums in key order, 256 keys at
-// a time; a NaN or +inf score settles the output before that.
-__global__ void __launch_bounds__(kRerunThreads) paged_f64_kernel(const __grid_constant__ PagedArgs a, const int* flags) {
-    __shared__ double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
-    __shared__ float qf[256];
-    __shared__ int64_t vat[kRerunThreads];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = threadIdx.x, d = a.d, G = a.hq / a.hkv;
-    const int count = *reinterpret_cast<volatile int*>(&a.hdr->nflag);
-    for (int f = blockIdx.x; f < count; f += gridDim.x) {
-        const int item = *reinterpret_cast<const volatile int*>(flags + f), row = item / a.hq, h = item % a.hq, g = h / G;
-        const int p = paged_pos(a.pos[row], a.most, a.page_log);
-        uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d;
-        const int lo = a.win > 0 ? max(0, p - a.win + 1) : 0;
-        const double scale = static_cast<double>(a.scale) * (a.kv[0].scale ? static_cast<double>(a.kv[0].scale[g]) : 1.0);
-        if (t < d) {
-            qd[t] = bf16_bits_to_f64(static_cast<const uint16_t*>(a.q)[row * a.q_row + static_cast<int64_t>(h) * d + t]);
-            qf[t] = static_cast<float>(qd[t]) * static_cast<float>(scale);     // only the score's class matters
-        }
-        __syncthreads();
-        // where key j's head starts in k or v; -1 in a page that is none
-        auto at = [&](const PageSide& side, int j) -> int64_t {
-            const int page = a.table[row * a.table_row + (j >> a.page_log)];
-            if (page < 0 || page >= a.pages) return -1;
-            return page * side.page + (j & ((1 << a.page_log) - 1)) * side.slot + g * side.head;
-        };
-        auto score = [&](int j) {
+// The float64 value of a (row, head), by the whole block: the maximum score, then weights and their sums in key order,
+// 256 keys at a time; a NaN or +inf score settles the output before that.
+struct PagedRerun {
+    double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
+    float qf[256];
+    int64_t vat[kRerunThreads];
+};
+
+__device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int row, int h) {
+    const int t = threadIdx.x, d = a.d, g = h / (a.hq / a.hkv);
+    const int p = paged_pos(a.pos[row], a.most, a.page_log), lo = a.win > 0 ? max(0, p - a.win + 1) : 0;
+    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d;
+    const double scale = static_cast<double>(a.scale) * (a.kv[0].scale ? static_cast<double>(a.kv[0].scale[g]) : 1.0);
+    if (t < d) {
+        sm.qd[t] = bf16_bits_to_f64(static_cast<const uint16_t*>(a.q)[row * a.q_row + static_cast<int64_t>(h) * d + t]);
+        sm.qf[t] = static_cast<float>(sm.qd[t]) * static_cast<float>(scale);     // only the score's class matters
+    }
+    __syncthreads();
+    // where key j's head starts in k or v; -1 in a page that is none
+    auto at = [&](const PageSide& side, int j) -> int64_t {
+        const int page = a.table[row * a.table_row + (j >> a.page_log)];
+        if (page < 0 || page >= a.pages) return -1;
+        return page * side.page + (j & ((1 << a.page_log) - 1)) * side.slot + g * side.head;
+    };
+    auto score = [&](int j) {
+        const int64_t k = at(a.kv[0], j);
+        double s = 0.0;
+        for (int e = 0; e < d; ++e) s = s + sm.qd[e] * (k < 0 ? 0.0 : static_cast<double>(stored(a.kv[0].base, k + e, a.e4m3)));
+        return s * scale;
+    };
+    // a float64 score that is NaN or +inf makes the output NaN; an fp32 one that is finite is neither
+    for (int base = lo; base <= p; base += kRerunThreads) {
+        const int j = base + t;
+        bool hit = false;
+        if (j <= p) {
             const int64_t k = at(a.kv[0], j);
-            double s = 0.0;
-            for (int e = 0; e < d; ++e) s = s + qd[e] * (k < 0 ? 0.0 : static_cast<double>(stored(a.kv[0].base, k + e, a.e4m3)));
-            return s * scale;
-        };
-        // a float64 score that is NaN or +inf makes the output NaN; an fp32 one that is finite is neither
-        bool settled = false;
-        for (int base = lo; base <= p && !settled; base += kRerunThreads) {
-            const int j = base + t;
-            bool hit = false;
-            if (j <= p) {
-                const int64_t k = at(a.kv[0], j);
-                float s = 0.f;
-                for (int e = 0; e < d; ++e) s = fmaf(qf[e], k < 0 ? 0.f : stored(a.kv[0].base, k + e, a.e4m3), s);
-                if (!isfinite(s)) {
-                    const double s64 = score(j);
-                    hit = isnan(s64) || (isinf(s64) && s64 > 0.0);
-                }
+            float s = 0.f;
+            for (int e = 0; e < d; ++e) s = fmaf(sm.qf[e], k < 0 ? 0.f : stored(a.kv[0].base, k + e, a.e4m3), s);
+            if (!isfinite(s)) {
+                const double s64 = score(j);
+                hit = isnan(s64) || (isinf(s64) && s64 > 0.0);
             }
-            settled = __syncthreads_or(hit) != 0;
         }
-        if (settled) {
+        if (__syncthreads_or(hit)) {
             if (t < d) orow[t] = 0x7FC0u;
-            __syncthreads();
-            continue;
+            return;
         }
-        double mloc = -INFINITY;
-        for (int j = lo + t; j <= p; j += kRerunThreads) {
-            const double s = score(j);
-            mloc = (isnan(s) || isnan(mloc)) ? (s + mloc) : fmax(mloc, s);
+    }
+    double mloc = -INFINITY;
+    for (int j = lo + t; j <= p; j += kRerunThreads) {
+        const double s = score(j);
+        mloc = (isnan(s) || isnan(mloc)) ? (s + mloc) : fmax(mloc, s);
+    }
+    const double M = block_reduce(mloc, true, sm.red);
+    double lloc = 0.0, acc = 0.0;
+    for (int base = lo; base <= p; base += kRerunThreads) {
+        const int j = base + t;
+        double w = 0.0;
+        if (j <= p) {
+            w = exp(score(j) - M);
+            lloc = lloc + w;
+            sm.vat[t] = at(a.kv[1], j);
         }
-        const double M = block_reduce(mloc, true, red);
-        double lloc = 0.0, acc = 0.0;
-        for (int base = lo; base <= p; base += kRerunThreads) {
-            const int j = base + t;
-            double w = 0.0;
-            if (j <= p) {
-                w = exp(score(j) - M);
-                lloc = lloc + w;
-                vat[t] = at(a.kv[1], j);
-            }
-            wb[t] = w;
-            __syncthreads();
-            if (t < d) {
-                const int cnt = min(kRerunThreads, p - base + 1);
-                for (int jj = 0; jj < cnt; ++jj)
-                    acc = acc + wb[jj] * (vat[jj] < 0 ? 0.0 : static_cast<double>(stored(a.kv[1].base, vat[jj] + t, a.e4m3)));
-            }
-            __syncthreads();
+        sm.wb[t] = w;
+        __syncthreads();
+        if (t < d) {
+            const int cnt = min(kRerunThreads, p - base + 1);
+            for (int jj = 0; jj < cnt; ++jj)
+                acc = acc + sm.wb[jj] * (sm.vat[jj] < 0 ? 0.0 : static_cast<double>(stored(a.kv[1].base, sm.vat[jj] + t, a.e4m3)));
         }
-        const double l = block_reduce(lloc, false, red);
-        if (t < d) orow[t] = f64_to_bf16_rn(acc / l * (a.kv[1].scale ? static_cast<double>(a.kv[1].scale[g]) : 1.0));
         __syncthreads();
     }
+    const double l = block_reduce(lloc, false, sm.red);
+    if (t < d) orow[t] = f64_to_bf16_rn(acc / l * (a.kv[1].scale ? static_cast<double>(a.kv[1].scale[g]) : 1.0));
+}
+
+// out = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M): a block a (row, head), a warp every eighth span, a lane 4
+// dims (and 4 more at head dim 256); the warps' sums in their order.  A result that is not finite is worked out again.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedArgs a, const float2* ml, const float* part,
+                                                          int spans_most, int align) {
+    constexpr int V = D / 128;
+    __shared__ float4 red[8][32 * V];
+    __shared__ PagedRerun again;
+    const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int p = paged_pos(__ldg(a.pos + row), a.most, a.page_log);
+    const int spans = row_cut(p, a.win, align, a.hkv).spans;
+    const float vs = a.kv[1].scale ? __ldg(a.kv[1].scale + g) : 1.f;
+    // Plain loads from here on: what they read is written while this kernel is there already.  Blocks without work wait
+    // too, so that nothing behind the call starts early.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D;
+    if (spans == 0) {
+        if (t < D / 8) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * spans_most;
+    auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
+    float M = -INFINITY;
+    for (int s = lane; s < spans; s += 32) M = fmaxf(M, ml[rec(s)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    float den = 0.f;
+    float4 num[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) num[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < spans; s0 += 32) {
+        float w = 0.f;
+        if (s0 + lane < spans) {
+            const float2 e = ml[rec(s0 + lane)];
+            w = exp2f(e.x - M);
+            den = fmaf(w, e.y, den);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + warp + 8 * i;
+            const float ws = __shfl_sync(0xFFFFFFFFu, w, warp + 8 * i);
+            if (s >= spans) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 o = reinterpret_cast<const float4*>(part + rec(s) * D)[v * 32 + lane];
+                num[v].x = fmaf(ws, o.x, num[v].x);
+                num[v].y = fmaf(ws, o.y, num[v].y);
+                num[v].z = fmaf(ws, o.z, num[v].z);
+                num[v].w = fmaf(ws, o.w, num[v].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
+#pragma unroll
+    for (int v = 0; v < V; ++v) red[warp][v * 32 + lane] = num[v];
+    __syncthreads();
+    bool bad = false;
+    if (t < 32 * V) {
+        float4 o = red[0][t];
+        for (int w = 1; w < (spans < 8 ? spans : 8); ++w) {
+            const float4 x = red[w][t];
+            o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
+        o.x = o.x / den * vs; o.y = o.y / den * vs; o.z = o.z / den * vs; o.w = o.w / den * vs;
+        bad = !(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w));
+        reinterpret_cast<uint2*>(orow)[t] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    }
+    if (__syncthreads_or(bad)) paged_rerun(a, again, row, h);
 }
 
 bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {
@@ -1044,12 +1056,10 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     // spans(t) = ceil(t / ceil(t hkv / kFill)) is at most kFill / hkv (rounded up) where that bounds a span, and t / kSpanTiles beyond
     const int64_t fill = (kFill + hkv - 1) / hkv, least = fill < tiles ? fill : tiles, most_spans = (tiles + kSpanTiles - 1) / kSpanTiles;
     pl.spans = static_cast<int>(least > most_spans ? least : most_spans);
-    const int64_t pairs = static_cast<int64_t>(rows) * hkv, heads = static_cast<int64_t>(rows) * hq;
+    const int64_t heads = static_cast<int64_t>(rows) * hq;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.flags = kHeaderBytes;
-    pl.counts = pl.flags + up(4 * heads * sizeof(int));
-    pl.clear = pairs + rows / kPagedRows + 1;
-    pl.ml = pl.counts + up(pl.clear * sizeof(int));
+    pl.taken = kHeaderBytes;
+    pl.ml = pl.taken + up((rows / kPagedRows + 1) * sizeof(int));
     pl.part = pl.ml + up(heads * pl.spans * sizeof(float2));
     pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
     return pl;
@@ -1070,8 +1080,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     for (int i = 0; i < 2; ++i)
         if (!encode_pages(&p.map[i], &p.at[i], a.kv[i], a, p.align)) return cudaErrorInvalidValue;
     uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
-    p.flags = reinterpret_cast<int*>(base + pl.flags);
-    p.counts = reinterpret_cast<int*>(base + pl.counts);
+    int* taken = reinterpret_cast<int*>(base + pl.taken);
     p.ml = reinterpret_cast<float2*>(base + pl.ml);
     p.part = reinterpret_cast<float*>(base + pl.part);
     p.spans = pl.spans;
@@ -1079,8 +1088,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    const int clear = static_cast<int>(pl.clear);
-    paged_clear_kernel<<<clear <= 4096 ? 1 : 16, 1024, 0, s>>>(a.hdr, p.counts, clear);
+    paged_clear_kernel<<<1, 128, 0, s>>>(a.hdr, taken, a.rows / kPagedRows + 1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // each kernel is launched while the one before runs, sets itself up and waits for it on the GPU
@@ -1094,7 +1102,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     for (int r0 = 0; r0 < a.rows; r0 += kPagedRows) {
         p.row0 = r0;
         p.rows = a.rows - r0 < kPagedRows ? a.rows - r0 : kPagedRows;
-        p.next_unit = p.counts + static_cast<int64_t>(a.rows) * a.hkv + r0 / kPagedRows;
+        p.next_unit = taken + r0 / kPagedRows;
         const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
         cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
         cfg.blockDim = dim3(kPThreads);
@@ -1105,10 +1113,11 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         });
         if (e != cudaSuccess) return e;
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.rows) * a.hq < 4LL * sms ? a.rows * a.hq : 4 * sms));
-    cfg.blockDim = dim3(kRerunThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.hq);
+    cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, paged_f64_kernel, a, const_cast<const int*>(p.flags));
+    e = cudaLaunchKernelEx(&cfg, a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>, a, const_cast<const float2*>(p.ml),
+                           const_cast<const float*>(p.part), pl.spans, p.align);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
