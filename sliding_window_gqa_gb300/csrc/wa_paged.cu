@@ -10,13 +10,15 @@
 // keys are the rows: S^T = K Q^T (128 keys x 16) and O^T = V^T P^T (128 dims x the parts of P).
 // Both A operands are then the cache's own tiles as the copies leave them, both B operands
 // small; P's parts are columns of one product, so V is read from shared memory once for all
-// of them.  A key is a lane of tensor memory, so a mask is one bit a thread, and the maximum
-// of a head is only worked out where some score exceeds the running one (a vote of 128 threads).
+// of them.  A key is a lane of tensor memory, so a mask is one bit a thread, and the scores of a whole
+// span (16 columns a tile) stay there: its keys come first, then its maximum is known, then
+// its values.  Nothing is ever scaled again.  (With a running maximum, tile by tile, every other tile of
+// 8-bit pages moved some head's, where P has to fit its type: 309 us instead of 170 for the batch.)
 //
 // 8-bit pages.  e4m3 has 4 significant bits, so a query, of 8, is two e4m3 numbers: 2^k q = hi +
-// lo / 16 to 2^-22 of the head's largest value, and S comes from exact products as with bf16.
-// P is three: 256 p = p1 + p2 / 16 + p3 / 256 to 2^-12 of p (one part alone: 2^-4; two: 2^-8, about
-// what the output's own rounding loses), or to 2^-26 of the largest where that is more.
+// lo, exactly down to 2^-10 of the head's largest value and to 2^-18 of it below, and S comes from exact
+// products as with bf16.  P is three: 256 p = p1 + p2 / 32 + p3 / 1024 to 2^-12 of p (one part alone: 2^-4; two:
+// 2^-8, about what the output's own rounding loses), or to 2^-28 of the largest where that is more.
 //
 // Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's
 // keys), are cut into even spans, as many as fill the GPU once (kFill) with this row
@@ -25,17 +27,19 @@
 // unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
 //
-// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 256 threads, that streams the keys
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 384 threads, that streams the keys
 // of its units without a break between units:
-//   warp 0      TMA producer: K and V tiles through a ring of slots, in the order the tensor core
-//               reads them (K0, K1, V0, K2, V1, ...), a copy a page (or piece of one)
+//   warp 0      TMA producer: tiles through a ring of slots, in the order the tensor core reads
+//               them: K of unit 0, K of unit 1, V of unit 0, K of unit 2, V of unit 1, ...; a copy a
+//               page (or piece of one)
 //   warp 1      allocates tensor memory, issues the products; before O += V^T P^T of a row's first
 //               and last tile it zeroes V's slots without a visible key, so that what they hold
 //               never meets a zero probability as 0 * inf
 //   warp 2      takes units by a counter, looks up their pages, publishes them
 //   warp 3      Q to shared memory, split in two for 8-bit pages
-//   warps 4..7  softmax, a key a thread: exponentials, P to shared memory, a lazy rescale of O, the
-//               unit's result
+//   warps 4..7  softmax of even units, a key a thread: the maximum, exponentials, P to shared
+//   and 8..11   memory, the unit's result; of odd units.  One group's chain (a unit's ends, 2,500
+//               cycles) runs beside the other's.
 // Every wait is bounded (a status bit after kWaitLimitNs).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -49,10 +53,10 @@ namespace wa {
 namespace {
 
 constexpr int kPTile = 128;          // keys a tile
-constexpr int kPThreads = 256;
+constexpr int kPThreads = 384;
 constexpr int kPUnits = 4;           // unit slots
 constexpr int kFill = 152;           // units that a row is cut into, over its key heads
-constexpr int kSpanTiles = 16;       // at most
+constexpr int kSpanTiles = 8;        // at most (their scores fit tensor memory twice, beside O)
 
 // How a row is cut.  `align`: keys of a copy.
 struct RowCut {
@@ -121,34 +125,38 @@ struct PagedCfg {
     static constexpr int KB = D * ESZ / 128;             // blocks of 128 bytes a key
     static constexpr int SLOT = kPTile * D * ESZ;        // a tile of K or V: [16 groups of 8 keys][KB][8][128 bytes]
     static constexpr int NSLOT = 196608 / SLOT;
-    static constexpr int QN = F8 && GP == 16 ? 32 : 16;  // columns of S: the heads (8-bit: hi of GP heads, lo of them)
+    // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
+    // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
+    static constexpr int QN = F8 && GP == 16 ? 32 : 16;
+    __host__ __device__ static constexpr int lo_row() { return QN / 2; }
     static constexpr int Q_BYTES = QN * D * ESZ;         // [KB][QN / 8][8][128 bytes]
     static constexpr int PARTS = F8 ? 3 : 2;
     static constexpr int PN = (PARTS * GP + 15) / 16 * 16;
     static constexpr int P_CHUNK = PN * 128;             // 128 bytes of keys: [PN / 8][8][128 bytes]
     static constexpr int P_BYTES = ESZ * P_CHUNK;
-    static constexpr int NP = D == 256 && !F8 && GP == 16 ? 1 : 2;   // P buffers that fit
+    static constexpr int NP = NSLOT * SLOT + 2 * Q_BYTES + 4 * P_BYTES <= 220 * 1024 ? 2 : 1;   // P buffers a group that fit
     static constexpr int KSTEP = 32 / ESZ;               // keys or dims a product
     static constexpr int MB = D / 128;
-    static constexpr int S_COL = 0, O_COL = 64;          // tensor memory: two buffers of S, O of MB blocks
-    static constexpr int TMEM_COLS = 256;
-    static_assert(O_COL + MB * PN <= TMEM_COLS, "tensor memory budget");
+    static constexpr int TMEM_COLS = 512;                // tensor memory: a group's scores, [tile][16]; its O, [MB][PN]
+    __host__ __device__ static constexpr int s_col(int group) { return group * kSpanTiles * 16; }
+    __host__ __device__ static constexpr int o_col(int group) { return 2 * kSpanTiles * 16 + group * MB * PN; }
+    static_assert(o_col(2) <= TMEM_COLS, "tensor memory budget");
     static constexpr int PAGES = kSpanTiles * kPTile / 16;   // copies of a unit at most
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = OFF_RING + NSLOT * SLOT;
-    static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
-    static constexpr int OFF_UNIT = OFF_P + NP * P_BYTES;    // 8 ints a slot
+    static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;        // [group][NP]
+    static constexpr int OFF_UNIT = OFF_P + 2 * NP * P_BYTES;    // 8 ints a slot
     static constexpr int OFF_PAGES = OFF_UNIT + kPUnits * 32;
     static constexpr int OFF_PRE = OFF_PAGES + kPUnits * PAGES * 4;   // units of the rows before
-    static constexpr int OFF_X = OFF_PRE + (kPagedRows + 4) * 4;      // [4 warps][16] maxima, then sums
-    static constexpr int OFF_C = OFF_X + 256;                // [kPUnits][16] c of each head (8-bit)
-    static constexpr int OFF_BAR = OFF_C + kPUnits * 64;
+    static constexpr int OFF_X = OFF_PRE + (kPagedRows + 4) * 4;      // [group][4 warps][16] maxima, then sums
+    static constexpr int OFF_C = OFF_X + 512;                // [kPUnits][16] c of each head (8-bit)
+    static constexpr int OFF_BAR = OFF_C + (F8 ? kPUnits * 64 : 0);
     static constexpr int B_FULL = 0;                         // [NSLOT]
     static constexpr int B_FREE = B_FULL + NSLOT;
-    static constexpr int B_SFULL = B_FREE + NSLOT;           // [tile & 1] from here
-    static constexpr int B_PFULL = B_SFULL + 2;
-    static constexpr int B_PVDONE = B_PFULL + 2;
-    static constexpr int B_QFULL = B_PVDONE + 2;             // [unit & 1]
+    static constexpr int B_SFULL = B_FREE + NSLOT;           // [group]: all scores of the unit
+    static constexpr int B_PFULL = B_SFULL + 2;              // [group][NP]
+    static constexpr int B_PVDONE = B_PFULL + 2 * NP;
+    static constexpr int B_QFULL = B_PVDONE + 2 * NP;        // [unit & 1]
     static constexpr int B_QFREE = B_QFULL + 2;
     static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod kPUnits] from here
     static constexpr int B_UFREE = B_UFULL + kPUnits;
@@ -156,8 +164,8 @@ struct PagedCfg {
     static constexpr int B_UC = B_UTOOK + kPUnits;           // the unit's c are there (8-bit)
     static constexpr int B_DRAIN = B_UC + kPUnits;
     static constexpr int NBAR = B_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base, flag words
-    static constexpr int SMEM = OFF_MISC + 32;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base
+    static constexpr int SMEM = OFF_MISC + 16;
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(NBAR <= 128, "warps 4..7 set up the barriers");
 };
@@ -237,12 +245,12 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
 
-// The softmax warps' barrier, alone and as a vote.
-__device__ __forceinline__ void group_sync() { named_bar_sync(1, 128); }
-__device__ __forceinline__ bool group_any(bool x) {
+// A softmax group's barrier, alone and as a vote.
+__device__ __forceinline__ void group_sync(int group) { named_bar_sync(1 + group, 128); }
+__device__ __forceinline__ bool group_any(int group, bool x) {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(x ? 1u : 0u), "r"(1 + group) : "memory");
     return r != 0;
 }
 
@@ -261,12 +269,12 @@ __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
 }
 
 // Clears what a call counts and reports; the next kernel sets itself up meanwhile.
-__global__ void __launch_bounds__(128) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
+__global__ void __launch_bounds__(256) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) hdr->status = 0;
     if (static_cast<int>(threadIdx.x) < n) taken[threadIdx.x] = 0;
 }
-static_assert(65535 / kPagedRows < 128, "a counter a thread");
+static_assert(65535 / kPagedRows < 256, "a counter a thread");
 
 // A published unit.  nt = 0 marks the end.
 struct PUnit {
@@ -305,22 +313,19 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         tmem_alloc(smem_u32(smem + C::OFF_MISC), C::TMEM_COLS);
         tmem_relinquish();
     }
-    for (int e = tid; e < (2 * C::Q_BYTES + C::NP * C::P_BYTES) / 16; e += kPThreads)
+    for (int e = tid; e < (2 * C::Q_BYTES + 2 * C::NP * C::P_BYTES) / 16; e += kPThreads)
         st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
-    int mine[2], bad = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = 2 * tid + e;
-        mine[e] = 0;
-        if (r < p.rows) {
-            const int raw = p.a.pos[p.row0 + r], at = paged_pos(raw, p.a.most, p.a.page_log);
-            if (raw != at) bad = 1;
-            mine[e] = row_cut(at, p.a.win, p.align, p.a.hkv).spans;
-        }
-    }
+    int bad = 0;
+    static_assert(kPagedRows <= kPThreads, "a row a thread");
     {
-        int sum = mine[0] + mine[1];
+        int mine = 0;
+        if (tid < p.rows) {
+            const int raw = p.a.pos[p.row0 + tid], at = paged_pos(raw, p.a.most, p.a.page_log);
+            bad = raw != at;
+            mine = row_cut(at, p.a.win, p.align, p.a.hkv).spans;
+        }
+        int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -329,10 +334,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int* tot = reinterpret_cast<int*>(smem + C::OFF_X);
         if (lane == 31) tot[warp] = sum;
         bad = __syncthreads_or(bad);
-        int before = sum - mine[0] - mine[1];
-        for (int w = 0; w < warp; ++w) before += tot[w];
-        pre[2 * tid + 1] = before + mine[0];
-        pre[2 * tid + 2] = before + mine[0] + mine[1];
+        for (int w = 0; w < warp; ++w) sum += tot[w];
+        if (tid < kPagedRows) pre[tid + 1] = sum;
         if (tid == 0) pre[0] = 0;
     }
     tc_fence_before();
@@ -340,7 +343,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tbase = misc[0];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the join waits for this kernel's end by itself
-    static_assert(kPagedRows == 2 * kPThreads, "rows a thread");
 
     auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % kPUnits) * 32); };
     auto unit_pages = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_PAGES + (U % kPUnits) * C::PAGES * 4); };
@@ -388,31 +390,17 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (lane == 0) mbar_arrive(BAR(C::B_UTOOK + U % kPUnits));
             return true;
         };
-        auto done = [&](int U) {                  // the unit's pages are read
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
-        };
+        // K of the first unit, then K of the next one and V of this one
         PUnit cur, nxt;
-        int U = 0, idx = 0;
-        bool ok = take(0, cur), more = ok && cur.nt > 0;
-        if (more) ok = load(0, cur, 0, 0);
-        while (ok && more) {
-            const bool same = idx + 1 < cur.nt;
-            if (same) {
-                if (!(ok = load(U, cur, idx + 1, 0))) break;
-            } else {
-                if (!(ok = take(U + 1, nxt))) break;
-                more = nxt.nt > 0;
-                if (more && !(ok = load(U + 1, nxt, 0, 0))) break;
-            }
-            if (!(ok = load(U, cur, idx, 1))) break;
-            if (same) {
-                ++idx;
-            } else {
-                done(U++);
-                cur = nxt;
-                idx = 0;
-            }
+        bool ok = take(0, cur);
+        for (int i = 0; ok && i < cur.nt; ++i) ok = load(0, cur, i, 0);
+        for (int U = 0; ok && cur.nt > 0; ++U) {
+            if (!(ok = take(U + 1, nxt))) break;
+            for (int i = 0; ok && i < nxt.nt; ++i) ok = load(U + 1, nxt, i, 0);
+            for (int i = 0; ok && i < cur.nt; ++i) ok = load(U, cur, i, 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));       // the unit's pages are read
+            cur = nxt;
         }
         // the copies in flight land before the block exits, whichever role stopped early
         for (int i = max(0, u - C::NSLOT); i < u; ++i)
@@ -421,7 +409,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         // ------------------------------------------------ MMA issuer: the warp together, one lane's instructions
         const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
         const bool leader = paged_elect();
-        constexpr uint32_t idS = paged_idesc(F8, C::QN, 0), idO = paged_idesc(F8, C::PN, 1);
+        constexpr uint32_t idS = paged_idesc(F8, 16, 0), idO = paged_idesc(F8, C::PN, 1);
         constexpr uint32_t kTileHi = desc_hi(C::KB * 1024), kSmallHi = desc_hi(1024);
         int s = 0, use = 0;                       // the next load's slot
         auto next_slot = [&]() {
@@ -430,29 +418,34 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 ++use;
             }
         };
-        // S^T(t) = K Q^T
-        auto issue_s = [&](int t, int U, bool last) -> bool {
+        // S^T = K Q^T of a unit's tile
+        auto issue_s = [&](int U, int idx, bool last) -> bool {
             if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
             tc_fence_after();
             if (leader) {
-                const uint32_t d = tb + C::S_COL + (t & 1) * 32, k = desc_lo(SLOT(s), 16),
+                const uint32_t d = tb + C::s_col(U & 1) + idx * 16, k = desc_lo(SLOT(s), 16),
                                q = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES, 16);
 #pragma unroll
-                for (int i = 0; i < D / C::KSTEP; ++i) {
-                    const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4), b = q + (((i / 4) * C::QN * 128 + (i % 4) * 32) >> 4);
-                    if (i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
-                    else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
-                }
+                for (int half = 0; half < C::QN / 16; ++half)
+#pragma unroll
+                    for (int i = 0; i < D / C::KSTEP; ++i) {
+                        const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
+                        const uint32_t b = q + (((i / 4) * C::QN * 128 + half * 2048 + (i % 4) * 32) >> 4);
+                        if (half == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
+                        else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                    }
                 mma_commit(BAR(C::B_FREE + s));
-                mma_commit(BAR(C::B_SFULL + (t & 1)));
-                if (last) mma_commit(BAR(C::B_QFREE + (U & 1)));
+                if (last) {
+                    mma_commit(BAR(C::B_SFULL + (U & 1)));
+                    mma_commit(BAR(C::B_QFREE + (U & 1)));
+                }
             }
             __syncwarp();
             next_slot();
             return true;
         };
-        // O^T += V^T P^T of a tile whose keys `from` .. `to` - 1 are visible
-        auto issue_pv = [&](int t, bool first, int from, int to) -> bool {
+        // O^T += V^T P^T of a tile whose keys `from` .. `to` - 1 are visible; tp: the group's tiles before it
+        auto issue_pv = [&](int group, int tp, bool first, int from, int to) -> bool {
             if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
             if (from > 0 || to < kPTile) {
                 const int nz = from + kPTile - to;
@@ -463,51 +456,53 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (!warp_wait(BAR(C::B_PFULL + (t & 1)), static_cast<uint32_t>(t >> 1) & 1u, status)) return false;
+            const int buf = group * C::NP + tp % C::NP;
+            if (!warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tp / C::NP) & 1u, status)) return false;
             tc_fence_after();
             if (leader) {
-                const uint32_t v = desc_lo(SLOT(s), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + (t % C::NP) * C::P_BYTES, 16);
+                const uint32_t v = desc_lo(SLOT(s), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + buf * C::P_BYTES, 16);
 #pragma unroll
                 for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
                     for (int i = 0; i < kPTile / C::KSTEP; ++i) {
-                        const uint32_t d = tb + C::O_COL + mb * C::PN;
+                        const uint32_t d = tb + C::o_col(group) + mb * C::PN;
                         const uint32_t a = v + ((mb * (C::KB / C::MB) * 1024 + i * (C::KSTEP / 8) * C::KB * 1024) >> 4);
                         const uint32_t b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
                         if (i == 0 && first) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
                         else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
                     }
                 mma_commit(BAR(C::B_FREE + s));
-                mma_commit(BAR(C::B_PVDONE + (t & 1)));
+                mma_commit(BAR(C::B_PVDONE + buf));
             }
             __syncwarp();
             next_slot();
             return true;
         };
-        PUnit x;
-        auto take = [&](int U) -> bool {
-            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
+        PUnit x, last;
+        last.nt = 0;
+        int tp[2] = {0, 0};                       // tiles of each group whose products with V are issued
+        auto values = [&](int group) -> bool {
+            bool ok = true;
+            for (int idx = 0; ok && idx < last.nt; ++idx) {
+                const int key0 = last.k0 + idx * kPTile;
+                ok = issue_pv(group, group ? tp[1] : tp[0], idx == 0, max(0, last.lo - key0), min(kPTile, last.p - key0 + 1));
+                if (group) ++tp[1]; else ++tp[0];
+            }
+            return ok;
+        };
+        bool ok = true;
+        for (int U = 0; ok; ++U) {
+            if (!(ok = warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status))) break;
             read_unit(U, x);
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
             x.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
-            return true;
-        };
-        int t = 0, from = 0, to = 0;              // of tile t - 1, whose P V is to come
-        bool ok = true, first = false;
-        for (int U = 0; ok; ++U) {
-            if (!(ok = take(U)) || x.nt <= 0) break;
-            if (!(ok = warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status))) break;
-            for (int idx = 0; ok && idx < x.nt; ++idx, ++t) {
-                ok = issue_s(t, U, idx == x.nt - 1);
-                if (ok && t > 0) ok = issue_pv(t - 1, first, from, to);
-                const int key0 = x.k0 + idx * kPTile;
-                from = max(0, x.lo - key0);
-                to = min(kPTile, x.p - key0 + 1);
-                first = idx == 0;
-            }
+            if (x.nt > 0) ok = warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status);
+            for (int idx = 0; ok && idx < x.nt; ++idx) ok = issue_s(U, idx, idx == x.nt - 1);
+            if (ok) ok = values((U - 1) & 1);
+            if (x.nt <= 0) break;
+            last = x;
         }
-        if (ok && t > 0) issue_pv(t - 1, first, from, to);
         // every product issued has finished before tensor memory can be released
         if (leader) {
             mma_commit(BAR(C::B_DRAIN));
@@ -521,6 +516,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         if (bad && blockIdx.x == 0 && lane == 0) atomicOr(status, WA_STATUS_BAD_POS);
         const int units = pre[p.rows] * p.a.hkv;
         int k = static_cast<int>(blockIdx.x);
+        bool ended = false;
         for (int U = 0;; ++U) {
             int nt = 0;
             // the slot's last unit has been read by everyone
@@ -559,7 +555,11 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFULL + U % kPUnits));
-            if (nt == 0) break;
+            if (nt == 0) {
+                if (ended) break;                 // an end for each softmax group
+                ended = true;
+                continue;
+            }
             // A unit is taken no earlier than needed, so that the last ones go to whoever is free: when the producer has
             // begun this one or, where units are short, the one before it.
             const int begun = nt >= 3 ? U : U - 1;
@@ -631,12 +631,12 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                         }
                         const uint32_t a = e4m3_pair(v[0], v[1]), b = e4m3_pair(v[2], v[3]);
                         const float2 fa = e4m3_pair_f32(a), fb = e4m3_pair_f32(b);
-                        r[0] = (v[0] - fa.x) * 16.f; r[1] = (v[1] - fa.y) * 16.f;
-                        r[2] = (v[2] - fb.x) * 16.f; r[3] = (v[3] - fb.y) * 16.f;
+                        r[0] = v[0] - fa.x; r[1] = v[1] - fa.y;
+                        r[2] = v[2] - fb.x; r[3] = v[3] - fb.y;
                         hi[w] = fine ? a | (b << 16) : 0x7F7F7F7Fu;          // NaN: the head is computed again
                         lo[w] = e4m3_pair(r[0], r[1]) | (e4m3_pair(r[2], r[3]) << 16);
                     }
-                    const int el = lane * EL, low = h + GP;
+                    const int el = lane * EL, low = h + C::lo_row();
                     const uint32_t block = dst + (el >> 7) * (C::QN * 128);
                     const uint32_t ah = block + (h >> 3) * 1024 + (h & 7) * 128 + ((el & 127) ^ ((h & 7) << 4));
                     const uint32_t al = block + (low >> 3) * 1024 + (low & 7) * 128 + ((el & 127) ^ ((low & 7) << 4));
@@ -660,10 +660,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         }
     } else {
         // ------------------------------------------------ softmax: key `quarter` * 32 + lane of a tile
-        const int quarter = warp & 3, gt = tid - 128;
+        const int quarter = warp & 3, group = (warp >> 2) - 1, gt = tid & 127;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        volatile int* xbuf = reinterpret_cast<volatile int*>(smem + C::OFF_X);
-        constexpr float kLazyP = F8 ? 0.75f : 32.0f;     // log2 units m may trail: P fits its type (8-bit: 2^8.75 is below 448)
+        volatile int* xbuf = reinterpret_cast<volatile int*>(smem + C::OFF_X) + group * 64;
         constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
         // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
         // next vote, at which the four warps leave together.
@@ -672,101 +671,89 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (!dead && !warp_wait(BAR(bar), ph, status)) dead = true;
         };
         const uint32_t pk = quarter * 32 + lane;         // this thread's key: its column of P
-        int t = 0;
-        for (int U = 0;; ++U) {
+        const uint32_t s_addr = tbase + lane_addr + C::s_col(group);
+        const uint32_t o_addr = tbase + lane_addr + C::o_col(group);
+        int t = 0;                                       // the group's tiles
+        for (int U = group;; U += 2) {
             PUnit x;
             wait(C::B_UFULL + U % kPUnits, uph(U));
             read_unit(U, x);
-            float c[GP];
-#pragma unroll
-            for (int h = 0; h < GP; ++h) c[h] = p.c;
-            if (F8 && !dead && x.nt > 0) {
-                wait(C::B_UC + U % kPUnits, uph(U));
+            float c[F8 ? GP : 1];
+            if constexpr (F8) {
+                if (!dead && x.nt > 0) wait(C::B_UC + U % kPUnits, uph(U));
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
                     c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % kPUnits) * 16 + h] : 0.f;
+            } else {
+                c[0] = p.c;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
-            if (group_any(dead) || x.nt <= 0) break;
+            if (group_any(group, dead) || x.nt <= 0) break;
+            wait(C::B_SFULL + group, static_cast<uint32_t>(U >> 1) & 1u);
+            tc_fence_after();
+            // a tile's scores of this thread's key, times c
+            auto scores = [&](int idx, float (&y)[GP]) {
+                if constexpr (F8 && GP < 16) {
+                    uint32_t r[GP], q[GP];
+                    tm_load(s_addr + idx * 16, r);
+                    tm_load(s_addr + idx * 16 + C::lo_row(), q);
+                    tm_wait(r);
+                    tm_wait(q);
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) y[h] = (__uint_as_float(r[h]) + __uint_as_float(q[h])) * c[h];
+                } else {
+                    uint32_t r[GP];
+                    tm_load(s_addr + idx * 16, r);
+                    tm_wait(r);
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) y[h] = __uint_as_float(r[h]) * c[F8 ? h : 0];
+                }
+            };
+            auto visible = [&](int idx) {
+                const int key = x.k0 + idx * kPTile + static_cast<int>(pk);
+                return key >= x.lo && key <= x.p;
+            };
+            // ---- the maximum of each head over the unit (of -inf where there is none: NaN then, worked out again)
             float m[GP], l[GP];
 #pragma unroll
             for (int h = 0; h < GP; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.f;
             }
-            bool left = false;
+            for (int idx = 0; idx < x.nt; ++idx) {
+                float y[GP];
+                scores(idx, y);
+                if (visible(idx)) {
+#pragma unroll
+                    for (int h = 0; h < GP; ++h) m[h] = fmaxf(m[h], y[h]);
+                }
+            }
+            int best = 0;
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+                const int b = __reduce_max_sync(0xFFFFFFFFu, p_ordered(m[h]));
+                if (lane == h) best = b;
+            }
+            if (lane < GP) xbuf[quarter * 16 + lane] = best;
+            group_sync(group);
+#pragma unroll
+            for (int h = 0; h < GP; ++h)
+                m[h] = p_unordered(max(max(xbuf[h], xbuf[16 + h]), max(xbuf[32 + h], xbuf[48 + h]))) - kShift;
+            // ---- P, tile by tile
             for (int idx = 0; idx < x.nt; ++idx, ++t) {
-                wait(C::B_SFULL + (t & 1), static_cast<uint32_t>(t >> 1) & 1u);
-                tc_fence_after();
-                const int key = x.k0 + idx * kPTile + static_cast<int>(pk);
-                const bool vis = key >= x.lo && key <= x.p;
                 float s[GP];
-                if constexpr (F8) {
-                    uint32_t r[2 * GP];
-                    tm_load(tbase + lane_addr + C::S_COL + (t & 1) * 32, r);
-                    tm_wait(r);
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) s[h] = fmaf(__uint_as_float(r[GP + h]), 0.0625f, __uint_as_float(r[h]));
-                } else {
-                    uint32_t r[GP];
-                    tm_load(tbase + lane_addr + C::S_COL + (t & 1) * 32, r);
-                    tm_wait(r);
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) s[h] = __uint_as_float(r[h]);
-                }
-                bool over = dead;
-#pragma unroll
-                for (int h = 0; h < GP; ++h) over |= vis && fmaf(s[h], c[h], -m[h]) > kLazyP;
-                if (group_any(over)) {
-                    // some head's maximum moves: the maxima over the tile's visible keys
-                    int best = 0;
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        const float y = vis ? fmaxf(s[h] * c[h], -INFINITY) : -INFINITY;     // NaN: no maximum
-                        const int b = __reduce_max_sync(0xFFFFFFFFu, p_ordered(y));
-                        if (lane == h) best = b;
-                    }
-                    if (lane < GP) xbuf[quarter * 16 + lane] = best;
-                    if (lane == 0) misc[2 + quarter] = dead ? 1u : 0u;
-                    group_sync();
-                    left = (misc[2] | misc[3] | misc[4] | misc[5]) != 0u;
-                    if (left) break;
-                    float alpha[GP];
-                    bool moved = false;
-#pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        const float top = p_unordered(max(max(xbuf[h], xbuf[16 + h]), max(xbuf[32 + h], xbuf[48 + h])));
-                        const float now = top - m[h] > kLazyP ? top : m[h];
-                        alpha[h] = now == m[h] ? 1.f : ex2(m[h] - now);
-                        moved |= now != m[h];
-                        l[h] *= alpha[h];
-                        m[h] = now;
-                    }
-                    if (idx > 0 && moved) {       // a unit's first product starts O afresh
-                        wait(C::B_PVDONE + ((t - 1) & 1), static_cast<uint32_t>((t - 1) >> 1) & 1u);
-                        tc_fence_after();
-#pragma unroll
-                        for (int part = 0; part < C::MB * C::PARTS; ++part) {
-                            uint32_t o[GP];
-                            const uint32_t ta = tbase + lane_addr + C::O_COL + part / C::PARTS * C::PN + part % C::PARTS * GP;
-                            tm_load(ta, o);
-                            tm_wait(o);
-#pragma unroll
-                            for (int h = 0; h < GP; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
-                            tm_store(ta, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
+                scores(idx, s);
+                const bool vis = visible(idx);
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
-                    s[h] = vis ? ex2(fmaf(s[h], c[h], kShift - m[h])) : 0.f;
+                    s[h] = vis ? ex2(s[h] - m[h]) : 0.f;
                     l[h] += s[h];
                 }
                 // the buffer's last product is done
-                if (t >= C::NP) wait(C::B_PVDONE + ((t - C::NP) & 1), static_cast<uint32_t>((t - C::NP) >> 1) & 1u);
-                const uint32_t pb = sbase + C::OFF_P + (t % C::NP) * C::P_BYTES;
+                const int buf = group * C::NP + t % C::NP;
+                if (t >= C::NP) wait(C::B_PVDONE + buf, static_cast<uint32_t>(t / C::NP - 1) & 1u);
+                const uint32_t pb = sbase + C::OFF_P + buf * C::P_BYTES;
                 // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row
                 if constexpr (F8) {
                     auto at = [&](int n) { return pb + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4)); };
@@ -780,8 +767,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                             st_shared_u8(at(part * GP + h + 1), e >> 8);
                             if (part < 2) {
                                 const float2 f = e4m3_pair_f32(e);
-                                a = (a - f.x) * 16.f;
-                                b = (b - f.y) * 16.f;
+                                a = (a - f.x) * 32.f;
+                                b = (b - f.y) * 32.f;
                             }
                         }
                     }
@@ -800,49 +787,46 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(C::B_PFULL + (t & 1)));
+                if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
             }
-            if (left) break;
             // ---- the unit's result: l over the 128 keys of a tile in a fixed order, O from tensor memory
 #pragma unroll
             for (int h = 0; h < GP; ++h) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
             }
-            group_sync();                         // the maxima in this buffer have been read
+            group_sync(group);                    // the maxima in this buffer have been read
             if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < GP; ++h) xbuf[quarter * 16 + h] = __float_as_int(l[h]);
             }
-            group_sync();
-#pragma unroll
-            for (int h = 0; h < GP; ++h)
-                l[h] = (__int_as_float(xbuf[h]) + __int_as_float(xbuf[16 + h])) + (__int_as_float(xbuf[32 + h]) + __int_as_float(xbuf[48 + h]));
-            wait(C::B_PVDONE + ((t - 1) & 1), static_cast<uint32_t>((t - 1) >> 1) & 1u);
-            tc_fence_after();
+            group_sync(group);
             const int64_t unit = (static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span;
-            if (gt < GP) {
-                float mine = 0.f, sum = 0.f;
+            if (gt < G) {
+                float mine = 0.f;
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
-                    if (gt == h) {
-                        mine = m[h];
-                        sum = l[h];
-                    }
-                if (gt < G) p.ml[unit * G + gt] = make_float2(mine - kShift, sum);
+                    if (gt == h) mine = m[h];
+                p.ml[unit * G + gt] = make_float2(mine, (__int_as_float(xbuf[gt]) + __int_as_float(xbuf[16 + gt])) +
+                                                            (__int_as_float(xbuf[32 + gt]) + __int_as_float(xbuf[48 + gt])));
             }
+            {
+                const int buf = group * C::NP + (t - 1) % C::NP;
+                wait(C::B_PVDONE + buf, static_cast<uint32_t>((t - 1) / C::NP) & 1u);
+            }
+            tc_fence_after();
 #pragma unroll
             for (int mb = 0; mb < C::MB; ++mb) {
                 float o[GP];
 #pragma unroll
                 for (int part = C::PARTS - 1; part >= 0; --part) {
                     uint32_t r[GP];
-                    tm_load(tbase + lane_addr + C::O_COL + mb * C::PN + part * GP, r);
+                    tm_load(o_addr + mb * C::PN + part * GP, r);
                     tm_wait(r);
 #pragma unroll
                     for (int h = 0; h < GP; ++h) {
                         if (part == C::PARTS - 1) o[h] = __uint_as_float(r[h]);
-                        else o[h] = fmaf(o[h], F8 ? 0.0625f : 1.f, __uint_as_float(r[h]));
+                        else o[h] = fmaf(o[h], F8 ? 0.03125f : 1.f, __uint_as_float(r[h]));
                     }
                 }
                 const int dim = mb * 128 + quarter * 32 + lane;
@@ -1088,7 +1072,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    paged_clear_kernel<<<1, 128, 0, s>>>(a.hdr, taken, a.rows / kPagedRows + 1);
+    paged_clear_kernel<<<1, 256, 0, s>>>(a.hdr, taken, a.rows / kPagedRows + 1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // each kernel is launched while the one before runs, sets itself up and waits for it on the GPU
