@@ -145,7 +145,6 @@ struct PagedPlan {
     size_t part;     // float[rows * hkv * spans * G * d]
     size_t bytes;
 };
-constexpr int kPagedRows = 256;      // rows a launch
 PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win);
 
 // Kept nodes' keys and values into the rings of several layers.

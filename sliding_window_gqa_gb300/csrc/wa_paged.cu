@@ -27,16 +27,17 @@
 // unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
 //
-// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 384 threads, that streams the keys
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 416 threads, that streams the keys
 // of its units without a break between units:
-//   warp 0      TMA producer: tiles through a ring of slots, in the order the tensor core reads
-//               them: K of unit 0, K of unit 1, V of unit 0, K of unit 2, V of unit 1, ...; a copy a
-//               page (or piece of one)
-//   warp 1      allocates tensor memory, issues the products; before O += V^T P^T of a row's first
+//   warps 0, 3  TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and
+//               128 dims.  (One warp for both took 900 cycles a load, where one of 8-bit pages
+//               lands every 700.)
+//   warp 1      allocates tensor memory, issues the products: S of unit 0, S of unit 1, P V of unit 0,
+//               S of unit 2, P V of unit 1, ...; before O += V^T P^T of a row's first
 //               and last tile it zeroes V's slots without a visible key, so that what they hold
 //               never meets a zero probability as 0 * inf
 //   warp 2      takes units by a counter, looks up their pages, publishes them
-//   warp 3      Q to shared memory, split in two for 8-bit pages
+//   warp 12     Q to shared memory, split in two for 8-bit pages
 //   warps 4..7  softmax of even units, a key a thread: the maximum, exponentials, P to shared
 //   and 8..11   memory, the unit's result; of odd units.  One group's chain (a unit's ends, 2,500
 //               cycles) runs beside the other's.
@@ -53,9 +54,11 @@ namespace wa {
 namespace {
 
 constexpr int kPTile = 128;          // keys a tile
-constexpr int kPThreads = 384;
+constexpr int kPThreads = 416;
 constexpr int kPUnits = 4;           // unit slots
 constexpr int kFill = 152;           // units that a row is cut into, over its key heads
+constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
+constexpr int kPagedFewest = 64;
 constexpr int kSpanTiles = 8;        // at most (their scores fit tensor memory twice, beside O)
 
 // How a row is cut.  `align`: keys of a copy.
@@ -76,11 +79,8 @@ __device__ __forceinline__ RowCut row_cut(int p, int win, int align, int hkv) {
     return c;
 }
 
-// Keys of one copy: a page, of at most 32 KiB and one tile.
-__host__ __device__ inline int copy_keys(int d, int e4m3, int page_log) {
-    const int most = d == 256 && !e4m3 ? 64 : 128;
-    return page_log >= 7 || (1 << page_log) > most ? most : 1 << page_log;
-}
+// Keys of one copy: a page, of at most one tile.
+__host__ __device__ inline int copy_keys(int page_log) { return page_log >= 7 ? kPTile : 1 << page_log; }
 
 // A row's last position as every kernel uses it.
 __device__ __forceinline__ int paged_pos(int raw, int most, int page_log) {
@@ -122,38 +122,41 @@ struct PagedCfg {
     static constexpr int D = D_, GP = GP_;               // GP: query heads a key head, rounded up to 4, 8 or 16
     static constexpr bool F8 = F8_;
     static constexpr int ESZ = F8 ? 1 : 2;
-    static constexpr int KB = D * ESZ / 128;             // blocks of 128 bytes a key
-    static constexpr int SLOT = kPTile * D * ESZ;        // a tile of K or V: [16 groups of 8 keys][KB][8][128 bytes]
-    static constexpr int NSLOT = 196608 / SLOT;
+    static constexpr int HV = D / 128;                   // loads a tile and operand: 128 keys x 128 dims each,
+    static constexpr int KB = ESZ;                       // in blocks of 128 bytes of a key,
+    static constexpr int SLOT = kPTile * KB * 128;       // as [16 groups of 8 keys][KB][8][128 bytes]
+    static constexpr int NSLOT = 98304 / SLOT;           // slots of K, and of V
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
     // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
     static constexpr int QN = F8 && GP == 16 ? 32 : 16;
     __host__ __device__ static constexpr int lo_row() { return QN / 2; }
-    static constexpr int Q_BYTES = QN * D * ESZ;         // [KB][QN / 8][8][128 bytes]
+    static constexpr int Q_BYTES = QN * D * ESZ;         // [D * ESZ / 128][QN / 8][8][128 bytes]
     static constexpr int PARTS = F8 ? 3 : 2;
     static constexpr int PN = (PARTS * GP + 15) / 16 * 16;
     static constexpr int P_CHUNK = PN * 128;             // 128 bytes of keys: [PN / 8][8][128 bytes]
     static constexpr int P_BYTES = ESZ * P_CHUNK;
-    static constexpr int NP = NSLOT * SLOT + 2 * Q_BYTES + 4 * P_BYTES <= 220 * 1024 ? 2 : 1;   // P buffers a group that fit
+    static constexpr int NP = 2 * NSLOT * SLOT + 2 * Q_BYTES + 4 * P_BYTES <= 220 * 1024 ? 2 : 1;   // P buffers a group that fit
     static constexpr int KSTEP = 32 / ESZ;               // keys or dims a product
-    static constexpr int MB = D / 128;
-    static constexpr int TMEM_COLS = 512;                // tensor memory: a group's scores, [tile][16]; its O, [MB][PN]
+    static constexpr int TMEM_COLS = 512;                // tensor memory: a group's scores, [tile][16]; its O, [HV][PN]
     __host__ __device__ static constexpr int s_col(int group) { return group * kSpanTiles * 16; }
-    __host__ __device__ static constexpr int o_col(int group) { return 2 * kSpanTiles * 16 + group * MB * PN; }
+    __host__ __device__ static constexpr int o_col(int group) { return 2 * kSpanTiles * 16 + group * HV * PN; }
     static_assert(o_col(2) <= TMEM_COLS, "tensor memory budget");
+    static constexpr int ROWS = D == 256 && !F8 && GP == 16 ? 64 : kPagedRows;   // rows a launch
+    static_assert(ROWS >= kPagedFewest, "counters");
     static constexpr int PAGES = kSpanTiles * kPTile / 16;   // copies of a unit at most
     static constexpr int OFF_RING = 0;
-    static constexpr int OFF_Q = OFF_RING + NSLOT * SLOT;
+    static constexpr int OFF_Q = OFF_RING + 2 * NSLOT * SLOT;
     static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;        // [group][NP]
     static constexpr int OFF_UNIT = OFF_P + 2 * NP * P_BYTES;    // 8 ints a slot
     static constexpr int OFF_PAGES = OFF_UNIT + kPUnits * 32;
     static constexpr int OFF_PRE = OFF_PAGES + kPUnits * PAGES * 4;   // units of the rows before
-    static constexpr int OFF_X = OFF_PRE + (kPagedRows + 4) * 4;      // [group][4 warps][16] maxima, then sums
+    static constexpr int OFF_LAST = OFF_PRE + (ROWS + 4) * 4;        // last positions
+    static constexpr int OFF_X = OFF_LAST + ROWS * 4;                 // [group][4 warps][16] maxima, then sums
     static constexpr int OFF_C = OFF_X + 512;                // [kPUnits][16] c of each head (8-bit)
     static constexpr int OFF_BAR = OFF_C + (F8 ? kPUnits * 64 : 0);
-    static constexpr int B_FULL = 0;                         // [NSLOT]
-    static constexpr int B_FREE = B_FULL + NSLOT;
-    static constexpr int B_SFULL = B_FREE + NSLOT;           // [group]: all scores of the unit
+    static constexpr int B_FULL = 0;                         // [K, V][NSLOT]
+    static constexpr int B_FREE = B_FULL + 2 * NSLOT;
+    static constexpr int B_SFULL = B_FREE + 2 * NSLOT;           // [group]: all scores of the unit
     static constexpr int B_PFULL = B_SFULL + 2;              // [group][NP]
     static constexpr int B_PVDONE = B_PFULL + 2 * NP;
     static constexpr int B_QFULL = B_PVDONE + 2 * NP;        // [unit & 1]
@@ -269,12 +272,12 @@ __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
 }
 
 // Clears what a call counts and reports; the next kernel sets itself up meanwhile.
-__global__ void __launch_bounds__(256) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
+__global__ void __launch_bounds__(1024) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) hdr->status = 0;
     if (static_cast<int>(threadIdx.x) < n) taken[threadIdx.x] = 0;
 }
-static_assert(65535 / kPagedRows < 256, "a counter a thread");
+static_assert(65535 / kPagedFewest < 1024, "a counter a thread");
 
 // A published unit.  nt = 0 marks the end.
 struct PUnit {
@@ -294,8 +297,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     }
     const uint32_t bar0 = sbase + C::OFF_BAR;
     auto BAR = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-    auto SLOT = [&](int s) { return sbase + C::OFF_RING + static_cast<uint32_t>(s) * C::SLOT; };
+    auto SLOT = [&](int s) { return sbase + C::OFF_RING + static_cast<uint32_t>(s) * C::SLOT; };      // V's after K's
     int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
+    int* lasts = reinterpret_cast<int*>(smem + C::OFF_LAST);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int G = p.a.hq / p.a.hkv;
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         const int i = tid - 128;
         int count = 1;
         if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // the softmax warps
-        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 7;                // producer, MMA, Q, softmax warps
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8;                // producers, MMA, Q, softmax warps
         mbar_init(BAR(i), count);
         fence_mbar_init();
     }
@@ -317,13 +321,14 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     int bad = 0;
-    static_assert(kPagedRows <= kPThreads, "a row a thread");
+    static_assert(C::ROWS <= kPThreads, "a row a thread");
     {
         int mine = 0;
         if (tid < p.rows) {
             const int raw = p.a.pos[p.row0 + tid], at = paged_pos(raw, p.a.most, p.a.page_log);
             bad = raw != at;
             mine = row_cut(at, p.a.win, p.align, p.a.hkv).spans;
+            lasts[tid] = at;
         }
         int sum = mine;
 #pragma unroll
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         if (lane == 31) tot[warp] = sum;
         bad = __syncthreads_or(bad);
         for (int w = 0; w < warp; ++w) sum += tot[w];
-        if (tid < kPagedRows) pre[tid + 1] = sum;
+        if (tid < C::ROWS) pre[tid + 1] = sum;
         if (tid == 0) pre[0] = 0;
     }
     tc_fence_before();
@@ -353,129 +358,144 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     };
     const int pieces = kPTile / p.align;          // copies a tile
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            prefetch_tensormap(&p.map[0]);
-            prefetch_tensormap(&p.map[1]);
-        }
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------ TMA producers: K, V
+        const int side = warp == 0 ? 0 : 1;
+        const PageCoord at = p.at[side];
+        const CUtensorMap* map = &p.map[side];
+        if (lane == 0) prefetch_tensormap(map);
         const uint64_t pol = policy_evict_first();
-        int u = 0;                                // loads issued
         const int in_page = (1 << p.a.page_log) - 1;
-        // a tile of K (side 0) or V: lane j copies its j-th piece
-        auto load = [&](int U, const PUnit& x, int idx, int side) -> bool {
-            const int s = u % C::NSLOT, use = u / C::NSLOT;
-            if (use > 0 && !warp_wait(BAR(C::B_FREE + s), (use - 1) & 1, status)) return false;
-            const uint32_t full = BAR(C::B_FULL + s);
-            int id = -2;
-            if (lane < pieces) id = unit_pages(U)[idx * pieces + lane];
-            const int wanted = __popc(__ballot_sync(0xFFFFFFFFu, id != -2));
-            if (lane == 0) mbar_arrive_expect_tx(full, wanted * p.align * D * C::ESZ);
-            __syncwarp();
-            if (id != -2) {
-                const PageCoord& at = p.at[side];
-                const int group = ((x.k0 + idx * kPTile + lane * p.align) & in_page) >> 3;
-                const int c3 = id < 0 ? at.none : at.by_slots ? id * at.ratio + group : group;
-                const int c4 = id < 0 || at.by_slots ? x.g : id * at.ratio + x.g;
-                tma_load_5d(SLOT(s) + lane * p.align * D * C::ESZ, &p.map[side], 0, 0, 0, c3, c4, full, pol);
+        static_assert(C::PAGES <= 64, "two copies of a unit a lane");
+        int c3[2], c4[2];                         // where the unit's copies `lane` and `lane` + 32 start
+        bool want[2];
+        auto look_up = [&](int U, const PUnit& x) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = lane + 32 * e, id = i < x.nt * pieces ? unit_pages(U)[i] : -2;
+                const int group = ((x.k0 + i * p.align) & in_page) >> 3;
+                want[e] = id != -2;
+                c3[e] = id < 0 ? at.none : at.by_slots ? id * at.ratio + group : group;
+                c4[e] = id < 0 || at.by_slots ? x.g : id * at.ratio + x.g;
             }
             __syncwarp();
-            ++u;
+            if (lane == 0) {
+                mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+                if (side == 0) mbar_arrive(BAR(C::B_UTOOK + U % kPUnits));
+            }
+        };
+        int s = 0, use = 0, loads = 0;            // the next load's slot
+        // tile idx of the unit: lane j copies its j-th piece, of each 128 dims
+        auto load = [&](int idx) -> bool {
+            const int first = idx * pieces, hi = first >> 5, from = (first & 31) + lane;
+            const int x3 = __shfl_sync(0xFFFFFFFFu, hi ? c3[1] : c3[0], from), x4 = __shfl_sync(0xFFFFFFFFu, hi ? c4[1] : c4[0], from);
+            const uint32_t wanted = (__ballot_sync(0xFFFFFFFFu, hi ? want[1] : want[0]) >> (first & 31)) & ((1u << pieces) - 1u);
+            const uint32_t bytes = __popc(wanted) * p.align * C::KB * 128;
+#pragma unroll
+            for (int half = 0; half < C::HV; ++half) {
+                const int at_s = side * C::NSLOT + s;
+                if (use > 0 && !warp_wait(BAR(C::B_FREE + at_s), (use - 1) & 1, status)) return false;
+                // (a copy may land before the barrier is told how much to expect: its one arrival is still to come)
+                if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + at_s), bytes);
+                if ((wanted >> lane) & 1u)
+                    tma_load_5d(SLOT(at_s) + lane * p.align * C::KB * 128, map, 0, 0, half * C::KB, x3, x4, BAR(C::B_FULL + at_s), pol);
+                __syncwarp();
+                ++loads;
+                if (++s == C::NSLOT) {
+                    s = 0;
+                    ++use;
+                }
+            }
             return true;
         };
-        auto take = [&](int U, PUnit& x) -> bool {
-            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
+        PUnit x;
+        for (int U = 0;; ++U) {
+            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
             read_unit(U, x);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UTOOK + U % kPUnits));
-            return true;
-        };
-        // K of the first unit, then K of the next one and V of this one
-        PUnit cur, nxt;
-        bool ok = take(0, cur);
-        for (int i = 0; ok && i < cur.nt; ++i) ok = load(0, cur, i, 0);
-        for (int U = 0; ok && cur.nt > 0; ++U) {
-            if (!(ok = take(U + 1, nxt))) break;
-            for (int i = 0; ok && i < nxt.nt; ++i) ok = load(U + 1, nxt, i, 0);
-            for (int i = 0; ok && i < cur.nt; ++i) ok = load(U, cur, i, 1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));       // the unit's pages are read
-            cur = nxt;
+            if (x.nt <= 0) break;
+            look_up(U, x);
+            bool ok = true;
+            for (int i = 0; ok && i < x.nt; ++i) ok = load(i);
+            if (!ok) break;
         }
         // the copies in flight land before the block exits, whichever role stopped early
-        for (int i = max(0, u - C::NSLOT); i < u; ++i)
-            if (!mbar_wait(BAR(C::B_FULL + i % C::NSLOT), static_cast<uint32_t>(i / C::NSLOT) & 1u, status)) break;
+        for (int i = max(0, loads - C::NSLOT); i < loads; ++i)
+            if (!mbar_wait(BAR(C::B_FULL + side * C::NSLOT + i % C::NSLOT), static_cast<uint32_t>(i / C::NSLOT) & 1u, status)) break;
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer: the warp together, one lane's instructions
         const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
         const bool leader = paged_elect();
         constexpr uint32_t idS = paged_idesc(F8, 16, 0), idO = paged_idesc(F8, C::PN, 1);
         constexpr uint32_t kTileHi = desc_hi(C::KB * 1024), kSmallHi = desc_hi(1024);
-        int s = 0, use = 0;                       // the next load's slot
-        auto next_slot = [&]() {
-            if (++s == C::NSLOT) {
-                s = 0;
-                ++use;
+        int s[2] = {0, 0}, use[2] = {0, 0};       // the next loads' slots, of K and of V
+        auto next_slot = [&](int side) {
+            if (++s[side] == C::NSLOT) {
+                s[side] = 0;
+                ++use[side];
             }
         };
         // S^T = K Q^T of a unit's tile
         auto issue_s = [&](int U, int idx, bool last) -> bool {
-            if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
-            tc_fence_after();
-            if (leader) {
-                const uint32_t d = tb + C::s_col(U & 1) + idx * 16, k = desc_lo(SLOT(s), 16),
-                               q = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES, 16);
 #pragma unroll
-                for (int half = 0; half < C::QN / 16; ++half)
+            for (int half = 0; half < C::HV; ++half) {
+                if (!warp_wait(BAR(C::B_FULL + s[0]), use[0] & 1, status)) return false;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t d = tb + C::s_col(U & 1) + idx * 16, k = desc_lo(SLOT(s[0]), 16),
+                                   q = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES + half * C::KB * C::QN * 128, 16);
 #pragma unroll
-                    for (int i = 0; i < D / C::KSTEP; ++i) {
-                        const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
-                        const uint32_t b = q + (((i / 4) * C::QN * 128 + half * 2048 + (i % 4) * 32) >> 4);
-                        if (half == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
-                        else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                    for (int set = 0; set < C::QN / 16; ++set)
+#pragma unroll
+                        for (int i = 0; i < 128 / C::KSTEP; ++i) {
+                            const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
+                            const uint32_t b = q + (((i / 4) * C::QN * 128 + set * 2048 + (i % 4) * 32) >> 4);
+                            if (half == 0 && set == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
+                            else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                        }
+                    mma_commit(BAR(C::B_FREE + s[0]));
+                    if (last && half == C::HV - 1) {
+                        mma_commit(BAR(C::B_SFULL + (U & 1)));
+                        mma_commit(BAR(C::B_QFREE + (U & 1)));
                     }
-                mma_commit(BAR(C::B_FREE + s));
-                if (last) {
-                    mma_commit(BAR(C::B_SFULL + (U & 1)));
-                    mma_commit(BAR(C::B_QFREE + (U & 1)));
                 }
+                __syncwarp();
+                next_slot(0);
             }
-            __syncwarp();
-            next_slot();
             return true;
         };
         // O^T += V^T P^T of a tile whose keys `from` .. `to` - 1 are visible; tp: the group's tiles before it
         auto issue_pv = [&](int group, int tp, bool first, int from, int to) -> bool {
-            if (!warp_wait(BAR(C::B_FULL + s), use & 1, status)) return false;
-            if (from > 0 || to < kPTile) {
-                const int nz = from + kPTile - to;
-                for (int e = lane; e < nz * C::KB * 8; e += 32) {
-                    const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
-                    st_shared_v4(SLOT(s) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
             const int buf = group * C::NP + tp % C::NP;
-            if (!warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tp / C::NP) & 1u, status)) return false;
-            tc_fence_after();
-            if (leader) {
-                const uint32_t v = desc_lo(SLOT(s), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + buf * C::P_BYTES, 16);
 #pragma unroll
-                for (int mb = 0; mb < C::MB; ++mb)
+            for (int half = 0; half < C::HV; ++half) {
+                const int at = C::NSLOT + s[1];
+                if (!warp_wait(BAR(C::B_FULL + at), use[1] & 1, status)) return false;
+                if (from > 0 || to < kPTile) {
+                    const int nz = from + kPTile - to;
+                    for (int e = lane; e < nz * C::KB * 8; e += 32) {
+                        const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
+                        st_shared_v4(SLOT(at) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (half == 0 && !warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tp / C::NP) & 1u, status)) return false;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t v = desc_lo(SLOT(at), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + buf * C::P_BYTES, 16);
+                    const uint32_t d = tb + C::o_col(group) + half * C::PN;
 #pragma unroll
                     for (int i = 0; i < kPTile / C::KSTEP; ++i) {
-                        const uint32_t d = tb + C::o_col(group) + mb * C::PN;
-                        const uint32_t a = v + ((mb * (C::KB / C::MB) * 1024 + i * (C::KSTEP / 8) * C::KB * 1024) >> 4);
-                        const uint32_t b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
+                        const uint32_t a = v + ((i * (C::KSTEP / 8) * C::KB * 1024) >> 4), b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
                         if (i == 0 && first) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
                         else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
                     }
-                mma_commit(BAR(C::B_FREE + s));
-                mma_commit(BAR(C::B_PVDONE + buf));
+                    mma_commit(BAR(C::B_FREE + at));
+                    if (half == C::HV - 1) mma_commit(BAR(C::B_PVDONE + buf));
+                }
+                __syncwarp();
+                next_slot(1);
             }
-            __syncwarp();
-            next_slot();
             return true;
         };
         PUnit x, last;
@@ -528,7 +548,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     const int m = (a + b) >> 1;
                     if (pre[m] <= s) a = m; else b = m;
                 }
-                const int row = p.row0 + a, last = paged_pos(p.a.pos[row], p.a.most, p.a.page_log);
+                const int row = p.row0 + a, last = lasts[a];
                 const RowCut cut = row_cut(last, p.a.win, p.align, p.a.hkv);
                 const int span = s - pre[a], each = cut.tiles / cut.spans, more = cut.tiles - each * cut.spans;
                 nt = each + (span < more ? 1 : 0);
@@ -562,13 +582,13 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             // A unit is taken no earlier than needed, so that the last ones go to whoever is free: when the producer has
             // begun this one or, where units are short, the one before it.
-            const int begun = nt >= 3 ? U : U - 1;
+            const int begun = U - 1;
             if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % kPUnits), uph(begun), status)) break;
             int nk = 0;
             if (lane == 0) nk = atomicAdd(p.next_unit, 1);
             k = __shfl_sync(0xFFFFFFFFu, nk, 0) + static_cast<int>(gridDim.x);
         }
-    } else if (warp == 3) {
+    } else if (warp == 12) {
         // ------------------------------------------------ Q
         constexpr int EL = D / 32;                // values a lane and head
         PUnit x;
@@ -816,7 +836,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             tc_fence_after();
 #pragma unroll
-            for (int mb = 0; mb < C::MB; ++mb) {
+            for (int mb = 0; mb < C::HV; ++mb) {
                 float o[GP];
 #pragma unroll
                 for (int part = C::PARTS - 1; part >= 0; --part) {
@@ -1007,7 +1027,7 @@ bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const Pag
                           static_cast<cuuint64_t>(groups), static_cast<cuuint64_t>(heads)};
     cuuint64_t strides[4] = {static_cast<cuuint64_t>(side.slot * esz), 128, static_cast<cuuint64_t>(8 * side.slot * esz),
                              static_cast<cuuint64_t>(side.head * esz)};
-    cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / esz), 8, static_cast<cuuint32_t>(a.d * esz / 128),
+    cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / esz), 8, static_cast<cuuint32_t>(esz),
                          static_cast<cuuint32_t>(align / 8), 1};
     cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return enc(m, a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, side.base, dims, strides, box, es,
@@ -1020,7 +1040,7 @@ template <class F>
 cudaError_t for_each_paged(F&& f) {
     cudaError_t e;
 #define WA_PAGED(D, F8, GP) \
-    if ((e = f(paged_kernel<D, F8, GP>, D, F8, GP, PagedCfg<D, F8, GP>::SMEM)) != cudaSuccess) return e
+    if ((e = f(paged_kernel<D, F8, GP>, D, F8, GP, PagedCfg<D, F8, GP>::SMEM, PagedCfg<D, F8, GP>::ROWS)) != cudaSuccess) return e
     WA_PAGED(128, false, 4); WA_PAGED(128, false, 8); WA_PAGED(128, false, 16);
     WA_PAGED(256, false, 4); WA_PAGED(256, false, 8); WA_PAGED(256, false, 16);
     WA_PAGED(128, true, 4); WA_PAGED(128, true, 8); WA_PAGED(128, true, 16);
@@ -1033,7 +1053,7 @@ cudaError_t for_each_paged(F&& f) {
 
 PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win) {
     PagedPlan pl{};
-    const int align = copy_keys(d, e4m3, page_log);
+    const int align = copy_keys(page_log);
     const int64_t keys = static_cast<int64_t>(most) << page_log;
     int64_t tiles = (keys + kPTile - 1) / kPTile;
     if (win > 0 && (win + align - 2) / kPTile + 1 < tiles) tiles = (static_cast<int64_t>(win) + align - 2) / kPTile + 1;
@@ -1043,14 +1063,14 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     const int64_t heads = static_cast<int64_t>(rows) * hq;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     pl.taken = kHeaderBytes;
-    pl.ml = pl.taken + up((rows / kPagedRows + 1) * sizeof(int));
+    pl.ml = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
     pl.part = pl.ml + up(heads * pl.spans * sizeof(float2));
     pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
     return pl;
 }
 
 cudaError_t paged_prepare_device(int) {
-    return for_each_paged([](auto kernel, int, bool, int, int smem) {
+    return for_each_paged([](auto kernel, int, bool, int, int smem, int) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
 }
@@ -1060,7 +1080,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     const int G = a.hq / a.hkv, gp = G <= 4 ? 4 : G <= 8 ? 8 : 16;
     PagedParams p{};
     p.a = a;
-    p.align = copy_keys(a.d, a.e4m3, a.page_log);
+    p.align = copy_keys(a.page_log);
     for (int i = 0; i < 2; ++i)
         if (!encode_pages(&p.map[i], &p.at[i], a.kv[i], a, p.align)) return cudaErrorInvalidValue;
     uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
@@ -1072,7 +1092,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    paged_clear_kernel<<<1, 256, 0, s>>>(a.hdr, taken, a.rows / kPagedRows + 1);
+    paged_clear_kernel<<<1, (a.rows / kPagedFewest / 32 + 1) * 32, 0, s>>>(a.hdr, taken, a.rows / kPagedFewest + 1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // each kernel is launched while the one before runs, sets itself up and waits for it on the GPU
@@ -1083,20 +1103,22 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    for (int r0 = 0; r0 < a.rows; r0 += kPagedRows) {
-        p.row0 = r0;
-        p.rows = a.rows - r0 < kPagedRows ? a.rows - r0 : kPagedRows;
-        p.next_unit = taken + r0 / kPagedRows;
-        const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
-        cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+    e = for_each_paged([&](auto kernel, int d, bool f8, int g, int smem, int most_rows) {
+        if (d != a.d || f8 != (a.e4m3 != 0) || g != gp) return cudaSuccess;
         cfg.blockDim = dim3(kPThreads);
-        e = for_each_paged([&](auto kernel, int d, bool f8, int g, int smem) {
-            if (d != a.d || f8 != (a.e4m3 != 0) || g != gp) return cudaSuccess;
-            cfg.dynamicSmemBytes = smem;
-            return cudaLaunchKernelEx(&cfg, kernel, p);
-        });
-        if (e != cudaSuccess) return e;
-    }
+        cfg.dynamicSmemBytes = smem;
+        for (int r0 = 0; r0 < a.rows; r0 += most_rows) {
+            p.row0 = r0;
+            p.rows = a.rows - r0 < most_rows ? a.rows - r0 : most_rows;
+            p.next_unit = taken + r0 / most_rows;
+            const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
+            cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+            const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p);
+            if (err != cudaSuccess) return err;
+        }
+        return cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.hq);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
