@@ -141,6 +141,7 @@ struct PagedArgs {
 struct PagedPlan {
     int spans;
     size_t taken;    // int[launches] units that are taken
+    size_t said;     // int[launches * CTAs] what they have to report
     size_t ml;       // float2[rows * hkv * spans * G]
     size_t part;     // float[rows * hkv * spans * G * d]
     size_t bytes;

@@ -21,8 +21,8 @@
 // 2^-8, about what the output's own rounding loses), or to 2^-28 of the largest where that is more.
 //
 // Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's
-// keys), are cut into even spans, as many as fill the GPU once (kFill) with this row
-// alone, of at most kSpanTiles.  A unit of work is (row, key head, span); it leaves (m, l, O) in
+// keys), are cut into even spans of at most kSpanTiles, as many as fill the GPU once, or twice, ..
+// (kFill) with this row alone.  A unit of work is (row, key head, span); it leaves (m, l, O) in
 // fp32, and paged_merge_kernel joins a row's spans.  (Joined by the CTA that finished a row's last
 // unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
@@ -56,18 +56,21 @@ namespace {
 constexpr int kPTile = 128;          // keys a tile
 constexpr int kPThreads = 416;
 constexpr int kPUnits = 4;           // unit slots
-constexpr int kFill = 152;           // units that a row is cut into, over its key heads
+constexpr int kFill = 152;           // a row is cut into this many units, or twice as many, .., over its key heads
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
+constexpr int kPagedGrid = 256;      // CTAs of a launch at most
+constexpr int kInTurn = 4;
 constexpr int kSpanTiles = 8;        // at most (their scores fit tensor memory twice, beside O)
 
 // How a row is cut.  `align`: keys of a copy.
 struct RowCut {
     int lo, k0, tiles, spans;        // first visible key, first key of the first tile
 };
+__host__ __device__ inline int64_t row_waves(int64_t tiles, int hkv) { return (tiles * hkv + kFill * kSpanTiles - 1) / (kFill * kSpanTiles); }
 __host__ __device__ inline int span_tiles(int64_t tiles, int hkv) {
-    const int64_t want = (tiles * hkv + kFill - 1) / kFill;
-    return want < kSpanTiles ? static_cast<int>(want) : kSpanTiles;
+    const int64_t units = kFill * row_waves(tiles, hkv);
+    return static_cast<int>((tiles * hkv + units - 1) / units);
 }
 __device__ __forceinline__ RowCut row_cut(int p, int win, int align, int hkv) {
     RowCut c;
@@ -108,7 +111,8 @@ struct PagedParams {
     CUtensorMap map[2];
     PageCoord at[2];
     PagedArgs a;
-    int* next_unit;
+    int* next_unit;                // null: units go to the CTAs in turn
+    int* said;                     // [CTA]: its WA_STATUS_* bits
     float2* ml;
     float* part;
     int row0, rows;                // the launch's rows
@@ -257,11 +261,24 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
     return r != 0;
 }
 
-__device__ __forceinline__ int p_ordered(float x) {     // integers of the same order as fp32 values
-    const int b = __float_as_int(x);
-    return b ^ ((b >> 31) & 0x7FFFFFFF);
+// Each of N values over the warp's lanes, by halves: lane l keeps N / 2 of them and hands on the others, and so on (for
+// 16 values 16 shuffles instead of 80).  Returns value l / (32 / N) in lane l.
+template <int N, class F>
+__device__ __forceinline__ float reduce_each(float (&x)[N], F op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = N / 2, o = 16; n >= 1; n >>= 1, o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = upper ? x[n + i] : x[i], give = upper ? x[i] : x[n + i];
+            x[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+        }
+    }
+#pragma unroll
+    for (int o = 16 / N; o >= 1; o >>= 1) x[0] = op(x[0], __shfl_xor_sync(0xFFFFFFFFu, x[0], o));
+    return x[0];
 }
-__device__ __forceinline__ float p_unordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF)); }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -271,10 +288,10 @@ __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
     return __half22float2(__half2(h));
 }
 
-// Clears what a call counts and reports; the next kernel sets itself up meanwhile.
-__global__ void __launch_bounds__(1024) paged_clear_kernel(WsHeader* hdr, int* taken, int n) {
+// Clears what a call counts; the next kernel sets itself up meanwhile.
+__global__ void __launch_bounds__(1024) paged_clear_kernel(int* taken, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) hdr->status = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (static_cast<int>(threadIdx.x) < n) taken[threadIdx.x] = 0;
 }
 static_assert(65535 / kPagedFewest < 1024, "a counter a thread");
@@ -289,10 +306,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     using C = PagedCfg<D, F8, GP>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
-    int* const status = &p.a.hdr->status;
+    int* const status = p.said + blockIdx.x;
     if (sbase & 1023u) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (threadIdx.x == 0) atomicOr(status, WA_STATUS_LAYOUT);
+        if (threadIdx.x == 0) *status = WA_STATUS_LAYOUT;
         return;
     }
     const uint32_t bar0 = sbase + C::OFF_BAR;
@@ -320,6 +337,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     for (int e = tid; e < (2 * C::Q_BYTES + 2 * C::NP * C::P_BYTES) / 16; e += kPThreads)
         st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
+    // nothing before this line reads or writes what a kernel before this one may be at
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the join waits for this kernel's end by itself
     int bad = 0;
     static_assert(C::ROWS <= kPThreads, "a row a thread");
     {
@@ -339,6 +359,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int* tot = reinterpret_cast<int*>(smem + C::OFF_X);
         if (lane == 31) tot[warp] = sum;
         bad = __syncthreads_or(bad);
+        if (tid == 0) *status = bad && blockIdx.x == 0 ? WA_STATUS_BAD_POS : 0;
         for (int w = 0; w < warp; ++w) sum += tot[w];
         if (tid < C::ROWS) pre[tid + 1] = sum;
         if (tid == 0) pre[0] = 0;
@@ -347,7 +368,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = misc[0];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the join waits for this kernel's end by itself
 
     auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % kPUnits) * 32); };
     auto unit_pages = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_PAGES + (U % kPUnits) * C::PAGES * 4); };
@@ -531,9 +551,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ units
-        // nothing before this line reads what the clear kernel writes
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (bad && blockIdx.x == 0 && lane == 0) atomicOr(status, WA_STATUS_BAD_POS);
         const int units = pre[p.rows] * p.a.hkv;
         int k = static_cast<int>(blockIdx.x);
         bool ended = false;
@@ -583,6 +600,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             // A unit is taken no earlier than needed, so that the last ones go to whoever is free: when the producer has
             // begun this one or, where units are short, the one before it.
             const int begun = U - 1;
+            if (!p.next_unit) {
+                k += static_cast<int>(gridDim.x);
+                continue;
+            }
             if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % kPUnits), uph(begun), status)) break;
             int nk = 0;
             if (lane == 0) nk = atomicAdd(p.next_unit, 1);
@@ -682,7 +703,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         // ------------------------------------------------ softmax: key `quarter` * 32 + lane of a tile
         const int quarter = warp & 3, group = (warp >> 2) - 1, gt = tid & 127;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        volatile int* xbuf = reinterpret_cast<volatile int*>(smem + C::OFF_X) + group * 64;
+        volatile float* xbuf = reinterpret_cast<volatile float*>(smem + C::OFF_X) + group * 64;
         constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
         // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
         // next vote, at which the four warps leave together.
@@ -749,17 +770,13 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     for (int h = 0; h < GP; ++h) m[h] = fmaxf(m[h], y[h]);
                 }
             }
-            int best = 0;
-#pragma unroll
-            for (int h = 0; h < GP; ++h) {
-                const int b = __reduce_max_sync(0xFFFFFFFFu, p_ordered(m[h]));
-                if (lane == h) best = b;
+            {
+                const float best = reduce_each(m, [](float a, float b) { return fmaxf(a, b); });
+                if (lane % (32 / GP) == 0) xbuf[quarter * 16 + lane / (32 / GP)] = best;
             }
-            if (lane < GP) xbuf[quarter * 16 + lane] = best;
             group_sync(group);
 #pragma unroll
-            for (int h = 0; h < GP; ++h)
-                m[h] = p_unordered(max(max(xbuf[h], xbuf[16 + h]), max(xbuf[32 + h], xbuf[48 + h]))) - kShift;
+            for (int h = 0; h < GP; ++h) m[h] = fmaxf(fmaxf(xbuf[h], xbuf[16 + h]), fmaxf(xbuf[32 + h], xbuf[48 + h])) - kShift;
             // ---- P, tile by tile
             for (int idx = 0; idx < x.nt; ++idx, ++t) {
                 float s[GP];
@@ -810,16 +827,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
             }
             // ---- the unit's result: l over the 128 keys of a tile in a fixed order, O from tensor memory
-#pragma unroll
-            for (int h = 0; h < GP; ++h) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
-            }
+            const float sum = reduce_each(l, [](float a, float b) { return a + b; });
             group_sync(group);                    // the maxima in this buffer have been read
-            if (lane == 0) {
-#pragma unroll
-                for (int h = 0; h < GP; ++h) xbuf[quarter * 16 + h] = __float_as_int(l[h]);
-            }
+            if (lane % (32 / GP) == 0) xbuf[quarter * 16 + lane / (32 / GP)] = sum;
             group_sync(group);
             const int64_t unit = (static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span;
             if (gt < G) {
@@ -827,8 +837,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
                     if (gt == h) mine = m[h];
-                p.ml[unit * G + gt] = make_float2(mine, (__int_as_float(xbuf[gt]) + __int_as_float(xbuf[16 + gt])) +
-                                                            (__int_as_float(xbuf[32 + gt]) + __int_as_float(xbuf[48 + gt])));
+                p.ml[unit * G + gt] = make_float2(mine, (xbuf[gt] + xbuf[16 + gt]) + (xbuf[32 + gt] + xbuf[48 + gt]));
             }
             {
                 const int buf = group * C::NP + (t - 1) % C::NP;
@@ -945,18 +954,28 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
 // dims (and 4 more at head dim 256); the warps' sums in their order.  A result that is not finite is worked out again.
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedArgs a, const float2* ml, const float* part,
-                                                          int spans_most, int align) {
+                                                          int spans_most, int align, const int* said, int ctas) {
     constexpr int V = D / 128;
     __shared__ float4 red[8][32 * V];
     __shared__ PagedRerun again;
     const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int p = paged_pos(__ldg(a.pos + row), a.most, a.page_log);
-    const int spans = row_cut(p, a.win, align, a.hkv).spans;
-    const float vs = a.kv[1].scale ? __ldg(a.kv[1].scale + g) : 1.f;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Plain loads from here on: what they read is written while this kernel is there already.  Blocks without work wait
     // too, so that nothing behind the call starts early.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int p = paged_pos(a.pos[row], a.most, a.page_log);
+    const int spans = row_cut(p, a.win, align, a.hkv).spans;
+    const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
+    if (blockIdx.x == 0) {       // the call's status: what its CTAs have to report
+        int bits = 0;
+        for (int i = t; i < ctas; i += 256) bits |= said[i];
+        const int bad_pos = __syncthreads_or(bits & WA_STATUS_BAD_POS), bad_page = __syncthreads_or(bits & WA_STATUS_BAD_PAGE),
+                  late = __syncthreads_or(bits & WA_STATUS_TIMEOUT), layout = __syncthreads_or(bits & WA_STATUS_LAYOUT);
+        if (t == 0)
+            a.hdr->status = (bad_pos ? WA_STATUS_BAD_POS : 0) | (bad_page ? WA_STATUS_BAD_PAGE : 0) | (late ? WA_STATUS_TIMEOUT : 0) |
+                            (layout ? WA_STATUS_LAYOUT : 0);
+    }
     uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D;
     if (spans == 0) {
         if (t < D / 8) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0u, 0u, 0u, 0u);
@@ -1057,13 +1076,14 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     const int64_t keys = static_cast<int64_t>(most) << page_log;
     int64_t tiles = (keys + kPTile - 1) / kPTile;
     if (win > 0 && (win + align - 2) / kPTile + 1 < tiles) tiles = (static_cast<int64_t>(win) + align - 2) / kPTile + 1;
-    // spans(t) = ceil(t / ceil(t hkv / kFill)) is at most kFill / hkv (rounded up) where that bounds a span, and t / kSpanTiles beyond
-    const int64_t fill = (kFill + hkv - 1) / hkv, least = fill < tiles ? fill : tiles, most_spans = (tiles + kSpanTiles - 1) / kSpanTiles;
-    pl.spans = static_cast<int>(least > most_spans ? least : most_spans);
+    // ceil(t / each) with each >= t hkv / (kFill waves(t)), and waves(t) no less for longer rows
+    const int64_t fill = (kFill * row_waves(tiles, hkv) + hkv - 1) / hkv;
+    pl.spans = static_cast<int>(fill < tiles ? fill : tiles);
     const int64_t heads = static_cast<int64_t>(rows) * hq;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     pl.taken = kHeaderBytes;
-    pl.ml = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
+    pl.said = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
+    pl.ml = pl.said + up((rows / kPagedFewest + 1) * kPagedGrid * sizeof(int));
     pl.part = pl.ml + up(heads * pl.spans * sizeof(float2));
     pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
     return pl;
@@ -1085,6 +1105,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         if (!encode_pages(&p.map[i], &p.at[i], a.kv[i], a, p.align)) return cudaErrorInvalidValue;
     uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
     int* taken = reinterpret_cast<int*>(base + pl.taken);
+    int* said = reinterpret_cast<int*>(base + pl.said);
     p.ml = reinterpret_cast<float2*>(base + pl.ml);
     p.part = reinterpret_cast<float*>(base + pl.part);
     p.spans = pl.spans;
@@ -1092,10 +1113,8 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cudaErrorInvalidValue;
-    paged_clear_kernel<<<1, (a.rows / kPagedFewest / 32 + 1) * 32, 0, s>>>(a.hdr, taken, a.rows / kPagedFewest + 1);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // each kernel is launched while the one before runs, sets itself up and waits for it on the GPU
+    // Each kernel is launched while the one before runs, sets itself up and waits for it on the GPU, the first one for
+    // whatever the stream holds before.
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1103,6 +1122,17 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    const int most_ctas = sms < kPagedGrid ? sms : kPagedGrid;
+    // Up to kInTurn units a CTA go to them in turn, which spares the launch that clears their counter
+    const bool in_turn = static_cast<int64_t>(a.rows) * a.hkv * pl.spans <= static_cast<int64_t>(kInTurn) * most_ctas;
+    cudaError_t e = cudaSuccess;
+    if (!in_turn) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3((a.rows / kPagedFewest / 32 + 1) * 32);
+        e = cudaLaunchKernelEx(&cfg, paged_clear_kernel, taken, a.rows / kPagedFewest + 1);
+        if (e != cudaSuccess) return e;
+    }
+    int ctas = 0;
     e = for_each_paged([&](auto kernel, int d, bool f8, int g, int smem, int most_rows) {
         if (d != a.d || f8 != (a.e4m3 != 0) || g != gp) return cudaSuccess;
         cfg.blockDim = dim3(kPThreads);
@@ -1110,9 +1140,11 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         for (int r0 = 0; r0 < a.rows; r0 += most_rows) {
             p.row0 = r0;
             p.rows = a.rows - r0 < most_rows ? a.rows - r0 : most_rows;
-            p.next_unit = taken + r0 / most_rows;
+            p.next_unit = in_turn ? nullptr : taken + r0 / most_rows;
+            p.said = said + ctas;
             const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
-            cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+            cfg.gridDim = dim3(static_cast<unsigned>(units < most_ctas ? units : most_ctas));
+            ctas += cfg.gridDim.x;
             const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p);
             if (err != cudaSuccess) return err;
         }
@@ -1123,7 +1155,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>, a, const_cast<const float2*>(p.ml),
-                           const_cast<const float*>(p.part), pl.spans, p.align);
+                           const_cast<const float*>(p.part), pl.spans, p.align, const_cast<const int*>(said), ctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
