@@ -27,15 +27,16 @@
 // unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
 //
-// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 416 threads, that streams the keys
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 448 threads, that streams the keys
 // of its units without a break between units:
 //   warps 0, 3  TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and
 //               128 dims.  (One warp for both took 900 cycles a load, where one of 8-bit pages
 //               lands every 700.)
-//   warp 1      allocates tensor memory, issues the products: S of unit 0, S of unit 1, P V of unit 0,
-//               S of unit 2, P V of unit 1, ...; before O += V^T P^T of a row's first
-//               and last tile it zeroes V's slots without a visible key, so that what they hold
-//               never meets a zero probability as 0 * inf
+//   warps 1, 13 MMA issuers of S (a unit ahead of its P V, at most two) and of P V.  Before O += V^T P^T
+//               of a row's first and last tile the second zeroes V's slots without a visible key, so
+//               that what they hold never meets a zero probability as 0 * inf.  (One warp for both took
+//               1,000 cycles a tile, where one of 8-bit pages lands every 1,400.)  Warp 1 allocates
+//               tensor memory.
 //   warp 2      takes units by a counter, looks up their pages, publishes them
 //   warp 12     Q to shared memory, split in two for 8-bit pages
 //   warps 4..7  softmax of even units, a key a thread: the maximum, exponentials, P to shared
@@ -54,7 +55,7 @@ namespace wa {
 namespace {
 
 constexpr int kPTile = 128;          // keys a tile
-constexpr int kPThreads = 416;
+constexpr int kPThreads = 448;
 constexpr int kPUnits = 4;           // unit slots
 constexpr int kFill = 152;           // a row is cut into this many units, or twice as many, .., over its key heads
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
@@ -163,14 +164,15 @@ struct PagedCfg {
     static constexpr int B_SFULL = B_FREE + 2 * NSLOT;           // [group]: all scores of the unit
     static constexpr int B_PFULL = B_SFULL + 2;              // [group][NP]
     static constexpr int B_PVDONE = B_PFULL + 2 * NP;
-    static constexpr int B_QFULL = B_PVDONE + 2 * NP;        // [unit & 1]
+    static constexpr int B_SFREE = B_PVDONE + 2 * NP;        // [group]: the unit's scores have been read
+    static constexpr int B_QFULL = B_SFREE + 2;              // [unit & 1]
     static constexpr int B_QFREE = B_QFULL + 2;
     static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod kPUnits] from here
     static constexpr int B_UFREE = B_UFULL + kPUnits;
     static constexpr int B_UTOOK = B_UFREE + kPUnits;        // the producer has begun the unit
     static constexpr int B_UC = B_UTOOK + kPUnits;           // the unit's c are there (8-bit)
     static constexpr int B_DRAIN = B_UC + kPUnits;
-    static constexpr int NBAR = B_DRAIN + 1;
+    static constexpr int NBAR = B_DRAIN + 2;                 // [S, P V]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base
     static constexpr int SMEM = OFF_MISC + 16;
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -325,8 +327,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     if (tid >= 128 && tid < 128 + C::NBAR) {
         const int i = tid - 128;
         int count = 1;
-        if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // the softmax warps
-        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8;                // producers, MMA, Q, softmax warps
+        if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // a group's softmax warps
+        else if (i >= C::B_SFREE && i < C::B_QFULL) count = 4;
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 9;                // producers, MMA, Q, softmax warps
         mbar_init(BAR(i), count);
         fence_mbar_init();
     }
@@ -441,112 +444,117 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         // the copies in flight land before the block exits, whichever role stopped early
         for (int i = max(0, loads - C::NSLOT); i < loads; ++i)
             if (!mbar_wait(BAR(C::B_FULL + side * C::NSLOT + i % C::NSLOT), static_cast<uint32_t>(i / C::NSLOT) & 1u, status)) break;
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer: the warp together, one lane's instructions
+    } else if (warp == 1 || warp == 13) {
+        // ------------------------------------------------ MMA issuers of S and of P V: the warp together, one lane's instructions
         const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
         const bool leader = paged_elect();
         constexpr uint32_t idS = paged_idesc(F8, 16, 0), idO = paged_idesc(F8, C::PN, 1);
         constexpr uint32_t kTileHi = desc_hi(C::KB * 1024), kSmallHi = desc_hi(1024);
-        int s[2] = {0, 0}, use[2] = {0, 0};       // the next loads' slots, of K and of V
-        auto next_slot = [&](int side) {
-            if (++s[side] == C::NSLOT) {
-                s[side] = 0;
-                ++use[side];
+        int s = warp == 1 ? 0 : C::NSLOT, use = 0;     // the next load's slot
+        const int end = s + C::NSLOT;
+        auto next_slot = [&]() {
+            if (++s == end) {
+                s -= C::NSLOT;
+                ++use;
             }
         };
-        // S^T = K Q^T of a unit's tile
-        auto issue_s = [&](int U, int idx, bool last) -> bool {
-#pragma unroll
-            for (int half = 0; half < C::HV; ++half) {
-                if (!warp_wait(BAR(C::B_FULL + s[0]), use[0] & 1, status)) return false;
-                tc_fence_after();
-                if (leader) {
-                    const uint32_t d = tb + C::s_col(U & 1) + idx * 16, k = desc_lo(SLOT(s[0]), 16),
-                                   q = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES + half * C::KB * C::QN * 128, 16);
-#pragma unroll
-                    for (int set = 0; set < C::QN / 16; ++set)
-#pragma unroll
-                        for (int i = 0; i < 128 / C::KSTEP; ++i) {
-                            const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
-                            const uint32_t b = q + (((i / 4) * C::QN * 128 + set * 2048 + (i % 4) * 32) >> 4);
-                            if (half == 0 && set == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
-                            else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
-                        }
-                    mma_commit(BAR(C::B_FREE + s[0]));
-                    if (last && half == C::HV - 1) {
-                        mma_commit(BAR(C::B_SFULL + (U & 1)));
-                        mma_commit(BAR(C::B_QFREE + (U & 1)));
-                    }
-                }
-                __syncwarp();
-                next_slot(0);
-            }
-            return true;
-        };
-        // O^T += V^T P^T of a tile whose keys `from` .. `to` - 1 are visible; tp: the group's tiles before it
-        auto issue_pv = [&](int group, int tp, bool first, int from, int to) -> bool {
-            const int buf = group * C::NP + tp % C::NP;
-#pragma unroll
-            for (int half = 0; half < C::HV; ++half) {
-                const int at = C::NSLOT + s[1];
-                if (!warp_wait(BAR(C::B_FULL + at), use[1] & 1, status)) return false;
-                if (from > 0 || to < kPTile) {
-                    const int nz = from + kPTile - to;
-                    for (int e = lane; e < nz * C::KB * 8; e += 32) {
-                        const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
-                        st_shared_v4(SLOT(at) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (half == 0 && !warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tp / C::NP) & 1u, status)) return false;
-                tc_fence_after();
-                if (leader) {
-                    const uint32_t v = desc_lo(SLOT(at), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + buf * C::P_BYTES, 16);
-                    const uint32_t d = tb + C::o_col(group) + half * C::PN;
-#pragma unroll
-                    for (int i = 0; i < kPTile / C::KSTEP; ++i) {
-                        const uint32_t a = v + ((i * (C::KSTEP / 8) * C::KB * 1024) >> 4), b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
-                        if (i == 0 && first) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
-                        else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
-                    }
-                    mma_commit(BAR(C::B_FREE + at));
-                    if (half == C::HV - 1) mma_commit(BAR(C::B_PVDONE + buf));
-                }
-                __syncwarp();
-                next_slot(1);
-            }
-            return true;
-        };
-        PUnit x, last;
-        last.nt = 0;
-        int tp[2] = {0, 0};                       // tiles of each group whose products with V are issued
-        auto values = [&](int group) -> bool {
-            bool ok = true;
-            for (int idx = 0; ok && idx < last.nt; ++idx) {
-                const int key0 = last.k0 + idx * kPTile;
-                ok = issue_pv(group, group ? tp[1] : tp[0], idx == 0, max(0, last.lo - key0), min(kPTile, last.p - key0 + 1));
-                if (group) ++tp[1]; else ++tp[0];
-            }
-            return ok;
-        };
-        bool ok = true;
-        for (int U = 0; ok; ++U) {
-            if (!(ok = warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status))) break;
+        PUnit x;
+        auto take = [&](int U) -> bool {
+            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
             read_unit(U, x);
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
             x.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
-            if (x.nt > 0) ok = warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status);
-            for (int idx = 0; ok && idx < x.nt; ++idx) ok = issue_s(U, idx, idx == x.nt - 1);
-            if (ok) ok = values((U - 1) & 1);
-            if (x.nt <= 0) break;
-            last = x;
+            return x.nt > 0;
+        };
+        if (warp == 1) {
+            // S^T = K Q^T
+            bool ok = true;
+            for (int U = 0; ok && take(U); ++U) {
+                // the group's last scores have been read, this unit's queries are there
+                if (U >= 2 && !warp_wait(BAR(C::B_SFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
+                if (!warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status)) break;
+                tc_fence_after();
+                const uint32_t q0 = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES, 16);
+                for (int idx = 0; ok && idx < x.nt; ++idx) {
+                    const uint32_t d = tb + C::s_col(U & 1) + idx * 16;
+#pragma unroll
+                    for (int half = 0; half < C::HV; ++half) {
+                        if (!(ok = warp_wait(BAR(C::B_FULL + s), use & 1, status))) break;
+                        if (leader) {
+                            const uint32_t k = desc_lo(SLOT(s), 16), q = q0 + ((half * C::KB * C::QN * 128) >> 4);
+#pragma unroll
+                            for (int set = 0; set < C::QN / 16; ++set)
+#pragma unroll
+                                for (int i = 0; i < 128 / C::KSTEP; ++i) {
+                                    const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
+                                    const uint32_t b = q + (((i / 4) * C::QN * 128 + set * 2048 + (i % 4) * 32) >> 4);
+                                    if (half == 0 && set == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
+                                    else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                                }
+                            mma_commit(BAR(C::B_FREE + s));
+                        }
+                        __syncwarp();
+                        next_slot();
+                    }
+                }
+                if (ok && leader) {
+                    mma_commit(BAR(C::B_SFULL + (U & 1)));
+                    mma_commit(BAR(C::B_QFREE + (U & 1)));
+                }
+                __syncwarp();
+            }
+        } else {
+            // O^T += V^T P^T
+            bool ok = true;
+            int tp[2] = {0, 0};                   // tiles of each group so far
+            for (int U = 0; ok && take(U); ++U) {
+                const int group = U & 1;
+                int tg = group ? tp[1] : tp[0];
+                for (int idx = 0; ok && idx < x.nt; ++idx, ++tg) {
+                    const int buf = group * C::NP + tg % C::NP;
+                    // keys from .. to - 1 of the tile are visible
+                    const int key0 = x.k0 + idx * kPTile, from = max(0, x.lo - key0), to = min(kPTile, x.p - key0 + 1);
+#pragma unroll
+                    for (int half = 0; half < C::HV; ++half) {
+                        if (!(ok = warp_wait(BAR(C::B_FULL + s), use & 1, status))) break;
+                        if (from > 0 || to < kPTile) {
+                            const int nz = from + kPTile - to;
+                            for (int e = lane; e < nz * C::KB * 8; e += 32) {
+                                const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
+                                st_shared_v4(SLOT(s) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (half == 0) {
+                            if (!(ok = warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tg / C::NP) & 1u, status))) break;
+                            tc_fence_after();
+                        }
+                        if (leader) {
+                            const uint32_t v = desc_lo(SLOT(s), F8 ? 16 : 1024), pp = desc_lo(sbase + C::OFF_P + buf * C::P_BYTES, 16);
+                            const uint32_t d = tb + C::o_col(group) + half * C::PN;
+#pragma unroll
+                            for (int i = 0; i < kPTile / C::KSTEP; ++i) {
+                                const uint32_t a = v + ((i * (C::KSTEP / 8) * C::KB * 1024) >> 4), b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
+                                if (i == 0 && idx == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
+                                else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
+                            }
+                            mma_commit(BAR(C::B_FREE + s));
+                            if (half == C::HV - 1) mma_commit(BAR(C::B_PVDONE + buf));
+                        }
+                        __syncwarp();
+                        next_slot();
+                    }
+                }
+                if (group) tp[1] = tg; else tp[0] = tg;
+            }
         }
         // every product issued has finished before tensor memory can be released
         if (leader) {
-            mma_commit(BAR(C::B_DRAIN));
-            mbar_wait(BAR(C::B_DRAIN), 0, status);
+            const int drain = C::B_DRAIN + (warp == 1 ? 0 : 1);
+            mma_commit(BAR(drain));
+            mbar_wait(BAR(drain), 0, status);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -824,7 +832,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(C::B_PFULL + buf));
+                if (lane == 0) {
+                    mbar_arrive(BAR(C::B_PFULL + buf));
+                    if (idx == x.nt - 1) mbar_arrive(BAR(C::B_SFREE + group));
+                }
             }
             // ---- the unit's result: l over the 128 keys of a tile in a fixed order, O from tensor memory
             const float sum = reduce_each(l, [](float a, float b) { return a + b; });
@@ -874,7 +885,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     if (warp == 1) tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
-// The float64 value of a (row, head), by the whole block: the maximum score, then weights and their sums in key order,
+// The float64 value of 64 of a (row, head)'s dims (from col0), by the whole block: the maximum score, then weights and their sums in key order,
 // 256 keys at a time; a NaN or +inf score settles the output before that.
 struct PagedRerun {
     double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
@@ -882,10 +893,10 @@ struct PagedRerun {
     int64_t vat[kRerunThreads];
 };
 
-__device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int row, int h) {
+__device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int row, int h, int col0) {
     const int t = threadIdx.x, d = a.d, g = h / (a.hq / a.hkv);
     const int p = paged_pos(a.pos[row], a.most, a.page_log), lo = a.win > 0 ? max(0, p - a.win + 1) : 0;
-    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d;
+    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * d + col0;
     const double scale = static_cast<double>(a.scale) * (a.kv[0].scale ? static_cast<double>(a.kv[0].scale[g]) : 1.0);
     if (t < d) {
         sm.qd[t] = bf16_bits_to_f64(static_cast<const uint16_t*>(a.q)[row * a.q_row + static_cast<int64_t>(h) * d + t]);
@@ -918,7 +929,7 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
             }
         }
         if (__syncthreads_or(hit)) {
-            if (t < d) orow[t] = 0x7FC0u;
+            if (t < 64) orow[t] = 0x7FC0u;
             return;
         }
     }
@@ -939,98 +950,215 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
         }
         sm.wb[t] = w;
         __syncthreads();
-        if (t < d) {
+        if (t < 64) {
             const int cnt = min(kRerunThreads, p - base + 1);
             for (int jj = 0; jj < cnt; ++jj)
-                acc = acc + sm.wb[jj] * (sm.vat[jj] < 0 ? 0.0 : static_cast<double>(stored(a.kv[1].base, sm.vat[jj] + t, a.e4m3)));
+                acc = acc + sm.wb[jj] * (sm.vat[jj] < 0 ? 0.0 : static_cast<double>(stored(a.kv[1].base, sm.vat[jj] + col0 + t, a.e4m3)));
         }
         __syncthreads();
     }
     const double l = block_reduce(lloc, false, sm.red);
-    if (t < d) orow[t] = f64_to_bf16_rn(acc / l * (a.kv[1].scale ? static_cast<double>(a.kv[1].scale[g]) : 1.0));
+    if (t < 64) orow[t] = f64_to_bf16_rn(acc / l * (a.kv[1].scale ? static_cast<double>(a.kv[1].scale[g]) : 1.0));
 }
 
-// out = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M): a block a (row, head), a warp every eighth span, a lane 4
-// dims (and 4 more at head dim 256); the warps' sums in their order.  A result that is not finite is worked out again.
+// out = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M).  Both sums run over groups of kMergeGroup spans: a group's
+// in order, then the groups' in order, whichever of the two kernels below takes the row.  A result that is not finite is
+// worked out again.
+constexpr int kMergeGroup = 16;
+
+// The status word of the call, by its first block: what the CTAs have to report.
+__device__ __forceinline__ void paged_report(WsHeader* hdr, const int* said, int ctas) {
+    int bits = 0;
+    for (int i = threadIdx.x; i < ctas; i += 256) bits |= said[i];
+    const int bad_pos = __syncthreads_or(bits & WA_STATUS_BAD_POS), bad_page = __syncthreads_or(bits & WA_STATUS_BAD_PAGE),
+              late = __syncthreads_or(bits & WA_STATUS_TIMEOUT), layout = __syncthreads_or(bits & WA_STATUS_LAYOUT);
+    if (threadIdx.x == 0)
+        hdr->status = (bad_pos ? WA_STATUS_BAD_POS : 0) | (bad_page ? WA_STATUS_BAD_PAGE : 0) | (late ? WA_STATUS_TIMEOUT : 0) |
+                      (layout ? WA_STATUS_LAYOUT : 0);
+}
+
+struct MergeArgs {
+    const float2* ml;
+    const float* part;
+    const int* said;
+    int spans_most, align, ctas;
+};
+
+__device__ __forceinline__ void fma4(float4& x, float w, const float4& o) {
+    x.x = fmaf(w, o.x, x.x);
+    x.y = fmaf(w, o.y, x.y);
+    x.z = fmaf(w, o.z, x.z);
+    x.w = fmaf(w, o.w, x.w);
+}
+__device__ __forceinline__ void add4(float4& x, const float4& o) {
+    x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
+}
+
+// Few rows: a block 64 dims of a (row, head), sixteen threads of 4 dims a group of spans.  The partial results are asked
+// for together with the position that says how many there are, so a call waits for one trip to memory (one row of 131,072
+// keys, 147 spans: 3 us; a warp every eighth span, after the position and the maxima: 5.4).
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedArgs a, const float2* ml, const float* part,
-                                                          int spans_most, int align, const int* said, int ctas) {
-    constexpr int V = D / 128;
-    __shared__ float4 red[8][32 * V];
+__global__ void __launch_bounds__(256) paged_merge_wide_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
+    __shared__ float4 red[16][17];
+    __shared__ float weight[256], sums[256], tops[8], group_den[16];
     __shared__ PagedRerun again;
-    const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G, col0 = blockIdx.y * 64;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, slice = t >> 4, quad = t & 15;
+    const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
+    auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
+    auto fetch = [&](int s) { return reinterpret_cast<const float4*>(x.part + rec(s) * D + col0)[quad]; };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Plain loads from here on: what they read is written while this kernel is there already.  Blocks without work wait
     // too, so that nothing behind the call starts early.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int p = paged_pos(a.pos[row], a.most, a.page_log);
-    const int spans = row_cut(p, a.win, align, a.hkv).spans;
+    const int raw = a.pos[row];
+    float4 ahead[kMergeGroup];      // (of spans that the row does not have: whatever the workspace holds, not used)
+#pragma unroll
+    for (int i = 0; i < kMergeGroup; ++i)
+        if (slice * kMergeGroup + i < x.spans_most) ahead[i] = fetch(slice * kMergeGroup + i);
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (t < x.spans_most) mine = x.ml[rec(t)];
     const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-    if (blockIdx.x == 0) {       // the call's status: what its CTAs have to report
-        int bits = 0;
-        for (int i = t; i < ctas; i += 256) bits |= said[i];
-        const int bad_pos = __syncthreads_or(bits & WA_STATUS_BAD_POS), bad_page = __syncthreads_or(bits & WA_STATUS_BAD_PAGE),
-                  late = __syncthreads_or(bits & WA_STATUS_TIMEOUT), layout = __syncthreads_or(bits & WA_STATUS_LAYOUT);
-        if (t == 0)
-            a.hdr->status = (bad_pos ? WA_STATUS_BAD_POS : 0) | (bad_page ? WA_STATUS_BAD_PAGE : 0) | (late ? WA_STATUS_TIMEOUT : 0) |
-                            (layout ? WA_STATUS_LAYOUT : 0);
-    }
-    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D;
+    const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv).spans;
+    if (blockIdx.x == 0 && blockIdx.y == 0) paged_report(a.hdr, x.said, x.ctas);
+    uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D + col0;
     if (spans == 0) {
-        if (t < D / 8) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < 8) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * spans_most;
-    auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
-    float M = -INFINITY;
-    for (int s = lane; s < spans; s += 32) M = fmaxf(M, ml[rec(s)].x);
+    float M = t < spans ? mine.x : -INFINITY;
+    for (int s = t + 256; s < spans; s += 256) M = fmaxf(M, x.ml[rec(s)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    float den = 0.f;
-    float4 num[V];
+    if (lane == 0) tops[warp] = M;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, tops[w]);
+    float den = 0.f, o = 0.f;        // of thread t < 64: dim t
+    for (int s0 = 0; s0 < spans; s0 += 256) {      // sixteen groups at a time
+        if (s0 + t < spans) {
+            const float2 e = s0 == 0 ? mine : x.ml[rec(s0 + t)];
+            weight[t] = exp2f(e.x - M);
+            sums[t] = e.y;
+        }
+        __syncthreads();
+        const int end = min(spans - s0, 256), s1 = slice * kMergeGroup;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float d = 0.f;
+        if (s0 > 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) num[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < spans; s0 += 32) {
-        float w = 0.f;
-        if (s0 + lane < spans) {
-            const float2 e = ml[rec(s0 + lane)];
-            w = exp2f(e.x - M);
-            den = fmaf(w, e.y, den);
+            for (int i = 0; i < kMergeGroup; ++i)
+                if (s1 + i < end) ahead[i] = fetch(s0 + s1 + i);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = s0 + warp + 8 * i;
-            const float ws = __shfl_sync(0xFFFFFFFFu, w, warp + 8 * i);
-            if (s >= spans) continue;
+        for (int i = 0; i < kMergeGroup; ++i)
+            if (s1 + i < end) {
+                fma4(num, weight[s1 + i], ahead[i]);
+                d = fmaf(weight[s1 + i], sums[s1 + i], d);
+            }
+        red[slice][quad] = num;
+        if (quad == 0) group_den[slice] = d;
+        __syncthreads();
+        if (t < 64)
+            for (int k = 0; k * kMergeGroup < end; ++k) {
+                o += reinterpret_cast<const float*>(red)[k * 68 + t];
+                den += group_den[k];
+            }
+        __syncthreads();
+    }
+    bool bad = false;
+    if (t < 64) {
+        o = o / den * vs;
+        bad = !isfinite(o);
+        orow[t] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+    }
+    if (__syncthreads_or(bad)) paged_rerun(a, again, row, h, col0);
+}
+
+// Many rows: a warp a (row, head).  (The kernel above takes 2 us a block whatever its row has: 48 rows of 32 heads of 256
+// over a window, 9 spans each, 18 us; this one 4.)
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
+    constexpr int V = D / 128, AHEAD = 8 / V;
+    __shared__ PagedRerun again;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x * 8 + warp, items = a.rows * a.hq;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // as above
+    if (blockIdx.x == 0) paged_report(a.hdr, x.said, x.ctas);
+    bool bad = false;
+    if (item < items) {
+        const int row = item / a.hq, h = item % a.hq, G = a.hq / a.hkv, g = h / G;
+        const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
+        auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
+        const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
+        const int raw = a.pos[row];
+        float2 mine = make_float2(-INFINITY, 0.f);
+        if (lane < x.spans_most) mine = x.ml[rec(lane)];
+        const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv).spans;
+        uint2* orow = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D);
+        float M = lane < spans ? mine.x : -INFINITY;
+        for (int s = lane + 32; s < spans; s += 32) M = fmaxf(M, x.ml[rec(s)].x);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float4 o = reinterpret_cast<const float4*>(part + rec(s) * D)[v * 32 + lane];
-                num[v].x = fmaf(ws, o.x, num[v].x);
-                num[v].y = fmaf(ws, o.y, num[v].y);
-                num[v].z = fmaf(ws, o.z, num[v].z);
-                num[v].w = fmaf(ws, o.w, num[v].w);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        float den = 0.f, d = 0.f, w = 0.f;
+        float4 num[V], sum[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) num[v] = sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        static_assert(kMergeGroup % AHEAD == 0, "loads of a group");
+        for (int s0 = 0; s0 < spans; s0 += AHEAD) {
+            if ((s0 & 31) == 0) {
+                if (s0 > 0) mine = s0 + lane < spans ? x.ml[rec(s0 + lane)] : make_float2(-INFINITY, 0.f);
+                w = exp2f(mine.x - M);
+            }
+            float4 o[AHEAD][V];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (s0 + i < spans) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o[i][v] = reinterpret_cast<const float4*>(x.part + rec(s0 + i) * D)[v * 32 + lane];
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float wi = __shfl_sync(0xFFFFFFFFu, w, (s0 + i) & 31), li = __shfl_sync(0xFFFFFFFFu, mine.y, (s0 + i) & 31);
+                if (s0 + i < spans) {
+                    d = fmaf(wi, li, d);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) fma4(num[v], wi, o[i][v]);
+                }
+            }
+            if ((s0 + AHEAD) % kMergeGroup == 0 || s0 + AHEAD >= spans) {       // the group's end
+                den += d;
+                d = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    add4(sum[v], num[v]);
+                    num[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
             }
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
-#pragma unroll
-    for (int v = 0; v < V; ++v) red[warp][v * 32 + lane] = num[v];
-    __syncthreads();
-    bool bad = false;
-    if (t < 32 * V) {
-        float4 o = red[0][t];
-        for (int w = 1; w < (spans < 8 ? spans : 8); ++w) {
-            const float4 x = red[w][t];
-            o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        for (int v = 0; v < V; ++v) {
+            float4 r = sum[v];
+            if (spans > 0) {
+                r.x = r.x / den * vs; r.y = r.y / den * vs; r.z = r.z / den * vs; r.w = r.w / den * vs;
+                bad |= !(isfinite(r.x) && isfinite(r.y) && isfinite(r.z) && isfinite(r.w));
+            }
+            orow[v * 32 + lane] = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
         }
-        o.x = o.x / den * vs; o.y = o.y / den * vs; o.z = o.z / den * vs; o.w = o.w / den * vs;
-        bad = !(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w));
-        reinterpret_cast<uint2*>(orow)[t] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     }
-    if (__syncthreads_or(bad)) paged_rerun(a, again, row, h);
+    __shared__ int again_for[8];
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane == 0) again_for[warp] = bad;
+    if (!__syncthreads_or(bad)) return;
+    for (int i = 0; i < 8; ++i) {
+        if (!again_for[i]) continue;
+        for (int c = 0; c < D; c += 64) {
+            paged_rerun(a, again, (blockIdx.x * 8 + i) / a.hq, (blockIdx.x * 8 + i) % a.hq, c);
+            __syncthreads();
+        }
+    }
 }
+constexpr int kMergeWide = 512;      // (row, head) pairs below which the first of them runs
 
 bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -1151,11 +1279,14 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         return cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * a.hq);
+    MergeArgs m{p.ml, p.part, said, pl.spans, p.align, ctas};
+    const int pairs = a.rows * a.hq;
+    cfg.gridDim = pairs < kMergeWide ? dim3(pairs, a.d / 64) : dim3((pairs + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>, a, const_cast<const float2*>(p.ml),
-                           const_cast<const float*>(p.part), pl.spans, p.align, const_cast<const int*>(said), ctas);
+    auto merge = pairs < kMergeWide ? (a.d == 256 ? paged_merge_wide_kernel<256> : paged_merge_wide_kernel<128>)
+                                    : (a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>);
+    e = cudaLaunchKernelEx(&cfg, merge, a, m);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -128,6 +128,19 @@ def test_a_rows_bits_are_its_own(wa, bits_):
     assert same(got, want[turn])
 
 
+@pytest.mark.parametrize("d, hq, hkv", [(128, 16, 2), (256, 24, 4)])
+def test_a_rows_bits_in_batches_of_many_rows(wa, d, hq, hkv):
+    """A row of many spans alone, and among enough rows that others join its spans."""
+    lengths = [20000, 700, 0, 2500] + [33] * 60
+    c = wa_synth.paged_case(lengths, hq, hkv, d, 64, seed=53, device="cuda", outside="keep")
+    want = call(wa, c)
+    for r in (0, 1, 2, 3, 63):
+        one = dict(c, q=c["q"][r:r + 1], table=c["table"][r:r + 1], pos=c["pos"][r:r + 1])
+        assert same(call(wa, one)[0], want[r]), r
+    r = check.compare(bits(want[:5]), reference(c, 1.0, rows=range(5)), TOL)
+    assert r["ok"], r
+
+
 def test_strided_queries_and_outputs_and_shared_pages(wa):
     """Queries inside projection rows, outputs inside a wider buffer, and two sequences with a common prefix."""
     c = wa_synth.paged_case([200, 200], 8, 4, 128, 64, seed=45, device="cuda")
