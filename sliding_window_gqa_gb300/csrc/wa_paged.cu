@@ -254,6 +254,8 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
 
+__device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" :: "l"(x)); }
+
 // A softmax group's barrier, alone and as a vote.
 __device__ __forceinline__ void group_sync(int group) { named_bar_sync(1 + group, 128); }
 __device__ __forceinline__ bool group_any(int group, bool x) {
@@ -336,6 +338,19 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     if (warp == 1) {
         tmem_alloc(smem_u32(smem + C::OFF_MISC), C::TMEM_COLS);
         tmem_relinquish();
+    }
+    // The queries and the table, a line a thread, into L2: once the keys stream, a read that has to go to memory waits
+    // behind them (a batch of 64 rows, 32/8 heads of 128: 309 us without this, 301 with it).
+    {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * kPThreads + tid;
+        const int q_lines = p.a.hq * D / 64, t_lines = (p.a.most + 31) / 32;
+        const int64_t q_all = static_cast<int64_t>(p.rows) * q_lines, t_all = static_cast<int64_t>(p.rows) * t_lines;
+        if (i < q_all) {
+            prefetch_l2(static_cast<const uint16_t*>(p.a.q) + (p.row0 + i / q_lines) * p.a.q_row + i % q_lines * 64);
+        } else if (i < q_all + t_all) {
+            const int64_t e = i - q_all;
+            prefetch_l2(p.a.table + (p.row0 + e / t_lines) * p.a.table_row + e % t_lines * 32);
+        }
     }
     for (int e = tid; e < (2 * C::Q_BYTES + 2 * C::NP * C::P_BYTES) / 16; e += kPThreads)
         st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
@@ -618,89 +633,110 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             k = __shfl_sync(0xFFFFFFFFu, nk, 0) + static_cast<int>(gridDim.x);
         }
     } else if (warp == 12) {
-        // ------------------------------------------------ Q
+        // ------------------------------------------------ Q: four heads at a time, in a loop, which a unit -1 of no heads
+        // goes through first: its code comes in while nothing else is asked of the memory.  (All heads' code in a row, 16
+        // heads split in two, came line by line behind the first keys: 6 us to the first product.)
         constexpr int EL = D / 32;                // values a lane and head
         PUnit x;
-        for (int U = 0;; ++U) {
-            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
-            read_unit(U, x);
-            if (x.nt <= 0) break;
+        x.row = x.g = 0;
+        for (int U = -1;; ++U) {
+            int live = 0;                         // heads (the buffer's other rows: zeros)
+            if (U >= 0) {
+                if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
+                read_unit(U, x);
+                if (x.nt <= 0) break;
+                live = G;
+            }
             const uint16_t* q = static_cast<const uint16_t*>(p.a.q) + x.row * p.a.q_row + static_cast<int64_t>(x.g) * G * D + lane * EL;
-            uint32_t raw[GP][EL / 2];
+            uint32_t raw[4][EL / 2];
+            auto fetch = [&](int h0) {
 #pragma unroll
-            for (int h = 0; h < GP; ++h) {
+                for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int e = 0; e < EL / 2; ++e) raw[h][e] = 0u;
-                if (h < G) {
-                    if constexpr (EL == 4) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(q + h * D);
-                        raw[h][0] = v.x; raw[h][1] = v.y;
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4*>(q + h * D);
-                        raw[h][0] = v.x; raw[h][1] = v.y; raw[h][2] = v.z; raw[h][3] = v.w;
+                    for (int e = 0; e < EL / 2; ++e) raw[i][e] = 0u;
+                    if (h0 + i < live) {
+                        if constexpr (EL == 4) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(q + (h0 + i) * D);
+                            raw[i][0] = v.x; raw[i][1] = v.y;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4*>(q + (h0 + i) * D);
+                            raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
+                        }
                     }
                 }
-            }
+            };
+            fetch(0);
             float c = p.a.scale * 1.4426950408889634f;
             if constexpr (F8) c *= p.a.kv[0].scale ? p.a.kv[0].scale[x.g] : 1.f;
             const bool neg = c < 0.f;             // the sign goes into Q, exactly
             // the buffer's last unit's S have been worked out
             if (U >= 2 && !warp_wait(BAR(C::B_QFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
             const uint32_t dst = sbase + C::OFF_Q + (U & 1) * C::Q_BYTES;
+#pragma unroll 1
+            for (int h0 = 0; h0 < GP; h0 += 4) {
+                uint32_t now[4][EL / 2];
 #pragma unroll
-            for (int h = 0; h < GP; ++h) {
-                if (h >= G) break;
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < EL / 2; ++e) now[i][e] = raw[i][e];
+                if (h0 + 4 < GP) fetch(h0 + 4);
                 if constexpr (!F8) {
                     // dims lane * EL ..: block of 64 dims, 16-byte chunk, swizzled by the row
                     const int el = lane * EL, chunk = (el & 63) * 2;
-                    const uint32_t at = dst + (el >> 6) * (C::QN * 128) + (h >> 3) * 1024 + (h & 7) * 128 + (chunk ^ ((h & 7) << 4));
                     const uint32_t flip = neg ? 0x80008000u : 0u;
 #pragma unroll
-                    for (int e = 0; e < EL / 2; ++e) st_shared_u32(at + 4 * e, raw[h][e] ^ flip);
+                    for (int i = 0; i < 4; ++i) {
+                        const int h = h0 + i;
+                        const uint32_t at = dst + (el >> 6) * (C::QN * 128) + (h >> 3) * 1024 + (h & 7) * 128 + (chunk ^ ((h & 7) << 4));
+#pragma unroll
+                        for (int e = 0; e < EL / 2; ++e) st_shared_u32(at + 4 * e, now[i][e] ^ flip);
+                    }
                 } else {
-                    uint32_t top = 0;
+                    // the largest value of each head (as bits: infinities and NaN are larger than any other)
+                    float top[4];
 #pragma unroll
-                    for (int e = 0; e < EL / 2; ++e) {
-                        top = max(top, (raw[h][e] << 16) & 0x7FFFFFFFu);
-                        top = max(top, raw[h][e] & 0x7FFF0000u);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b = 0;
+#pragma unroll
+                        for (int e = 0; e < EL / 2; ++e) b = max(b, max((now[i][e] << 16) & 0x7FFFFFFFu, now[i][e] & 0x7FFF0000u));
+                        top[i] = __uint_as_float(b);
                     }
-                    top = __reduce_max_sync(0xFFFFFFFFu, top);
-                    // 2^k brings the largest value to [128, 256) (k at most 120: what is smaller than 2^-113 loses bits)
-                    const int k = min(134 - static_cast<int>(top >> 23), 120);
-                    const float f = __int_as_float((k + 127) << 23) * (neg ? -1.f : 1.f);
-                    const bool fine = top < 0x7F800000u;
-                    uint32_t hi[EL / 4], lo[EL / 4];
+                    const float most = reduce_each(top, [](float a, float b) {
+                        return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+                    });
 #pragma unroll
-                    for (int w = 0; w < EL / 4; ++w) {
-                        float v[4], r[4];
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bits = __float_as_uint(__shfl_sync(0xFFFFFFFFu, most, 8 * i));
+                        // 2^k brings the largest value to [128, 256) (k at most 120: what is smaller than 2^-113 loses bits)
+                        const int h = h0 + i, k = min(134 - static_cast<int>(bits >> 23), 120);
+                        const float f = __int_as_float((k + 127) << 23) * (neg ? -1.f : 1.f);
+                        const bool fine = bits < 0x7F800000u;
+                        const int el = lane * EL, low = h + C::lo_row();
+                        const uint32_t block = dst + (el >> 7) * (C::QN * 128);
+                        const uint32_t ah = block + (h >> 3) * 1024 + (h & 7) * 128 + ((el & 127) ^ ((h & 7) << 4));
+                        const uint32_t al = block + (low >> 3) * 1024 + (low & 7) * 128 + ((el & 127) ^ ((low & 7) << 4));
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            v[2 * e] = __uint_as_float(raw[h][2 * w + e] << 16) * f;
-                            v[2 * e + 1] = __uint_as_float(raw[h][2 * w + e] & 0xFFFF0000u) * f;
+                        for (int w = 0; w < EL / 4; ++w) {
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                v[2 * e] = __uint_as_float(now[i][2 * w + e] << 16) * f;
+                                v[2 * e + 1] = __uint_as_float(now[i][2 * w + e] & 0xFFFF0000u) * f;
+                            }
+                            const uint32_t a = e4m3_pair(v[0], v[1]), b = e4m3_pair(v[2], v[3]);
+                            const float2 fa = e4m3_pair_f32(a), fb = e4m3_pair_f32(b);
+                            const uint32_t rest = e4m3_pair(v[0] - fa.x, v[1] - fa.y) | (e4m3_pair(v[2] - fb.x, v[3] - fb.y) << 16);
+                            st_shared_u32(ah + 4 * w, fine ? a | (b << 16) : 0x7F7F7F7Fu);      // NaN: the head is computed again
+                            st_shared_u32(al + 4 * w, fine ? rest : 0u);
                         }
-                        const uint32_t a = e4m3_pair(v[0], v[1]), b = e4m3_pair(v[2], v[3]);
-                        const float2 fa = e4m3_pair_f32(a), fb = e4m3_pair_f32(b);
-                        r[0] = v[0] - fa.x; r[1] = v[1] - fa.y;
-                        r[2] = v[2] - fb.x; r[3] = v[3] - fb.y;
-                        hi[w] = fine ? a | (b << 16) : 0x7F7F7F7Fu;          // NaN: the head is computed again
-                        lo[w] = e4m3_pair(r[0], r[1]) | (e4m3_pair(r[2], r[3]) << 16);
+                        if (lane == i)
+                            reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U & (kPUnits - 1)) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
                     }
-                    const int el = lane * EL, low = h + C::lo_row();
-                    const uint32_t block = dst + (el >> 7) * (C::QN * 128);
-                    const uint32_t ah = block + (h >> 3) * 1024 + (h & 7) * 128 + ((el & 127) ^ ((h & 7) << 4));
-                    const uint32_t al = block + (low >> 3) * 1024 + (low & 7) * 128 + ((el & 127) ^ ((low & 7) << 4));
-#pragma unroll
-                    for (int w = 0; w < EL / 4; ++w) {
-                        st_shared_u32(ah + 4 * w, hi[w]);
-                        st_shared_u32(al + 4 * w, fine ? lo[w] : 0u);
-                    }
-                    if (lane == 0)
-                        reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % kPUnits) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && U >= 0) {
                 mbar_arrive(BAR(C::B_QFULL + (U & 1)));
                 if constexpr (F8) mbar_arrive(BAR(C::B_UC + U % kPUnits));
                 mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
@@ -795,40 +831,48 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     s[h] = vis ? ex2(s[h] - m[h]) : 0.f;
                     l[h] += s[h];
                 }
-                // the buffer's last product is done
-                const int buf = group * C::NP + t % C::NP;
-                if (t >= C::NP) wait(C::B_PVDONE + buf, static_cast<uint32_t>(t / C::NP - 1) & 1u);
-                const uint32_t pb = sbase + C::OFF_P + buf * C::P_BYTES;
-                // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row
-                if constexpr (F8) {
-                    auto at = [&](int n) { return pb + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4)); };
+                // the parts of two heads each
+                uint32_t part[GP / 2][C::PARTS];
 #pragma unroll
-                    for (int h = 0; h < GP; h += 2) {
+                for (int h = 0; h < GP; h += 2) {
+                    if constexpr (F8) {
                         float a = s[h], b = s[h + 1];
 #pragma unroll
-                        for (int part = 0; part < 3; ++part) {
-                            const uint32_t e = e4m3_pair(a, b);
-                            st_shared_u8(at(part * GP + h), e);
-                            st_shared_u8(at(part * GP + h + 1), e >> 8);
-                            if (part < 2) {
+                        for (int i = 0; i < 3; ++i) {
+                            const uint32_t e = part[h / 2][i] = e4m3_pair(a, b);
+                            if (i < 2) {
                                 const float2 f = e4m3_pair_f32(e);
                                 a = (a - f.x) * 32.f;
                                 b = (b - f.y) * 32.f;
                             }
                         }
-                    }
-                } else {
-                    auto at = [&](int n) { return pb + (pk >> 6) * C::P_CHUNK + (n >> 3) * 1024 + (n & 7) * 128 + (((pk & 63) * 2) ^ ((n & 7) << 4)); };
-#pragma unroll
-                    for (int h = 0; h < GP; h += 2) {
-                        const uint32_t hi = pack_bf16(s[h], s[h + 1]);
-                        const uint32_t lo = pack_bf16(s[h] - __uint_as_float(hi << 16), s[h + 1] - __uint_as_float(hi & 0xFFFF0000u));
-                        st_shared_u16(at(h), hi);
-                        st_shared_u16(at(h + 1), hi >> 16);
-                        st_shared_u16(at(GP + h), lo);
-                        st_shared_u16(at(GP + h + 1), lo >> 16);
+                    } else {
+                        const uint32_t hi = part[h / 2][0] = pack_bf16(s[h], s[h + 1]);
+                        part[h / 2][1] = pack_bf16(s[h] - __uint_as_float(hi << 16), s[h + 1] - __uint_as_float(hi & 0xFFFF0000u));
                     }
                 }
+                // the buffer's last product is done
+                const int buf = group * C::NP + t % C::NP;
+                if (t >= C::NP) wait(C::B_PVDONE + buf, static_cast<uint32_t>(t / C::NP - 1) & 1u);
+                const uint32_t pb = sbase + C::OFF_P + buf * C::P_BYTES;
+                // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row
+                auto at = [&](int n) {
+                    if constexpr (F8) return pb + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4));
+                    else return pb + (pk >> 6) * C::P_CHUNK + (n >> 3) * 1024 + (n & 7) * 128 + (((pk & 63) * 2) ^ ((n & 7) << 4));
+                };
+#pragma unroll
+                for (int h = 0; h < GP; h += 2)
+#pragma unroll
+                    for (int i = 0; i < C::PARTS; ++i) {
+                        const uint32_t v = part[h / 2][i];
+                        if constexpr (F8) {
+                            st_shared_u8(at(i * GP + h), v);
+                            st_shared_u8(at(i * GP + h + 1), v >> 8);
+                        } else {
+                            st_shared_u16(at(i * GP + h), v);
+                            st_shared_u16(at(i * GP + h + 1), v >> 16);
+                        }
+                    }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
