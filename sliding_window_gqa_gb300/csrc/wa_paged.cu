@@ -27,7 +27,7 @@
 // unit, one long row ended in 60 us of one SM reading what the others had left.)
 // Nothing in a unit depends on the other rows, so neither do the bits.
 //
-// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 448 threads, that streams the keys
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 512 threads, that streams the keys
 // of its units without a break between units:
 //   warps 0, 3  TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and
 //               128 dims.  (One warp for both took 900 cycles a load, where one of 8-bit pages
@@ -38,7 +38,8 @@
 //               1,000 cycles a tile, where one of 8-bit pages lands every 1,400.)  Warp 1 allocates
 //               tensor memory.
 //   warp 2      takes units by a counter, looks up their pages, publishes them
-//   warp 12     Q to shared memory, split in two for 8-bit pages
+//   warps 12,   Q to shared memory, split in two for 8-bit pages
+//   14, 15
 //   warps 4..7  softmax of even units, a key a thread: the maximum, exponentials, P to shared
 //   and 8..11   memory, the unit's result; of odd units.  One group's chain (a unit's ends, 2,500
 //               cycles) runs beside the other's.
@@ -55,7 +56,8 @@ namespace wa {
 namespace {
 
 constexpr int kPTile = 128;          // keys a tile
-constexpr int kPThreads = 448;
+constexpr int kPThreads = 512;
+constexpr int kQWarps = 3;           // 12, 14, 15
 constexpr int kPUnits = 4;           // unit slots
 constexpr int kFill = 152;           // a row is cut into this many units, or twice as many, .., over its key heads
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
@@ -331,7 +333,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int count = 1;
         if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // a group's softmax warps
         else if (i >= C::B_SFREE && i < C::B_QFULL) count = 4;
-        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 9;                // producers, MMA, Q, softmax warps
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8 + kQWarps;       // producers, MMA, Q, softmax warps
+        else if (i >= C::B_QFULL && i < C::B_QFREE) count = kQWarps;
+        else if (i >= C::B_UC && i < C::B_DRAIN) count = kQWarps;
         mbar_init(BAR(i), count);
         fence_mbar_init();
     }
@@ -632,11 +636,12 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (lane == 0) nk = atomicAdd(p.next_unit, 1);
             k = __shfl_sync(0xFFFFFFFFu, nk, 0) + static_cast<int>(gridDim.x);
         }
-    } else if (warp == 12) {
+    } else if (warp >= 12) {
         // ------------------------------------------------ Q: four heads at a time, in a loop, which a unit -1 of no heads
         // goes through first: its code comes in while nothing else is asked of the memory.  (All heads' code in a row, 16
         // heads split in two, came line by line behind the first keys: 6 us to the first product.)
         constexpr int EL = D / 32;                // values a lane and head
+        const int turn = warp == 12 ? 0 : warp - 13;
         PUnit x;
         x.row = x.g = 0;
         for (int U = -1;; ++U) {
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     }
                 }
             };
-            fetch(0);
+            fetch(4 * turn);
             float c = p.a.scale * 1.4426950408889634f;
             if constexpr (F8) c *= p.a.kv[0].scale ? p.a.kv[0].scale[x.g] : 1.f;
             const bool neg = c < 0.f;             // the sign goes into Q, exactly
@@ -673,13 +678,13 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (U >= 2 && !warp_wait(BAR(C::B_QFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
             const uint32_t dst = sbase + C::OFF_Q + (U & 1) * C::Q_BYTES;
 #pragma unroll 1
-            for (int h0 = 0; h0 < GP; h0 += 4) {
+            for (int h0 = 4 * turn; h0 < GP; h0 += 4 * kQWarps) {
                 uint32_t now[4][EL / 2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < EL / 2; ++e) now[i][e] = raw[i][e];
-                if (h0 + 4 < GP) fetch(h0 + 4);
+                if (h0 + 4 * kQWarps < GP) fetch(h0 + 4 * kQWarps);
                 if constexpr (!F8) {
                     // dims lane * EL ..: block of 64 dims, 16-byte chunk, swizzled by the row
                     const int el = lane * EL, chunk = (el & 63) * 2;
