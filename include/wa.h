@@ -463,7 +463,7 @@ typedef struct wa_pages {
  * A token that is left out has nothing written, q_out included.  Two tokens of
  * one call must not share a place of the cache (one sequence and position, or
  * sequences whose tables name one page there).  page_size is a power of two from
- * 16 to 256; hq % hkv == 0, hq / hkv <= 16; no two elements of the k pages, and of
+ * 16 to 256; hq % hkv == 0, hq / hkv <= 16, hq + 2 hkv <= 65535; no two elements of the k pages, and of
  * the v pages, may share memory; pointers 16-byte aligned, strides of the pages
  * multiples of 16 bytes, others of 8 elements.  Returns WA_EINVAL otherwise.
  */

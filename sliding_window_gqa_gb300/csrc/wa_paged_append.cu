@@ -33,8 +33,19 @@ constexpr int kStatusBlockTokens = 2048;
 
 struct AppendParams {
     PagedAppendArgs a;
-    int warps_per_token, status_block;
+    int status_block;
 };
+
+// Two products, and two fused multiply-adds, an instruction.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -90,8 +101,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     constexpr int L = D / 16;              // lanes a head
     constexpr int P = 32 / L;              // heads a pass
     constexpr int HPW = P * kAppendPasses; // heads a warp
+    constexpr int NA = D / 64;             // pairs whose angle a lane works out
     if constexpr (CACHE) {
         if (p.status_block && blockIdx.x == gridDim.x - 1) {
+            if (blockIdx.y > 0) return;
             int bad = 0, page;
             for (int t = threadIdx.x; t < a.n; t += kAppendWarps * 32) bad |= place(a, t, a.pos[t], page);
             const int where = __syncthreads_or(bad & WA_STATUS_BAD_POS), which = __syncthreads_or(bad & WA_STATUS_BAD_PAGE);
@@ -99,10 +112,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
             return;
         }
     }
-    const int64_t wid = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    if (wid >= static_cast<int64_t>(a.n) * p.warps_per_token) return;     // warp-uniform
+    const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (static_cast<int>(threadIdx.x) >> 5), first = static_cast<int>(blockIdx.y) * HPW;
+    if (t >= a.n) return;                  // warp-uniform
     const int lane = threadIdx.x & 31, li = lane % L, hp = lane / L;
-    const int t = static_cast<int>(wid / p.warps_per_token), first = static_cast<int>(wid % p.warps_per_token) * HPW;
     const int nqk = a.hq + a.hkv, heads = nqk + a.hkv;
     const int pos = a.pos[t];
     const bool turns = li < a.dims / 16;
@@ -128,16 +140,25 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
         }
         if (pos < 0 || (pos >> a.page_log) >= a.most) return;
     }
+    // Angles: a lane works out NA pairs of the token, and takes the eight of its dims from where they are.
     float c[8], s[8];
-    if (turns && first < nqk) {
+    if (a.dims > 0 && first < nqk) {
+        float mc[NA], ms[NA];
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = NA * lane + i;
+            const float w = 2 * j < a.dims ? a.inv_freq[j] : 0.f;
+            const uint64_t turn = turn_fraction(w) * static_cast<uint64_t>(static_cast<int64_t>(pos));
+            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &ms[i], &mc[i]);
+            const float f = fabsf(w) < 16.f ? a.factor : NAN;
+            mc[i] *= f;
+            ms[i] *= a.inverse ? -f : f;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float w = a.inv_freq[8 * li + e];
-            const uint64_t turn = turn_fraction(w) * static_cast<uint64_t>(static_cast<int64_t>(pos));
-            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s[e], &c[e]);
-            const float f = fabsf(w) < 16.f ? a.factor : NAN;
-            c[e] *= f;
-            s[e] *= a.inverse ? -f : f;
+            const int from = li * (8 / NA) + e / NA;
+            c[e] = __shfl_sync(0xFFFFFFFFu, mc[e % NA], from);
+            s[e] = __shfl_sync(0xFFFFFFFFu, ms[e % NA], from);
         }
     }
     const int64_t slot = CACHE ? pos & ((1 << a.page_log) - 1) : 0;
@@ -151,17 +172,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
         if (turns && h < nqk) {
             if (a.layout == WA_ROTARY_HALF) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xa = x[e], xb = x[8 + e];
-                    x[e] = fmaf(xa, c[e], -xb * s[e]);
-                    x[8 + e] = fmaf(xb, c[e], xa * s[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    float u0, u1, v0, v1;
+                    mul2(u0, u1, x[8 + e], x[9 + e], -s[e], -s[e + 1]);
+                    mul2(v0, v1, x[e], x[e + 1], s[e], s[e + 1]);
+                    fma2(x[e], x[e + 1], x[e], x[e + 1], c[e], c[e + 1], u0, u1);
+                    fma2(x[8 + e], x[9 + e], x[8 + e], x[9 + e], c[e], c[e + 1], v0, v1);
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float xa = x[2 * e], xb = x[2 * e + 1];
-                    x[2 * e] = fmaf(xa, c[e], -xb * s[e]);
-                    x[2 * e + 1] = fmaf(xb, c[e], xa * s[e]);
+                    float u0, u1;
+                    mul2(u0, u1, x[2 * e + 1], x[2 * e], -s[e], s[e]);
+                    fma2(x[2 * e], x[2 * e + 1], x[2 * e], x[2 * e + 1], c[e], c[e], u0, u1);
                 }
             }
         }
@@ -194,16 +217,13 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     AppendParams p{};
     p.a = a;
     const int hpw = 32 / (a.d / 16) * kAppendPasses;
-    p.warps_per_token = (a.hq + 2 * a.hkv + hpw - 1) / hpw;
     const bool cache = a.hkv > 0;
     p.status_block = cache && a.n <= kStatusBlockTokens;
     if (cache && !p.status_block) {
         const cudaError_t e = cudaMemsetAsync(a.hdr, 0, sizeof(int), s);
         if (e != cudaSuccess) return e;
     }
-    const int64_t blocks = (static_cast<int64_t>(a.n) * p.warps_per_token + kAppendWarps - 1) / kAppendWarps + p.status_block;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(blocks);
+    const dim3 grid((a.n - 1) / kAppendWarps + 1 + p.status_block, (a.hq + 2 * a.hkv + hpw - 1) / hpw);
     constexpr int threads = kAppendWarps * 32;
     if (a.d == 256) {
         if (!cache) append_kernel<256, false, false><<<grid, threads, 0, s>>>(p);
