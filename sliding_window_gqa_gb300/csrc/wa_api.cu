@@ -456,7 +456,7 @@ int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int
                     const wa_pages* cache, const wa_rotary* rot, int64_t src_tok, int64_t q_tok, void* q_out,
                     void* ws, size_t ws_bytes, void* stream) {
     if (!src || !pos || !q_out || n <= 0 || !pages_ok(cache, hq, 0) || !rotary_ok(rot, cache->d)) return WA_EINVAL;
-    if (hq + 2 * cache->hkv > 65535) return WA_EINVAL;
+    if (hq + 2 * cache->hkv > 65535) return WA_EINVAL;     // (a grid's second dimension)
     if ((!row && n > cache->rows) || cache->k == cache->v) return WA_EINVAL;
     if (!aligned16(src) || !aligned16(q_out) || ((src_tok | q_tok) & 7)) return WA_EINVAL;
     const int64_t width = static_cast<int64_t>(hq + 2 * cache->hkv) * cache->d;

@@ -12,8 +12,8 @@
 //
 // HBM-bound: a head is served by L = d / 16 lanes of two 16-byte pieces each, so
 // that both halves of a pair sit in one lane for either layout, a warp takes P =
-// 32 / L heads a pass and kAppendPasses passes of one token, all loads issued
-// before the angles are worked out (once a warp, whatever its heads).
+// 32 / L heads a pass and PASSES passes of one token, all loads issued before the
+// angles are worked out, two or four a lane, which the others fetch by shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -25,11 +25,10 @@ namespace wa {
 
 namespace {
 
-constexpr int kAppendWarps = 8;
-constexpr int kAppendPasses = 4;
-// Up to this many tokens one more block checks them all and writes the status word; beyond, the word is cleared
-// before the launch and a warp a token reports.
-constexpr int kStatusBlockTokens = 2048;
+constexpr int kAppendWarps = 4;       // (of 8, blocks ended unevenly: rope of 8,192 x 40 heads of 128 30.2 us, with 4 26.5)
+// Up to this many tokens one more block checks them all and writes the status word; beyond, a kernel of its own does,
+// which runs beside this one.
+constexpr int kStatusBlockTokens = 1024;
 
 struct AppendParams {
     PagedAppendArgs a;
@@ -95,22 +94,41 @@ __device__ __forceinline__ int place(const PagedAppendArgs& a, int t, int pos, i
     return WA_STATUS_BAD_PAGE;
 }
 
-template <int D, bool CACHE, bool FP8>
+// Checks every token's place and writes the status word, by a block of THREADS; kAtOnce tokens a thread at a time.
+constexpr int kAtOnce = 4;
+template <int THREADS>
+__device__ void append_status(const PagedAppendArgs& a) {
+    int bad = 0;
+    for (int t0 = threadIdx.x; t0 < a.n; t0 += kAtOnce * THREADS) {
+        int pos[kAtOnce], page;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) pos[i] = t0 + i * THREADS < a.n ? a.pos[t0 + i * THREADS] : -1;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) bad |= place(a, t0 + i * THREADS, pos[i], page);
+    }
+    const int where = __syncthreads_or(bad & WA_STATUS_BAD_POS), which = __syncthreads_or(bad & WA_STATUS_BAD_PAGE);
+    if (threadIdx.x == 0) a.hdr->status = (where ? WA_STATUS_BAD_POS : 0) | (which ? WA_STATUS_BAD_PAGE : 0);
+}
+
+__global__ void __launch_bounds__(1024) append_status_kernel(const __grid_constant__ AppendParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    append_status<1024>(p.a);
+}
+
+template <int D, bool CACHE, bool FP8, int PASSES>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendParams p) {
     const PagedAppendArgs& a = p.a;
     constexpr int L = D / 16;              // lanes a head
     constexpr int P = 32 / L;              // heads a pass
-    constexpr int HPW = P * kAppendPasses; // heads a warp
+    constexpr int HPW = P * PASSES;        // heads a warp
     constexpr int NA = D / 64;             // pairs whose angle a lane works out
     if constexpr (CACHE) {
         if (p.status_block && blockIdx.x == gridDim.x - 1) {
-            if (blockIdx.y > 0) return;
-            int bad = 0, page;
-            for (int t = threadIdx.x; t < a.n; t += kAppendWarps * 32) bad |= place(a, t, a.pos[t], page);
-            const int where = __syncthreads_or(bad & WA_STATUS_BAD_POS), which = __syncthreads_or(bad & WA_STATUS_BAD_PAGE);
-            if (threadIdx.x == 0) a.hdr->status = (where ? WA_STATUS_BAD_POS : 0) | (which ? WA_STATUS_BAD_PAGE : 0);
+            if (blockIdx.y == 0) append_status<kAppendWarps * 32>(a);
             return;
         }
+        // this kernel is over no sooner than the one that writes the status
+        if (!p.status_block && blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (static_cast<int>(threadIdx.x) >> 5), first = static_cast<int>(blockIdx.y) * HPW;
     if (t >= a.n) return;                  // warp-uniform
@@ -122,10 +140,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     const int one = turns && a.layout == WA_ROTARY_HALF ? 8 * li : 16 * li;
     const int two = turns && a.layout == WA_ROTARY_HALF ? a.dims / 2 + 8 * li : 16 * li + 8;
     const uint16_t* src = static_cast<const uint16_t*>(a.src) + t * a.src_tok;
-    uint4 raw[kAppendPasses][2];
+    uint4 raw[PASSES][2];
+    float scale[PASSES];
 #pragma unroll
-    for (int u = 0; u < kAppendPasses; ++u) {
+    for (int u = 0; u < PASSES; ++u) {
         const int h = first + u * P + hp;
+        scale[u] = 1.f;
+        if (CACHE && FP8 && h >= a.hq && h < heads) {
+            const float* of = a.kv[h < nqk ? 0 : 1].scale;
+            if (of) scale[u] = of[h - (h < nqk ? a.hq : nqk)];
+        }
         if (h < heads) {
             const uint16_t* x = src + static_cast<int64_t>(h) * D;
             raw[u][0] = *reinterpret_cast<const uint4*>(x + (h < nqk ? one : 16 * li));
@@ -134,10 +158,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     }
     int page = -1;
     if constexpr (CACHE) {
-        if (first + HPW > a.hq || (first == 0 && !p.status_block)) {       // a warp with keys or values, or one that reports
-            const int bad = place(a, t, pos, page);
-            if (bad && first == 0 && !p.status_block && lane == 0) atomicOr(&a.hdr->status, bad);
-        }
+        if (first + HPW > a.hq) place(a, t, pos, page);                    // a warp with keys or values
         if (pos < 0 || (pos >> a.page_log) >= a.most) return;
     }
     // Angles: a lane works out NA pairs of the token, and takes the eight of its dims from where they are.
@@ -163,7 +184,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     }
     const int64_t slot = CACHE ? pos & ((1 << a.page_log) - 1) : 0;
 #pragma unroll
-    for (int u = 0; u < kAppendPasses; ++u) {
+    for (int u = 0; u < PASSES; ++u) {
         const int h = first + u * P + hp;
         if (h >= heads) continue;
         float x[16];
@@ -198,10 +219,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
             const int g = h - (h < nqk ? a.hq : nqk);
             const int64_t at = page * side.page + slot * side.slot + g * side.head;
             if constexpr (FP8) {
-                const float scale = side.scale ? side.scale[g] : 1.f;
                 uint8_t* out = static_cast<uint8_t*>(side.base) + at;
-                *reinterpret_cast<uint2*>(out + o1) = make_uint2(quad_e4m3(x, scale), quad_e4m3(x + 4, scale));
-                *reinterpret_cast<uint2*>(out + o2) = make_uint2(quad_e4m3(x + 8, scale), quad_e4m3(x + 12, scale));
+                *reinterpret_cast<uint2*>(out + o1) = make_uint2(quad_e4m3(x, scale[u]), quad_e4m3(x + 4, scale[u]));
+                *reinterpret_cast<uint2*>(out + o2) = make_uint2(quad_e4m3(x + 8, scale[u]), quad_e4m3(x + 12, scale[u]));
             } else {
                 uint16_t* out = static_cast<uint16_t*>(side.base) + at;
                 *reinterpret_cast<uint4*>(out + o1) = pack(x);
@@ -213,28 +233,49 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
 
 }  // namespace
 
+namespace {
+
+template <int PASSES>
+cudaError_t launch_append(const AppendParams& p, cudaLaunchConfig_t& cfg) {
+    const PagedAppendArgs& a = p.a;
+    const int hpw = 32 / (a.d / 16) * PASSES;
+    cfg.gridDim = dim3((a.n - 1) / kAppendWarps + 1 + p.status_block, (a.hq + 2 * a.hkv + hpw - 1) / hpw);
+    cfg.blockDim = dim3(kAppendWarps * 32);
+    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
+    if (a.d == 256) {
+        if (a.hkv == 0) return run(append_kernel<256, false, false, PASSES>);
+        return a.e4m3 ? run(append_kernel<256, true, true, PASSES>) : run(append_kernel<256, true, false, PASSES>);
+    }
+    if (a.hkv == 0) return run(append_kernel<128, false, false, PASSES>);
+    return a.e4m3 ? run(append_kernel<128, true, true, PASSES>) : run(append_kernel<128, true, false, PASSES>);
+}
+
+// Few tokens: one pass a warp, for more warps at once (64 tokens of 48 heads of 128 to 8-bit pages: 3.2 us, with four passes
+// 4.8); many: four, for fewer angles and more bytes in flight (rope of 8,192 x 40 heads of 128: 26.5 us, with two 27.4).
+constexpr int64_t kFewValues = 1 << 20;
+
+}  // namespace
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     AppendParams p{};
     p.a = a;
-    const int hpw = 32 / (a.d / 16) * kAppendPasses;
     const bool cache = a.hkv > 0;
     p.status_block = cache && a.n <= kStatusBlockTokens;
+    cudaLaunchConfig_t cfg{};
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
     if (cache && !p.status_block) {
-        const cudaError_t e = cudaMemsetAsync(a.hdr, 0, sizeof(int), s);
+        append_status_kernel<<<1, 1024, 0, s>>>(p);
+        const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
     }
-    const dim3 grid((a.n - 1) / kAppendWarps + 1 + p.status_block, (a.hq + 2 * a.hkv + hpw - 1) / hpw);
-    constexpr int threads = kAppendWarps * 32;
-    if (a.d == 256) {
-        if (!cache) append_kernel<256, false, false><<<grid, threads, 0, s>>>(p);
-        else if (a.e4m3) append_kernel<256, true, true><<<grid, threads, 0, s>>>(p);
-        else append_kernel<256, true, false><<<grid, threads, 0, s>>>(p);
-    } else {
-        if (!cache) append_kernel<128, false, false><<<grid, threads, 0, s>>>(p);
-        else if (a.e4m3) append_kernel<128, true, true><<<grid, threads, 0, s>>>(p);
-        else append_kernel<128, true, false><<<grid, threads, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    const bool few = static_cast<int64_t>(a.n) * (a.hq + 2 * a.hkv) * a.d <= kFewValues;
+    const cudaError_t e = few ? launch_append<1>(p, cfg) : launch_append<4>(p, cfg);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace wa
