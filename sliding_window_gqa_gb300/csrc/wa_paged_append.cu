@@ -32,7 +32,7 @@ constexpr int kStatusBlockTokens = 1024;
 
 struct AppendParams {
     PagedAppendArgs a;
-    int status_block;
+    int beside;      // the status is another kernel's
 };
 
 // Two products, and two fused multiply-adds, an instruction.
@@ -110,7 +110,9 @@ __device__ void append_status(const PagedAppendArgs& a) {
     if (threadIdx.x == 0) a.hdr->status = (where ? WA_STATUS_BAD_POS : 0) | (which ? WA_STATUS_BAD_PAGE : 0);
 }
 
+// (The kernel beside it starts once what the stream held before is over, and need not wait for this one.)
 __global__ void __launch_bounds__(1024) append_status_kernel(const __grid_constant__ AppendParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     append_status<1024>(p.a);
 }
@@ -122,13 +124,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     constexpr int P = 32 / L;              // heads a pass
     constexpr int HPW = P * PASSES;        // heads a warp
     constexpr int NA = D / 64;             // pairs whose angle a lane works out
+    // Launched while the kernel before still runs, waits for its end here; beside the status kernel, one block does, so that
+    // this one is over no sooner.
+    if (!p.beside || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (CACHE) {
-        if (p.status_block && blockIdx.x == gridDim.x - 1) {
+        if (!p.beside && blockIdx.x == gridDim.x - 1) {
             if (blockIdx.y == 0) append_status<kAppendWarps * 32>(a);
             return;
         }
-        // this kernel is over no sooner than the one that writes the status
-        if (!p.status_block && blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (static_cast<int>(threadIdx.x) >> 5), first = static_cast<int>(blockIdx.y) * HPW;
     if (t >= a.n) return;                  // warp-uniform
@@ -239,7 +243,7 @@ template <int PASSES>
 cudaError_t launch_append(const AppendParams& p, cudaLaunchConfig_t& cfg) {
     const PagedAppendArgs& a = p.a;
     const int hpw = 32 / (a.d / 16) * PASSES;
-    cfg.gridDim = dim3((a.n - 1) / kAppendWarps + 1 + p.status_block, (a.hq + 2 * a.hkv + hpw - 1) / hpw);
+    cfg.gridDim = dim3((a.n - 1) / kAppendWarps + 1 + (a.hkv > 0 && !p.beside), (a.hq + 2 * a.hkv + hpw - 1) / hpw);
     cfg.blockDim = dim3(kAppendWarps * 32);
     auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
     if (a.d == 256) {
@@ -259,19 +263,19 @@ constexpr int64_t kFewValues = 1 << 20;
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     AppendParams p{};
     p.a = a;
-    const bool cache = a.hkv > 0;
-    p.status_block = cache && a.n <= kStatusBlockTokens;
+    p.beside = a.hkv > 0 && a.n > kStatusBlockTokens;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    if (cache && !p.status_block) {
-        append_status_kernel<<<1, 1024, 0, s>>>(p);
-        const cudaError_t e = cudaGetLastError();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (p.beside) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(1024);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, append_status_kernel, p);
         if (e != cudaSuccess) return e;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
     }
     const bool few = static_cast<int64_t>(a.n) * (a.hq + 2 * a.hkv) * a.d <= kFewValues;
     const cudaError_t e = few ? launch_append<1>(p, cfg) : launch_append<4>(p, cfg);
