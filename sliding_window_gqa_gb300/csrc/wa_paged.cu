@@ -132,7 +132,7 @@ struct PagedCfg {
     static constexpr int HV = D / 128;                   // loads a tile and operand: 128 keys x 128 dims each,
     static constexpr int KB = ESZ;                       // in blocks of 128 bytes of a key,
     static constexpr int SLOT = kPTile * KB * 128;       // as [16 groups of 8 keys][KB][8][128 bytes]
-    static constexpr int NSLOT = 98304 / SLOT;           // slots of K, and of V
+    static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;   // slots of K, and of V: as many as leave room for P
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
     // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
     static constexpr int QN = F8 && GP == 16 ? 32 : 16;
