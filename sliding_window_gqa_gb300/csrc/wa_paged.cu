@@ -1013,7 +1013,7 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
 // out = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M).  Both sums run over groups of kMergeGroup spans: a group's
 // in order, then the groups' in order, whichever of the two kernels below takes the row.  A result that is not finite is
 // worked out again.
-constexpr int kMergeGroup = 16;
+constexpr int kMergeGroup = 4;
 
 // The status word of the call, by its first block: what the CTAs have to report.
 __device__ __forceinline__ void paged_report(WsHeader* hdr, const int* said, int ctas) {
@@ -1043,28 +1043,32 @@ __device__ __forceinline__ void add4(float4& x, const float4& o) {
     x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
 }
 
-// Few rows: a block 64 dims of a (row, head), sixteen threads of 4 dims a group of spans.  The partial results are asked
-// for together with the position that says how many there are, so a call waits for one trip to memory (one row of 131,072
-// keys, 147 spans: 3 us; a warp every eighth span, after the position and the maxima: 5.4).
+// Few rows: a block 64 dims of a (row, head), sixteen threads of 4 dims a group of spans.  The partial results of the first
+// kWideAhead groups a thread are asked for together with the position that says how many there are, so a call of up to 128
+// spans waits for one trip to memory.
+constexpr int kWideAhead = 2;
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_wide_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
-    __shared__ float4 red[16][17];
-    __shared__ float weight[256], sums[256], tops[8], group_den[16];
+__global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
+    __shared__ float4 red[64][16];
+    __shared__ float weight[256], sums[256], tops[8], group_den[64];
     __shared__ PagedRerun again;
     const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G, col0 = blockIdx.y * 64;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, slice = t >> 4, quad = t & 15;
     const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
     auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
-    auto fetch = [&](int s) { return reinterpret_cast<const float4*>(x.part + rec(s) * D + col0)[quad]; };
+    float4 ahead[kWideAhead][kMergeGroup];      // (of spans that the row does not have: whatever the workspace holds, not used)
+    auto fetch = [&](int s, int most, float4 (&o)[kMergeGroup]) {
+#pragma unroll
+        for (int i = 0; i < kMergeGroup; ++i)
+            if (s + i < most) o[i] = reinterpret_cast<const float4*>(x.part + rec(s + i) * D + col0)[quad];
+    };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Plain loads from here on: what they read is written while this kernel is there already.  Blocks without work wait
     // too, so that nothing behind the call starts early.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int raw = a.pos[row];
-    float4 ahead[kMergeGroup];      // (of spans that the row does not have: whatever the workspace holds, not used)
 #pragma unroll
-    for (int i = 0; i < kMergeGroup; ++i)
-        if (slice * kMergeGroup + i < x.spans_most) ahead[i] = fetch(slice * kMergeGroup + i);
+    for (int i = 0; i < kWideAhead; ++i) fetch((16 * i + slice) * kMergeGroup, x.spans_most, ahead[i]);
     float2 mine = make_float2(-INFINITY, 0.f);
     if (t < x.spans_most) mine = x.ml[rec(t)];
     const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
@@ -1083,34 +1087,43 @@ __global__ void __launch_bounds__(256) paged_merge_wide_kernel(const __grid_cons
     __syncthreads();
     for (int w = 0; w < 8; ++w) M = fmaxf(M, tops[w]);
     float den = 0.f, o = 0.f;        // of thread t < 64: dim t
-    for (int s0 = 0; s0 < spans; s0 += 256) {      // sixteen groups at a time
+    for (int s0 = 0; s0 < spans; s0 += 256) {      // 64 groups at a time
         if (s0 + t < spans) {
             const float2 e = s0 == 0 ? mine : x.ml[rec(s0 + t)];
             weight[t] = exp2f(e.x - M);
             sums[t] = e.y;
         }
         __syncthreads();
-        const int end = min(spans - s0, 256), s1 = slice * kMergeGroup;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        float d = 0.f;
-        if (s0 > 0) {
+        const int end = min(spans - s0, 256);
+        auto group = [&](int k, const float4 (&part)[kMergeGroup]) {
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            float d = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMergeGroup; ++i)
-                if (s1 + i < end) ahead[i] = fetch(s0 + s1 + i);
-        }
-#pragma unroll
-        for (int i = 0; i < kMergeGroup; ++i)
-            if (s1 + i < end) {
-                fma4(num, weight[s1 + i], ahead[i]);
-                d = fmaf(weight[s1 + i], sums[s1 + i], d);
+            for (int i = 0; i < kMergeGroup; ++i) {
+                const int s = k * kMergeGroup + i;
+                if (s < end) {
+                    fma4(num, weight[s], part[i]);
+                    d = fmaf(weight[s], sums[s], d);
+                }
             }
-        red[slice][quad] = num;
-        if (quad == 0) group_den[slice] = d;
+            red[k][quad] = num;
+            if (quad == 0) group_den[k] = d;
+        };
+        int k = slice;
+        if (s0 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWideAhead; ++i, k += 16)
+                if (k * kMergeGroup < end) group(k, ahead[i]);
+        }
+        for (; k * kMergeGroup < end; k += 16) {
+            fetch(s0 + k * kMergeGroup, s0 + end, ahead[0]);
+            group(k, ahead[0]);
+        }
         __syncthreads();
         if (t < 64)
-            for (int k = 0; k * kMergeGroup < end; ++k) {
-                o += reinterpret_cast<const float*>(red)[k * 68 + t];
-                den += group_den[k];
+            for (int e = 0; e * kMergeGroup < end; ++e) {
+                o += reinterpret_cast<const float*>(red[e])[t];
+                den += group_den[e];
             }
         __syncthreads();
     }
@@ -1123,11 +1136,12 @@ __global__ void __launch_bounds__(256) paged_merge_wide_kernel(const __grid_cons
     if (__syncthreads_or(bad)) paged_rerun(a, again, row, h, col0);
 }
 
-// Many rows: a warp a (row, head).  (The kernel above takes 2 us a block whatever its row has: 48 rows of 32 heads of 256
-// over a window, 9 spans each, 18 us; this one 4.)
+// Many rows: a warp a (row, head); the first kNarrowAhead / V spans are asked for with the position, too.
+constexpr int kNarrowAhead = 16;
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
-    constexpr int V = D / 128, AHEAD = 8 / V;
+__global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
+    constexpr int V = D / 128, AHEAD = kNarrowAhead / V;
+    static_assert(AHEAD % kMergeGroup == 0 && 32 % AHEAD == 0, "whole groups");
     __shared__ PagedRerun again;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int item = blockIdx.x * 8 + warp, items = a.rows * a.hq;
@@ -1139,50 +1153,55 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
         const int row = item / a.hq, h = item % a.hq, G = a.hq / a.hkv, g = h / G;
         const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
         auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
-        const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
+        float4 o[AHEAD][V];
+        auto fetch = [&](int s, int most) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (s + i < most) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o[i][v] = reinterpret_cast<const float4*>(x.part + rec(s + i) * D)[v * 32 + lane];
+                }
+        };
         const int raw = a.pos[row];
         float2 mine = make_float2(-INFINITY, 0.f);
         if (lane < x.spans_most) mine = x.ml[rec(lane)];
+        fetch(0, x.spans_most);
+        const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
         const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv).spans;
         uint2* orow = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D);
         float M = lane < spans ? mine.x : -INFINITY;
         for (int s = lane + 32; s < spans; s += 32) M = fmaxf(M, x.ml[rec(s)].x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        float den = 0.f, d = 0.f, w = 0.f;
-        float4 num[V], sum[V];
+        for (int e = 16; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, e));
+        float den = 0.f, w = 0.f;
+        float4 sum[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) num[v] = sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        static_assert(kMergeGroup % AHEAD == 0, "loads of a group");
+        for (int v = 0; v < V; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s0 = 0; s0 < spans; s0 += AHEAD) {
+            if (s0 > 0) fetch(s0, spans);
             if ((s0 & 31) == 0) {
                 if (s0 > 0) mine = s0 + lane < spans ? x.ml[rec(s0 + lane)] : make_float2(-INFINITY, 0.f);
                 w = exp2f(mine.x - M);
             }
-            float4 o[AHEAD][V];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (s0 + i < spans) {
+            for (int k = 0; k < AHEAD; k += kMergeGroup) {
+                if (s0 + k >= spans) break;
+                float4 num[V];
+                float d = 0.f;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[i][v] = reinterpret_cast<const float4*>(x.part + rec(s0 + i) * D)[v * 32 + lane];
+                for (int v = 0; v < V; ++v) num[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = k; i < k + kMergeGroup; ++i) {
+                    const float wi = __shfl_sync(0xFFFFFFFFu, w, (s0 + i) & 31), li = __shfl_sync(0xFFFFFFFFu, mine.y, (s0 + i) & 31);
+                    if (s0 + i < spans) {
+                        d = fmaf(wi, li, d);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) fma4(num[v], wi, o[i][v]);
+                    }
                 }
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const float wi = __shfl_sync(0xFFFFFFFFu, w, (s0 + i) & 31), li = __shfl_sync(0xFFFFFFFFu, mine.y, (s0 + i) & 31);
-                if (s0 + i < spans) {
-                    d = fmaf(wi, li, d);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) fma4(num[v], wi, o[i][v]);
-                }
-            }
-            if ((s0 + AHEAD) % kMergeGroup == 0 || s0 + AHEAD >= spans) {       // the group's end
                 den += d;
-                d = 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    add4(sum[v], num[v]);
-                    num[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                for (int v = 0; v < V; ++v) add4(sum[v], num[v]);
             }
         }
 #pragma unroll
