@@ -142,7 +142,8 @@ struct PagedPlan {
     int spans;
     size_t taken;    // int[launches] units that are taken
     size_t said;     // int[launches * CTAs] what they have to report
-    size_t ml;       // float2[rows * hkv * spans * G]
+    size_t m;        // float[rows * hkv * spans * G]
+    size_t l;        // float[rows * hkv * spans * G * 4]
     size_t part;     // float[rows * hkv * spans * G * d]
     size_t bytes;
 };

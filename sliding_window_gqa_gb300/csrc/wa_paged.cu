@@ -57,31 +57,47 @@ namespace {
 
 constexpr int kPTile = 128;          // keys a tile
 constexpr int kPThreads = 512;
-constexpr int kQWarps = 3;           // 12, 14, 15
-constexpr int kPUnits = 4;           // unit slots
-constexpr int kFill = 152;           // a row is cut into this many units, or twice as many, .., over its key heads
+constexpr int kSmallUnit = 3;        // tiles below which units are published further ahead
+constexpr int kFill = 100;           // a row is cut into this many units, or twice as many, .., over its key heads
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
 constexpr int kPagedGrid = 256;      // CTAs of a launch at most
-constexpr int kInTurn = 4;
+constexpr int kInTurn = 8;           // units a CTA up to which they are taken in turn
+constexpr int kJobs = 4;             // jobs a CTA, at least
+constexpr int kFewestBytes = 65536;
 constexpr int kSpanTiles = 8;        // at most (their scores fit tensor memory twice, beside O)
 
-// How a row is cut.  `align`: keys of a copy.
+// How a row is cut: spans of `each` tiles, the first `more` of them of one more.  (Without runtime divisions: as two of 64
+// bits and two of 32 this took 2,000 cycles, and each unit's publication waited for it.)
+// Tiles of a span at least: 64 KiB of keys and values.
+__host__ __device__ constexpr int fewest_tiles(int d, int e4m3) { return d * (e4m3 ? 1 : 2) >= kFewestBytes / 256 ? 1 : kFewestBytes / 256 / (d * (e4m3 ? 1 : 2)); }
 struct RowCut {
-    int lo, k0, tiles, spans;        // first visible key, first key of the first tile
+    int lo, k0, tiles, spans, each, more;      // lo: the first visible key; k0: the first tile's first key
 };
 __host__ __device__ inline int64_t row_waves(int64_t tiles, int hkv) { return (tiles * hkv + kFill * kSpanTiles - 1) / (kFill * kSpanTiles); }
-__host__ __device__ inline int span_tiles(int64_t tiles, int hkv) {
-    const int64_t units = kFill * row_waves(tiles, hkv);
-    return static_cast<int>((tiles * hkv + units - 1) / units);
-}
-__device__ __forceinline__ RowCut row_cut(int p, int win, int align, int hkv) {
-    RowCut c;
-    c.lo = win > 0 ? max(0, p - win + 1) : 0;
+// `align`: keys of a copy
+__host__ __device__ inline RowCut row_cut(int p, int win, int align, int hkv, int fewest) {
+    RowCut c{};
+    c.lo = win > 0 && p - win + 1 > 0 ? p - win + 1 : 0;
     c.k0 = c.lo & ~(align - 1);
-    c.tiles = p < 0 ? 0 : (p - c.k0) / kPTile + 1;
-    const int each = span_tiles(c.tiles, hkv);
-    c.spans = c.tiles == 0 ? 0 : (c.tiles + each - 1) / each;
+    if (p < 0) return c;
+    c.tiles = (p - c.k0) / kPTile + 1;
+    const int64_t all = static_cast<int64_t>(c.tiles) * hkv, units = kFill * row_waves(c.tiles, hkv);
+    int most = 1;                              // tiles of a span at most: all / units, rounded up, or `fewest`
+#pragma unroll
+    for (int e = 1; e < kSpanTiles; ++e) most += e * units < all;
+    most = most < fewest ? fewest : most;
+    // tiles / most, rounded up: by 2^32 / most, rounded up, for up to 2^28 tiles
+    constexpr uint32_t by[kSpanTiles + 1] = {0u, 0u, 0x80000000u, 0x55555556u, 0x40000000u, 0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 2; e <= kSpanTiles; ++e) m = e == most ? by[e] : m;
+    const uint64_t up = static_cast<uint64_t>(c.tiles + most - 1) * m;
+    c.spans = most == 1 ? c.tiles : static_cast<int>(up >> 32);
+    c.each = 0;
+#pragma unroll
+    for (int e = 1; e <= kSpanTiles; ++e) c.each += static_cast<int64_t>(e) * c.spans <= c.tiles;
+    c.more = c.tiles - c.each * c.spans;
     return c;
 }
 
@@ -116,8 +132,9 @@ struct PagedParams {
     PagedArgs a;
     int* next_unit;                // null: units go to the CTAs in turn
     int* said;                     // [CTA]: its WA_STATUS_* bits
-    float2* ml;
-    float* part;
+    float* m;                      // [unit][G]
+    float* l;                      // [unit][G][4]: of each quarter of a tile's keys
+    float* part;                   // [unit][G][d]
     int row0, rows;                // the launch's rows
     int spans;                     // most spans of a (row, key head)
     int align;                     // keys of a copy
@@ -137,6 +154,7 @@ struct PagedCfg {
     // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
     static constexpr int QN = F8 && GP == 16 ? 32 : 16;
     __host__ __device__ static constexpr int lo_row() { return QN / 2; }
+    static constexpr int Q_WARPS = GP == 16 ? 3 : 1;     // that stage a unit's queries
     static constexpr int Q_BYTES = QN * D * ESZ;         // [D * ESZ / 128][QN / 8][8][128 bytes]
     static constexpr int PARTS = F8 ? 3 : 2;
     static constexpr int PN = (PARTS * GP + 15) / 16 * 16;
@@ -150,17 +168,21 @@ struct PagedCfg {
     static_assert(o_col(2) <= TMEM_COLS, "tensor memory budget");
     static constexpr int ROWS = D == 256 && !F8 && GP == 16 ? 64 : kPagedRows;   // rows a launch
     static_assert(ROWS >= kPagedFewest, "counters");
+    static constexpr int UNITS = ROWS == kPagedRows ? 8 : 4;  // unit slots
+    static constexpr int FEWEST = fewest_tiles(D, F8);
+    static constexpr int JOB_TILES = 262144 / (2 * kPTile * D * ESZ);   // tiles of K and V in 256 KiB
     static constexpr int PAGES = kSpanTiles * kPTile / 16;   // copies of a unit at most
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = OFF_RING + 2 * NSLOT * SLOT;
     static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;        // [group][NP]
     static constexpr int OFF_UNIT = OFF_P + 2 * NP * P_BYTES;    // 8 ints a slot
-    static constexpr int OFF_PAGES = OFF_UNIT + kPUnits * 32;
-    static constexpr int OFF_PRE = OFF_PAGES + kPUnits * PAGES * 4;   // units of the rows before
+    static constexpr int OFF_PAGES = OFF_UNIT + UNITS * 32;
+    static constexpr int OFF_PRE = OFF_PAGES + UNITS * PAGES * 4;   // units of the rows before
     static constexpr int OFF_LAST = OFF_PRE + (ROWS + 4) * 4;        // last positions
-    static constexpr int OFF_X = OFF_LAST + ROWS * 4;                 // [group][4 warps][16] maxima, then sums
-    static constexpr int OFF_C = OFF_X + 512;                // [kPUnits][16] c of each head (8-bit)
-    static constexpr int OFF_BAR = OFF_C + (F8 ? kPUnits * 64 : 0);
+    static constexpr int OFF_EACH = OFF_LAST + ROWS * 4;              // tiles of a row's spans, a byte each
+    static constexpr int OFF_X = OFF_EACH + ROWS;                     // [group][4 warps][16] maxima
+    static constexpr int OFF_C = OFF_X + 512;                // [UNITS][16] c of each head (8-bit)
+    static constexpr int OFF_BAR = OFF_C + (F8 ? UNITS * 64 : 0);
     static constexpr int B_FULL = 0;                         // [K, V][NSLOT]
     static constexpr int B_FREE = B_FULL + 2 * NSLOT;
     static constexpr int B_SFULL = B_FREE + 2 * NSLOT;           // [group]: all scores of the unit
@@ -169,11 +191,11 @@ struct PagedCfg {
     static constexpr int B_SFREE = B_PVDONE + 2 * NP;        // [group]: the unit's scores have been read
     static constexpr int B_QFULL = B_SFREE + 2;              // [unit & 1]
     static constexpr int B_QFREE = B_QFULL + 2;
-    static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod kPUnits] from here
-    static constexpr int B_UFREE = B_UFULL + kPUnits;
-    static constexpr int B_UTOOK = B_UFREE + kPUnits;        // the producer has begun the unit
-    static constexpr int B_UC = B_UTOOK + kPUnits;           // the unit's c are there (8-bit)
-    static constexpr int B_DRAIN = B_UC + kPUnits;
+    static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod UNITS] from here
+    static constexpr int B_UFREE = B_UFULL + UNITS;
+    static constexpr int B_UTOOK = B_UFREE + UNITS;        // the producer has begun the unit
+    static constexpr int B_UC = B_UTOOK + UNITS;           // the unit's c are there (8-bit)
+    static constexpr int B_DRAIN = B_UC + UNITS;
     static constexpr int NBAR = B_DRAIN + 2;                 // [S, P V]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base
     static constexpr int SMEM = OFF_MISC + 16;
@@ -256,6 +278,11 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" :: "l"(x)); }
 
 // A softmax group's barrier, alone and as a vote.
@@ -333,9 +360,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int count = 1;
         if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // a group's softmax warps
         else if (i >= C::B_SFREE && i < C::B_QFULL) count = 4;
-        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8 + kQWarps;       // producers, MMA, Q, softmax warps
-        else if (i >= C::B_QFULL && i < C::B_QFREE) count = kQWarps;
-        else if (i >= C::B_UC && i < C::B_DRAIN) count = kQWarps;
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8 + C::Q_WARPS;       // producers, MMA, Q, softmax warps
+        else if (i >= C::B_QFULL && i < C::B_QFREE) count = C::Q_WARPS;
+        else if (i >= C::B_UC && i < C::B_DRAIN) count = C::Q_WARPS;
         mbar_init(BAR(i), count);
         fence_mbar_init();
     }
@@ -362,16 +389,20 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     // nothing before this line reads or writes what a kernel before this one may be at
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");    // the join waits for this kernel's end by itself
-    int bad = 0;
+    int bad = 0, tiles = 0;
     static_assert(C::ROWS <= kPThreads, "a row a thread");
     {
         int mine = 0;
         if (tid < p.rows) {
             const int raw = p.a.pos[p.row0 + tid], at = paged_pos(raw, p.a.most, p.a.page_log);
             bad = raw != at;
-            mine = row_cut(at, p.a.win, p.align, p.a.hkv).spans;
+            const RowCut cut = row_cut(at, p.a.win, p.align, p.a.hkv, C::FEWEST);
+            mine = cut.spans;
+            tiles = min(cut.tiles, 1 << 20);
             lasts[tid] = at;
+            smem[C::OFF_EACH + tid] = static_cast<uint8_t>(cut.each);
         }
+        tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
         int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -379,10 +410,15 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (lane >= o) sum += y;
         }
         int* tot = reinterpret_cast<int*>(smem + C::OFF_X);
-        if (lane == 31) tot[warp] = sum;
+        if (lane == 31) {
+            tot[warp] = sum;
+            tot[16 + warp] = tiles;
+        }
         bad = __syncthreads_or(bad);
         if (tid == 0) *status = bad && blockIdx.x == 0 ? WA_STATUS_BAD_POS : 0;
         for (int w = 0; w < warp; ++w) sum += tot[w];
+        tiles = 0;
+        for (int w = 0; w < kPThreads / 32; ++w) tiles += tot[16 + w];
         if (tid < C::ROWS) pre[tid + 1] = sum;
         if (tid == 0) pre[0] = 0;
     }
@@ -391,9 +427,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tbase = misc[0];
 
-    auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % kPUnits) * 32); };
-    auto unit_pages = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_PAGES + (U % kPUnits) * C::PAGES * 4); };
-    auto uph = [](int U) { return static_cast<uint32_t>(U / kPUnits) & 1u; };
+    auto unit_ints = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_UNIT + (U % C::UNITS) * 32); };
+    auto unit_pages = [&](int U) { return reinterpret_cast<volatile int*>(smem + C::OFF_PAGES + (U % C::UNITS) * C::PAGES * 4); };
+    auto uph = [](int U) { return static_cast<uint32_t>(U / C::UNITS) & 1u; };
     auto read_unit = [&](int U, PUnit& x) {
         volatile int* e = unit_ints(U);
         x.row = e[0]; x.g = e[1]; x.span = e[2]; x.spans = e[3]; x.k0 = e[4]; x.nt = e[5]; x.lo = e[6]; x.p = e[7];
@@ -422,8 +458,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
-                if (side == 0) mbar_arrive(BAR(C::B_UTOOK + U % kPUnits));
+                mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
+                if (side == 0) mbar_arrive(BAR(C::B_UTOOK + U % C::UNITS));
             }
         };
         int s = 0, use = 0, loads = 0;            // the next load's slot
@@ -452,7 +488,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         };
         PUnit x;
         for (int U = 0;; ++U) {
-            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
+            if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
             read_unit(U, x);
             if (x.nt <= 0) break;
             look_up(U, x);
@@ -479,10 +515,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         };
         PUnit x;
         auto take = [&](int U) -> bool {
-            if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) return false;
+            if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) return false;
             read_unit(U, x);
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             x.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
             return x.nt > 0;
         };
@@ -578,76 +614,149 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ units
+        // In turn, or in jobs of about kSpanTiles tiles that a counter gives out.  A unit's pages are asked for before the unit
+        // ahead of it is published, where units are small (one after another they came every 2 to 3 us: 64 rows of 4,000
+        // keys, 8-bit pages, 151 us), and otherwise no earlier than its turn comes, so that the last ones go to whoever is free.
         const int units = pre[p.rows] * p.a.hkv;
-        int k = static_cast<int>(blockIdx.x);
+        const int ctas = static_cast<int>(gridDim.x);
+        const int job = max(1, min(min(16, units / (kJobs * ctas)), C::JOB_TILES * pre[p.rows] / max(tiles, 1)));
+        const bool in_turn = !p.next_unit || units <= kInTurn * ctas;
+        // unit k is span s (of all rows'), key head g; the row and what it is cut into are kept from one unit to the next
+        int k = 0, s = 0, g = 0, in_job = 0, row = -1;
+        int last = 0, lo = 0, k00 = 0, each = 0, more = 0, first = 0, spans = 0;
+        const int turn_s = ctas / p.a.hkv, turn_g = ctas - turn_s * p.a.hkv;
+        auto jump = [&](int to) {
+            k = to;
+            s = static_cast<int>(static_cast<uint32_t>(k) / static_cast<uint32_t>(p.a.hkv));
+            g = k - s * p.a.hkv;
+        };
+        jump(static_cast<int>(blockIdx.x) * (in_turn ? 1 : job));
+        int asked = -1;                           // lane 0: the next job's number
+        bool pending = false;
+        auto ask = [&]() {
+            if (lane == 0) asked = atomicAdd(p.next_unit, 1);
+            pending = true;
+        };
+        PUnit cur, nxt;
+        int id[2], id_next[2];                    // the unit's pages `lane` and `lane` + 32
+        static_assert(C::PAGES <= 64, "two pages a lane");
+        auto look_up = [&](PUnit& x, int (&ids)[2]) {
+            x.nt = 0;
+            if (k >= units) return;
+            if (static_cast<uint32_t>(s - first) >= static_cast<uint32_t>(spans)) {       // another row: pre[row] <= s < pre[row + 1]
+                if (row >= 0 && s == first + spans && pre[row + 2] > s) {
+                    ++row;
+                } else {
+                    int a = 0, b = p.rows;
+                    while (b - a > 1) {
+                        const int m = (a + b) >> 1;
+                        if (pre[m] <= s) a = m; else b = m;
+                    }
+                    row = a;
+                }
+                first = pre[row];
+                spans = pre[row + 1] - first;
+                last = lasts[row];
+                lo = p.a.win > 0 ? max(0, last - p.a.win + 1) : 0;
+                k00 = lo & ~(p.align - 1);
+                each = smem[C::OFF_EACH + row];
+                more = (last - k00) / kPTile + 1 - each * spans;
+            }
+            x.row = p.row0 + row;
+            x.g = g;
+            x.p = last;
+            x.lo = lo;
+            x.spans = spans;
+            x.span = s - first;
+            x.nt = each + (x.span < more ? 1 : 0);
+            x.k0 = k00 + (x.span * each + min(x.span, more)) * kPTile;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = lane + 32 * e, key = x.k0 + i * p.align;
+                ids[e] = -2;                      // without a visible key: nothing is copied
+                if (i < x.nt * pieces && key <= last && key + p.align > lo) ids[e] = max(-1, p.a.table[x.row * p.a.table_row + (key >> p.a.page_log)]);
+            }
+        };
+        auto step = [&]() {                       // the next unit's number
+            if (in_turn) {
+                k += ctas;
+                s += turn_s;
+                g += turn_g;
+                if (g >= p.a.hkv) {
+                    g -= p.a.hkv;
+                    ++s;
+                }
+            } else if (++in_job < job) {
+                ++k;
+                if (++g == p.a.hkv) {
+                    g = 0;
+                    ++s;
+                }
+            } else {
+                if (!pending) ask();
+                jump((__shfl_sync(0xFFFFFFFFu, asked, 0) + ctas) * job);
+                in_job = 0;
+                pending = false;
+            }
+        };
+        look_up(cur, id);
         bool ended = false;
         for (int U = 0;; ++U) {
-            int nt = 0;
+            const bool small = cur.nt < kSmallUnit;
+            if (small && cur.nt > 0) {
+                step();
+                look_up(nxt, id_next);
+                if (!in_turn && in_job == job - 1) ask();        // the job after: a unit before it is needed
+            }
             // the slot's last unit has been read by everyone
-            if (U >= kPUnits && !warp_wait(BAR(C::B_UFREE + U % kPUnits), uph(U - kPUnits), status)) break;
-            if (k < units) {
-                const int s = k / p.a.hkv, g = k - s * p.a.hkv;
-                int a = 0, b = p.rows;            // pre[a] <= s < pre[b]
-                while (b - a > 1) {
-                    const int m = (a + b) >> 1;
-                    if (pre[m] <= s) a = m; else b = m;
-                }
-                const int row = p.row0 + a, last = lasts[a];
-                const RowCut cut = row_cut(last, p.a.win, p.align, p.a.hkv);
-                const int span = s - pre[a], each = cut.tiles / cut.spans, more = cut.tiles - each * cut.spans;
-                nt = each + (span < more ? 1 : 0);
-                const int k0 = cut.k0 + (span * each + min(span, more)) * kPTile;
+            if (U >= C::UNITS && !warp_wait(BAR(C::B_UFREE + U % C::UNITS), uph(U - C::UNITS), status)) break;
+            if (cur.nt > 0) {
                 volatile int* ids = unit_pages(U);
-                for (int e = lane; e < nt * pieces; e += 32) {
-                    const int key = k0 + e * p.align;
-                    int id = -2;                  // without a visible key: nothing is copied
-                    if (key <= last && key + p.align > cut.lo) {
-                        id = p.a.table[row * p.a.table_row + (key >> p.a.page_log)];
-                        if (id < 0 || id >= p.a.pages) {
-                            id = -1;
-                            atomicOr(status, WA_STATUS_BAD_PAGE);
-                        }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (lane + 32 * e >= cur.nt * pieces) continue;
+                    if (id[e] != -2 && (id[e] < 0 || id[e] >= p.a.pages)) {
+                        id[e] = -1;
+                        atomicOr(status, WA_STATUS_BAD_PAGE);
                     }
-                    ids[e] = id;
+                    ids[lane + 32 * e] = id[e];
                 }
-                if (lane == 0) {
-                    volatile int* x = unit_ints(U);
-                    x[0] = row; x[1] = g; x[2] = span; x[3] = cut.spans; x[4] = k0; x[5] = nt; x[6] = cut.lo; x[7] = last;
-                }
-            } else if (lane == 0) {
-                unit_ints(U)[5] = 0;
+            }
+            if (lane == 0) {
+                volatile int* x = unit_ints(U);
+                x[0] = cur.row; x[1] = cur.g; x[2] = cur.span; x[3] = cur.spans; x[4] = cur.k0; x[5] = cur.nt; x[6] = cur.lo; x[7] = cur.p;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UFULL + U % kPUnits));
-            if (nt == 0) {
+            if (lane == 0) mbar_arrive(BAR(C::B_UFULL + U % C::UNITS));
+            if (cur.nt == 0) {
                 if (ended) break;                 // an end for each softmax group
                 ended = true;
                 continue;
             }
-            // A unit is taken no earlier than needed, so that the last ones go to whoever is free: when the producer has
-            // begun this one or, where units are short, the one before it.
-            const int begun = U - 1;
-            if (!p.next_unit) {
-                k += static_cast<int>(gridDim.x);
-                continue;
+            const int begun = small ? U - C::UNITS / 4 : U;      // the producer has begun it
+            if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % C::UNITS), uph(begun), status)) break;
+            if (!small) {
+                step();
+                look_up(nxt, id_next);
             }
-            if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % kPUnits), uph(begun), status)) break;
-            int nk = 0;
-            if (lane == 0) nk = atomicAdd(p.next_unit, 1);
-            k = __shfl_sync(0xFFFFFFFFu, nk, 0) + static_cast<int>(gridDim.x);
+            cur = nxt;
+            id[0] = id_next[0];
+            id[1] = id_next[1];
         }
     } else if (warp >= 12) {
         // ------------------------------------------------ Q: four heads at a time, in a loop, which a unit -1 of no heads
         // goes through first: its code comes in while nothing else is asked of the memory.  (All heads' code in a row, 16
         // heads split in two, came line by line behind the first keys: 6 us to the first product.)
         constexpr int EL = D / 32;                // values a lane and head
-        const int turn = warp == 12 ? 0 : warp - 13;
+        // up to 8 heads: a warp the even units, one the odd ones; 16: three warps every unit
+        constexpr bool ALL = C::Q_WARPS > 1;
+        const int turn = ALL && warp > 12 ? warp - 13 : 0;
         PUnit x;
         x.row = x.g = 0;
-        for (int U = -1;; ++U) {
+        for (int U = ALL ? -1 : warp == 12 ? -2 : -1; ALL || warp != 15; U += ALL ? 1 : 2) {
             int live = 0;                         // heads (the buffer's other rows: zeros)
             if (U >= 0) {
-                if (!warp_wait(BAR(C::B_UFULL + U % kPUnits), uph(U), status)) break;
+                if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
                 read_unit(U, x);
                 if (x.nt <= 0) break;
                 live = G;
@@ -678,13 +787,13 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (U >= 2 && !warp_wait(BAR(C::B_QFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
             const uint32_t dst = sbase + C::OFF_Q + (U & 1) * C::Q_BYTES;
 #pragma unroll 1
-            for (int h0 = 4 * turn; h0 < GP; h0 += 4 * kQWarps) {
+            for (int h0 = 4 * turn; h0 < GP; h0 += 4 * C::Q_WARPS) {
                 uint32_t now[4][EL / 2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < EL / 2; ++e) now[i][e] = raw[i][e];
-                if (h0 + 4 * kQWarps < GP) fetch(h0 + 4 * kQWarps);
+                if (h0 + 4 * C::Q_WARPS < GP) fetch(h0 + 4 * C::Q_WARPS);
                 if constexpr (!F8) {
                     // dims lane * EL ..: block of 64 dims, 16-byte chunk, swizzled by the row
                     const int el = lane * EL, chunk = (el & 63) * 2;
@@ -735,7 +844,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                             st_shared_u32(al + 4 * w, fine ? rest : 0u);
                         }
                         if (lane == i)
-                            reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U & (kPUnits - 1)) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
+                            reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U & (C::UNITS - 1)) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
                     }
                 }
             }
@@ -743,8 +852,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0 && U >= 0) {
                 mbar_arrive(BAR(C::B_QFULL + (U & 1)));
-                if constexpr (F8) mbar_arrive(BAR(C::B_UC + U % kPUnits));
-                mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+                if constexpr (F8) mbar_arrive(BAR(C::B_UC + U % C::UNITS));
+                mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             }
             __syncwarp();
         }
@@ -753,6 +862,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         const int quarter = warp & 3, group = (warp >> 2) - 1, gt = tid & 127;
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         volatile float* xbuf = reinterpret_cast<volatile float*>(smem + C::OFF_X) + group * 64;
+        const uint32_t x_addr = sbase + C::OFF_X + group * 256;
         constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
         // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
         // next vote, at which the four warps leave together.
@@ -766,19 +876,19 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int t = 0;                                       // the group's tiles
         for (int U = group;; U += 2) {
             PUnit x;
-            wait(C::B_UFULL + U % kPUnits, uph(U));
+            wait(C::B_UFULL + U % C::UNITS, uph(U));
             read_unit(U, x);
             float c[F8 ? GP : 1];
             if constexpr (F8) {
-                if (!dead && x.nt > 0) wait(C::B_UC + U % kPUnits, uph(U));
+                if (!dead && x.nt > 0) wait(C::B_UC + U % C::UNITS, uph(U));
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
-                    c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % kPUnits) * 16 + h] : 0.f;
+                    c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % C::UNITS) * 16 + h] : 0.f;
             } else {
                 c[0] = p.c;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % kPUnits));
+            if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             if (group_any(group, dead) || x.nt <= 0) break;
             wait(C::B_SFULL + group, static_cast<uint32_t>(U >> 1) & 1u);
             tc_fence_after();
@@ -825,7 +935,15 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             group_sync(group);
 #pragma unroll
-            for (int h = 0; h < GP; ++h) m[h] = fmaxf(fmaxf(xbuf[h], xbuf[16 + h]), fmaxf(xbuf[32 + h], xbuf[48 + h])) - kShift;
+            for (int h = 0; h < GP; h += 4) {
+                float4 e[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) e[w] = ld_shared_f4(x_addr + (16 * w + h) * 4);
+                m[h] = fmaxf(fmaxf(e[0].x, e[1].x), fmaxf(e[2].x, e[3].x)) - kShift;
+                m[h + 1] = fmaxf(fmaxf(e[0].y, e[1].y), fmaxf(e[2].y, e[3].y)) - kShift;
+                m[h + 2] = fmaxf(fmaxf(e[0].z, e[1].z), fmaxf(e[2].z, e[3].z)) - kShift;
+                m[h + 3] = fmaxf(fmaxf(e[0].w, e[1].w), fmaxf(e[2].w, e[3].w)) - kShift;
+            }
             // ---- P, tile by tile
             for (int idx = 0; idx < x.nt; ++idx, ++t) {
                 float s[GP];
@@ -886,18 +1004,16 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     if (idx == x.nt - 1) mbar_arrive(BAR(C::B_SFREE + group));
                 }
             }
-            // ---- the unit's result: l over the 128 keys of a tile in a fixed order, O from tensor memory
+            // ---- the unit's result: l of this quarter of the keys in a fixed order, O from tensor memory
+            const int64_t unit = ((static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span) * G;
             const float sum = reduce_each(l, [](float a, float b) { return a + b; });
-            group_sync(group);                    // the maxima in this buffer have been read
-            if (lane % (32 / GP) == 0) xbuf[quarter * 16 + lane / (32 / GP)] = sum;
-            group_sync(group);
-            const int64_t unit = (static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span;
+            if (lane % (32 / GP) == 0 && lane / (32 / GP) < G) p.l[(unit + lane / (32 / GP)) * 4 + quarter] = sum;
             if (gt < G) {
                 float mine = 0.f;
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
                     if (gt == h) mine = m[h];
-                p.ml[unit * G + gt] = make_float2(mine, (xbuf[gt] + xbuf[16 + gt]) + (xbuf[32 + gt] + xbuf[48 + gt]));
+                p.m[unit + gt] = mine;
             }
             {
                 const int buf = group * C::NP + (t - 1) % C::NP;
@@ -922,7 +1038,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
                     if (h >= G) break;
-                    p.part[(unit * G + h) * D + dim] = o[h];
+                    p.part[(unit + h) * D + dim] = o[h];
                 }
             }
         }
@@ -1027,11 +1143,19 @@ __device__ __forceinline__ void paged_report(WsHeader* hdr, const int* said, int
 }
 
 struct MergeArgs {
-    const float2* ml;
+    const float* m;
+    const float4* l;
     const float* part;
     const int* said;
     int spans_most, align, ctas;
 };
+
+// (m, l) of a record, l over the quarters in order
+__device__ __forceinline__ float2 record(const MergeArgs& x, int64_t at) {
+    const float m = x.m[at];
+    const float4 l = x.l[at];
+    return make_float2(m, (l.x + l.y) + (l.z + l.w));
+}
 
 __device__ __forceinline__ void fma4(float4& x, float w, const float4& o) {
     x.x = fmaf(w, o.x, x.x);
@@ -1070,9 +1194,9 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < kWideAhead; ++i) fetch((16 * i + slice) * kMergeGroup, x.spans_most, ahead[i]);
     float2 mine = make_float2(-INFINITY, 0.f);
-    if (t < x.spans_most) mine = x.ml[rec(t)];
+    if (t < x.spans_most) mine = record(x, rec(t));
     const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-    const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv).spans;
+    const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv, fewest_tiles(a.d, a.e4m3)).spans;
     if (blockIdx.x == 0 && blockIdx.y == 0) paged_report(a.hdr, x.said, x.ctas);
     uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D + col0;
     if (spans == 0) {
@@ -1080,7 +1204,7 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
         return;
     }
     float M = t < spans ? mine.x : -INFINITY;
-    for (int s = t + 256; s < spans; s += 256) M = fmaxf(M, x.ml[rec(s)].x);
+    for (int s = t + 256; s < spans; s += 256) M = fmaxf(M, x.m[rec(s)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
     if (lane == 0) tops[warp] = M;
@@ -1089,7 +1213,7 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
     float den = 0.f, o = 0.f;        // of thread t < 64: dim t
     for (int s0 = 0; s0 < spans; s0 += 256) {      // 64 groups at a time
         if (s0 + t < spans) {
-            const float2 e = s0 == 0 ? mine : x.ml[rec(s0 + t)];
+            const float2 e = s0 == 0 ? mine : record(x, rec(s0 + t));
             weight[t] = exp2f(e.x - M);
             sums[t] = e.y;
         }
@@ -1164,13 +1288,13 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
         };
         const int raw = a.pos[row];
         float2 mine = make_float2(-INFINITY, 0.f);
-        if (lane < x.spans_most) mine = x.ml[rec(lane)];
+        if (lane < x.spans_most) mine = record(x, rec(lane));
         fetch(0, x.spans_most);
         const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-        const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv).spans;
+        const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv, fewest_tiles(a.d, a.e4m3)).spans;
         uint2* orow = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D);
         float M = lane < spans ? mine.x : -INFINITY;
-        for (int s = lane + 32; s < spans; s += 32) M = fmaxf(M, x.ml[rec(s)].x);
+        for (int s = lane + 32; s < spans; s += 32) M = fmaxf(M, x.m[rec(s)]);
 #pragma unroll
         for (int e = 16; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, e));
         float den = 0.f, w = 0.f;
@@ -1180,7 +1304,7 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
         for (int s0 = 0; s0 < spans; s0 += AHEAD) {
             if (s0 > 0) fetch(s0, spans);
             if ((s0 & 31) == 0) {
-                if (s0 > 0) mine = s0 + lane < spans ? x.ml[rec(s0 + lane)] : make_float2(-INFINITY, 0.f);
+                if (s0 > 0) mine = s0 + lane < spans ? record(x, rec(s0 + lane)) : make_float2(-INFINITY, 0.f);
                 w = exp2f(mine.x - M);
             }
 #pragma unroll
@@ -1271,7 +1395,8 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     const int align = copy_keys(page_log);
     const int64_t keys = static_cast<int64_t>(most) << page_log;
     int64_t tiles = (keys + kPTile - 1) / kPTile;
-    if (win > 0 && (win + align - 2) / kPTile + 1 < tiles) tiles = (static_cast<int64_t>(win) + align - 2) / kPTile + 1;
+    const int64_t seen = (static_cast<int64_t>(win) + align - 2) / kPTile + 1;      // tiles of a window, wherever it begins
+    if (win > 0 && seen < tiles) tiles = seen;
     // ceil(t / each) with each >= t hkv / (kFill waves(t)), and waves(t) no less for longer rows
     const int64_t fill = (kFill * row_waves(tiles, hkv) + hkv - 1) / hkv;
     pl.spans = static_cast<int>(fill < tiles ? fill : tiles);
@@ -1279,8 +1404,9 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     pl.taken = kHeaderBytes;
     pl.said = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
-    pl.ml = pl.said + up((rows / kPagedFewest + 1) * kPagedGrid * sizeof(int));
-    pl.part = pl.ml + up(heads * pl.spans * sizeof(float2));
+    pl.m = pl.said + up((rows / kPagedFewest + 1) * kPagedGrid * sizeof(int));
+    pl.l = pl.m + up(heads * pl.spans * sizeof(float));
+    pl.part = pl.l + up(heads * pl.spans * 4 * sizeof(float));
     pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
     return pl;
 }
@@ -1302,7 +1428,8 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
     int* taken = reinterpret_cast<int*>(base + pl.taken);
     int* said = reinterpret_cast<int*>(base + pl.said);
-    p.ml = reinterpret_cast<float2*>(base + pl.ml);
+    p.m = reinterpret_cast<float*>(base + pl.m);
+    p.l = reinterpret_cast<float*>(base + pl.l);
     p.part = reinterpret_cast<float*>(base + pl.part);
     p.spans = pl.spans;
     p.c = fabsf(a.scale) * 1.4426950408889634f;
@@ -1347,7 +1474,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         return cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    MergeArgs m{p.ml, p.part, said, pl.spans, p.align, ctas};
+    MergeArgs m{p.m, reinterpret_cast<const float4*>(p.l), p.part, said, pl.spans, p.align, ctas};
     const int pairs = a.rows * a.hq;
     cfg.gridDim = pairs < kMergeWide ? dim3(pairs, a.d / 64) : dim3((pairs + 7) / 8);
     cfg.blockDim = dim3(256);

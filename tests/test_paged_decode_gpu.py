@@ -141,6 +141,51 @@ def test_a_rows_bits_in_batches_of_many_rows(wa, d, hq, hkv):
     assert r["ok"], r
 
 
+@pytest.mark.parametrize("rows, hq, hkv, d, length, bits_", [
+    (48, 32, 16, 128, 300, 16),         # more units than the CTAs take in turn: short ones, given out by jobs,
+    (40, 64, 16, 256, 260, 16),
+    (64, 32, 16, 128, 900, 8),
+    (24, 32, 8, 128, 8000, 16),         # and long ones, one by one
+    (30, 16, 2, 256, 20000, 8),
+    (70, 16, 1, 256, 140, 16),          # and more rows than one launch takes
+    (300, 8, 4, 128, 140, 8),
+], ids=str)
+def test_large_batches(wa, rows, hq, hkv, d, length, bits_):
+    """Rows of like lengths, some empty: sampled rows against the oracle, and alone."""
+    lengths = [0 if r % 17 == 5 else max(1, length - 7 * (r % 13)) for r in range(rows)]
+    c = wa_synth.paged_case(lengths, hq, hkv, d, 64, seed=54, bits=bits_, device="cuda", outside="keep", peaked=False)
+    out = call(wa, c)
+    some = [0, 5, rows // 2, rows - 1]
+    r = check.compare(bits(out[some]), reference(c, 1.0, rows=some), TOL)
+    assert r["ok"], r
+    for i in some:
+        one = dict(c, q=c["q"][i:i + 1], table=c["table"][i:i + 1], pos=c["pos"][i:i + 1])
+        assert same(call(wa, one)[0], out[i]), i
+    for _ in range(3):                  # whoever takes which unit
+        assert same(call(wa, c), out)
+
+
+def test_parts_of_a_pool(wa):
+    """Some heads, some slots and some pages of a larger pool."""
+    c = wa_synth.paged_case([300, 64], 8, 2, 128, 16, seed=55, device="cuda")
+    pages = c["k"].shape[0]
+    pool = torch.full((2 * pages, 32, 5, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    k, v = pool[::2, :16, 3:], pool[1::2, 16:, 1:3]
+    k.copy_(c["k"])
+    v.copy_(c["v"])
+    want = call(wa, c)
+    assert same(call(wa, dict(c, k=k, v=v)), want)
+
+
+def test_the_widest_window(wa):
+    c = wa_synth.paged_case([300, 64], 8, 2, 128, 16, seed=56, device="cuda")
+    want = call(wa, c)
+    for win in (300, 2 ** 31 - 1):
+        assert wa.paged_decode_ws_bytes(2, 8, 2, 128, 16, c["table"].shape[1], win) == \
+            wa.paged_decode_ws_bytes(2, 8, 2, 128, 16, c["table"].shape[1])
+        assert same(call(wa, dict(c, win=win)), want)
+
+
 def test_strided_queries_and_outputs_and_shared_pages(wa):
     """Queries inside projection rows, outputs inside a wider buffer, and two sequences with a common prefix."""
     c = wa_synth.paged_case([200, 200], 8, 4, 128, 64, seed=45, device="cuda")
