@@ -111,9 +111,12 @@ bool pages_ok(const wa_pages* c, int32_t hq, int32_t win) {
     return pages_apart(*c, c->k_page, c->k_slot, c->k_head, align) && pages_apart(*c, c->v_page, c->v_slot, c->v_head, align);
 }
 
+// The head stride as the kernels use it: a lone head's means nothing.
+int64_t head_stride(const wa_pages& c, int64_t head) { return c.hkv > 1 ? head : c.d; }
+
 // Whether the decode's copies can name a page's keys by one index: pages apart by a whole number of 8 positions, or of heads.
 bool pages_in_steps(const wa_pages& c, int64_t page, int64_t slot, int64_t head) {
-    const int64_t step = page % (8 * slot) == 0 ? 8 * slot : head;
+    const int64_t step = page % (8 * slot) == 0 ? 8 * slot : head_stride(c, head);
     return c.pages == 1 || (page % step == 0 && (c.pages - 1) * (page / step) + c.hkv + c.page_size < INT32_MAX);
 }
 
@@ -467,8 +470,8 @@ int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int
     if (rc != WA_OK) return rc;
     wa::PagedAppendArgs a{};
     a.src = src; a.pos = pos; a.row = row; a.q_out = q_out;
-    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, cache->k_head};
-    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, cache->v_head};
+    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, head_stride(*cache, cache->k_head)};
+    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, head_stride(*cache, cache->v_head)};
     a.table = cache->table; a.table_row = cache->table_row;
     a.src_tok = src_tok; a.q_tok = q_tok;
     a.hdr = static_cast<wa::WsHeader*>(ws);
@@ -500,8 +503,8 @@ int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_page
     if (rc != WA_OK) return rc;
     wa::PagedArgs a{};
     a.q = q; a.pos = pos; a.out = out;
-    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, cache->k_head};
-    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, cache->v_head};
+    a.kv[0] = {cache->k, cache->k_scale, cache->k_page, cache->k_slot, head_stride(*cache, cache->k_head)};
+    a.kv[1] = {cache->v, cache->v_scale, cache->v_page, cache->v_slot, head_stride(*cache, cache->v_head)};
     a.table = cache->table; a.table_row = cache->table_row; a.q_row = q_row; a.o_row = out_row;
     a.hdr = static_cast<wa::WsHeader*>(ws);
     a.rows = cache->rows; a.hq = hq; a.hkv = cache->hkv; a.d = cache->d;

@@ -74,6 +74,16 @@ def test_decode_argument_errors(bad):
     assert _decode(**bad) == wa.WA_EINVAL
 
 
+def test_a_lone_head_may_have_any_head_stride():
+    """(There is no other head to be apart from.  The checks before the workspace pass, without a division by it.)"""
+    for stride in (0, -256, 256, 1 << 50):
+        c = dict(hkv=1, **{f"{s}_{n}": v for s in "kv" for n, v in (("head", stride), ("slot", 256), ("page", 16 * 256 + 256))})
+        assert _decode(cache=c, hq=2, ws=None) == wa.WA_EWORKSPACE
+        assert _append(cache=c, hq=2, ws=None) == wa.WA_EWORKSPACE
+        c["k_page"] += 8                  # a multiple of neither
+        assert _decode(cache=c, hq=2, ws=None) == wa.WA_EINVAL
+
+
 def test_workspace_errors():
     L = ensure_built().lib()
     assert _append(ws=None) == _append(ws_bytes=255) == _append(ws=FAKE + 128) == wa.WA_EWORKSPACE
