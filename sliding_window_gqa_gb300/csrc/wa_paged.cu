@@ -5,45 +5,43 @@
 // over the row's visible keys, for the G query heads of a key head together, so K and V
 // are read once.
 //
-// Turned round.  With one token a row there are at most 16 query heads a key head, and a
-// product with the queries as the 128 rows of the tensor core would be 7/8 padding.  So the
-// keys are the rows: S^T = K Q^T (128 keys x 16) and O^T = V^T P^T (128 dims x the parts of P).
-// Both A operands are then the cache's own tiles as the copies leave them, both B operands
-// small; P's parts are columns of one product, so V is read from shared memory once for all
-// of them.  A key is a lane of tensor memory, so a mask is one bit a thread, and the scores of a whole
-// span (16 columns a tile) stay there: its keys come first, then its maximum is known, then
-// its values.  Nothing is ever scaled again.  (With a running maximum, tile by tile, every other tile of
-// 8-bit pages moved some head's, where P has to fit its type: 309 us instead of 170 for the batch.)
+// Turned round.  With one token a row there are at most 16 query heads a key head, and a product with the queries as the
+// 128 rows of the tensor core would be 7/8 padding.  So the keys are the rows: S^T = K Q^T (128 keys x 16) and O^T = V^T P^T
+// (128 dims x the parts of P).  Both A operands are then the cache's own tiles as the copies leave them, both B operands
+// small; P's parts are columns of one product, so V is read from shared memory once for all of them.  A key is a lane of
+// tensor memory, so a mask is one bit a thread, and the scores of a whole span (16 columns a tile) stay there: its keys come
+// first, then its maximum is known, then its values.  Nothing is ever scaled again.  (With a running maximum every other
+// tile of 8-bit pages moved some head's, since P has to fit its type: 309 us for the batch below, 199 without.)
 //
-// 8-bit pages.  e4m3 has 4 significant bits, so a query, of 8, is two e4m3 numbers: 2^k q = hi +
-// lo, exactly down to 2^-10 of the head's largest value and to 2^-18 of it below, and S comes from exact
-// products as with bf16.  P is three: 256 p = p1 + p2 / 32 + p3 / 1024 to 2^-12 of p (one part alone: 2^-4; two:
-// 2^-8, about what the output's own rounding loses), or to 2^-28 of the largest where that is more.
+// 8-bit pages.  e4m3 has 4 significant bits, so a query, of 8, is two e4m3 numbers: 2^k q = hi + lo, exactly down to 2^-10 of
+// the head's largest value and to 2^-18 of it below, and S comes from exact products as with bf16.  P is three:
+// 256 p = p1 + p2 / 32 + p3 / 1024 to 2^-12 of p (one part alone: 2^-4; two: 2^-8, about what the output's own rounding
+// loses), or to 2^-28 of the largest where that is more.
 //
-// Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's
-// keys), are cut into even spans of at most kSpanTiles, as many as fill the GPU once, or twice, ..
-// (kFill) with this row alone.  A unit of work is (row, key head, span); it leaves (m, l, O) in
-// fp32, and paged_merge_kernel joins a row's spans.  (Joined by the CTA that finished a row's last
-// unit, one long row ended in 60 us of one SM reading what the others had left.)
-// Nothing in a unit depends on the other rows, so neither do the bits.
+// Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's keys), are cut into even spans
+// (row_cut).  A unit of work is (row, key head, span); it leaves (m, l, O) in fp32, and a kernel of its own joins a row's
+// spans.  (Joined by the CTA that finished a row's last unit, one long row ended in 60 us of one SM reading what the others
+// had left.)  Nothing in a unit depends on the other rows, so neither do the bits.
 //
-// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 512 threads, that streams the keys
-// of its units without a break between units:
-//   warps 0, 3  TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and
-//               128 dims.  (One warp for both took 900 cycles a load, where one of 8-bit pages
-//               lands every 700.)
-//   warps 1, 13 MMA issuers of S (a unit ahead of its P V, at most two) and of P V.  Before O += V^T P^T
-//               of a row's first and last tile the second zeroes V's slots without a visible key, so
-//               that what they hold never meets a zero probability as 0 * inf.  (One warp for both took
-//               1,000 cycles a tile, where one of 8-bit pages lands every 1,400.)  Warp 1 allocates
-//               tensor memory.
-//   warp 2      takes units by a counter, looks up their pages, publishes them
-//   warps 12,   Q to shared memory, split in two for 8-bit pages
-//   14, 15
-//   warps 4..7  softmax of even units, a key a thread: the maximum, exponentials, P to shared
-//   and 8..11   memory, the unit's result; of odd units.  One group's chain (a unit's ends, 2,500
-//               cycles) runs beside the other's.
+// paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 512 threads, that streams the keys of its units without a break
+// between units:
+//   warps 0, 3    TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and 128 dims.  (One warp
+//                 for both took 900 cycles a load, where one of 8-bit pages lands every 700: 199 us, 182 with two.)
+//   warps 1, 13   MMA issuers of S (a unit ahead of its P V, at most two) and of P V.  Before O += V^T P^T of a row's first
+//                 and last tile the second zeroes V's slots without a visible key, so that what they hold never meets a
+//                 zero probability as 0 * inf.  (One warp for both took 1,000 cycles a tile, where one of 8-bit pages lands
+//                 every 1,400: 186 us, 170 with two.)  Warp 1 allocates tensor memory.
+//   warp 2        takes units, looks up their pages, publishes them
+//   warps 12, 14  Q to shared memory, split in two for 8-bit pages, once for units of one (row, key head) in a row: every
+//                 other one each; of 16 heads, they and warp 15 four heads each of all
+//   warps 4..7    softmax of even units, a key a thread: the maximum, exponentials, P to shared memory, the unit's result;
+//   and 8..11     of odd units.  One group's chain (a unit's ends, 2,500 cycles) runs beside the other's.
 // Every wait is bounded (a status bit after kWaitLimitNs).
+//
+// Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128, 304 us for 311 at the rate of a copy; 48 rows,
+// 32/16 heads of 256, window 1,024, 124 for 117; one row of 131,072 keys, 32/4 heads of 128, 49 for 40 (start and join);
+// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 37 for
+// 21 (the softmax warps' chain, few units an SM).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -57,20 +55,35 @@ namespace {
 
 constexpr int kPTile = 128;          // keys a tile
 constexpr int kPThreads = 512;
-constexpr int kSmallUnit = 3;        // tiles below which units are published further ahead
-constexpr int kFill = 100;           // a row is cut into this many units, or twice as many, .., over its key heads
+// Tiles of a span at most: as many as have room for their scores twice, beside O.  (Of 4, 6 and 8: the 8-bit batch 179, 163
+// and 161 us; one row of 131,072 keys 51, 51 and 49.)
+constexpr int kSpanTiles = 8;
+// A span holds at least so many bytes of keys and values, and of 8-bit pages at least two tiles, for a unit has costs of its
+// own, of which those of the softmax warps show most with 8-bit pages.  (bf16 pages, 64 and 128 KiB, 32/8 heads of 128: one
+// row of 1,000 keys 8.1 and 8.9 us, 64 rows of 500 30.3 and 29.8.  8-bit pages of 2, 3 and 4 tiles of 32 KiB, 32/4 heads of
+// 128: one row of 2,000 keys 9.8, 10.2 and 11.0, 64 rows of 4,000 61, 54 and 50; of 1 and 2 tiles of 64 KiB, 24/2 heads of 256:
+// one row of 1,000 11.3 and 12.9, 64 rows of 1,000 37 and 26.)
+__host__ __device__ constexpr int fewest_bytes(int e4m3) { return e4m3 ? 98304 : 65536; }
+// A row is cut into this many units over its key heads, or twice as many, .., as spans of kSpanTiles allow: fewer than the
+// SMs, for two thirds of them read as fast as all.  (With 152, 100 and 76: 7 rows of up to 40,000 keys, 8-bit pages, 40.5,
+// 36.9 and 37.5 us; one row of 8,000 keys, 32/8 heads of 128, 14.2, 14.3 and 15.4.)
+constexpr int kFill = 100;
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
 constexpr int kPagedGrid = 256;      // CTAs of a launch at most
-constexpr int kInTurn = 8;           // units a CTA up to which they are taken in turn
-constexpr int kJobs = 4;             // jobs a CTA, at least
-constexpr int kFewestBytes = 65536;
-constexpr int kSpanTiles = 8;        // at most (their scores fit tensor memory twice, beside O)
+// Units go to the CTAs in turn up to kInTurn a CTA, beyond that by a counter, in jobs of about 256 KiB of units and kJobs a CTA
+// at least.  (In turn up to 2, 8 and 16 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 21.3, 20.0 and 19.9 us; a ragged batch's
+// last units wait longer.  By jobs of one unit 64 rows of 4,000 keys, 32/4 heads, 8-bit pages, took 151 us, by these then 65;
+// with jobs of 1 MiB 256 rows of 300, 32/8 heads, bf16 pages, take 72, not 67.)
+constexpr int kInTurn = 8;
+constexpr int kJobs = 4;
 
 // How a row is cut: spans of `each` tiles, the first `more` of them of one more.  (Without runtime divisions: as two of 64
 // bits and two of 32 this took 2,000 cycles, and each unit's publication waited for it.)
-// Tiles of a span at least: 64 KiB of keys and values.
-__host__ __device__ constexpr int fewest_tiles(int d, int e4m3) { return d * (e4m3 ? 1 : 2) >= kFewestBytes / 256 ? 1 : kFewestBytes / 256 / (d * (e4m3 ? 1 : 2)); }
+__host__ __device__ constexpr int fewest_tiles(int d, int e4m3) {
+    const int tiles = fewest_bytes(e4m3) / (2 * kPTile * d * (e4m3 ? 1 : 2)), least = e4m3 ? 2 : 1;
+    return tiles > least ? tiles : least;
+}
 struct RowCut {
     int lo, k0, tiles, spans, each, more;      // lo: the first visible key; k0: the first tile's first key
 };
@@ -147,14 +160,18 @@ struct PagedCfg {
     static constexpr bool F8 = F8_;
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int HV = D / 128;                   // loads a tile and operand: 128 keys x 128 dims each,
+    static constexpr int UNROLL = GP == 16 ? 1 : HV;     // (the most code: see the softmax's)
     static constexpr int KB = ESZ;                       // in blocks of 128 bytes of a key,
     static constexpr int SLOT = kPTile * KB * 128;       // as [16 groups of 8 keys][KB][8][128 bytes]
-    static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;   // slots of K, and of V: as many as leave room for P
+    // slots of K, and of V: as many as leave room for P.  (Of 96 KB together instead of 192: one row of 131,072 keys 50.3 us,
+    // now 49.5; a batch 312, now 308.)
+    static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
     // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
     static constexpr int QN = F8 && GP == 16 ? 32 : 16;
     __host__ __device__ static constexpr int lo_row() { return QN / 2; }
-    static constexpr int Q_WARPS = GP == 16 ? 3 : 1;     // that stage a unit's queries
+    static constexpr int Q_WARPS = GP == 16 ? 3 : 1;     // that stage a (row, key head)'s queries
+    static constexpr int Q_READERS = GP == 16 ? 3 : 2;   // that look at each unit for it
     static constexpr int Q_BYTES = QN * D * ESZ;         // [D * ESZ / 128][QN / 8][8][128 bytes]
     static constexpr int PARTS = F8 ? 3 : 2;
     static constexpr int PN = (PARTS * GP + 15) / 16 * 16;
@@ -181,7 +198,7 @@ struct PagedCfg {
     static constexpr int OFF_LAST = OFF_PRE + (ROWS + 4) * 4;        // last positions
     static constexpr int OFF_EACH = OFF_LAST + ROWS * 4;              // tiles of a row's spans, a byte each
     static constexpr int OFF_X = OFF_EACH + ROWS;                     // [group][4 warps][16] maxima
-    static constexpr int OFF_C = OFF_X + 512;                // [UNITS][16] c of each head (8-bit)
+    static constexpr int OFF_C = OFF_X + 512;                // [n mod UNITS][16] c of each head (8-bit)
     static constexpr int OFF_BAR = OFF_C + (F8 ? UNITS * 64 : 0);
     static constexpr int B_FULL = 0;                         // [K, V][NSLOT]
     static constexpr int B_FREE = B_FULL + 2 * NSLOT;
@@ -189,12 +206,12 @@ struct PagedCfg {
     static constexpr int B_PFULL = B_SFULL + 2;              // [group][NP]
     static constexpr int B_PVDONE = B_PFULL + 2 * NP;
     static constexpr int B_SFREE = B_PVDONE + 2 * NP;        // [group]: the unit's scores have been read
-    static constexpr int B_QFULL = B_SFREE + 2;              // [unit & 1]
+    static constexpr int B_QFULL = B_SFREE + 2;              // [n & 1]
     static constexpr int B_QFREE = B_QFULL + 2;
     static constexpr int B_UFULL = B_QFREE + 2;              // [unit mod UNITS] from here
     static constexpr int B_UFREE = B_UFULL + UNITS;
     static constexpr int B_UTOOK = B_UFREE + UNITS;        // the producer has begun the unit
-    static constexpr int B_UC = B_UTOOK + UNITS;           // the unit's c are there (8-bit)
+    static constexpr int B_UC = B_UTOOK + UNITS;           // [n mod UNITS]: c are there (8-bit)
     static constexpr int B_DRAIN = B_UC + UNITS;
     static constexpr int NBAR = B_DRAIN + 2;                 // [S, P V]
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;      // tensor-memory base
@@ -207,18 +224,18 @@ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u 
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
 
 // One tcgen05.mma, descriptors as two halves of which only the low one (the address) changes.
-template <bool F8, uint32_t A_HI, uint32_t B_HI, bool ACC>
-__device__ __forceinline__ void paged_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+template <bool F8, uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void paged_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool more) {
     if constexpr (F8)
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
             "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}"
-            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(A_HI), "n"(B_HI));
+            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(more ? 1u : 0u), "n"(A_HI), "n"(B_HI));
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
             "setp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
-            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(A_HI), "n"(B_HI));
+            :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(more ? 1u : 0u), "n"(A_HI), "n"(B_HI));
 }
 
 // Instruction descriptor: fp32 accumulator, bf16 or e4m3 operands, B K-major.
@@ -321,6 +338,19 @@ __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
     return __half22float2(__half2(h));
 }
 
+// warp_wait in less code (see the softmax's).
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, int* status) {
+    bool ok = mbar_try(bar, parity);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+        const uint64_t t0 = globaltimer();
+#pragma unroll 1
+        while (!(ok = mbar_try(bar, parity)) && globaltimer() - t0 <= kWaitLimitNs) {}
+        if (!ok) atomicOr(status, WA_STATUS_TIMEOUT);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    return ok;
+}
+
 // Clears what a call counts; the next kernel sets itself up meanwhile.
 __global__ void __launch_bounds__(1024) paged_clear_kernel(int* taken, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -329,9 +359,9 @@ __global__ void __launch_bounds__(1024) paged_clear_kernel(int* taken, int n) {
 }
 static_assert(65535 / kPagedFewest < 1024, "a counter a thread");
 
-// A published unit.  nt = 0 marks the end.
+// A published unit.  nt = 0 marks the end; n counts the (row, key head)s so far, whose queries are staged one after another.
 struct PUnit {
-    int row, g, span, spans, k0, nt, lo, p;
+    int row, g, span, k0, nt, lo, p, n;
 };
 
 template <int D, bool F8, int GP>
@@ -360,7 +390,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         int count = 1;
         if (i >= C::B_PFULL && i < C::B_PVDONE) count = 4;                    // a group's softmax warps
         else if (i >= C::B_SFREE && i < C::B_QFULL) count = 4;
-        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8 + C::Q_WARPS;       // producers, MMA, Q, softmax warps
+        else if (i >= C::B_UFREE && i < C::B_UTOOK) count = 8 + C::Q_READERS;       // producers, MMA, Q, softmax warps
         else if (i >= C::B_QFULL && i < C::B_QFREE) count = C::Q_WARPS;
         else if (i >= C::B_UC && i < C::B_DRAIN) count = C::Q_WARPS;
         mbar_init(BAR(i), count);
@@ -373,14 +403,14 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     // The queries and the table, a line a thread, into L2: once the keys stream, a read that has to go to memory waits
     // behind them (a batch of 64 rows, 32/8 heads of 128: 309 us without this, 301 with it).
     {
-        const int64_t i = static_cast<int64_t>(blockIdx.x) * kPThreads + tid;
-        const int q_lines = p.a.hq * D / 64, t_lines = (p.a.most + 31) / 32;
-        const int64_t q_all = static_cast<int64_t>(p.rows) * q_lines, t_all = static_cast<int64_t>(p.rows) * t_lines;
+        // (at most 2^8 rows of 2^22 lines each: 32 bits)
+        const uint32_t i = blockIdx.x * kPThreads + tid, rows = p.rows;
+        const uint32_t q_lines = p.a.hq * (D / 64), t_lines = (p.a.most + 31) / 32, q_all = rows * q_lines, t_all = rows * t_lines;
         if (i < q_all) {
-            prefetch_l2(static_cast<const uint16_t*>(p.a.q) + (p.row0 + i / q_lines) * p.a.q_row + i % q_lines * 64);
+            prefetch_l2(static_cast<const uint16_t*>(p.a.q) + (p.row0 + static_cast<int64_t>(i / q_lines)) * p.a.q_row + i % q_lines * 64);
         } else if (i < q_all + t_all) {
-            const int64_t e = i - q_all;
-            prefetch_l2(p.a.table + (p.row0 + e / t_lines) * p.a.table_row + e % t_lines * 32);
+            const uint32_t e = i - q_all;
+            prefetch_l2(p.a.table + (p.row0 + static_cast<int64_t>(e / t_lines)) * p.a.table_row + e % t_lines * 32);
         }
     }
     for (int e = tid; e < (2 * C::Q_BYTES + 2 * C::NP * C::P_BYTES) / 16; e += kPThreads)
@@ -432,7 +462,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     auto uph = [](int U) { return static_cast<uint32_t>(U / C::UNITS) & 1u; };
     auto read_unit = [&](int U, PUnit& x) {
         volatile int* e = unit_ints(U);
-        x.row = e[0]; x.g = e[1]; x.span = e[2]; x.spans = e[3]; x.k0 = e[4]; x.nt = e[5]; x.lo = e[6]; x.p = e[7];
+        x.row = e[0]; x.g = e[1]; x.span = e[2]; x.k0 = e[3]; x.nt = e[4]; x.lo = e[5]; x.p = e[6]; x.n = e[7];
     };
     const int pieces = kPTile / p.align;          // copies a tile
 
@@ -469,10 +499,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             const int x3 = __shfl_sync(0xFFFFFFFFu, hi ? c3[1] : c3[0], from), x4 = __shfl_sync(0xFFFFFFFFu, hi ? c4[1] : c4[0], from);
             const uint32_t wanted = (__ballot_sync(0xFFFFFFFFu, hi ? want[1] : want[0]) >> (first & 31)) & ((1u << pieces) - 1u);
             const uint32_t bytes = __popc(wanted) * p.align * C::KB * 128;
-#pragma unroll
+#pragma unroll(C::UNROLL)
             for (int half = 0; half < C::HV; ++half) {
                 const int at_s = side * C::NSLOT + s;
-                if (use > 0 && !warp_wait(BAR(C::B_FREE + at_s), (use - 1) & 1, status)) return false;
+                if (use > 0 && !paged_wait(BAR(C::B_FREE + at_s), (use - 1) & 1, status)) return false;
                 // (a copy may land before the barrier is told how much to expect: its one arrival is still to come)
                 if (lane == 0) mbar_arrive_expect_tx(BAR(C::B_FULL + at_s), bytes);
                 if ((wanted >> lane) & 1u)
@@ -487,16 +517,19 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             return true;
         };
         PUnit x;
+#pragma unroll 1
         for (int U = 0;; ++U) {
-            if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
+            if (!paged_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
             read_unit(U, x);
             if (x.nt <= 0) break;
             look_up(U, x);
             bool ok = true;
+#pragma unroll 1
             for (int i = 0; ok && i < x.nt; ++i) ok = load(i);
             if (!ok) break;
         }
         // the copies in flight land before the block exits, whichever role stopped early
+#pragma unroll 1
         for (int i = max(0, loads - C::NSLOT); i < loads; ++i)
             if (!mbar_wait(BAR(C::B_FULL + side * C::NSLOT + i % C::NSLOT), static_cast<uint32_t>(i / C::NSLOT) & 1u, status)) break;
     } else if (warp == 1 || warp == 13) {
@@ -515,27 +548,35 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         };
         PUnit x;
         auto take = [&](int U) -> bool {
-            if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) return false;
+            if (!paged_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) return false;
             read_unit(U, x);
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             x.nt = __shfl_sync(0xFFFFFFFFu, x.nt, 0);
+            x.n = __shfl_sync(0xFFFFFFFFu, x.n, 0);
             return x.nt > 0;
         };
         if (warp == 1) {
             // S^T = K Q^T
             bool ok = true;
+            int n = 0;
             for (int U = 0; ok && take(U); ++U) {
+                if (x.n != n) {                   // the queries before are done with
+                    if (leader) mma_commit(BAR(C::B_QFREE + (n & 1)));
+                    __syncwarp();
+                    n = x.n;
+                }
                 // the group's last scores have been read, this unit's queries are there
-                if (U >= 2 && !warp_wait(BAR(C::B_SFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
-                if (!warp_wait(BAR(C::B_QFULL + (U & 1)), static_cast<uint32_t>(U >> 1) & 1u, status)) break;
+                if (U >= 2 && !paged_wait(BAR(C::B_SFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
+                if (!paged_wait(BAR(C::B_QFULL + (n & 1)), static_cast<uint32_t>(n >> 1) & 1u, status)) break;
                 tc_fence_after();
-                const uint32_t q0 = desc_lo(sbase + C::OFF_Q + (U & 1) * C::Q_BYTES, 16);
+                const uint32_t q0 = desc_lo(sbase + C::OFF_Q + (n & 1) * C::Q_BYTES, 16);
+#pragma unroll 1
                 for (int idx = 0; ok && idx < x.nt; ++idx) {
                     const uint32_t d = tb + C::s_col(U & 1) + idx * 16;
-#pragma unroll
+#pragma unroll(C::UNROLL)
                     for (int half = 0; half < C::HV; ++half) {
-                        if (!(ok = warp_wait(BAR(C::B_FULL + s), use & 1, status))) break;
+                        if (!(ok = paged_wait(BAR(C::B_FULL + s), use & 1, status))) break;
                         if (leader) {
                             const uint32_t k = desc_lo(SLOT(s), 16), q = q0 + ((half * C::KB * C::QN * 128) >> 4);
 #pragma unroll
@@ -544,8 +585,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                                 for (int i = 0; i < 128 / C::KSTEP; ++i) {
                                     const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
                                     const uint32_t b = q + (((i / 4) * C::QN * 128 + set * 2048 + (i % 4) * 32) >> 4);
-                                    if (half == 0 && set == 0 && i == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idS);
-                                    else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idS);
+                                    paged_mma<F8, kTileHi, kSmallHi>(d, a, b, idS, half > 0 || set > 0 || i > 0);
                                 }
                             mma_commit(BAR(C::B_FREE + s));
                         }
@@ -553,10 +593,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                         next_slot();
                     }
                 }
-                if (ok && leader) {
-                    mma_commit(BAR(C::B_SFULL + (U & 1)));
-                    mma_commit(BAR(C::B_QFREE + (U & 1)));
-                }
+                if (ok && leader) mma_commit(BAR(C::B_SFULL + (U & 1)));
                 __syncwarp();
             }
         } else {
@@ -566,15 +603,17 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             for (int U = 0; ok && take(U); ++U) {
                 const int group = U & 1;
                 int tg = group ? tp[1] : tp[0];
+#pragma unroll 1
                 for (int idx = 0; ok && idx < x.nt; ++idx, ++tg) {
                     const int buf = group * C::NP + tg % C::NP;
                     // keys from .. to - 1 of the tile are visible
                     const int key0 = x.k0 + idx * kPTile, from = max(0, x.lo - key0), to = min(kPTile, x.p - key0 + 1);
-#pragma unroll
+#pragma unroll(C::UNROLL)
                     for (int half = 0; half < C::HV; ++half) {
-                        if (!(ok = warp_wait(BAR(C::B_FULL + s), use & 1, status))) break;
+                        if (!(ok = paged_wait(BAR(C::B_FULL + s), use & 1, status))) break;
                         if (from > 0 || to < kPTile) {
                             const int nz = from + kPTile - to;
+#pragma unroll 1
                             for (int e = lane; e < nz * C::KB * 8; e += 32) {
                                 const int zr = e / (C::KB * 8), rem = e % (C::KB * 8), key = zr < from ? zr : to + (zr - from);
                                 st_shared_v4(SLOT(s) + (key >> 3) * (C::KB * 1024) + (rem >> 3) * 1024 + (key & 7) * 128 + (rem & 7) * 16, 0u, 0u, 0u, 0u);
@@ -583,7 +622,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                             __syncwarp();
                         }
                         if (half == 0) {
-                            if (!(ok = warp_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tg / C::NP) & 1u, status))) break;
+                            if (!(ok = paged_wait(BAR(C::B_PFULL + buf), static_cast<uint32_t>(tg / C::NP) & 1u, status))) break;
                             tc_fence_after();
                         }
                         if (leader) {
@@ -592,8 +631,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 #pragma unroll
                             for (int i = 0; i < kPTile / C::KSTEP; ++i) {
                                 const uint32_t a = v + ((i * (C::KSTEP / 8) * C::KB * 1024) >> 4), b = pp + (((i / 4) * C::P_CHUNK + (i % 4) * 32) >> 4);
-                                if (i == 0 && idx == 0) paged_mma<F8, kTileHi, kSmallHi, false>(d, a, b, idO);
-                                else paged_mma<F8, kTileHi, kSmallHi, true>(d, a, b, idO);
+                                paged_mma<F8, kTileHi, kSmallHi>(d, a, b, idO, i > 0 || idx > 0);
                             }
                             mma_commit(BAR(C::B_FREE + s));
                             if (half == C::HV - 1) mma_commit(BAR(C::B_PVDONE + buf));
@@ -614,102 +652,101 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ units
-        // In turn, or in jobs of about kSpanTiles tiles that a counter gives out.  A unit's pages are asked for before the unit
-        // ahead of it is published, where units are small (one after another they came every 2 to 3 us: 64 rows of 4,000
-        // keys, 8-bit pages, 151 us), and otherwise no earlier than its turn comes, so that the last ones go to whoever is free.
+        // In turn, or in jobs that a counter gives out.  A unit's pages are asked for once the producer has
+        // begun the unit before: no earlier, so that the last units go to whoever is free.
         const int units = pre[p.rows] * p.a.hkv;
         const int ctas = static_cast<int>(gridDim.x);
-        const int job = max(1, min(min(16, units / (kJobs * ctas)), C::JOB_TILES * pre[p.rows] / max(tiles, 1)));
         const bool in_turn = !p.next_unit || units <= kInTurn * ctas;
-        // unit k is span s (of all rows'), key head g; the row and what it is cut into are kept from one unit to the next
-        int k = 0, s = 0, g = 0, in_job = 0, row = -1;
+        int job = 1;
+        if (!in_turn) {
+            const float of_tiles = static_cast<float>(C::JOB_TILES) * static_cast<float>(pre[p.rows]) / static_cast<float>(max(tiles, 1));
+            job = max(1, min(min(16, units / (kJobs * ctas)), static_cast<int>(of_tiles)));
+        }
+        // A row's units are numbered span by span of each key head where they come in jobs, so that a job's queries are often
+        // those of the unit before and are not staged again (64 rows of 2,000 keys, 32/8 heads of 128, 88 us, then 85; of 4,000,
+        // 24/2 heads of 256, 8-bit pages, 74, then 67), and otherwise key head by key head of each span.
+        int k = 0, in_job = 0, row = -1, s = 0, g = 0;       // span s of the row, key head g
         int last = 0, lo = 0, k00 = 0, each = 0, more = 0, first = 0, spans = 0;
-        const int turn_s = ctas / p.a.hkv, turn_g = ctas - turn_s * p.a.hkv;
-        auto jump = [&](int to) {
-            k = to;
-            s = static_cast<int>(static_cast<uint32_t>(k) / static_cast<uint32_t>(p.a.hkv));
-            g = k - s * p.a.hkv;
-        };
-        jump(static_cast<int>(blockIdx.x) * (in_turn ? 1 : job));
-        int asked = -1;                           // lane 0: the next job's number
-        bool pending = false;
-        auto ask = [&]() {
-            if (lane == 0) asked = atomicAdd(p.next_unit, 1);
-            pending = true;
-        };
-        PUnit cur, nxt;
-        int id[2], id_next[2];                    // the unit's pages `lane` and `lane` + 32
+        bool moved = true;                                    // s and g are not those of k
+        PUnit cur;
+        int id[2];                                // the unit's pages `lane` and `lane` + 32
         static_assert(C::PAGES <= 64, "two pages a lane");
-        auto look_up = [&](PUnit& x, int (&ids)[2]) {
+        auto look_up = [&]() {
+            PUnit& x = cur;
             x.nt = 0;
             if (k >= units) return;
-            if (static_cast<uint32_t>(s - first) >= static_cast<uint32_t>(spans)) {       // another row: pre[row] <= s < pre[row + 1]
-                if (row >= 0 && s == first + spans && pre[row + 2] > s) {
-                    ++row;
-                } else {
-                    int a = 0, b = p.rows;
+            if (static_cast<uint32_t>(k - first) >= static_cast<uint32_t>(spans * p.a.hkv)) {
+                int a = row + 1, b = p.rows;          // pre[row] hkv <= k < pre[row + 1] hkv
+                if (row < 0 || k < first || k >= pre[row + 2] * p.a.hkv) {
+                    a = 0;
+#pragma unroll 1
                     while (b - a > 1) {
                         const int m = (a + b) >> 1;
-                        if (pre[m] <= s) a = m; else b = m;
+                        if (pre[m] * p.a.hkv <= k) a = m; else b = m;
                     }
-                    row = a;
                 }
-                first = pre[row];
-                spans = pre[row + 1] - first;
+                row = a;
+                first = pre[row] * p.a.hkv;
+                spans = pre[row + 1] - pre[row];
                 last = lasts[row];
                 lo = p.a.win > 0 ? max(0, last - p.a.win + 1) : 0;
                 k00 = lo & ~(p.align - 1);
                 each = smem[C::OFF_EACH + row];
                 more = (last - k00) / kPTile + 1 - each * spans;
+                moved = true;
             }
+            if (moved) {
+                const uint32_t at = k - first;
+                if (in_turn) {
+                    s = at / static_cast<uint32_t>(p.a.hkv);
+                    g = at - s * p.a.hkv;
+                } else {
+                    g = at / static_cast<uint32_t>(spans);
+                    s = at - g * spans;
+                }
+                moved = false;
+            }
+            x.n += x.row != p.row0 + row || x.g != g;
             x.row = p.row0 + row;
             x.g = g;
             x.p = last;
             x.lo = lo;
-            x.spans = spans;
-            x.span = s - first;
+            x.span = s;
             x.nt = each + (x.span < more ? 1 : 0);
             x.k0 = k00 + (x.span * each + min(x.span, more)) * kPTile;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = lane + 32 * e, key = x.k0 + i * p.align;
-                ids[e] = -2;                      // without a visible key: nothing is copied
-                if (i < x.nt * pieces && key <= last && key + p.align > lo) ids[e] = max(-1, p.a.table[x.row * p.a.table_row + (key >> p.a.page_log)]);
+                id[e] = -2;                      // without a visible key: nothing is copied
+                if (i < x.nt * pieces && key <= last && key + p.align > lo) id[e] = max(-1, p.a.table[x.row * p.a.table_row + (key >> p.a.page_log)]);
             }
         };
         auto step = [&]() {                       // the next unit's number
             if (in_turn) {
                 k += ctas;
-                s += turn_s;
-                g += turn_g;
-                if (g >= p.a.hkv) {
-                    g -= p.a.hkv;
-                    ++s;
-                }
+                moved = true;
             } else if (++in_job < job) {
                 ++k;
-                if (++g == p.a.hkv) {
-                    g = 0;
-                    ++s;
+                if (++s == spans) {
+                    s = 0;
+                    ++g;
                 }
             } else {
-                if (!pending) ask();
-                jump((__shfl_sync(0xFFFFFFFFu, asked, 0) + ctas) * job);
+                int asked = 0;
+                if (lane == 0) asked = atomicAdd(p.next_unit, 1);
+                k = (__shfl_sync(0xFFFFFFFFu, asked, 0) + ctas) * job;
+                moved = true;
                 in_job = 0;
-                pending = false;
             }
         };
-        look_up(cur, id);
+        k = static_cast<int>(blockIdx.x) * (in_turn ? 1 : job);
+        cur.row = cur.g = cur.n = -1;
         bool ended = false;
+#pragma unroll 1
         for (int U = 0;; ++U) {
-            const bool small = cur.nt < kSmallUnit;
-            if (small && cur.nt > 0) {
-                step();
-                look_up(nxt, id_next);
-                if (!in_turn && in_job == job - 1) ask();        // the job after: a unit before it is needed
-            }
+            look_up();
             // the slot's last unit has been read by everyone
-            if (U >= C::UNITS && !warp_wait(BAR(C::B_UFREE + U % C::UNITS), uph(U - C::UNITS), status)) break;
+            if (U >= C::UNITS && !paged_wait(BAR(C::B_UFREE + U % C::UNITS), uph(U - C::UNITS), status)) break;
             if (cur.nt > 0) {
                 volatile int* ids = unit_pages(U);
 #pragma unroll
@@ -724,7 +761,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             }
             if (lane == 0) {
                 volatile int* x = unit_ints(U);
-                x[0] = cur.row; x[1] = cur.g; x[2] = cur.span; x[3] = cur.spans; x[4] = cur.k0; x[5] = cur.nt; x[6] = cur.lo; x[7] = cur.p;
+                x[0] = cur.row; x[1] = cur.g; x[2] = cur.span; x[3] = cur.k0; x[4] = cur.nt; x[5] = cur.lo; x[6] = cur.p; x[7] = cur.n;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFULL + U % C::UNITS));
@@ -733,34 +770,37 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 ended = true;
                 continue;
             }
-            const int begun = small ? U - C::UNITS / 4 : U;      // the producer has begun it
-            if (begun >= 0 && !warp_wait(BAR(C::B_UTOOK + begun % C::UNITS), uph(begun), status)) break;
-            if (!small) {
-                step();
-                look_up(nxt, id_next);
-            }
-            cur = nxt;
-            id[0] = id_next[0];
-            id[1] = id_next[1];
+            if (!paged_wait(BAR(C::B_UTOOK + U % C::UNITS), uph(U), status)) break;
+            step();
         }
     } else if (warp >= 12) {
         // ------------------------------------------------ Q: four heads at a time, in a loop, which a unit -1 of no heads
         // goes through first: its code comes in while nothing else is asked of the memory.  (All heads' code in a row, 16
         // heads split in two, came line by line behind the first keys: 6 us to the first product.)
         constexpr int EL = D / 32;                // values a lane and head
-        // up to 8 heads: a warp the even units, one the odd ones; 16: three warps every unit
+        // up to 8 heads: a warp every other (row, key head); 16: three warps all
         constexpr bool ALL = C::Q_WARPS > 1;
         const int turn = ALL && warp > 12 ? warp - 13 : 0;
+        const int mine = warp == 12 ? 0 : 1;      // of what this warp stages, unless ALL
         PUnit x;
         x.row = x.g = 0;
-        for (int U = ALL ? -1 : warp == 12 ? -2 : -1; ALL || warp != 15; U += ALL ? 1 : 2) {
+        int n = -1;
+        for (int U = -1; ALL || warp != 15; ++U) {
             int live = 0;                         // heads (the buffer's other rows: zeros)
             if (U >= 0) {
-                if (!warp_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
+                if (!paged_wait(BAR(C::B_UFULL + U % C::UNITS), uph(U), status)) break;
                 read_unit(U, x);
                 if (x.nt <= 0) break;
+                x.n = __shfl_sync(0xFFFFFFFFu, x.n, 0);
+                if (x.n == n || (!ALL && (x.n & 1) != mine)) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
+                    continue;
+                }
+                n = x.n;
                 live = G;
             }
+            const int at_q = U < 0 ? mine : n;
             const uint16_t* q = static_cast<const uint16_t*>(p.a.q) + x.row * p.a.q_row + static_cast<int64_t>(x.g) * G * D + lane * EL;
             uint32_t raw[4][EL / 2];
             auto fetch = [&](int h0) {
@@ -783,9 +823,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             float c = p.a.scale * 1.4426950408889634f;
             if constexpr (F8) c *= p.a.kv[0].scale ? p.a.kv[0].scale[x.g] : 1.f;
             const bool neg = c < 0.f;             // the sign goes into Q, exactly
-            // the buffer's last unit's S have been worked out
-            if (U >= 2 && !warp_wait(BAR(C::B_QFREE + (U & 1)), static_cast<uint32_t>((U >> 1) - 1) & 1u, status)) break;
-            const uint32_t dst = sbase + C::OFF_Q + (U & 1) * C::Q_BYTES;
+            // the scores by the buffer's last queries have been worked out
+            if (U >= 0 && n >= 2 && !paged_wait(BAR(C::B_QFREE + (n & 1)), static_cast<uint32_t>((n >> 1) - 1) & 1u, status)) break;
+            const uint32_t dst = sbase + C::OFF_Q + (at_q & 1) * C::Q_BYTES;
 #pragma unroll 1
             for (int h0 = 4 * turn; h0 < GP; h0 += 4 * C::Q_WARPS) {
                 uint32_t now[4][EL / 2];
@@ -844,15 +884,15 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                             st_shared_u32(al + 4 * w, fine ? rest : 0u);
                         }
                         if (lane == i)
-                            reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U & (C::UNITS - 1)) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
+                            reinterpret_cast<volatile float*>(smem + C::OFF_C)[(at_q & (C::UNITS - 1)) * 16 + h] = fabsf(c) * __int_as_float((127 - k) << 23);
                     }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && U >= 0) {
-                mbar_arrive(BAR(C::B_QFULL + (U & 1)));
-                if constexpr (F8) mbar_arrive(BAR(C::B_UC + U % C::UNITS));
+                mbar_arrive(BAR(C::B_QFULL + (n & 1)));
+                if constexpr (F8) mbar_arrive(BAR(C::B_UC + n % C::UNITS));
                 mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             }
             __syncwarp();
@@ -864,50 +904,65 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         volatile float* xbuf = reinterpret_cast<volatile float*>(smem + C::OFF_X) + group * 64;
         const uint32_t x_addr = sbase + C::OFF_X + group * 256;
         constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
+        // Sixteen heads go through the code of eight twice, with their values exchanged in between: the warps' roles are more
+        // code than the instruction cache holds, and waited for it (64 rows of 4,000 keys, 24/2 heads of 256, 8-bit pages, 66 us,
+        // then 60; one such row 12.7, then 13.2).
+        constexpr int H = GP == 16 ? 8 : GP, TURNS = GP / H;
+        auto turn = [](float (&x)[GP]) {
+#pragma unroll
+            for (int h = 0; h < GP / 2; ++h) {
+                if constexpr (TURNS == 2) {
+                    const float y = x[h];
+                    x[h] = x[h + H];
+                    x[h + H] = y;
+                }
+            }
+        };
         // A wait that runs out does not take a warp from the others' barriers: it carries on without waiting until the
         // next vote, at which the four warps leave together.
         bool dead = false;
         auto wait = [&](int bar, uint32_t ph) {
-            if (!dead && !warp_wait(BAR(bar), ph, status)) dead = true;
+            if (!dead && !paged_wait(BAR(bar), ph, status)) dead = true;
         };
         const uint32_t pk = quarter * 32 + lane;         // this thread's key: its column of P
         const uint32_t s_addr = tbase + lane_addr + C::s_col(group);
         const uint32_t o_addr = tbase + lane_addr + C::o_col(group);
         int t = 0;                                       // the group's tiles
+#pragma unroll 1
         for (int U = group;; U += 2) {
             PUnit x;
             wait(C::B_UFULL + U % C::UNITS, uph(U));
             read_unit(U, x);
-            float c[F8 ? GP : 1];
+            float c[GP];
             if constexpr (F8) {
-                if (!dead && x.nt > 0) wait(C::B_UC + U % C::UNITS, uph(U));
+                if (!dead && x.nt > 0) wait(C::B_UC + x.n % C::UNITS, uph(x.n));
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
-                    c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(U % C::UNITS) * 16 + h] : 0.f;
+                    c[h] = h < G ? reinterpret_cast<volatile float*>(smem + C::OFF_C)[(x.n % C::UNITS) * 16 + h] : 0.f;
             } else {
-                c[0] = p.c;
+                c[0] = p.c;                     // (of every head)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_UFREE + U % C::UNITS));
             if (group_any(group, dead) || x.nt <= 0) break;
             wait(C::B_SFULL + group, static_cast<uint32_t>(U >> 1) & 1u);
             tc_fence_after();
-            // a tile's scores of this thread's key, times c
-            auto scores = [&](int idx, float (&y)[GP]) {
+            // a tile's scores of this thread's key and heads from h0 on, times c
+            auto scores = [&](int idx, int h0, float (&y)[H]) {
                 if constexpr (F8 && GP < 16) {
-                    uint32_t r[GP], q[GP];
+                    uint32_t r[H], q[H];
                     tm_load(s_addr + idx * 16, r);
                     tm_load(s_addr + idx * 16 + C::lo_row(), q);
                     tm_wait(r);
                     tm_wait(q);
 #pragma unroll
-                    for (int h = 0; h < GP; ++h) y[h] = (__uint_as_float(r[h]) + __uint_as_float(q[h])) * c[h];
+                    for (int h = 0; h < H; ++h) y[h] = (__uint_as_float(r[h]) + __uint_as_float(q[h])) * c[h];
                 } else {
-                    uint32_t r[GP];
-                    tm_load(s_addr + idx * 16, r);
+                    uint32_t r[H];
+                    tm_load(s_addr + idx * 16 + h0, r);
                     tm_wait(r);
 #pragma unroll
-                    for (int h = 0; h < GP; ++h) y[h] = __uint_as_float(r[h]) * c[F8 ? h : 0];
+                    for (int h = 0; h < H; ++h) y[h] = __uint_as_float(r[h]) * c[F8 ? h : 0];
                 }
             };
             auto visible = [&](int idx) {
@@ -917,21 +972,24 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             // ---- the maximum of each head over the unit (of -inf where there is none: NaN then, worked out again)
             float m[GP], l[GP];
 #pragma unroll
-            for (int h = 0; h < GP; ++h) {
-                m[h] = -INFINITY;
-                l[h] = 0.f;
-            }
-            for (int idx = 0; idx < x.nt; ++idx) {
-                float y[GP];
-                scores(idx, y);
-                if (visible(idx)) {
+            for (int h = 0; h < GP; ++h) l[h] = 0.f;
+#pragma unroll 1
+            for (int h0 = 0; h0 < GP; h0 += H) {
+                float best[H];
 #pragma unroll
-                    for (int h = 0; h < GP; ++h) m[h] = fmaxf(m[h], y[h]);
+                for (int h = 0; h < H; ++h) best[h] = -INFINITY;
+#pragma unroll 1
+                for (int idx = 0; idx < x.nt; ++idx) {
+                    float y[H];
+                    scores(idx, h0, y);
+                    if (visible(idx)) {
+#pragma unroll
+                        for (int h = 0; h < H; ++h) best[h] = fmaxf(best[h], y[h]);
+                    }
                 }
-            }
-            {
-                const float best = reduce_each(m, [](float a, float b) { return fmaxf(a, b); });
-                if (lane % (32 / GP) == 0) xbuf[quarter * 16 + lane / (32 / GP)] = best;
+                const float top = reduce_each(best, [](float a, float b) { return fmaxf(a, b); });
+                if (lane % (32 / H) == 0) xbuf[quarter * 16 + h0 + lane / (32 / H)] = top;
+                if constexpr (F8) turn(c);
             }
             group_sync(group);
 #pragma unroll
@@ -945,57 +1003,65 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 m[h + 3] = fmaxf(fmaxf(e[0].w, e[1].w), fmaxf(e[2].w, e[3].w)) - kShift;
             }
             // ---- P, tile by tile
+#pragma unroll 1
             for (int idx = 0; idx < x.nt; ++idx, ++t) {
-                float s[GP];
-                scores(idx, s);
                 const bool vis = visible(idx);
+                const int buf = group * C::NP + t % C::NP;
+                const uint32_t pb = sbase + C::OFF_P + buf * C::P_BYTES;
+#pragma unroll 1
+                for (int h0 = 0; h0 < GP; h0 += H) {
+                    float s[H];
+                    scores(idx, h0, s);
 #pragma unroll
-                for (int h = 0; h < GP; ++h) {
-                    s[h] = vis ? ex2(s[h] - m[h]) : 0.f;
-                    l[h] += s[h];
-                }
-                // the parts of two heads each
-                uint32_t part[GP / 2][C::PARTS];
+                    for (int h = 0; h < H; ++h) {
+                        s[h] = vis ? ex2(s[h] - m[h]) : 0.f;
+                        l[h] += s[h];
+                    }
+                    // the parts of two heads each
+                    uint32_t part[H / 2][C::PARTS];
 #pragma unroll
-                for (int h = 0; h < GP; h += 2) {
-                    if constexpr (F8) {
-                        float a = s[h], b = s[h + 1];
+                    for (int h = 0; h < H; h += 2) {
+                        if constexpr (F8) {
+                            float a = s[h], b = s[h + 1];
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) {
-                            const uint32_t e = part[h / 2][i] = e4m3_pair(a, b);
-                            if (i < 2) {
-                                const float2 f = e4m3_pair_f32(e);
-                                a = (a - f.x) * 32.f;
-                                b = (b - f.y) * 32.f;
+                            for (int i = 0; i < 3; ++i) {
+                                const uint32_t e = part[h / 2][i] = e4m3_pair(a, b);
+                                if (i < 2) {
+                                    const float2 f = e4m3_pair_f32(e);
+                                    a = (a - f.x) * 32.f;
+                                    b = (b - f.y) * 32.f;
+                                }
+                            }
+                        } else {
+                            const uint32_t hi = part[h / 2][0] = pack_bf16(s[h], s[h + 1]);
+                            part[h / 2][1] = pack_bf16(s[h] - __uint_as_float(hi << 16), s[h + 1] - __uint_as_float(hi & 0xFFFF0000u));
+                        }
+                    }
+                    // the buffer's last product is done
+                    if (h0 == 0 && t >= C::NP) wait(C::B_PVDONE + buf, static_cast<uint32_t>(t / C::NP - 1) & 1u);
+                    // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row (h0 is 0 or whole groups of 8 rows)
+                    const uint32_t pr = pb + (h0 >> 3) * 1024;
+                    auto at = [&](int n) {
+                        if constexpr (F8) return pr + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4));
+                        else return pr + (pk >> 6) * C::P_CHUNK + (n >> 3) * 1024 + (n & 7) * 128 + (((pk & 63) * 2) ^ ((n & 7) << 4));
+                    };
+#pragma unroll
+                    for (int h = 0; h < H; h += 2)
+#pragma unroll
+                        for (int i = 0; i < C::PARTS; ++i) {
+                            const uint32_t v = part[h / 2][i];
+                            if constexpr (F8) {
+                                st_shared_u8(at(i * GP + h), v);
+                                st_shared_u8(at(i * GP + h + 1), v >> 8);
+                            } else {
+                                st_shared_u16(at(i * GP + h), v);
+                                st_shared_u16(at(i * GP + h + 1), v >> 16);
                             }
                         }
-                    } else {
-                        const uint32_t hi = part[h / 2][0] = pack_bf16(s[h], s[h + 1]);
-                        part[h / 2][1] = pack_bf16(s[h] - __uint_as_float(hi << 16), s[h + 1] - __uint_as_float(hi & 0xFFFF0000u));
-                    }
+                    turn(m);
+                    turn(l);
+                    if constexpr (F8) turn(c);
                 }
-                // the buffer's last product is done
-                const int buf = group * C::NP + t % C::NP;
-                if (t >= C::NP) wait(C::B_PVDONE + buf, static_cast<uint32_t>(t / C::NP - 1) & 1u);
-                const uint32_t pb = sbase + C::OFF_P + buf * C::P_BYTES;
-                // row n of P^T (part * GP + head), key pk: 128-byte rows, swizzled by the row
-                auto at = [&](int n) {
-                    if constexpr (F8) return pb + (n >> 3) * 1024 + (n & 7) * 128 + (pk ^ ((n & 7) << 4));
-                    else return pb + (pk >> 6) * C::P_CHUNK + (n >> 3) * 1024 + (n & 7) * 128 + (((pk & 63) * 2) ^ ((n & 7) << 4));
-                };
-#pragma unroll
-                for (int h = 0; h < GP; h += 2)
-#pragma unroll
-                    for (int i = 0; i < C::PARTS; ++i) {
-                        const uint32_t v = part[h / 2][i];
-                        if constexpr (F8) {
-                            st_shared_u8(at(i * GP + h), v);
-                            st_shared_u8(at(i * GP + h + 1), v >> 8);
-                        } else {
-                            st_shared_u16(at(i * GP + h), v);
-                            st_shared_u16(at(i * GP + h + 1), v >> 16);
-                        }
-                    }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -1020,25 +1086,28 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 wait(C::B_PVDONE + buf, static_cast<uint32_t>((t - 1) / C::NP) & 1u);
             }
             tc_fence_after();
-#pragma unroll
+#pragma unroll(C::UNROLL)
             for (int mb = 0; mb < C::HV; ++mb) {
-                float o[GP];
+                float* dst = p.part + unit * D + mb * 128 + quarter * 32 + lane;
+#pragma unroll 1
+                for (int h0 = 0; h0 < G; h0 += H) {
+                    uint32_t r[C::PARTS][H];
 #pragma unroll
-                for (int part = C::PARTS - 1; part >= 0; --part) {
-                    uint32_t r[GP];
-                    tm_load(o_addr + mb * C::PN + part * GP, r);
-                    tm_wait(r);
+                    for (int part = 0; part < C::PARTS; ++part) tm_load(o_addr + mb * C::PN + part * GP + h0, r[part]);
 #pragma unroll
-                    for (int h = 0; h < GP; ++h) {
-                        if (part == C::PARTS - 1) o[h] = __uint_as_float(r[h]);
-                        else o[h] = fmaf(o[h], F8 ? 0.03125f : 1.f, __uint_as_float(r[h]));
+                    for (int part = 0; part < C::PARTS; ++part) tm_wait(r[part]);
+                    float o[H];
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        o[h] = __uint_as_float(r[C::PARTS - 1][h]);
+#pragma unroll
+                        for (int part = C::PARTS - 2; part >= 0; --part) o[h] = fmaf(o[h], F8 ? 0.03125f : 1.f, __uint_as_float(r[part][h]));
                     }
-                }
-                const int dim = mb * 128 + quarter * 32 + lane;
 #pragma unroll
-                for (int h = 0; h < GP; ++h) {
-                    if (h >= G) break;
-                    p.part[(unit + h) * D + dim] = o[h];
+                    for (int h = 0; h < H; ++h) {
+                        if (h0 + h >= G) break;
+                        dst[(h0 + h) * D] = o[h];
+                    }
                 }
             }
         }
@@ -1350,7 +1419,11 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
         }
     }
 }
-constexpr int kMergeWide = 512;      // (row, head) pairs below which the first of them runs
+// (row, head) pairs below which the wide kernel runs.  (It, and the other one: one row of 131,072 keys, 32 heads of 128, 49.6 and
+// 66.3 us, 7 ragged rows, 24 heads of 256, 36.7 and 43.5, 4 rows of 32 14.4 and 15.3, 8 rows 16.2 and 15.3, 64 rows of 500 47 and
+// 30.)
+constexpr int kMergeWide = 256;
+
 
 bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
