@@ -414,7 +414,7 @@ typedef struct wa_rotary {
  *   out  [n, heads, d]  bf16, token stride out_tok, head stride d; x itself (with the
  *                       same stride) or memory that does not overlap it
  *
- * d is 128 or 256; pointers 16-byte aligned, token strides multiples of 8
+ * n >= 1; d is 128 or 256; pointers 16-byte aligned, token strides multiples of 8
  * elements and at least heads * d.  Returns WA_EINVAL otherwise.  No workspace.
  */
 int wa_rope(const void* x, const int32_t* pos, int32_t n, int32_t heads, int32_t d, const wa_rotary* rot,
@@ -463,9 +463,10 @@ typedef struct wa_pages {
  * A token that is left out has nothing written, q_out included.  Two tokens of
  * one call must not share a place of the cache (one sequence and position, or
  * sequences whose tables name one page there).  page_size is a power of two from
- * 16 to 256; hq % hkv == 0, hq / hkv <= 16, hq + 2 hkv <= 65535; no two elements of the k pages, and of
- * the v pages, may share memory; pointers 16-byte aligned, strides of the pages
- * multiples of 16 bytes, others of 8 elements.  Returns WA_EINVAL otherwise.
+ * 16 to 256; hq % hkv == 0, hq / hkv <= 16, hq + 2 hkv <= 65535; n >= 1; no two
+ * elements of the k pages, of the v pages, or of both (which is not checked), may
+ * share memory; pointers 16-byte aligned, strides of the pages multiples of 16
+ * bytes, others of 8 elements.  Returns WA_EINVAL otherwise.
  */
 int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int32_t n, int32_t hq,
                     const wa_pages* cache, const wa_rotary* rot, int64_t src_tok, int64_t q_tok, void* q_out,
@@ -497,9 +498,10 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  * which pages hold its keys, or `most`.  Slots past pos and before the window may
  * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /
  * hkv <= 16; strides of the pages multiples of 16 bytes, and the page stride a
- * multiple of 8 slot strides or of the head stride; rows * hq < 2^31.  Returns WA_EINVAL otherwise.  Calls
- * whose work can overlap need workspaces of their own; two captured graphs that
- * replay at the same time do too.
+ * multiple of 8 slot strides or of the head stride (a lone head's stride is not
+ * used); rows is 1 .. 65535 and rows * hq < 2^31.  Returns WA_EINVAL otherwise.
+ * Calls whose work can overlap need workspaces of their own; two captured graphs
+ * that replay at the same time do too.
  */
 int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_pages* cache, int32_t win, float scale,
                     int64_t q_row, int64_t out_row, void* out, void* ws, size_t ws_bytes, void* stream);

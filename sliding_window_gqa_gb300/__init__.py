@@ -97,7 +97,7 @@ class _Pages(ctypes.Structure):
 
 
 _lib = None
-_bind = False     # the short way to the drafted-token calls (csrc/wa_bind.cpp); None: there is none, False: not looked for
+_bind = False     # the short way to the drafted-token and paged-cache calls (csrc/wa_bind.cpp); None: there is none, False: not looked for
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 
@@ -178,7 +178,7 @@ def _short_way():
             _bind = module
         except (ImportError, OSError) as e:
             _bind = None
-            warnings.warn(f"{_BIND_PATH} cannot be used ({e}): the drafted-token calls take some microseconds longer",
+            warnings.warn(f"{_BIND_PATH} cannot be used ({e}): the drafted-token and paged-cache calls take some microseconds longer",
                           RuntimeWarning, stacklevel=3)
     return _bind
 

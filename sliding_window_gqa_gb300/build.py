@@ -89,7 +89,7 @@ def build(verbose: bool = False, extra=()) -> str:
     except Exception as e:
         if os.path.exists(BIND):        # an earlier build's, of other sources
             os.remove(BIND)
-        print(f"wa_bind.so was not built, the drafted-token calls go through ctypes: {e}", file=sys.stderr)
+        print(f"wa_bind.so was not built, the drafted-token and paged-cache calls go through ctypes: {e}", file=sys.stderr)
     if verbose:
         print("built", LIB)
     return LIB

@@ -3,8 +3,8 @@
 // A call for one sequence runs for five to twenty microseconds on the GPU, and the checks of its tensors as
 // Python expressions took as long again.  This module does them on the tensors themselves (under a
 // microsecond) for the ordinary call: tensors of the right types (contiguous, or in the paged-cache calls laid out as
-// the library takes them) on the current device, its current stream.  For any other call, valid or not, each function returns None and the package's own checks, which name
-// what is wrong, take it from there.  On success a function returns the call's tensors, and a WA_E* code as an
+// the library takes them) on the current device, its current stream.  For any other call, valid or not, each function
+// returns None and the package's own checks, which name what is wrong, take it from there.  On success a function returns the call's tensors, and a WA_E* code as an
 // int where the library refused it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
