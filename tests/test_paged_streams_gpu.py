@@ -162,3 +162,109 @@ def test_a_lone_head_in_a_pool_of_odd_page_strides(wa):
     r = check.compare(bits(got), ref, check.TOL_FP32_P)
     assert r["ok"], r
     assert _same(got, wa.paged_decode(c["q"], c["k"], c["v"], c["table"], c["pos"], scale=0.1))
+
+
+def test_a_token_changed_between_two_appends(wa):
+    """The second of two large appends reads a few tokens that a small kernel between them has just written, and the rest
+    again, with nothing else in between that would make an SM forget what it read for the first."""
+    n, rows, hq, hkv, d, page = 1600, 4, 8, 2, 128, 16
+    gen = torch.Generator(device="cuda").manual_seed(75)
+    inv, _ = wa.rope_frequencies(d, device="cuda")
+    most = n // rows // page
+    table = torch.arange(rows * most, dtype=torch.int32, device="cuda").view(rows, most)
+    k, v = (torch.zeros((rows * most, page, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    start = torch.randn((n, (hq + 2 * hkv) * d), generator=gen, device="cuda").to(torch.bfloat16)
+    x = start.clone()
+    pos = torch.arange(n // rows, dtype=torch.int32).repeat(rows).cuda()
+    row = torch.arange(rows, dtype=torch.int32).repeat_interleave(n // rows).cuda()
+    one, two = (torch.empty((n, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    few = x[777:781, :hq * d].unflatten(1, (hq, d))
+
+    def run(between):
+        wa.paged_append(x, pos, one, k, v, table, row=row, inv_freq=inv, ws=ws)
+        between()
+        wa.rope(few, pos[777:781], inv, out=few)
+        between()
+        wa.paged_append(x, pos, two, k, v, table, row=row, inv_freq=inv, ws=ws)
+
+    run(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    want = one.clone(), two.clone()
+    changed = (want[0] != want[1]).flatten(1).any(1)
+    assert changed[777:781].all() and changed.sum() == 4
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            run(lambda: None)
+    for way in (g.replay, lambda: [run(lambda: None) for _ in range(3)]):
+        for _ in range(20):
+            x.copy_(start)
+            one.zero_(), two.zero_()
+            run(lambda: None)
+            torch.cuda.synchronize()
+            assert _same(one, want[0]) and _same(two, want[1])
+            # (each run turns the few tokens once more: the last append's queries are once more than the first's)
+            before = few.clone()
+            way()
+            torch.cuda.synchronize()
+            for _ in range(3):
+                before = wa.rope(before, pos[777:781], inv)
+            assert _same(few, before) and _same(two[777:781], wa.rope(before, pos[777:781], inv))
+
+
+def test_a_capture_whose_branches_meet_at_a_call(wa):
+    """Two branches of a captured graph, joined before a decode: it waits for both."""
+    c = wa_synth.paged_case([400, 77], 8, 2, 128, 16, seed=76, device="cuda", outside="keep")
+    want = [wa.paged_decode(q, c["k"], c["v"], c["table"], c["pos"], scale=0.1) for q in (c["q"], c["q"].flip(1))]
+    q, k = torch.zeros_like(c["q"]), torch.zeros_like(c["k"])
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    src = [c["q"].clone(), c["k"].clone()]
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)            # about 0.1 ms
+            k.copy_(src[1])
+        q.copy_(src[0])
+        main.wait_stream(side)
+        out = wa.paged_decode(q, k, c["v"], c["table"], c["pos"], scale=0.1)
+        k.zero_()
+    for i in range(6):
+        src[0].copy_(c["q"] if i % 2 == 0 else c["q"].flip(1))
+        g.replay()
+        torch.cuda.synchronize()
+        assert _same(out, want[i % 2])
+
+
+def test_layouts_of_the_pool_and_the_table(wa):
+    """Keys and values side by side in the innermost dims, one heads first and the other not, and a table that is part of a
+    wider one: the same bits as over plain pools."""
+    for bits_ in (16, 8):
+        c = wa_synth.paged_case([300, 1, 0, 1111], 12, 3, 128, 32, seed=77, device="cuda", bits=bits_, outside="nan")
+        call = lambda k, v, table: wa.paged_decode(c["q"], k, v, table, c["pos"], scale=0.1, k_scale=c["k_scale"], v_scale=c["v_scale"])
+        want = call(c["k"], c["v"], c["table"])
+        pages, page, hkv, d = c["k"].shape
+        inner = torch.empty((pages, page, hkv, 2, d), dtype=c["k"].dtype, device="cuda")
+        inner[:, :, :, 0], inner[:, :, :, 1] = c["k"], c["v"]
+        first = c["k"].transpose(1, 2).contiguous().transpose(1, 2)
+        wide = torch.full((4, c["table"].shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+        wide[:, 2:-3] = c["table"]
+        assert _same(call(inner[:, :, :, 0], inner[:, :, :, 1], c["table"]), want)
+        assert _same(call(first, c["v"], c["table"]), want)
+        assert _same(call(c["k"], first.copy_(c["v"]), wide[:, 2:-3]), want)
+
+
+@pytest.mark.parametrize("hq, hkv", [(64, 64), (40, 20), (16, 1)])
+def test_many_key_heads_and_few(wa, hq, hkv):
+    """As many key heads as query heads, groups of two, and one for all."""
+    for bits_ in (16, 8):
+        c = wa_synth.paged_case([1, 260, 900], hq, hkv, 128, 64, seed=78, device="cuda", bits=bits_)
+        got = wa.paged_decode(c["q"], c["k"], c["v"], c["table"], c["pos"], scale=0.1, k_scale=c["k_scale"], v_scale=c["v_scale"])
+        values = [oracle.bf16_to_f64(bits(t)) if bits_ == 16 else paged.e4m3_to_f64(t.contiguous().view(torch.uint8).cpu().numpy())
+                  for t in (c["k"], c["v"])]
+        scales = [None if t is None else t.cpu().numpy() for t in (c["k_scale"], c["v_scale"])]
+        ref = paged.decode(oracle.bf16_to_f64(bits(c["q"])), *values, c["table"].cpu().numpy(), c["pos"].cpu().numpy(), 0, 0.1, *scales)
+        r = check.compare(bits(got), ref, check.TOL_FP32_P)
+        assert r["ok"], r
