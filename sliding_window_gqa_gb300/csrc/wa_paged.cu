@@ -38,9 +38,9 @@
 //   and 8..11     of odd units.  One group's chain (a unit's ends, 2,500 cycles) runs beside the other's.
 // Every wait is bounded (a status bit after kWaitLimitNs).
 //
-// Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128, 304 us for 311 at the rate of a copy; 48 rows,
-// 32/16 heads of 256, window 1,024, 124 for 117; one row of 131,072 keys, 32/4 heads of 128, 49 for 40 (start and join);
-// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 37 for
+// Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128, 309 us for 311 at the rate of a copy; 48 rows,
+// 32/16 heads of 256, window 1,024, 125 for 117; one row of 131,072 keys, 32/4 heads of 128, 50 for 40 (start and join);
+// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 38 for
 // 21 (the softmax warps' chain, few units an SM).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -55,35 +55,35 @@ namespace {
 
 constexpr int kPTile = 128;          // keys a tile
 constexpr int kPThreads = 512;
-// Tiles of a span at most: as many as have room for their scores twice, beside O.  (Of 4, 6 and 8: the 8-bit batch 179, 163
-// and 161 us; one row of 131,072 keys 51, 51 and 49.)
+// Tiles of a span at most: as many as have room for their scores twice, beside O.  (Of 4, 6 and 8: the 8-bit batch 170, 162
+// and 159 us; one row of 131,072 keys 51.1, 50.3 and 49.1.)
 constexpr int kSpanTiles = 8;
 // A span holds at least so many bytes of keys and values, and of 8-bit pages at least two tiles, for a unit has costs of its
 // own, of which those of the softmax warps show most with 8-bit pages.  (bf16 pages, 64 and 128 KiB, 32/8 heads of 128: one
-// row of 1,000 keys 8.1 and 8.9 us, 64 rows of 500 30.3 and 29.8.  8-bit pages of 2, 3 and 4 tiles of 32 KiB, 32/4 heads of
-// 128: one row of 2,000 keys 9.8, 10.2 and 11.0, 64 rows of 4,000 61, 54 and 50; of 1 and 2 tiles of 64 KiB, 24/2 heads of 256:
-// one row of 1,000 11.3 and 12.9, 64 rows of 1,000 37 and 26.)
+// row of 1,000 keys 8.0 and 8.7 us, 256 rows of 300 67.9 and 66.2.  8-bit pages of 2, 3 and 4 tiles of 32 KiB, 32/4 heads of
+// 128: one row of 2,000 keys 9.8, 10.0 and 10.8, 64 rows of 4,000 59.9, 54.4 and 50.5; of 1 and 2 tiles of 64 KiB, 24/2 heads of
+// 256: one row of 1,000 11.2 and 12.8, 64 rows of 1,000 34.2 and 25.7.)
 __host__ __device__ constexpr int fewest_bytes(int e4m3) { return e4m3 ? 98304 : 65536; }
+__host__ __device__ constexpr int fewest_tiles(int d, int e4m3) {
+    const int tiles = fewest_bytes(e4m3) / (2 * kPTile * d * (e4m3 ? 1 : 2)), least = e4m3 ? 2 : 1;
+    return tiles > least ? tiles : least;
+}
 // A row is cut into this many units over its key heads, or twice as many, .., as spans of kSpanTiles allow: fewer than the
-// SMs, for two thirds of them read as fast as all.  (With 152, 100 and 76: 7 rows of up to 40,000 keys, 8-bit pages, 40.5,
-// 36.9 and 37.5 us; one row of 8,000 keys, 32/8 heads of 128, 14.2, 14.3 and 15.4.)
+// SMs, for two thirds of them read as fast as all, and a unit has costs of its own.  (With 152, 100 and 76: one row of 8,000
+// keys, 32/8 heads of 128, 14.0, 14.1 and 15.0 us; 48 rows, 32/16 heads of 256, window 1,024, 130.5, 127.5 and 128.0; 7 rows of
+// up to 40,000, 8-bit pages, 36.8, 38.0 and 37.4.)
 constexpr int kFill = 100;
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
 constexpr int kPagedGrid = 256;      // CTAs of a launch at most
 // Units go to the CTAs in turn up to kInTurn a CTA, beyond that by a counter, in jobs of about 256 KiB of units and kJobs a CTA
-// at least.  (In turn up to 2, 8 and 16 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 21.3, 20.0 and 19.9 us; a ragged batch's
-// last units wait longer.  By jobs of one unit 64 rows of 4,000 keys, 32/4 heads, 8-bit pages, took 151 us, by these then 65;
-// with jobs of 1 MiB 256 rows of 300, 32/8 heads, bf16 pages, take 72, not 67.)
+// at least.  (In turn up to 2 and 8 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 20.9 and 19.9 us; always: the batch of 64
+// rows below 317, not 309.  8 jobs a CTA and 4: 64 rows of 500 33.3 and 29.2; jobs of 1 MiB: 256 rows of 300 72, not 67.)
 constexpr int kInTurn = 8;
 constexpr int kJobs = 4;
 
 // How a row is cut: spans of `each` tiles, the first `more` of them of one more.  (Without runtime divisions: as two of 64
 // bits and two of 32 this took 2,000 cycles, and each unit's publication waited for it.)
-__host__ __device__ constexpr int fewest_tiles(int d, int e4m3) {
-    const int tiles = fewest_bytes(e4m3) / (2 * kPTile * d * (e4m3 ? 1 : 2)), least = e4m3 ? 2 : 1;
-    return tiles > least ? tiles : least;
-}
 struct RowCut {
     int lo, k0, tiles, spans, each, more;      // lo: the first visible key; k0: the first tile's first key
 };
@@ -163,8 +163,8 @@ struct PagedCfg {
     static constexpr int UNROLL = GP == 16 ? 1 : HV;     // (the most code: see the softmax's)
     static constexpr int KB = ESZ;                       // in blocks of 128 bytes of a key,
     static constexpr int SLOT = kPTile * KB * 128;       // as [16 groups of 8 keys][KB][8][128 bytes]
-    // slots of K, and of V: as many as leave room for P.  (Of 96 KB together instead of 192: one row of 131,072 keys 50.3 us,
-    // now 49.5; a batch 312, now 308.)
+    // slots of K, and of V: as many as leave room for P.  (Of half as many: one row of 8,000 keys, bf16
+    // pages, 15.4 us, not 14.1, the batch of 64 rows 305, not 301; 64 rows of 4,000, 8-bit pages, 52.4, not 54.4.)
     static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
     // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
@@ -300,7 +300,6 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void prefetch_l2(const void* x) { asm volatile("prefetch.global.L2 [%0];" :: "l"(x)); }
 
 // A softmax group's barrier, alone and as a vote.
 __device__ __forceinline__ void group_sync(int group) { named_bar_sync(1 + group, 128); }
@@ -399,19 +398,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
     if (warp == 1) {
         tmem_alloc(smem_u32(smem + C::OFF_MISC), C::TMEM_COLS);
         tmem_relinquish();
-    }
-    // The queries and the table, a line a thread, into L2: once the keys stream, a read that has to go to memory waits
-    // behind them (a batch of 64 rows, 32/8 heads of 128: 309 us without this, 301 with it).
-    {
-        // (at most 2^8 rows of 2^22 lines each: 32 bits)
-        const uint32_t i = blockIdx.x * kPThreads + tid, rows = p.rows;
-        const uint32_t q_lines = p.a.hq * (D / 64), t_lines = (p.a.most + 31) / 32, q_all = rows * q_lines, t_all = rows * t_lines;
-        if (i < q_all) {
-            prefetch_l2(static_cast<const uint16_t*>(p.a.q) + (p.row0 + static_cast<int64_t>(i / q_lines)) * p.a.q_row + i % q_lines * 64);
-        } else if (i < q_all + t_all) {
-            const uint32_t e = i - q_all;
-            prefetch_l2(p.a.table + (p.row0 + static_cast<int64_t>(e / t_lines)) * p.a.table_row + e % t_lines * 32);
-        }
     }
     for (int e = tid; e < (2 * C::Q_BYTES + 2 * C::NP * C::P_BYTES) / 16; e += kPThreads)
         st_shared_v4(sbase + C::OFF_Q + 16 * e, 0u, 0u, 0u, 0u);
