@@ -84,7 +84,7 @@ def build(verbose: bool = False, extra=()) -> str:
             raise bind_error
         tmp = BIND + ".tmp"
         _run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT, "-l:libwa.so", "-L" + os.path.join(torch_dir, "lib"),
-              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of wa_bind.so")
+              "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "link of wa_bind.so")
         os.replace(tmp, BIND)
     except Exception as e:
         if os.path.exists(BIND):        # an earlier build's, of other sources

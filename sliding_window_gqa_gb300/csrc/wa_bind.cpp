@@ -4,13 +4,13 @@
 // Python expressions took as long again.  This module does them on the tensors themselves (under a
 // microsecond) for the ordinary call: tensors of the right types (contiguous, or in the paged-cache calls laid out as
 // the library takes them) on the current device, its current stream.  For any other call, valid or not, each function
-// returns None and the package's own checks, which name what is wrong, take it from there.  On success a function returns the call's tensors, and a WA_E* code as an
-// int where the library refused it.
+// returns None and the package's own checks, which name what is wrong, take it from there.  On success a function returns
+// the call's tensors, and a WA_E* code as an int where the library refused it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -51,7 +51,7 @@ PyObject* guarded(F&& f) {
 }
 
 Tensor make(at::IntArrayRef sizes, at::ScalarType type, const Tensor& like) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+    return Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
 
 // The caller's workspace, if it is an ordinary byte buffer, or a new one.
