@@ -142,6 +142,7 @@ struct PagedPlan {
     int spans;
     size_t taken;    // int[launches] units that are taken
     size_t said;     // int[launches * CTAs] what they have to report
+    size_t cut;      // int[rows] spans of a row
     size_t m;        // float[rows * hkv * spans * G]
     size_t l;        // float[rows * hkv * spans * G * 4]
     size_t part;     // float[rows * hkv * spans * G * d]

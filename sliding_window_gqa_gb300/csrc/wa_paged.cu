@@ -145,6 +145,7 @@ struct PagedParams {
     PagedArgs a;
     int* next_unit;                // null: units go to the CTAs in turn
     int* said;                     // [CTA]: its WA_STATUS_* bits
+    int* cut;                      // [row]: its spans, for the join
     float* m;                      // [unit][G]
     float* l;                      // [unit][G][4]: of each quarter of a tile's keys
     float* part;                   // [unit][G][d]
@@ -415,6 +416,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             const RowCut cut = row_cut(at, p.a.win, p.align, p.a.hkv, C::FEWEST);
             mine = cut.spans;
             tiles = min(cut.tiles, 1 << 20);
+            if (blockIdx.x == 0) p.cut[p.row0 + tid] = cut.spans;
             lasts[tid] = at;
             smem[C::OFF_EACH + tid] = static_cast<uint8_t>(cut.each);
         }
@@ -432,9 +434,12 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         }
         bad = __syncthreads_or(bad);
         if (tid == 0) *status = bad && blockIdx.x == 0 ? WA_STATUS_BAD_POS : 0;
-        for (int w = 0; w < warp; ++w) sum += tot[w];
         tiles = 0;
-        for (int w = 0; w < kPThreads / 32; ++w) tiles += tot[16 + w];
+#pragma unroll
+        for (int w = 0; w < C::ROWS / 32; ++w) {      // (the warps that have rows)
+            if (w < warp) sum += tot[w];
+            tiles += tot[16 + w];
+        }
         if (tid < C::ROWS) pre[tid + 1] = sum;
         if (tid == 0) pre[0] = 0;
     }
@@ -1201,9 +1206,13 @@ struct MergeArgs {
     const float* m;
     const float4* l;
     const float* part;
-    const int* said;
-    int spans_most, align, ctas;
+    const int *said, *cut;
+    int spans_most, ctas;
 };
+
+// A row's spans (as many as there is room for at most, whatever is read).  Working them out from the position here, once
+// more, would take 0.3 us of a short call.
+__device__ __forceinline__ int spans_of(const MergeArgs& x, int row) { return max(0, min(x.cut[row], x.spans_most)); }
 
 // (m, l) of a record, l over the quarters in order
 __device__ __forceinline__ float2 record(const MergeArgs& x, int64_t at) {
@@ -1223,7 +1232,7 @@ __device__ __forceinline__ void add4(float4& x, const float4& o) {
 }
 
 // Few rows: a block 64 dims of a (row, head), sixteen threads of 4 dims a group of spans.  The partial results of the first
-// kWideAhead groups a thread are asked for together with the position that says how many there are, so a call of up to 128
+// kWideAhead groups a thread are asked for together with their number, so a call of up to 128
 // spans waits for one trip to memory.
 constexpr int kWideAhead = 2;
 template <int D>
@@ -1245,13 +1254,12 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
     // Plain loads from here on: what they read is written while this kernel is there already.  Blocks without work wait
     // too, so that nothing behind the call starts early.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int raw = a.pos[row];
+    const int spans = spans_of(x, row);
 #pragma unroll
     for (int i = 0; i < kWideAhead; ++i) fetch((16 * i + slice) * kMergeGroup, x.spans_most, ahead[i]);
     float2 mine = make_float2(-INFINITY, 0.f);
     if (t < x.spans_most) mine = record(x, rec(t));
     const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-    const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv, fewest_tiles(a.d, a.e4m3)).spans;
     if (blockIdx.x == 0 && blockIdx.y == 0) paged_report(a.hdr, x.said, x.ctas);
     uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D + col0;
     if (spans == 0) {
@@ -1315,7 +1323,7 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
     if (__syncthreads_or(bad)) paged_rerun(a, again, row, h, col0);
 }
 
-// Many rows: a warp a (row, head), kNarrowAhead / V spans at a time.  The position comes first here, for spans that a row does
+// Many rows: a warp a (row, head), kNarrowAhead / V spans at a time.  Their number comes first here, for spans that a row does
 // not have are not free when there are many rows (256 rows of 300 keys, a table for 38,400: 77 us, now 69).  (8 at a time, for
 // more warps an SM: 256 rows of 300 66 us, not 68, 64 rows of 500 to 30,000 over 8-bit pages 164, not 162.)
 constexpr int kNarrowAhead = 16;
@@ -1343,9 +1351,8 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
                     for (int v = 0; v < V; ++v) o[i][v] = reinterpret_cast<const float4*>(x.part + rec(s + i) * D)[v * 32 + lane];
                 }
         };
-        const int raw = a.pos[row];
+        const int spans = spans_of(x, row);
         const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-        const int spans = row_cut(paged_pos(raw, a.most, a.page_log), a.win, x.align, a.hkv, fewest_tiles(a.d, a.e4m3)).spans;
         uint2* orow = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D);
         fetch(0, spans);
         float2 mine = make_float2(-INFINITY, 0.f);
@@ -1465,7 +1472,8 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     pl.taken = kHeaderBytes;
     pl.said = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
-    pl.m = pl.said + up((rows / kPagedFewest + 1) * kPagedGrid * sizeof(int));
+    pl.cut = pl.said + up((rows / kPagedFewest + 1) * kPagedGrid * sizeof(int));
+    pl.m = pl.cut + up(rows * sizeof(int));
     pl.l = pl.m + up(heads * pl.spans * sizeof(float));
     pl.part = pl.l + up(heads * pl.spans * 4 * sizeof(float));
     pl.bytes = pl.part + up(static_cast<size_t>(heads) * pl.spans * d * sizeof(float));
@@ -1489,6 +1497,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     uint8_t* base = reinterpret_cast<uint8_t*>(a.hdr);
     int* taken = reinterpret_cast<int*>(base + pl.taken);
     int* said = reinterpret_cast<int*>(base + pl.said);
+    p.cut = reinterpret_cast<int*>(base + pl.cut);
     p.m = reinterpret_cast<float*>(base + pl.m);
     p.l = reinterpret_cast<float*>(base + pl.l);
     p.part = reinterpret_cast<float*>(base + pl.part);
@@ -1535,7 +1544,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         return cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    MergeArgs m{p.m, reinterpret_cast<const float4*>(p.l), p.part, said, pl.spans, p.align, ctas};
+    MergeArgs m{p.m, reinterpret_cast<const float4*>(p.l), p.part, said, p.cut, pl.spans, ctas};
     const int pairs = a.rows * a.hq;
     cfg.gridDim = pairs < kMergeWide ? dim3(pairs, a.d / 64) : dim3((pairs + 7) / 8);
     cfg.blockDim = dim3(256);
