@@ -40,8 +40,8 @@
 //
 // Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128, 309 us for 311 at the rate of a copy; 48 rows,
 // 32/16 heads of 256, window 1,024, 125 for 117; one row of 131,072 keys, 32/4 heads of 128, 50 for 40 (start and join);
-// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 38 for
-// 21 (the softmax warps' chain, few units an SM).
+// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 36 for
+// 21 (the softmax warps' chain, few units an SM).  One row of 700 keys, 16/8 heads of 256: 8.7 (two kernels' trips to memory).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
