@@ -268,3 +268,20 @@ def test_many_key_heads_and_few(wa, hq, hkv):
         ref = paged.decode(oracle.bf16_to_f64(bits(c["q"])), *values, c["table"].cpu().numpy(), c["pos"].cpu().numpy(), 0, 0.1, *scales)
         r = check.compare(bits(got), ref, check.TOL_FP32_P)
         assert r["ok"], r
+
+
+@pytest.mark.parametrize("d, hq", [(128, 1), (256, 16)])
+def test_as_many_rows_as_a_call_takes(wa, d, hq):
+    """65,535 sequences, most of them over the same few pages: those of a row are what the row alone gives."""
+    rows, page = 65535, 16
+    gen = torch.Generator(device="cuda").manual_seed(79)
+    k, v = (torch.randn((9, page, 1, d), generator=gen, device="cuda").to(torch.bfloat16) for _ in "kv")
+    q = torch.randn((rows, hq, d), generator=gen, device="cuda").to(torch.bfloat16)
+    table = torch.randint(0, 9, (rows, 2), generator=gen, device="cuda").int()
+    pos = torch.randint(-1, 2 * page, (rows,), generator=gen, device="cuda").int()
+    ws = torch.empty(wa.paged_decode_ws_bytes(rows, hq, 1, d, page, 2), dtype=torch.uint8, device="cuda")
+    out = wa.paged_decode(q, k, v, table, pos, scale=0.1, ws=ws)
+    assert wa.status(ws) == 0
+    some = torch.tensor([0, 1, 255, 256, 63 * 1000, 65279, 65280, 65534], device="cuda")
+    assert _same(out[some], wa.paged_decode(q[some], k, v, table[some], pos[some], scale=0.1))
+    assert (out[pos == -1] == 0).all() and (out[pos >= 0].flatten(1) != 0).any(1).all()
