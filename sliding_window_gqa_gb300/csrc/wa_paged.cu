@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         volatile float* xbuf = reinterpret_cast<volatile float*>(smem + C::OFF_X) + group * 64;
         const uint32_t x_addr = sbase + C::OFF_X + group * 256;
-        constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight
+        constexpr float kShift = F8 ? 8.f : 0.f;         // P is 2^kShift times the weight, in l and O alike
         // Sixteen heads go through the code of eight twice, with their values exchanged in between: the warps' roles are more
         // code than the instruction cache holds, and waited for it (64 rows of 4,000 keys, 24/2 heads of 256, 8-bit pages, 66 us,
         // then 60; one such row 12.7, then 13.2).
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
             if (group_any(group, dead) || x.nt <= 0) break;
             wait(C::B_SFULL + group, static_cast<uint32_t>(U >> 1) & 1u);
             tc_fence_after();
-            // a tile's scores of this thread's key and heads from h0 on, times c
+            // a tile's products q.k of this thread's key and heads from h0 on
             auto scores = [&](int idx, int h0, float (&y)[H]) {
                 if constexpr (F8 && GP < 16) {
                     uint32_t r[H], q[H];
@@ -947,20 +947,22 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     tm_wait(r);
                     tm_wait(q);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) y[h] = (__uint_as_float(r[h]) + __uint_as_float(q[h])) * c[h];
+                    for (int h = 0; h < H; ++h) y[h] = __uint_as_float(r[h]) + __uint_as_float(q[h]);
                 } else {
                     uint32_t r[H];
                     tm_load(s_addr + idx * 16 + h0, r);
                     tm_wait(r);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) y[h] = __uint_as_float(r[h]) * c[F8 ? h : 0];
+                    for (int h = 0; h < H; ++h) y[h] = __uint_as_float(r[h]);
                 }
             };
             auto visible = [&](int idx) {
                 const int key = x.k0 + idx * kPTile + static_cast<int>(pk);
                 return key >= x.lo && key <= x.p;
             };
-            // ---- the maximum of each head over the unit (of -inf where there is none: NaN then, worked out again)
+            // ---- the largest product of each head over the unit (-inf where there is none: not finite then, worked out again).
+            // It is taken from the others before they are multiplied by c, so that its own weight is 1 whatever its size: c q.k
+            // less the rounded c of the largest would be up to half a step of those away from zero, and e4m3 holds no 2^9.
             float m[GP], l[GP];
 #pragma unroll
             for (int h = 0; h < GP; ++h) l[h] = 0.f;
@@ -980,7 +982,6 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 }
                 const float top = reduce_each(best, [](float a, float b) { return fmaxf(a, b); });
                 if (lane % (32 / H) == 0) xbuf[quarter * 16 + h0 + lane / (32 / H)] = top;
-                if constexpr (F8) turn(c);
             }
             group_sync(group);
 #pragma unroll
@@ -988,10 +989,10 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 float4 e[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) e[w] = ld_shared_f4(x_addr + (16 * w + h) * 4);
-                m[h] = fmaxf(fmaxf(e[0].x, e[1].x), fmaxf(e[2].x, e[3].x)) - kShift;
-                m[h + 1] = fmaxf(fmaxf(e[0].y, e[1].y), fmaxf(e[2].y, e[3].y)) - kShift;
-                m[h + 2] = fmaxf(fmaxf(e[0].z, e[1].z), fmaxf(e[2].z, e[3].z)) - kShift;
-                m[h + 3] = fmaxf(fmaxf(e[0].w, e[1].w), fmaxf(e[2].w, e[3].w)) - kShift;
+                m[h] = fmaxf(fmaxf(e[0].x, e[1].x), fmaxf(e[2].x, e[3].x));
+                m[h + 1] = fmaxf(fmaxf(e[0].y, e[1].y), fmaxf(e[2].y, e[3].y));
+                m[h + 2] = fmaxf(fmaxf(e[0].z, e[1].z), fmaxf(e[2].z, e[3].z));
+                m[h + 3] = fmaxf(fmaxf(e[0].w, e[1].w), fmaxf(e[2].w, e[3].w));
             }
             // ---- P, tile by tile
 #pragma unroll 1
@@ -1005,7 +1006,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     scores(idx, h0, s);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        s[h] = vis ? ex2(s[h] - m[h]) : 0.f;
+                        s[h] = vis ? ex2(fmaf(s[h] - m[h], c[F8 ? h : 0], kShift)) : 0.f;
                         l[h] += s[h];
                     }
                     // the parts of two heads each
@@ -1069,7 +1070,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 float mine = 0.f;
 #pragma unroll
                 for (int h = 0; h < GP; ++h)
-                    if (gt == h) mine = m[h];
+                    if (gt == h) mine = m[h] * c[F8 ? h : 0];
                 p.m[unit + gt] = mine;
             }
             {
