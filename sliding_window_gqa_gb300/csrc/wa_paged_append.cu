@@ -26,13 +26,15 @@ namespace wa {
 namespace {
 
 constexpr int kAppendWarps = 4;       // (of 8, blocks ended unevenly: rope of 8,192 x 40 heads of 128 30.2 us, with 4 26.5)
-// Up to this many tokens one more block checks them all and writes the status word; beyond, a kernel of its own does,
-// which runs beside this one.
+// Up to this many tokens one more block checks them all and writes the status word, which spares a launch; beyond, a kernel
+// before this one clears it and the warps that look up the places of keys and values report what is wrong with them.  (The
+// block, and two launches: 600 tokens of 8 + 2 x 1 heads of 128 3.2 us each, 3.5 and 4.6 eager; 1,024 4.9 and 4.1, of 32 + 2 x 8
+// heads 6.5 each.  A block goes on at 0.7 us more for every 512 tokens.)
 constexpr int kStatusBlockTokens = 1024;
 
 struct AppendParams {
     PagedAppendArgs a;
-    int beside;      // the status is another kernel's
+    int cleared;      // the status word is clear: the warps report
 };
 
 // Two products, and two fused multiply-adds, an instruction.
@@ -81,12 +83,6 @@ __device__ __forceinline__ uint64_t turn_fraction(float w) {
     return (b >> 31) ? 0ull - f : f;
 }
 
-__device__ __forceinline__ int load_acquire(const int* x) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(x) : "memory");
-    return v;
-}
-
 // The bad bits of token t's place, and where it is: page < 0 for none.
 __device__ __forceinline__ int place(const PagedAppendArgs& a, int t, int pos, int& page) {
     page = -1;
@@ -116,11 +112,11 @@ __device__ void append_status(const PagedAppendArgs& a) {
     if (threadIdx.x == 0) a.hdr->status = (where ? WA_STATUS_BAD_POS : 0) | (which ? WA_STATUS_BAD_PAGE : 0);
 }
 
-// (The kernel beside it starts once what the stream held before is over, and need not wait for this one.)
-__global__ void __launch_bounds__(1024) append_status_kernel(const __grid_constant__ AppendParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+// Clears the status word; the next kernel sets itself up meanwhile and waits for this one's end.
+__global__ void append_clear_kernel(int* status) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    append_status<1024>(p.a);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    *status = 0;
 }
 
 template <int D, bool CACHE, bool FP8, int PASSES>
@@ -130,13 +126,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     constexpr int P = 32 / L;              // heads a pass
     constexpr int HPW = P * PASSES;        // heads a warp
     constexpr int NA = D / 64;             // pairs whose angle a lane works out
-    // Launched while the kernel before still runs, waits for its end here.  Beside the status kernel, which has waited for what
-    // the stream held before it let this one start, one block does, so that this one is over no sooner; the others make
-    // sure by an acquire that they read nothing their SM remembers from before (32.1 us for a chunk, 31.8 without).
-    if (!p.beside || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Launched while the kernel before still runs, waits for its end here.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (CACHE) {
-        if (!p.beside && blockIdx.x == gridDim.x - 1) {
+        if (!p.cleared && blockIdx.x == gridDim.x - 1) {
             if (blockIdx.y == 0) append_status<kAppendWarps * 32>(a);
             return;
         }
@@ -145,7 +139,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     if (t >= a.n) return;                  // warp-uniform
     const int lane = threadIdx.x & 31, li = lane % L, hp = lane / L;
     const int nqk = a.hq + a.hkv, heads = nqk + a.hkv;
-    const int pos = CACHE && p.beside ? load_acquire(a.pos + t) : a.pos[t];
+    const int pos = a.pos[t];
     const bool turns = li < a.dims / 16;
     // a lane's two pieces of a head that turns: of dims (j, j + dims / 2), or 16 neighbours; of any other, 16 neighbours
     const int one = turns && a.layout == WA_ROTARY_HALF ? 8 * li : 16 * li;
@@ -169,7 +163,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     }
     int page = -1;
     if constexpr (CACHE) {
-        if (first + HPW > a.hq) place(a, t, pos, page);                    // a warp with keys or values
+        if (first + HPW > a.hq) {                                          // a warp with keys or values
+            const int bad = place(a, t, pos, page);
+            if (p.cleared && bad && blockIdx.y == gridDim.y - 1 && lane == 0) atomicOr(&a.hdr->status, bad);
+        }
         if (pos < 0 || (pos >> a.page_log) >= a.most) return;
     }
     // Angles: a lane works out NA pairs of the token, and takes the eight of its dims from where they are.
@@ -250,7 +247,7 @@ template <int PASSES>
 cudaError_t launch_append(const AppendParams& p, cudaLaunchConfig_t& cfg) {
     const PagedAppendArgs& a = p.a;
     const int hpw = 32 / (a.d / 16) * PASSES;
-    cfg.gridDim = dim3((a.n - 1) / kAppendWarps + 1 + (a.hkv > 0 && !p.beside), (a.hq + 2 * a.hkv + hpw - 1) / hpw);
+    cfg.gridDim = dim3((a.n - 1) / kAppendWarps + 1 + (a.hkv > 0 && !p.cleared), (a.hq + 2 * a.hkv + hpw - 1) / hpw);
     cfg.blockDim = dim3(kAppendWarps * 32);
     auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
     if (a.d == 256) {
@@ -270,7 +267,7 @@ constexpr int64_t kFewValues = 1 << 20;
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     AppendParams p{};
     p.a = a;
-    p.beside = a.hkv > 0 && a.n > kStatusBlockTokens;
+    p.cleared = a.hkv > 0 && a.n > kStatusBlockTokens;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -278,10 +275,10 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (p.beside) {
+    if (p.cleared) {
         cfg.gridDim = dim3(1);
-        cfg.blockDim = dim3(1024);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, append_status_kernel, p);
+        cfg.blockDim = dim3(1);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, append_clear_kernel, &a.hdr->status);
         if (e != cudaSuccess) return e;
     }
     const bool few = static_cast<int64_t>(a.n) * (a.hq + 2 * a.hkv) * a.d <= kFewValues;
