@@ -13,10 +13,14 @@
 // first, then its maximum is known, then its values.  Nothing is ever scaled again.  (With a running maximum every other
 // tile of 8-bit pages moved some head's, since P has to fit its type: 309 us for the batch below, 199 without.)
 //
-// 8-bit pages.  e4m3 has 4 significant bits, so a query, of 8, is two e4m3 numbers: 2^k q = hi + lo, exactly down to 2^-10 of
-// the head's largest value and to 2^-18 of it below, and S comes from exact products as with bf16.  P is three:
-// 256 p = p1 + p2 / 32 + p3 / 1024 to 2^-12 of p (one part alone: 2^-4; two: 2^-8, about what the output's own rounding
-// loses), or to 2^-28 of the largest where that is more.
+// 8-bit pages.  A query, of 8 significant bits, is two 8-bit numbers, and S comes from exact products as with bf16.  Up to 8
+// heads: 2^k q = hi + lo / 32, both e4m3 (4 significant bits), columns of their own, with the head's largest value at 128 to 256:
+// exactly down to 2^-14 of that value and to 2^-22 of it below.  16 heads have no columns left for lo, so the two products add
+// up and lo has to reach further down by itself: hi is e5m2 (3 bits, so what is left takes 4), lo e4m3, the largest at 2^11 to
+// 2^12: exactly down to 2^-13 of it and to 2^-21 below.  (As e4m3 numbers hi + lo, exactly down to 2^-9 only: outputs 0.7 off
+// where one value of a head is 4,096 times the others.  16 heads as three e5m2 numbers: 64 us for 61.)  P is three e4m3 numbers:
+// 256 p = p1 + p2 / 32 + p3 / 1024 to 2^-14 of p (two: 2^-9, about what the output's own rounding loses), or to 2^-28 of the
+// largest where that is more.
 //
 // Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's keys), are cut into even spans
 // (row_cut).  A unit of work is (row, key head, span); it leaves (m, l, O) in fp32, and a kernel of its own joins a row's
@@ -168,7 +172,7 @@ struct PagedCfg {
     // pages, 15.4 us, not 14.1, the batch of 64 rows 305, not 301; 64 rows of 4,000, 8-bit pages, 52.4, not 54.4.)
     static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
-    // columns of its own (S = column h + column 8 + h) and a larger one adds by a second product
+    // columns of its own (S = column h + column 8 + h / 32) and a larger one adds by a second product
     static constexpr int QN = F8 && GP == 16 ? 32 : 16;
     __host__ __device__ static constexpr int lo_row() { return QN / 2; }
     static constexpr int Q_WARPS = GP == 16 ? 3 : 1;     // that stage a (row, key head)'s queries
@@ -239,9 +243,9 @@ __device__ __forceinline__ void paged_mma(uint32_t d, uint32_t a_lo, uint32_t b_
             :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(more ? 1u : 0u), "n"(A_HI), "n"(B_HI));
 }
 
-// Instruction descriptor: fp32 accumulator, bf16 or e4m3 operands, B K-major.
-constexpr uint32_t paged_idesc(bool f8, uint32_t n, uint32_t a_mn) {
-    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (a_mn << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor: fp32 accumulator, bf16 or e4m3 operands, or B in e5m2; B K-major.
+constexpr uint32_t paged_idesc(bool f8, uint32_t n, uint32_t a_mn, bool b_e5m2 = false) {
+    return (1u << 4) | (f8 ? (b_e5m2 ? 1u << 10 : 0u) : (1u << 7) | (1u << 10)) | (a_mn << 15) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 __device__ __forceinline__ bool paged_elect() {
@@ -335,6 +339,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
 }
 __device__ __forceinline__ float2 e4m3_pair_f32(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+__device__ __forceinline__ uint32_t e5m2_pair(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 e5m2_pair_f32(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E5M2);
     return __half22float2(__half2(h));
 }
 
@@ -527,7 +539,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
         // ------------------------------------------------ MMA issuers of S and of P V: the warp together, one lane's instructions
         const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
         const bool leader = paged_elect();
-        constexpr uint32_t idS = paged_idesc(F8, 16, 0), idO = paged_idesc(F8, C::PN, 1);
+        constexpr uint32_t idS[2] = {paged_idesc(F8, 16, 0, GP == 16), paged_idesc(F8, 16, 0)}, idO = paged_idesc(F8, C::PN, 1);
         constexpr uint32_t kTileHi = desc_hi(C::KB * 1024), kSmallHi = desc_hi(1024);
         int s = warp == 1 ? 0 : C::NSLOT, use = 0;     // the next load's slot
         const int end = s + C::NSLOT;
@@ -576,7 +588,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                                 for (int i = 0; i < 128 / C::KSTEP; ++i) {
                                     const uint32_t a = k + (((i / 4) * 1024 + (i % 4) * 32) >> 4);
                                     const uint32_t b = q + (((i / 4) * C::QN * 128 + set * 2048 + (i % 4) * 32) >> 4);
-                                    paged_mma<F8, kTileHi, kSmallHi>(d, a, b, idS, half > 0 || set > 0 || i > 0);
+                                    paged_mma<F8, kTileHi, kSmallHi>(d, a, b, idS[set], half > 0 || set > 0 || i > 0);
                                 }
                             mma_commit(BAR(C::B_FREE + s));
                         }
@@ -852,8 +864,9 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t bits = __float_as_uint(__shfl_sync(0xFFFFFFFFu, most, 8 * i));
-                        // 2^k brings the largest value to [128, 256) (k at most 120: what is smaller than 2^-113 loses bits)
-                        const int h = h0 + i, k = min(134 - static_cast<int>(bits >> 23), 120);
+                        // 2^k brings the largest value to [2^TOP, 2^(TOP + 1)) (k at most 120: what is smaller than 2^-113 loses bits)
+                        constexpr int TOP = GP == 16 ? 11 : 7;
+                        const int h = h0 + i, k = min(127 + TOP - static_cast<int>(bits >> 23), 120);
                         const float f = __int_as_float((k + 127) << 23) * (neg ? -1.f : 1.f);
                         const bool fine = bits < 0x7F800000u;
                         const int el = lane * EL, low = h + C::lo_row();
@@ -868,9 +881,18 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                                 v[2 * e] = __uint_as_float(now[i][2 * w + e] << 16) * f;
                                 v[2 * e + 1] = __uint_as_float(now[i][2 * w + e] & 0xFFFF0000u) * f;
                             }
-                            const uint32_t a = e4m3_pair(v[0], v[1]), b = e4m3_pair(v[2], v[3]);
-                            const float2 fa = e4m3_pair_f32(a), fb = e4m3_pair_f32(b);
-                            const uint32_t rest = e4m3_pair(v[0] - fa.x, v[1] - fa.y) | (e4m3_pair(v[2] - fb.x, v[3] - fb.y) << 16);
+                            uint32_t a, b;
+                            float2 fa, fb;
+                            if constexpr (GP == 16) {
+                                a = e5m2_pair(v[0], v[1]); b = e5m2_pair(v[2], v[3]);
+                                fa = e5m2_pair_f32(a); fb = e5m2_pair_f32(b);
+                            } else {
+                                a = e4m3_pair(v[0], v[1]); b = e4m3_pair(v[2], v[3]);
+                                fa = e4m3_pair_f32(a); fb = e4m3_pair_f32(b);
+                            }
+                            constexpr float UP = GP == 16 ? 1.f : 32.f;
+                            const uint32_t rest = e4m3_pair((v[0] - fa.x) * UP, (v[1] - fa.y) * UP) |
+                                                  (e4m3_pair((v[2] - fb.x) * UP, (v[3] - fb.y) * UP) << 16);
                             st_shared_u32(ah + 4 * w, fine ? a | (b << 16) : 0x7F7F7F7Fu);      // NaN: the head is computed again
                             st_shared_u32(al + 4 * w, fine ? rest : 0u);
                         }
@@ -947,7 +969,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                     tm_wait(r);
                     tm_wait(q);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) y[h] = __uint_as_float(r[h]) + __uint_as_float(q[h]);
+                    for (int h = 0; h < H; ++h) y[h] = fmaf(__uint_as_float(q[h]), 0.03125f, __uint_as_float(r[h]));
                 } else {
                     uint32_t r[H];
                     tm_load(s_addr + idx * 16 + h0, r);

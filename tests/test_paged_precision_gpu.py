@@ -1,13 +1,15 @@
 """What the paged decode keeps of its probabilities, queries and scores, on the GPU, at inputs that show it."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import wa_synth
 from _util import bits, ensure_built
 from oracle import check
-from test_paged_decode_gpu import call, reference
+from test_paged_decode_gpu import call, reference, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +42,32 @@ def test_scores_of_any_size(wa, e, bits_, d, hq, hkv):
     c = dict(c, q=c["q"][one], table=c["table"][one], pos=c["pos"][one])
     r = check.compare(bits(call(wa, c, -(2.0 ** 0.5))), reference(c, -(2.0 ** 0.5)), 0.0)
     assert r["ok"], r
+
+
+def near(got, exact, off):
+    """Outputs within `off` of 64-bit values before their rounding to bf16 (half a step: 2^-8 of the value)."""
+    got = oracle.bf16_to_f64(bits(got))
+    over = np.abs(got - exact) - (off + 2.0 ** -8 * (np.abs(exact) + off))
+    assert (over <= 0).all(), (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("hq, hkv", [(4, 1), (16, 2), (16, 1), (9, 1)])
+@pytest.mark.parametrize("d", [128, 256])
+def test_a_query_with_one_large_value(wa, d, hq, hkv):
+    """Over 8-bit pages a query's value is a sum of 8-bit numbers, within 2^-21 of its head's largest value.  The largest stands
+    where every key is zero, the scores come from one value of about 2^-12 of it.  With every score off by at most x, weights
+    are off by a factor of e^(2 x) of one another at most."""
+    c = wa_synth.paged_case([40, 300, 1, 1100], hq, hkv, d, 32, seed=82, bits=8, device="cuda", outside="keep", peaked=False)
+    gen = torch.Generator(device="cuda").manual_seed(83)
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1.0
+    c["q"][:, :, 1] = ((1 + torch.rand((4, hq), generator=gen, device="cuda")) * 2.0 ** -12).to(torch.bfloat16)
+    k = torch.zeros(c["k"].shape, device="cuda")
+    k[..., 1] = torch.randint(-8, 9, k.shape[:-1], generator=gen, device="cuda").float()
+    c["k"].copy_(k)
+    c["k_scale"], c["v_scale"] = torch.full((hkv,), 1024.0, device="cuda"), None
+    ref = reference(c, 1.0)
+    off = np.exp(2 * 8 * 1024 * 2.0 ** -21) - 1
+    # sum_j w_j |v_j| / sum_j w_j; scores of up to 8 (11.6 in units of log2: 2^-19.3 in a weight) and weights within 2^-14
+    size = reference(dict(c, v=torch.from_numpy(np.abs(stored(c["v"]))).cuda().float().to(c["v"].dtype)), 1.0)
+    near(call(wa, c), ref, (off + 2.0 ** -14 + 2.0 ** -18) * size)
