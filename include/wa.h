@@ -492,7 +492,8 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  *   out  [rows, hq, d]  bf16, row stride out_row; must not overlap the inputs
  *
  * Probabilities are fp32 in the sums and enter P V as two bf16 parts, whose sum is
- * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-12).  With e4m3
+ * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-14, or
+ * 2^-28 of the largest weight where that is more).  With e4m3
  * pages a query's value is a sum of two 8-bit numbers, exact down to 2^-13 of its
  * head's largest value and within 2^-21 of that below.  A (row,
  * head) whose result is NaN or infinite is computed again in float64.  A row's

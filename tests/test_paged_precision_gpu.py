@@ -7,6 +7,7 @@ import torch
 
 import oracle
 import wa_synth
+from _paged_precision import LIVE, cancelling, place
 from _util import bits, ensure_built
 from oracle import check
 from test_paged_decode_gpu import call, reference, stored
@@ -49,6 +50,27 @@ def near(got, exact, off):
     got = oracle.bf16_to_f64(bits(got))
     over = np.abs(got - exact) - (off + 2.0 ** -8 * (np.abs(exact) + off))
     assert (over <= 0).all(), (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("hq, hkv", [(4, 1), (16, 2), (16, 1), (12, 1)])
+@pytest.mark.parametrize("bits_, bound", [(16, 2.0 ** -17), (8, 2.0 ** -14)])
+@pytest.mark.parametrize("d", [128, 256])
+def test_probabilities_keep_their_parts(wa, d, bits_, bound, hq, hkv):
+    """Values that cancel: what the weights lose is the output's error, of size sum_j w_j |v_j| / sum_j w_j.
+
+    Besides the bound for P, 2^-19 of that size: a score in units of log2 of up to 1.45 is off by 2^-23 of it (its factor's
+    rounding and its own), with 8 added to it by 2^-22, in a weight both times ln 2, 2^-22.1; the exponential 2^-22; and the
+    eight products' sum by 2^-24 or, where a tensor core cuts off, 2^-23 a step, 2^-20."""
+    seeds, rng = range(4), np.random.default_rng(d + hq)
+    lengths = [128, 1000, 700, 129]
+    c = wa_synth.paged_case(lengths, hq, hkv, d, 16, seed=81, bits=bits_, device="cuda", outside="keep", peaked=False)
+    sets = [cancelling(d, s) for s in seeds]
+    first = [0, 512, 384, 0]
+    place(c, [f + rng.choice(128, LIVE, replace=False) for f in first], [t for t, _ in sets], [v for _, v in sets])
+    out = call(wa, c).cpu()
+    for r, (t, v) in enumerate(sets):
+        w = np.exp(t)
+        near(out[r], np.broadcast_to(w @ v / w.sum(), (hq, d)), (bound + 2.0 ** -19) * (w @ np.abs(v) / w.sum()))
 
 
 @pytest.mark.parametrize("hq, hkv", [(4, 1), (16, 2), (16, 1), (9, 1)])
