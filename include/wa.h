@@ -473,7 +473,12 @@ int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int
                     void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes wa_paged_decode needs for `cache` (sizes and type are read, no
- * pointers); 0 for invalid sizes. */
+ * pointers); 0 for invalid sizes.  They are for rows that fill the table, whatever the
+ * rows hold: (d + 5) floats a query head for each span that such a row, or its window,
+ * is cut into, for 256 rows or as many as 64 MiB hold.  Spans: 100 / hkv, rounded up, for each 102,400 /
+ * hkv keys begun, and never more than one for 128 keys.  256 rows of 64/8 heads of 128
+ * take 1.2 GB where `most` * page_size is 131,072, and 8.9 GB where it is 1,048,576: a
+ * table cut to what the batch's longest row needs keeps it small. */
 size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
 
 /*

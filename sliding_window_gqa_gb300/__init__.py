@@ -963,7 +963,11 @@ def paged_append(src, pos, q_out, k_pages, v_pages, table, row=None, inv_freq=No
 
 def paged_decode_ws_bytes(rows: int, hq: int, hkv: int, d: int, page: int, most: int, win: int = 0,
                           dtype=torch.bfloat16) -> int:
-    """Workspace bytes of paged_decode for these sizes (most: the table's columns); 0 for invalid ones."""
+    """Workspace bytes of paged_decode for these sizes (most: the table's columns); 0 for invalid ones.
+
+    They grow with ``most``, whatever the rows hold, and with up to 256 rows: 64/8 heads of 128 and a table for 131,072
+    positions take 4.7 MB a row.  Pass the columns that the batch's longest sequence needs (``table[:, :columns]``) to keep
+    them small; no row's output depends on it."""
     if not _fit_32_bits(rows, hq, hkv, d, page, most, win) or dtype not in _PAGE_TYPES:
         return 0
     sizes = _Pages(pages=1, page_size=page, rows=rows, most=most, hkv=hkv, d=d, type=_PAGE_TYPES[dtype])

@@ -140,12 +140,13 @@ struct PagedArgs {
 // The workspace of a paged decode call in bytes from its start, and the most spans of a (row, key head).
 struct PagedPlan {
     int spans;
+    int held;        // rows whose partial results are held at a time: of whole launches
     size_t taken;    // int[launches] units that are taken
     size_t said;     // int[launches * CTAs] what they have to report
     size_t cut;      // int[rows] spans of a row
-    size_t m;        // float[rows * hkv * spans * G]
-    size_t l;        // float[rows * hkv * spans * G * 4]
-    size_t part;     // float[rows * hkv * spans * G * d]
+    size_t m;        // float[held * hkv * spans * G]
+    size_t l;        // float[held * hkv * spans * G * 4]
+    size_t part;     // float[held * hkv * spans * G * d]
     size_t bytes;
 };
 PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win);

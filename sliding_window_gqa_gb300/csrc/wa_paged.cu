@@ -80,6 +80,10 @@ constexpr int kFill = 100;
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
 constexpr int kPagedGrid = 256;      // CTAs of a launch at most
+// Launches are joined together as long as their partial results are no more than this, and each by itself beyond, so that the
+// workspace does not grow with the rows.  (Each by itself always: 4,096 rows of 41 keys, 8/1 heads of 128, 188 us, together
+// 178; 512 rows of 300, 32/8 heads, 136 and 137.)
+constexpr int64_t kHeldBytes = 64 << 20;
 // Units go to the CTAs in turn up to kInTurn a CTA, beyond that by a counter, in jobs of about 256 KiB of units and kJobs a CTA
 // at least.  (In turn up to 2 and 8 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 20.9 and 19.9 us; always: the batch of 64
 // rows below 317, not 309.  8 jobs a CTA and 4: 64 rows of 500 33.3 and 29.2; jobs of 1 MiB: 256 rows of 300 72, not 67.)
@@ -150,10 +154,11 @@ struct PagedParams {
     int* next_unit;                // null: units go to the CTAs in turn
     int* said;                     // [CTA]: its WA_STATUS_* bits
     int* cut;                      // [row]: its spans, for the join
-    float* m;                      // [unit][G]
+    float* m;                      // [unit of the rows from held0 on][G]
     float* l;                      // [unit][G][4]: of each quarter of a tile's keys
     float* part;                   // [unit][G][d]
     int row0, rows;                // the launch's rows
+    int held0;                     // the first row whose partial results are held
     int spans;                     // most spans of a (row, key head)
     int align;                     // keys of a copy
     float c;                       // |scale| log2(e) (bf16 pages)
@@ -1085,7 +1090,7 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
                 }
             }
             // ---- the unit's result: l of this quarter of the keys in a fixed order, O from tensor memory
-            const int64_t unit = ((static_cast<int64_t>(x.row) * p.a.hkv + x.g) * p.spans + x.span) * G;
+            const int64_t unit = ((static_cast<int64_t>(x.row - p.held0) * p.a.hkv + x.g) * p.spans + x.span) * G;
             const float sum = reduce_each(l, [](float a, float b) { return a + b; });
             if (lane % (32 / GP) == 0 && lane / (32 / GP) < G) p.l[(unit + lane / (32 / GP)) * 4 + quarter] = sum;
             if (gt < G) {
@@ -1214,7 +1219,7 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
 // worked out again.
 constexpr int kMergeGroup = 4;
 
-// The status word of the call, by its first block: what the CTAs have to report.
+// The status word of the call, by the last join's first block: what the CTAs of all its launches have to report.
 __device__ __forceinline__ void paged_report(WsHeader* hdr, const int* said, int ctas) {
     int bits = 0;
     for (int i = threadIdx.x; i < ctas; i += 256) bits |= said[i];
@@ -1230,7 +1235,8 @@ struct MergeArgs {
     const float4* l;
     const float* part;
     const int *said, *cut;
-    int spans_most, ctas;
+    int spans_most, ctas;      // ctas: to report on; 0 for a join that another one follows
+    int row0, rows;            // whose partial results are held
 };
 
 // A row's spans (as many as there is room for at most, whatever is read).  Working them out from the position here, once
@@ -1263,9 +1269,9 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
     __shared__ float4 red[64][16];
     __shared__ float weight[256], sums[256], tops[8], group_den[64];
     __shared__ PagedRerun again;
-    const int row = blockIdx.x / a.hq, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G, col0 = blockIdx.y * 64;
+    const int at = blockIdx.x / a.hq, row = x.row0 + at, h = blockIdx.x % a.hq, G = a.hq / a.hkv, g = h / G, col0 = blockIdx.y * 64;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, slice = t >> 4, quad = t & 15;
-    const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
+    const int64_t first = (static_cast<int64_t>(at) * a.hkv + g) * x.spans_most;
     auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
     float4 ahead[kWideAhead][kMergeGroup];      // (of spans that the row does not have: whatever the workspace holds, not used)
     auto fetch = [&](int s, int most, float4 (&o)[kMergeGroup]) {
@@ -1283,7 +1289,7 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
     float2 mine = make_float2(-INFINITY, 0.f);
     if (t < x.spans_most) mine = record(x, rec(t));
     const float vs = a.kv[1].scale ? a.kv[1].scale[g] : 1.f;
-    if (blockIdx.x == 0 && blockIdx.y == 0) paged_report(a.hdr, x.said, x.ctas);
+    if (x.ctas > 0 && blockIdx.x == 0 && blockIdx.y == 0) paged_report(a.hdr, x.said, x.ctas);
     uint16_t* orow = static_cast<uint16_t*>(a.out) + row * a.o_row + static_cast<int64_t>(h) * D + col0;
     if (spans == 0) {
         if (t < 8) reinterpret_cast<uint4*>(orow)[t] = make_uint4(0u, 0u, 0u, 0u);
@@ -1356,14 +1362,14 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
     static_assert(AHEAD % kMergeGroup == 0 && 32 % AHEAD == 0, "whole groups");
     __shared__ PagedRerun again;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int item = blockIdx.x * 8 + warp, items = a.rows * a.hq;
+    const int item = blockIdx.x * 8 + warp, items = x.rows * a.hq;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");          // as above
-    if (blockIdx.x == 0) paged_report(a.hdr, x.said, x.ctas);
+    if (x.ctas > 0 && blockIdx.x == 0) paged_report(a.hdr, x.said, x.ctas);
     bool bad = false;
     if (item < items) {
-        const int row = item / a.hq, h = item % a.hq, G = a.hq / a.hkv, g = h / G;
-        const int64_t first = (static_cast<int64_t>(row) * a.hkv + g) * x.spans_most;
+        const int at = item / a.hq, row = x.row0 + at, h = item % a.hq, G = a.hq / a.hkv, g = h / G;
+        const int64_t first = (static_cast<int64_t>(at) * a.hkv + g) * x.spans_most;
         auto rec = [&](int s) { return (first + s) * G + (h - g * G); };
         float4 o[AHEAD][V];
         auto fetch = [&](int s, int most) {
@@ -1432,7 +1438,7 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
     for (int i = 0; i < 8; ++i) {
         if (!again_for[i]) continue;
         for (int c = 0; c < D; c += 64) {
-            paged_rerun(a, again, (blockIdx.x * 8 + i) / a.hq, (blockIdx.x * 8 + i) % a.hq, c);
+            paged_rerun(a, again, x.row0 + (blockIdx.x * 8 + i) / a.hq, (blockIdx.x * 8 + i) % a.hq, c);
             __syncthreads();
         }
     }
@@ -1491,7 +1497,11 @@ PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, i
     // ceil(t / each) with each >= t hkv / (kFill waves(t)), and waves(t) no less for longer rows
     const int64_t fill = (kFill * row_waves(tiles, hkv) + hkv - 1) / hkv;
     pl.spans = static_cast<int>(fill < tiles ? fill : tiles);
-    const int64_t heads = static_cast<int64_t>(rows) * hq;
+    // a row takes hq * spans * (d + 5) floats
+    const int64_t fit = kHeldBytes / (static_cast<int64_t>(hq) * pl.spans * (d + 5) * static_cast<int64_t>(sizeof(float))) / kPagedRows;
+    const int64_t held = (fit > 1 ? fit : 1) * kPagedRows;
+    pl.held = static_cast<int>(held < rows ? held : rows);
+    const int64_t heads = static_cast<int64_t>(pl.held) * hq;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     pl.taken = kHeaderBytes;
     pl.said = pl.taken + up((rows / kPagedFewest + 1) * sizeof(int));
@@ -1548,11 +1558,10 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
         e = cudaLaunchKernelEx(&cfg, paged_clear_kernel, taken, a.rows / kPagedFewest + 1);
         if (e != cudaSuccess) return e;
     }
+    MergeArgs m{p.m, reinterpret_cast<const float4*>(p.l), p.part, said, p.cut, pl.spans, 0, 0, 0};
     int ctas = 0;
     e = for_each_paged([&](auto kernel, int d, bool f8, int g, int smem, int most_rows) {
         if (d != a.d || f8 != (a.e4m3 != 0) || g != gp) return cudaSuccess;
-        cfg.blockDim = dim3(kPThreads);
-        cfg.dynamicSmemBytes = smem;
         for (int r0 = 0; r0 < a.rows; r0 += most_rows) {
             p.row0 = r0;
             p.rows = a.rows - r0 < most_rows ? a.rows - r0 : most_rows;
@@ -1560,21 +1569,28 @@ cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
             p.said = said + ctas;
             const int64_t units = static_cast<int64_t>(p.rows) * a.hkv * pl.spans;
             cfg.gridDim = dim3(static_cast<unsigned>(units < most_ctas ? units : most_ctas));
+            cfg.blockDim = dim3(kPThreads);
+            cfg.dynamicSmemBytes = smem;
             ctas += cfg.gridDim.x;
-            const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p);
+            cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, p);
+            if (err != cudaSuccess) return err;
+            const bool last = r0 + p.rows == a.rows;
+            m.row0 = p.held0;
+            m.rows = r0 + p.rows - p.held0;
+            if (!last && m.rows < pl.held) continue;
+            m.ctas = last ? ctas : 0;
+            p.held0 = r0 + p.rows;
+            const int pairs = m.rows * a.hq;
+            cfg.gridDim = pairs < kMergeWide ? dim3(pairs, a.d / 64) : dim3((pairs + 7) / 8);
+            cfg.blockDim = dim3(256);
+            cfg.dynamicSmemBytes = 0;
+            auto merge = pairs < kMergeWide ? (a.d == 256 ? paged_merge_wide_kernel<256> : paged_merge_wide_kernel<128>)
+                                            : (a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>);
+            err = cudaLaunchKernelEx(&cfg, merge, a, m);
             if (err != cudaSuccess) return err;
         }
         return cudaSuccess;
     });
-    if (e != cudaSuccess) return e;
-    MergeArgs m{p.m, reinterpret_cast<const float4*>(p.l), p.part, said, p.cut, pl.spans, ctas};
-    const int pairs = a.rows * a.hq;
-    cfg.gridDim = pairs < kMergeWide ? dim3(pairs, a.d / 64) : dim3((pairs + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    auto merge = pairs < kMergeWide ? (a.d == 256 ? paged_merge_wide_kernel<256> : paged_merge_wide_kernel<128>)
-                                    : (a.d == 256 ? paged_merge_kernel<256> : paged_merge_kernel<128>);
-    e = cudaLaunchKernelEx(&cfg, merge, a, m);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
