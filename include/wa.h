@@ -406,8 +406,8 @@ typedef struct wa_rotary {
  * pos[t] * inv_freq[j]:
  *   out[a] = factor (x[a] c - x[b] s),   out[b] = factor (x[b] c + x[a] s),
  * one rounding to bf16.  inverse = 1 turns the other way (s -> -s): the gradient
- * of x given that of out.  Angles are exact to 2^-32 of a turn for every position,
- * so far positions lose nothing.
+ * of x given that of out.  Angles are off by 2^-25.9 of a turn at most, the fp32 angle's
+ * own rounding, at every position: far ones lose nothing more.
  *
  *   x    [n, heads, d]  bf16, token stride x_tok, head stride d
  *   pos  [n]            int32, device, any value

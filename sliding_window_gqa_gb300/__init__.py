@@ -836,7 +836,7 @@ def rope(x, pos, inv_freq, layout: str = "half", factor: float = 1.0, inverse: b
 
     Pair (j, j + dims / 2) ("half") or (2 j, 2 j + 1) ("interleaved") of the first dims dims turns by pos * inv_freq[j]
     and grows by ``factor``; the other dims stay.  ``inverse`` turns back: the gradient of x, given that of the
-    result.  Angles are exact for every position.  ``out`` may be x itself.  Returns out, [n, heads, d] bf16."""
+    result.  Angles are within 2^-25.9 of a turn at every position.  ``out`` may be x itself.  Returns out, [n, heads, d] bf16."""
     bind = _short_way() if stream is None else None
     if bind is not None:
         got = bind.rope(x, pos, inv_freq, layout, factor, inverse, out)

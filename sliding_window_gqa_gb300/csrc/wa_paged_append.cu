@@ -8,7 +8,8 @@
 // position 10^6, and a float64 product runs at a fiftieth of the fp32 rate here.
 // So inv_freq / (2 pi) becomes a 64-bit fixed-point fraction of a turn, by a 24 x
 // 96-bit integer product, and times pos, modulo 2^64, that is the angle's
-// fraction of a turn to 2^-33 for every int32 position; sincospif takes it from there.
+// fraction of a turn to 2^-33 for every int32 position.  Its upper 32 bits, rounded to fp32 (by 2^-26 of a turn at most), go to
+// sincospif.
 //
 // HBM-bound: a head is served by L = d / 16 lanes of two 16-byte pieces each, so
 // that both halves of a pair sit in one lane for either layout, a warp takes P =
@@ -29,7 +30,7 @@ constexpr int kAppendWarps = 4;       // (of 8, blocks ended unevenly: rope of 8
 // Up to this many tokens one more block checks them all and writes the status word, which spares a launch; beyond, a kernel
 // before this one clears it and the warps that look up the places of keys and values report what is wrong with them.  (The
 // block, and two launches: 600 tokens of 8 + 2 x 1 heads of 128 3.2 us each, 3.5 and 4.6 eager; 1,024 4.9 and 4.1, of 32 + 2 x 8
-// heads 6.5 each.  A block goes on at 0.7 us more for every 512 tokens.)
+// heads 6.5 each.)
 constexpr int kStatusBlockTokens = 1024;
 
 struct AppendParams {
