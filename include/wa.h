@@ -500,8 +500,9 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-14, or
  * 2^-28 of the largest weight where that is more).  With e4m3
  * pages a query's value is a sum of two 8-bit numbers, exact down to 2^-13 of its
- * head's largest value and within 2^-21 of that below.  A (row,
- * head) whose result is NaN or infinite is computed again in float64.  A row's
+ * head's largest value and within 2^-21 of that below.  Dims
+ * 64 j to 64 j + 63 of a (row, head) that hold a NaN or an infinity are computed
+ * again in float64.  A row's
  * bits depend on its own inputs alone: not on the batch, the row's place in it,
  * which pages hold its keys, or `most`.  Slots past pos and before the window may
  * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /

@@ -1215,8 +1215,8 @@ __device__ __noinline__ void paged_rerun(const PagedArgs& a, PagedRerun& sm, int
 }
 
 // out = vs sum_s a_s O_s / sum_s a_s l_s, a_s = 2^(m_s - M).  Both sums run over groups of kMergeGroup spans: a group's
-// in order, then the groups' in order, whichever of the two kernels below takes the row.  A result that is not finite is
-// worked out again.
+// in order, then the groups' in order, whichever of the two kernels below takes the row.  64 dims that hold a value that
+// is not finite are worked out again.
 constexpr int kMergeGroup = 4;
 
 // The status word of the call, by the last join's first block: what the CTAs of all its launches have to report.
@@ -1366,7 +1366,7 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");          // as above
     if (x.ctas > 0 && blockIdx.x == 0) paged_report(a.hdr, x.said, x.ctas);
-    bool bad = false;
+    uint32_t bad = 0u;                          // the lane's 4 dims of each 128 that are not finite
     if (item < items) {
         const int at = item / a.hq, row = x.row0 + at, h = item % a.hq, G = a.hq / a.hkv, g = h / G;
         const int64_t first = (static_cast<int64_t>(at) * a.hkv + g) * x.spans_most;
@@ -1426,19 +1426,25 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
             float4 r = sum[v];
             if (spans > 0) {
                 r.x = r.x / den * vs; r.y = r.y / den * vs; r.z = r.z / den * vs; r.w = r.w / den * vs;
-                bad |= !(isfinite(r.x) && isfinite(r.y) && isfinite(r.z) && isfinite(r.w));
+                if (!(isfinite(r.x) && isfinite(r.y) && isfinite(r.z) && isfinite(r.w))) bad |= 1u << v;
             }
             orow[v * 32 + lane] = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
         }
     }
-    __shared__ int again_for[8];
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) again_for[warp] = bad;
-    if (!__syncthreads_or(bad)) return;
+    // Of 64 dims that hold one all are computed again, and no others: what the wide kernel does.
+    __shared__ uint32_t again_for[8];           // of each warp's pair, a bit for 64 dims
+    uint32_t again_dims = 0u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, (bad >> v) & 1u);
+        again_dims |= ((lanes & 0xFFFFu) != 0u ? 1u : 0u) << (2 * v) | ((lanes >> 16) != 0u ? 2u : 0u) << (2 * v);
+    }
+    if (lane == 0) again_for[warp] = again_dims;
+    if (!__syncthreads_or(again_dims != 0u)) return;
     for (int i = 0; i < 8; ++i) {
-        if (!again_for[i]) continue;
-        for (int c = 0; c < D; c += 64) {
-            paged_rerun(a, again, x.row0 + (blockIdx.x * 8 + i) / a.hq, (blockIdx.x * 8 + i) % a.hq, c);
+        for (int c = 0; c < D / 64; ++c) {
+            if (!((again_for[i] >> c) & 1u)) continue;
+            paged_rerun(a, again, x.row0 + (blockIdx.x * 8 + i) / a.hq, (blockIdx.x * 8 + i) % a.hq, 64 * c);
             __syncthreads();
         }
     }

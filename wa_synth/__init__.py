@@ -305,7 +305,7 @@ def paged_case(lengths, hq, hkv, d, page, seed, win=0, bits=16, heads_first=Fals
     held = torch.zeros((count, page), dtype=torch.bool)
     gp = _gen(seed, "peak", "cpu")
     for r, n in enumerate(lengths):
-        for at in range(window_lo(n - 1, win), n):
+        for at in range(window_lo(n - 1, win), n if outside == "nan" else 0):
             held[table[r, at // page], at % page] = True
         for g in range(hkv if peaked and n > 0 else 0):
             lo = window_lo(n - 1, win)
