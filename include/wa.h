@@ -502,8 +502,9 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  * pages a query's value is a sum of two 8-bit numbers, exact down to 2^-13 of its
  * head's largest value and within 2^-21 of that below.  Dims
  * 64 j to 64 j + 63 of a (row, head) that hold a NaN or an infinity are computed
- * again in float64.  A row's
- * bits depend on its own inputs alone: not on the batch, the row's place in it,
+ * again in float64, by one block, which holds the call up: 2 ms for 4,000 keys, 0.18 s
+ * for 131,072 (heads of 128), less than 0.1 ms where a score is a NaN early in the row.
+ * A row's bits depend on its own inputs alone: not on the batch, the row's place in it,
  * which pages hold its keys, or `most`.  Slots past pos and before the window may
  * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /
  * hkv <= 16; strides of the pages multiples of 16 bytes, and the page stride a

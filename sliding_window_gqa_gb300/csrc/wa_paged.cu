@@ -1139,7 +1139,8 @@ __global__ void __launch_bounds__(kPThreads, 1) paged_kernel(const __grid_consta
 }
 
 // The float64 value of 64 of a (row, head)'s dims (from col0), by the whole block: the maximum score, then weights and their sums in key order,
-// 256 keys at a time; a NaN or +inf score settles the output before that.
+// 256 keys at a time; a NaN or +inf score settles the output before that.  (Without one: 2.0 ms for 4,000 keys of 128 dims, 181 ms
+// for 131,072: the block's own chain.)
 struct PagedRerun {
     double qd[256], wb[kRerunThreads], red[kRerunThreads / 32];
     float qf[256];
