@@ -484,8 +484,7 @@ int wa_paged_append(const void* src, const int32_t* pos, const int32_t* row, int
 
 size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win) {
     if (!cache || !page_sizes_ok(*cache, hq, win)) return 0;
-    return wa::paged_plan(cache->rows, hq, cache->hkv, cache->d, log2_of(cache->page_size), cache->most,
-                          cache->type == WA_PAGE_E4M3, win).bytes;
+    return wa::paged_plan(cache->rows, hq, cache->hkv, cache->d, log2_of(cache->page_size), cache->most, win).bytes;
 }
 
 int wa_paged_decode(const void* q, const int32_t* pos, int32_t hq, const wa_pages* cache, int32_t win, float scale,

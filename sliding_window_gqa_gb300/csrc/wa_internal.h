@@ -149,7 +149,7 @@ struct PagedPlan {
     size_t part;     // float[held * hkv * spans * G * d]
     size_t bytes;
 };
-PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win);
+PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int win);
 
 // Kept nodes' keys and values into the rings of several layers.
 struct CommitArgs {

@@ -262,21 +262,14 @@ __device__ __forceinline__ bool paged_elect() {
 // N consecutive columns of the thread's own lane.
 template <int N>
 __device__ __forceinline__ void tm_load(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "columns");
+    static_assert(N == 4 || N == 8, "columns");
     if constexpr (N == 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
-    else if constexpr (N == 8)
+    else
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr));
-    else if constexpr (N == 16)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(taddr));
-    else
-        tmem_ld32(taddr, r);
 }
 // The wait, with the registers passed through it, so that no use of them is scheduled before the data has arrived.
 template <int N>
@@ -285,20 +278,6 @@ __device__ __forceinline__ void tm_wait(uint32_t (&r)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
 }
-template <int N>
-__device__ __forceinline__ void tm_store(uint32_t taddr, const uint32_t (&r)[N]) {
-    static_assert(N == 4 || N == 8 || N == 16, "columns");
-    if constexpr (N == 4)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
-                     :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-    else if constexpr (N == 8)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                     :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    else
-        tmem_st16(taddr, r);
-}
-
 __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" :: "r"(addr), "r"(v) : "memory"); }
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
     asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" :: "r"(addr), "r"(v) : "memory");
@@ -1450,11 +1429,11 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
         }
     }
 }
+
 // (row, head) pairs below which the wide kernel runs.  (It, and the other one: one row of 131,072 keys, 32 heads of 128, 49.6 and
 // 66.3 us, 7 ragged rows, 24 heads of 256, 36.7 and 43.5, 4 rows of 32 14.4 and 15.3, 8 rows 16.2 and 15.3, 64 rows of 500 47 and
 // 30.)
 constexpr int kMergeWide = 256;
-
 
 bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -1494,7 +1473,7 @@ cudaError_t for_each_paged(F&& f) {
 
 }  // namespace
 
-PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int e4m3, int win) {
+PagedPlan paged_plan(int rows, int hq, int hkv, int d, int page_log, int most, int win) {
     PagedPlan pl{};
     const int align = copy_keys(page_log);
     const int64_t keys = static_cast<int64_t>(most) << page_log;
@@ -1527,7 +1506,7 @@ cudaError_t paged_prepare_device(int) {
 }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
-    const PagedPlan pl = paged_plan(a.rows, a.hq, a.hkv, a.d, a.page_log, a.most, a.e4m3, a.win);
+    const PagedPlan pl = paged_plan(a.rows, a.hq, a.hkv, a.d, a.page_log, a.most, a.win);
     const int G = a.hq / a.hkv, gp = G <= 4 ? 4 : G <= 8 ? 8 : 16;
     PagedParams p{};
     p.a = a;
