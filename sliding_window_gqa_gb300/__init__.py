@@ -746,7 +746,7 @@ def rope_frequencies(dims: int, base: float = 10000.0, scaling=None, device=None
       {"kind": "ramp", "factor", "original", "slow": 1, "fast": 32, "attention": None}: the pairs between the one of
           `fast` turns over the original length and the one of `slow` blended linearly in the pair's index, and both
           sides of the scores grow by `attention` (None: 0.1 ln s + 1), which is the factor returned.
-    Worked out in float64 and rounded once."""
+    Worked out in float64 and rounded once.  A scaling that brings a pair's frequency to 16 or more is refused."""
     dims = int(dims)
     if dims <= 0 or dims % 2:
         raise ValueError(f"dims must be even and positive, not {dims}")
@@ -797,7 +797,10 @@ def rope_frequencies(dims: int, base: float = 10000.0, scaling=None, device=None
         raise ValueError(f'scaling kind must be "linear", "base", "wavelength" or "ramp", not {kind!r}')
     if opt:
         raise ValueError(f"scaling has entries that {kind!r} does not take: {sorted(opt)}")
-    return torch.tensor(inv, dtype=torch.float64).float().to(device=device), float(factor)
+    inv_freq = torch.tensor(inv, dtype=torch.float64).float()
+    if not (inv_freq < 16.0).all():
+        raise ValueError(f"a pair's frequency of {max(inv)} is not below 16, which is all that the rotation takes")
+    return inv_freq.to(device=device), float(factor)
 
 
 def _rotary(inv_freq, layout, factor, d: int):
@@ -835,8 +838,10 @@ def rope(x, pos, inv_freq, layout: str = "half", factor: float = 1.0, inverse: b
     """Rotary positions: x [n, heads, d] bf16 (token-strided), pos int32 [n], inv_freq fp32 [dims / 2] on the GPU.
 
     Pair (j, j + dims / 2) ("half") or (2 j, 2 j + 1) ("interleaved") of the first dims dims turns by pos * inv_freq[j]
-    and grows by ``factor``; the other dims stay.  ``inverse`` turns back: the gradient of x, given that of the
-    result.  Angles are within 2^-25.9 of a turn at every position.  ``out`` may be x itself.  Returns out, [n, heads, d] bf16."""
+    and grows by ``factor``; the other dims stay.  A frequency of 16 or more in size gives NaN to its
+    pair.  ``inverse`` turns back: the gradient of x, given that of the result.  The call itself records nothing for autograd, so
+    an output has no history whatever x requires.  Angles are within 2^-25.9 of a turn at every position.  ``out`` may be x
+    itself.  Returns out, [n, heads, d] bf16."""
     bind = _short_way() if stream is None else None
     if bind is not None:
         got = bind.rope(x, pos, inv_freq, layout, factor, inverse, out)
@@ -917,8 +922,8 @@ def paged_append(src, pos, q_out, k_pages, v_pages, table, row=None, inv_freq=No
     into q_out [n, hq, d] (which may be their place in src), the key heads rotated and the value heads as they are into
     position pos[t] (int32 [n]; -1: a token to leave out) of sequence row[t] (int32 [n], None: sequence t): slot
     pos mod page of page table[row, pos / page] of k_pages / v_pages [pages, page, hkv, d], bf16 or float8_e4m3fn
-    (a value is stored as x / scale of its head, k_scale / v_scale fp32 [hkv]).  inv_freq, layout, factor as in rope();
-    None: no rotation.  Returns the workspace, whose status status() reads."""
+    (a value is stored as x / scale of its head, k_scale / v_scale fp32 [hkv]).  inv_freq (below 16 in size, or NaN), layout,
+    factor as in rope(); None: no rotation.  Returns the workspace, whose status status() reads."""
     bind = _short_way() if stream is None else None
     if bind is not None:
         got = bind.paged_append(src, pos, q_out, k_pages, v_pages, table, row, inv_freq, layout, factor, k_scale, v_scale, ws)
