@@ -414,8 +414,8 @@ typedef struct wa_rotary {
  *   out  [n, heads, d]  bf16, token stride out_tok, head stride d; x itself (with the
  *                       same stride) or memory that does not overlap it
  *
- * n >= 1; d is 128 or 256; pointers 16-byte aligned, token strides multiples of 8
- * elements and at least heads * d.  Returns WA_EINVAL otherwise.  No workspace.
+ * n >= 1; heads is 1 .. 65535; d is 128 or 256; pointers 16-byte aligned, token
+ * strides multiples of 8 elements and at least heads * d.  Returns WA_EINVAL otherwise.  No workspace.
  */
 int wa_rope(const void* x, const int32_t* pos, int32_t n, int32_t heads, int32_t d, const wa_rotary* rot,
             int32_t inverse, int64_t x_tok, int64_t out_tok, void* out, void* stream);
@@ -426,7 +426,8 @@ int wa_rope(const void* x, const int32_t* pos, int32_t n, int32_t heads, int32_t
 /* A cache in pages of page_size positions: position p of sequence (row) r is slot
  * p mod page_size of page table[r, p / page_size].  Sequences may share pages.
  * Strides are in elements; either layout of a page (positions of heads, heads of
- * positions), and k and v in one tensor, are a matter of them. */
+ * positions), and k and v in one tensor, are a matter of them.  Both calls below
+ * take up to 65535 rows with rows * hq < 2^31, and most * page_size up to 2^31 - 4097. */
 typedef struct wa_pages {
     void* k;                      /* [pages][page_size][hkv][d] by the strides below */
     void* v;
@@ -509,7 +510,7 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /
  * hkv <= 16; strides of the pages multiples of 16 bytes, and the page stride a
  * multiple of 8 slot strides or of the head stride (a lone head's stride is not
- * used); rows is 1 .. 65535 and rows * hq < 2^31.  Returns WA_EINVAL otherwise.
+ * used).  Returns WA_EINVAL otherwise.
  * Calls whose work can overlap need workspaces of their own; two captured graphs
  * that replay at the same time do too.
  */
