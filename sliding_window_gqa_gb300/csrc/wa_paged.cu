@@ -11,7 +11,7 @@
 // small; P's parts are columns of one product, so V is read from shared memory once for all of them.  A key is a lane of
 // tensor memory, so a mask is one bit a thread, and the scores of a whole span (16 columns a tile) stay there: its keys come
 // first, then its maximum is known, then its values.  Nothing is ever scaled again.  (With a running maximum every other
-// tile of 8-bit pages moved some head's, since P has to fit its type: 309 us for the batch below, 199 without.)
+// tile of 8-bit pages moved some head's, since P has to fit its type: 309 us for the 8-bit batch below, then 199 without.)
 //
 // 8-bit pages.  A query, of 8 significant bits, is two 8-bit numbers, and S comes from exact products as with bf16.  Up to 8
 // heads: 2^k q = hi + lo / 32, both e4m3 (4 significant bits), columns of their own, with the head's largest value at 128 to 256:
@@ -24,17 +24,17 @@
 //
 // Split.  A row's tiles of 128 keys, from its first visible one (rounded down to a copy's keys), are cut into even spans
 // (row_cut).  A unit of work is (row, key head, span); it leaves (m, l, O) in fp32, and a kernel of its own joins a row's
-// spans.  (Joined by the CTA that finished a row's last unit, one long row ended in 60 us of one SM reading what the others
-// had left.)  Nothing in a unit depends on the other rows, so neither do the bits.
+// spans.  (Joined by the CTA that finished a row's last unit, one long row ended, then, in 60 us of one SM reading what the
+// others had left.)  Nothing in a unit depends on the other rows, so neither do the bits.
 //
 // paged_kernel<D, F8, GP>: a persistent grid, one CTA an SM, 512 threads, that streams the keys of its units without a break
 // between units:
 //   warps 0, 3    TMA producers of K and of V, a ring of slots each, a copy a page (or piece of one) and 128 dims.  (One warp
-//                 for both took 900 cycles a load, where one of 8-bit pages lands every 700: 199 us, 182 with two.)
+//                 for both took 900 cycles a load, where one of 8-bit pages lands every 700: then 199 us, 182 with two.)
 //   warps 1, 13   MMA issuers of S (a unit ahead of its P V, at most two) and of P V.  Before O += V^T P^T of a row's first
 //                 and last tile the second zeroes V's slots without a visible key, so that what they hold never meets a
 //                 zero probability as 0 * inf.  (One warp for both took 1,000 cycles a tile, where one of 8-bit pages lands
-//                 every 1,400: 186 us, 170 with two.)  Warp 1 allocates tensor memory.
+//                 every 1,400: then 186 us, 170 with two.)  Warp 1 allocates tensor memory.
 //   warp 2        takes units, looks up their pages, publishes them
 //   warps 12, 14  Q to shared memory, split in two for 8-bit pages, once for units of one (row, key head) in a row: every
 //                 other one each; of 16 heads, they and warp 15 four heads each of all
@@ -42,10 +42,12 @@
 //   and 8..11     of odd units.  One group's chain (a unit's ends, 2,500 cycles) runs beside the other's.
 // Every wait is bounded (a status bit after kWaitLimitNs).
 //
-// Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128, 309 us for 311 at the rate of a copy; 48 rows,
-// 32/16 heads of 256, window 1,024, 125 for 117; one row of 131,072 keys, 32/4 heads of 128, 50 for 40 (start and join);
-// 8-bit pages, 64 rows of 500 to 30,000 keys ("the batch"), 162 for 148; 7 rows of 0 to 40,000, 24/2 heads of 256, 36 for
-// 21 (the softmax warps' chain, few units an SM).  One row of 700 keys, 16/8 heads of 256: 8.7 (two kernels' trips to memory).
+// Times here and beside the constants are of replayed graphs of calls on one workspace, from one run of the present code but
+// where a comment says "then".  Bound by HBM for batches: 64 rows of 100 to 16,000 keys, 32/8 heads of 128 ("the batch"), 315 us for
+// 311 at the rate of a copy; 48 rows, 32/16 heads of 256, window 1,024 ("the window"), 126 for 117; one row of 131,072 keys, 32/4
+// heads of 128, 49 for 40 (start and join); 8-bit pages, 64 rows of 500 to 30,000 keys ("the 8-bit batch"), 163 for 148; 7 rows of 0 to
+// 40,000, 24/2 heads of 256 ("the ragged one"), 37 for 21 (the softmax warps' chain, few units an SM).  One row of 700 keys, 16/8
+// heads of 256: 9.1 (two kernels' trips to memory).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -59,34 +61,34 @@ namespace {
 
 constexpr int kPTile = 128;          // keys a tile
 constexpr int kPThreads = 512;
-// Tiles of a span at most: as many as have room for their scores twice, beside O.  (Of 4, 6 and 8: the 8-bit batch 170, 162
-// and 159 us; one row of 131,072 keys 51.1, 50.3 and 49.1.)
+// Tiles of a span at most: as many as have room for their scores twice, beside O.  (Of 4, 6 and 8: the 8-bit batch 172.5, 164.1
+// and 163.0 us; one row of 131,072 keys 51.5, 50.4 and 49.2; one of 8,000, 32/8 heads, 14.9, 13.9 and 14.0.)
 constexpr int kSpanTiles = 8;
 // A span holds at least so many bytes of keys and values, and of 8-bit pages at least two tiles, for a unit has costs of its
-// own, of which those of the softmax warps show most with 8-bit pages.  (bf16 pages, 64 and 128 KiB, 32/8 heads of 128: one
-// row of 1,000 keys 8.0 and 8.7 us, 256 rows of 300 67.9 and 66.2.  8-bit pages of 2, 3 and 4 tiles of 32 KiB, 32/4 heads of
-// 128: one row of 2,000 keys 9.8, 10.0 and 10.8, 64 rows of 4,000 59.9, 54.4 and 50.5; of 1 and 2 tiles of 64 KiB, 24/2 heads of
-// 256: one row of 1,000 11.2 and 12.8, 64 rows of 1,000 34.2 and 25.7.)
+// own, of which those of the softmax warps show most with 8-bit pages.  Large batches would like more, one row of a few thousand
+// keys less.  (bf16 pages, 64 and 128 KiB, 32/8 heads of 128: 256 rows of 300 keys 66.6 and 65.1 us, 64 of 500 30.0 and 28.9, 4 of
+// 2,000 13.6 and 13.7.  8-bit pages of 2, 3 and 4 tiles of 32 KiB, 32/4 heads of 128: one row of 2,000 keys 9.1, 9.5 and 10.3, 64 rows
+// of 4,000 60.3, 54.5 and 48.9; of 1 and 2 tiles of 64 KiB, 24/2 heads of 256: 64 rows of 4,000 79.2 and 61.2.)
 __host__ __device__ constexpr int fewest_bytes(int e4m3) { return e4m3 ? 98304 : 65536; }
 __host__ __device__ constexpr int fewest_tiles(int d, int e4m3) {
     const int tiles = fewest_bytes(e4m3) / (2 * kPTile * d * (e4m3 ? 1 : 2)), least = e4m3 ? 2 : 1;
     return tiles > least ? tiles : least;
 }
 // A row is cut into this many units over its key heads, or twice as many, .., as spans of kSpanTiles allow: fewer than the
-// SMs, for two thirds of them read as fast as all, and a unit has costs of its own.  (With 152, 100 and 76: one row of 8,000
-// keys, 32/8 heads of 128, 14.0, 14.1 and 15.0 us; 48 rows, 32/16 heads of 256, window 1,024, 130.5, 127.5 and 128.0; 7 rows of
-// up to 40,000, 8-bit pages, 36.8, 38.0 and 37.4.)
+// SMs, for two thirds of them read as fast as all, and a unit has costs of its own.  Of 152, 100 and 76 the one that loses least
+// where it is not the best: one row of 8,000 keys, 32/8 heads of 128, 13.7, 14.2 and 15.3 us; over 8-bit pages, 32/4 heads, 11.1, 10.4
+// and 10.8; the window 130.2, 126.9 and 126.4; the ragged one 37.4, 37.3 and 37.2.
 constexpr int kFill = 100;
 constexpr int kPagedRows = 256;      // rows a launch, and the fewest that some kernels have room for
 constexpr int kPagedFewest = 64;
 constexpr int kPagedGrid = 256;      // CTAs of a launch at most
 // Launches are joined together as long as their partial results are no more than this, and each by itself beyond, so that the
 // workspace does not grow with the rows.  (Each by itself always: 4,096 rows of 41 keys, 8/1 heads of 128, 188 us, together
-// 178; 512 rows of 300, 32/8 heads, 136 and 137.)
+// 178; 512 rows of 300, 32/8 heads, 136 each.)
 constexpr int64_t kHeldBytes = 64 << 20;
 // Units go to the CTAs in turn up to kInTurn a CTA, beyond that by a counter, in jobs of about 256 KiB of units and kJobs a CTA
-// at least.  (In turn up to 2 and 8 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 20.9 and 19.9 us; always: the batch of 64
-// rows below 317, not 309.  8 jobs a CTA and 4: 64 rows of 500 33.3 and 29.2; jobs of 1 MiB: 256 rows of 300 72, not 67.)
+// at least.  (In turn up to 2 and 8 a CTA: 16 rows of 1,000 keys, 32/8 heads of 128, 20.0 and 19.2 us; always: the batch 324.5, not
+// 314.5, 64 rows of 500 31.0, not 30.0.  8 jobs a CTA and 4: 64 rows of 500 32.7 and 30.0; jobs of 1 MiB: 256 rows of 300 70.6, not 66.6.)
 constexpr int kInTurn = 8;
 constexpr int kJobs = 4;
 
@@ -173,8 +175,9 @@ struct PagedCfg {
     static constexpr int UNROLL = GP == 16 ? 1 : HV;     // (the most code: see the softmax's)
     static constexpr int KB = ESZ;                       // in blocks of 128 bytes of a key,
     static constexpr int SLOT = kPTile * KB * 128;       // as [16 groups of 8 keys][KB][8][128 bytes]
-    // slots of K, and of V: as many as leave room for P.  (Of half as many: one row of 8,000 keys, bf16
-    // pages, 15.4 us, not 14.1, the batch of 64 rows 305, not 301; 64 rows of 4,000, 8-bit pages, 52.4, not 54.4.)
+    // slots of K, and of V: as many as leave room for P.  (bf16 pages, 2 and 3: one row of 8,000 keys 15.4 and 14.0 us, the batch
+    // 318.5 and 314.5.  8-bit pages, 3 and 6: the batch 164.7 and 163.0, the ragged one (of 5) 37.2 and 36.6, 64 rows of 4,000 and
+    // one of 8,000 the same.)
     static constexpr int NSLOT = F8 ? (D == 256 && GP == 16 ? 5 : 6) : 3;
     // rows of Q: the heads; 8-bit: their hi parts, then from lo_row() on the lo parts, which a group of up to 8 heads has as
     // columns of its own (S = column h + column 8 + h / 32) and a larger one adds by a second product
@@ -1333,8 +1336,8 @@ __global__ void __launch_bounds__(256, 3) paged_merge_wide_kernel(const __grid_c
 }
 
 // Many rows: a warp a (row, head), kNarrowAhead / V spans at a time.  Their number comes first here, for spans that a row does
-// not have are not free when there are many rows (256 rows of 300 keys, a table for 38,400: 77 us, now 69).  (8 at a time, for
-// more warps an SM: 256 rows of 300 66 us, not 68, 64 rows of 500 to 30,000 over 8-bit pages 164, not 162.)
+// not have are not free when there are many rows (256 rows of 300 keys, a table for 38,400: 77 us, then 69).  (8 and 16 at
+// a time: 256 rows of 300 65.9 and 66.6 us, 64 of 500 29.6 and 30.0, the 8-bit batch 163.3 and 163.0.)
 constexpr int kNarrowAhead = 16;
 template <int D>
 __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ MergeArgs x) {
@@ -1430,9 +1433,9 @@ __global__ void __launch_bounds__(256, 2) paged_merge_kernel(const __grid_consta
     }
 }
 
-// (row, head) pairs below which the wide kernel runs.  (It, and the other one: one row of 131,072 keys, 32 heads of 128, 49.6 and
-// 66.3 us, 7 ragged rows, 24 heads of 256, 36.7 and 43.5, 4 rows of 32 14.4 and 15.3, 8 rows 16.2 and 15.3, 64 rows of 500 47 and
-// 30.)
+// (row, head) pairs below which the wide kernel runs.  (It, and the other one: one row of 131,072 keys, 32 heads of 128, 49.2 and
+// 65.3 us, 7 ragged rows, 24 heads of 256, 36.6 and 42.9, 4 rows of 2,000, 32 heads, 13.7 and 14.1, 8 rows 19.3 and 18.7, 64 rows of
+// 500 43.6 and 30.0.)
 constexpr int kMergeWide = 256;
 
 bool encode_pages(CUtensorMap* m, PageCoord* at, const PageSide& side, const PagedArgs& a, int align) {

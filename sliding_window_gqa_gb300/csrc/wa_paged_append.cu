@@ -14,7 +14,9 @@
 // HBM-bound: a head is served by L = d / 16 lanes of two 16-byte pieces each, so
 // that both halves of a pair sit in one lane for either layout, a warp takes P =
 // 32 / L heads a pass and PASSES passes of one token, all loads issued before the
-// angles are worked out, two or four a lane, which the others fetch by shuffles.
+// angles are worked out, two or four a lane, which the others fetch by shuffles.  (8,185 tokens of 32 + 2 x 8 heads of 128 into bf16
+// pages 32.3 us for 29.7 at the rate of a copy, into 8-bit pages 39.2 for 27.2, a division a value; rope of 8,192 x 40 heads of
+// 128 26.0 for 24.7, its inverse over 64 of 256 dims of 5,003 x 24 heads 20.2 for 18.1.  Times of replayed graphs.)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -26,7 +28,7 @@ namespace wa {
 
 namespace {
 
-constexpr int kAppendWarps = 4;       // (of 8, blocks ended unevenly: rope of 8,192 x 40 heads of 128 30.2 us, with 4 26.5)
+constexpr int kAppendWarps = 4;       // (of 8, blocks end unevenly: rope of 8,192 x 40 heads of 128 29.7 us, with 4 26.0)
 // Up to this many tokens one more block checks them all and writes the status word, which spares a launch; beyond, a kernel
 // before this one clears it and the warps that look up the places of keys and values report what is wrong with them.  (The
 // block, and two launches: 600 tokens of 8 + 2 x 1 heads of 128 3.2 us each, 3.5 and 4.6 eager; 1,024 4.9 and 4.1, of 32 + 2 x 8
@@ -259,8 +261,9 @@ cudaError_t launch_append(const AppendParams& p, cudaLaunchConfig_t& cfg) {
     return a.e4m3 ? run(append_kernel<128, true, true, PASSES>) : run(append_kernel<128, true, false, PASSES>);
 }
 
-// Few tokens: one pass a warp, for more warps at once (64 tokens of 48 heads of 128 to 8-bit pages: 3.2 us, with four passes
-// 4.8); many: four, for fewer angles and more bytes in flight (rope of 8,192 x 40 heads of 128: 26.5 us, with two 27.4).
+// Few tokens: one pass a warp, for more warps at once (64 tokens of 48 heads of 128 to 8-bit pages: 2.5 us, with four passes
+// 4.7); many: four, for fewer angles and more bytes in flight (rope of 8,192 x 40 heads of 128: 26.0 us, with two 26.9, with one
+// 32.5; 8,185 tokens of 48 heads appended to bf16 pages 32.3, 33.9 and 42.0, to 8-bit ones 39.2, 37.0 and 45.1).
 constexpr int64_t kFewValues = 1 << 20;
 
 }  // namespace
