@@ -498,19 +498,18 @@ size_t wa_paged_decode_ws_bytes(const wa_pages* cache, int32_t hq, int32_t win);
  *   out  [rows, hq, d]  bf16, row stride out_row; must not overlap the inputs
  *
  * Probabilities are fp32 in the sums and enter P V as two bf16 parts, whose sum is
- * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-14, or
- * 2^-28 of the largest weight where that is more).  With e4m3
- * pages a query's value is a sum of two 8-bit numbers, exact down to 2^-13 of its
- * head's largest value and within 2^-21 of that below.  Dims
- * 64 j to 64 j + 63 of a (row, head) that hold a NaN or an infinity are computed
- * again in float64, by one block, which holds the call up: 2 ms for 4,000 keys, 0.18 s
- * for 131,072 (heads of 128), less than 0.1 ms where a score is a NaN early in the row.
- * A row's bits depend on its own inputs alone: not on the batch, the row's place in it,
- * which pages hold its keys, or `most`.  Slots past pos and before the window may
- * hold anything.  page_size is a power of two from 16 to 256; hq % hkv == 0, hq /
- * hkv <= 16; strides of the pages multiples of 16 bytes, and the page stride a
- * multiple of 8 slot strides or of the head stride (a lone head's stride is not
- * used).  Returns WA_EINVAL otherwise.
+ * within 2^-17 of them, or with e4m3 pages as three e4m3 parts (2^-14, or 2^-28 of
+ * the largest weight where that is more).  With e4m3 pages a query's value is a sum
+ * of two 8-bit numbers, exact down to 2^-13 of its head's largest value and within
+ * 2^-21 of that below.  Dims 64 j to 64 j + 63 of a (row, head) that hold a NaN or
+ * an infinity are computed again in float64, by one block, which holds the call up:
+ * 2 ms for 4,000 keys, 0.18 s for 131,072 (heads of 128), less than 0.1 ms where a
+ * score is a NaN early in the row. A row's bits depend on its own inputs alone: not
+ * on the batch, the row's place in it, which pages hold its keys, or `most`.  Slots
+ * past pos and before the window may hold anything.  page_size is a power of two
+ * from 16 to 256; hq % hkv == 0, hq / hkv <= 16; strides of the pages multiples of
+ * 16 bytes, and the page stride a multiple of 8 slot strides or of the head stride
+ * (a lone head's stride is not used).  Returns WA_EINVAL otherwise.
  * Calls whose work can overlap need workspaces of their own; two captured graphs
  * that replay at the same time do too.
  */
